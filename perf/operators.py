@@ -138,11 +138,11 @@ def work(c):
 # --------------------------------------------------------------------------------------------------------- inputs
 def _quantise(x):
     """Codes [.., d] (as numbers) and (scale, bias) bf16 [.., d/64, 2] of x [.., d]: scale = bf16((max-min)/15),
-    bias = bf16(min), code = the nearest whole number to (x-bias)/scale, ties to even, within 0..15."""
+    bias = bf16(min), code = the nearest whole number to (x-bias)/scale, halves up, within 0..15."""
     g = x.float().unflatten(-1, (-1, GROUP))
     low, high = g.amin(-1, keepdim=True), g.amax(-1, keepdim=True)
     scale, bias = ((high - low) / 15).bfloat16(), low.bfloat16()
-    code = torch.round((g.double() - bias.double()) / scale.double()).clamp(0, 15)
+    code = torch.floor((g.double() - bias.double()) / scale.double() + 0.5).clamp(0, 15)
     code = torch.where(scale == 0, torch.zeros_like(code), code)
     return code.flatten(-2), torch.cat([scale, bias], -1)
 
@@ -366,7 +366,8 @@ def _exact_cache(s):
             g = s[name].double().unflatten(-1, (-1, GROUP))
             bias = g.min(-1, keepdim=True).values
             scale = ((g.max(-1, keepdim=True).values - bias) / 15).bfloat16().double()
-            code = torch.where(scale > 0, torch.round((g - bias) / torch.where(scale > 0, scale, torch.ones_like(scale))), torch.zeros_like(g))
+            steps = (g - bias) / torch.where(scale > 0, scale, torch.ones_like(scale))
+            code = torch.where(scale > 0, torch.ceil(steps - 0.5) + (torch.ceil(steps - 0.5) == steps - 0.5), torch.zeros_like(g))
             outs.append((code.clamp(0, 15) * scale + bias).flatten(-2))
             continue
         page, place = _row_places(s)
