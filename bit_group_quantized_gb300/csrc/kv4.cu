@@ -1,0 +1,260 @@
+// kv4.cu — writing keys and values into the 4-bit cache, and reading them back.
+//
+// One group of 64 columns of a token's head: bias = min, scale =
+// bf16((max - min) / 15), code = floor((x - bias)/scale + 1/2). A code is one
+// fused multiply-add: (x - bias) * r + 1.5 * 2^23 rounds to a whole number in
+// the low bits of the sum, with r = (1/scale)(1 + 2^-22). The small excess sends exact
+// halves up whatever way 1/scale was rounded, and moves no value that is more than 2^-18
+// of a step away from a half.
+//
+// Both kernels are bound by memory (2 bytes of bf16 and 0.56 bytes of cache a
+// value). Four lanes share a group, 16 values a lane in two 16-byte loads (the
+// reductions over a group then cost two shuffles, and the scale's division
+// is spread over 16 values); a lane's codes are two words of the group.
+#include "attn.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bgq {
+
+constexpr int kKvThreads = 256;
+constexpr int kKvUnits = 2;  // lane-units (16 values) a thread has in flight
+constexpr int kKvMaxRows = 32;
+
+struct KvGeo {
+  int units_row;     // lane-units of a row: K heads, then V heads
+  int units_k;       // the K part
+  int units_head;    // lane-units of a head
+  int rb;            // rows of a block
+  uint32_t m_row, m_head;  // u / n == umulhi(u, m) for u, n below 2^16
+  int chunk;         // lane-units of a row that one block takes
+};
+
+__host__ inline KvGeo kv_geo(int heads, int d, int rows) {
+  KvGeo g;
+  g.units_head = d / 16;
+  g.units_k = heads * g.units_head;
+  g.units_row = 2 * g.units_k;
+  const int want = kKvThreads * kKvUnits;
+  g.rb = 1;
+  while (g.rb < kKvMaxRows && g.rb * 2 * g.units_row <= want && (long long)rows >= 4ll * num_sms() * g.rb) g.rb *= 2;
+  g.chunk = g.rb > 1 || g.units_row <= want ? g.units_row : want;
+  g.m_row = (uint32_t)((0x100000000ull + g.units_row - 1) / g.units_row);
+  g.m_head = (uint32_t)((0x100000000ull + g.units_head - 1) / g.units_head);
+  return g;
+}
+
+struct KvUnit {  // where a lane-unit's values live
+  int row, head, lane;  // row of the block, head, lane-unit inside the head
+  bool val;             // V, otherwise K
+};
+__device__ __forceinline__ KvUnit kv_unit(const KvGeo& g, int u, int u0, int per) {
+  KvUnit k;
+  k.row = g.rb > 1 ? (int)__umulhi((uint32_t)u, g.m_row) : 0;
+  int r = u - k.row * per + u0;
+  k.val = r >= g.units_k;
+  if (k.val) r -= g.units_k;
+  k.head = (int)__umulhi((uint32_t)r, g.m_head);
+  k.lane = r - k.head * g.units_head;
+  return k;
+}
+
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Slots of the block's rows (-1: none), looked up once.
+__device__ __forceinline__ void kv_slots(const Kv4View& v, int r0, int nr, long long* slot) {
+  if ((int)threadIdx.x < nr) slot[threadIdx.x] = kv4_row_slot(v, r0 + threadIdx.x);
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant__ bgq_kv4_cache c,
+                                                           const __grid_constant__ Kv4View v,
+                                                           const __grid_constant__ KvGeo g,
+                                                           const uint16_t* __restrict__ k, long long k_stride,
+                                                           const uint16_t* __restrict__ val, long long v_stride) {
+  __shared__ long long slot[kKvMaxRows];
+  pdl_wait();
+  pdl_trigger();
+  const int r0 = blockIdx.x * g.rb, nr = min(g.rb, v.rows - r0);
+  const int u0 = blockIdx.y * g.chunk, per = min(u0 + g.chunk, g.units_row) - u0, total = nr * per;
+  bool ready = false;
+  // `total` and the strides are multiples of 4, so the four lanes of a group are in or out together
+  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kKvThreads * kKvUnits) {
+    uint4 in[kKvUnits][2];
+#pragma unroll
+    for (int i = 0; i < kKvUnits; ++i) {
+      const int u = base + i * kKvThreads;
+      in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
+      if (u < total) {
+        const KvUnit ku = kv_unit(g, u, u0, per);
+        const uint16_t* src = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
+                              ku.head * c.head_dim + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+        in[i][0] = ldg_stream16(src);
+        in[i][1] = ldg_stream16(src + 32);
+      }
+    }
+    if (!ready) {
+      kv_slots(v, r0, nr, slot);
+      ready = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kKvUnits; ++i) {
+      const int u = base + i * kKvThreads;
+      const uint32_t* w = &in[i][0].x;  // eight words of two values
+      uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        lo = min_nan2(lo, w[j]);
+        hi = max_nan2(hi, w[j]);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        lo = min_nan2(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = max_nan2(hi, __shfl_xor_sync(kFull, hi, o));
+      }
+      lo = min_nan2(lo, lo >> 16 | lo << 16);
+      hi = max_nan2(hi, hi >> 16 | hi << 16);
+      const float b = bf16lo(lo), range = bf16lo(hi) - b;
+      uint16_t s16 = f2bf(__fdiv_rn(range, 15.f)), b16 = (uint16_t)lo;
+      float s = bf16f(s16);
+      float r = 0.f;
+      if (!(s < __int_as_float(0x7f800000))) {  // a NaN or an infinity among the values
+        s16 = b16 = 0x7fc0;
+      } else if (s < 0x1p-126f) {
+        s16 = 0;  // one value, or a range below normal numbers
+      } else {
+        r = 1.f / s;
+        r = fmaf(r, 0x1p-22f, r);
+      }
+      constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: whole numbers in the low bits
+      uint32_t q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t acc = 0;
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {
+          const uint32_t x2 = w[h * 4 + j];
+          const uint32_t c1 = __float_as_uint(fmaf(bf16hi(x2) - b, r, kWhole));
+          const uint32_t c0 = __float_as_uint(fmaf(bf16lo(x2) - b, r, kWhole));
+          acc = acc * 256 + (c1 * 16 + c0);
+        }
+        // every code came with the bits of 1.5 * 2^23 in front: their sum over the eight places
+        q[h] = acc - 0x4B400000u * 0x11111111u;
+      }
+      const uint32_t bad = s16 == 0x7fc0;
+      if (u < total) {
+        const KvUnit ku = kv_unit(g, u, u0, per);
+        const long long sl = slot[ku.row];
+        if (sl >= 0) {
+          const long long page = sl / c.page_size;
+          const long long row = (page * c.kv_heads + ku.head) * c.page_size + (sl - page * c.page_size);
+          const int gr = ku.lane >> 2, l = ku.lane & 3;
+          uint32_t* qd = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
+          qd[0] = bad ? 0 : q[0];
+          qd[4] = bad ? 0 : q[1];
+          if (l == 0)
+            reinterpret_cast<uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (c.head_dim / kGroup) + gr] =
+                (uint32_t)s16 | (uint32_t)b16 << 16;
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__ bgq_kv4_cache c,
+                                                         const __grid_constant__ Kv4View v,
+                                                         const __grid_constant__ KvGeo g, uint16_t* __restrict__ k,
+                                                         long long k_stride, uint16_t* __restrict__ val,
+                                                         long long v_stride) {
+  __shared__ long long slot[kKvMaxRows];
+  __shared__ int held[kKvMaxRows];
+  pdl_wait();
+  pdl_trigger();
+  const int r0 = blockIdx.x * g.rb, nr = min(g.rb, v.rows - r0);
+  if ((int)threadIdx.x < nr) {  // rows of no sequence are left as they are
+    const int row = r0 + threadIdx.x;
+    held[threadIdx.x] = v.q_start ? row >= v.q_start[0] && row < v.q_start[v.batch] : row < v.batch;
+  }
+  kv_slots(v, r0, nr, slot);
+  const int u0 = blockIdx.y * g.chunk, per = min(u0 + g.chunk, g.units_row) - u0, total = nr * per;
+  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kKvThreads * kKvUnits) {
+    uint32_t q[kKvUnits][2], sb[kKvUnits];
+#pragma unroll
+    for (int i = 0; i < kKvUnits; ++i) {
+      const int u = base + i * kKvThreads;
+      q[i][0] = q[i][1] = sb[i] = 0;
+      if (u < total) {
+        const KvUnit ku = kv_unit(g, u, u0, per);
+        const long long sl = slot[ku.row];
+        if (sl >= 0) {
+          const long long page = sl / c.page_size;
+          const long long row = (page * c.kv_heads + ku.head) * c.page_size + (sl - page * c.page_size);
+          const int gr = ku.lane >> 2, l = ku.lane & 3;
+          const uint32_t* qs = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
+          q[i][0] = qs[0];
+          q[i][1] = qs[4];
+          sb[i] = reinterpret_cast<const uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (c.head_dim / kGroup) + gr];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kKvUnits; ++i) {
+      const int u = base + i * kKvThreads;
+      if (u >= total) continue;
+      const KvUnit ku = kv_unit(g, u, u0, per);
+      if (!held[ku.row]) continue;
+      const float s = bf16lo(sb[i]), b = bf16hi(sb[i]);
+      uint16_t* dst = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
+                      ku.head * c.head_dim + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // code under the exponent of 2^23: the value 2^23 + code
+          const float c0 = __uint_as_float((q[i][h] >> (8 * j) & 15u) | 0x4B000000u) - 8388608.f;
+          const float c1 = __uint_as_float((q[i][h] >> (8 * j + 4) & 15u) | 0x4B000000u) - 8388608.f;
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(fmaf(c0, s, b), fmaf(c1, s, b));
+          o[j] = *reinterpret_cast<const uint32_t*>(&p2);
+        }
+        *reinterpret_cast<uint4*>(dst + h * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+template <typename... KArgs, typename... Args>
+static cudaError_t kv_launch(void (*kern)(KArgs...), const KvGeo& g, int rows, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((rows + g.rb - 1) / g.rb, (g.units_row + g.chunk - 1) / g.chunk);
+  cfg.blockDim = dim3(kKvThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+cudaError_t launch_kv4_append(const bgq_kv4_cache& c, const Kv4View& v, const uint16_t* k, long long k_stride,
+                              const uint16_t* val, long long v_stride, cudaStream_t s) {
+  const KvGeo g = kv_geo(c.kv_heads, c.head_dim, v.rows);
+  return kv_launch(k_kv4_append, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
+}
+cudaError_t launch_kv4_read(const bgq_kv4_cache& c, const Kv4View& v, uint16_t* k, long long k_stride, uint16_t* val,
+                            long long v_stride, cudaStream_t s) {
+  const KvGeo g = kv_geo(c.kv_heads, c.head_dim, v.rows);
+  return kv_launch(k_kv4_read, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
+}
+
+}  // namespace bgq

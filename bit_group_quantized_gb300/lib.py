@@ -44,6 +44,21 @@ class bgq_moe_layer(C.Structure):
                 ("expert_sb_stride", C.c_int64), ("shared_q", C.c_void_p), ("shared_sb", C.c_void_p)]
 
 
+class bgq_rope_plan(C.Structure):
+    _fields_ = [("freq", C.c_uint64 * 128), ("axis", C.c_uint8 * 128), ("head_dim", C.c_int32),
+                ("rot_dim", C.c_int32), ("n_axes", C.c_int32), ("flags", C.c_int32)]
+
+
+class bgq_kv4_cache(C.Structure):
+    _fields_ = [("k_q", C.c_void_p), ("k_sb", C.c_void_p), ("v_q", C.c_void_p), ("v_sb", C.c_void_p),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class bgq_kv4_seqs(C.Structure):
+    _fields_ = [("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("pages", C.c_void_p), ("batch", C.c_int32),
+                ("max_pages", C.c_int32), ("rows", C.c_int32), ("max_q", C.c_int32)]
+
+
 _lib = None
 _P = C.c_void_p
 _I = C.c_int32
@@ -70,6 +85,13 @@ _SIGS = {
     "bgq_residual_add": (_I, [_P, _P, C.c_int64, _P]),
     "bgq_gemv_chain_workspace_bytes": (_S, [C.POINTER(bgq_qmatrix), _I, _I]),
     "bgq_gemv_chain": (_I, [C.POINTER(bgq_qmatrix), _I, _P, _I, _I, _P, C.c_float, _I, _P, _P, _P, _S, _P]),
+    "bgq_rope_init": (_I, [C.POINTER(bgq_rope_plan), _I, _I, C.c_double, _I, C.POINTER(_I), _I]),
+    "bgq_rope": (_I, [C.POINTER(bgq_rope_plan), _P, C.c_int64, _P, C.c_int64, _I, _I, _P, C.c_int64, _I, _P]),
+    "bgq_kv4_append": (_I, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _P, C.c_int64, _P, C.c_int64, _P]),
+    "bgq_kv4_read": (_I, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _P, C.c_int64, _P, C.c_int64, _P]),
+    "bgq_kv4_attention_workspace_bytes": (_S, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _I]),
+    "bgq_kv4_attention": (_I, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _P, C.c_int64, _I, C.c_float, _I,
+                               _I, _P, C.c_int64, _P, _P, _S, _P]),
     "moe_stack_workspace_bytes": (_S, [C.POINTER(bgq_moe_layer), _I]),
     "moe_stack_decode": (_I, [C.POINTER(bgq_moe_layer), C.POINTER(_P), _I, C.c_float, _P, _P, _P, _P, _P, _S,
                               _P]),
@@ -372,6 +394,218 @@ def gemv_chain(mats: list, x: torch.Tensor, norm: bool = False, rho=None, eps: f
     _check(lib.bgq_gemv_chain(arr, len(mats), _ptr(x2), B, int(norm), _ptr(rho), eps, int(residual), _ptr(out),
                               _ptr(out_f32), _ptr(ws), ws.numel(), _stream(stream)), "bgq_gemv_chain")
     return out, out_f32
+
+
+# ------------------------------------------------------------------ attention
+def _need(ok: bool, what: str):
+    if not ok:
+        raise BGQError(ERR_INVALID_ARG, what)
+
+
+def _on(t, dtype, device, dims: int, what: str):
+    """t is a CUDA tensor of this type, rank and device."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dims
+          and (device is None or t.device == device), what)
+
+
+def _heads(t, heads, d: int, device, what: str):
+    """t is bf16 [tokens][heads][d] whose heads lie one behind the other."""
+    _on(t, torch.bfloat16, device, 3, what)
+    _need((heads is None or t.shape[1] == heads) and t.shape[2] == d and t.stride(2) == 1
+          and (t.shape[1] == 1 or t.stride(1) == d), what)
+
+
+def _row_stride(t) -> int:
+    """Values between rows; of a single row, whose stride torch leaves open, its width."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 8)
+
+
+class _Launch:
+    """The device of a call's tensors made current, and the stream to run on:
+    the given one, else the device's current one. Buffers that the binding
+    creates belong to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None:
+            self.guard = torch.cuda.stream(stream)
+        else:
+            self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+class RopePlan:
+    """Rotary positions of heads of head_dim columns (bgq_rope_init): the first
+    rot_dim turn, sections[a] pairs by axis a."""
+
+    def __init__(self, head_dim: int, rot_dim: int, theta: float, sections, pairs: bool = False, cycle: bool = False,
+                 restart: bool = False):
+        self.c = bgq_rope_plan()
+        _check(load().bgq_rope_init(C.byref(self.c), head_dim, rot_dim, theta, len(sections),
+                                    (_I * max(len(sections), 1))(*sections),
+                                    int(pairs) | 2 * int(cycle) | 4 * int(restart)), "bgq_rope_init")
+        self.ref = C.byref(self.c)
+        self.head_dim, self.n_axes = head_dim, len(sections)
+
+
+def bgq_rope(plan: RopePlan, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor | None = None,
+             inverse: bool = False, stream=None) -> torch.Tensor:
+    """bgq_rope: x bf16 [tokens][heads][head_dim] (tokens may lie further
+    apart), pos int32 [n_axes][tokens] ([tokens] for one axis) -> y (x itself
+    is allowed). inverse: the gradient's direction."""
+    lib = load()
+    _heads(x, None, plan.head_dim, None, "bgq_rope: x must be a CUDA bf16 tensor [tokens][heads][head_dim]")
+    T, H, d = x.shape
+    p2 = pos.unsqueeze(0) if isinstance(pos, torch.Tensor) and pos.dim() == 1 else pos
+    _on(p2, torch.int32, x.device, 2, "bgq_rope: pos must be an int32 tensor [n_axes][tokens] on x's device")
+    _need(p2.shape == (plan.n_axes, T) and (T < 2 or p2.stride(1) == 1),
+          "bgq_rope: pos must be [n_axes][tokens] with its tokens one behind the other")
+    with _Launch(x.device, stream) as st:
+        if y is None:
+            y = alloc((T, H, d), torch.bfloat16, x.device)
+        else:
+            _heads(y, H, d, x.device, "bgq_rope: y must be a bf16 tensor like x")
+            _need(y.shape[0] == T, "bgq_rope: y must be a bf16 tensor like x")
+        if T == 0 or H == 0:
+            return y
+        _check(lib.bgq_rope(plan.ref, x.data_ptr(), _row_stride(x), p2.data_ptr(),
+                            p2.stride(0) if plan.n_axes > 1 else T, T, H, y.data_ptr(), _row_stride(y), inverse,
+                            st), "bgq_rope")
+    return y
+
+
+class KV4Cache:
+    """A paged 4-bit key/value cache: k_q, v_q int32 [n_pages][kv_heads][page_size][head_dim/8] and k_sb, v_sb
+    bf16 [n_pages][kv_heads][page_size][head_dim/64][2], all contiguous."""
+
+    def __init__(self, k_q: torch.Tensor, k_sb: torch.Tensor, v_q: torch.Tensor, v_sb: torch.Tensor):
+        for q, sb in ((k_q, k_sb), (v_q, v_sb)):
+            _on(q, torch.int32, k_q.device, 4, "KV4Cache: codes must be CUDA int32 tensors of rank 4")
+            _on(sb, torch.bfloat16, k_q.device, 5, "KV4Cache: scales must be bf16 tensors of rank 5 beside the codes")
+            _need(q.shape == k_q.shape and tuple(sb.shape) == (*q.shape[:3], q.shape[3] * 8 // GROUP, 2)
+                  and q.is_contiguous() and sb.is_contiguous(),
+                  "KV4Cache: codes [n_pages][kv_heads][page_size][head_dim/8], scales "
+                  "[n_pages][kv_heads][page_size][head_dim/64][2], contiguous")
+        self.k_q, self.k_sb, self.v_q, self.v_sb = k_q, k_sb, v_q, v_sb
+        self.n_pages, self.kv_heads, self.page_size = k_q.shape[:3]
+        self.head_dim, self.device = k_q.shape[3] * 8, k_q.device
+        self.c = bgq_kv4_cache(k_q.data_ptr(), k_sb.data_ptr(), v_q.data_ptr(), v_sb.data_ptr(), self.n_pages,
+                               self.page_size, self.kv_heads, self.head_dim)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KV4Cache":
+        """A cache of zeros."""
+        q = (n_pages, kv_heads, page_size, head_dim // 8)
+        sb = (n_pages, kv_heads, page_size, head_dim // GROUP, 2)
+        return cls(*(torch.zeros(s, dtype=t, device=device) for _ in range(2)
+                     for s, t in ((q, torch.int32), (sb, torch.bfloat16))))
+
+
+class KV4Seqs:
+    """The sequences of a call: kv_len int32 [batch], pages int32 [batch][max_pages] or None (sequence b has page
+    b), q_start int32 [batch+1] or None (row b alone). rows: rows of q, k, v
+    and out; max_q: the largest number of rows of a sequence. The tensors may
+    change between calls; their addresses are kept."""
+
+    def __init__(self, kv_len: torch.Tensor, rows: int | None = None, pages: torch.Tensor | None = None,
+                 q_start: torch.Tensor | None = None, max_q: int = 1):
+        dev = kv_len.device
+        _on(kv_len, torch.int32, dev, 1, "KV4Seqs: kv_len must be a CUDA int32 tensor [batch]")
+        B = kv_len.shape[0]
+        _need(kv_len.is_contiguous(), "KV4Seqs: kv_len must be contiguous")
+        if pages is not None:
+            _on(pages, torch.int32, dev, 2, "KV4Seqs: pages must be an int32 tensor [batch][max_pages] beside kv_len")
+            _need(pages.shape[0] == B and pages.is_contiguous(), "KV4Seqs: pages must be [batch][max_pages], contiguous")
+        if q_start is not None:
+            _on(q_start, torch.int32, dev, 1, "KV4Seqs: q_start must be an int32 tensor [batch+1] beside kv_len")
+            _need(q_start.shape[0] == B + 1 and q_start.is_contiguous() and rows is not None,
+                  "KV4Seqs: q_start must be [batch+1], contiguous, with rows given")
+        self.kv_len, self.pages, self.q_start, self.device = kv_len, pages, q_start, dev
+        self.rows = B if rows is None else rows
+        self.c = bgq_kv4_seqs(None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
+                              None if pages is None else pages.data_ptr(), B,
+                              0 if pages is None else pages.shape[1], self.rows, max_q)
+        self.ref = C.byref(self.c)
+
+
+def _kv_rows(cache, seqs, t, what):
+    _heads(t, cache.kv_heads, cache.head_dim, cache.device, what)
+    _need(t.shape[0] == seqs.rows and seqs.device == cache.device, what)
+
+
+def bgq_kv4_append(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """bgq_kv4_append: k, v bf16 [rows][kv_heads][head_dim] (rows may lie further apart) into the cache."""
+    for t in (k, v):
+        _kv_rows(cache, seqs, t, "bgq_kv4_append: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache")
+    if seqs.rows == 0:
+        return
+    with _Launch(cache.device, stream) as st:
+        _check(load().bgq_kv4_append(cache.ref, seqs.ref, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
+                                     st), "bgq_kv4_append")
+
+
+def bgq_kv4_read(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                 stream=None):
+    """bgq_kv4_read: (k, v) bf16 [rows][kv_heads][head_dim] of the rows' tokens."""
+    with _Launch(cache.device, stream) as st:
+        made = []
+        for t in (k, v):
+            if t is None:
+                t = alloc((seqs.rows, cache.kv_heads, cache.head_dim), torch.bfloat16, cache.device)
+            else:
+                _kv_rows(cache, seqs, t, "bgq_kv4_read: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache")
+            made.append(t)
+        k, v = made
+        if seqs.rows:
+            _check(load().bgq_kv4_read(cache.ref, seqs.ref, k.data_ptr(), _row_stride(k), v.data_ptr(),
+                                       _row_stride(v), st), "bgq_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(cache: KV4Cache, seqs: KV4Seqs, q_heads: int) -> int:
+    return load().bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, q_heads)
+
+
+def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: float | None = None,
+                      causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, want_lse: bool = False, ws: torch.Tensor | None = None,
+                      stream=None):
+    """bgq_kv4_attention: q bf16 [rows][q_heads][head_dim] -> (out, lse or None). scale defaults to
+    head_dim ** -0.5; lse fp32 [rows][q_heads] is written when given or wanted."""
+    lib = load()
+    _heads(q, None, cache.head_dim, cache.device, "bgq_kv4_attention: q must be bf16 [rows][q_heads][head_dim] beside the cache")
+    H = q.shape[1]
+    _need(q.shape[0] == seqs.rows and seqs.device == cache.device, "bgq_kv4_attention: q must have the sequences' rows")
+    with _Launch(cache.device, stream) as st:
+        if out is None:
+            out = alloc((seqs.rows, H, cache.head_dim), torch.bfloat16, cache.device)
+        else:
+            _heads(out, H, cache.head_dim, cache.device, "bgq_kv4_attention: out must be a bf16 tensor like q")
+            _need(out.shape[0] == seqs.rows, "bgq_kv4_attention: out must be a bf16 tensor like q")
+        if lse is None and want_lse:
+            lse = alloc((seqs.rows, H), torch.float32, cache.device)
+        elif lse is not None:
+            _on(lse, torch.float32, cache.device, 2, "bgq_kv4_attention: lse must be fp32 [rows][q_heads]")
+            _need(tuple(lse.shape) == (seqs.rows, H) and lse.is_contiguous(),
+                  "bgq_kv4_attention: lse must be fp32 [rows][q_heads], contiguous")
+        if seqs.rows == 0:
+            return out, lse
+        if ws is None:
+            ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
+        _check(lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), _row_stride(q), H,
+                                     cache.head_dim ** -0.5 if scale is None else scale, causal, window,
+                                     out.data_ptr(), _row_stride(out), None if lse is None else lse.data_ptr(),
+                                     ws.data_ptr(), ws.numel() * ws.element_size(), st), "bgq_kv4_attention")
+    return out, lse
 
 
 class Stack:

@@ -319,6 +319,128 @@ int32_t bgq_gemv_chain(const bgq_qmatrix* W, int32_t n, const uint16_t* x, int32
                        const uint16_t* rho, float eps, int32_t residual, uint16_t* out, float* out_f32, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- attention
+ * What a decoder layer does between its projections: rotary positions, a
+ * 4-bit key/value cache, and attention over it. The Flash-MoE page names the
+ * attention of its per-token pipeline ("架构设计") without describing it; the
+ * cache is held in this library's own packed format. */
+
+/* Rotary positions with several axes (time, height, width).
+ * Pair i of a head, (a, b), becomes (a cos t - b sin t, a sin t + b cos t),
+ *   t = pos[axis(i)] * f(i), f(i) = theta^(-2i/rot_dim), i < rot_dim/2;
+ * columns from rot_dim on are copied. Pair i is columns (i, i + rot_dim/2), or
+ * (2i, 2i+1) with BGQ_ROPE_PAIRS. sections[a] pairs belong to axis a: the
+ * first sections[0] pairs to axis 0, the next to axis 1, and so on; with
+ * BGQ_ROPE_CYCLE pair i belongs to axis a = i mod n_axes where i / n_axes <
+ * sections[a], else to axis 0. With BGQ_ROPE_RESTART the frequencies start
+ * again in every section: f = theta^(-j/sections[a]) for its pair j.
+ * The angle is held as a 64-bit fixed-point fraction of a turn, exact at any
+ * int32 position; the result is computed in fp32 and rounded once to bf16.
+ *
+ * bgq_rope_init fills a HOST struct from HOST arguments (sections: n_axes
+ * counts with sum rot_dim/2; theta > 0 and finite); it makes no CUDA call.
+ * head_dim: a multiple of 8 in 16..256, rot_dim: a multiple of 16. RESTART and
+ * CYCLE exclude each other. Fill it once and keep it. */
+enum { BGQ_ROPE_PAIRS = 1, BGQ_ROPE_CYCLE = 2, BGQ_ROPE_RESTART = 4 };
+enum { BGQ_ROPE_MAX_AXES = 8 };
+typedef struct bgq_rope_plan {
+  uint64_t freq[128]; /* turns of one position step, times 2^64 */
+  uint8_t axis[128];
+  int32_t head_dim;
+  int32_t rot_dim;
+  int32_t n_axes;
+  int32_t flags;
+} bgq_rope_plan;
+int32_t bgq_rope_init(bgq_rope_plan* p, int32_t head_dim, int32_t rot_dim, double theta, int32_t n_axes,
+                      const int32_t* sections, int32_t flags);
+
+/* y[t][h] = x[t][h] turned to token t's position; x, y: bf16 [tokens][heads]
+ * [head_dim], tokens x_stride / y_stride values apart (multiples of 8, at
+ * least heads*head_dim: the query and key heads of a fused projection's output
+ * can be turned where they stand). y may be x (with the same stride); any other overlap
+ * is not allowed. pos: int32 [n_axes][pos_stride], axis by axis, any values.
+ * inverse != 0 turns the other way: the gradient with respect to x of a
+ * forward call, given the gradient of y. tokens may be 0; heads <= 1024. */
+int32_t bgq_rope(const bgq_rope_plan* p, const uint16_t* x, int64_t x_stride, const int32_t* pos, int64_t pos_stride,
+                 int32_t tokens, int32_t heads, uint16_t* y, int64_t y_stride, int32_t inverse, void* stream);
+
+/* A paged cache of keys and values in 4 bits (host struct, device arrays).
+ *   k_q, v_q   : codes, uint32 [n_pages][kv_heads][page_size][head_dim/8], eight codes a word, the first in
+ *                the lowest bits;
+ *   k_sb, v_sb : bf16 (scale, bias) pairs [n_pages][kv_heads][page_size][head_dim/64][2].
+ *   value = code*scale + bias, one pair for each 64 columns of a token's head
+ *   (a page's head is a bgq_qmatrix of page_size rows).
+ * head_dim 64, 128 or 256; page_size a multiple of 16; kv_heads <= 256; all
+ * four arrays 16-byte aligned device memory. */
+typedef struct bgq_kv4_cache {
+  uint32_t* k_q;
+  uint16_t* k_sb;
+  uint32_t* v_q;
+  uint16_t* v_sb;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+} bgq_kv4_cache;
+
+/* The sequences of one call (host struct, device arrays; the lengths stay on
+ * the device, so a captured graph serves growing sequences).
+ *   q_start : int32 [batch+1], not decreasing: rows q_start[b] .. q_start[b+1]-1 of q, k,
+ *             v and out belong to sequence b. NULL: row b alone (then rows ==
+ *             batch and max_q == 1).
+ *   kv_len  : int32 [batch], tokens of sequence b in the cache, the ones of
+ *             its rows among them: row j of q_len stands at position
+ *             kv_len - q_len + j.
+ *   pages   : int32 [batch][max_pages], token t of sequence b lives in page pages[b][t / page_size]. NULL:
+ *             in page b (then a page is a sequence's whole space).
+ *   rows    : rows of q, k, v and out (no row behind them is touched).
+ *   max_q   : the largest q_len, or more (it sets launch sizes; a larger q_len is computed all the same).
+ * Rows of no sequence are left as they are. Tokens whose position is negative
+ * or beyond the page list, or whose page number is outside 0..n_pages-1 (-1,
+ * say, for a page given up) are absent: not written, read back as zeros, and
+ * masked in attention. 1 <= batch <= 4096, rows may be 0. */
+typedef struct bgq_kv4_seqs {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* pages;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t rows;
+  int32_t max_q;
+} bgq_kv4_seqs;
+
+/* Quantises new keys and values into the cache, at the positions of their
+ * rows. k, v: bf16 [rows][kv_heads][head_dim], rows k_stride / v_stride values
+ * apart (multiples of 8). Per group of 64 columns: bias = min, scale = bf16((max - min)/15) (0 when that
+ * is below 2^-126), code = floor((x - bias)/scale + 1/2) in fp32. A group that
+ * holds a NaN or an infinity, or whose range overflows fp32, reads back as NaN. Two rows
+ * of one call must not share a page's slot. */
+int32_t bgq_kv4_append(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const uint16_t* k, int64_t k_stride,
+                       const uint16_t* v, int64_t v_stride, void* stream);
+
+/* Reads the tokens of the rows back: k, v bf16 [rows][kv_heads][head_dim] =
+ * bf16(code*scale + bias). With q_len = kv_len a whole sequence is read. */
+int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k, int64_t k_stride, uint16_t* v,
+                     int64_t v_stride, void* stream);
+
+/* Attention over the cache:
+ *   out[r][h] = sum_t softmax_t(scale * q[r][h] . K[t][h']) V[t][h'],
+ *   h' = h / (q_heads / kv_heads), over the tokens t < kv_len of the row's
+ *   sequence that are not absent, t <= the row's position when causal != 0,
+ *   and t > position - window when window > 0.
+ * q, out: bf16 [rows][q_heads][head_dim], rows q_stride / out_stride values
+ * apart (multiples of 8). lse (nullable): fp32 [rows][q_heads], the logarithm
+ * of the sum of exponentials. A row that sees no token gets zeros and lse
+ * -infinity. What a masked or absent token holds never reaches a row; a row
+ * that sees a NaN gets NaN. q_heads a multiple of kv_heads, at most 64 times as many and
+ * at most 1024.
+ * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
+ * max_q and heads). The same inputs give the same bits. */
+size_t bgq_kv4_attention_workspace_bytes(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, int32_t q_heads);
+int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const uint16_t* q, int64_t q_stride,
+                          int32_t q_heads, float scale, int32_t causal, int32_t window, uint16_t* out,
+                          int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* One decode token through a stack of n_layers resident layers (batch 1):
  *   h = x (widened to fp32); for each layer l:
  *     a = bf16(rmsnorm(h, rho[l], eps)); h += layer_l(a)  (fp32, unrounded);
