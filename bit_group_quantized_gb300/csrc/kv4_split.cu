@@ -1,0 +1,753 @@
+// kv4_split.cu — attention over the 4-bit cache for few query rows a sequence
+// (decode steps, drafted tokens): bound by reading the cache once.
+//
+// A unit is one key head of one sequence with up to 8*NT columns, a column
+// being one (query row, query head) pair that shares this key head, so the
+// cache is read once for all of them. A unit's tokens are cut into tiles; all units' tiles
+// form one list, and every CTA takes an equal, contiguous share of it, so
+// ragged lengths balance by themselves and a single long sequence spreads over
+// the whole GPU. The list is worked out on the device from the lengths there.
+//
+// In a CTA each warp runs on its own: it copies its next tiles into its own ring
+// (cp.async), and takes tiles w, w + kWarps, ... of a segment (the part of a
+// unit inside the CTA's share) with a running maximum and sum per column.
+// Per tile, with mma.sync m16n8k16 (fp16 in, fp32 out):
+//   scores  S[token][col] = sum_g s_g (codes . x)_g + b_g sum(x)_g: the codes are the A
+//           operand as whole numbers (64 + code, placed by masks under the exponent of 64;
+//           the accumulator starts at -64 sum(x)), the query the B operand, scaled
+//           by a power of two per column, which is exact;
+//   output  O[dim][col] += (code - 8) (p s_g): the codes transposed by byte
+//           permutes as the A operand, the probabilities times the token's scale
+//           as the B operand; p (b_g + 8 s_g) is summed apart in fp32. Codes are
+//           centred so that long sums stay small beside what is added to them.
+// p s_g is rounded to fp16 (11 bits); its exponent is kept in range by a power
+// of two 2^E per warp that follows the largest scale seen. The maximum is only
+// raised when a score passes it by 2^8, so that most tiles need no reduction over the warp.
+// A segment ends with the CTA's warps joined in shared memory; a unit cut by a
+// CTA's share is joined by the last of its CTAs to arrive, in CTA order (the same
+// bits every time).
+#include <cuda_fp16.h>
+
+#include "attn.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bgq {
+
+constexpr int kSplitWarps = 8;
+constexpr int kSplitThreads = kSplitWarps * 32;
+constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then the arrival counters
+constexpr int kSplitMaxGrid = (kSplitHead - 256) / 4;
+
+template <int D, int NT>
+struct Split {
+  static constexpr int G = D / kGroup;
+  static constexpr int C = 8 * NT;                 // columns of a unit
+  static constexpr int TT = D == 256 ? 16 : 32;    // tokens of a tile
+  static constexpr int MT = TT / 16;
+  static constexpr int ST = D == 64 ? 3 : D == 256 && NT == 2 ? 4 : 2;  // tiles of a warp's ring
+  static constexpr int CPT = D / 32;               // 16-byte chunks of a token's codes
+  static constexpr int kCode = TT * D / 2;         // bytes of a tile's K (or V) codes
+  static constexpr int kSb = TT * D / 16;          // bytes of a tile's K (or V) pairs
+  static constexpr int kStage = 2 * kCode + 2 * kSb;
+  static constexpr int RD = D * NT >= 256 && NT == 2 ? 64 : (D < 128 ? D : 128);  // dims joined per round
+  static constexpr int RS = RD + 4;                // row stride of the join area (floats)
+  static constexpr bool kQs = D * NT > 128;        // query fragments in shared memory
+  static constexpr int kQBytes = kQs ? NT * G * 4 * 32 * 8 : 0;
+  static constexpr int kSmem = kSplitWarps * ST * kStage + kSplitWarps * C * RS * 4 + kQBytes;
+  static constexpr int kCtas = D == 256 && NT == 2 ? 1 : 2;  // per SM
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movm(uint32_t a) {  // transpose of an 8x8 fp16 matrix held by a warp
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(m), "r"(o));
+  return d;
+}
+
+// A sequence's part of the tile list.
+struct SeqTiles {
+  Span sp;
+  int begin;  // first token of its first tile
+  int tiles;  // of one unit (at least one, so that rows that see no token are written)
+  int rtiles;  // column tiles
+  long long units;
+};
+template <int TT, int C>
+__device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int b) {
+  SeqTiles s;
+  s.sp = kv4_span(a.v, b);
+  const int group = a.q_heads / a.c.kv_heads;
+  const int pos0 = s.sp.kv_len - s.sp.q_len;
+  s.begin = a.window > 0 ? max(0, pos0 - a.window + 1) / TT * TT : 0;
+  s.tiles = max(1, (s.sp.held - s.begin + TT - 1) / TT);
+  const long long cols = (long long)s.sp.q_len * group;
+  const bool mine = s.sp.q_len > 0 && cols <= a.split_cols;
+  s.rtiles = mine ? (int)((cols + C - 1) / C) : 0;
+  s.units = (long long)s.rtiles * a.c.kv_heads;
+  return s;
+}
+
+// One segment: tiles i0..i1-1 of a unit.
+struct Walk {
+  int b;
+  SeqTiles q;
+  long long unit;
+  int i0, i1;
+  long long x, x1;  // list position of i0, end of the CTA's share
+
+  __device__ __forceinline__ bool live() const { return x < x1; }
+  template <int TT, int C>
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    x += i1 - i0;
+    if (x >= x1) return;
+    i0 = 0;
+    if (++unit >= q.units) {
+      unit = 0;
+      do q = seq_tiles<TT, C>(a, ++b);
+      while (q.units == 0 && b + 1 < a.v.batch);
+    }
+    i1 = (int)min((long long)q.tiles, x1 - x);
+  }
+};
+
+struct SplitWs {
+  int* count;   // [grid] arrivals at the unit that CTA c began and did not end; left at zero
+  float* part;  // [grid][2][C][D + 2]: slot 0 a unit begun by an earlier CTA, slot 1 a unit that goes on
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_split(const __grid_constant__ AttnArgs a) {
+  using P = Split<D, NT>;
+  constexpr int G = P::G, C = P::C, TT = P::TT, MT = P::MT, ST = P::ST, RD = P::RD, RS = P::RS;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float s_m[kSplitWarps][C], s_l[kSplitWarps][C];
+  __shared__ long long s_scan[kSplitWarps + 1], s_base;
+  __shared__ int s_b, s_last, s_gaps[kSplitWarps][ST];
+  unsigned char* const ring = smem + (threadIdx.x >> 5) * (ST * P::kStage);
+  float* const area = reinterpret_cast<float*>(smem + kSplitWarps * ST * P::kStage);
+  uint2* const qf_s = reinterpret_cast<uint2*>(smem + kSplitWarps * ST * P::kStage + kSplitWarps * C * RS * 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the list: how long it is, and where this CTA's share begins
+  const int per = (a.v.batch + kSplitThreads - 1) / kSplitThreads;
+  const int b_lo = min((int)threadIdx.x * per, a.v.batch), b_hi = min(b_lo + per, a.v.batch);
+  long long own = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const SeqTiles s = seq_tiles<TT, C>(a, b);
+    own += s.units * s.tiles;
+  }
+  long long pre = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(kFull, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) s_scan[warp] = pre;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kSplitWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  pre += before - own;
+  const long long ctas = min((long long)gridDim.x, (total + kSplitWarps - 1) / kSplitWarps);
+  const int cta = blockIdx.x;
+  if (cta >= ctas) return;
+  Walk wk;
+  wk.x = total * cta / ctas;
+  wk.x1 = total * (cta + 1) / ctas;
+  if (wk.x >= pre && wk.x < pre + own) {
+    int b = b_lo;
+    for (; b < b_hi; ++b) {
+      const SeqTiles s = seq_tiles<TT, C>(a, b);
+      const long long n = s.units * s.tiles;
+      if (wk.x < pre + n) break;
+      pre += n;
+    }
+    s_b = b;
+    s_base = pre;
+  }
+  __syncthreads();
+  wk.b = s_b;
+  wk.q = seq_tiles<TT, C>(a, wk.b);
+  wk.unit = (wk.x - s_base) / wk.q.tiles;
+  wk.i0 = (int)((wk.x - s_base) % wk.q.tiles);
+  wk.i1 = (int)min((long long)wk.q.tiles, wk.i0 + wk.x1 - wk.x);
+
+  const int heads = a.c.kv_heads, group = a.q_heads / heads;
+  const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
+
+  // ---- copies: the warp's next tile of its share into ring slot `slot`
+  Walk fw = wk;
+  int fi = fw.i0 + warp;
+  auto fetch = [&](int slot) {
+    while (fw.live() && fi >= fw.i1) {
+      fw.next<TT, C>(a);
+      fi = fw.i0 + warp;
+    }
+    if (fw.live()) {
+      const int t0 = fw.q.begin + fi * TT, h = (int)(fw.unit / fw.q.rtiles);
+      const uint32_t dst = ring_u + slot * P::kStage;
+      int gaps = 0;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {  // 16 tokens lie in one page
+        const int t = t0 + 16 * m;
+        const int page = t < fw.q.sp.held ? kv4_page(a.v, fw.b, t) : -1;
+        const bool ok = page >= 0;
+        gaps |= ok ? 0 : 1 << m;
+        const long long row = ok ? ((long long)page * heads + h) * a.c.page_size + t % a.c.page_size : 0;
+        const char* ks = reinterpret_cast<const char*>(a.c.k_q) + row * (D / 2) + lane * 16;
+        const char* vs = reinterpret_cast<const char*>(a.c.v_q) + row * (D / 2) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < P::CPT / 2; ++i) {  // 16 tokens are 16 * CPT chunks
+          const int id = i * 32 + lane, tok = id / P::CPT, ch = id % P::CPT;
+          int at;
+          if (D == 64) at = (tok >> 2) * 128 + (((tok & 3) ^ ((tok >> 2) & 1)) * 32) + ch * 16;
+          else if (D == 128) at = (tok >> 1) * 128 + ((((tok & 1) * 2 + (ch >> 1)) ^ ((tok >> 1) & 3)) * 32) + (ch & 1) * 16;
+          else at = tok * 128 + (((ch >> 1) ^ (tok & 3) ^ ((tok >> 2) & 1)) * 32) + (ch & 1) * 16;
+          cp16(dst + m * (8 * D) + at, ks + i * 512, ok);
+          cp16(dst + P::kCode + m * (8 * D) + at, vs + i * 512, ok);
+        }
+        // pairs: D bytes per 16 tokens, K by the low lanes, V by the high ones
+        constexpr int n = D / 16;
+        if ((lane & 15) < n) {
+          const char* src = reinterpret_cast<const char*>(lane < 16 ? a.c.k_sb : a.c.v_sb) + row * (D / 16) + (lane & 15) * 16;
+          cp16(dst + 2 * P::kCode + (lane < 16 ? 0 : P::kSb) + m * D + (lane & 15) * 16, src, ok);
+        }
+      }
+      if (lane == 0) s_gaps[warp][slot] = gaps;
+      fi += kSplitWarps;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) fetch(i);
+  int slot = 0;
+
+  // lane's place in a tile's codes: K row g, V tokens 2c and 2c+1
+  int koff, voff0, voff1;
+  if (D == 64) {
+    koff = (g >> 2) * 128 + (((g & 3) ^ (g >> 2)) * 32) + c * 8;
+    const int t0 = 2 * c, t1 = 2 * c + 1;
+    voff0 = (t0 >> 2) * 128 + (((t0 & 3) ^ (t0 >> 2)) * 32) + g * 4;
+    voff1 = (t1 >> 2) * 128 + (((t1 & 3) ^ (t1 >> 2)) * 32) + g * 4;
+  } else if (D == 128) {
+    koff = (g >> 1) * 128 + ((((g & 1) * 2) ^ (g >> 1)) * 32) + c * 8;
+    voff0 = c * 128 + (c * 32) + g * 4;
+    voff1 = c * 128 + ((2 ^ c) * 32) + g * 4;
+  } else {
+    koff = g * 128 + (((g & 3) ^ (g >> 2)) * 32) + c * 8;
+    const int t0 = 2 * c, t1 = 2 * c + 1;
+    voff0 = t0 * 128 + (((t0 & 3) ^ (t0 >> 2)) * 32) + g * 4;
+    voff1 = t1 * 128 + (((t1 & 3) ^ (t1 >> 2)) * 32) + g * 4;
+  }
+
+  for (; wk.live(); wk.template next<TT, C>(a)) {
+    const int h = (int)(wk.unit / wk.q.rtiles), col0 = (int)(wk.unit - (long long)h * wk.q.rtiles) * C;
+    const int ncol = min(C, wk.q.sp.q_len * group - col0);
+    const int pos0 = wk.q.sp.kv_len - wk.q.sp.q_len;
+
+    // ---- the query: fp16 fragments of column g, scaled by a power of two
+    uint32_t qf[P::kQs ? 1 : NT * G * 8];
+    float xs[NT][2][G], cs[NT][2];  // of columns 2c, 2c+1: group sums, and scale * log2(e) / 2^shift
+    int hi[NT][2], lo[NT][2];       // the tokens that columns 2c, 2c+1 see: lo <= t < hi
+    if (P::kQs) __syncthreads();    // the last segment's fragments are read
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = n * 8 + g;
+      const int j = (col0 + col) / group, hh = (col0 + col) - j * group;
+      const int row = wk.q.sp.first + j;
+      const bool ok = col < ncol && row >= 0 && row < a.v.rows;
+      const uint16_t* src = a.q + (long long)(ok ? row : 0) * a.q_stride + (h * group + hh) * D + c * 16;
+      uint32_t raw[G][8];
+      float top = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (ok) v = *reinterpret_cast<const uint4*>(src + gr * 64 + i * 8);
+          raw[gr][i * 4] = v.x; raw[gr][i * 4 + 1] = v.y; raw[gr][i * 4 + 2] = v.z; raw[gr][i * 4 + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(raw[gr][i])), fabsf(bf16hi(raw[gr][i]))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      // largest magnitude into [8, 16): fp16 keeps 2^-28 of it
+      const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
+      const float up = exp2i(-e);
+      float sum[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        sum[gr] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // word w of the lane: dims 16c + 8w + 0..7; pair i is dims (i, i + 4)
+          const uint32_t* r = raw[gr] + w * 4;
+          uint32_t f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = i & 1 ? bf16hi(r[i >> 1]) : bf16lo(r[i >> 1]);
+            const float x1 = i & 1 ? bf16hi(r[2 + (i >> 1)]) : bf16lo(r[2 + (i >> 1)]);
+            f[i] = half2_of(x0 * up, x1 * up);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
+            sum[gr] += back.x + back.y;
+          }
+          if (P::kQs) {
+            if (warp == n % kSplitWarps) {
+              qf_s[((n * G + gr) * 4 + w * 2) * 32 + lane] = make_uint2(f[0], f[1]);
+              qf_s[((n * G + gr) * 4 + w * 2 + 1) * 32 + lane] = make_uint2(f[2], f[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[((n * G + gr) * 4 + w * 2) * 2 + i] = f[i];
+          }
+        }
+        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 1);
+        sum[gr] += __shfl_xor_sync(kFull, sum[gr], 2);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int from = (2 * c + k) * 4;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) xs[n][k][gr] = __shfl_sync(kFull, sum[gr], from);
+        cs[n][k] = a.scale * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from));
+        const int cc = n * 8 + 2 * c + k, jj = (col0 + cc) / group;
+        const int pos = pos0 + jj;
+        // columns behind the last see what the first one sees, and are dropped at the end
+        const int p2 = cc < ncol ? pos : pos0 + col0 / group;
+        hi[n][k] = min(wk.q.sp.held, a.causal ? p2 + 1 : wk.q.sp.kv_len);
+        lo[n][k] = a.window > 0 ? p2 - a.window + 1 : 0;
+      }
+    }
+    if (P::kQs) __syncthreads();
+    int all_lo = lo[0][0], all_hi = hi[0][0];  // what every column sees
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        all_lo = max(all_lo, lo[n][k]);
+        all_hi = min(all_hi, hi[n][k]);
+      }
+    all_lo = __reduce_max_sync(kFull, all_lo);
+    all_hi = __reduce_min_sync(kFull, all_hi);
+
+    float m[NT][2], l[NT][2], bias[NT][2][G], o[NT][G][4][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[n][k] = -INFINITY;
+        l[n][k] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) bias[n][k][gr] = 0.f;
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][gr][j][i] = 0.f;
+    }
+    float unit = 1.f, inv = 1.f, limit = 0.f;  // 2^E, 2^-E, and the largest scale that 2^-E takes in
+
+    for (int it = wk.i0 + warp; it < wk.i1; it += kSplitWarps) {
+      cp_wait<ST - 1>();
+      __syncwarp();
+      const unsigned char* st = ring + slot * P::kStage;
+      const int t0 = wk.q.begin + it * TT;
+      const int gaps = s_gaps[warp][slot];
+      const bool masked = gaps || t0 < all_lo || t0 + TT > all_hi;
+
+      // ---- scores
+      float s[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const unsigned char* kc = st + mt * (8 * D);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][n][i] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const uint2 w0 = *reinterpret_cast<const uint2*>(kc + (koff ^ (gr * 32)));
+          const uint2 w1 = *reinterpret_cast<const uint2*>(kc + 4 * D + (koff ^ (gr * 32)));
+          float acc[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[n][0] = acc[n][2] = -64.f * xs[n][0][gr];
+            acc[n][1] = acc[n][3] = -64.f * xs[n][1][gr];
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t r0 = w ? w0.y : w0.x, r1 = w ? w1.y : w1.x;
+            uint32_t f0[4], f1[4];  // 64 + code, pairs (i, i + 4)
+            f0[0] = and_or(r0 << 4, 0x00F000F0u, 0x54005400u);
+            f1[0] = and_or(r1 << 4, 0x00F000F0u, 0x54005400u);
+            f0[1] = and_or(r0, 0x00F000F0u, 0x54005400u);
+            f1[1] = and_or(r1, 0x00F000F0u, 0x54005400u);
+            f0[2] = and_or(r0 >> 4, 0x00F000F0u, 0x54005400u);
+            f1[2] = and_or(r1 >> 4, 0x00F000F0u, 0x54005400u);
+            f0[3] = and_or(r0 >> 8, 0x00F000F0u, 0x54005400u);
+            f1[3] = and_or(r1 >> 8, 0x00F000F0u, 0x54005400u);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int step = (n * G + gr) * 4 + w * 2 + i;
+                uint32_t b0, b1;
+                if (P::kQs) {
+                  const uint2 q2 = qf_s[step * 32 + lane];
+                  b0 = q2.x;
+                  b1 = q2.y;
+                } else {
+                  b0 = qf[step * 2];
+                  b1 = qf[step * 2 + 1];
+                }
+                mma16816(acc[n], f0[2 * i], f1[2 * i], f0[2 * i + 1], f1[2 * i + 1], b0, b1);
+              }
+            }
+          }
+          const uint32_t* kp = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode) + mt * 16 * G;
+          const uint32_t p0 = kp[g * G + gr], p1 = kp[(g + 8) * G + gr];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], fmaf(bf16hi(p0), xs[n][0][gr], s[mt][n][0]));
+            s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], fmaf(bf16hi(p0), xs[n][1][gr], s[mt][n][1]));
+            s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], fmaf(bf16hi(p1), xs[n][0][gr], s[mt][n][2]));
+            s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], fmaf(bf16hi(p1), xs[n][1][gr], s[mt][n][3]));
+          }
+        }
+      }
+      // ---- V's pairs, masks, the maximum
+      float vs[MT][2][G], vb[MT][2][G];
+      float big = 0.f;
+      bool raise = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode + P::kSb) + (mt * 16 + r * 8 + g) * G;
+          const int t = t0 + mt * 16 + r * 8 + g;
+          const bool some = !masked || (!(gaps >> mt & 1) && t < wk.q.sp.held);
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const uint32_t pr = some ? vp[gr] : 0u;
+            vs[mt][r][gr] = bf16lo(pr);
+            vb[mt][r][gr] = fmaf(8.f, bf16lo(pr), bf16hi(pr));
+            const float mag = fabsf(vs[mt][r][gr]);
+            if (mag < INFINITY) big = fmaxf(big, mag);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float& v = s[mt][n][r * 2 + k];
+              v *= cs[n][k];
+              if (masked && (!some || t < lo[n][k] || t >= hi[n][k])) v = -INFINITY;
+              raise |= v > m[n][k] + 8.f;
+            }
+        }
+      if (__any_sync(kFull, raise || big > limit)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = m[n][k];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(s[mt][n][k], s[mt][n][2 + k]));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+            const float f = m[n][k] == top ? 1.f : ex2(m[n][k] - top);
+            m[n][k] = top;
+            l[n][k] *= f;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              bias[n][k][gr] *= f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                o[n][gr][j][k] *= f;
+                o[n][gr][j][2 + k] *= f;
+              }
+            }
+          }
+        big = warp_max(big);
+        if (big > limit) {  // p 2^-E s below 2^8 2^6
+          const int e = min(max((int)(__float_as_uint(big) >> 23) - 132, -120), 120);
+          const float f = limit > 0.f ? unit * exp2i(-e) : 0.f;
+          unit = exp2i(e);
+          inv = exp2i(-e);
+          limit = exp2i(min(e + 6, 127));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][gr][j][i] *= f;
+        }
+      }
+      // ---- probabilities, and the output
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t bf[NT][G][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float p[2];
+            bool gone[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float v = s[mt][n][r * 2 + k];
+              p[k] = ex2(v - (m[n][k] == -INFINITY ? 0.f : m[n][k]));
+              gone[k] = masked && v == -INFINITY;
+              l[n][k] += p[k];
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              // a token that the mask hides adds nothing, whatever its pair holds
+#pragma unroll
+              for (int k = 0; k < 2; ++k) bias[n][k][gr] = gone[k] ? bias[n][k][gr] : fmaf(p[k], vb[mt][r][gr], bias[n][k][gr]);
+              const float sc = vs[mt][r][gr] * inv;
+              bf[n][gr][r] = movm(half2_of(gone[0] ? 0.f : p[0] * sc, gone[1] ? 0.f : p[1] * sc));
+            }
+          }
+        const unsigned char* vc = st + P::kCode + mt * (8 * D);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const uint32_t w00 = *reinterpret_cast<const uint32_t*>(vc + (voff0 ^ (gr * 32)));
+          const uint32_t w01 = *reinterpret_cast<const uint32_t*>(vc + (voff1 ^ (gr * 32)));
+          const uint32_t w10 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff0 ^ (gr * 32)));
+          const uint32_t w11 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff1 ^ (gr * 32)));
+          uint32_t r[4] = {__byte_perm(w00, w01, 0x5410), __byte_perm(w00, w01, 0x7632), __byte_perm(w10, w11, 0x5410),
+                           __byte_perm(w10, w11, 0x7632)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // code - 8 of dims 8g + j (row g) and 8g + 4 + j (row g + 8)
+            uint32_t f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = j & 2 ? r[i] >> 8 : r[i];
+              f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u)  // (1024 + 16q)/16 - 72
+                           : hadd2_u(and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u);              // 1024 + q - 1032
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][gr][j], f[0], f[1], f[2], f[3], bf[n][gr][0], bf[n][gr][1]);
+          }
+        }
+      }
+      __syncwarp();
+      fetch(slot);
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+
+    // ---- join the CTA's warps
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[n][k] += __shfl_xor_sync(kFull, l[n][k], x);
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) bias[n][k][gr] += __shfl_xor_sync(kFull, bias[n][k][gr], x);
+        }
+        if (g == 0) s_m[warp][n * 8 + 2 * c + k] = m[n][k];
+      }
+    __syncthreads();
+    float f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * c + k]);
+        f[n][k] = m[n][k] == top ? 1.f : ex2(m[n][k] - top);
+        if (g == 0) s_l[warp][n * 8 + 2 * c + k] = l[n][k] * f[n][k];
+      }
+    const bool whole = wk.i0 == 0 && wk.i1 == wk.q.tiles;
+    const SplitWs ws{reinterpret_cast<int*>(static_cast<char*>(a.ws) + 256), reinterpret_cast<float*>(static_cast<char*>(a.ws) + kSplitHead)};
+    float* part = ws.part + ((long long)cta * 2 + (wk.i0 == 0)) * (C * (D + 2));
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += RD) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int gr = d0 / 64; gr < (d0 + RD) / 64; ++gr) {
+            float* dst = area + (warp * C + n * 8 + 2 * c + k) * RS + (gr - d0 / 64) * 64 + g * 8;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = fmaf(o[n][gr][j][k], unit, bias[n][k][gr]) * f[n][k];
+              v[4 + j] = fmaf(o[n][gr][j][2 + k], unit, bias[n][k][gr]) * f[n][k];
+            }
+            *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          }
+      __syncthreads();
+      for (int i = threadIdx.x; i < ncol * (RD / 4); i += kSplitThreads) {
+        const int col = i / (RD / 4), d4 = i % (RD / 4) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(area + (w * C + col) * RS + d4);
+          acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+          sum += s_l[w][col];
+        }
+        if (whole) {
+          const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
+          const float r = sum == 0.f ? 0.f : 1.f / sum;
+          if (row >= 0 && row < a.v.rows)
+            *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + (h * group + hh) * D + d0 + d4) =
+                make_uint2((uint32_t)f2bf(acc.x * r) | (uint32_t)f2bf(acc.y * r) << 16,
+                           (uint32_t)f2bf(acc.z * r) | (uint32_t)f2bf(acc.w * r) << 16);
+        } else {
+          *reinterpret_cast<float4*>(part + col * D + d0 + d4) = acc;
+        }
+      }
+      if (d0 + RD < D) __syncthreads();
+    }
+    if ((int)threadIdx.x < ncol) {
+      const int col = threadIdx.x;
+      float sum = 0.f, top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) {
+        sum += s_l[w][col];
+        top = fmaxf(top, s_m[w][col]);
+      }
+      if (whole) {
+        const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
+        if (a.lse && row >= 0 && row < a.v.rows)
+          a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+      } else {
+        part[C * D + col] = top;
+        part[C * D + C + col] = sum;
+      }
+    }
+    if (!whole) {  // the last CTA to arrive joins the unit's parts
+      const long long u0 = wk.x - wk.i0, u1 = u0 + wk.q.tiles - 1;  // the unit's first and last tile in the list
+      const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int last = atomicAdd(ws.count + c0, 1) == c1 - c0;
+        if (last) ws.count[c0] = 0;
+        s_last = last;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const int np = c1 - c0 + 1;
+        auto at = [&](int i) { return ws.part + ((long long)(c0 + i) * 2 + (i == 0)) * (C * (D + 2)); };
+        for (int i = threadIdx.x; i < ncol * (D / 4); i += kSplitThreads) {
+          const int col = i / (D / 4), d4 = i % (D / 4) * 4;
+          float top = -INFINITY;
+          for (int p = 0; p < np; ++p) top = fmaxf(top, __ldcg(at(p) + C * D + col));
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum = 0.f;
+#pragma unroll 8
+          for (int p = 0; p < np; ++p) {
+            const float* pp = at(p);
+            const float mp = __ldcg(pp + C * D + col);
+            const float w = mp == top ? 1.f : ex2(mp - top);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + col * D + d4));
+            acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
+            sum = fmaf(w, __ldcg(pp + C * D + C + col), sum);
+          }
+          const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
+          const float r = sum == 0.f ? 0.f : 1.f / sum;
+          if (row >= 0 && row < a.v.rows) {
+            *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + (h * group + hh) * D + d4) =
+                make_uint2((uint32_t)f2bf(acc.x * r) | (uint32_t)f2bf(acc.y * r) << 16,
+                           (uint32_t)f2bf(acc.z * r) | (uint32_t)f2bf(acc.w * r) << 16);
+            if (a.lse && d4 == 0)
+              a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+          }
+        }
+      }
+    }
+    __syncthreads();  // the join area and the sums are free again
+  }
+  cp_wait<0>();
+}
+
+// Columns a unit takes: the smallest of 8 and 16 that holds a whole sequence's, else 16.
+static int split_nt(int max_q, int q_heads, int kv_heads) { return (long long)max_q * (q_heads / kv_heads) <= 8 ? 1 : 2; }
+
+static int split_grid(int d, int nt) {
+  const int n = num_sms() * (d == 256 && nt == 2 ? 1 : 2);
+  return n < kSplitMaxGrid ? n : kSplitMaxGrid;
+}
+
+size_t split_workspace_bytes(int max_q, int q_heads, int kv_heads, int d) {
+  const int nt = split_nt(max_q, q_heads, kv_heads);
+  return kSplitHead + (((size_t)split_grid(d, nt) * 2 * 8 * nt * (d + 2) * 4 + 255) & ~(size_t)255);
+}
+
+template <int D, int NT>
+static cudaError_t launch_split_t(const AttnArgs& a, cudaStream_t s) {
+  using P = Split<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(k_attn_split<D, NT>, split_grid(D, NT), kSplitThreads, P::kSmem, s, a);
+}
+
+cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s) {
+  const int nt = split_nt(a.max_q, a.q_heads, a.c.kv_heads);
+  switch (a.c.head_dim) {
+    case 64: return nt == 1 ? launch_split_t<64, 1>(a, s) : launch_split_t<64, 2>(a, s);
+    case 128: return nt == 1 ? launch_split_t<128, 1>(a, s) : launch_split_t<128, 2>(a, s);
+    default: return nt == 1 ? launch_split_t<256, 1>(a, s) : launch_split_t<256, 2>(a, s);
+  }
+}
+
+}  // namespace bgq
