@@ -81,6 +81,7 @@ struct AttnArgs {
   float* lse;  // nullable
   long long q_stride, out_stride;
   int q_heads, causal, window, max_q;
+  int page_shift;  // log2 of the page size, or -1
   float scale;
   long long split_cols;  // sequences of at most so many columns (rows * heads that share a key head) are kv4_split.cu's
   void* ws;

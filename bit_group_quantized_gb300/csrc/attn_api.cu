@@ -27,7 +27,7 @@ int check_cache(const bgq_kv4_cache* c) {
   if (!al(c->k_q, 16) || !al(c->k_sb, 16) || !al(c->v_q, 16) || !al(c->v_sb, 16)) return BGQ_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->page_size < 16 || c->page_size % 16 || c->kv_heads < 1) return BGQ_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return BGQ_ERR_UNSUPPORTED;
-  if (c->kv_heads > kMaxHeads) return BGQ_ERR_UNSUPPORTED;
+  if (c->kv_heads > kMaxHeads || (int64_t)c->n_pages * c->kv_heads > INT32_MAX) return BGQ_ERR_UNSUPPORTED;
   return BGQ_OK;
 }
 
@@ -175,6 +175,7 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   a.causal = causal != 0;
   a.window = window;
   a.max_q = s->max_q;
+  a.page_shift = (c->page_size & (c->page_size - 1)) ? -1 : __builtin_ctz(c->page_size);
   a.scale = scale;
   a.ws = ws;
   return cuda_status(launch_attn(a, st(stream)));

@@ -130,7 +130,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int b) {
 struct Walk {
   int b;
   SeqTiles q;
-  long long unit;
+  int h, rt;  // the unit: key head and column tile
   int i0, i1;
   long long x, x1;  // list position of i0, end of the CTA's share
 
@@ -140,8 +140,12 @@ struct Walk {
     x += i1 - i0;
     if (x >= x1) return;
     i0 = 0;
-    if (++unit >= q.units) {
-      unit = 0;
+    if (++rt >= q.rtiles) {
+      rt = 0;
+      ++h;
+    }
+    if (h >= a.c.kv_heads) {
+      h = 0;
       do q = seq_tiles<TT, C>(a, ++b);
       while (q.units == 0 && b + 1 < a.v.batch);
     }
@@ -153,6 +157,180 @@ struct SplitWs {
   int* count;   // [grid] arrivals at the unit that CTA c began and did not end; left at zero
   float* part;  // [grid][2][C][D + 2]: slot 0 a unit begun by an earlier CTA, slot 1 a unit that goes on
 };
+
+// A warp's state over a segment; columns 2c and 2c + 1 of each eight.
+template <int D, int NT>
+struct SplitAcc {
+  static constexpr int G = D / kGroup;
+  float m[NT][2], mm[NT][2];      // the maximum the probabilities refer to; the same, or 0 before the first score
+  float l[NT][2], bias[NT][2][G];  // this lane's tokens' sums of p, and of p (b + 8 s)
+  float o[NT][G][4][4];           // sum of (code - 8) p s, in units of 2^E
+  float cs[NT][2];                // scale * log2(e) / 2^shift
+  int hi[NT][2], lo[NT][2];       // the tokens that the columns see: lo <= t < hi
+  float unit, inv;                // 2^E, 2^-E
+  uint32_t limit;                 // bits of the largest scale that 2^-E takes in
+};
+
+// What follows a tile's scores s; MASKED where some column does not see all of its tokens.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT>::MT][NT][4], const unsigned char* st,
+                                             int t0, int gaps, int held, int g, int voff0, int voff1) {
+  using P = Split<D, NT>;
+  constexpr int G = P::G, MT = P::MT;
+  bool hid[MT][NT][4];
+  uint32_t vp[MT][2][G], big = 0;  // V's pairs; the largest scale, as bits
+  bool raise = false;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode + P::kSb) + (mt * 16 + r * 8 + g) * G;
+      const int t = t0 + mt * 16 + r * 8 + g;
+      const bool some = !MASKED || (!(gaps >> mt & 1) && t < held);
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        vp[mt][r][gr] = src[gr];
+        if (MASKED && !some) vp[mt][r][gr] = 0u;
+        big = max(big, vp[mt][r][gr] << 16);
+      }
+      if (MASKED) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            hid[mt][n][r * 2 + k] = !some || t < A.lo[n][k] || t >= A.hi[n][k];
+            if (hid[mt][n][r * 2 + k]) s[mt][n][r * 2 + k] = -INFINITY;
+          }
+      }
+    }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float top = s[0][n][k];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, mt ? fmaxf(s[mt][n][k], s[mt][n][2 + k]) : s[mt][n][2 + k]);
+      raise |= top * A.cs[n][k] > A.m[n][k] + 8.f;
+    }
+  // a scale with its sign set, an infinity or a NaN compares as large: looked at more closely there
+  if (__any_sync(kFull, raise || big > A.limit)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(s[mt][n][k], s[mt][n][2 + k]));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+        top = fmaxf(A.m[n][k], top * A.cs[n][k]);
+        const float f = A.m[n][k] == top ? 1.f : ex2(A.m[n][k] - top);
+        A.m[n][k] = top;
+        A.mm[n][k] = top == -INFINITY ? 0.f : top;
+        A.l[n][k] *= f;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          A.bias[n][k][gr] *= f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            A.o[n][gr][j][k] *= f;
+            A.o[n][gr][j][2 + k] *= f;
+          }
+        }
+      }
+    big = 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const uint32_t mag = (vp[mt][r][gr] & 0x7fffu) << 16;
+          if (mag < 0x7f800000u) big = max(big, mag);
+        }
+    big = __reduce_max_sync(kFull, big);
+    if (big > A.limit) {  // from here on p 2^-E s stays below 2^8 2^6
+      const int e = min(max((int)(big >> 23) - 132, -120), 120);
+      const float f = A.limit ? A.unit * exp2i(-e) : 0.f;
+      A.unit = exp2i(e);
+      A.inv = exp2i(-e);
+      A.limit = __float_as_uint(exp2i(e + 6));
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A.o[n][gr][j][i] *= f;
+    }
+  }
+  // ---- probabilities, and the output
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    uint32_t bf[NT][G][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float sc[G], vb[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const float v = bf16lo(vp[mt][r][gr]);
+        sc[gr] = v * A.inv;
+        vb[gr] = fmaf(8.f, v, bf16hi(vp[mt][r][gr]));
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          p[k] = ex2(fmaf(s[mt][n][r * 2 + k], A.cs[n][k], -A.mm[n][k]));
+          if (MASKED && hid[mt][n][r * 2 + k]) p[k] = 0.f;
+          A.l[n][k] += p[k];
+        }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          // a token that the mask hides adds nothing, whatever its pair holds
+          float ps[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            ps[k] = p[k] * sc[gr];
+            const float bs = fmaf(p[k], vb[gr], A.bias[n][k][gr]);
+            const bool gone = MASKED && hid[mt][n][r * 2 + k];
+            if (gone) ps[k] = 0.f;
+            A.bias[n][k][gr] = gone ? A.bias[n][k][gr] : bs;
+          }
+          bf[n][gr][r] = movm(half2_of(ps[0], ps[1]));
+        }
+      }
+    }
+    const unsigned char* vc = st + P::kCode + mt * (8 * D);
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      const uint32_t w00 = *reinterpret_cast<const uint32_t*>(vc + (voff0 ^ (gr * 32)));
+      const uint32_t w01 = *reinterpret_cast<const uint32_t*>(vc + (voff1 ^ (gr * 32)));
+      const uint32_t w10 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff0 ^ (gr * 32)));
+      const uint32_t w11 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff1 ^ (gr * 32)));
+      uint32_t r[4] = {__byte_perm(w00, w01, 0x5410), __byte_perm(w00, w01, 0x7632), __byte_perm(w10, w11, 0x5410),
+                       __byte_perm(w10, w11, 0x7632)};
+      uint32_t r8[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r8[i] = r[i] >> 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // code - 8 of dims 8g + j (row g) and 8g + 4 + j (row g + 8)
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = j & 2 ? r8[i] : r[i];
+          f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u)  // (1024 + 16q)/16 - 72
+                       : hadd2_u(and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u);              // 1024 + q - 1032
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(A.o[n][gr][j], f[0], f[1], f[2], f[3], bf[n][gr][0], bf[n][gr][1]);
+      }
+    }
+  }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_split(const __grid_constant__ AttnArgs a) {
@@ -212,7 +390,9 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   __syncthreads();
   wk.b = s_b;
   wk.q = seq_tiles<TT, C>(a, wk.b);
-  wk.unit = (wk.x - s_base) / wk.q.tiles;
+  const int unit0 = (int)((wk.x - s_base) / wk.q.tiles);
+  wk.h = unit0 / wk.q.rtiles;
+  wk.rt = unit0 - wk.h * wk.q.rtiles;
   wk.i0 = (int)((wk.x - s_base) % wk.q.tiles);
   wk.i1 = (int)min((long long)wk.q.tiles, wk.i0 + wk.x1 - wk.x);
 
@@ -228,16 +408,25 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       fi = fw.i0 + warp;
     }
     if (fw.live()) {
-      const int t0 = fw.q.begin + fi * TT, h = (int)(fw.unit / fw.q.rtiles);
+      const int t0 = fw.q.begin + fi * TT;
       const uint32_t dst = ring_u + slot * P::kStage;
       int gaps = 0;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {  // 16 tokens lie in one page
         const int t = t0 + 16 * m;
-        const int page = t < fw.q.sp.held ? kv4_page(a.v, fw.b, t) : -1;
-        const bool ok = page >= 0;
+        int pg, at_p;  // page of the list, place in it
+        if (a.page_shift >= 0) {
+          pg = t >> a.page_shift;
+          at_p = t & (a.c.page_size - 1);
+        } else {
+          pg = t / a.c.page_size;
+          at_p = t - pg * a.c.page_size;
+        }
+        int page = -1;
+        if (t < fw.q.sp.held) page = a.v.pages ? a.v.pages[(long long)fw.b * a.v.max_pages + pg] : fw.b;
+        const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
         gaps |= ok ? 0 : 1 << m;
-        const long long row = ok ? ((long long)page * heads + h) * a.c.page_size + t % a.c.page_size : 0;
+        const long long row = ok ? (long long)(page * heads + fw.h) * a.c.page_size + at_p : 0;
         const char* ks = reinterpret_cast<const char*>(a.c.k_q) + row * (D / 2) + lane * 16;
         const char* vs = reinterpret_cast<const char*>(a.c.v_q) + row * (D / 2) + lane * 16;
 #pragma unroll
@@ -285,14 +474,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   }
 
   for (; wk.live(); wk.template next<TT, C>(a)) {
-    const int h = (int)(wk.unit / wk.q.rtiles), col0 = (int)(wk.unit - (long long)h * wk.q.rtiles) * C;
+    const int h = wk.h, col0 = wk.rt * C;
     const int ncol = min(C, wk.q.sp.q_len * group - col0);
     const int pos0 = wk.q.sp.kv_len - wk.q.sp.q_len;
 
     // ---- the query: fp16 fragments of column g, scaled by a power of two
     uint32_t qf[P::kQs ? 1 : NT * G * 8];
-    float xs[NT][2][G], cs[NT][2];  // of columns 2c, 2c+1: group sums, and scale * log2(e) / 2^shift
-    int hi[NT][2], lo[NT][2];       // the tokens that columns 2c, 2c+1 see: lo <= t < hi
+    float xs[NT][2][G];             // group sums of columns 2c, 2c + 1
+    SplitAcc<D, NT> A;
     if (P::kQs) __syncthreads();    // the last segment's fragments are read
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -318,7 +507,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
       // largest magnitude into [8, 16): fp16 keeps 2^-28 of it
       const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
-      const float up = exp2i(-e);
+      const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
       float sum[G];
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
@@ -353,45 +542,46 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
         const int from = (2 * c + k) * 4;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) xs[n][k][gr] = __shfl_sync(kFull, sum[gr], from);
-        cs[n][k] = a.scale * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from));
+        // at least the smallest normal number, so that -infinity times it stays -infinity
+        A.cs[n][k] = fmaxf(fabsf(a.scale) * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from)), 0x1p-126f);
         const int cc = n * 8 + 2 * c + k, jj = (col0 + cc) / group;
         const int pos = pos0 + jj;
         // columns behind the last see what the first one sees, and are dropped at the end
         const int p2 = cc < ncol ? pos : pos0 + col0 / group;
-        hi[n][k] = min(wk.q.sp.held, a.causal ? p2 + 1 : wk.q.sp.kv_len);
-        lo[n][k] = a.window > 0 ? p2 - a.window + 1 : 0;
+        A.hi[n][k] = min(wk.q.sp.held, a.causal ? p2 + 1 : wk.q.sp.kv_len);
+        A.lo[n][k] = a.window > 0 ? p2 - a.window + 1 : 0;
       }
     }
     if (P::kQs) __syncthreads();
-    int all_lo = lo[0][0], all_hi = hi[0][0];  // what every column sees
+    int all_lo = A.lo[0][0], all_hi = A.hi[0][0];  // what every column sees
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        all_lo = max(all_lo, lo[n][k]);
-        all_hi = min(all_hi, hi[n][k]);
+        all_lo = max(all_lo, A.lo[n][k]);
+        all_hi = min(all_hi, A.hi[n][k]);
       }
     all_lo = __reduce_max_sync(kFull, all_lo);
     all_hi = __reduce_min_sync(kFull, all_hi);
 
-    float m[NT][2], l[NT][2], bias[NT][2][G], o[NT][G][4][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[n][k] = -INFINITY;
-        l[n][k] = 0.f;
+        A.m[n][k] = -INFINITY;
+        A.mm[n][k] = A.l[n][k] = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) bias[n][k][gr] = 0.f;
+        for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] = 0.f;
       }
 #pragma unroll
       for (int gr = 0; gr < G; ++gr)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][gr][j][i] = 0.f;
+          for (int i = 0; i < 4; ++i) A.o[n][gr][j][i] = 0.f;
     }
-    float unit = 1.f, inv = 1.f, limit = 0.f;  // 2^E, 2^-E, and the largest scale that 2^-E takes in
+    A.unit = A.inv = 1.f;
+    A.limit = 0;
 
     for (int it = wk.i0 + warp; it < wk.i1; it += kSplitWarps) {
       cp_wait<ST - 1>();
@@ -461,125 +651,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
           }
         }
       }
-      // ---- V's pairs, masks, the maximum
-      float vs[MT][2][G], vb[MT][2][G];
-      float big = 0.f;
-      bool raise = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode + P::kSb) + (mt * 16 + r * 8 + g) * G;
-          const int t = t0 + mt * 16 + r * 8 + g;
-          const bool some = !masked || (!(gaps >> mt & 1) && t < wk.q.sp.held);
-#pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            const uint32_t pr = some ? vp[gr] : 0u;
-            vs[mt][r][gr] = bf16lo(pr);
-            vb[mt][r][gr] = fmaf(8.f, bf16lo(pr), bf16hi(pr));
-            const float mag = fabsf(vs[mt][r][gr]);
-            if (mag < INFINITY) big = fmaxf(big, mag);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float& v = s[mt][n][r * 2 + k];
-              v *= cs[n][k];
-              if (masked && (!some || t < lo[n][k] || t >= hi[n][k])) v = -INFINITY;
-              raise |= v > m[n][k] + 8.f;
-            }
-        }
-      if (__any_sync(kFull, raise || big > limit)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float top = m[n][k];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(s[mt][n][k], s[mt][n][2 + k]));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-            const float f = m[n][k] == top ? 1.f : ex2(m[n][k] - top);
-            m[n][k] = top;
-            l[n][k] *= f;
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-              bias[n][k][gr] *= f;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                o[n][gr][j][k] *= f;
-                o[n][gr][j][2 + k] *= f;
-              }
-            }
-          }
-        big = warp_max(big);
-        if (big > limit) {  // p 2^-E s below 2^8 2^6
-          const int e = min(max((int)(__float_as_uint(big) >> 23) - 132, -120), 120);
-          const float f = limit > 0.f ? unit * exp2i(-e) : 0.f;
-          unit = exp2i(e);
-          inv = exp2i(-e);
-          limit = exp2i(min(e + 6, 127));
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][gr][j][i] *= f;
-        }
-      }
-      // ---- probabilities, and the output
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t bf[NT][G][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float p[2];
-            bool gone[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float v = s[mt][n][r * 2 + k];
-              p[k] = ex2(v - (m[n][k] == -INFINITY ? 0.f : m[n][k]));
-              gone[k] = masked && v == -INFINITY;
-              l[n][k] += p[k];
-            }
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-              // a token that the mask hides adds nothing, whatever its pair holds
-#pragma unroll
-              for (int k = 0; k < 2; ++k) bias[n][k][gr] = gone[k] ? bias[n][k][gr] : fmaf(p[k], vb[mt][r][gr], bias[n][k][gr]);
-              const float sc = vs[mt][r][gr] * inv;
-              bf[n][gr][r] = movm(half2_of(gone[0] ? 0.f : p[0] * sc, gone[1] ? 0.f : p[1] * sc));
-            }
-          }
-        const unsigned char* vc = st + P::kCode + mt * (8 * D);
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          const uint32_t w00 = *reinterpret_cast<const uint32_t*>(vc + (voff0 ^ (gr * 32)));
-          const uint32_t w01 = *reinterpret_cast<const uint32_t*>(vc + (voff1 ^ (gr * 32)));
-          const uint32_t w10 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff0 ^ (gr * 32)));
-          const uint32_t w11 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff1 ^ (gr * 32)));
-          uint32_t r[4] = {__byte_perm(w00, w01, 0x5410), __byte_perm(w00, w01, 0x7632), __byte_perm(w10, w11, 0x5410),
-                           __byte_perm(w10, w11, 0x7632)};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // code - 8 of dims 8g + j (row g) and 8g + 4 + j (row g + 8)
-            uint32_t f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w = j & 2 ? r[i] >> 8 : r[i];
-              f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u)  // (1024 + 16q)/16 - 72
-                           : hadd2_u(and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u);              // 1024 + q - 1032
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][gr][j], f[0], f[1], f[2], f[3], bf[n][gr][0], bf[n][gr][1]);
-          }
-        }
-      }
+      if (masked) split_finish<D, NT, true>(A, s, st, t0, gaps, wk.q.sp.held, g, voff0, voff1);
+      else split_finish<D, NT, false>(A, s, st, t0, gaps, wk.q.sp.held, g, voff0, voff1);
       __syncwarp();
       fetch(slot);
       slot = slot + 1 == ST ? 0 : slot + 1;
@@ -592,11 +665,11 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
-          l[n][k] += __shfl_xor_sync(kFull, l[n][k], x);
+          A.l[n][k] += __shfl_xor_sync(kFull, A.l[n][k], x);
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) bias[n][k][gr] += __shfl_xor_sync(kFull, bias[n][k][gr], x);
+          for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] += __shfl_xor_sync(kFull, A.bias[n][k][gr], x);
         }
-        if (g == 0) s_m[warp][n * 8 + 2 * c + k] = m[n][k];
+        if (g == 0) s_m[warp][n * 8 + 2 * c + k] = A.m[n][k];
       }
     __syncthreads();
     float f[NT][2];
@@ -607,8 +680,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * c + k]);
-        f[n][k] = m[n][k] == top ? 1.f : ex2(m[n][k] - top);
-        if (g == 0) s_l[warp][n * 8 + 2 * c + k] = l[n][k] * f[n][k];
+        f[n][k] = A.m[n][k] == top ? 1.f : ex2(A.m[n][k] - top);
+        if (g == 0) s_l[warp][n * 8 + 2 * c + k] = A.l[n][k] * f[n][k];
       }
     const bool whole = wk.i0 == 0 && wk.i1 == wk.q.tiles;
     const SplitWs ws{reinterpret_cast<int*>(static_cast<char*>(a.ws) + 256), reinterpret_cast<float*>(static_cast<char*>(a.ws) + kSplitHead)};
@@ -625,8 +698,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
             float v[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              v[j] = fmaf(o[n][gr][j][k], unit, bias[n][k][gr]) * f[n][k];
-              v[4 + j] = fmaf(o[n][gr][j][2 + k], unit, bias[n][k][gr]) * f[n][k];
+              v[j] = fmaf(A.o[n][gr][j][k], A.unit, A.bias[n][k][gr]) * f[n][k];
+              v[4 + j] = fmaf(A.o[n][gr][j][2 + k], A.unit, A.bias[n][k][gr]) * f[n][k];
             }
             *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);

@@ -81,7 +81,8 @@ def slot(t: int, b: int, pages, page_size: int, n_pages: int):
 
 def kv4_attention(cache, kv_len, q_start, rows, pages, q, scale, causal=True, window=0):
     """cache: (k_q, k_sb bits, v_q, v_sb bits) as [n_pages][heads][page_size][..]; q [rows][q_heads][d] float64.
-    Returns out and lse (NaN in rows of no sequence), sum p |v| and max_t scale * sum |q k| (for error bounds)."""
+    Returns out and lse (NaN in rows of no sequence), and for error bounds sum p (|v| + 8 s), s the scale of v's group,
+    and max_t scale * sum |q k|."""
     k_q, k_sb, v_q, v_sb = cache
     n_pages, hkv, size = k_q.shape[:3]
     hq, d = q.shape[1:]
@@ -101,6 +102,7 @@ def kv4_attention(cache, kv_len, q_start, rows, pages, q, scale, causal=True, wi
         if window > 0:
             seen &= tok[None] > pos[:, None] - window
         for h in range(hkv):
+            vs = np.repeat(np.abs(bf16_to_f64(v_sb[page, h, place])[..., 0]), GROUP, -1)
             K, V = kv4_values(k_q[page, h, place], k_sb[page, h, place]), kv4_values(v_q[page, h, place], v_sb[page, h, place])
             for g in range(h * hq // hkv, (h + 1) * hq // hkv):
                 for j in range(m):  # row by row: what a row may not see never enters its sums
@@ -114,6 +116,6 @@ def kv4_attention(cache, kv_len, q_start, rows, pages, q, scale, causal=True, wi
                     e = np.exp(s - top)
                     lse[first + j, g] = top + np.log(e.sum())
                     out[first + j, g] = (e / e.sum()) @ V[see]
-                    size_v[first + j, g] = (e / e.sum()) @ np.abs(V[see])
+                    size_v[first + j, g] = (e / e.sum()) @ (np.abs(V[see]) + 8 * vs[see])
                     size_s[first + j, g] = (np.abs(K[see]) @ np.abs(qj)).max() * abs(scale)
     return out, lse, size_v, size_s

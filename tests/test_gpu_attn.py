@@ -4,8 +4,10 @@ decoder layer's attention block made of them.
 Tolerances. A bf16 output is off by half a step, 2^-8 relative, beyond the kernel's own error. Attention's own error: the
 kernels round the probabilities, and whole-prompt rows also the dequantised keys and values, to fp16 (2^-11 relative
 each), so a score is off by at most 2^-11 * scale * sum|q k| =: e, a probability by 2e + 2^-10 relative, and an
-output by (2e + 2^-10 + 2^-11) * sum p|v|. Sums in fp32 over at most some thousand terms stay below 2^-12 of sum p|v|, and of
-sum|q k| for a score: 2^-9 * (1 + scale * sum|q k|) * sum p|v| covers all of them.
+output by (2e + 2^-10 + 2^-11) * sum p|v|. Few rows round p s (s the scale of v's group) instead, which multiplies
+code - 8, while p (bias + 8 s) is summed in fp32: off by 2^-11 p s |code - 8| <= 2^-11 p 8 s, which does not shrink
+where v itself is near zero, so A := sum p (|v| + 8 s) takes the place of sum p|v|. Sums in fp32 over at most some
+thousand terms stay below 2^-12 of A, and of sum|q k| for a score: 2^-9 * (1 + scale * sum|q k|) * A covers all of them.
 """
 
 import math
@@ -251,7 +253,7 @@ def attn_close(c, q, out, lse, scale=None, causal=True, window=0):
     none = np.isneginf(l)
     assert np.array_equal(np.isneginf(gl) & live, none)
     seen = live & ~none
-    assert (np.abs(gl - l) <= 2.0 ** -10 * (s + 1))[seen].all()
+    assert (np.abs(gl[seen] - l[seen]) <= 2.0 ** -10 * (s[seen] + 1)).all()
     assert (got[none] == 0).all()
     return live
 
