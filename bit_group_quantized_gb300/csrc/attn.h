@@ -83,13 +83,14 @@ struct AttnArgs {
   int q_heads, causal, window, max_q;
   int page_shift;  // log2 of the page size, or -1
   float scale;
-  long long split_cols;  // sequences of at most so many columns (rows * heads that share a key head) are kv4_split.cu's
   void* ws;
 };
 size_t attn_workspace_bytes(int batch, int rows, int max_q, int q_heads, int kv_heads, int head_dim);
-cudaError_t launch_attn(AttnArgs a, cudaStream_t s);
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 
 size_t split_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);
+size_t prompt_workspace_bytes(int batch, int rows, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace bgq

@@ -1,0 +1,912 @@
+// kv4_prompt.cu — attention over the 4-bit cache for many query rows a
+// sequence (whole prompts, chunks of one, many drafted tokens): a dense
+// contraction, on tcgen05.
+//
+// A unit is one key head of one sequence with kRows = 128 * NQ columns (a
+// column being one (query row, query head) pair that shares the key head), as
+// NQ tiles of 128 accumulator rows. Per 128 tokens:
+//   S = Q K^T   both fp16 in shared memory, S fp32 in tensor memory;
+//   P = exp2(S c - m), fp16, written over S in tensor memory;
+//   O += P V    P from tensor memory, V fp16 in shared memory.
+// The warps are specialised: four dequantise K and V (a thread takes a token: codes and
+// pairs by plain loads one tile ahead, value = code * scale + bias in fp16,
+// stored in the 128-byte swizzled layout: K as the K-major, V as the MN-major
+// operand), four for each tile of rows do the softmax (a thread owns a row: its
+// maximum and sum need no shuffles), one thread issues the MMAs. With two row tiles the
+// tensor cores multiply one while the other's softmax runs; with one (head dim 256,
+// whose O fills tensor memory) S is double-buffered.
+// The maximum is raised, and O rescaled, only where a row's scores pass it by
+// 2^8: P then reaches 2^8 at most, far inside fp16.
+//
+// Half precision's range: queries are scaled by a power of two per row, K and V
+// by one per 32 tokens where they leave [2^-6, 2^15) (else none); the softmax
+// undoes K's in the score's factor and V's in P. A key or value pair that is not
+// finite is stored as zeros, and the rows that see it are made NaN at the end.
+//
+// All (unit, key head, 128 tokens) triples form one list, which k_prompt_plan lays out from
+// the lengths on the device; every CTA takes an equal, contiguous share, and units cut by a
+// share are joined by the last CTA to arrive, in CTA order (the same bits every time).
+// Every wait is bounded: on expiry the status word is set to BGQ_ERR_TIMEOUT and all
+// later waits fall through, so the kernel ends by itself.
+#include <cuda_fp16.h>
+
+#include "attn.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace bgq {
+
+constexpr int kPrThreads = 416;  // warps 0-3: rows 0-127, 4-7: rows 128-255, 8-11: dequantisation, 12: MMAs
+constexpr int kPrTok = 128;      // tokens of a tile
+constexpr long long kPrTimeoutNs = 1000000000ll;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 4096;
+
+template <int D>
+struct Prompt {
+  static constexpr int G = D / kGroup;
+  static constexpr int NQ = D == 256 ? 1 : 2;
+  static constexpr int kRows = 128 * NQ;
+  static constexpr int ST = D == 256 ? 1 : 2;  // K and V tiles held
+  static constexpr int kTile = kPrTok * D * 2;  // bytes of a Q, K or V tile
+  // more than half an SM's, so that no second CTA comes to wait for this one's tensor memory
+  static constexpr int kSmem = 1024 + (NQ + 2 * ST) * kTile > 120 * 1024 ? 1024 + (NQ + 2 * ST) * kTile : 120 * 1024;
+  static constexpr int kSlot = 128 * D + 256;  // floats of a part: O by 4 columns and row, then m, then l
+};
+
+// A unit's place in the list.
+struct PrUnit {
+  int b, rt, tiles, begin;
+};
+struct PrPlan {  // at the start of the workspace, behind the control block
+  int units, pad;
+  long long sum;  // tiles of all units, for one key head
+};
+
+struct PrWs {
+  Ctrl* ctrl;
+  PrPlan* plan;
+  int* count;         // [grid][NQ] arrivals, left at zero
+  PrUnit* units;      // [cap]
+  long long* prefix;  // [cap] tiles before a unit
+  float* part;        // [grid][2][NQ][kSlot]
+  int cap;
+  size_t bytes;
+};
+
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+static PrWs carve_prompt(void* ws, int batch, int rows, int group, int d, int grid) {
+  char* p = static_cast<char*>(ws);
+  const int nq = d == 256 ? 1 : 2;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char* r = p ? p + at : nullptr;
+    at += up256(n);
+    return r;
+  };
+  PrWs w;
+  w.cap = (int)((long long)rows * group / (128 * nq)) + batch + 1;
+  w.ctrl = reinterpret_cast<Ctrl*>(take(sizeof(Ctrl)));
+  w.plan = reinterpret_cast<PrPlan*>(take(sizeof(PrPlan)));
+  w.count = reinterpret_cast<int*>(take((size_t)grid * nq * 4));
+  w.units = reinterpret_cast<PrUnit*>(take((size_t)w.cap * sizeof(PrUnit)));
+  w.prefix = reinterpret_cast<long long*>(take((size_t)w.cap * 8));
+  w.part = reinterpret_cast<float*>(take((size_t)grid * 2 * nq * (128 * d + 256) * 4));
+  w.bytes = at;
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// The list: one CTA; row tiles per sequence, then tiles per unit.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ long long plan_scan(long long v, long long* warp_sum, long long& total) {  // inclusive
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  return v + before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_constant__ AttnArgs a, PrWs w, int rows_unit) {
+  __shared__ int first[kPlanSeqs + 1];  // units before a sequence
+  __shared__ long long warp_sum[kPlanThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int group = a.q_heads / a.c.kv_heads;
+  constexpr int per = kPlanSeqs / kPlanThreads;
+  int n[per], own = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    n[i] = b < a.v.batch ? (int)(((long long)min(kv4_span(a.v, b).q_len, a.v.rows) * group + rows_unit - 1) / rows_unit) : 0;
+    own += n[i];
+  }
+  long long total;
+  int at = (int)(plan_scan(own, warp_sum, total) - own);
+  for (int i = 0; i < per; ++i) {
+    first[threadIdx.x * per + i] = at;
+    at += n[i];
+  }
+  const int units = (int)min(total, (long long)w.cap);  // never more, unless the rows of sequences overlap
+  __syncthreads();
+  long long sum = 0;
+  for (int base = 0; base < units; base += kPlanThreads) {
+    const int u = base + threadIdx.x;
+    PrUnit un = {0, 0, 0, 0};
+    if (u < units) {
+      int lo = 0, hi = a.v.batch;  // the last sequence whose first unit is at or before u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= u) lo = mid; else hi = mid;
+      }
+      const Span sp = kv4_span(a.v, lo);
+      const int pos0 = sp.kv_len - sp.q_len;
+      un.b = lo;
+      un.rt = u - first[lo];
+      const int j0 = (int)((long long)un.rt * rows_unit / group);
+      const int j1 = (int)min((long long)sp.q_len - 1, (((long long)un.rt + 1) * rows_unit - 1) / group);
+      un.begin = a.window > 0 ? min(max(0, pos0 + j0 - a.window + 1), sp.held) : 0;
+      const int end = a.causal ? min(sp.held, pos0 + j1 + 1) : sp.held;
+      un.tiles = max(1, (end - un.begin + kPrTok - 1) / kPrTok);  // at least one: rows that see no token are written too
+    }
+    long long chunk;
+    const long long pre = plan_scan(un.tiles, warp_sum, chunk) - un.tiles;
+    if (u < units) {
+      w.units[u] = un;
+      w.prefix[u] = sum + pre;
+    }
+    sum += chunk;
+  }
+  if (threadIdx.x == 0) {
+    w.plan->units = units;
+    w.plan->sum = sum;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tensor memory in 32 columns of the warp's 32 lanes, and waits
+// ---------------------------------------------------------------------------
+#define BGQ_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define BGQ_U8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+#define BGQ_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+__device__ __forceinline__ void pr_ld32(uint32_t t, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : BGQ_R8(r, 0), BGQ_R8(r, 8), BGQ_R8(r, 16), BGQ_R8(r, 24)
+      : "r"(t));
+}
+// Loads done: the registers pass through, so that nothing that uses them moves ahead.
+__device__ __forceinline__ void pr_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0), BGQ_U8(r, 8), BGQ_U8(r, 16), BGQ_U8(r, 24)::"memory");
+}
+__device__ __forceinline__ void pr_st16(uint32_t t, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      BGQ_I8(r, 0), BGQ_I8(r, 8)
+      : "memory");
+}
+__device__ __forceinline__ void pr_st32(uint32_t t, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      BGQ_I8(r, 0), BGQ_I8(r, 8), BGQ_I8(r, 16), BGQ_I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void pr_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+static __device__ __noinline__ void pr_wait_loop(uint64_t* m, uint32_t parity, volatile int* fail) {
+  const unsigned long long t0 = tc_time();
+  while (!*fail && !tc_mbar_try_suspend(m, parity))
+    if ((long long)(tc_time() - t0) > kPrTimeoutNs) *fail = 1;
+}
+__device__ __forceinline__ void pr_wait(uint64_t* m, uint32_t parity, volatile int* fail) {
+  if (!tc_mbar_try(m, parity)) pr_wait_loop(m, parity, fail);
+}
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Operand tiles: panels of 64 columns (128-byte rows, 128-byte swizzle, 128 rows: 16 KB).
+constexpr int kPanel = 128 * 128;
+__device__ __forceinline__ uint64_t pr_desc(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ constexpr uint32_t pr_idesc(int n, bool b_mn) {  // fp16 x fp16 -> fp32, M = 128
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ float pr_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pr_max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ uint32_t pr_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight codes of a word as fp16 values code * s + b, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t s2, uint32_t b2) {
+  uint32_t o[4];
+  const uint32_t r[4] = {w << 4, w, w >> 4, w >> 8};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // 64 + code under the exponent of 64; exact, then one rounding
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(r[i]), "r"(0x00F000F0u), "r"(0x54005400u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(0xD400D400u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(v), "r"(s2), "r"(b2));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// What the softmax needs to know of 32 tokens.
+struct PrMeta {
+  float kf;        // 2^E of the keys: a score's factor
+  int ve;          // E of the values
+  uint32_t gap;    // tokens that are absent
+  uint32_t bad;    // whether any pair is not finite (then the masks below)
+};
+constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at most two ahead of the softmax
+
+template <int D>
+struct PrShared {
+  static constexpr int G = D / kGroup, NQ = Prompt<D>::NQ, ST = Prompt<D>::ST;
+  uint64_t k_full[ST], k_free[ST], v_full[ST], v_free[ST];
+  uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], pv_done, drain;
+  PrMeta meta[kMetaTiles][4];
+  uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
+  uint32_t tmem;
+  int fail, last[NQ];
+};
+
+// A CTA's share of the list, unit by unit.
+struct PrWalk {
+  long long x, x1, sum;
+  int h, u, i0, i1;
+  PrUnit un;
+  __device__ __forceinline__ void set(const PrWs& w) { un = w.units[u]; }
+  __device__ __forceinline__ void start(const PrWs& w, long long x_, long long x1_, long long sum_, int units) {
+    x = x_;
+    x1 = x1_;
+    sum = sum_;
+    if (x >= x1) return;
+    h = (int)(x / sum);
+    const long long y = x - h * sum;
+    int lo = 0, hi = units;  // the last unit that starts at or before y
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (w.prefix[mid] <= y) lo = mid; else hi = mid;
+    }
+    u = lo;
+    set(w);
+    i0 = (int)(y - w.prefix[u]);
+    i1 = (int)min((long long)un.tiles, i0 + x1 - x);
+  }
+  __device__ __forceinline__ bool live() const { return x < x1; }
+  __device__ __forceinline__ void next(const PrWs& w, int units) {
+    x += i1 - i0;
+    if (x >= x1) return;
+    if (++u == units) {
+      u = 0;
+      ++h;
+    }
+    set(w);
+    i0 = 0;
+    i1 = (int)min((long long)un.tiles, x1 - x);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Dequantisation: 128 threads, a token each.
+// ---------------------------------------------------------------------------
+template <int D>
+struct PrRow {  // one token's codes and pairs of K or V
+  uint4 q[D / 32];
+  uint32_t sb[D / kGroup];
+};
+template <int D>
+__device__ __forceinline__ void pr_load(PrRow<D>& r, const uint32_t* q, const uint16_t* sb, long long row) {
+  if (row < 0) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / kGroup; ++i) r.sb[i] = 0;
+    return;
+  }
+  const uint4* qs = reinterpret_cast<const uint4*>(q + row * (D / 8));
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) r.q[i] = qs[i];
+  const uint32_t* ss = reinterpret_cast<const uint32_t*>(sb) + row * (D / kGroup);
+#pragma unroll
+  for (int i = 0; i < D / kGroup; ++i) r.sb[i] = ss[i];
+}
+// Writes the token's values into its row of the tile; the exponent that the 32 tokens were divided by, and
+// the tokens whose pair of a group is not finite.
+template <int D>
+__device__ __forceinline__ int pr_store(const PrRow<D>& r, unsigned char* tile, int t, uint32_t (&bad)[D / kGroup]) {
+  constexpr int G = D / kGroup;
+  float big = 0.f;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float s = bf16lo(r.sb[g]), b = bf16hi(r.sb[g]);
+    const bool fin = fabsf(s) < INFINITY && fabsf(b) < INFINITY;
+    bad[g] = __ballot_sync(kFull, !fin);
+    if (fin) big = fmaxf(big, fmaxf(fabsf(b), fminf(fabsf(fmaf(15.f, s, b)), 3e38f)));
+  }
+  const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
+  const int k = (int)(bits >> 23) - 127;
+  const int e = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+  const float down = exp2i(-e);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const bool fin = !(bad[g] >> (t & 31) & 1);
+    const float s = fin ? bf16lo(r.sb[g]) * down : 0.f, b = fin ? bf16hi(r.sb[g]) * down : 0.f;
+    const uint32_t s2 = pr_half2(s, s), b2 = pr_half2(b, b);
+    unsigned char* row = tile + g * kPanel + t * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4& q = r.q[g * 2 + (c >> 2)];
+      const uint32_t w = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
+      *reinterpret_cast<uint4*>(row + ((c ^ (t & 7)) * 16)) = pr_values(w, s2, b2);
+    }
+  }
+  return e;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
+  using P = Prompt<D>;
+  constexpr int G = P::G, NQ = P::NQ, ST = P::ST;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ PrShared<D> sh;
+  unsigned char* const smem = smem_raw + ((1024 - (tc_smem(smem_raw) & 1023)) & 1023);
+  unsigned char* const q_s = smem;
+  unsigned char* const k_s = q_s + NQ * P::kTile;
+  unsigned char* const v_s = k_s + ST * P::kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* const fail = &sh.fail;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      tc_mbar_init(&sh.k_full[i], 128);
+      tc_mbar_init(&sh.v_full[i], 128);
+      tc_mbar_init(&sh.k_free[i]);
+      tc_mbar_init(&sh.v_free[i]);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      tc_mbar_init(&sh.q_full[i], 128);
+      tc_mbar_init(&sh.o_full[i]);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc_mbar_init(&sh.s_full[i]);
+      tc_mbar_init(&sh.p_full[i], 128);
+    }
+    tc_mbar_init(&sh.pv_done);
+    tc_mbar_init(&sh.drain);
+    sh.fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  const int units = w.plan->units;
+  const long long sum = w.plan->sum, total = sum * a.c.kv_heads;
+  // at least two tiles a CTA: a cut unit costs about as much as one
+  const long long ctas = min((long long)gridDim.x, (total + 1) / 2);
+  const int cta = blockIdx.x;
+  const int group = a.q_heads / a.c.kv_heads;
+  PrWalk wk;
+  wk.x = wk.x1 = 0;
+  if (cta < ctas) wk.start(w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
+
+  if (warp < 4 * NQ) {
+    // ---------------------------------------------------------------- softmax: a thread owns a row
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
+    const uint32_t o_t = tmem + 256 + i * D + lanes;
+    uint32_t s_par = 0, o_par = 0;  // parities: s_full (bit per slot), o_full
+    uint32_t pv_par = 0;
+    for (; wk.live(); wk.next(w, units)) {
+      const Span sp = kv4_span(a.v, wk.un.b);
+      const int pos0 = sp.kv_len - sp.q_len;
+      const long long cols = (long long)min(sp.q_len, a.v.rows) * group;
+      const long long col = (long long)wk.un.rt * P::kRows + i * 128 + r;
+      const bool own = col < cols;
+      const long long cc = own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
+      const int j = (int)(cc / group), hh = (int)(cc - (long long)j * group), row = sp.first + j;
+      const bool ok = own && row >= 0 && row < a.v.rows;
+      const int pos = pos0 + j;
+      const int hi = min(sp.held, a.causal ? pos + 1 : sp.kv_len), lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int hi_min = __reduce_min_sync(kFull, hi), hi_max = __reduce_max_sync(kFull, hi);
+      const int lo_min = __reduce_min_sync(kFull, lo), lo_max = __reduce_max_sync(kFull, lo);
+      const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
+
+      // the query row: fp16, scaled by a power of two
+      float c2;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(ok ? row : 0) * a.q_stride + (wk.h * group + hh) * D);
+        float top = 0.f;
+        uint4 raw[D / 8 < 16 ? D / 8 : 16];
+        constexpr int R = D / 8 < 16 ? D / 8 : 16, PASS = D / 8 / R;
+#pragma unroll
+        for (int p = 0; p < PASS; ++p)
+#pragma unroll
+          for (int n = 0; n < R; ++n) {
+            const uint4 v = ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
+            if (p == PASS - 1) raw[n] = v;
+            float f[8];
+            unpack_bf16x8(v, f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(f[x]));
+          }
+        const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
+        const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
+        c2 = fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
+        unsigned char* qrow = q_s + i * P::kTile + r * 128;
+#pragma unroll
+        for (int p = PASS - 1; p >= 0; --p)
+#pragma unroll
+          for (int n = 0; n < R; ++n) {
+            const uint4 v = p == PASS - 1 ? raw[n] : ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
+            float f[8];
+            unpack_bf16x8(v, f);
+            const int ch = p * R + n;
+            *reinterpret_cast<uint4*>(qrow + (ch >> 3) * kPanel + (((ch & 7) ^ (r & 7)) * 16)) =
+                make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
+                           pr_half2(f[3] * up, f[7] * up));
+          }
+        tc_fence_proxy();
+        tc_arrive(&sh.q_full[i]);
+      }
+
+      float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;
+      int e_run = 0;         // O is in units of 2^e_run
+      uint32_t poison = 0;   // bit 0: a key that is not finite is seen; bit 1 + g: a value of group g
+      for (int it = wk.i0; it < wk.i1; ++it) {
+        const int slot = NQ == 2 ? i : (it - wk.i0) & 1;
+        const uint32_t s_t = tmem + slot * 128 + lanes;
+        pr_wait(&sh.s_full[slot], s_par >> slot & 1, fail);
+        s_par ^= 1u << slot;
+        tc_fence_after();
+        // tiles are numbered over the CTA's whole share: see the dequantisation
+        const int mt = (int)((wk.x + (it - wk.i0)) & (kMetaTiles - 1));
+        const int t0 = wk.un.begin + it * kPrTok;
+        if (!dead) {
+          uint32_t v[32];
+          // pass 1: the largest score
+          float top = -INFINITY;
+          int e_new = it == wk.i0 ? -1000 : e_run;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const PrMeta me = sh.meta[mt][c];
+            const int t = t0 + c * 32;
+            if (t >= hi_max || t + 32 <= lo_min) continue;
+            pr_ld32(s_t + c * 32, v);
+            e_new = max(e_new, me.ve);
+            pr_wait_ld(v);
+            if (me.gap || t < lo_max || t + 32 > hi_min) {
+              const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
+              uint32_t see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
+              see &= ~me.gap;
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] = see >> x & 1 ? v[x] : 0xff800000u;
+              if (me.bad) {
+                if (see & sh.kbad[mt][c]) poison |= 1;
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                  if (see & sh.vbad[mt][c][g]) poison |= 2u << g;
+              }
+            } else if (me.bad) {
+              if (sh.kbad[mt][c]) poison |= 1;
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+                if (sh.vbad[mt][c][g]) poison |= 2u << g;
+            }
+            float t0f = -INFINITY, t1f = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              t0f = pr_max3(t0f, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+              t1f = pr_max3(t1f, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+            }
+            top = fmaxf(top, fmaxf(t0f, t1f) * fmaxf(c2 * me.kf, 0x1p-126f));
+          }
+          if (e_new == -1000) e_new = 0;
+          const bool raise = top > m + 8.f;
+          if (__any_sync(kFull, raise || e_new != e_run)) {
+            const float up = raise ? top : m;
+            float f = up == m ? 1.f : pr_ex2(m - up);
+            m = up;
+            mm = up == -INFINITY ? 0.f : up;
+            l0 *= f;
+            l1 *= f;
+            if (it > wk.i0) {
+              f *= exp2i(max(e_run - e_new, -126));  // e_new >= e_run
+              if (NQ == 1) {  // the product before this one may still be running
+                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+                tc_fence_after();
+              }
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                pr_ld32(o_t + d, v);
+                pr_wait_ld(v);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+                pr_st32(o_t + d, v);
+              }
+            }
+            e_run = e_new;
+          }
+          // pass 2: the probabilities, over the scores
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const PrMeta me = sh.meta[mt][c];
+            const int t = t0 + c * 32;
+            uint32_t pk[16];
+            if (t >= hi_max || t + 32 <= lo_min) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) pk[x] = 0;
+              pr_st16(s_t + c * 16, pk);
+              continue;
+            }
+            pr_ld32(s_t + c * 32, v);
+            const float ck = fmaxf(c2 * me.kf, 0x1p-126f);
+            uint32_t see = 0xffffffffu;
+            if (me.gap || t < lo_max || t + 32 > hi_min) {
+              const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
+              see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
+              see &= ~me.gap;
+            }
+            const bool part = __any_sync(kFull, see != 0xffffffffu);
+            pr_wait_ld(v);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float p0 = pr_ex2(fmaf(__uint_as_float(v[x]), ck, -mm)), p1 = pr_ex2(fmaf(__uint_as_float(v[x + 1]), ck, -mm));
+              if (part) {
+                p0 = see >> x & 1 ? p0 : 0.f;
+                p1 = see >> (x + 1) & 1 ? p1 : 0.f;
+              }
+              l0 += p0;
+              l1 += p1;
+              v[x] = __float_as_uint(p0);
+              v[x + 1] = __float_as_uint(p1);
+            }
+            if (me.ve != e_run) {  // values of another unit than O
+              const float f = exp2i(max(me.ve - e_run, -126));
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[x] = pr_half2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
+            pr_st16(s_t + c * 16, pk);
+          }
+          pr_wait_st();
+        }
+        pv_par ^= 1;
+        tc_fence_before();
+        tc_arrive(&sh.p_full[slot]);
+      }
+
+      // ---- the unit's end: O / l, or a part of it
+      pr_wait(&sh.o_full[i], o_par, fail);
+      o_par ^= 1;
+      tc_fence_after();
+      const bool whole = wk.i0 == 0 && wk.i1 == wk.un.tiles;
+      float l = poison & 1 ? NAN : l0 + l1;
+      float* const part = w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot;
+      const float unit = exp2i(e_run);
+      uint16_t* out = a.out + (long long)(ok ? row : 0) * a.out_stride + (wk.h * group + hh) * D;
+      if (!dead) {
+        const float inv = l == 0.f ? 0.f : unit / l;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t v[32];
+          pr_ld32(o_t + d, v);
+          pr_wait_ld(v);
+          float f = whole ? inv : unit;
+          if (poison >> (1 + d / kGroup) & 1) f = NAN;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+          if (whole) {
+            if (ok) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) {  // columns come as 0 4 1 5 2 6 3 7
+                auto b2 = [&](int p, int q) {
+                  return (uint32_t)f2bf(__uint_as_float(v[x + p])) | (uint32_t)f2bf(__uint_as_float(v[x + q])) << 16;
+                };
+                *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; x += 4)
+              *reinterpret_cast<uint4*>(part + ((d + x) / 4 * 128 + r) * 4) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+          }
+        }
+        if (whole) {
+          if (ok && a.lse) a.lse[(long long)row * a.q_heads + wk.h * group + hh] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+        } else {
+          part[128 * D + r] = m;
+          part[128 * D + 128 + r] = l;
+        }
+      }
+      tc_fence_before();
+      if (!whole) {
+        const long long u0 = wk.x - wk.i0, u1 = u0 + wk.un.tiles - 1;
+        const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
+        __threadfence();
+        wg_sync(1 + i);
+        if (r == 0) {
+          const int last = atomicAdd(w.count + c0 * NQ + i, 1) == c1 - c0;
+          if (last) w.count[c0 * NQ + i] = 0;
+          sh.last[i] = last;
+        }
+        wg_sync(1 + i);
+        if (sh.last[i] && !dead) {
+          __threadfence();
+          auto at = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * NQ + i) * P::kSlot; };
+          float top = -INFINITY, ls = 0.f;
+          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + 128 * D + r));
+          for (int c = c0; c <= c1; ++c) {
+            const float mc = __ldcg(at(c) + 128 * D + r);
+            ls = fmaf(mc == top ? 1.f : pr_ex2(mc - top), __ldcg(at(c) + 128 * D + 128 + r), ls);
+          }
+          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+              const float mc = __ldcg(at(c) + 128 * D + r);
+              const float f = mc == top ? 1.f : pr_ex2(mc - top);
+#pragma unroll
+              for (int x = 0; x < 16; x += 4) {
+                const float4 p = __ldcg(reinterpret_cast<const float4*>(at(c) + ((d + x) / 4 * 128 + r) * 4));
+                v[x] = fmaf(f, p.x, v[x]);
+                v[x + 1] = fmaf(f, p.y, v[x + 1]);
+                v[x + 2] = fmaf(f, p.z, v[x + 2]);
+                v[x + 3] = fmaf(f, p.w, v[x + 3]);
+              }
+            }
+            if (ok) {
+#pragma unroll
+              for (int x = 0; x < 16; x += 8) {
+                auto b2 = [&](int p, int q) { return (uint32_t)f2bf(v[x + p] * inv) | (uint32_t)f2bf(v[x + q] * inv) << 16; };
+                *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
+              }
+            }
+          }
+          if (ok && a.lse) a.lse[(long long)row * a.q_heads + wk.h * group + hh] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
+        }
+      }
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---------------------------------------------------------------- dequantisation: a thread owns a token
+    const int t = tid & 127;
+    int st = 0;
+    uint32_t par = 1;  // the first pass over the ring finds it free
+    PrWalk fw = wk;    // one tile ahead
+    int ft = fw.i0;
+    PrRow<D> kr, vr;
+    bool gap_next = false;
+    auto load = [&]() {
+      if (!fw.live()) return;
+      const Span sp = kv4_span(a.v, fw.un.b);
+      const int tok = fw.un.begin + ft * kPrTok + t;
+      long long row = -1;
+      if (tok < sp.held) {
+        const int page = kv4_page(a.v, fw.un.b, tok);
+        if (page >= 0) row = ((long long)page * a.c.kv_heads + fw.h) * a.c.page_size + tok % a.c.page_size;
+      }
+      gap_next = row < 0;
+      pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);
+      pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
+      if (++ft == fw.i1) {
+        fw.next(w, units);
+        ft = fw.i0;
+      }
+    };
+    load();
+    for (long long x = wk.x; x < wk.x1; ++x) {
+      const int mt = (int)(x & (kMetaTiles - 1));
+      const uint32_t gap = __ballot_sync(kFull, gap_next);
+      uint32_t bad[G], any = 0;
+      pr_wait(&sh.k_free[st], par, fail);
+      const int ke = pr_store<D>(kr, k_s + st * P::kTile, t, bad);
+      if (lane == 0) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) b |= bad[g];
+        sh.kbad[mt][warp - 8] = b;
+        any = b;
+        sh.meta[mt][warp - 8].kf = exp2i(ke);
+        sh.meta[mt][warp - 8].gap = gap;
+        sh.meta[mt][warp - 8].bad = any;
+      }
+      // V's notes before K's tile is handed over: the softmax reads them with the scores
+      PrRow<D> v_now = vr;
+      {
+        // exponent and bad pairs of V follow from its pairs alone
+        float big = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float s = bf16lo(v_now.sb[g]), b = bf16hi(v_now.sb[g]);
+          const bool fin = fabsf(s) < INFINITY && fabsf(b) < INFINITY;
+          bad[g] = __ballot_sync(kFull, !fin);
+          if (fin) big = fmaxf(big, fmaxf(fabsf(b), fminf(fabsf(fmaf(15.f, s, b)), 3e38f)));
+        }
+        const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
+        const int k = (int)(bits >> 23) - 127;
+        if (lane == 0) {
+          sh.meta[mt][warp - 8].ve = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            sh.vbad[mt][warp - 8][g] = bad[g];
+            any |= bad[g];
+          }
+          sh.meta[mt][warp - 8].bad = any;
+        }
+        __syncwarp();
+      }
+      tc_fence_proxy();
+      tc_arrive(&sh.k_full[st]);
+      pr_wait(&sh.v_free[st], par, fail);
+      pr_store<D>(v_now, v_s + st * P::kTile, t, bad);
+      tc_fence_proxy();
+      tc_arrive(&sh.v_full[st]);
+      load();
+      if (++st == ST) {
+        st = 0;
+        par ^= 1;
+      }
+    }
+  } else if (warp == 12) {
+    // ---------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
+      const uint32_t qa = tc_smem(q_s), ka = tc_smem(k_s), va = tc_smem(v_s);
+      uint32_t q_par = 0, p_par = 0;          // bit per tile / slot
+      int ks = 0, vs = 0;                      // ring places
+      uint32_t k_par = 0, v_par = 0;
+      auto scores = [&](int i, int slot) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+          mma_ss(tmem + slot * 128, pr_desc(qa + i * P::kTile + off, 16), pr_desc(ka + ks * P::kTile + off, 16), id_s, k > 0);
+        }
+        tc_commit(&sh.s_full[slot]);
+      };
+      auto product = [&](int i, int slot, bool first) {
+#pragma unroll
+        for (int k = 0; k < kPrTok / 16; ++k)
+          mma_ts(tmem + 256 + i * D, tmem + slot * 128 + k * 8, pr_desc(va + vs * P::kTile + k * 2048, kPanel), id_o,
+                 !(first && k == 0));
+      };
+      auto k_next = [&]() {
+        tc_commit(&sh.k_free[ks]);
+        if (++ks == ST) {
+          ks = 0;
+          k_par ^= 1;
+        }
+      };
+      for (; wk.live(); wk.next(w, units)) {
+        const int n = wk.i1 - wk.i0;
+        for (int it = -1; it < n; ++it) {  // step it: the product of tile it, the scores of tile it + 1
+          if (NQ == 2) {
+            if (it >= 0) pr_wait(&sh.v_full[vs], v_par, fail);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+              if (it >= 0) {
+                pr_wait(&sh.p_full[i], p_par >> i & 1, fail);
+                p_par ^= 1u << i;
+                tc_fence_after();
+                product(i, i, it == 0);
+                if (it == n - 1) tc_commit(&sh.o_full[i]);
+              } else {
+                pr_wait(&sh.q_full[i], q_par >> i & 1, fail);
+                q_par ^= 1u << i;
+              }
+              if (it + 1 < n) {
+                if (i == 0) pr_wait(&sh.k_full[ks], k_par, fail);
+                tc_fence_after();
+                scores(i, i);
+              }
+            }
+            if (it + 1 < n) k_next();
+          } else {
+            if (it < 0) {
+              pr_wait(&sh.q_full[0], q_par & 1, fail);
+              q_par ^= 1;
+            }
+            const int slot = it & 1;
+            if (it + 1 < n) {
+              pr_wait(&sh.k_full[ks], k_par, fail);
+              tc_fence_after();
+              scores(0, (it + 1) & 1);
+              k_next();
+            }
+            if (it >= 0) {
+              pr_wait(&sh.v_full[vs], v_par, fail);
+              pr_wait(&sh.p_full[slot], p_par >> slot & 1, fail);
+              p_par ^= 1u << slot;
+              tc_fence_after();
+              product(0, slot, it == 0);
+              tc_commit(&sh.pv_done);
+              if (it == n - 1) tc_commit(&sh.o_full[0]);
+            }
+          }
+          if (it >= 0) {
+            tc_commit(&sh.v_free[vs]);
+            if (++vs == ST) {
+              vs = 0;
+              v_par ^= 1;
+            }
+          }
+        }
+      }
+      // nothing is left in flight, whatever ended the loop
+      tc_commit(&sh.drain);
+      tc_mbar_wait(&sh.drain, 0, kPrTimeoutNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sh.fail) atomicExch(&w.ctrl->status, BGQ_ERR_TIMEOUT);
+  if (warp == 12) tmem_free(tmem, 512);
+}
+
+static int prompt_grid() { return num_sms(); }
+
+size_t prompt_workspace_bytes(int batch, int rows, int q_heads, int kv_heads, int d) {
+  return carve_prompt(nullptr, batch, rows, q_heads / kv_heads, d, prompt_grid()).bytes;
+}
+
+template <int D>
+static cudaError_t launch_prompt_t(const AttnArgs& a, cudaStream_t s) {
+  using P = Prompt<D>;
+  const PrWs w = carve_prompt(a.ws, a.v.batch, a.v.rows, a.q_heads / a.c.kv_heads, D, prompt_grid());
+  cudaError_t e = cudaFuncSetAttribute(k_attn_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_overlapped(k_prompt_plan, 1, kPlanThreads, 0, s, a, w, P::kRows);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(k_attn_prompt<D>, prompt_grid(), kPrThreads, P::kSmem, s, a, w);
+}
+
+cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t s) {
+  switch (a.c.head_dim) {
+    case 64: return launch_prompt_t<64>(a, s);
+    case 128: return launch_prompt_t<128>(a, s);
+    default: return launch_prompt_t<256>(a, s);
+  }
+}
+
+}  // namespace bgq

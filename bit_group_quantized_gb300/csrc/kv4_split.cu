@@ -120,8 +120,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int b) {
   s.begin = a.window > 0 ? max(0, pos0 - a.window + 1) / TT * TT : 0;
   s.tiles = max(1, (s.sp.held - s.begin + TT - 1) / TT);
   const long long cols = (long long)s.sp.q_len * group;
-  const bool mine = s.sp.q_len > 0 && cols <= a.split_cols;
-  s.rtiles = mine ? (int)((cols + C - 1) / C) : 0;
+  s.rtiles = (int)((cols + C - 1) / C);
   s.units = (long long)s.rtiles * a.c.kv_heads;
   return s;
 }
