@@ -12,7 +12,8 @@
 // pairs by plain loads one tile ahead, value = code * scale + bias in fp16,
 // stored in the 128-byte swizzled layout: K as the K-major, V as the MN-major
 // operand), four for each tile of rows do the softmax (a thread owns a row: its
-// maximum and sum need no shuffles), one thread issues the MMAs. With two row tiles the
+// maximum and sum need no shuffles), and bring the next unit's queries while the last
+// product runs, one thread issues the MMAs. With two row tiles the
 // tensor cores multiply one while the other's softmax runs; with one (head dim 256,
 // whose O fills tensor memory) S is double-buffered.
 // The maximum is raised, and O rescaled, only where a row's scores pass it by
@@ -37,7 +38,7 @@
 
 namespace bgq {
 
-constexpr int kPrThreads = 416;  // warps 0-3: rows 0-127, 4-7: rows 128-255, 8-11: dequantisation, 12: MMAs
+constexpr int kPrThreads = 512;  // warps 0-3: rows 0-127, 4-7: rows 128-255, 8-11: dequantisation, 12: MMAs
 constexpr int kPrTok = 128;      // tokens of a tile
 constexpr long long kPrTimeoutNs = 1000000000ll;
 constexpr int kPlanThreads = 1024;
@@ -53,6 +54,9 @@ struct Prompt {
   // more than half an SM's, so that no second CTA comes to wait for this one's tensor memory
   static constexpr int kSmem = 1024 + (NQ + 2 * ST) * kTile > 120 * 1024 ? 1024 + (NQ + 2 * ST) * kTile : 120 * 1024;
   static constexpr int kSlot = 128 * D + 256;  // floats of a part: O by 4 columns and row, then m, then l
+  // registers of the four warpgroups: together at most the 512 * 128 of the launch
+  static constexpr int kRegSoft = D == 256 ? 240 : 184, kRegDeq = D == 256 ? 184 : 104, kRegRest = 40;
+  static_assert(NQ * kRegSoft + kRegDeq + (3 - NQ) * kRegRest <= 4 * 128, "more registers than the launch has");
 };
 
 // A unit's place in the list.
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
 #define BGQ_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define BGQ_U8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
 #define BGQ_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-__device__ __forceinline__ void pr_ld32(uint32_t t, uint32_t (&r)[32]) {
+__device__ __forceinline__ void pr_ld32(uint32_t t, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -188,7 +192,7 @@ __device__ __forceinline__ void pr_ld32(uint32_t t, uint32_t (&r)[32]) {
       : "r"(t));
 }
 // Loads done: the registers pass through, so that nothing that uses them moves ahead.
-__device__ __forceinline__ void pr_wait_ld(uint32_t (&r)[32]) {
+__device__ __forceinline__ void pr_wait_ld(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0), BGQ_U8(r, 8), BGQ_U8(r, 16), BGQ_U8(r, 24)::"memory");
 }
 __device__ __forceinline__ void pr_st16(uint32_t t, const uint32_t (&r)[16]) {
@@ -197,16 +201,46 @@ __device__ __forceinline__ void pr_st16(uint32_t t, const uint32_t (&r)[16]) {
       BGQ_I8(r, 0), BGQ_I8(r, 8)
       : "memory");
 }
-__device__ __forceinline__ void pr_st32(uint32_t t, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-      BGQ_I8(r, 0), BGQ_I8(r, 8), BGQ_I8(r, 16), BGQ_I8(r, 24)
-      : "memory");
-}
 __device__ __forceinline__ void pr_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-static __device__ __noinline__ void pr_wait_loop(uint64_t* m, uint32_t parity, volatile int* fail) {
+// O of the warp's rows times f (a row's own), eight columns at a time: rare, and few registers.
+template <int D>
+__device__ __forceinline__ void pr_scale(uint32_t t, float f) {
+#pragma unroll 1
+  for (int d = 0; d < D; d += 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(r, 0) : "r"(t + d));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
+#pragma unroll
+    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
+  }
+}
+// Two fp32 values in one register pair, one instruction for both.
+__device__ __forceinline__ uint64_t pr_pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void pr_split(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t pr_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Registers of a warpgroup's threads, from the launch's 128.
+template <int N>
+__device__ __forceinline__ void pr_regs() {
+  if (N > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void pr_wait_loop(uint64_t* m, uint32_t parity, volatile int* fail) {
   const unsigned long long t0 = tc_time();
   while (!*fail && !tc_mbar_try_suspend(m, parity))
     if ((long long)(tc_time() - t0) > kPrTimeoutNs) *fail = 1;
@@ -243,7 +277,11 @@ __device__ __forceinline__ float pr_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float pr_max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t pr_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -263,7 +301,8 @@ __device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t s2, uint32_t b2)
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// What the softmax needs to know of 32 tokens.
+// What the softmax needs to know of 32 tokens. `odd` is zero for tokens all there, in half precision's range and
+// finite: then nothing else is looked at.
 struct PrMeta {
   float kf;        // 2^E of the keys: a score's factor
   int ve;          // E of the values
@@ -278,6 +317,7 @@ struct PrShared {
   uint64_t k_full[ST], k_free[ST], v_full[ST], v_free[ST];
   uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], pv_done, drain;
   PrMeta meta[kMetaTiles][4];
+  uint4 odd[kMetaTiles];
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
   uint32_t tmem;
   int fail, last[NQ];
@@ -377,6 +417,66 @@ __device__ __forceinline__ int pr_store(const PrRow<D>& r, unsigned char* tile, 
   return e;
 }
 
+// The query row of a softmax thread in a unit.
+struct PrRowOf {
+  int row, head, pos;
+  bool own, ok;  // a row of the unit; and one that may be read and written
+};
+template <int D>
+__device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk& wk, const Span& sp, int group, int at) {
+  const long long cols = (long long)min(sp.q_len, a.v.rows) * group;
+  const long long col = (long long)wk.un.rt * Prompt<D>::kRows + at;
+  PrRowOf r;
+  r.own = col < cols;
+  const long long cc = r.own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
+  const int j = (int)(cc / group);
+  r.head = wk.h * group + (int)(cc - (long long)j * group);
+  r.row = sp.first + j;
+  r.ok = r.own && r.row >= 0 && r.row < a.v.rows;
+  r.pos = sp.kv_len - sp.q_len + j;
+  return r;
+}
+// Its values into row r of the query tile, fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7;
+// returns the factor of its scores.
+template <int D>
+__device__ __forceinline__ float pr_query(const AttnArgs& a, const PrRowOf& q, unsigned char* tile, int r) {
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(q.ok ? q.row : 0) * a.q_stride + q.head * D);
+  constexpr int R = D / 8 < 16 ? D / 8 : 16, PASS = D / 8 / R;
+  float top = 0.f;
+  uint4 raw[R];
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+#pragma unroll
+    for (int n = 0; n < R; ++n) raw[n] = q.ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+      float f[8];
+      unpack_bf16x8(raw[n], f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(f[x]));
+    }
+  }
+  const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
+  const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
+#pragma unroll
+  for (int p = PASS - 1; p >= 0; --p) {
+    if (p < PASS - 1) {
+#pragma unroll
+      for (int n = 0; n < R; ++n) raw[n] = q.ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+      float f[8];
+      unpack_bf16x8(raw[n], f);
+      const int ch = p * R + n;
+      *reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) =
+          make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
+                     pr_half2(f[3] * up, f[7] * up));
+    }
+  }
+  return fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
   using P = Prompt<D>;
@@ -429,63 +529,32 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
   if (warp < 4 * NQ) {
     // ---------------------------------------------------------------- softmax: a thread owns a row
+    pr_regs<P::kRegSoft>();
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
     const uint32_t o_t = tmem + 256 + i * D + lanes;
     uint32_t s_par = 0, o_par = 0;  // parities: s_full (bit per slot), o_full
     uint32_t pv_par = 0;
-    for (; wk.live(); wk.next(w, units)) {
-      const Span sp = kv4_span(a.v, wk.un.b);
-      const int pos0 = sp.kv_len - sp.q_len;
-      const long long cols = (long long)min(sp.q_len, a.v.rows) * group;
-      const long long col = (long long)wk.un.rt * P::kRows + i * 128 + r;
-      const bool own = col < cols;
-      const long long cc = own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
-      const int j = (int)(cc / group), hh = (int)(cc - (long long)j * group), row = sp.first + j;
-      const bool ok = own && row >= 0 && row < a.v.rows;
-      const int pos = pos0 + j;
+    Span sp;
+    PrRowOf me_row;
+    float c2_next = 0.f;
+    auto bring = [&]() {  // the rows and queries of the unit in wk
+      if (!wk.live()) return;
+      sp = kv4_span(a.v, wk.un.b);
+      me_row = pr_row<D>(a, wk, sp, group, i * 128 + r);
+      c2_next = pr_query<D>(a, me_row, q_s + i * P::kTile, r);
+      tc_fence_proxy();
+      tc_arrive(&sh.q_full[i]);
+    };
+    bring();
+    while (wk.live()) {
+      const float c2 = c2_next;
+      const int row = me_row.row, pos = me_row.pos;
+      const bool own = me_row.own, ok = me_row.ok;
       const int hi = min(sp.held, a.causal ? pos + 1 : sp.kv_len), lo = a.window > 0 ? pos - a.window + 1 : 0;
       const int hi_min = __reduce_min_sync(kFull, hi), hi_max = __reduce_max_sync(kFull, hi);
       const int lo_min = __reduce_min_sync(kFull, lo), lo_max = __reduce_max_sync(kFull, lo);
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
-
-      // the query row: fp16, scaled by a power of two
-      float c2;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(ok ? row : 0) * a.q_stride + (wk.h * group + hh) * D);
-        float top = 0.f;
-        uint4 raw[D / 8 < 16 ? D / 8 : 16];
-        constexpr int R = D / 8 < 16 ? D / 8 : 16, PASS = D / 8 / R;
-#pragma unroll
-        for (int p = 0; p < PASS; ++p)
-#pragma unroll
-          for (int n = 0; n < R; ++n) {
-            const uint4 v = ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
-            if (p == PASS - 1) raw[n] = v;
-            float f[8];
-            unpack_bf16x8(v, f);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(f[x]));
-          }
-        const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
-        const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
-        c2 = fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
-        unsigned char* qrow = q_s + i * P::kTile + r * 128;
-#pragma unroll
-        for (int p = PASS - 1; p >= 0; --p)
-#pragma unroll
-          for (int n = 0; n < R; ++n) {
-            const uint4 v = p == PASS - 1 ? raw[n] : ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
-            float f[8];
-            unpack_bf16x8(v, f);
-            const int ch = p * R + n;
-            *reinterpret_cast<uint4*>(qrow + (ch >> 3) * kPanel + (((ch & 7) ^ (r & 7)) * 16)) =
-                make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
-                           pr_half2(f[3] * up, f[7] * up));
-          }
-        tc_fence_proxy();
-        tc_arrive(&sh.q_full[i]);
-      }
 
       float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;
       int e_run = 0;         // O is in units of 2^e_run
@@ -499,7 +568,62 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // tiles are numbered over the CTA's whole share: see the dequantisation
         const int mt = (int)((wk.x + (it - wk.i0)) & (kMetaTiles - 1));
         const int t0 = wk.un.begin + it * kPrTok;
-        if (!dead) {
+        const uint4 odd = sh.odd[mt];
+        const bool plain = !(odd.x | odd.y | odd.z | odd.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && (e_run == 0 || it == wk.i0);
+        if (dead) {
+        } else if (plain) {
+          // every row sees every token, and no factor but the row's: the scores stay in registers
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pr_ld32(s_t + c * 32, v + c * 32);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pr_wait_ld(v + c * 32);
+          float tp[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tp[c] = pr_max3(__uint_as_float(v[c]), __uint_as_float(v[4 + c]), __uint_as_float(v[8 + c]));
+#pragma unroll
+          for (int x = 12; x < 124; x += 8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tp[c] = pr_max3(tp[c], __uint_as_float(v[x + c]), __uint_as_float(v[x + 4 + c]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tp[c] = fmaxf(tp[c], __uint_as_float(v[124 + c]));
+          const float ck = fmaxf(c2, 0x1p-126f);
+          const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
+          const bool raise = top > m + 8.f;
+          if (__any_sync(kFull, raise)) {
+            const float up = raise ? top : m;
+            const float f = up == m ? 1.f : pr_ex2(m - up);
+            m = up;
+            mm = up == -INFINITY ? 0.f : up;
+            l0 *= f;
+            l1 *= f;
+            if (it > wk.i0) {
+              if (NQ == 1) {
+                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+                tc_fence_after();
+              }
+              pr_scale<D>(o_t, f);
+            }
+          }
+          uint64_t ll = pr_pair(l0, l1);
+          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float p0, p1;
+              pr_split(pr_fma2(pr_pair(__uint_as_float(v[c * 32 + 2 * x]), __uint_as_float(v[c * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
+              p0 = pr_ex2(p0);
+              p1 = pr_ex2(p1);
+              ll = pr_add2(ll, pr_pair(p0, p1));
+              pk[x] = pr_half2(p0, p1);
+            }
+            pr_st16(s_t + c * 16, pk);
+          }
+          pr_split(ll, l0, l1);
+          pr_wait_st();
+        } else {
           uint32_t v[32];
           // pass 1: the largest score
           float top = -INFINITY;
@@ -553,14 +677,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 pr_wait(&sh.pv_done, pv_par ^ 1, fail);
                 tc_fence_after();
               }
-#pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
-                pr_ld32(o_t + d, v);
-                pr_wait_ld(v);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-                pr_st32(o_t + d, v);
-              }
+              pr_scale<D>(o_t, f);
             }
             e_run = e_new;
           }
@@ -614,15 +731,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         tc_arrive(&sh.p_full[slot]);
       }
 
-      // ---- the unit's end: O / l, or a part of it
+      // ---- the unit's end: the next one's queries (the last scores are done), then O / l, or a part of it
+      const bool whole = wk.i0 == 0 && wk.i1 == wk.un.tiles;
+      const long long u0 = wk.x - wk.i0, u1 = u0 + wk.un.tiles - 1;  // the unit's first and last place in the list
+      const int head = me_row.head;
+      float* const part = w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot;
+      wk.next(w, units);
+      bring();
       pr_wait(&sh.o_full[i], o_par, fail);
       o_par ^= 1;
       tc_fence_after();
-      const bool whole = wk.i0 == 0 && wk.i1 == wk.un.tiles;
       float l = poison & 1 ? NAN : l0 + l1;
-      float* const part = w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot;
       const float unit = exp2i(e_run);
-      uint16_t* out = a.out + (long long)(ok ? row : 0) * a.out_stride + (wk.h * group + hh) * D;
+      uint16_t* out = a.out + (long long)(ok ? row : 0) * a.out_stride + head * D;
       if (!dead) {
         const float inv = l == 0.f ? 0.f : unit / l;
 #pragma unroll 1
@@ -651,7 +772,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
         }
         if (whole) {
-          if (ok && a.lse) a.lse[(long long)row * a.q_heads + wk.h * group + hh] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+          if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
         } else {
           part[128 * D + r] = m;
           part[128 * D + 128 + r] = l;
@@ -659,7 +780,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       }
       tc_fence_before();
       if (!whole) {
-        const long long u0 = wk.x - wk.i0, u1 = u0 + wk.un.tiles - 1;
         const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
         __threadfence();
         wg_sync(1 + i);
@@ -704,12 +824,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
               }
             }
           }
-          if (ok && a.lse) a.lse[(long long)row * a.q_heads + wk.h * group + hh] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
+          if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
         }
       }
     }
   } else if (warp >= 8 && warp < 12) {
     // ---------------------------------------------------------------- dequantisation: a thread owns a token
+    pr_regs<P::kRegDeq>();
     const int t = tid & 127;
     int st = 0;
     uint32_t par = 1;  // the first pass over the ring finds it free
@@ -766,13 +887,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
         const int k = (int)(bits >> 23) - 127;
         if (lane == 0) {
-          sh.meta[mt][warp - 8].ve = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+          const int ve = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+          sh.meta[mt][warp - 8].ve = ve;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             sh.vbad[mt][warp - 8][g] = bad[g];
             any |= bad[g];
           }
           sh.meta[mt][warp - 8].bad = any;
+          reinterpret_cast<uint32_t*>(&sh.odd[mt])[warp - 8] = gap | any | (uint32_t)ke | (uint32_t)ve;
         }
         __syncwarp();
       }
@@ -788,9 +911,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         par ^= 1;
       }
     }
-  } else if (warp == 12) {
-    // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
+  } else {
+    // ---------------------------------------------------------------- MMAs, by one thread
+    pr_regs<P::kRegRest>();
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
       const uint32_t qa = tc_smem(q_s), ka = tc_smem(k_s), va = tc_smem(v_s);
       uint32_t q_par = 0, p_par = 0;          // bit per tile / slot
@@ -874,7 +998,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       }
       // nothing is left in flight, whatever ended the loop
       tc_commit(&sh.drain);
-      tc_mbar_wait(&sh.drain, 0, kPrTimeoutNs);
+      const unsigned long long t0 = tc_time();
+      while (!tc_mbar_try_suspend(&sh.drain, 0) && (long long)(tc_time() - t0) < kPrTimeoutNs) {
+      }
     }
     __syncwarp();
   }
