@@ -59,9 +59,10 @@ struct Prompt {
   static_assert(NQ * kRegSoft + kRegDeq + (3 - NQ) * kRegRest <= 4 * 128, "more registers than the launch has");
 };
 
-// A unit's place in the list.
-struct PrUnit {
+// A unit: its sequence and row tile, its tokens' first and how many tiles of them, and the sequence's span.
+struct __align__(16) PrUnit {
   int b, rt, tiles, begin;
+  Span sp;
 };
 struct PrPlan {  // at the start of the workspace, behind the control block
   int units, pad;
@@ -147,14 +148,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
   long long sum = 0;
   for (int base = 0; base < units; base += kPlanThreads) {
     const int u = base + threadIdx.x;
-    PrUnit un = {0, 0, 0, 0};
+    PrUnit un = {};
     if (u < units) {
       int lo = 0, hi = a.v.batch;  // the last sequence whose first unit is at or before u
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (first[mid] <= u) lo = mid; else hi = mid;
       }
-      const Span sp = kv4_span(a.v, lo);
+      const Span sp = un.sp = kv4_span(a.v, lo);
       const int pos0 = sp.kv_len - sp.q_len;
       un.b = lo;
       un.rt = u - first[lo];
@@ -323,16 +324,19 @@ struct PrShared {
   int fail, last[NQ];
 };
 
-// A CTA's share of the list, unit by unit.
+// A CTA's share of the list, unit by unit; the unit behind is fetched while one is worked on.
 struct PrWalk {
-  long long x, x1, sum;
+  long long x, x1;
   int h, u, i0, i1;
-  PrUnit un;
-  __device__ __forceinline__ void set(const PrWs& w) { un = w.units[u]; }
-  __device__ __forceinline__ void start(const PrWs& w, long long x_, long long x1_, long long sum_, int units) {
+  PrUnit un, nx;
+  __device__ __forceinline__ static PrUnit get(const PrWs& w, int u) {
+    const int4* p = reinterpret_cast<const int4*>(w.units + u);
+    const int4 a = p[0], b = p[1];
+    return PrUnit{a.x, a.y, a.z, a.w, {b.x, b.y, b.z, b.w}};
+  }
+  __device__ __forceinline__ void start(const PrWs& w, long long x_, long long x1_, long long sum, int units) {
     x = x_;
     x1 = x1_;
-    sum = sum_;
     if (x >= x1) return;
     h = (int)(x / sum);
     const long long y = x - h * sum;
@@ -342,7 +346,8 @@ struct PrWalk {
       if (w.prefix[mid] <= y) lo = mid; else hi = mid;
     }
     u = lo;
-    set(w);
+    un = get(w, u);
+    nx = get(w, u + 1 == units ? 0 : u + 1);
     i0 = (int)(y - w.prefix[u]);
     i1 = (int)min((long long)un.tiles, i0 + x1 - x);
   }
@@ -354,7 +359,8 @@ struct PrWalk {
       u = 0;
       ++h;
     }
-    set(w);
+    un = nx;
+    nx = get(w, u + 1 == units ? 0 : u + 1);
     i0 = 0;
     i1 = (int)min((long long)un.tiles, x1 - x);
   }
@@ -384,14 +390,12 @@ __device__ __forceinline__ void pr_load(PrRow<D>& r, const uint32_t* q, const ui
 #pragma unroll
   for (int i = 0; i < D / kGroup; ++i) r.sb[i] = ss[i];
 }
-// Writes the token's values into its row of the tile; the exponent that the 32 tokens were divided by, and
-// the tokens whose pair of a group is not finite.
+// The exponent that the values of the warp's 32 tokens are divided by, and the tokens whose pair of a group is not finite.
 template <int D>
-__device__ __forceinline__ int pr_store(const PrRow<D>& r, unsigned char* tile, int t, uint32_t (&bad)[D / kGroup]) {
-  constexpr int G = D / kGroup;
+__device__ __forceinline__ int pr_range(const PrRow<D>& r, uint32_t (&bad)[D / kGroup]) {
   float big = 0.f;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
+  for (int g = 0; g < D / kGroup; ++g) {
     const float s = bf16lo(r.sb[g]), b = bf16hi(r.sb[g]);
     const bool fin = fabsf(s) < INFINITY && fabsf(b) < INFINITY;
     bad[g] = __ballot_sync(kFull, !fin);
@@ -399,10 +403,14 @@ __device__ __forceinline__ int pr_store(const PrRow<D>& r, unsigned char* tile, 
   }
   const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
   const int k = (int)(bits >> 23) - 127;
-  const int e = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+  return bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+}
+// Writes the token's values into its row of the tile.
+template <int D>
+__device__ __forceinline__ void pr_store(const PrRow<D>& r, unsigned char* tile, int t, const uint32_t (&bad)[D / kGroup], int e) {
   const float down = exp2i(-e);
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
+  for (int g = 0; g < D / kGroup; ++g) {
     const bool fin = !(bad[g] >> (t & 31) & 1);
     const float s = fin ? bf16lo(r.sb[g]) * down : 0.f, b = fin ? bf16hi(r.sb[g]) * down : 0.f;
     const uint32_t s2 = pr_half2(s, s), b2 = pr_half2(b, b);
@@ -414,7 +422,6 @@ __device__ __forceinline__ int pr_store(const PrRow<D>& r, unsigned char* tile, 
       *reinterpret_cast<uint4*>(row + ((c ^ (t & 7)) * 16)) = pr_values(w, s2, b2);
     }
   }
-  return e;
 }
 
 // The query row of a softmax thread in a unit.
@@ -423,7 +430,8 @@ struct PrRowOf {
   bool own, ok;  // a row of the unit; and one that may be read and written
 };
 template <int D>
-__device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk& wk, const Span& sp, int group, int at) {
+__device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk& wk, int group, int at) {
+  const Span& sp = wk.un.sp;
   const long long cols = (long long)min(sp.q_len, a.v.rows) * group;
   const long long col = (long long)wk.un.rt * Prompt<D>::kRows + at;
   PrRowOf r;
@@ -535,13 +543,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     const uint32_t o_t = tmem + 256 + i * D + lanes;
     uint32_t s_par = 0, o_par = 0;  // parities: s_full (bit per slot), o_full
     uint32_t pv_par = 0;
-    Span sp;
     PrRowOf me_row;
     float c2_next = 0.f;
     auto bring = [&]() {  // the rows and queries of the unit in wk
       if (!wk.live()) return;
-      sp = kv4_span(a.v, wk.un.b);
-      me_row = pr_row<D>(a, wk, sp, group, i * 128 + r);
+      me_row = pr_row<D>(a, wk, group, i * 128 + r);
       c2_next = pr_query<D>(a, me_row, q_s + i * P::kTile, r);
       tc_fence_proxy();
       tc_arrive(&sh.q_full[i]);
@@ -550,6 +556,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     while (wk.live()) {
       const float c2 = c2_next;
       const int row = me_row.row, pos = me_row.pos;
+      const Span& sp = wk.un.sp;
       const bool own = me_row.own, ok = me_row.ok;
       const int hi = min(sp.held, a.causal ? pos + 1 : sp.kv_len), lo = a.window > 0 ? pos - a.window + 1 : 0;
       const int hi_min = __reduce_min_sync(kFull, hi), hi_max = __reduce_max_sync(kFull, hi);
@@ -831,81 +838,72 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   } else if (warp >= 8 && warp < 12) {
     // ---------------------------------------------------------------- dequantisation: a thread owns a token
     pr_regs<P::kRegDeq>();
+    // its codes are loaded one tile ahead, and its page two
     const int t = tid & 127;
     int st = 0;
     uint32_t par = 1;  // the first pass over the ring finds it free
-    PrWalk fw = wk;    // one tile ahead
+    PrWalk fw = wk;
     int ft = fw.i0;
-    PrRow<D> kr, vr;
-    bool gap_next = false;
-    auto load = [&]() {
-      if (!fw.live()) return;
-      const Span sp = kv4_span(a.v, fw.un.b);
+    auto find = [&]() -> long long {  // the row of this thread's token in the next tile to be loaded, -1: absent
+      if (!fw.live()) return -1;
       const int tok = fw.un.begin + ft * kPrTok + t;
       long long row = -1;
-      if (tok < sp.held) {
-        const int page = kv4_page(a.v, fw.un.b, tok);
-        if (page >= 0) row = ((long long)page * a.c.kv_heads + fw.h) * a.c.page_size + tok % a.c.page_size;
+      if (tok < fw.un.sp.held) {
+        int pg, at;
+        if (a.page_shift >= 0) {
+          pg = tok >> a.page_shift;
+          at = tok & (a.c.page_size - 1);
+        } else {
+          pg = tok / a.c.page_size;
+          at = tok - pg * a.c.page_size;
+        }
+        const int page = a.v.pages ? a.v.pages[(long long)fw.un.b * a.v.max_pages + pg] : fw.un.b;
+        if ((unsigned)page < (unsigned)a.c.n_pages) row = (long long)(page * a.c.kv_heads + fw.h) * a.c.page_size + at;
       }
-      gap_next = row < 0;
-      pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);
-      pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
       if (++ft == fw.i1) {
         fw.next(w, units);
         ft = fw.i0;
       }
+      return row;
     };
-    load();
+    PrRow<D> kr, vr;
+    long long row = find();
+    pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);
+    pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
+    bool gone = row < 0;
+    row = find();
+#pragma unroll 1
     for (long long x = wk.x; x < wk.x1; ++x) {
       const int mt = (int)(x & (kMetaTiles - 1));
-      const uint32_t gap = __ballot_sync(kFull, gap_next);
-      uint32_t bad[G], any = 0;
+      const uint32_t gap = __ballot_sync(kFull, gone);
+      uint32_t kb[G], vb[G];
+      const int ke = pr_range<D>(kr, kb), ve = pr_range<D>(vr, vb);
       pr_wait(&sh.k_free[st], par, fail);
-      const int ke = pr_store<D>(kr, k_s + st * P::kTile, t, bad);
+      // the notes on both go out with K: the softmax reads them with the scores
       if (lane == 0) {
-        uint32_t b = 0;
-#pragma unroll
-        for (int g = 0; g < G; ++g) b |= bad[g];
-        sh.kbad[mt][warp - 8] = b;
-        any = b;
-        sh.meta[mt][warp - 8].kf = exp2i(ke);
-        sh.meta[mt][warp - 8].gap = gap;
-        sh.meta[mt][warp - 8].bad = any;
-      }
-      // V's notes before K's tile is handed over: the softmax reads them with the scores
-      PrRow<D> v_now = vr;
-      {
-        // exponent and bad pairs of V follow from its pairs alone
-        float big = 0.f;
+        uint32_t kany = 0, vany = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float s = bf16lo(v_now.sb[g]), b = bf16hi(v_now.sb[g]);
-          const bool fin = fabsf(s) < INFINITY && fabsf(b) < INFINITY;
-          bad[g] = __ballot_sync(kFull, !fin);
-          if (fin) big = fmaxf(big, fmaxf(fabsf(b), fminf(fabsf(fmaf(15.f, s, b)), 3e38f)));
+          kany |= kb[g];
+          vany |= vb[g];
+          sh.vbad[mt][warp - 8][g] = vb[g];
         }
-        const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
-        const int k = (int)(bits >> 23) - 127;
-        if (lane == 0) {
-          const int ve = bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
-          sh.meta[mt][warp - 8].ve = ve;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            sh.vbad[mt][warp - 8][g] = bad[g];
-            any |= bad[g];
-          }
-          sh.meta[mt][warp - 8].bad = any;
-          reinterpret_cast<uint32_t*>(&sh.odd[mt])[warp - 8] = gap | any | (uint32_t)ke | (uint32_t)ve;
-        }
-        __syncwarp();
+        sh.kbad[mt][warp - 8] = kany;
+        sh.meta[mt][warp - 8] = PrMeta{exp2i(ke), ve, gap, kany | vany};
+        reinterpret_cast<uint32_t*>(&sh.odd[mt])[warp - 8] = gap | kany | vany | (uint32_t)ke | (uint32_t)ve;
       }
+      __syncwarp();
+      pr_store<D>(kr, k_s + st * P::kTile, t, kb, ke);
       tc_fence_proxy();
       tc_arrive(&sh.k_full[st]);
+      pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);  // the next tile's keys, while this one's values are stored
       pr_wait(&sh.v_free[st], par, fail);
-      pr_store<D>(v_now, v_s + st * P::kTile, t, bad);
+      pr_store<D>(vr, v_s + st * P::kTile, t, vb, ve);
       tc_fence_proxy();
       tc_arrive(&sh.v_full[st]);
-      load();
+      pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
+      gone = row < 0;
+      row = find();
       if (++st == ST) {
         st = 0;
         par ^= 1;
@@ -916,23 +914,40 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     pr_regs<P::kRegRest>();
     if (warp == 12 && lane == 0) {
       constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
-      const uint32_t qa = tc_smem(q_s), ka = tc_smem(k_s), va = tc_smem(v_s);
+      // Short loops and few instructions per MMA: this thread's code competes with the other warps' for the
+      // instruction caches. Only the low word of a descriptor changes (addresses stay below 2^18).
+      const uint32_t hi_k = (uint32_t)(pr_desc(0, 16) >> 32), lo_k = (uint32_t)pr_desc(0, 16);
+      const uint32_t hi_v = (uint32_t)(pr_desc(0, kPanel) >> 32), lo_v = (uint32_t)pr_desc(0, kPanel);
+      const uint32_t qa = lo_k + (tc_smem(q_s) >> 4), ka = lo_k + (tc_smem(k_s) >> 4), va = lo_v + (tc_smem(v_s) >> 4);
       uint32_t q_par = 0, p_par = 0;          // bit per tile / slot
       int ks = 0, vs = 0;                      // ring places
       uint32_t k_par = 0, v_par = 0;
       auto scores = [&](int i, int slot) {
+        const uint32_t d = tmem + slot * 128;
+        uint32_t qd = qa + i * (P::kTile >> 4), kd = ka + ks * (P::kTile >> 4);
+#pragma unroll 1
+        for (int p = 0; p < G; ++p) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-          mma_ss(tmem + slot * 128, pr_desc(qa + i * P::kTile + off, 16), pr_desc(ka + ks * P::kTile + off, 16), id_s, k > 0);
+          for (int k = 0; k < 4; ++k)
+            mma_ss(d, (uint64_t)hi_k << 32 | (qd + k * 2), (uint64_t)hi_k << 32 | (kd + k * 2), id_s, p + k > 0);
+          qd += kPanel >> 4;
+          kd += kPanel >> 4;
         }
         tc_commit(&sh.s_full[slot]);
       };
       auto product = [&](int i, int slot, bool first) {
+        const uint32_t d = tmem + 256 + i * D;
+        uint32_t pa = tmem + slot * 128, vd = va + vs * (P::kTile >> 4), acc = !first;
+#pragma unroll 1
+        for (int k = 0; k < kPrTok / 64; ++k) {
 #pragma unroll
-        for (int k = 0; k < kPrTok / 16; ++k)
-          mma_ts(tmem + 256 + i * D, tmem + slot * 128 + k * 8, pr_desc(va + vs * P::kTile + k * 2048, kPanel), id_o,
-                 !(first && k == 0));
+          for (int n = 0; n < 4; ++n) {
+            mma_ts(d, pa + n * 8, (uint64_t)hi_v << 32 | (vd + n * 128), id_o, acc);
+            acc = 1;
+          }
+          pa += 32;
+          vd += 512;
+        }
       };
       auto k_next = [&]() {
         tc_commit(&sh.k_free[ks]);
@@ -946,7 +961,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         for (int it = -1; it < n; ++it) {  // step it: the product of tile it, the scores of tile it + 1
           if (NQ == 2) {
             if (it >= 0) pr_wait(&sh.v_full[vs], v_par, fail);
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < NQ; ++i) {
               if (it >= 0) {
                 pr_wait(&sh.p_full[i], p_par >> i & 1, fail);
