@@ -38,7 +38,7 @@
 
 namespace bgq {
 
-constexpr int kPrThreads = 512;  // warps 0-3: rows 0-127, 4-7: rows 128-255, 8-11: dequantisation, 12: MMAs
+constexpr int kPrThreads = 512;  // warp 0: MMAs, 4-7: dequantisation, 8-11: rows 0-127, 12-15: rows 128-255
 constexpr int kPrTok = 128;      // tokens of a tile
 constexpr long long kPrTimeoutNs = 1000000000ll;
 constexpr int kPlanThreads = 1024;
@@ -204,6 +204,10 @@ __device__ __forceinline__ void pr_st16(uint32_t t, const uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void pr_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ uint32_t pr_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // O of the warp's rows times f (a row's own), eight columns at a time: rare, and few registers.
 template <int D>
 __device__ __forceinline__ void pr_scale(uint32_t t, float f) {
@@ -214,6 +218,19 @@ __device__ __forceinline__ void pr_scale(uint32_t t, float f) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
 #pragma unroll
     for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
+  }
+}
+// 32 tokens' probabilities of the warp's rows times f.
+__device__ __forceinline__ void pr_scale_p(uint32_t t, float f) {
+  const uint32_t f2 = pr_half2(f, f);
+#pragma unroll 1
+  for (int d = 0; d < 16; d += 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(r, 0) : "r"(t + d));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
+#pragma unroll
+    for (int x = 0; x < 8; ++x) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[x]) : "r"(r[x]), "r"(f2));
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
   }
 }
@@ -283,10 +300,6 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t pr_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Eight codes of a word as fp16 values code * s + b, in the order 0 4 1 5 2 6 3 7.
 __device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t s2, uint32_t b2) {
@@ -316,9 +329,9 @@ template <int D>
 struct PrShared {
   static constexpr int G = D / kGroup, NQ = Prompt<D>::NQ, ST = Prompt<D>::ST;
   uint64_t k_full[ST], k_free[ST], v_full[ST], v_free[ST];
-  uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], pv_done, drain;
+  uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], drain, pv_done;
   PrMeta meta[kMetaTiles][4];
-  uint4 odd[kMetaTiles];
+  uint32_t odd[kMetaTiles][4];
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
   uint32_t tmem;
   int fail, last[NQ];
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  if (warp == 0) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -535,10 +548,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   wk.x = wk.x1 = 0;
   if (cta < ctas) wk.start(w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
 
-  if (warp < 4 * NQ) {
+  if (warp >= 8 && warp < 8 + 4 * NQ) {
     // ---------------------------------------------------------------- softmax: a thread owns a row
     pr_regs<P::kRegSoft>();
-    const int i = warp >> 2, r = tid & 127;
+    const int i = (warp >> 2) - 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
     const uint32_t o_t = tmem + 256 + i * D + lanes;
     uint32_t s_par = 0, o_par = 0;  // parities: s_full (bit per slot), o_full
@@ -564,175 +577,114 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
 
       float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;
-      int e_run = 0;         // O is in units of 2^e_run
-      uint32_t poison = 0;   // bit 0: a key that is not finite is seen; bit 1 + g: a value of group g
+      int e_run = 0;        // O and P are in units of 2^e_run
+      bool fresh = true;    // no value has set e_run yet
+      uint32_t poison = 0;  // bit 0: a key that is not finite is seen; bit 1 + g: a value of group g
+#pragma unroll 1
       for (int it = wk.i0; it < wk.i1; ++it) {
         const int slot = NQ == 2 ? i : (it - wk.i0) & 1;
         const uint32_t s_t = tmem + slot * 128 + lanes;
         pr_wait(&sh.s_full[slot], s_par >> slot & 1, fail);
         s_par ^= 1u << slot;
         tc_fence_after();
-        // tiles are numbered over the CTA's whole share: see the dequantisation
+        // tiles are numbered over the CTA's whole share, as in the dequantisation
         const int mt = (int)((wk.x + (it - wk.i0)) & (kMetaTiles - 1));
         const int t0 = wk.un.begin + it * kPrTok;
-        const uint4 odd = sh.odd[mt];
-        const bool plain = !(odd.x | odd.y | odd.z | odd.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && (e_run == 0 || it == wk.i0);
-        if (dead) {
-        } else if (plain) {
-          // every row sees every token, and no factor but the row's: the scores stay in registers
-          uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pr_ld32(s_t + c * 32, v + c * 32);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pr_wait_ld(v + c * 32);
-          float tp[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tp[c] = pr_max3(__uint_as_float(v[c]), __uint_as_float(v[4 + c]), __uint_as_float(v[8 + c]));
-#pragma unroll
-          for (int x = 12; x < 124; x += 8)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tp[c] = pr_max3(tp[c], __uint_as_float(v[x + c]), __uint_as_float(v[x + 4 + c]));
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tp[c] = fmaxf(tp[c], __uint_as_float(v[124 + c]));
-          const float ck = fmaxf(c2, 0x1p-126f);
-          const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
-          const bool raise = top > m + 8.f;
-          if (__any_sync(kFull, raise)) {
-            const float up = raise ? top : m;
-            const float f = up == m ? 1.f : pr_ex2(m - up);
-            m = up;
-            mm = up == -INFINITY ? 0.f : up;
-            l0 *= f;
-            l1 *= f;
-            if (it > wk.i0) {
-              if (NQ == 1) {
-                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
-                tc_fence_after();
-              }
-              pr_scale<D>(o_t, f);
-            }
-          }
-          uint64_t ll = pr_pair(l0, l1);
-          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float p0, p1;
-              pr_split(pr_fma2(pr_pair(__uint_as_float(v[c * 32 + 2 * x]), __uint_as_float(v[c * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
-              p0 = pr_ex2(p0);
-              p1 = pr_ex2(p1);
-              ll = pr_add2(ll, pr_pair(p0, p1));
-              pk[x] = pr_half2(p0, p1);
-            }
-            pr_st16(s_t + c * 16, pk);
-          }
-          pr_split(ll, l0, l1);
-          pr_wait_st();
-        } else {
-          uint32_t v[32];
-          // pass 1: the largest score
-          float top = -INFINITY;
-          int e_new = it == wk.i0 ? -1000 : e_run;
+        // 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < (dead ? 0 : 4); ++c) {
+          const int t = t0 + c * 32;
+          if (t >= hi_max || t + 32 <= lo_min) {  // no row sees any
+            const uint32_t none[16] = {};
+            pr_st16(s_t + c * 16, none);
+            continue;
+          }
+          uint32_t v[32];
+          pr_ld32(s_t + c * 32, v);
+          const uint32_t odd = sh.odd[mt][c];
+          const bool cut = t < lo_max || t + 32 > hi_min;
+          float ck = c2;
+          int ve = 0;
+          uint32_t see = 0xffffffffu;
+          if (odd || cut) {
             const PrMeta me = sh.meta[mt][c];
-            const int t = t0 + c * 32;
-            if (t >= hi_max || t + 32 <= lo_min) continue;
-            pr_ld32(s_t + c * 32, v);
-            e_new = max(e_new, me.ve);
-            pr_wait_ld(v);
-            if (me.gap || t < lo_max || t + 32 > hi_min) {
-              const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
-              uint32_t see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
-              see &= ~me.gap;
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = see >> x & 1 ? v[x] : 0xff800000u;
-              if (me.bad) {
-                if (see & sh.kbad[mt][c]) poison |= 1;
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                  if (see & sh.vbad[mt][c][g]) poison |= 2u << g;
-              }
-            } else if (me.bad) {
-              if (sh.kbad[mt][c]) poison |= 1;
+            ck *= me.kf;
+            ve = me.ve;
+            const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
+            see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
+            see &= ~me.gap;
+            if (me.bad) {
+              if (see & sh.kbad[mt][c]) poison |= 1;
 #pragma unroll
               for (int g = 0; g < G; ++g)
-                if (sh.vbad[mt][c][g]) poison |= 2u << g;
+                if (see & sh.vbad[mt][c][g]) poison |= 2u << g;
             }
-            float t0f = -INFINITY, t1f = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              t0f = pr_max3(t0f, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-              t1f = pr_max3(t1f, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-            }
-            top = fmaxf(top, fmaxf(t0f, t1f) * fmaxf(c2 * me.kf, 0x1p-126f));
           }
-          if (e_new == -1000) e_new = 0;
+          ck = fmaxf(ck, 0x1p-126f);  // -infinity stays -infinity
+          pr_wait_ld(v);
+          if (odd || cut) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = see >> x & 1 ? v[x] : 0xff800000u;
+          }
+          float ta = pr_max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+          float tb = pr_max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+          for (int x = 6; x < 30; x += 4) {
+            ta = pr_max3(ta, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+            tb = pr_max3(tb, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+          }
+          const float top = pr_max3(fmaxf(ta, tb), __uint_as_float(v[30]), __uint_as_float(v[31])) * ck;
           const bool raise = top > m + 8.f;
-          if (__any_sync(kFull, raise || e_new != e_run)) {
+          if (__any_sync(kFull, raise || fresh || ve > e_run)) {
             const float up = raise ? top : m;
             float f = up == m ? 1.f : pr_ex2(m - up);
             m = up;
             mm = up == -INFINITY ? 0.f : up;
             l0 *= f;
             l1 *= f;
-            if (it > wk.i0) {
-              f *= exp2i(max(e_run - e_new, -126));  // e_new >= e_run
-              if (NQ == 1) {  // the product before this one may still be running
-                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
-                tc_fence_after();
-              }
-              pr_scale<D>(o_t, f);
-            }
+            const int e_new = fresh ? ve : max(ve, e_run);
+            f *= exp2i(max(e_run - e_new, -126));
             e_run = e_new;
-          }
-          // pass 2: the probabilities, over the scores
+            if (!fresh) {
+              pr_wait_st();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const PrMeta me = sh.meta[mt][c];
-            const int t = t0 + c * 32;
-            uint32_t pk[16];
-            if (t >= hi_max || t + 32 <= lo_min) {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) pk[x] = 0;
-              pr_st16(s_t + c * 16, pk);
-              continue;
-            }
-            pr_ld32(s_t + c * 32, v);
-            const float ck = fmaxf(c2 * me.kf, 0x1p-126f);
-            uint32_t see = 0xffffffffu;
-            if (me.gap || t < lo_max || t + 32 > hi_min) {
-              const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
-              see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
-              see &= ~me.gap;
-            }
-            const bool part = __any_sync(kFull, see != 0xffffffffu);
-            pr_wait_ld(v);
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              float p0 = pr_ex2(fmaf(__uint_as_float(v[x]), ck, -mm)), p1 = pr_ex2(fmaf(__uint_as_float(v[x + 1]), ck, -mm));
-              if (part) {
-                p0 = see >> x & 1 ? p0 : 0.f;
-                p1 = see >> (x + 1) & 1 ? p1 : 0.f;
+              for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
+              if (it > wk.i0) {
+                if (NQ == 1) {  // the product before this one may still be running
+                  pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+                  tc_fence_after();
+                }
+                pr_scale<D>(o_t, f);
               }
-              l0 += p0;
-              l1 += p1;
-              v[x] = __float_as_uint(p0);
-              v[x + 1] = __float_as_uint(p1);
             }
-            if (me.ve != e_run) {  // values of another unit than O
-              const float f = exp2i(max(me.ve - e_run, -126));
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) pk[x] = pr_half2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-            pr_st16(s_t + c * 16, pk);
+            fresh = false;
           }
-          pr_wait_st();
+          uint64_t ll = pr_pair(l0, l1);
+          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float p0, p1;
+            // a hidden score is -infinity: its probability is zero
+            pr_split(pr_fma2(pr_pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), ck2, mm2), p0, p1);
+            p0 = pr_ex2(p0);
+            p1 = pr_ex2(p1);
+            ll = pr_add2(ll, pr_pair(p0, p1));
+            pk[x] = pr_half2(p0, p1);
+          }
+          pr_split(ll, l0, l1);
+          if (ve != e_run) {  // values of another unit than O (never larger): in fp32, rounded once
+            const float f = exp2i(max(ve - e_run, -126));
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float p0, p1;
+              pr_split(pr_fma2(pr_pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), ck2, mm2), p0, p1);
+              pk[x] = pr_half2(pr_ex2(p0) * f, pr_ex2(p1) * f);
+            }
+          }
+          pr_st16(s_t + c * 16, pk);
         }
+        pr_wait_st();
         pv_par ^= 1;
         tc_fence_before();
         tc_arrive(&sh.p_full[slot]);
@@ -835,7 +787,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
       }
     }
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------------- dequantisation: a thread owns a token
     pr_regs<P::kRegDeq>();
     // its codes are loaded one tile ahead, and its page two
@@ -866,53 +818,60 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       }
       return row;
     };
-    PrRow<D> kr, vr;
-    long long row = find();
-    pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);
-    pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
+    // K and V tiles take turns through one copy of the code: `now` is stored while `then` (the other of the
+    // two, half a tile on) is on its way
+    PrRow<D> now, then;
+    long long row = find(), row_next = find();
+    pr_load<D>(now, a.c.k_q, a.c.k_sb, row);
+    pr_load<D>(then, a.c.v_q, a.c.v_sb, row);
     bool gone = row < 0;
-    row = find();
 #pragma unroll 1
-    for (long long x = wk.x; x < wk.x1; ++x) {
-      const int mt = (int)(x & (kMetaTiles - 1));
+    for (long long y = wk.x * 2; y < wk.x1 * 2; ++y) {
+      const bool val = y & 1;
+      const int mt = (int)((y >> 1) & (kMetaTiles - 1));
+      uint32_t bad[G], any = 0;
+      const int e = pr_range<D>(now, bad);
       const uint32_t gap = __ballot_sync(kFull, gone);
-      uint32_t kb[G], vb[G];
-      const int ke = pr_range<D>(kr, kb), ve = pr_range<D>(vr, vb);
-      pr_wait(&sh.k_free[st], par, fail);
-      // the notes on both go out with K: the softmax reads them with the scores
-      if (lane == 0) {
-        uint32_t kany = 0, vany = 0;
+      pr_wait(val ? &sh.v_free[st] : &sh.k_free[st], par, fail);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          kany |= kb[g];
-          vany |= vb[g];
-          sh.vbad[mt][warp - 8][g] = vb[g];
+      for (int g = 0; g < G; ++g) any |= bad[g];
+      if (!val) {
+        // the notes on both go out with K, for the softmax reads them with the scores
+        uint32_t vb[G], vany = 0;
+        const int ve = pr_range<D>(then, vb);
+        if (lane == 0) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            vany |= vb[g];
+            sh.vbad[mt][warp - 4][g] = vb[g];
+          }
+          sh.kbad[mt][warp - 4] = any;
+          sh.meta[mt][warp - 4] = PrMeta{exp2i(e), ve, gap, any | vany};
+          sh.odd[mt][warp - 4] = gap | any | vany | (uint32_t)e | (uint32_t)ve;
         }
-        sh.kbad[mt][warp - 8] = kany;
-        sh.meta[mt][warp - 8] = PrMeta{exp2i(ke), ve, gap, kany | vany};
-        reinterpret_cast<uint32_t*>(&sh.odd[mt])[warp - 8] = gap | kany | vany | (uint32_t)ke | (uint32_t)ve;
+        __syncwarp();
       }
-      __syncwarp();
-      pr_store<D>(kr, k_s + st * P::kTile, t, kb, ke);
+      pr_store<D>(now, (val ? v_s : k_s) + st * P::kTile, t, bad, e);
       tc_fence_proxy();
-      tc_arrive(&sh.k_full[st]);
-      pr_load<D>(kr, a.c.k_q, a.c.k_sb, row);  // the next tile's keys, while this one's values are stored
-      pr_wait(&sh.v_free[st], par, fail);
-      pr_store<D>(vr, v_s + st * P::kTile, t, vb, ve);
-      tc_fence_proxy();
-      tc_arrive(&sh.v_full[st]);
-      pr_load<D>(vr, a.c.v_q, a.c.v_sb, row);
-      gone = row < 0;
-      row = find();
-      if (++st == ST) {
-        st = 0;
-        par ^= 1;
+      tc_arrive(val ? &sh.v_full[st] : &sh.k_full[st]);
+      now = then;
+      if (!val) {
+        row = row_next;
+        row_next = find();
+        pr_load<D>(then, a.c.k_q, a.c.k_sb, row);
+      } else {
+        gone = row < 0;
+        pr_load<D>(then, a.c.v_q, a.c.v_sb, row);
+        if (++st == ST) {
+          st = 0;
+          par ^= 1;
+        }
       }
     }
   } else {
     // ---------------------------------------------------------------- MMAs, by one thread
     pr_regs<P::kRegRest>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 0 && lane == 0) {
       constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
       // Short loops and few instructions per MMA: this thread's code competes with the other warps' for the
       // instruction caches. Only the low word of a descriptor changes (addresses stay below 2^18).
@@ -1022,7 +981,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sh.fail) atomicExch(&w.ctrl->status, BGQ_ERR_TIMEOUT);
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 static int prompt_grid() { return num_sms(); }
