@@ -13,7 +13,7 @@
 // stored in the 128-byte swizzled layout: K as the K-major, V as the MN-major
 // operand), four for each tile of rows do the softmax (a thread owns a row: its
 // maximum and sum need no shuffles), and bring the next unit's queries while the last
-// product runs, one thread issues the MMAs. With two row tiles the
+// product runs, one warp issues the MMAs. With two row tiles the
 // tensor cores multiply one while the other's softmax runs; with one (head dim 256,
 // whose O fills tensor memory) S is double-buffered.
 // The maximum is raised, and O rescaled, only where a row's scores pass it by
@@ -276,19 +276,33 @@ __device__ __forceinline__ uint64_t pr_desc(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ constexpr uint32_t pr_idesc(int n, bool b_mn) {  // fp16 x fp16 -> fp32, M = 128
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Issued by the lane that has `lead`; the whole warp runs the code around them, so that addresses and descriptors stay
+// in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* m, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc_smem(m)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ float pr_ex2(float x) {
   float y;
@@ -331,7 +345,7 @@ struct PrShared {
   uint64_t k_full[ST], k_free[ST], v_full[ST], v_free[ST];
   uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], drain, pv_done;
   PrMeta meta[kMetaTiles][4];
-  uint32_t odd[kMetaTiles][4];
+  __align__(16) uint32_t odd[kMetaTiles][4];
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
   uint32_t tmem;
   int fail, last[NQ];
@@ -590,9 +604,63 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         // tiles are numbered over the CTA's whole share, as in the dequantisation
         const int mt = (int)((wk.x + (it - wk.i0)) & (kMetaTiles - 1));
         const int t0 = wk.un.begin + it * kPrTok;
-        // 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
+        const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
+        const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && !fresh && e_run == 0;
+        if (plain && !dead) {
+          // every row sees every token, and no factor but the row's: all scores in registers at once
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pr_ld32(s_t + c * 32, v + c * 32);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pr_wait_ld(v + c * 32);
+          float tp[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tp[c] = pr_max3(__uint_as_float(v[c]), __uint_as_float(v[4 + c]), __uint_as_float(v[8 + c]));
+#pragma unroll
+          for (int x = 12; x < 124; x += 8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tp[c] = pr_max3(tp[c], __uint_as_float(v[x + c]), __uint_as_float(v[x + 4 + c]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tp[c] = fmaxf(tp[c], __uint_as_float(v[124 + c]));
+          const float ck = fmaxf(c2, 0x1p-126f);
+          const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
+          const bool raise = top > m + 8.f;
+          if (__any_sync(kFull, raise)) {
+            const float up = raise ? top : m;
+            const float f = up == m ? 1.f : pr_ex2(m - up);
+            m = up;
+            mm = up == -INFINITY ? 0.f : up;
+            l0 *= f;
+            l1 *= f;
+            if (it > wk.i0) {
+              if (NQ == 1) {  // the product before this one may still be running
+                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+                tc_fence_after();
+              }
+              pr_scale<D>(o_t, f);
+            }
+          }
+          uint64_t ll = pr_pair(l0, l1);
+          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float p0, p1;
+              pr_split(pr_fma2(pr_pair(__uint_as_float(v[c * 32 + 2 * x]), __uint_as_float(v[c * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
+              p0 = pr_ex2(p0);
+              p1 = pr_ex2(p1);
+              ll = pr_add2(ll, pr_pair(p0, p1));
+              pk[x] = pr_half2(p0, p1);
+            }
+            pr_st16(s_t + c * 16, pk);
+          }
+          pr_split(ll, l0, l1);
+        }
+        // otherwise 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
 #pragma unroll 1
-        for (int c = 0; c < (dead ? 0 : 4); ++c) {
+        for (int c = 0; c < (dead || plain ? 0 : 4); ++c) {
           const int t = t0 + c * 32;
           if (t >= hi_max || t + 32 <= lo_min) {  // no row sees any
             const uint32_t none[16] = {};
@@ -869,9 +937,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       }
     }
   } else {
-    // ---------------------------------------------------------------- MMAs, by one thread
+    // ---------------------------------------------------------------- MMAs, by one warp
     pr_regs<P::kRegRest>();
-    if (warp == 0 && lane == 0) {
+    if (__shfl_sync(kFull, warp, 0) == 0) {
+      const uint32_t lead = elect_lane();
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
       // Short loops and few instructions per MMA: this thread's code competes with the other warps' for the
       // instruction caches. Only the low word of a descriptor changes (addresses stay below 2^18).
@@ -882,26 +952,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       int ks = 0, vs = 0;                      // ring places
       uint32_t k_par = 0, v_par = 0;
       auto scores = [&](int i, int slot) {
-        const uint32_t d = tmem + slot * 128;
+        const uint32_t d = tm + slot * 128;
         uint32_t qd = qa + i * (P::kTile >> 4), kd = ka + ks * (P::kTile >> 4);
 #pragma unroll 1
         for (int p = 0; p < G; ++p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ss(d, (uint64_t)hi_k << 32 | (qd + k * 2), (uint64_t)hi_k << 32 | (kd + k * 2), id_s, p + k > 0);
+            mma_ss(d, (uint64_t)hi_k << 32 | (qd + k * 2), (uint64_t)hi_k << 32 | (kd + k * 2), id_s, p + k > 0, lead);
           qd += kPanel >> 4;
           kd += kPanel >> 4;
         }
-        tc_commit(&sh.s_full[slot]);
+        mma_commit(&sh.s_full[slot], lead);
       };
       auto product = [&](int i, int slot, bool first) {
-        const uint32_t d = tmem + 256 + i * D;
-        uint32_t pa = tmem + slot * 128, vd = va + vs * (P::kTile >> 4), acc = !first;
+        const uint32_t d = tm + 256 + i * D;
+        uint32_t pa = tm + slot * 128, vd = va + vs * (P::kTile >> 4), acc = !first;
 #pragma unroll 1
         for (int k = 0; k < kPrTok / 64; ++k) {
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            mma_ts(d, pa + n * 8, (uint64_t)hi_v << 32 | (vd + n * 128), id_o, acc);
+            mma_ts(d, pa + n * 8, (uint64_t)hi_v << 32 | (vd + n * 128), id_o, acc, lead);
             acc = 1;
           }
           pa += 32;
@@ -909,14 +979,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
       };
       auto k_next = [&]() {
-        tc_commit(&sh.k_free[ks]);
+        mma_commit(&sh.k_free[ks], lead);
         if (++ks == ST) {
           ks = 0;
           k_par ^= 1;
         }
       };
-      for (; wk.live(); wk.next(w, units)) {
-        const int n = wk.i1 - wk.i0;
+      for (; __shfl_sync(kFull, (int)wk.live(), 0); wk.next(w, units)) {
+        const int n = __shfl_sync(kFull, wk.i1 - wk.i0, 0);
         for (int it = -1; it < n; ++it) {  // step it: the product of tile it, the scores of tile it + 1
           if (NQ == 2) {
             if (it >= 0) pr_wait(&sh.v_full[vs], v_par, fail);
@@ -927,7 +997,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 p_par ^= 1u << i;
                 tc_fence_after();
                 product(i, i, it == 0);
-                if (it == n - 1) tc_commit(&sh.o_full[i]);
+                if (it == n - 1) mma_commit(&sh.o_full[i], lead);
               } else {
                 pr_wait(&sh.q_full[i], q_par >> i & 1, fail);
                 q_par ^= 1u << i;
@@ -957,12 +1027,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
               p_par ^= 1u << slot;
               tc_fence_after();
               product(0, slot, it == 0);
-              tc_commit(&sh.pv_done);
-              if (it == n - 1) tc_commit(&sh.o_full[0]);
+              mma_commit(&sh.pv_done, lead);
+              if (it == n - 1) mma_commit(&sh.o_full[0], lead);
             }
           }
           if (it >= 0) {
-            tc_commit(&sh.v_free[vs]);
+            mma_commit(&sh.v_free[vs], lead);
             if (++vs == ST) {
               vs = 0;
               v_par ^= 1;
@@ -971,7 +1041,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
       }
       // nothing is left in flight, whatever ended the loop
-      tc_commit(&sh.drain);
+      mma_commit(&sh.drain, lead);
       const unsigned long long t0 = tc_time();
       while (!tc_mbar_try_suspend(&sh.drain, 0) && (long long)(tc_time() - t0) < kPrTimeoutNs) {
       }
