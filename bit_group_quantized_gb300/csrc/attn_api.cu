@@ -162,6 +162,7 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   if (!ws || !al(ws, 256) ||
       ws_bytes < attn_workspace_bytes(s->batch, s->rows, s->max_q, q_heads, c->kv_heads, c->head_dim))
     return BGQ_ERR_WORKSPACE;
+  if ((int64_t)s->rows * (q_heads / c->kv_heads) > INT32_MAX) return BGQ_ERR_UNSUPPORTED;
   if (s->rows == 0) return BGQ_OK;
   AttnArgs a;
   a.c = *c;

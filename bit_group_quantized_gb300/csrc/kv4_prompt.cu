@@ -8,8 +8,8 @@
 //   S = Q K^T   both fp16 in shared memory, S fp32 in tensor memory;
 //   P = exp2(S c - m), fp16, written over S in tensor memory;
 //   O += P V    P from tensor memory, V fp16 in shared memory.
-// The warps are specialised: four dequantise K and V (a thread takes a token: codes and
-// pairs by plain loads one tile ahead, value = code * scale + bias in fp16,
+// The warps are specialised: eight dequantise K and V (a thread takes a token: its codes
+// come by cp.async a tile ahead, value = code * scale + bias in fp16,
 // stored in the 128-byte swizzled layout: K as the K-major, V as the MN-major
 // operand), four for each tile of rows do the softmax (a thread owns a row: its
 // maximum and sum need no shuffles), and bring the next unit's queries while the last
@@ -38,11 +38,14 @@
 
 namespace bgq {
 
-constexpr int kPrThreads = 512;  // warp 0: MMAs, 4-7: dequantisation, 8-11: rows 0-127, 12-15: rows 128-255
+constexpr int kPrThreads = 640;  // warp 0: MMAs, 4-7: K's dequantisation, 8-11: V's, 12-15: rows 0-127, 16-19: rows 128-255
+constexpr int kPrRegs = 96;      // of a thread at launch: 65536 / 640, in eights
 constexpr int kPrTok = 128;      // tokens of a tile
 constexpr long long kPrTimeoutNs = 1000000000ll;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 4096;
+// What bringing a unit's queries and writing its rows costs, in tiles: CTAs with many short units take fewer tiles.
+constexpr int kUnitCost = 3;
 
 template <int D>
 struct Prompt {
@@ -51,12 +54,14 @@ struct Prompt {
   static constexpr int kRows = 128 * NQ;
   static constexpr int ST = D == 256 ? 1 : 2;  // K and V tiles held
   static constexpr int kTile = kPrTok * D * 2;  // bytes of a Q, K or V tile
+  static constexpr int kRaw = kPrTok * D / 2;   // bytes of a tile's K or V codes
   // more than half an SM's, so that no second CTA comes to wait for this one's tensor memory
-  static constexpr int kSmem = 1024 + (NQ + 2 * ST) * kTile > 120 * 1024 ? 1024 + (NQ + 2 * ST) * kTile : 120 * 1024;
+  static constexpr int kNeed = 1024 + (NQ + 2 * ST) * kTile + 2 * kRaw;
+  static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
   static constexpr int kSlot = 128 * D + 256;  // floats of a part: O by 4 columns and row, then m, then l
-  // registers of the four warpgroups: together at most the 512 * 128 of the launch
-  static constexpr int kRegSoft = D == 256 ? 240 : 184, kRegDeq = D == 256 ? 184 : 104, kRegRest = 40;
-  static_assert(NQ * kRegSoft + kRegDeq + (3 - NQ) * kRegRest <= 4 * 128, "more registers than the launch has");
+  // registers of a softmax, dequantisation and other warpgroup's threads: together at most the launch's
+  static constexpr int kRegSoft = D == 256 ? 176 : 136, kRegDeq = D == 256 ? 104 : 80, kRegRest = 40;
+  static_assert(NQ * kRegSoft + 2 * kRegDeq + (3 - NQ) * kRegRest <= 5 * kPrRegs, "more registers than the launch has");
 };
 
 // A unit: its sequence and row tile, its tokens' first and how many tiles of them, and the sequence's span.
@@ -64,9 +69,21 @@ struct __align__(16) PrUnit {
   int b, rt, tiles, begin;
   Span sp;
 };
+// A sequence's row tiles, and the tokens of one of them.
+__device__ __forceinline__ int pr_row_tiles(const AttnArgs& a, const Span& sp, int rows_unit) {
+  return (min(sp.q_len, a.v.rows) * (a.q_heads / a.c.kv_heads) + rows_unit - 1) / rows_unit;
+}
+__device__ __forceinline__ void pr_tokens(const AttnArgs& a, PrUnit& un, int rows_unit) {
+  const int group = a.q_heads / a.c.kv_heads, pos0 = un.sp.kv_len - un.sp.q_len;
+  const int j0 = un.rt * rows_unit / group;
+  const int j1 = min(un.sp.q_len - 1, (un.rt * rows_unit + rows_unit - 1) / group);
+  un.begin = a.window > 0 ? min(max(0, pos0 + j0 - a.window + 1), un.sp.held) / 16 * 16 : 0;  // 16 tokens lie in one page
+  const int end = a.causal ? min(un.sp.held, pos0 + j1 + 1) : un.sp.held;
+  un.tiles = max(1, (end - un.begin + kPrTok - 1) / kPrTok);  // at least one: rows that see no token are written too
+}
 struct PrPlan {  // at the start of the workspace, behind the control block
   int units, pad;
-  long long sum;  // tiles of all units, for one key head
+  long long sum;  // cost of all units, for one key head
 };
 
 struct PrWs {
@@ -74,7 +91,7 @@ struct PrWs {
   PrPlan* plan;
   int* count;         // [grid][NQ] arrivals, left at zero
   PrUnit* units;      // [cap]
-  long long* prefix;  // [cap] tiles before a unit
+  long long* prefix;  // [cap] cost of the units before a unit
   float* part;        // [grid][2][NQ][kSlot]
   int cap;
   size_t bytes;
@@ -129,12 +146,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
   __shared__ long long warp_sum[kPlanThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int group = a.q_heads / a.c.kv_heads;
   constexpr int per = kPlanSeqs / kPlanThreads;
   int n[per], own = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
-    n[i] = b < a.v.batch ? (int)(((long long)min(kv4_span(a.v, b).q_len, a.v.rows) * group + rows_unit - 1) / rows_unit) : 0;
+    n[i] = b < a.v.batch ? pr_row_tiles(a, kv4_span(a.v, b), rows_unit) : 0;
     own += n[i];
   }
   long long total;
@@ -155,18 +171,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
         const int mid = (lo + hi) >> 1;
         if (first[mid] <= u) lo = mid; else hi = mid;
       }
-      const Span sp = un.sp = kv4_span(a.v, lo);
-      const int pos0 = sp.kv_len - sp.q_len;
+      un.sp = kv4_span(a.v, lo);
       un.b = lo;
       un.rt = u - first[lo];
-      const int j0 = (int)((long long)un.rt * rows_unit / group);
-      const int j1 = (int)min((long long)sp.q_len - 1, (((long long)un.rt + 1) * rows_unit - 1) / group);
-      un.begin = a.window > 0 ? min(max(0, pos0 + j0 - a.window + 1), sp.held) : 0;
-      const int end = a.causal ? min(sp.held, pos0 + j1 + 1) : sp.held;
-      un.tiles = max(1, (end - un.begin + kPrTok - 1) / kPrTok);  // at least one: rows that see no token are written too
+      pr_tokens(a, un, rows_unit);
     }
     long long chunk;
-    const long long pre = plan_scan(un.tiles, warp_sum, chunk) - un.tiles;
+    const int cost = u < units ? un.tiles + kUnitCost : 0;
+    const long long pre = plan_scan(cost, warp_sum, chunk) - cost;
     if (u < units) {
       w.units[u] = un;
       w.prefix[u] = sum + pre;
@@ -206,6 +218,10 @@ __device__ __forceinline__ void pr_wait_st() { asm volatile("tcgen05.wait::st.sy
 
 __device__ __forceinline__ uint32_t pr_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pr_bf2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // O of the warp's rows times f (a row's own), eight columns at a time: rare, and few registers.
@@ -251,11 +267,11 @@ __device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Registers of a warpgroup's threads, from the launch's 128.
+// Registers of a warpgroup's threads, from the launch's.
 template <int N>
 __device__ __forceinline__ void pr_regs() {
-  if (N > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  if (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  if (N > kPrRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if (N < kPrRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void pr_wait_loop(uint64_t* m, uint32_t parity, volatile int* fail) {
@@ -351,44 +367,55 @@ struct PrShared {
   int fail, last[NQ];
 };
 
-// A CTA's share of the list, unit by unit; the unit behind is fetched while one is worked on.
+// A CTA's share of the list, unit by unit. A unit takes kUnitCost places of the list, then one for each tile; the
+// CTA whose share holds a tile's place does the tile. Within a sequence the next unit is worked out, not loaded.
+template <int D>
 struct PrWalk {
-  long long x, x1;
-  int h, u, i0, i1;
-  PrUnit un, nx;
-  __device__ __forceinline__ static PrUnit get(const PrWs& w, int u) {
+  long long x, x1;  // the first tile's place of the unit in hand; the share's end
+  int h, u, i0, i1, n0;  // tiles i0 .. i1 - 1 of unit u; tiles of the share before them
+  PrUnit un;
+  __device__ __forceinline__ void get(const PrWs& w) {
     const int4* p = reinterpret_cast<const int4*>(w.units + u);
     const int4 a = p[0], b = p[1];
-    return PrUnit{a.x, a.y, a.z, a.w, {b.x, b.y, b.z, b.w}};
+    un = PrUnit{a.x, a.y, a.z, a.w, {b.x, b.y, b.z, b.w}};
   }
-  __device__ __forceinline__ void start(const PrWs& w, long long x_, long long x1_, long long sum, int units) {
-    x = x_;
+  __device__ __forceinline__ void start(const AttnArgs& a, const PrWs& w, long long x0, long long x1_, long long sum, int units) {
     x1 = x1_;
-    if (x >= x1) return;
-    h = (int)(x / sum);
-    const long long y = x - h * sum;
+    h = (int)(x0 / sum);
+    const long long y = x0 - h * sum;
     int lo = 0, hi = units;  // the last unit that starts at or before y
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (w.prefix[mid] <= y) lo = mid; else hi = mid;
     }
     u = lo;
-    un = get(w, u);
-    nx = get(w, u + 1 == units ? 0 : u + 1);
-    i0 = (int)(y - w.prefix[u]);
-    i1 = (int)min((long long)un.tiles, i0 + x1 - x);
+    get(w);
+    n0 = 0;
+    x = x0 - y + w.prefix[u] + kUnitCost;
+    i0 = (int)max(0ll, x0 - x);
+    i1 = (int)min((long long)un.tiles, x1 - x);
+    if (i1 <= i0) {
+      i0 = i1 = un.tiles;  // nothing of this unit
+      next(a, w, units);
+    }
   }
-  __device__ __forceinline__ bool live() const { return x < x1; }
-  __device__ __forceinline__ void next(const PrWs& w, int units) {
-    x += i1 - i0;
+  __device__ __forceinline__ bool live() const { return i1 > i0; }
+  __device__ __forceinline__ void next(const AttnArgs& a, const PrWs& w, int units) {
+    x += un.tiles + kUnitCost;
+    n0 += i1 - i0;
+    i0 = i1 = 0;
     if (x >= x1) return;
+    const bool same = un.rt + 1 < pr_row_tiles(a, un.sp, Prompt<D>::kRows);
     if (++u == units) {
       u = 0;
       ++h;
     }
-    un = nx;
-    nx = get(w, u + 1 == units ? 0 : u + 1);
-    i0 = 0;
+    if (same && u > 0) {
+      ++un.rt;
+      pr_tokens(a, un, Prompt<D>::kRows);
+    } else {
+      get(w);
+    }
     i1 = (int)min((long long)un.tiles, x1 - x);
   }
 };
@@ -396,37 +423,67 @@ struct PrWalk {
 // ---------------------------------------------------------------------------
 // Dequantisation: 128 threads, a token each.
 // ---------------------------------------------------------------------------
+// Codes come 16 bytes a lane, 16 tokens (of one page) at a time, into a buffer whose 16-byte pieces are
+// swizzled so that 8 threads that read a piece each of their own token's row hit different banks.
 template <int D>
-struct PrRow {  // one token's codes and pairs of K or V
-  uint4 q[D / 32];
-  uint32_t sb[D / kGroup];
-};
-template <int D>
-__device__ __forceinline__ void pr_load(PrRow<D>& r, const uint32_t* q, const uint16_t* sb, long long row) {
-  if (row < 0) {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < D / kGroup; ++i) r.sb[i] = 0;
-    return;
-  }
-  const uint4* qs = reinterpret_cast<const uint4*>(q + row * (D / 8));
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) r.q[i] = qs[i];
-  const uint32_t* ss = reinterpret_cast<const uint32_t*>(sb) + row * (D / kGroup);
-#pragma unroll
-  for (int i = 0; i < D / kGroup; ++i) r.sb[i] = ss[i];
+__device__ __forceinline__ int pr_raw(int tok, int ch) {
+  if (D == 64) return (tok >> 2) * 128 + (tok & 3) * 32 + ((ch ^ (tok >> 2)) & 1) * 16;
+  if (D == 128) return (tok >> 1) * 128 + (tok & 1) * 64 + ((ch ^ (tok >> 1)) & 3) * 16;
+  return tok * 128 + ((ch ^ tok) & 7) * 16;
 }
-// The exponent that the values of the warp's 32 tokens are divided by, and the tokens whose pair of a group is not finite.
+__device__ __forceinline__ void pr_cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+// The codes of the warp's 32 tokens. Lanes 0 and 16 hold in `base` the row of the first of their 16 tokens, which lie in
+// one page; -1: absent, zeros.
 template <int D>
-__device__ __forceinline__ int pr_range(const PrRow<D>& r, uint32_t (&bad)[D / kGroup]) {
+__device__ __forceinline__ void pr_fetch(uint32_t raw, const uint32_t* q, long long base, int lane) {
+  constexpr int CPT = D / 32;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const long long row = __shfl_sync(kFull, base, 16 * m);
+    const char* src = reinterpret_cast<const char*>(q) + (row < 0 ? 0 : row) * (D / 2) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < CPT / 2; ++i) {
+      const int id = i * 32 + lane;
+      pr_cp16(raw + m * (8 * D) + pr_raw<D>(id / CPT, id % CPT), src + i * 512, row >= 0);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void pr_pairs(uint32_t (&sb)[D / kGroup], const uint16_t* p, long long row) {
+#pragma unroll
+  for (int i = 0; i < D / kGroup; ++i) sb[i] = 0;
+  if (row >= 0) {
+    const uint32_t* ss = reinterpret_cast<const uint32_t*>(p) + row * (D / kGroup);
+#pragma unroll
+    for (int i = 0; i < D / kGroup; ++i) sb[i] = ss[i];
+  }
+}
+// The exponent that the values of the warp's 32 tokens are divided by (from 16 |s| + |b|, which none passes), and whether
+// any pair is not finite: then also which tokens' of which group.
+template <int D>
+__device__ __forceinline__ int pr_range(const uint32_t (&sb)[D / kGroup], uint32_t& any, uint32_t (&bad)[D / kGroup]) {
   float big = 0.f;
+  bool odd = false;
 #pragma unroll
   for (int g = 0; g < D / kGroup; ++g) {
-    const float s = bf16lo(r.sb[g]), b = bf16hi(r.sb[g]);
-    const bool fin = fabsf(s) < INFINITY && fabsf(b) < INFINITY;
-    bad[g] = __ballot_sync(kFull, !fin);
-    if (fin) big = fmaxf(big, fmaxf(fabsf(b), fminf(fabsf(fmaf(15.f, s, b)), 3e38f)));
+    const float top = fmaf(16.f, fabsf(bf16lo(sb[g])), fabsf(bf16hi(sb[g])));
+    odd |= !(top < INFINITY);
+    big = fmaxf(big, top);
+  }
+  any = __ballot_sync(kFull, odd);
+  if (any) {
+    big = 0.f;
+    any = 0;
+#pragma unroll
+    for (int g = 0; g < D / kGroup; ++g) {
+      const float s = fabsf(bf16lo(sb[g])), b = fabsf(bf16hi(sb[g]));
+      const bool fin = s < INFINITY && b < INFINITY;
+      bad[g] = __ballot_sync(kFull, !fin);
+      any |= bad[g];
+      if (fin) big = fmaxf(big, fminf(fmaf(16.f, s, b), 3e38f));
+    }
   }
   const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
   const int k = (int)(bits >> 23) - 127;
@@ -434,19 +491,22 @@ __device__ __forceinline__ int pr_range(const PrRow<D>& r, uint32_t (&bad)[D / k
 }
 // Writes the token's values into its row of the tile.
 template <int D>
-__device__ __forceinline__ void pr_store(const PrRow<D>& r, unsigned char* tile, int t, const uint32_t (&bad)[D / kGroup], int e) {
+__device__ __forceinline__ void pr_store(const unsigned char* raw, const uint32_t (&sb)[D / kGroup], unsigned char* tile, int t,
+                                         int e) {
   const float down = exp2i(-e);
 #pragma unroll
   for (int g = 0; g < D / kGroup; ++g) {
-    const bool fin = !(bad[g] >> (t & 31) & 1);
-    const float s = fin ? bf16lo(r.sb[g]) * down : 0.f, b = fin ? bf16hi(r.sb[g]) * down : 0.f;
+    float s = bf16lo(sb[g]) * down, b = bf16hi(sb[g]) * down;
+    if (!(fabsf(s) < INFINITY && fabsf(b) < INFINITY)) s = b = 0.f;
     const uint32_t s2 = pr_half2(s, s), b2 = pr_half2(b, b);
     unsigned char* row = tile + g * kPanel + t * 128;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4& q = r.q[g * 2 + (c >> 2)];
-      const uint32_t w = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
-      *reinterpret_cast<uint4*>(row + ((c ^ (t & 7)) * 16)) = pr_values(w, s2, b2);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 q = *reinterpret_cast<const uint4*>(raw + pr_raw<D>(t & 31, g * 2 + h));
+      *reinterpret_cast<uint4*>(row + (((h * 4) ^ (t & 7)) * 16)) = pr_values(q.x, s2, b2);
+      *reinterpret_cast<uint4*>(row + (((h * 4 + 1) ^ (t & 7)) * 16)) = pr_values(q.y, s2, b2);
+      *reinterpret_cast<uint4*>(row + (((h * 4 + 2) ^ (t & 7)) * 16)) = pr_values(q.z, s2, b2);
+      *reinterpret_cast<uint4*>(row + (((h * 4 + 3) ^ (t & 7)) * 16)) = pr_values(q.w, s2, b2);
     }
   }
 }
@@ -457,57 +517,57 @@ struct PrRowOf {
   bool own, ok;  // a row of the unit; and one that may be read and written
 };
 template <int D>
-__device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk& wk, int group, int at) {
+__device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk<D>& wk, int group, int at) {
   const Span& sp = wk.un.sp;
-  const long long cols = (long long)min(sp.q_len, a.v.rows) * group;
-  const long long col = (long long)wk.un.rt * Prompt<D>::kRows + at;
+  const int cols = min(sp.q_len, a.v.rows) * group;  // rows * group is below 2^31
+  const int col = wk.un.rt * Prompt<D>::kRows + at;
   PrRowOf r;
   r.own = col < cols;
-  const long long cc = r.own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
-  const int j = (int)(cc / group);
-  r.head = wk.h * group + (int)(cc - (long long)j * group);
+  const int cc = r.own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
+  const int j = cc / group;
+  r.head = wk.h * group + cc - j * group;
   r.row = sp.first + j;
   r.ok = r.own && r.row >= 0 && r.row < a.v.rows;
   r.pos = sp.kv_len - sp.q_len + j;
   return r;
 }
-// Its values into row r of the query tile, fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7;
-// returns the factor of its scores.
+// The warp's 32 query rows on their way into the query tile as they are (bf16), 16 bytes a lane.
 template <int D>
-__device__ __forceinline__ float pr_query(const AttnArgs& a, const PrRowOf& q, unsigned char* tile, int r) {
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(q.ok ? q.row : 0) * a.q_stride + q.head * D);
-  constexpr int R = D / 8 < 16 ? D / 8 : 16, PASS = D / 8 / R;
-  float top = 0.f;
-  uint4 raw[R];
-#pragma unroll
-  for (int p = 0; p < PASS; ++p) {
-#pragma unroll
-    for (int n = 0; n < R; ++n) raw[n] = q.ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int n = 0; n < R; ++n) {
-      float f[8];
-      unpack_bf16x8(raw[n], f);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(f[x]));
-    }
+__device__ __forceinline__ void pr_query_fetch(const AttnArgs& a, const PrRowOf& q, uint32_t tile, int r0, int lane) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows at a time
+  const long long mine = q.ok ? (long long)q.row * a.q_stride + q.head * D : -1;
+  const int ch = lane % LPR;
+#pragma unroll 8
+  for (int k = 0; k < 32; k += RPW) {
+    const int rl = k + lane / LPR, r = r0 + rl;
+    const long long at = __shfl_sync(kFull, mine, rl);
+    pr_cp16(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16), a.q + (at < 0 ? 0 : at) + ch * 8, at >= 0);
   }
-  const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
+}
+// Row r of the tile, in place: fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7; returns the
+// factor of its scores.
+template <int D>
+__device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char* tile, int r) {
+  auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16)); };
+  uint32_t t2[4] = {};
+#pragma unroll 8
+  for (int n = 0; n < D / 8; ++n) {
+    const uint4 v = *chunk(n);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(t2[k]) : "r"(w[k]));
+  }
+  uint32_t top = 0;  // the largest magnitude's bits: without their signs they order like values (NaN is passed over)
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = max(top, max(t2[k] & 0x7fff0000u, t2[k] << 17 >> 1));
+  const int e = top && top < 0x7f800000u ? min(max((int)(top >> 23) - 130, -110), 110) : 0;
   const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
-#pragma unroll
-  for (int p = PASS - 1; p >= 0; --p) {
-    if (p < PASS - 1) {
-#pragma unroll
-      for (int n = 0; n < R; ++n) raw[n] = q.ok ? src[p * R + n] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int n = 0; n < R; ++n) {
-      float f[8];
-      unpack_bf16x8(raw[n], f);
-      const int ch = p * R + n;
-      *reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) =
-          make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
-                     pr_half2(f[3] * up, f[7] * up));
-    }
+#pragma unroll 4
+  for (int n = 0; n < D / 8; ++n) {
+    float f[8];
+    unpack_bf16x8(*chunk(n), f);
+    *chunk(n) = make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
+                           pr_half2(f[3] * up, f[7] * up));
   }
   return fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
 }
@@ -554,37 +614,33 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
   const int units = w.plan->units;
   const long long sum = w.plan->sum, total = sum * a.c.kv_heads;
-  // at least two tiles a CTA: a cut unit costs about as much as one
-  const long long ctas = min((long long)gridDim.x, (total + 1) / 2);
+  // every CTA's share holds a tile, as its length is above kUnitCost
+  const long long ctas = min((long long)gridDim.x, total / (kUnitCost + 1));
   const int cta = blockIdx.x;
   const int group = a.q_heads / a.c.kv_heads;
-  PrWalk wk;
-  wk.x = wk.x1 = 0;
-  if (cta < ctas) wk.start(w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
+  PrWalk<D> wk;
+  wk.i0 = wk.i1 = 0;
+  if (cta < ctas) wk.start(a, w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
 
-  if (warp >= 8 && warp < 8 + 4 * NQ) {
+  if (warp >= 12 && warp < 12 + 4 * NQ) {
     // ---------------------------------------------------------------- softmax: a thread owns a row
     pr_regs<P::kRegSoft>();
-    const int i = (warp >> 2) - 2, r = tid & 127;
+    const int i = (warp >> 2) - 3, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
     const uint32_t o_t = tmem + 256 + i * D + lanes;
     uint32_t s_par = 0, o_par = 0;  // parities: s_full (bit per slot), o_full
     uint32_t pv_par = 0;
-    PrRowOf me_row;
-    float c2_next = 0.f;
-    auto bring = [&]() {  // the rows and queries of the unit in wk
-      if (!wk.live()) return;
-      me_row = pr_row<D>(a, wk, group, i * 128 + r);
-      c2_next = pr_query<D>(a, me_row, q_s + i * P::kTile, r);
-      tc_fence_proxy();
-      tc_arrive(&sh.q_full[i]);
-    };
-    bring();
-    while (wk.live()) {
-      const float c2 = c2_next;
-      const int row = me_row.row, pos = me_row.pos;
+    // A unit's end runs beside the next one's first product: the next queries are brought after the last
+    // probabilities (the last scores are done then), before O is waited for. The first unit follows none.
+    PrWalk<D> nw = wk;
+    float c2 = 0.f, c2_next = 0.f;
+    unsigned char* const q_tile = q_s + i * P::kTile;
+    PrRowOf rw, next_row;
+    bool none = true;
+    for (;;) {
+      const int row = rw.row, pos = rw.pos, head = rw.head;
       const Span& sp = wk.un.sp;
-      const bool own = me_row.own, ok = me_row.ok;
+      const bool own = !none && rw.own, ok = rw.ok;
       const int hi = min(sp.held, a.causal ? pos + 1 : sp.kv_len), lo = a.window > 0 ? pos - a.window + 1 : 0;
       const int hi_min = __reduce_min_sync(kFull, hi), hi_max = __reduce_max_sync(kFull, hi);
       const int lo_min = __reduce_min_sync(kFull, lo), lo_max = __reduce_max_sync(kFull, lo);
@@ -595,33 +651,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       bool fresh = true;    // no value has set e_run yet
       uint32_t poison = 0;  // bit 0: a key that is not finite is seen; bit 1 + g: a value of group g
 #pragma unroll 1
-      for (int it = wk.i0; it < wk.i1; ++it) {
+      for (int it = wk.i0; it < (none ? wk.i0 : wk.i1); ++it) {
         const int slot = NQ == 2 ? i : (it - wk.i0) & 1;
         const uint32_t s_t = tmem + slot * 128 + lanes;
         pr_wait(&sh.s_full[slot], s_par >> slot & 1, fail);
         s_par ^= 1u << slot;
         tc_fence_after();
         // tiles are numbered over the CTA's whole share, as in the dequantisation
-        const int mt = (int)((wk.x + (it - wk.i0)) & (kMetaTiles - 1));
+        const int mt = (wk.n0 + it - wk.i0) & (kMetaTiles - 1);
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
         const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && !fresh && e_run == 0;
-        if (plain && !dead) {
-          // every row sees every token, and no factor but the row's: all scores in registers at once
-          uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pr_ld32(s_t + c * 32, v + c * 32);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pr_wait_ld(v + c * 32);
+        // every row sees every token, and no factor but the row's: 64 tokens at a time
+#pragma unroll 1
+        for (int c = 0; c < (plain && !dead ? 4 : 0); c += 2) {
+          uint32_t v[64];
+          pr_ld32(s_t + c * 32, v);
+          pr_ld32(s_t + c * 32 + 32, v + 32);
+          pr_wait_ld(v);
+          pr_wait_ld(v + 32);
           float tp[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tp[c] = pr_max3(__uint_as_float(v[c]), __uint_as_float(v[4 + c]), __uint_as_float(v[8 + c]));
+          for (int k = 0; k < 4; ++k) tp[k] = pr_max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
 #pragma unroll
-          for (int x = 12; x < 124; x += 8)
+          for (int x = 12; x < 60; x += 8)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tp[c] = pr_max3(tp[c], __uint_as_float(v[x + c]), __uint_as_float(v[x + 4 + c]));
+            for (int k = 0; k < 4; ++k) tp[k] = pr_max3(tp[k], __uint_as_float(v[x + k]), __uint_as_float(v[x + 4 + k]));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tp[c] = fmaxf(tp[c], __uint_as_float(v[124 + c]));
+          for (int k = 0; k < 4; ++k) tp[k] = fmaxf(tp[k], __uint_as_float(v[60 + k]));
           const float ck = fmaxf(c2, 0x1p-126f);
           const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
           const bool raise = top > m + 8.f;
@@ -632,6 +689,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             mm = up == -INFINITY ? 0.f : up;
             l0 *= f;
             l1 *= f;
+            pr_wait_st();
+#pragma unroll 1
+            for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
             if (it > wk.i0) {
               if (NQ == 1) {  // the product before this one may still be running
                 pr_wait(&sh.pv_done, pv_par ^ 1, fail);
@@ -643,18 +703,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           uint64_t ll = pr_pair(l0, l1);
           const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               float p0, p1;
-              pr_split(pr_fma2(pr_pair(__uint_as_float(v[c * 32 + 2 * x]), __uint_as_float(v[c * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
+              pr_split(pr_fma2(pr_pair(__uint_as_float(v[k * 32 + 2 * x]), __uint_as_float(v[k * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
               p0 = pr_ex2(p0);
               p1 = pr_ex2(p1);
               ll = pr_add2(ll, pr_pair(p0, p1));
               pk[x] = pr_half2(p0, p1);
             }
-            pr_st16(s_t + c * 16, pk);
+            pr_st16(s_t + (c + k) * 16, pk);
           }
           pr_split(ll, l0, l1);
         }
@@ -741,14 +801,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             pk[x] = pr_half2(p0, p1);
           }
           pr_split(ll, l0, l1);
-          if (ve != e_run) {  // values of another unit than O (never larger): in fp32, rounded once
-            const float f = exp2i(max(ve - e_run, -126));
+          if (ve != e_run) {  // values of another unit than O, never larger
+            const float f = exp2i(max(ve - e_run, -24));
+            const uint32_t f2 = pr_half2(f, f);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float p0, p1;
-              pr_split(pr_fma2(pr_pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), ck2, mm2), p0, p1);
-              pk[x] = pr_half2(pr_ex2(p0) * f, pr_ex2(p1) * f);
-            }
+            for (int x = 0; x < 16; ++x) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(pk[x]) : "r"(pk[x]), "r"(f2));
           }
           pr_st16(s_t + c * 16, pk);
         }
@@ -758,13 +815,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         tc_arrive(&sh.p_full[slot]);
       }
 
-      // ---- the unit's end: the next one's queries (the last scores are done), then O / l, or a part of it
+      if (!none) nw.next(a, w, units);
+      if (nw.live()) {
+        next_row = pr_row<D>(a, nw, group, i * 128 + r);
+        pr_query_fetch<D>(a, next_row, tc_smem(q_tile), r & ~31, lane);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        c2_next = pr_query_scale<D>(a, q_tile, r);
+        tc_fence_proxy();
+        tc_arrive(&sh.q_full[i]);
+      }
+      // ---- the unit's end: O / l, or a part of it
+      if (!none) {
       const bool whole = wk.i0 == 0 && wk.i1 == wk.un.tiles;
-      const long long u0 = wk.x - wk.i0, u1 = u0 + wk.un.tiles - 1;  // the unit's first and last place in the list
-      const int head = me_row.head;
+      const long long u0 = wk.x, u1 = u0 + wk.un.tiles - 1;  // the first and last tile's places in the list
       float* const part = w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot;
-      wk.next(w, units);
-      bring();
       pr_wait(&sh.o_full[i], o_par, fail);
       o_par ^= 1;
       tc_fence_after();
@@ -786,9 +851,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (ok) {
 #pragma unroll
               for (int x = 0; x < 32; x += 8) {  // columns come as 0 4 1 5 2 6 3 7
-                auto b2 = [&](int p, int q) {
-                  return (uint32_t)f2bf(__uint_as_float(v[x + p])) | (uint32_t)f2bf(__uint_as_float(v[x + q])) << 16;
-                };
+                auto b2 = [&](int p, int q) { return pr_bf2(__uint_as_float(v[x + p]), __uint_as_float(v[x + q])); };
                 *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
               }
             }
@@ -820,7 +883,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           __threadfence();
           auto at = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * NQ + i) * P::kSlot; };
           float top = -INFINITY, ls = 0.f;
+#pragma unroll 1
           for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + 128 * D + r));
+#pragma unroll 1
           for (int c = c0; c <= c1; ++c) {
             const float mc = __ldcg(at(c) + 128 * D + r);
             ls = fmaf(mc == top ? 1.f : pr_ex2(mc - top), __ldcg(at(c) + 128 * D + 128 + r), ls);
@@ -831,12 +896,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             float v[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) v[x] = 0.f;
+#pragma unroll 1
             for (int c = c0; c <= c1; ++c) {
+              const float* const pp = at(c) + r * 4;
               const float mc = __ldcg(at(c) + 128 * D + r);
               const float f = mc == top ? 1.f : pr_ex2(mc - top);
 #pragma unroll
               for (int x = 0; x < 16; x += 4) {
-                const float4 p = __ldcg(reinterpret_cast<const float4*>(at(c) + ((d + x) / 4 * 128 + r) * 4));
+                const float4 p = __ldcg(reinterpret_cast<const float4*>(pp + (d + x) * 128));
                 v[x] = fmaf(f, p.x, v[x]);
                 v[x + 1] = fmaf(f, p.y, v[x + 1]);
                 v[x + 2] = fmaf(f, p.z, v[x + 2]);
@@ -846,7 +913,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             if (ok) {
 #pragma unroll
               for (int x = 0; x < 16; x += 8) {
-                auto b2 = [&](int p, int q) { return (uint32_t)f2bf(v[x + p] * inv) | (uint32_t)f2bf(v[x + q] * inv) << 16; };
+                auto b2 = [&](int p, int q) { return pr_bf2(v[x + p] * inv, v[x + q] * inv); };
                 *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
               }
             }
@@ -854,88 +921,102 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
         }
       }
+      }
+      if (!nw.live()) break;
+      wk = nw;
+      rw = next_row;
+      c2 = c2_next;
+      none = false;
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---------------------------------------------------------------- dequantisation: a thread owns a token
+  } else if (warp >= 4 && warp < 12) {
+    // ---------------------------------------------------------------- dequantisation
     pr_regs<P::kRegDeq>();
-    // its codes are loaded one tile ahead, and its page two
-    const int t = tid & 127;
+    // four warps take K, four V; a warp has 32 tokens, a lane one of them. As soon as a warp has read its codes of a
+    // tile, the next tile's go on their way into the same place; the pages are looked up a tile earlier still.
+    const bool val = warp >= 8;
+    const int part = (warp & 3) * 32;
+    uint64_t* const full = val ? sh.v_full : sh.k_full;
+    uint64_t* const free_ = val ? sh.v_free : sh.k_free;
+    unsigned char* const tiles = val ? v_s : k_s;
+    const uint32_t* const codes = val ? a.c.v_q : a.c.k_q;
+    const uint16_t* const pairs = val ? a.c.v_sb : a.c.k_sb;
+    const unsigned char* const raw = v_s + ST * P::kTile + (val ? P::kRaw : 0) + (warp & 3) * (P::kRaw / 4);
+    const uint32_t raw_u = tc_smem(raw);
     int st = 0;
     uint32_t par = 1;  // the first pass over the ring finds it free
-    PrWalk fw = wk;
+    PrWalk<D> fw = wk;
     int ft = fw.i0;
-    auto find = [&]() -> long long {  // the row of this thread's token in the next tile to be loaded, -1: absent
-      if (!fw.live()) return -1;
-      const int tok = fw.un.begin + ft * kPrTok + t;
-      long long row = -1;
-      if (tok < fw.un.sp.held) {
-        int pg, at;
-        if (a.page_shift >= 0) {
-          pg = tok >> a.page_shift;
-          at = tok & (a.c.page_size - 1);
-        } else {
-          pg = tok / a.c.page_size;
-          at = tok - pg * a.c.page_size;
-        }
-        const int page = a.v.pages ? a.v.pages[(long long)fw.un.b * a.v.max_pages + pg] : fw.un.b;
-        if ((unsigned)page < (unsigned)a.c.n_pages) row = (long long)(page * a.c.kv_heads + fw.h) * a.c.page_size + at;
+    int page = -1, place = 0, page_h = 0, left = 0;  // of the lane's own 16 tokens; tokens of the 32 that exist
+    auto find = [&]() {  // false: the share ends
+      page = -1;
+      left = 0;
+      if (!fw.live()) return false;
+      const int tok0 = fw.un.begin + ft * kPrTok + part, tok = tok0 + (lane & 16);
+      page_h = fw.h;
+      left = fw.un.sp.held - tok0;
+      int pg;
+      if (a.page_shift >= 0) {
+        pg = tok >> a.page_shift;
+        place = tok & (a.c.page_size - 1);
+      } else {
+        pg = tok / a.c.page_size;
+        place = tok - pg * a.c.page_size;
       }
+      if (tok < fw.un.sp.held) page = a.v.pages ? a.v.pages[(long long)fw.un.b * a.v.max_pages + pg] : fw.un.b;
       if (++ft == fw.i1) {
-        fw.next(w, units);
+        fw.next(a, w, units);
         ft = fw.i0;
       }
-      return row;
+      return true;
     };
-    // K and V tiles take turns through one copy of the code: `now` is stored while `then` (the other of the
-    // two, half a tile on) is on its way
-    PrRow<D> now, then;
-    long long row = find(), row_next = find();
-    pr_load<D>(now, a.c.k_q, a.c.k_sb, row);
-    pr_load<D>(then, a.c.v_q, a.c.v_sb, row);
-    bool gone = row < 0;
+    uint32_t sb[G], vs[G];  // the token's pairs; a K warp has V's too, for the notes
+    bool gone = true;
+    bool more = find();
 #pragma unroll 1
-    for (long long y = wk.x * 2; y < wk.x1 * 2; ++y) {
-      const bool val = y & 1;
-      const int mt = (int)((y >> 1) & (kMetaTiles - 1));
-      uint32_t bad[G], any = 0;
-      const int e = pr_range<D>(now, bad);
-      const uint32_t gap = __ballot_sync(kFull, gone);
-      pr_wait(val ? &sh.v_free[st] : &sh.k_free[st], par, fail);
+    for (int x = -1;; ++x) {  // tile x is stored, the next one fetched
+      if (x >= 0) {
+        const int mt = x & (kMetaTiles - 1);
+        uint32_t any, bad[G];
+        const int e = pr_range<D>(sb, any, bad);
+        pr_wait(&free_[st], par, fail);
+        if (!val) {  // the notes on both go out with K, for the softmax reads them with the scores
+          uint32_t vany, vbad[G];
+          const int ve = pr_range<D>(vs, vany, vbad), c = part / 32;
+          const uint32_t gap = __ballot_sync(kFull, gone);
+          if (lane == 0) {
+            const uint32_t odd = gap | any | vany | (uint32_t)e | (uint32_t)ve;
+            sh.odd[mt][c] = odd;
+            sh.meta[mt][c] = PrMeta{exp2i(e), ve, gap, any | vany};
+            if (odd) {
+              sh.kbad[mt][c] = any;
 #pragma unroll
-      for (int g = 0; g < G; ++g) any |= bad[g];
-      if (!val) {
-        // the notes on both go out with K, for the softmax reads them with the scores
-        uint32_t vb[G], vany = 0;
-        const int ve = pr_range<D>(then, vb);
-        if (lane == 0) {
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            vany |= vb[g];
-            sh.vbad[mt][warp - 4][g] = vb[g];
+              for (int g = 0; g < G; ++g) sh.vbad[mt][c][g] = vany ? vbad[g] : 0;
+            }
           }
-          sh.kbad[mt][warp - 4] = any;
-          sh.meta[mt][warp - 4] = PrMeta{exp2i(e), ve, gap, any | vany};
-          sh.odd[mt][warp - 4] = gap | any | vany | (uint32_t)e | (uint32_t)ve;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-      }
-      pr_store<D>(now, (val ? v_s : k_s) + st * P::kTile, t, bad, e);
-      tc_fence_proxy();
-      tc_arrive(val ? &sh.v_full[st] : &sh.k_full[st]);
-      now = then;
-      if (!val) {
-        row = row_next;
-        row_next = find();
-        pr_load<D>(then, a.c.k_q, a.c.k_sb, row);
-      } else {
-        gone = row < 0;
-        pr_load<D>(then, a.c.v_q, a.c.v_sb, row);
+        pr_store<D>(raw, sb, tiles + st * P::kTile, part + lane, e);
+        tc_fence_proxy();
+        tc_arrive(&full[st]);
+        __syncwarp();
         if (++st == ST) {
           st = 0;
           par ^= 1;
         }
       }
+      // the next tile on its way, and the page of the one behind
+      if (!more) break;
+      long long row =
+          (unsigned)page < (unsigned)a.c.n_pages ? (long long)(page * a.c.kv_heads + page_h) * a.c.page_size + place : -1;
+      pr_fetch<D>(raw_u, codes, row, lane);
+      row = row < 0 || lane >= left ? -1 : row + (lane & 15);
+      gone = row < 0;
+      pr_pairs<D>(sb, pairs, row);
+      if (!val) pr_pairs<D>(vs, a.c.v_sb, row);
+      more = find();
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // ---------------------------------------------------------------- MMAs, by one warp
     pr_regs<P::kRegRest>();
@@ -985,7 +1066,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           k_par ^= 1;
         }
       };
-      for (; __shfl_sync(kFull, (int)wk.live(), 0); wk.next(w, units)) {
+      for (; __shfl_sync(kFull, (int)wk.live(), 0); wk.next(a, w, units)) {
         const int n = __shfl_sync(kFull, wk.i1 - wk.i0, 0);
         for (int it = -1; it < n; ++it) {  // step it: the product of tile it, the scores of tile it + 1
           if (NQ == 2) {
