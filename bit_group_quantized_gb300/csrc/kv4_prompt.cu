@@ -42,7 +42,7 @@ constexpr int kPrThreads = 640;  // warp 0: MMAs, 4-7: K's dequantisation, 8-11:
 constexpr int kPrRegs = 96;      // of a thread at launch: 65536 / 640, in eights
 constexpr int kPrTok = 128;      // tokens of a tile
 constexpr long long kPrTimeoutNs = 1000000000ll;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 constexpr int kPlanSeqs = 4096;
 // What bringing a unit's queries and writing its rows costs, in tiles: CTAs with many short units take fewer tiles.
 constexpr int kUnitCost = 3;
@@ -122,23 +122,26 @@ static PrWs carve_prompt(void* ws, int batch, int rows, int group, int d, int gr
 // ---------------------------------------------------------------------------
 // The list: one CTA; row tiles per sequence, then tiles per unit.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ long long plan_scan(long long v, long long* warp_sum, long long& total) {  // inclusive
+__device__ __forceinline__ long long plan_scan(long long v, long long* warp_sum, long long& total) {  // exclusive
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long own = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long u = __shfl_up_sync(kFull, v, o);
     if (lane >= o) v += u;
   }
-  __syncthreads();
   if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
   long long before = 0;
   total = 0;
+#pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
+    const long long n = warp_sum[w];
+    if (w < warp) before += n;
+    total += n;
   }
-  return v + before;
+  __syncthreads();
+  return v + before - own;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_constant__ AttnArgs a, PrWs w, int rows_unit) {
@@ -146,19 +149,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
   __shared__ long long warp_sum[kPlanThreads / 32];
   pdl_wait();
   pdl_trigger();
-  constexpr int per = kPlanSeqs / kPlanThreads;
-  int n[per], own = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    n[i] = b < a.v.batch ? pr_row_tiles(a, kv4_span(a.v, b), rows_unit) : 0;
-    own += n[i];
+  const int per = (a.v.batch + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min((int)threadIdx.x * per, a.v.batch), b1 = min(b0 + per, a.v.batch);
+  int own = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = pr_row_tiles(a, kv4_span(a.v, b), rows_unit);
+    first[b] = own;  // so far within the thread's sequences
+    own += n;
   }
   long long total;
-  int at = (int)(plan_scan(own, warp_sum, total) - own);
-  for (int i = 0; i < per; ++i) {
-    first[threadIdx.x * per + i] = at;
-    at += n[i];
-  }
+  const int at = (int)plan_scan(own, warp_sum, total);
+  for (int b = b0; b < b1; ++b) first[b] += at;
   const int units = (int)min(total, (long long)w.cap);  // never more, unless the rows of sequences overlap
   __syncthreads();
   long long sum = 0;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
     }
     long long chunk;
     const int cost = u < units ? un.tiles + kUnitCost : 0;
-    const long long pre = plan_scan(cost, warp_sum, chunk) - cost;
+    const long long pre = plan_scan(cost, warp_sum, chunk);
     if (u < units) {
       w.units[u] = un;
       w.prefix[u] = sum + pre;
@@ -365,6 +366,8 @@ struct PrShared {
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
   uint32_t tmem;
   int fail, last[NQ];
+  float log2_sum[NQ][128];  // of the rows of a unit being joined
+  int row[NQ][128];
 };
 
 // A CTA's share of the list, unit by unit. A unit takes kUnitCost places of the list, then one for each tile; the
@@ -857,8 +860,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
           } else {
 #pragma unroll
-            for (int x = 0; x < 32; x += 4)
-              *reinterpret_cast<uint4*>(part + ((d + x) / 4 * 128 + r) * 4) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            for (int x = 0; x < 32; x += 8) {
+              *reinterpret_cast<uint4*>(part + ((d + x) / 4 * 128 + r) * 4) = make_uint4(v[x], v[x + 2], v[x + 4], v[x + 6]);
+              *reinterpret_cast<uint4*>(part + ((d + x) / 4 * 128 + 128 + r) * 4) = make_uint4(v[x + 1], v[x + 3], v[x + 5], v[x + 7]);
+            }
           }
         }
         if (whole) {
@@ -879,46 +884,56 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           sh.last[i] = last;
         }
         wg_sync(1 + i);
-        if (sh.last[i] && !dead) {
+        if (sh.last[i]) {
+          // joined by the whole warpgroup, 4 columns of a row at a time
           __threadfence();
           auto at = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * NQ + i) * P::kSlot; };
           float top = -INFINITY, ls = 0.f;
-#pragma unroll 1
-          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + 128 * D + r));
-#pragma unroll 1
-          for (int c = c0; c <= c1; ++c) {
-            const float mc = __ldcg(at(c) + 128 * D + r);
-            ls = fmaf(mc == top ? 1.f : pr_ex2(mc - top), __ldcg(at(c) + 128 * D + 128 + r), ls);
+          if (!dead) {
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + 128 * D + r));
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float mc = __ldcg(at(c) + 128 * D + r);
+              ls = fmaf(mc == top ? 1.f : pr_ex2(mc - top), __ldcg(at(c) + 128 * D + 128 + r), ls);
+            }
+            if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
           }
-          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+          sh.log2_sum[i][r] = ls == 0.f ? INFINITY : top + log2f(ls);
+          sh.row[i][r] = ok ? row : -1;
+          wg_sync(1 + i);
+          const int rows = (min(128, min(sp.q_len, a.v.rows) * group - wk.un.rt * P::kRows - i * 128) + 31) & ~31;
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
+          for (int n = r; n < rows * (D / 16); n += 128) {  // a row's 16 columns: four loads of each part at a time
+            const int d16 = n / rows, rr = n - d16 * rows, row_o = sh.row[i][rr];
+            const float t = sh.log2_sum[i][rr];
             float v[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) v[x] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
-              const float* const pp = at(c) + r * 4;
-              const float mc = __ldcg(at(c) + 128 * D + r);
-              const float f = mc == top ? 1.f : pr_ex2(mc - top);
+              const float* const pp = at(c);
+              const float4* const po = reinterpret_cast<const float4*>(pp) + d16 * 512 + rr;
+              float4 p[4];
 #pragma unroll
-              for (int x = 0; x < 16; x += 4) {
-                const float4 p = __ldcg(reinterpret_cast<const float4*>(pp + (d + x) * 128));
-                v[x] = fmaf(f, p.x, v[x]);
-                v[x + 1] = fmaf(f, p.y, v[x + 1]);
-                v[x + 2] = fmaf(f, p.z, v[x + 2]);
-                v[x + 3] = fmaf(f, p.w, v[x + 3]);
+              for (int x = 0; x < 4; ++x) p[x] = __ldcg(po + x * 128);
+              const float f = pr_ex2(__ldcg(pp + 128 * D + rr) - t);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                v[4 * x] = fmaf(f, p[x].x, v[4 * x]);
+                v[4 * x + 1] = fmaf(f, p[x].y, v[4 * x + 1]);
+                v[4 * x + 2] = fmaf(f, p[x].z, v[4 * x + 2]);
+                v[4 * x + 3] = fmaf(f, p[x].w, v[4 * x + 3]);
               }
             }
-            if (ok) {
-#pragma unroll
-              for (int x = 0; x < 16; x += 8) {
-                auto b2 = [&](int p, int q) { return pr_bf2(v[x + p] * inv, v[x + q] * inv); };
-                *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
-              }
+            if (row_o >= 0) {
+              const int h_o = wk.h * group + (wk.un.rt * P::kRows + i * 128 + rr) % group;
+              uint4* const o = reinterpret_cast<uint4*>(a.out + (long long)row_o * a.out_stride + h_o * D + d16 * 16);
+              o[0] = make_uint4(pr_bf2(v[0], v[1]), pr_bf2(v[2], v[3]), pr_bf2(v[4], v[5]), pr_bf2(v[6], v[7]));
+              o[1] = make_uint4(pr_bf2(v[8], v[9]), pr_bf2(v[10], v[11]), pr_bf2(v[12], v[13]), pr_bf2(v[14], v[15]));
             }
           }
-          if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
+          wg_sync(1 + i);  // the rows' sums are free again
         }
       }
       }
