@@ -402,44 +402,58 @@ def _need(ok: bool, what: str):
         raise BGQError(ERR_INVALID_ARG, what)
 
 
-def _on(t, dtype, device, dims: int, what: str):
-    """t is a CUDA tensor of this type, rank and device."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == dims
-          and (device is None or t.device == device), what)
+def _on(t, dtype, index, dims: int, what: str):
+    """t is a tensor of this type and rank on CUDA device `index` (None: any)."""
+    _need(isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dims
+          and (t.is_cuda if index is None else t.get_device() == index), what)
 
 
-def _heads(t, heads, d: int, device, what: str):
-    """t is bf16 [tokens][heads][d] whose heads lie one behind the other."""
-    _on(t, torch.bfloat16, device, 3, what)
-    _need((heads is None or t.shape[1] == heads) and t.shape[2] == d and t.stride(2) == 1
-          and (t.shape[1] == 1 or t.stride(1) == d), what)
+def _heads(t, rows, heads, d: int, index, what: str):
+    """t is bf16 [rows][heads][d] on CUDA device `index` (None: any), its heads one behind the other; rows and heads are
+    free where None. Returns its rows, heads and the values between rows (of a single row, whose stride torch
+    leaves open, its width)."""
+    _need(isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3
+          and (t.is_cuda if index is None else t.get_device() == index), what)
+    R, H, D = t.shape
+    sr, sh, sd = t.stride()
+    if D != d or sd != 1 or (sh != d and H != 1) or (rows is not None and R != rows) or (heads is not None and H != heads):
+        raise BGQError(ERR_INVALID_ARG, what)
+    return R, H, sr if R > 1 else max(H * d, 8)
 
 
-def _row_stride(t) -> int:
-    """Values between rows; of a single row, whose stride torch leaves open, its width."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 8)
+def _raw_stream(index: int, stream) -> int:
+    """The stream to run on: the given one, else the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-class _Launch:
-    """The device of a call's tensors made current, and the stream to run on:
-    the given one, else the device's current one. Buffers that the binding
-    creates belong to that stream."""
+class _Here:
+    """Makes the call's device current, and the given stream, to which the buffers that the binding creates then belong."""
 
-    def __init__(self, device, stream):
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        else:
-            self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self.device, self.stream = device, stream
+    def __init__(self, index, stream):
+        self.guard = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+        return self.guard.__enter__()
 
     def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+        return self.guard.__exit__(*e)
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *e):
+        return None
+
+
+_NOTHING = _Nothing()
+
+
+def _here(index: int, stream):
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return _NOTHING
+    return _Here(index, stream)
 
 
 class RopePlan:
@@ -461,24 +475,20 @@ def bgq_rope(plan: RopePlan, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor
     """bgq_rope: x bf16 [tokens][heads][head_dim] (tokens may lie further
     apart), pos int32 [n_axes][tokens] ([tokens] for one axis) -> y (x itself
     is allowed). inverse: the gradient's direction."""
-    lib = load()
-    _heads(x, None, plan.head_dim, None, "bgq_rope: x must be a CUDA bf16 tensor [tokens][heads][head_dim]")
-    T, H, d = x.shape
-    p2 = pos.unsqueeze(0) if isinstance(pos, torch.Tensor) and pos.dim() == 1 else pos
-    _on(p2, torch.int32, x.device, 2, "bgq_rope: pos must be an int32 tensor [n_axes][tokens] on x's device")
-    _need(p2.shape == (plan.n_axes, T) and (T < 2 or p2.stride(1) == 1),
+    T, H, sx = _heads(x, None, None, plan.head_dim, None, "bgq_rope: x must be a CUDA bf16 tensor [tokens][heads][head_dim]")
+    dev = x.get_device()
+    _need(isinstance(pos, torch.Tensor) and pos.dtype is torch.int32 and pos.get_device() == dev,
+          "bgq_rope: pos must be an int32 tensor [n_axes][tokens] on x's device")
+    ps, pt = tuple(pos.shape), pos.stride()
+    _need((ps == (plan.n_axes, T) or (plan.n_axes == 1 and ps == (T,))) and (T < 2 or pt[-1] == 1),
           "bgq_rope: pos must be [n_axes][tokens] with its tokens one behind the other")
-    with _Launch(x.device, stream) as st:
+    with _here(dev, stream):
         if y is None:
-            y = alloc((T, H, d), torch.bfloat16, x.device)
-        else:
-            _heads(y, H, d, x.device, "bgq_rope: y must be a bf16 tensor like x")
-            _need(y.shape[0] == T, "bgq_rope: y must be a bf16 tensor like x")
-        if T == 0 or H == 0:
-            return y
-        _check(lib.bgq_rope(plan.ref, x.data_ptr(), _row_stride(x), p2.data_ptr(),
-                            p2.stride(0) if plan.n_axes > 1 else T, T, H, y.data_ptr(), _row_stride(y), inverse,
-                            st), "bgq_rope")
+            y = alloc((T, H, plan.head_dim), torch.bfloat16, x.device)
+        sy = _heads(y, T, H, plan.head_dim, dev, "bgq_rope: y must be a bf16 tensor like x")[2]
+        if T and H:
+            _check(load().bgq_rope(plan.ref, x.data_ptr(), sx, pos.data_ptr(), pt[0] if plan.n_axes > 1 else T, T, H,
+                                   y.data_ptr(), sy, inverse, _raw_stream(dev, stream)), "bgq_rope")
     return y
 
 
@@ -487,9 +497,10 @@ class KV4Cache:
     bf16 [n_pages][kv_heads][page_size][head_dim/64][2], all contiguous."""
 
     def __init__(self, k_q: torch.Tensor, k_sb: torch.Tensor, v_q: torch.Tensor, v_sb: torch.Tensor):
+        self.index = k_q.get_device()
         for q, sb in ((k_q, k_sb), (v_q, v_sb)):
-            _on(q, torch.int32, k_q.device, 4, "KV4Cache: codes must be CUDA int32 tensors of rank 4")
-            _on(sb, torch.bfloat16, k_q.device, 5, "KV4Cache: scales must be bf16 tensors of rank 5 beside the codes")
+            _on(q, torch.int32, self.index if k_q.is_cuda else None, 4, "KV4Cache: codes must be CUDA int32 tensors of rank 4")
+            _on(sb, torch.bfloat16, self.index, 5, "KV4Cache: scales must be bf16 tensors of rank 5 beside the codes")
             _need(q.shape == k_q.shape and tuple(sb.shape) == (*q.shape[:3], q.shape[3] * 8 // GROUP, 2)
                   and q.is_contiguous() and sb.is_contiguous(),
                   "KV4Cache: codes [n_pages][kv_heads][page_size][head_dim/8], scales "
@@ -518,9 +529,8 @@ class KV4Seqs:
 
     def __init__(self, kv_len: torch.Tensor, rows: int | None = None, pages: torch.Tensor | None = None,
                  q_start: torch.Tensor | None = None, max_q: int = 1):
-        dev = kv_len.device
-        _on(kv_len, torch.int32, dev, 1, "KV4Seqs: kv_len must be a CUDA int32 tensor [batch]")
-        B = kv_len.shape[0]
+        _on(kv_len, torch.int32, None, 1, "KV4Seqs: kv_len must be a CUDA int32 tensor [batch]")
+        B, dev = kv_len.shape[0], kv_len.get_device()
         _need(kv_len.is_contiguous(), "KV4Seqs: kv_len must be contiguous")
         if pages is not None:
             _on(pages, torch.int32, dev, 2, "KV4Seqs: pages must be an int32 tensor [batch][max_pages] beside kv_len")
@@ -529,7 +539,7 @@ class KV4Seqs:
             _on(q_start, torch.int32, dev, 1, "KV4Seqs: q_start must be an int32 tensor [batch+1] beside kv_len")
             _need(q_start.shape[0] == B + 1 and q_start.is_contiguous() and rows is not None,
                   "KV4Seqs: q_start must be [batch+1], contiguous, with rows given")
-        self.kv_len, self.pages, self.q_start, self.device = kv_len, pages, q_start, dev
+        self.kv_len, self.pages, self.q_start, self.index = kv_len, pages, q_start, dev
         self.rows = B if rows is None else rows
         self.c = bgq_kv4_seqs(None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
                               None if pages is None else pages.data_ptr(), B,
@@ -537,37 +547,34 @@ class KV4Seqs:
         self.ref = C.byref(self.c)
 
 
-def _kv_rows(cache, seqs, t, what):
-    _heads(t, cache.kv_heads, cache.head_dim, cache.device, what)
-    _need(t.shape[0] == seqs.rows and seqs.device == cache.device, what)
-
-
 def bgq_kv4_append(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """bgq_kv4_append: k, v bf16 [rows][kv_heads][head_dim] (rows may lie further apart) into the cache."""
-    for t in (k, v):
-        _kv_rows(cache, seqs, t, "bgq_kv4_append: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache")
-    if seqs.rows == 0:
-        return
-    with _Launch(cache.device, stream) as st:
-        _check(load().bgq_kv4_append(cache.ref, seqs.ref, k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
-                                     st), "bgq_kv4_append")
+    dev, rows = cache.index, seqs.rows
+    what = "bgq_kv4_append: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache"
+    sk = _heads(k, rows, cache.kv_heads, cache.head_dim, dev, what)[2]
+    sv = _heads(v, rows, cache.kv_heads, cache.head_dim, dev, what)[2]
+    _need(seqs.index == dev, what)
+    if rows:
+        with _here(dev, stream):
+            _check(load().bgq_kv4_append(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev, stream)),
+                   "bgq_kv4_append")
 
 
 def bgq_kv4_read(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
                  stream=None):
     """bgq_kv4_read: (k, v) bf16 [rows][kv_heads][head_dim] of the rows' tokens."""
-    with _Launch(cache.device, stream) as st:
-        made = []
-        for t in (k, v):
-            if t is None:
-                t = alloc((seqs.rows, cache.kv_heads, cache.head_dim), torch.bfloat16, cache.device)
-            else:
-                _kv_rows(cache, seqs, t, "bgq_kv4_read: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache")
-            made.append(t)
-        k, v = made
-        if seqs.rows:
-            _check(load().bgq_kv4_read(cache.ref, seqs.ref, k.data_ptr(), _row_stride(k), v.data_ptr(),
-                                       _row_stride(v), st), "bgq_kv4_read")
+    dev, rows, H, d = cache.index, seqs.rows, cache.kv_heads, cache.head_dim
+    what = "bgq_kv4_read: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache"
+    _need(seqs.index == dev, what)
+    with _here(dev, stream):
+        if k is None:
+            k = alloc((rows, H, d), torch.bfloat16, cache.device)
+        if v is None:
+            v = alloc((rows, H, d), torch.bfloat16, cache.device)
+        sk, sv = _heads(k, rows, H, d, dev, what)[2], _heads(v, rows, H, d, dev, what)[2]
+        if rows:
+            _check(load().bgq_kv4_read(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev, stream)),
+                   "bgq_kv4_read")
     return k, v
 
 
@@ -581,30 +588,27 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
                       stream=None):
     """bgq_kv4_attention: q bf16 [rows][q_heads][head_dim] -> (out, lse or None). scale defaults to
     head_dim ** -0.5; lse fp32 [rows][q_heads] is written when given or wanted."""
-    lib = load()
-    _heads(q, None, cache.head_dim, cache.device, "bgq_kv4_attention: q must be bf16 [rows][q_heads][head_dim] beside the cache")
-    H = q.shape[1]
-    _need(q.shape[0] == seqs.rows and seqs.device == cache.device, "bgq_kv4_attention: q must have the sequences' rows")
-    with _Launch(cache.device, stream) as st:
+    lib, dev, rows, d = load(), cache.index, seqs.rows, cache.head_dim
+    _, H, sq = _heads(q, rows, None, d, dev, "bgq_kv4_attention: q must be bf16 [rows][q_heads][head_dim] beside the cache")
+    _need(seqs.index == dev, "bgq_kv4_attention: the sequences must be beside the cache")
+    with _here(dev, stream):
         if out is None:
-            out = alloc((seqs.rows, H, cache.head_dim), torch.bfloat16, cache.device)
-        else:
-            _heads(out, H, cache.head_dim, cache.device, "bgq_kv4_attention: out must be a bf16 tensor like q")
-            _need(out.shape[0] == seqs.rows, "bgq_kv4_attention: out must be a bf16 tensor like q")
+            out = alloc((rows, H, d), torch.bfloat16, cache.device)
+        so = _heads(out, rows, H, d, dev, "bgq_kv4_attention: out must be a bf16 tensor like q")[2]
         if lse is None and want_lse:
-            lse = alloc((seqs.rows, H), torch.float32, cache.device)
-        elif lse is not None:
-            _on(lse, torch.float32, cache.device, 2, "bgq_kv4_attention: lse must be fp32 [rows][q_heads]")
-            _need(tuple(lse.shape) == (seqs.rows, H) and lse.is_contiguous(),
+            lse = alloc((rows, H), torch.float32, cache.device)
+        if lse is not None:
+            _on(lse, torch.float32, dev, 2, "bgq_kv4_attention: lse must be fp32 [rows][q_heads]")
+            _need(tuple(lse.shape) == (rows, H) and lse.is_contiguous(),
                   "bgq_kv4_attention: lse must be fp32 [rows][q_heads], contiguous")
-        if seqs.rows == 0:
+        if rows == 0:
             return out, lse
         if ws is None:
             ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
-        _check(lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), _row_stride(q), H,
-                                     cache.head_dim ** -0.5 if scale is None else scale, causal, window,
-                                     out.data_ptr(), _row_stride(out), None if lse is None else lse.data_ptr(),
-                                     ws.data_ptr(), ws.numel() * ws.element_size(), st), "bgq_kv4_attention")
+        _need(ws.get_device() == dev, "bgq_kv4_attention: ws must be beside the cache")
+        _check(lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), sq, H, d ** -0.5 if scale is None else scale, causal,
+                                     window, out.data_ptr(), so, None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), _raw_stream(dev, stream)), "bgq_kv4_attention")
     return out, lse
 
 
