@@ -27,7 +27,8 @@ int check_cache(const bgq_kv4_cache* c) {
   if (!al(c->k_q, 16) || !al(c->k_sb, 16) || !al(c->v_q, 16) || !al(c->v_sb, 16)) return BGQ_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->page_size < 16 || c->page_size % 16 || c->kv_heads < 1) return BGQ_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return BGQ_ERR_UNSUPPORTED;
-  if (c->kv_heads > kMaxHeads || (int64_t)c->n_pages * c->kv_heads > INT32_MAX) return BGQ_ERR_UNSUPPORTED;
+  // kernels count a pool's heads, and 16-token blocks of them, in 32 bits
+  if (c->kv_heads > kMaxHeads || (int64_t)c->n_pages * c->kv_heads > INT32_MAX / (c->page_size / 16)) return BGQ_ERR_UNSUPPORTED;
   return BGQ_OK;
 }
 

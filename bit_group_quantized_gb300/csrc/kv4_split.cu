@@ -38,6 +38,8 @@ constexpr int kSplitWarps = 8;
 constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then the arrival counters
 constexpr int kSplitMaxGrid = (kSplitHead - 256) / 4;
+// What a unit costs beside its tiles (its queries, the joining of the warps), in tiles.
+constexpr int kSplitUnitCost = 6;
 
 template <int D, int NT>
 struct Split {
@@ -56,6 +58,8 @@ struct Split {
   static constexpr int kQBytes = kQs ? NT * G * 4 * 32 * 8 : 0;
   static constexpr int kSmem = kSplitWarps * ST * kStage + kSplitWarps * C * RS * 4 + kQBytes;
   static constexpr int kCtas = D == 256 && NT == 2 ? 1 : 2;  // per SM
+  // the joining of CTAs keeps a weight for every part and column, and a column group for every thread
+  static_assert((kSplitWarps * C * RS) >= 304 / (3 - kCtas) * C + 4 + kSplitThreads * 4, "join area too small");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -72,6 +76,33 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with an accumulator that starts from (c0, c1) in both rows.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// Four 8x8 matrices of 16-bit units from shared memory, a row address a lane; TRANS: transposed.
+template <bool TRANS>
+__device__ __forceinline__ void ldmat4(uint32_t (&r)[4], uint32_t addr) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// Where 16-byte piece ch of token t (of 16) stands in a tile's codes: eight tokens' pieces lie in different banks.
+template <int D>
+__device__ __forceinline__ int split_at(int t, int ch) {
+  if (D == 64) return (t >> 2) * 128 + (t & 3) * 32 + ((ch ^ (t >> 2)) & 1) * 16;
+  if (D == 128) return (t >> 1) * 128 + (t & 1) * 64 + ((ch ^ (t >> 1)) & 3) * 16;
+  return t * 128 + ((ch ^ t) & 7) * 16;
 }
 __device__ __forceinline__ uint32_t movm(uint32_t a) {  // transpose of an 8x8 fp16 matrix held by a warp
   uint32_t d;
@@ -103,42 +134,38 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
   return d;
 }
 
-// A sequence's part of the tile list.
+// A sequence's units and their tiles.
 struct SeqTiles {
   Span sp;
-  int begin;  // first token of its first tile
-  int tiles;  // of one unit (at least one, so that rows that see no token are written)
+  int begin;   // first token of its first tile
+  int tiles;   // of one unit (at least one, so that rows that see no token are written)
   int rtiles;  // column tiles
-  long long units;
 };
 template <int TT, int C>
 __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int b) {
   SeqTiles s;
   s.sp = kv4_span(a.v, b);
-  const int group = a.q_heads / a.c.kv_heads;
   const int pos0 = s.sp.kv_len - s.sp.q_len;
   s.begin = a.window > 0 ? max(0, pos0 - a.window + 1) / TT * TT : 0;
   s.tiles = max(1, (s.sp.held - s.begin + TT - 1) / TT);
-  const long long cols = (long long)s.sp.q_len * group;
-  s.rtiles = (int)((cols + C - 1) / C);
-  s.units = (long long)s.rtiles * a.c.kv_heads;
+  s.rtiles = (min(s.sp.q_len, a.v.rows) * (a.q_heads / a.c.kv_heads) + C - 1) / C;
   return s;
 }
 
-// One segment: tiles i0..i1-1 of a unit.
+// A CTA's share of the list, segment by segment (tiles i0 .. i1 - 1 of a unit). A unit takes kSplitUnitCost places, then one
+// for each tile, and the CTA whose share holds a tile's place does the tile; `flat`: every unit takes this
+// many places, which is also a share's length.
+template <int TT, int C>
 struct Walk {
-  int b;
+  long long x, x1;  // the place of the unit's first tile, the share's end
+  int b, h, rt, i0, i1, flat;
   SeqTiles q;
-  int h, rt;  // the unit: key head and column tile
-  int i0, i1;
-  long long x, x1;  // list position of i0, end of the CTA's share
 
-  __device__ __forceinline__ bool live() const { return x < x1; }
-  template <int TT, int C>
+  __device__ __forceinline__ bool live() const { return i1 > i0; }
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    x += i1 - i0;
+    x += flat ? flat : q.tiles + kSplitUnitCost;
+    i0 = i1 = 0;
     if (x >= x1) return;
-    i0 = 0;
     if (++rt >= q.rtiles) {
       rt = 0;
       ++h;
@@ -146,7 +173,7 @@ struct Walk {
     if (h >= a.c.kv_heads) {
       h = 0;
       do q = seq_tiles<TT, C>(a, ++b);
-      while (q.units == 0 && b + 1 < a.v.batch);
+      while (q.rtiles == 0 && b + 1 < a.v.batch);
     }
     i1 = (int)min((long long)q.tiles, x1 - x);
   }
@@ -173,7 +200,7 @@ struct SplitAcc {
 // What follows a tile's scores s; MASKED where some column does not see all of its tokens.
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT>::MT][NT][4], const unsigned char* st,
-                                             int t0, int gaps, int held, int g, int voff0, int voff1) {
+                                             uint32_t st_u, int t0, int gaps, int held, int g) {
   using P = Split<D, NT>;
   constexpr int G = P::G, MT = P::MT;
   bool hid[MT][NT][4];
@@ -303,20 +330,15 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
         }
       }
     }
-    const unsigned char* vc = st + P::kCode + mt * (8 * D);
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
-      const uint32_t w00 = *reinterpret_cast<const uint32_t*>(vc + (voff0 ^ (gr * 32)));
-      const uint32_t w01 = *reinterpret_cast<const uint32_t*>(vc + (voff1 ^ (gr * 32)));
-      const uint32_t w10 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff0 ^ (gr * 32)));
-      const uint32_t w11 = *reinterpret_cast<const uint32_t*>(vc + 4 * D + (voff1 ^ (gr * 32)));
-      uint32_t r[4] = {__byte_perm(w00, w01, 0x5410), __byte_perm(w00, w01, 0x7632), __byte_perm(w10, w11, 0x5410),
-                       __byte_perm(w10, w11, 0x7632)};
-      uint32_t r8[4];
+      // four codes (dims 4g .. 4g + 3, then 32 + those) of tokens 2c and 2c + 1, then 8 + those, side by side
+      uint32_t r[4], r8[4];
+      ldmat4<true>(r, (st_u + P::kCode + mt * (8 * D)) ^ (gr * 32));
 #pragma unroll
       for (int i = 0; i < 4; ++i) r8[i] = r[i] >> 8;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // code - 8 of dims 8g + j (row g) and 8g + 4 + j (row g + 8)
+      for (int j = 0; j < 4; ++j) {  // code - 8 of dims 4g + j (row g) and 32 + 4g + j (row g + 8)
         uint32_t f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -325,7 +347,7 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
                        : hadd2_u(and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u);              // 1024 + q - 1032
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(A.o[n][gr][j], f[0], f[1], f[2], f[3], bf[n][gr][0], bf[n][gr][1]);
+        for (int n = 0; n < NT; ++n) mma16816(A.o[n][gr][j], f[0], f[2], f[1], f[3], bf[n][gr][0], bf[n][gr][1]);
       }
     }
   }
@@ -337,8 +359,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   constexpr int G = P::G, C = P::C, TT = P::TT, MT = P::MT, ST = P::ST, RD = P::RD, RS = P::RS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_m[kSplitWarps][C], s_l[kSplitWarps][C];
-  __shared__ long long s_scan[kSplitWarps + 1], s_base;
-  __shared__ int s_b, s_last, s_gaps[kSplitWarps][ST];
+  __shared__ long long s_scan[kSplitWarps], s_units[kSplitWarps], s_base;
+  __shared__ int s_b, s_last, s_most[kSplitWarps], s_gaps[kSplitWarps][ST];
   unsigned char* const ring = smem + (threadIdx.x >> 5) * (ST * P::kStage);
   float* const area = reinterpret_cast<float*>(smem + kSplitWarps * ST * P::kStage);
   uint2* const qf_s = reinterpret_cast<uint2*>(smem + kSplitWarps * ST * P::kStage + kSplitWarps * C * RS * 4);
@@ -349,38 +371,66 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   // ---- the list: how long it is, and where this CTA's share begins
   const int per = (a.v.batch + kSplitThreads - 1) / kSplitThreads;
   const int b_lo = min((int)threadIdx.x * per, a.v.batch), b_hi = min(b_lo + per, a.v.batch);
-  long long own = 0;
+  long long own = 0, own_units = 0;
+  int most = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const SeqTiles s = seq_tiles<TT, C>(a, b);
-    own += s.units * s.tiles;
+    const long long n = (long long)s.rtiles * a.c.kv_heads;
+    own_units += n;
+    own += n * (s.tiles + kSplitUnitCost);
+    if (n) most = max(most, s.tiles);
   }
-  long long pre = own;
+  most = __reduce_max_sync(kFull, most);
+  long long pre = own, pre_units = own_units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(kFull, pre, o);
-    if (lane >= o) pre += v;
+    const long long v = __shfl_up_sync(kFull, pre, o), vu = __shfl_up_sync(kFull, pre_units, o);
+    if (lane >= o) {
+      pre += v;
+      pre_units += vu;
+    }
   }
-  if (lane == 31) s_scan[warp] = pre;
+  if (lane == 31) {
+    s_scan[warp] = pre;
+    s_units[warp] = pre_units;
+    s_most[warp] = most;
+  }
   __syncthreads();
-  long long total = 0, before = 0;
+  long long total = 0, before = 0, units = 0, before_units = 0;
 #pragma unroll
   for (int w = 0; w < kSplitWarps; ++w) {
-    if (w < warp) before += s_scan[w];
+    if (w < warp) {
+      before += s_scan[w];
+      before_units += s_units[w];
+    }
     total += s_scan[w];
+    units += s_units[w];
+    most = max(most, s_most[w]);
   }
-  pre += before - own;
-  const long long ctas = min((long long)gridDim.x, (total + kSplitWarps - 1) / kSplitWarps);
+  // Few short units: one a CTA, and nothing to join between CTAs. Otherwise equal shares, of at least a tile a warp.
+  Walk<TT, C> wk;
+  long long ctas;
+  if (units <= gridDim.x && most <= 4 * kSplitWarps) {
+    wk.flat = most;
+    total = units * most;
+    ctas = units;
+    pre = (pre_units + before_units - own_units) * most;
+    own = own_units * most;
+  } else {
+    wk.flat = 0;
+    ctas = max(1ll, min((long long)gridDim.x, total / (kSplitWarps + kSplitUnitCost)));
+    pre += before - own;
+  }
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;
-  Walk wk;
-  wk.x = total * cta / ctas;
+  if (cta >= ctas || total == 0) return;
+  const long long x0 = total * cta / ctas;
   wk.x1 = total * (cta + 1) / ctas;
-  if (wk.x >= pre && wk.x < pre + own) {
+  if (x0 >= pre && x0 < pre + own) {
     int b = b_lo;
     for (; b < b_hi; ++b) {
       const SeqTiles s = seq_tiles<TT, C>(a, b);
-      const long long n = s.units * s.tiles;
-      if (wk.x < pre + n) break;
+      const long long n = (long long)s.rtiles * a.c.kv_heads * (wk.flat ? wk.flat : s.tiles + kSplitUnitCost);
+      if (x0 < pre + n) break;
       pre += n;
     }
     s_b = b;
@@ -389,62 +439,74 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   __syncthreads();
   wk.b = s_b;
   wk.q = seq_tiles<TT, C>(a, wk.b);
-  const int unit0 = (int)((wk.x - s_base) / wk.q.tiles);
-  wk.h = unit0 / wk.q.rtiles;
-  wk.rt = unit0 - wk.h * wk.q.rtiles;
-  wk.i0 = (int)((wk.x - s_base) % wk.q.tiles);
-  wk.i1 = (int)min((long long)wk.q.tiles, wk.i0 + wk.x1 - wk.x);
+  {
+    const int cost = wk.flat ? wk.flat : wk.q.tiles + kSplitUnitCost, unit0 = (int)((x0 - s_base) / cost);
+    wk.h = unit0 / wk.q.rtiles;
+    wk.rt = unit0 - wk.h * wk.q.rtiles;
+    wk.x = s_base + (long long)unit0 * cost + (wk.flat ? 0 : kSplitUnitCost);
+    wk.i0 = (int)max(0ll, x0 - wk.x);
+    wk.i1 = (int)min((long long)wk.q.tiles, wk.x1 - wk.x);
+    if (wk.i1 <= wk.i0) wk.next(a);
+  }
 
   const int heads = a.c.kv_heads, group = a.q_heads / heads;
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
+  // the lane's part of 16 tokens' copies
+  const char* const lane_k = reinterpret_cast<const char*>(a.c.k_q) + lane * 16;
+  const char* const lane_v = reinterpret_cast<const char*>(a.c.v_q) + lane * 16;
+  const char* const lane_sb = reinterpret_cast<const char*>(lane < 16 ? a.c.k_sb : a.c.v_sb) + (lane & 15) * 16;
+  const uint32_t lane_dst = split_at<D>(lane / P::CPT, lane % P::CPT);
+  const uint32_t pair_dst = ring_u + 2 * P::kCode + (lane < 16 ? 0 : P::kSb) + (lane & 15) * 16;
 
-  // ---- copies: the warp's next tile of its share into ring slot `slot`
-  Walk fw = wk;
-  int fi = fw.i0 + warp;
+  // ---- copies: the warp's next tile of its share into ring slot `slot`. Lane l looks up the l-th 16 tokens (which lie in one
+  // page) of the warp's next tiles, 32 at a time.
+  Walk<TT, C> fw = wk;
+  int fi = fw.i0 + warp, blk = -1, blk_at = 32;
   auto fetch = [&](int slot) {
     while (fw.live() && fi >= fw.i1) {
-      fw.next<TT, C>(a);
+      fw.next(a);
       fi = fw.i0 + warp;
+      blk_at = 32;
     }
     if (fw.live()) {
-      const int t0 = fw.q.begin + fi * TT;
-      const uint32_t dst = ring_u + slot * P::kStage;
+      if (blk_at == 32) {
+        const int t = fw.q.begin + (fi + lane / MT * kSplitWarps) * TT + lane % MT * 16;
+        blk = -1;
+        if (t < fw.q.sp.held) {
+          int pg, place;  // page of the list, 16 tokens of it
+          if (a.page_shift >= 0) {
+            pg = t >> a.page_shift;
+            place = (t & (a.c.page_size - 1)) >> 4;
+          } else {
+            pg = t / a.c.page_size;
+            place = (t - pg * a.c.page_size) >> 4;
+          }
+          const int page = a.v.pages ? a.v.pages[(long long)fw.b * a.v.max_pages + pg] : fw.b;
+          if ((unsigned)page < (unsigned)a.c.n_pages) blk = (page * heads + fw.h) * (a.c.page_size >> 4) + place;
+        }
+        blk_at = 0;
+      }
+      const uint32_t dst = ring_u + slot * P::kStage + lane_dst;
       int gaps = 0;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {  // 16 tokens lie in one page
-        const int t = t0 + 16 * m;
-        int pg, at_p;  // page of the list, place in it
-        if (a.page_shift >= 0) {
-          pg = t >> a.page_shift;
-          at_p = t & (a.c.page_size - 1);
-        } else {
-          pg = t / a.c.page_size;
-          at_p = t - pg * a.c.page_size;
-        }
-        int page = -1;
-        if (t < fw.q.sp.held) page = a.v.pages ? a.v.pages[(long long)fw.b * a.v.max_pages + pg] : fw.b;
-        const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
+      for (int m = 0; m < MT; ++m) {
+        const int bk = __shfl_sync(kFull, blk, blk_at + m);
+        const bool ok = bk >= 0;
         gaps |= ok ? 0 : 1 << m;
-        const long long row = ok ? (long long)(page * heads + fw.h) * a.c.page_size + at_p : 0;
-        const char* ks = reinterpret_cast<const char*>(a.c.k_q) + row * (D / 2) + lane * 16;
-        const char* vs = reinterpret_cast<const char*>(a.c.v_q) + row * (D / 2) + lane * 16;
+        const long long at = ok ? bk : 0;
+        const char* ks = lane_k + at * (8 * D);
+        const char* vs = lane_v + at * (8 * D);
 #pragma unroll
-        for (int i = 0; i < P::CPT / 2; ++i) {  // 16 tokens are 16 * CPT chunks
-          const int id = i * 32 + lane, tok = id / P::CPT, ch = id % P::CPT;
-          int at;
-          if (D == 64) at = (tok >> 2) * 128 + (((tok & 3) ^ ((tok >> 2) & 1)) * 32) + ch * 16;
-          else if (D == 128) at = (tok >> 1) * 128 + ((((tok & 1) * 2 + (ch >> 1)) ^ ((tok >> 1) & 3)) * 32) + (ch & 1) * 16;
-          else at = tok * 128 + (((ch >> 1) ^ (tok & 3) ^ ((tok >> 2) & 1)) * 32) + (ch & 1) * 16;
-          cp16(dst + m * (8 * D) + at, ks + i * 512, ok);
-          cp16(dst + P::kCode + m * (8 * D) + at, vs + i * 512, ok);
+        for (int i = 0; i < P::CPT / 2; ++i) {  // 16 tokens are 16 * CPT pieces
+          // 32 pieces are whole periods of the swizzle, or (head dim 256) half of one, which flips its third bit
+          const uint32_t to = (D == 256 && (i & 1) ? dst ^ 64 : dst) + m * (8 * D) + i * 512;
+          cp16(to, ks + i * 512, ok);
+          cp16(to + P::kCode, vs + i * 512, ok);
         }
         // pairs: D bytes per 16 tokens, K by the low lanes, V by the high ones
-        constexpr int n = D / 16;
-        if ((lane & 15) < n) {
-          const char* src = reinterpret_cast<const char*>(lane < 16 ? a.c.k_sb : a.c.v_sb) + row * (D / 16) + (lane & 15) * 16;
-          cp16(dst + 2 * P::kCode + (lane < 16 ? 0 : P::kSb) + m * D + (lane & 15) * 16, src, ok);
-        }
+        if ((lane & 15) < D / 16) cp16(pair_dst + slot * P::kStage + m * D, lane_sb + at * D, ok);
       }
+      blk_at += MT;
       if (lane == 0) s_gaps[warp][slot] = gaps;
       fi += kSplitWarps;
     }
@@ -454,32 +516,17 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   for (int i = 0; i < ST; ++i) fetch(i);
   int slot = 0;
 
-  // lane's place in a tile's codes: K row g, V tokens 2c and 2c+1
-  int koff, voff0, voff1;
-  if (D == 64) {
-    koff = (g >> 2) * 128 + (((g & 3) ^ (g >> 2)) * 32) + c * 8;
-    const int t0 = 2 * c, t1 = 2 * c + 1;
-    voff0 = (t0 >> 2) * 128 + (((t0 & 3) ^ (t0 >> 2)) * 32) + g * 4;
-    voff1 = (t1 >> 2) * 128 + (((t1 & 3) ^ (t1 >> 2)) * 32) + g * 4;
-  } else if (D == 128) {
-    koff = (g >> 1) * 128 + ((((g & 1) * 2) ^ (g >> 1)) * 32) + c * 8;
-    voff0 = c * 128 + (c * 32) + g * 4;
-    voff1 = c * 128 + ((2 ^ c) * 32) + g * 4;
-  } else {
-    koff = g * 128 + (((g & 3) ^ (g >> 2)) * 32) + c * 8;
-    const int t0 = 2 * c, t1 = 2 * c + 1;
-    voff0 = t0 * 128 + (((t0 & 3) ^ (t0 >> 2)) * 32) + g * 4;
-    voff1 = t1 * 128 + (((t1 & 3) ^ (t1 >> 2)) * 32) + g * 4;
-  }
+  // the row address that the lane gives ldmatrix: token lane % 16, piece lane / 16 of a group
+  const uint32_t mat_at = split_at<D>(lane & 15, lane >> 4);
 
-  for (; wk.live(); wk.template next<TT, C>(a)) {
+  for (; wk.live(); wk.next(a)) {
     const int h = wk.h, col0 = wk.rt * C;
     const int ncol = min(C, wk.q.sp.q_len * group - col0);
     const int pos0 = wk.q.sp.kv_len - wk.q.sp.q_len;
 
     // ---- the query: fp16 fragments of column g, scaled by a power of two
     uint32_t qf[P::kQs ? 1 : NT * G * 8];
-    float xs[NT][2][G];             // group sums of columns 2c, 2c + 1
+    float xn[NT][2][G];             // of columns 2c, 2c + 1: -64 times the group's sum of x
     SplitAcc<D, NT> A;
     if (P::kQs) __syncthreads();    // the last segment's fragments are read
 #pragma unroll
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       const int j = (col0 + col) / group, hh = (col0 + col) - j * group;
       const int row = wk.q.sp.first + j;
       const bool ok = col < ncol && row >= 0 && row < a.v.rows;
-      const uint16_t* src = a.q + (long long)(ok ? row : 0) * a.q_stride + (h * group + hh) * D + c * 16;
+      const uint16_t* src = a.q + (long long)(ok ? row : 0) * a.q_stride + (h * group + hh) * D + c * 8;
       uint32_t raw[G][8];
       float top = 0.f;
 #pragma unroll
@@ -496,7 +543,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (ok) v = *reinterpret_cast<const uint4*>(src + gr * 64 + i * 8);
+          if (ok) v = *reinterpret_cast<const uint4*>(src + gr * 64 + i * 32);
           raw[gr][i * 4] = v.x; raw[gr][i * 4 + 1] = v.y; raw[gr][i * 4 + 2] = v.z; raw[gr][i * 4 + 3] = v.w;
         }
 #pragma unroll
@@ -512,7 +559,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       for (int gr = 0; gr < G; ++gr) {
         sum[gr] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {  // word w of the lane: dims 16c + 8w + 0..7; pair i is dims (i, i + 4)
+        for (int w = 0; w < 2; ++w) {  // word w of the lane: dims 32w + 8c + 0..7; pair i is dims (i, i + 4)
           const uint32_t* r = raw[gr] + w * 4;
           uint32_t f[4];
 #pragma unroll
@@ -540,7 +587,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       for (int k = 0; k < 2; ++k) {
         const int from = (2 * c + k) * 4;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) xs[n][k][gr] = __shfl_sync(kFull, sum[gr], from);
+        for (int gr = 0; gr < G; ++gr) xn[n][k][gr] = -64.f * __shfl_sync(kFull, sum[gr], from);
         // at least the smallest normal number, so that -infinity times it stays -infinity
         A.cs[n][k] = fmaxf(fabsf(a.scale) * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from)), 0x1p-126f);
         const int cc = n * 8 + 2 * c + k, jj = (col0 + cc) / group;
@@ -586,6 +633,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       cp_wait<ST - 1>();
       __syncwarp();
       const unsigned char* st = ring + slot * P::kStage;
+      const uint32_t st_u = ring_u + slot * P::kStage + mat_at;
       const int t0 = wk.q.begin + it * TT;
       const int gaps = s_gaps[warp][slot];
       const bool masked = gaps || t0 < all_lo || t0 + TT > all_hi;
@@ -594,24 +642,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       float s[MT][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const unsigned char* kc = st + mt * (8 * D);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][n][i] = 0.f;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          const uint2 w0 = *reinterpret_cast<const uint2*>(kc + (koff ^ (gr * 32)));
-          const uint2 w1 = *reinterpret_cast<const uint2*>(kc + 4 * D + (koff ^ (gr * 32)));
+          uint32_t w[4];  // word c of tokens g and g + 8, then word 4 + c
+          ldmat4<false>(w, (st_u + mt * (8 * D)) ^ (gr * 32));
           float acc[NT][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[n][0] = acc[n][2] = -64.f * xs[n][0][gr];
-            acc[n][1] = acc[n][3] = -64.f * xs[n][1][gr];
-          }
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t r0 = w ? w0.y : w0.x, r1 = w ? w1.y : w1.x;
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t r0 = w[2 * k], r1 = w[2 * k + 1];
             uint32_t f0[4], f1[4];  // 64 + code, pairs (i, i + 4)
             f0[0] = and_or(r0 << 4, 0x00F000F0u, 0x54005400u);
             f1[0] = and_or(r1 << 4, 0x00F000F0u, 0x54005400u);
@@ -625,7 +663,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const int step = (n * G + gr) * 4 + w * 2 + i;
+                const int step = (n * G + gr) * 4 + k * 2 + i;
                 uint32_t b0, b1;
                 if (P::kQs) {
                   const uint2 q2 = qf_s[step * 32 + lane];
@@ -635,7 +673,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
                   b0 = qf[step * 2];
                   b1 = qf[step * 2 + 1];
                 }
-                mma16816(acc[n], f0[2 * i], f1[2 * i], f0[2 * i + 1], f1[2 * i + 1], b0, b1);
+                if (k + i == 0) mma16816_from(acc[n], f0[0], f1[0], f0[1], f1[1], b0, b1, xn[n][0][gr], xn[n][1][gr]);
+                else mma16816(acc[n], f0[2 * i], f1[2 * i], f0[2 * i + 1], f1[2 * i + 1], b0, b1);
               }
             }
           }
@@ -643,15 +682,25 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
           const uint32_t p0 = kp[g * G + gr], p1 = kp[(g + 8) * G + gr];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], fmaf(bf16hi(p0), xs[n][0][gr], s[mt][n][0]));
-            s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], fmaf(bf16hi(p0), xs[n][1][gr], s[mt][n][1]));
-            s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], fmaf(bf16hi(p1), xs[n][0][gr], s[mt][n][2]));
-            s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], fmaf(bf16hi(p1), xs[n][1][gr], s[mt][n][3]));
+            // bias * sum(x): sum(x) is -1/64 of what the accumulator started from
+            const float b0 = bf16hi(p0) * -0x1p-6f, b1 = bf16hi(p1) * -0x1p-6f;
+            const float x0 = xn[n][0][gr], x1 = xn[n][1][gr];
+            if (gr == 0) {
+              s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], b0 * x0);
+              s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], b0 * x1);
+              s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], b1 * x0);
+              s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], b1 * x1);
+            } else {
+              s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], fmaf(b0, x0, s[mt][n][0]));
+              s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], fmaf(b0, x1, s[mt][n][1]));
+              s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], fmaf(b1, x0, s[mt][n][2]));
+              s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], fmaf(b1, x1, s[mt][n][3]));
+            }
           }
         }
       }
-      if (masked) split_finish<D, NT, true>(A, s, st, t0, gaps, wk.q.sp.held, g, voff0, voff1);
-      else split_finish<D, NT, false>(A, s, st, t0, gaps, wk.q.sp.held, g, voff0, voff1);
+      if (masked) split_finish<D, NT, true>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g);
+      else split_finish<D, NT, false>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g);
       __syncwarp();
       fetch(slot);
       slot = slot + 1 == ST ? 0 : slot + 1;
@@ -693,7 +742,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int gr = d0 / 64; gr < (d0 + RD) / 64; ++gr) {
-            float* dst = area + (warp * C + n * 8 + 2 * c + k) * RS + (gr - d0 / 64) * 64 + g * 8;
+            float* dst = area + (warp * C + n * 8 + 2 * c + k) * RS + (gr - d0 / 64) * 64 + g * 4;
             float v[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -701,7 +750,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
               v[4 + j] = fmaf(A.o[n][gr][j][2 + k], A.unit, A.bias[n][k][gr]) * f[n][k];
             }
             *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float4*>(dst + 32) = make_float4(v[4], v[5], v[6], v[7]);
           }
       __syncthreads();
       for (int i = threadIdx.x; i < ncol * (RD / 4); i += kSplitThreads) {
@@ -745,7 +794,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       }
     }
     if (!whole) {  // the last CTA to arrive joins the unit's parts
-      const long long u0 = wk.x - wk.i0, u1 = u0 + wk.q.tiles - 1;  // the unit's first and last tile in the list
+      const long long u0 = wk.x, u1 = u0 + wk.q.tiles - 1;  // the places of the unit's first and last tile
       const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
       __threadfence();
       __syncthreads();
@@ -759,30 +808,58 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
         __threadfence();
         const int np = c1 - c0 + 1;
         auto at = [&](int i) { return ws.part + ((long long)(c0 + i) * 2 + (i == 0)) * (C * (D + 2)); };
-        for (int i = threadIdx.x; i < ncol * (D / 4); i += kSplitThreads) {
-          const int col = i / (D / 4), d4 = i % (D / 4) * 4;
-          float top = -INFINITY;
-          for (int p = 0; p < np; ++p) top = fmaxf(top, __ldcg(at(p) + C * D + col));
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.f;
-#pragma unroll 8
-          for (int p = 0; p < np; ++p) {
-            const float* pp = at(p);
-            const float mp = __ldcg(pp + C * D + col);
-            const float w = mp == top ? 1.f : ex2(mp - top);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + col * D + d4));
-            acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-            sum = fmaf(w, __ldcg(pp + C * D + C + col), sum);
+        // the parts' weights: 2^(m - largest m) / sum, a warp a column
+        float* const wm = area;
+        for (int i = threadIdx.x; i < np * ncol; i += kSplitThreads) wm[i] = __ldcg(at(i / ncol) + C * D + i % ncol);
+        __syncthreads();
+        for (int col = warp; col < ncol; col += kSplitWarps) {
+          float top = -INFINITY, sum = 0.f;
+          for (int p = lane; p < np; p += 32) top = fmaxf(top, wm[p * ncol + col]);
+          top = warp_max(top);
+#pragma unroll 4
+          for (int p = lane; p < np; p += 32) {
+            const float mp = wm[p * ncol + col];
+            sum = fmaf(mp == top ? 1.f : ex2(mp - top), __ldcg(at(p) + C * D + C + col), sum);
+          }
+          sum = warp_sum(sum);
+          const float r = sum == 0.f ? 0.f : 1.f / sum;
+          for (int p = lane; p < np; p += 32) {
+            const float mp = wm[p * ncol + col];
+            wm[p * ncol + col] = (mp == top ? 1.f : ex2(mp - top)) * r;
           }
           const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
-          const float r = sum == 0.f ? 0.f : 1.f / sum;
-          if (row >= 0 && row < a.v.rows) {
-            *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + (h * group + hh) * D + d4) =
-                make_uint2((uint32_t)f2bf(acc.x * r) | (uint32_t)f2bf(acc.y * r) << 16,
-                           (uint32_t)f2bf(acc.z * r) | (uint32_t)f2bf(acc.w * r) << 16);
-            if (a.lse && d4 == 0)
-              a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+          if (a.lse && lane == 0 && row >= 0 && row < a.v.rows)
+            a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+        }
+        __syncthreads();
+        // every thread four columns of a row; with threads to spare, the parts are dealt out over them
+        const int items = ncol * (D / 4), deal = max(1, kSplitThreads / items);
+        float4* const sums = reinterpret_cast<float4*>(area + (np * ncol + 3) / 4 * 4);
+        for (int i0 = 0; i0 < items; i0 += kSplitThreads) {
+          const int i = i0 + (int)threadIdx.x % (items < kSplitThreads ? items : kSplitThreads);
+          const int share = items < kSplitThreads ? threadIdx.x / items : 0;
+          const int col = i / (D / 4), d4 = i % (D / 4) * 4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < items && share < deal) {
+#pragma unroll 8
+            for (int p = share; p < np; p += deal) {
+              const float w = wm[p * ncol + col];
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(at(p) + col * D + d4));
+              acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+              acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
+            }
+            if (deal > 1) sums[share * items + i] = acc;
+          }
+          if (deal > 1) __syncthreads();
+          if (i < items && share == 0) {
+            for (int k = 1; k < deal; ++k) {
+              const float4 v = sums[k * items + i];
+              acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+            }
+            const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
+            if (row >= 0 && row < a.v.rows)
+              *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + (h * group + hh) * D + d4) =
+                  make_uint2((uint32_t)f2bf(acc.x) | (uint32_t)f2bf(acc.y) << 16, (uint32_t)f2bf(acc.z) | (uint32_t)f2bf(acc.w) << 16);
           }
         }
       }
