@@ -54,7 +54,7 @@ struct Split {
   static constexpr int kStage = 2 * kCode + 2 * kSb;
   static constexpr int RD = D * NT >= 256 && NT == 2 ? 64 : (D < 128 ? D : 128);  // dims joined per round
   static constexpr int RS = RD + 4;                // row stride of the join area (floats)
-  static constexpr bool kQs = D * NT > 128;        // query fragments in shared memory
+  static constexpr bool kQs = D * NT > 64;         // query fragments in shared memory
   static constexpr int kQBytes = kQs ? NT * G * 4 * 32 * 8 : 0;
   static constexpr int kSmem = kSplitWarps * ST * kStage + kSplitWarps * C * RS * 4 + kQBytes;
   static constexpr int kCtas = D == 256 && NT == 2 ? 1 : 2;  // per SM
@@ -96,6 +96,18 @@ __device__ __forceinline__ void ldmat4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+// Constants of the code placement, kept in registers: instructions take one constant, and these are the second ones.
+struct SplitK {
+  uint32_t or64, or1024, by16, less72;
+};
+__device__ __forceinline__ SplitK split_constants() {
+  SplitK k;
+  asm volatile("mov.b32 %0, 0x54005400;" : "=r"(k.or64));
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k.or1024));
+  asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(k.by16));
+  asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(k.less72));
+  return k;
 }
 // Where 16-byte piece ch of token t (of 16) stands in a tile's codes: eight tokens' pieces lie in different banks.
 template <int D>
@@ -200,7 +212,7 @@ struct SplitAcc {
 // What follows a tile's scores s; MASKED where some column does not see all of its tokens.
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT>::MT][NT][4], const unsigned char* st,
-                                             uint32_t st_u, int t0, int gaps, int held, int g) {
+                                             uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
   using P = Split<D, NT>;
   constexpr int G = P::G, MT = P::MT;
   bool hid[MT][NT][4];
@@ -343,8 +355,8 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = j & 2 ? r8[i] : r[i];
-          f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u)  // (1024 + 16q)/16 - 72
-                       : hadd2_u(and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u);              // 1024 + q - 1032
+          f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, k_.or1024), k_.by16, k_.less72)  // (1024 + 16q)/16 - 72
+                       : hadd2_u(and_or(w, 0x000F000Fu, k_.or1024), 0xE408E408u);              // 1024 + q - 1032
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma16816(A.o[n][gr][j], f[0], f[2], f[1], f[3], bf[n][gr][0], bf[n][gr][1]);
@@ -516,6 +528,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
   for (int i = 0; i < ST; ++i) fetch(i);
   int slot = 0;
 
+  const SplitK k_ = split_constants();
   // the row address that the lane gives ldmatrix: token lane % 16, piece lane / 16 of a group
   const uint32_t mat_at = split_at<D>(lane & 15, lane >> 4);
 
@@ -641,66 +654,69 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       // ---- scores
       float s[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int gr = 0; gr < G; ++gr) {
+        uint32_t w[MT][4];  // word c of tokens g and g + 8, then word 4 + c
+        float acc[MT][NT][4];
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t w[4];  // word c of tokens g and g + 8, then word 4 + c
-          ldmat4<false>(w, (st_u + mt * (8 * D)) ^ (gr * 32));
-          float acc[NT][4];
+        for (int mt = 0; mt < MT; ++mt) ldmat4<false>(w[mt], (st_u + mt * (8 * D)) ^ (gr * 32));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t r0 = w[2 * k], r1 = w[2 * k + 1];
-            uint32_t f0[4], f1[4];  // 64 + code, pairs (i, i + 4)
-            f0[0] = and_or(r0 << 4, 0x00F000F0u, 0x54005400u);
-            f1[0] = and_or(r1 << 4, 0x00F000F0u, 0x54005400u);
-            f0[1] = and_or(r0, 0x00F000F0u, 0x54005400u);
-            f1[1] = and_or(r1, 0x00F000F0u, 0x54005400u);
-            f0[2] = and_or(r0 >> 4, 0x00F000F0u, 0x54005400u);
-            f1[2] = and_or(r1 >> 4, 0x00F000F0u, 0x54005400u);
-            f0[3] = and_or(r0 >> 8, 0x00F000F0u, 0x54005400u);
-            f1[3] = and_or(r1 >> 8, 0x00F000F0u, 0x54005400u);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t f[MT][4];  // 64 + code, pairs (2i, 2i + 4), (2i + 1, 2i + 5) of both tokens
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint32_t r0 = w[mt][2 * k], r1 = w[mt][2 * k + 1];
+              f[mt][0] = and_or(i ? r0 >> 4 : r0 << 4, 0x00F000F0u, k_.or64);
+              f[mt][1] = and_or(i ? r1 >> 4 : r1 << 4, 0x00F000F0u, k_.or64);
+              f[mt][2] = and_or(i ? r0 >> 8 : r0, 0x00F000F0u, k_.or64);
+              f[mt][3] = and_or(i ? r1 >> 8 : r1, 0x00F000F0u, k_.or64);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+              const int step = (n * G + gr) * 4 + k * 2 + i;
+              uint32_t b0, b1;
+              if (P::kQs) {
+                const uint2 q2 = qf_s[step * 32 + lane];
+                b0 = q2.x;
+                b1 = q2.y;
+              } else {
+                b0 = qf[step * 2];
+                b1 = qf[step * 2 + 1];
+              }
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int step = (n * G + gr) * 4 + k * 2 + i;
-                uint32_t b0, b1;
-                if (P::kQs) {
-                  const uint2 q2 = qf_s[step * 32 + lane];
-                  b0 = q2.x;
-                  b1 = q2.y;
-                } else {
-                  b0 = qf[step * 2];
-                  b1 = qf[step * 2 + 1];
-                }
-                if (k + i == 0) mma16816_from(acc[n], f0[0], f1[0], f0[1], f1[1], b0, b1, xn[n][0][gr], xn[n][1][gr]);
-                else mma16816(acc[n], f0[2 * i], f1[2 * i], f0[2 * i + 1], f1[2 * i + 1], b0, b1);
+              for (int mt = 0; mt < MT; ++mt) {
+                if (k + i == 0) mma16816_from(acc[mt][n], f[mt][0], f[mt][1], f[mt][2], f[mt][3], b0, b1, xn[n][0][gr], xn[n][1][gr]);
+                else mma16816(acc[mt][n], f[mt][0], f[mt][1], f[mt][2], f[mt][3], b0, b1);
               }
             }
           }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
           const uint32_t* kp = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode) + mt * 16 * G;
           const uint32_t p0 = kp[g * G + gr], p1 = kp[(g + 8) * G + gr];
+          // bias * sum(x): sum(x) is -1/64 of what the accumulator started from
+          const float b0 = bf16hi(p0) * -0x1p-6f, b1 = bf16hi(p1) * -0x1p-6f;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            // bias * sum(x): sum(x) is -1/64 of what the accumulator started from
-            const float b0 = bf16hi(p0) * -0x1p-6f, b1 = bf16hi(p1) * -0x1p-6f;
             const float x0 = xn[n][0][gr], x1 = xn[n][1][gr];
             if (gr == 0) {
-              s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], b0 * x0);
-              s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], b0 * x1);
-              s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], b1 * x0);
-              s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], b1 * x1);
+              s[mt][n][0] = fmaf(bf16lo(p0), acc[mt][n][0], b0 * x0);
+              s[mt][n][1] = fmaf(bf16lo(p0), acc[mt][n][1], b0 * x1);
+              s[mt][n][2] = fmaf(bf16lo(p1), acc[mt][n][2], b1 * x0);
+              s[mt][n][3] = fmaf(bf16lo(p1), acc[mt][n][3], b1 * x1);
             } else {
-              s[mt][n][0] = fmaf(bf16lo(p0), acc[n][0], fmaf(b0, x0, s[mt][n][0]));
-              s[mt][n][1] = fmaf(bf16lo(p0), acc[n][1], fmaf(b0, x1, s[mt][n][1]));
-              s[mt][n][2] = fmaf(bf16lo(p1), acc[n][2], fmaf(b1, x0, s[mt][n][2]));
-              s[mt][n][3] = fmaf(bf16lo(p1), acc[n][3], fmaf(b1, x1, s[mt][n][3]));
+              s[mt][n][0] = fmaf(bf16lo(p0), acc[mt][n][0], fmaf(b0, x0, s[mt][n][0]));
+              s[mt][n][1] = fmaf(bf16lo(p0), acc[mt][n][1], fmaf(b0, x1, s[mt][n][1]));
+              s[mt][n][2] = fmaf(bf16lo(p1), acc[mt][n][2], fmaf(b1, x0, s[mt][n][2]));
+              s[mt][n][3] = fmaf(bf16lo(p1), acc[mt][n][3], fmaf(b1, x1, s[mt][n][3]));
             }
           }
         }
       }
-      if (masked) split_finish<D, NT, true>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g);
-      else split_finish<D, NT, false>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g);
+      if (masked) split_finish<D, NT, true>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_);
+      else split_finish<D, NT, false>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_);
       __syncwarp();
       fetch(slot);
       slot = slot + 1 == ST ? 0 : slot + 1;
