@@ -45,8 +45,8 @@ __device__ __forceinline__ int kv4_page(const Kv4View& v, int b, int t) {
   return p >= 0 && p < v.n_pages ? p : -1;
 }
 
-// Where a row's token lives: its slot (page * page_size + place) or -1.
-__device__ __forceinline__ long long kv4_row_slot(const Kv4View& v, int row) {
+// Where a row's token stands in head 0 of its page: its row of the pool's [n_pages][heads][page_size], or -1.
+__device__ __forceinline__ long long kv4_row_at(const Kv4View& v, int row) {
   int b = row;
   if (v.q_start) {  // the last sequence that starts at or before the row
     int lo = 0, hi = v.batch;
@@ -58,11 +58,11 @@ __device__ __forceinline__ long long kv4_row_slot(const Kv4View& v, int row) {
     if (row < v.q_start[b] || row >= v.q_start[b + 1]) return -1;
   }
   if (b >= v.batch) return -1;
-  const int first = v.q_start ? v.q_start[b] : b, end = v.q_start ? v.q_start[b + 1] : b + 1;
+  const int end = v.q_start ? v.q_start[b + 1] : b + 1;
   const long long t = (long long)v.kv_len[b] - end + row;
-  if (t < 0 || t >= v.cap || row < first) return -1;
+  if (t < 0 || t >= v.cap) return -1;
   const int p = kv4_page(v, b, (int)t);
-  return p < 0 ? -1 : (long long)p * v.page_size + t % v.page_size;
+  return p < 0 ? -1 : (long long)p * v.heads * v.page_size + (int)t % v.page_size;
 }
 
 cudaError_t launch_rope(const bgq_rope_plan& p, const uint16_t* x, long long x_stride, const int32_t* pos,

@@ -70,10 +70,27 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Slots of the block's rows (-1: none), looked up once.
-__device__ __forceinline__ void kv_slots(const Kv4View& v, int r0, int nr, long long* slot) {
-  if ((int)threadIdx.x < nr) slot[threadIdx.x] = kv4_row_slot(v, r0 + threadIdx.x);
+// Where the block's rows' tokens stand in head 0 of their pages (-1: nowhere), looked up once; head h is h pages' heads on.
+__device__ __forceinline__ void kv_rows(const Kv4View& v, int r0, int nr, long long* at) {
+  if ((int)threadIdx.x < nr) at[threadIdx.x] = kv4_row_at(v, r0 + threadIdx.x);
   __syncthreads();
+}
+// Two fp32 values in a register pair: one instruction for both.
+__device__ __forceinline__ uint64_t kv_pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void kv_split(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t kv_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t kv_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant__ bgq_kv4_cache c,
@@ -81,7 +98,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
                                                            const __grid_constant__ KvGeo g,
                                                            const uint16_t* __restrict__ k, long long k_stride,
                                                            const uint16_t* __restrict__ val, long long v_stride) {
-  __shared__ long long slot[kKvMaxRows];
+  __shared__ long long rows[kKvMaxRows];
   pdl_wait();
   pdl_trigger();
   const int r0 = blockIdx.x * g.rb, nr = min(g.rb, v.rows - r0);
@@ -103,7 +120,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
       }
     }
     if (!ready) {
-      kv_slots(v, r0, nr, slot);
+      kv_rows(v, r0, nr, rows);
       ready = true;
     }
 #pragma unroll
@@ -136,6 +153,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
         r = fmaf(r, 0x1p-22f, r);
       }
       constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: whole numbers in the low bits
+      const uint64_t b2 = kv_pair(-b, -b), r2 = kv_pair(r, r), whole2 = kv_pair(kWhole, kWhole);
       uint32_t q[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -143,9 +161,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           const uint32_t x2 = w[h * 4 + j];
-          const uint32_t c1 = __float_as_uint(fmaf(bf16hi(x2) - b, r, kWhole));
-          const uint32_t c0 = __float_as_uint(fmaf(bf16lo(x2) - b, r, kWhole));
-          acc = acc * 256 + (c1 * 16 + c0);
+          float c0, c1;
+          kv_split(kv_fma2(kv_add2(kv_pair(bf16lo(x2), bf16hi(x2)), b2), r2, whole2), c0, c1);
+          acc = acc * 256 + (__float_as_uint(c1) * 16 + __float_as_uint(c0));
         }
         // every code came with the bits of 1.5 * 2^23 in front: their sum over the eight places
         q[h] = acc - 0x4B400000u * 0x11111111u;
@@ -153,10 +171,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
       const uint32_t bad = s16 == 0x7fc0;
       if (u < total) {
         const KvUnit ku = kv_unit(g, u, u0, per);
-        const long long sl = slot[ku.row];
-        if (sl >= 0) {
-          const long long page = sl / c.page_size;
-          const long long row = (page * c.kv_heads + ku.head) * c.page_size + (sl - page * c.page_size);
+        const long long at = rows[ku.row];
+        if (at >= 0) {
+          const long long row = at + ku.head * c.page_size;
           const int gr = ku.lane >> 2, l = ku.lane & 3;
           uint32_t* qd = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
           qd[0] = bad ? 0 : q[0];
@@ -175,7 +192,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
                                                          const __grid_constant__ KvGeo g, uint16_t* __restrict__ k,
                                                          long long k_stride, uint16_t* __restrict__ val,
                                                          long long v_stride) {
-  __shared__ long long slot[kKvMaxRows];
+  __shared__ long long rows[kKvMaxRows];
   __shared__ int held[kKvMaxRows];
   pdl_wait();
   pdl_trigger();
@@ -184,7 +201,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
     const int row = r0 + threadIdx.x;
     held[threadIdx.x] = v.q_start ? row >= v.q_start[0] && row < v.q_start[v.batch] : row < v.batch;
   }
-  kv_slots(v, r0, nr, slot);
+  kv_rows(v, r0, nr, rows);
   const int u0 = blockIdx.y * g.chunk, per = min(u0 + g.chunk, g.units_row) - u0, total = nr * per;
   for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kKvThreads * kKvUnits) {
     uint32_t q[kKvUnits][2], sb[kKvUnits];
@@ -194,10 +211,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
       q[i][0] = q[i][1] = sb[i] = 0;
       if (u < total) {
         const KvUnit ku = kv_unit(g, u, u0, per);
-        const long long sl = slot[ku.row];
-        if (sl >= 0) {
-          const long long page = sl / c.page_size;
-          const long long row = (page * c.kv_heads + ku.head) * c.page_size + (sl - page * c.page_size);
+        const long long at = rows[ku.row];
+        if (at >= 0) {
+          const long long row = at + ku.head * c.page_size;
           const int gr = ku.lane >> 2, l = ku.lane & 3;
           const uint32_t* qs = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
           q[i][0] = qs[0];
@@ -212,21 +228,25 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
       if (u >= total) continue;
       const KvUnit ku = kv_unit(g, u, u0, per);
       if (!held[ku.row]) continue;
+      // A code n places up in a word, put under the exponent of 2^23, is the number 2^23 + code * 16^n (n < 5); the rest of the
+      // word comes down three places first. One subtraction, then one fused multiply-add with the scale / 16^n.
       const float s = bf16lo(sb[i]), b = bf16hi(sb[i]);
+      const float s1 = s * 0x1p-4f, s2 = s * 0x1p-8f, s3 = s * 0x1p-12f, s4 = s * 0x1p-16f;
+      const uint64_t f01 = kv_pair(s, s1), f23 = kv_pair(s2, s3), f42 = kv_pair(s4, s2), f34 = kv_pair(s3, s4);
+      const uint64_t b2 = kv_pair(b, b), less = kv_pair(-8388608.f, -8388608.f);
       uint16_t* dst = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
                       ku.head * c.head_dim + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // code under the exponent of 2^23: the value 2^23 + code
-          const float c0 = __uint_as_float((q[i][h] >> (8 * j) & 15u) | 0x4B000000u) - 8388608.f;
-          const float c1 = __uint_as_float((q[i][h] >> (8 * j + 4) & 15u) | 0x4B000000u) - 8388608.f;
-          const __nv_bfloat162 p2 = __floats2bfloat162_rn(fmaf(c0, s, b), fmaf(c1, s, b));
-          o[j] = *reinterpret_cast<const uint32_t*>(&p2);
-        }
-        *reinterpret_cast<uint4*>(dst + h * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t w = q[i][h], wd = w >> 12;
+        auto two = [&](uint32_t c0, uint32_t c1, uint64_t f) {
+          float v0, v1;
+          kv_split(kv_fma2(kv_add2(kv_pair(__uint_as_float(c0 | 0x4B000000u), __uint_as_float(c1 | 0x4B000000u)), less), f, b2), v0, v1);
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(v0, v1);
+          return *reinterpret_cast<const uint32_t*>(&p2);
+        };
+        *reinterpret_cast<uint4*>(dst + h * 32) = make_uint4(two(w & 0xFu, w & 0xF0u, f01), two(w & 0xF00u, w & 0xF000u, f23),
+                                                             two(w & 0xF0000u, wd & 0xF00u, f42), two(wd & 0xF000u, wd & 0xF0000u, f34));
       }
     }
   }

@@ -39,7 +39,7 @@ constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then the arrival counters
 constexpr int kSplitMaxGrid = (kSplitHead - 256) / 4;
 // What a unit costs beside its tiles (its queries, the joining of the warps), in tiles.
-constexpr int kSplitUnitCost = 6;
+constexpr int kSplitUnitCost = 20;
 
 template <int D, int NT>
 struct Split {

@@ -9,13 +9,15 @@
 // Bound by memory (2 bytes in, 2 bytes out per value). A block takes whole
 // tokens: its first loads are in flight while it computes the angles of its
 // tokens once, for all heads, into shared memory.
+#include <algorithm>
+
 #include "attn.h"
 #include "common.cuh"
 #include "kernels.h"
 
 namespace bgq {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxThreads = 512;
 constexpr int kRopeLoads = 4;       // units a thread has in flight
 constexpr int kRopeMaxTokens = 16;  // tokens of a block
 
@@ -30,7 +32,7 @@ struct RopeGeo {
 // HALF: pair i is columns (i, i + rot/2): a unit is 8 pairs, two 16-byte chunks.
 // Otherwise pair i is columns (2i, 2i+1): a unit is one 16-byte chunk, 4 pairs.
 template <bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ bgq_rope_plan p,
+__global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant__ bgq_rope_plan p,
                                                        const __grid_constant__ RopeGeo g, const uint16_t* x, long long x_stride,
                                                        const int32_t* __restrict__ pos,
                                                        long long pos_stride, int tokens, uint16_t* y,
@@ -52,11 +54,12 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ b
     col = head * p.head_dim + (unit < turn_units ? unit * 8 : p.rot_dim + (unit - turn_units) * 8);
   };
   bool ready = false;
-  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kRopeThreads * kRopeLoads) {
+  const int T = blockDim.x;
+  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += T * kRopeLoads) {
     uint4 lo[kRopeLoads], hi[kRopeLoads];
 #pragma unroll
     for (int k = 0; k < kRopeLoads; ++k) {
-      const int u = base + k * kRopeThreads;
+      const int u = base + k * T;
       if (u < total) {
         int tok, col, unit;
         place(u, tok, col, unit);
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ b
       }
     }
     if (!ready) {
-      for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+      for (int i = threadIdx.x; i < nt * half; i += T) {
         const int tok = i / half, pr = i - tok * half;
         const long long at = pos[p.axis[pr] * pos_stride + t0 + tok];
         const unsigned long long turn = (unsigned long long)at * p.freq[pr];
@@ -79,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ b
     }
 #pragma unroll
     for (int k = 0; k < kRopeLoads; ++k) {
-      const int u = base + k * kRopeThreads;
+      const int u = base + k * T;
       if (u < total) {
         int tok, col, unit;
         place(u, tok, col, unit);
@@ -124,17 +127,20 @@ cudaError_t launch_rope(const bgq_rope_plan& p, const uint16_t* x, long long x_s
   RopeGeo g;
   g.upt = (pairs ? p.rot_dim : half) / 8 + (p.head_dim - p.rot_dim) / 8;
   g.units_tok = g.upt * heads;
-  // A block takes as many tokens as keep its threads' loads in flight, unless
-  // that leaves SMs without a block; a token of many heads is shared out.
-  const int want = kRopeThreads * kRopeLoads;
+  // A block takes as many tokens as fill its threads' loads (up to 384 threads, which leaves an SM its five blocks), unless
+  // that leaves SMs without a block; a token of many heads is shared out. The threads divide the units evenly: with a
+  // fixed 256 the 320 units of 40 heads of 128 left most of them idle (8191 tokens: 36 us).
+  const int most = 384 * kRopeLoads;
   g.tb = 1;
-  while (g.tb < kRopeMaxTokens && g.tb * 2 * g.units_tok <= want && (long long)tokens >= 4ll * num_sms() * g.tb) g.tb *= 2;
-  g.chunk = g.tb > 1 || g.units_tok <= want ? g.units_tok : want;
+  while (g.tb < kRopeMaxTokens && g.tb * 2 * g.units_tok <= most && (long long)tokens >= 4ll * num_sms() * g.tb) g.tb *= 2;
+  g.chunk = g.tb > 1 || g.units_tok <= most ? g.units_tok : most;
+  const int loads = tokens < num_sms() * 4 ? 1 : kRopeLoads;  // few tokens: more threads, fewer units each
+  const int threads = std::min(kRopeMaxThreads, ((g.tb * g.chunk + loads - 1) / loads + 31) / 32 * 32);
   g.m_upt = (uint32_t)((0x100000000ull + g.upt - 1) / g.upt);
   g.m_tok = (uint32_t)((0x100000000ull + g.units_tok - 1) / g.units_tok);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((tokens + g.tb - 1) / g.tb, (g.units_tok + g.chunk - 1) / g.chunk);
-  cfg.blockDim = dim3(kRopeThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)g.tb * half * sizeof(float2);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
