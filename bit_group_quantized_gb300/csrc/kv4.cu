@@ -18,29 +18,27 @@
 namespace bgq {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvUnits = 2;  // lane-units (16 values) a thread has in flight
-constexpr int kKvMaxRows = 32;
+constexpr int kKvUnits = 2;    // lane-units (16 values) a thread has in flight
+constexpr int kKvRounds = 8;   // of them, in a block: its rows are looked up once, which takes longer than a round
+constexpr int kKvMaxRows = 256;
 
 struct KvGeo {
   int units_row;     // lane-units of a row: K heads, then V heads
   int units_k;       // the K part
-  int units_head;    // lane-units of a head
   int rb;            // rows of a block
-  uint32_t m_row, m_head;  // u / n == umulhi(u, m) for u, n below 2^16
+  uint32_t m_row;    // u / units_row == umulhi(u, m_row) for u, units_row below 2^16
   int chunk;         // lane-units of a row that one block takes
 };
 
 __host__ inline KvGeo kv_geo(int heads, int d, int rows) {
   KvGeo g;
-  g.units_head = d / 16;
-  g.units_k = heads * g.units_head;
+  g.units_k = heads * (d / 16);
   g.units_row = 2 * g.units_k;
   const int want = kKvThreads * kKvUnits;
   g.rb = 1;
-  while (g.rb < kKvMaxRows && g.rb * 2 * g.units_row <= want && (long long)rows >= 4ll * num_sms() * g.rb) g.rb *= 2;
+  while (g.rb < kKvMaxRows && g.rb * 2 * g.units_row <= want * kKvRounds && (long long)rows >= 8ll * num_sms() * g.rb) g.rb *= 2;
   g.chunk = g.rb > 1 || g.units_row <= want ? g.units_row : want;
   g.m_row = (uint32_t)((0x100000000ull + g.units_row - 1) / g.units_row);
-  g.m_head = (uint32_t)((0x100000000ull + g.units_head - 1) / g.units_head);
   return g;
 }
 
@@ -48,14 +46,15 @@ struct KvUnit {  // where a lane-unit's values live
   int row, head, lane;  // row of the block, head, lane-unit inside the head
   bool val;             // V, otherwise K
 };
+template <int D>
 __device__ __forceinline__ KvUnit kv_unit(const KvGeo& g, int u, int u0, int per) {
   KvUnit k;
   k.row = g.rb > 1 ? (int)__umulhi((uint32_t)u, g.m_row) : 0;
   int r = u - k.row * per + u0;
   k.val = r >= g.units_k;
   if (k.val) r -= g.units_k;
-  k.head = (int)__umulhi((uint32_t)r, g.m_head);
-  k.lane = r - k.head * g.units_head;
+  k.head = r / (D / 16);
+  k.lane = r % (D / 16);
   return k;
 }
 
@@ -93,6 +92,7 @@ __device__ __forceinline__ uint64_t kv_fma2(uint64_t a, uint64_t b, uint64_t c) 
   return d;
 }
 
+template <int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant__ bgq_kv4_cache c,
                                                            const __grid_constant__ Kv4View v,
                                                            const __grid_constant__ KvGeo g,
@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
       const int u = base + i * kKvThreads;
       in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
       if (u < total) {
-        const KvUnit ku = kv_unit(g, u, u0, per);
+        const KvUnit ku = kv_unit<D>(g, u, u0, per);
         const uint16_t* src = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
-                              ku.head * c.head_dim + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+                              ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
         in[i][0] = ldg_stream16(src);
         in[i][1] = ldg_stream16(src + 32);
       }
@@ -170,16 +170,16 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
       }
       const uint32_t bad = s16 == 0x7fc0;
       if (u < total) {
-        const KvUnit ku = kv_unit(g, u, u0, per);
+        const KvUnit ku = kv_unit<D>(g, u, u0, per);
         const long long at = rows[ku.row];
         if (at >= 0) {
           const long long row = at + ku.head * c.page_size;
           const int gr = ku.lane >> 2, l = ku.lane & 3;
-          uint32_t* qd = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
+          uint32_t* qd = (ku.val ? c.v_q : c.k_q) + row * (D / 8) + gr * 8 + l;
           qd[0] = bad ? 0 : q[0];
           qd[4] = bad ? 0 : q[1];
           if (l == 0)
-            reinterpret_cast<uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (c.head_dim / kGroup) + gr] =
+            reinterpret_cast<uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (D / kGroup) + gr] =
                 (uint32_t)s16 | (uint32_t)b16 << 16;
         }
       }
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
   }
 }
 
+template <int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__ bgq_kv4_cache c,
                                                          const __grid_constant__ Kv4View v,
                                                          const __grid_constant__ KvGeo g, uint16_t* __restrict__ k,
@@ -210,15 +211,15 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
       const int u = base + i * kKvThreads;
       q[i][0] = q[i][1] = sb[i] = 0;
       if (u < total) {
-        const KvUnit ku = kv_unit(g, u, u0, per);
+        const KvUnit ku = kv_unit<D>(g, u, u0, per);
         const long long at = rows[ku.row];
         if (at >= 0) {
           const long long row = at + ku.head * c.page_size;
           const int gr = ku.lane >> 2, l = ku.lane & 3;
-          const uint32_t* qs = (ku.val ? c.v_q : c.k_q) + row * (c.head_dim / 8) + gr * 8 + l;
+          const uint32_t* qs = (ku.val ? c.v_q : c.k_q) + row * (D / 8) + gr * 8 + l;
           q[i][0] = qs[0];
           q[i][1] = qs[4];
-          sb[i] = reinterpret_cast<const uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (c.head_dim / kGroup) + gr];
+          sb[i] = reinterpret_cast<const uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (D / kGroup) + gr];
         }
       }
     }
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
     for (int i = 0; i < kKvUnits; ++i) {
       const int u = base + i * kKvThreads;
       if (u >= total) continue;
-      const KvUnit ku = kv_unit(g, u, u0, per);
+      const KvUnit ku = kv_unit<D>(g, u, u0, per);
       if (!held[ku.row]) continue;
       // A code n places up in a word, put under the exponent of 2^23, is the number 2^23 + code * 16^n (n < 5); the rest of the
       // word comes down three places first. One subtraction, then one fused multiply-add with the scale / 16^n.
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
       const uint64_t f01 = kv_pair(s, s1), f23 = kv_pair(s2, s3), f42 = kv_pair(s4, s2), f34 = kv_pair(s3, s4);
       const uint64_t b2 = kv_pair(b, b), less = kv_pair(-8388608.f, -8388608.f);
       uint16_t* dst = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
-                      ku.head * c.head_dim + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+                      ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t w = q[i][h], wd = w >> 12;
@@ -269,12 +270,12 @@ static cudaError_t kv_launch(void (*kern)(KArgs...), const KvGeo& g, int rows, c
 cudaError_t launch_kv4_append(const bgq_kv4_cache& c, const Kv4View& v, const uint16_t* k, long long k_stride,
                               const uint16_t* val, long long v_stride, cudaStream_t s) {
   const KvGeo g = kv_geo(c.kv_heads, c.head_dim, v.rows);
-  return kv_launch(k_kv4_append, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
+  return kv_launch(c.head_dim == 64 ? k_kv4_append<64> : c.head_dim == 128 ? k_kv4_append<128> : k_kv4_append<256>, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
 }
 cudaError_t launch_kv4_read(const bgq_kv4_cache& c, const Kv4View& v, uint16_t* k, long long k_stride, uint16_t* val,
                             long long v_stride, cudaStream_t s) {
   const KvGeo g = kv_geo(c.kv_heads, c.head_dim, v.rows);
-  return kv_launch(k_kv4_read, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
+  return kv_launch(c.head_dim == 64 ? k_kv4_read<64> : c.head_dim == 128 ? k_kv4_read<128> : k_kv4_read<256>, g, v.rows, s, c, v, g, k, k_stride, val, v_stride);
 }
 
 }  // namespace bgq

@@ -37,7 +37,10 @@ __global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant_
                                                        const int32_t* __restrict__ pos,
                                                        long long pos_stride, int tokens, uint16_t* y,
                                                        long long y_stride, float sign) {
-  extern __shared__ __align__(16) float2 cs[];  // [tb][rot/2]
+  // cos and sin of two pairs side by side, [tb][pairs of a unit / 2][units of a head]: threads on neighbouring units read
+  // neighbouring 16 bytes
+  extern __shared__ __align__(16) float4 cs[];
+  constexpr int kPair = HALF ? 8 : 4;  // pairs of a unit
   pdl_wait();
   pdl_trigger();
   const int half = p.rot_dim >> 1;
@@ -75,7 +78,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant_
         const unsigned long long turn = (unsigned long long)at * p.freq[pr];
         float s, c;
         sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);  // [-1, 1) half turns
-        cs[i] = make_float2(c, s * sign);
+        const int un = pr / kPair, in = pr % kPair;
+        reinterpret_cast<float2*>(cs + (tok * (kPair / 2) + in / 2) * turn_units + un)[in & 1] = make_float2(c, s * sign);
       }
       __syncthreads();
       ready = true;
@@ -91,10 +95,9 @@ __global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant_
           uint32_t* l = &lo[k].x;
           if (HALF) {
             uint32_t* h = &hi[k].x;
-            const float4* c4 = reinterpret_cast<const float4*>(cs + tok * half + unit * 8);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float4 c = c4[j];
+              const float4 c = cs[(tok * 4 + j) * turn_units + unit];
               const float a0 = bf16lo(l[j]), a1 = bf16hi(l[j]), b0 = bf16lo(h[j]), b1 = bf16hi(h[j]);
               const __nv_bfloat162 lv = __floats2bfloat162_rn(fmaf(a0, c.x, -b0 * c.y), fmaf(a1, c.z, -b1 * c.w));
               const __nv_bfloat162 hv = __floats2bfloat162_rn(fmaf(a0, c.y, b0 * c.x), fmaf(a1, c.w, b1 * c.z));
@@ -103,10 +106,10 @@ __global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant_
             }
             *reinterpret_cast<uint4*>(o + half) = hi[k];
           } else {
-            const float2* c2 = cs + tok * half + unit * 4;
+            const float4 c4[2] = {cs[tok * 2 * turn_units + unit], cs[(tok * 2 + 1) * turn_units + unit]};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 c = c2[j];
+              const float2 c = j & 1 ? make_float2(c4[j >> 1].z, c4[j >> 1].w) : make_float2(c4[j >> 1].x, c4[j >> 1].y);
               const float a = bf16lo(l[j]), b = bf16hi(l[j]);
               const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, c.x, -b * c.y), fmaf(a, c.y, b * c.x));
               l[j] = *reinterpret_cast<const uint32_t*>(&v);
