@@ -18,41 +18,37 @@
 namespace bgq {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvUnits = 2;    // lane-units (16 values) a thread has in flight
-constexpr int kKvRounds = 8;   // of them, in a block: its rows are looked up once, which takes longer than a round
+// A thread's unit is 16 values of a token's head, of K and of V; a block looks its rows' places up once and takes this many rounds of
+// units (18003 rows of 8 heads of 128 written and read back: 1 round 33.6 us, 2 32.1, 4 34.1, the blocks then being few; a read of
+// 74000 tokens of 2 heads of 256: 40.8, 36.2, 35.9).
+constexpr int kKvRounds = 2;
 constexpr int kKvMaxRows = 256;
 
 struct KvGeo {
-  int units_row;     // lane-units of a row: K heads, then V heads
-  int units_k;       // the K part
-  int rb;            // rows of a block
-  uint32_t m_row;    // u / units_row == umulhi(u, m_row) for u, units_row below 2^16
-  int chunk;         // lane-units of a row that one block takes
+  int units_row;   // units of a row
+  int rb;          // rows of a block
+  uint32_t m_row;  // u / units_row == umulhi(u, m_row) for u, units_row below 2^16
+  int chunk;       // units of a row that one block takes
 };
 
 __host__ inline KvGeo kv_geo(int heads, int d, int rows) {
   KvGeo g;
-  g.units_k = heads * (d / 16);
-  g.units_row = 2 * g.units_k;
-  const int want = kKvThreads * kKvUnits;
+  g.units_row = heads * (d / 16);
   g.rb = 1;
-  while (g.rb < kKvMaxRows && g.rb * 2 * g.units_row <= want * kKvRounds && (long long)rows >= 8ll * num_sms() * g.rb) g.rb *= 2;
-  g.chunk = g.rb > 1 || g.units_row <= want ? g.units_row : want;
+  while (g.rb < kKvMaxRows && g.rb * 2 * g.units_row <= kKvThreads * kKvRounds && (long long)rows >= 8ll * num_sms() * g.rb) g.rb *= 2;
+  g.chunk = g.rb > 1 || g.units_row <= kKvThreads ? g.units_row : kKvThreads;
   g.m_row = (uint32_t)((0x100000000ull + g.units_row - 1) / g.units_row);
   return g;
 }
 
-struct KvUnit {  // where a lane-unit's values live
-  int row, head, lane;  // row of the block, head, lane-unit inside the head
-  bool val;             // V, otherwise K
+struct KvUnit {
+  int row, head, lane;  // row of the block, head, unit inside the head: 16-byte pieces lane % 4 and 4 + lane % 4 of its group
 };
 template <int D>
 __device__ __forceinline__ KvUnit kv_unit(const KvGeo& g, int u, int u0, int per) {
   KvUnit k;
   k.row = g.rb > 1 ? (int)__umulhi((uint32_t)u, g.m_row) : 0;
-  int r = u - k.row * per + u0;
-  k.val = r >= g.units_k;
-  if (k.val) r -= g.units_k;
+  const int r = u - k.row * per + u0;
   k.head = r / (D / 16);
   k.lane = r % (D / 16);
   return k;
@@ -105,27 +101,28 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
   const int u0 = blockIdx.y * g.chunk, per = min(u0 + g.chunk, g.units_row) - u0, total = nr * per;
   bool ready = false;
   // `total` and the strides are multiples of 4, so the four lanes of a group are in or out together
-  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kKvThreads * kKvUnits) {
-    uint4 in[kKvUnits][2];
-#pragma unroll
-    for (int i = 0; i < kKvUnits; ++i) {
-      const int u = base + i * kKvThreads;
-      in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
-      if (u < total) {
-        const KvUnit ku = kv_unit<D>(g, u, u0, per);
-        const uint16_t* src = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
-                              ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
-        in[i][0] = ldg_stream16(src);
-        in[i][1] = ldg_stream16(src + 32);
-      }
+  for (int u = threadIdx.x; u - (int)threadIdx.x < total; u += kKvThreads) {
+    const KvUnit ku = kv_unit<D>(g, u, u0, per);
+    const int col = ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+    uint4 in[2][2];
+    if (u < total) {
+      const uint16_t* ks = k + (long long)(r0 + ku.row) * k_stride + col;
+      const uint16_t* vs = val + (long long)(r0 + ku.row) * v_stride + col;
+      in[0][0] = ldg_stream16(ks);
+      in[0][1] = ldg_stream16(ks + 32);
+      in[1][0] = ldg_stream16(vs);
+      in[1][1] = ldg_stream16(vs + 32);
+    } else {
+      in[0][0] = in[0][1] = in[1][0] = in[1][1] = make_uint4(0, 0, 0, 0);
     }
     if (!ready) {
       kv_rows(v, r0, nr, rows);
       ready = true;
     }
+    const long long at = u < total ? rows[ku.row] : -1;
+    const long long row = (at < 0 ? 0 : at + (long long)ku.head * c.page_size) * (D / kGroup) + (ku.lane >> 2);  // group's pair
 #pragma unroll
-    for (int i = 0; i < kKvUnits; ++i) {
-      const int u = base + i * kKvThreads;
+    for (int i = 0; i < 2; ++i) {
       const uint32_t* w = &in[i][0].x;  // eight words of two values
       uint32_t lo = w[0], hi = w[0];
 #pragma unroll
@@ -168,20 +165,12 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
         // every code came with the bits of 1.5 * 2^23 in front: their sum over the eight places
         q[h] = acc - 0x4B400000u * 0x11111111u;
       }
-      const uint32_t bad = s16 == 0x7fc0;
-      if (u < total) {
-        const KvUnit ku = kv_unit<D>(g, u, u0, per);
-        const long long at = rows[ku.row];
-        if (at >= 0) {
-          const long long row = at + ku.head * c.page_size;
-          const int gr = ku.lane >> 2, l = ku.lane & 3;
-          uint32_t* qd = (ku.val ? c.v_q : c.k_q) + row * (D / 8) + gr * 8 + l;
-          qd[0] = bad ? 0 : q[0];
-          qd[4] = bad ? 0 : q[1];
-          if (l == 0)
-            reinterpret_cast<uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (D / kGroup) + gr] =
-                (uint32_t)s16 | (uint32_t)b16 << 16;
-        }
+      const bool bad = s16 == 0x7fc0;
+      if (at >= 0) {
+        uint32_t* qd = (i ? c.v_q : c.k_q) + row * 8 + (ku.lane & 3);
+        qd[0] = bad ? 0 : q[0];
+        qd[4] = bad ? 0 : q[1];
+        if ((ku.lane & 3) == 0) reinterpret_cast<uint32_t*>(i ? c.v_sb : c.k_sb)[row] = (uint32_t)s16 | (uint32_t)b16 << 16;
       }
     }
   }
@@ -204,39 +193,33 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
   }
   kv_rows(v, r0, nr, rows);
   const int u0 = blockIdx.y * g.chunk, per = min(u0 + g.chunk, g.units_row) - u0, total = nr * per;
-  for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kKvThreads * kKvUnits) {
-    uint32_t q[kKvUnits][2], sb[kKvUnits];
+  for (int u = threadIdx.x; u < total; u += kKvThreads) {
+    const KvUnit ku = kv_unit<D>(g, u, u0, per);
+    uint32_t q[2][2], sb[2];
+    const long long at = rows[ku.row];
+    if (at >= 0) {
+      const long long row = (at + (long long)ku.head * c.page_size) * (D / kGroup) + (ku.lane >> 2);  // group's pair
 #pragma unroll
-    for (int i = 0; i < kKvUnits; ++i) {
-      const int u = base + i * kKvThreads;
-      q[i][0] = q[i][1] = sb[i] = 0;
-      if (u < total) {
-        const KvUnit ku = kv_unit<D>(g, u, u0, per);
-        const long long at = rows[ku.row];
-        if (at >= 0) {
-          const long long row = at + ku.head * c.page_size;
-          const int gr = ku.lane >> 2, l = ku.lane & 3;
-          const uint32_t* qs = (ku.val ? c.v_q : c.k_q) + row * (D / 8) + gr * 8 + l;
-          q[i][0] = qs[0];
-          q[i][1] = qs[4];
-          sb[i] = reinterpret_cast<const uint32_t*>(ku.val ? c.v_sb : c.k_sb)[row * (D / kGroup) + gr];
-        }
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t* qs = (i ? c.v_q : c.k_q) + row * 8 + (ku.lane & 3);
+        q[i][0] = __ldg(qs);
+        q[i][1] = __ldg(qs + 4);
+        sb[i] = __ldg(reinterpret_cast<const uint32_t*>(i ? c.v_sb : c.k_sb) + row);
       }
+    } else {
+      q[0][0] = q[0][1] = q[1][0] = q[1][1] = sb[0] = sb[1] = 0;
     }
+    if (!held[ku.row]) continue;
+    const int col = ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < kKvUnits; ++i) {
-      const int u = base + i * kKvThreads;
-      if (u >= total) continue;
-      const KvUnit ku = kv_unit<D>(g, u, u0, per);
-      if (!held[ku.row]) continue;
+    for (int i = 0; i < 2; ++i) {
       // A code n places up in a word, put under the exponent of 2^23, is the number 2^23 + code * 16^n (n < 5); the rest of the
       // word comes down three places first. One subtraction, then one fused multiply-add with the scale / 16^n.
       const float s = bf16lo(sb[i]), b = bf16hi(sb[i]);
       const float s1 = s * 0x1p-4f, s2 = s * 0x1p-8f, s3 = s * 0x1p-12f, s4 = s * 0x1p-16f;
       const uint64_t f01 = kv_pair(s, s1), f23 = kv_pair(s2, s3), f42 = kv_pair(s4, s2), f34 = kv_pair(s3, s4);
       const uint64_t b2 = kv_pair(b, b), less = kv_pair(-8388608.f, -8388608.f);
-      uint16_t* dst = (ku.val ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) +
-                      ku.head * D + (ku.lane >> 2) * kGroup + (ku.lane & 3) * 8;
+      uint16_t* dst = (i ? val + (long long)(r0 + ku.row) * v_stride : k + (long long)(r0 + ku.row) * k_stride) + col;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t w = q[i][h], wd = w >> 12;
