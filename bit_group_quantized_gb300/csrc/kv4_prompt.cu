@@ -26,10 +26,12 @@
 //
 // All (unit, key head, 128 tokens) triples form one list, which k_prompt_plan lays out from
 // the lengths on the device; every CTA takes an equal, contiguous share, and units cut by a
-// share are joined by the last CTA to arrive, in CTA order (the same bits every time).
+// share are joined by k_prompt_join, in CTA order (the same bits every time).
 // Every wait is bounded: on expiry the status word is set to BGQ_ERR_TIMEOUT and all
 // later waits fall through, so the kernel ends by itself.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "attn.h"
 #include "common.cuh"
@@ -86,10 +88,17 @@ struct PrPlan {  // at the start of the workspace, behind the control block
   long long sum;  // cost of all units, for one key head
 };
 
+// A unit that CTA c began and did not end: CTAs c .. c1 have parts of it.
+struct __align__(16) PrCut {
+  int c1;  // -1: none
+  int first, col0, cols;  // the sequence's first row, the unit's first column, the sequence's columns
+  int h, pad[3];
+};
+
 struct PrWs {
   Ctrl* ctrl;
   PrPlan* plan;
-  int* count;         // [grid][NQ] arrivals, left at zero
+  PrCut* cuts;        // [grid]
   PrUnit* units;      // [cap]
   long long* prefix;  // [cap] cost of the units before a unit
   float* part;        // [grid][2][NQ][kSlot]
@@ -111,7 +120,7 @@ static PrWs carve_prompt(void* ws, int batch, int rows, int group, int d, int gr
   w.cap = (int)((long long)rows * group / (128 * nq)) + batch + 1;
   w.ctrl = reinterpret_cast<Ctrl*>(take(sizeof(Ctrl)));
   w.plan = reinterpret_cast<PrPlan*>(take(sizeof(PrPlan)));
-  w.count = reinterpret_cast<int*>(take((size_t)grid * nq * 4));
+  w.cuts = reinterpret_cast<PrCut*>(take((size_t)grid * sizeof(PrCut)));
   w.units = reinterpret_cast<PrUnit*>(take((size_t)w.cap * sizeof(PrUnit)));
   w.prefix = reinterpret_cast<long long*>(take((size_t)w.cap * 8));
   w.part = reinterpret_cast<float*>(take((size_t)grid * 2 * nq * (128 * d + 256) * 4));
@@ -283,7 +292,6 @@ __device__ __forceinline__ void pr_wait_loop(uint64_t* m, uint32_t parity, volat
 __device__ __forceinline__ void pr_wait(uint64_t* m, uint32_t parity, volatile int* fail) {
   if (!tc_mbar_try(m, parity)) pr_wait_loop(m, parity, fail);
 }
-__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Operand tiles: panels of 64 columns (128-byte rows, 128-byte swizzle, 128 rows: 16 KB).
 constexpr int kPanel = 128 * 128;
@@ -365,9 +373,7 @@ struct PrShared {
   __align__(16) uint32_t odd[kMetaTiles][4];
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
   uint32_t tmem;
-  int fail, last[NQ];
-  float log2_sum[NQ][128];  // of the rows of a unit being joined
-  int row[NQ][128];
+  int fail;
 };
 
 // A CTA's share of the list, unit by unit. A unit takes kUnitCost places of the list, then one for each tile; the
@@ -621,6 +627,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   const long long ctas = min((long long)gridDim.x, total / (kUnitCost + 1));
   const int cta = blockIdx.x;
   const int group = a.q_heads / a.c.kv_heads;
+  if (tid == 0) w.cuts[cta].c1 = -1;
   PrWalk<D> wk;
   wk.i0 = wk.i1 = 0;
   if (cta < ctas) wk.start(a, w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
@@ -831,7 +838,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       // ---- the unit's end: O / l, or a part of it
       if (!none) {
       const bool whole = wk.i0 == 0 && wk.i1 == wk.un.tiles;
-      const long long u0 = wk.x, u1 = u0 + wk.un.tiles - 1;  // the first and last tile's places in the list
       float* const part = w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot;
       pr_wait(&sh.o_full[i], o_par, fail);
       o_par ^= 1;
@@ -874,67 +880,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
       }
       tc_fence_before();
-      if (!whole) {
-        const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
-        __threadfence();
-        wg_sync(1 + i);
-        if (r == 0) {
-          const int last = atomicAdd(w.count + c0 * NQ + i, 1) == c1 - c0;
-          if (last) w.count[c0 * NQ + i] = 0;
-          sh.last[i] = last;
-        }
-        wg_sync(1 + i);
-        if (sh.last[i]) {
-          // joined by the whole warpgroup, 4 columns of a row at a time
-          __threadfence();
-          auto at = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * NQ + i) * P::kSlot; };
-          float top = -INFINITY, ls = 0.f;
-          if (!dead) {
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(at(c) + 128 * D + r));
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float mc = __ldcg(at(c) + 128 * D + r);
-              ls = fmaf(mc == top ? 1.f : pr_ex2(mc - top), __ldcg(at(c) + 128 * D + 128 + r), ls);
-            }
-            if (ok && a.lse) a.lse[(long long)row * a.q_heads + head] = ls == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(ls));
-          }
-          sh.log2_sum[i][r] = ls == 0.f ? INFINITY : top + log2f(ls);
-          sh.row[i][r] = ok ? row : -1;
-          wg_sync(1 + i);
-          const int rows = (min(128, min(sp.q_len, a.v.rows) * group - wk.un.rt * P::kRows - i * 128) + 31) & ~31;
-#pragma unroll 1
-          for (int n = r; n < rows * (D / 16); n += 128) {  // a row's 16 columns: four loads of each part at a time
-            const int d16 = n / rows, rr = n - d16 * rows, row_o = sh.row[i][rr];
-            const float t = sh.log2_sum[i][rr];
-            float v[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] = 0.f;
-#pragma unroll 2
-            for (int c = c0; c <= c1; ++c) {
-              const float* const pp = at(c);
-              const float4* const po = reinterpret_cast<const float4*>(pp) + d16 * 512 + rr;
-              float4 p[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) p[x] = __ldcg(po + x * 128);
-              const float f = pr_ex2(__ldcg(pp + 128 * D + rr) - t);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                v[4 * x] = fmaf(f, p[x].x, v[4 * x]);
-                v[4 * x + 1] = fmaf(f, p[x].y, v[4 * x + 1]);
-                v[4 * x + 2] = fmaf(f, p[x].z, v[4 * x + 2]);
-                v[4 * x + 3] = fmaf(f, p[x].w, v[4 * x + 3]);
-              }
-            }
-            if (row_o >= 0) {
-              const int h_o = wk.h * group + (wk.un.rt * P::kRows + i * 128 + rr) % group;
-              uint4* const o = reinterpret_cast<uint4*>(a.out + (long long)row_o * a.out_stride + h_o * D + d16 * 16);
-              o[0] = make_uint4(pr_bf2(v[0], v[1]), pr_bf2(v[2], v[3]), pr_bf2(v[4], v[5]), pr_bf2(v[6], v[7]));
-              o[1] = make_uint4(pr_bf2(v[8], v[9]), pr_bf2(v[10], v[11]), pr_bf2(v[12], v[13]), pr_bf2(v[14], v[15]));
-            }
-          }
-          wg_sync(1 + i);  // the rows' sums are free again
-        }
+      if (!whole && wk.i0 == 0 && r == 0 && i == 0) {
+        const long long last = wk.x + wk.un.tiles - 1;  // the unit's last tile's place in the list
+        w.cuts[cta] = PrCut{(int)(((last + 1) * ctas - 1) / total), sp.first, wk.un.rt * P::kRows, min(sp.q_len, a.v.rows) * group, wk.h, {}};
       }
       }
       if (!nw.live()) break;
@@ -1150,6 +1098,53 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   if (warp == 0) tmem_free(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------
+// The units that a CTA's share cut: every CTA's part, weighted, in CTA order. A block takes eight rows of one such unit, a
+// thread four columns (eight at head dim 256) of one row; neighbouring threads read neighbouring rows.
+// ---------------------------------------------------------------------------
+constexpr int kJoinRows = 8;
+template <int D>
+__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
+  using P = Prompt<D>;
+  constexpr int Q = D / 128 > 0 ? D / 128 : 1;
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x;
+  const PrCut cut = w.cuts[c0];
+  const int at_row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, col = cut.col0 + at_row, d4 = threadIdx.x / kJoinRows * Q;
+  if (cut.c1 < 0 || col >= cut.cols || d4 >= D / 4) return;
+  const int i = at_row >> 7, r = at_row & 127, group = a.q_heads / a.c.kv_heads;
+  const int j = col / group, row = cut.first + j, head = cut.h * group + col - j * group;
+  auto part = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * P::NQ + i) * P::kSlot; };
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= cut.c1; ++c) top = fmaxf(top, __ldg(part(c) + 128 * D + r));
+  float4 v[Q];
+#pragma unroll
+  for (int x = 0; x < Q; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= cut.c1; ++c) {
+    const float* pp = part(c);
+    const float mc = __ldg(pp + 128 * D + r), f = mc == top ? 1.f : pr_ex2(mc - top);
+    sum = fmaf(f, __ldg(pp + 128 * D + 128 + r), sum);
+#pragma unroll
+    for (int x = 0; x < Q; ++x) {
+      const float4 p = __ldg(reinterpret_cast<const float4*>(pp) + (d4 + x) * 128 + r);
+      v[x].x = fmaf(f, p.x, v[x].x);
+      v[x].y = fmaf(f, p.y, v[x].y);
+      v[x].z = fmaf(f, p.z, v[x].z);
+      v[x].w = fmaf(f, p.w, v[x].w);
+    }
+  }
+  if (row < 0 || row >= a.v.rows) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int x = 0; x < Q; ++x)
+    *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + head * D + (d4 + x) * 4) =
+        make_uint2(pr_bf2(v[x].x * inv, v[x].y * inv), pr_bf2(v[x].z * inv, v[x].w * inv));
+  if (a.lse && d4 == 0) a.lse[(long long)row * a.q_heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+}
+
 static int prompt_grid() { return num_sms(); }
 
 size_t prompt_workspace_bytes(int batch, int rows, int q_heads, int kv_heads, int d) {
@@ -1164,7 +1159,19 @@ static cudaError_t launch_prompt_t(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_overlapped(k_prompt_plan, 1, kPlanThreads, 0, s, a, w, P::kRows);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(k_attn_prompt<D>, prompt_grid(), kPrThreads, P::kSmem, s, a, w);
+  e = launch_overlapped(k_attn_prompt<D>, prompt_grid(), kPrThreads, P::kSmem, s, a, w);
+  if (e != cudaSuccess) return e;
+  const int rows = (int)std::min((long long)P::kRows, (long long)a.v.rows * (a.q_heads / a.c.kv_heads));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(prompt_grid(), (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_prompt_join<D>, a, w);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t s) {
