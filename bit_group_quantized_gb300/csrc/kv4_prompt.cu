@@ -672,61 +672,57 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
         const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && !fresh && e_run == 0;
-        // every row sees every token, and no factor but the row's: 64 tokens at a time
+        // Every row sees every token, and no factor but the row's: 64 tokens at a time. The probabilities are taken with the
+        // maximum so far while the scores' own is found; where that is too far above (seldom), it is raised and they are taken again.
 #pragma unroll 1
-        for (int c = 0; c < (plain && !dead ? 4 : 0); c += 2) {
-          uint32_t v[64];
+        for (int c = 0; c < (plain && !dead ? 4 : 0);) {
+          uint32_t v[64], pk[32];
           pr_ld32(s_t + c * 32, v);
           pr_ld32(s_t + c * 32 + 32, v + 32);
+          const float ck = fmaxf(c2, 0x1p-126f);
+          uint64_t ll = pr_pair(l0, l1);
+          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
           pr_wait_ld(v);
           pr_wait_ld(v + 32);
           float tp[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tp[k] = pr_max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
+          for (int k = 0; k < 4; ++k) tp[k] = __uint_as_float(v[k]);
 #pragma unroll
-          for (int x = 12; x < 60; x += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tp[k] = pr_max3(tp[k], __uint_as_float(v[x + k]), __uint_as_float(v[x + 4 + k]));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tp[k] = fmaxf(tp[k], __uint_as_float(v[60 + k]));
-          const float ck = fmaxf(c2, 0x1p-126f);
+          for (int x = 0; x < 32; ++x) {
+            const float s0 = __uint_as_float(v[2 * x]), s1 = __uint_as_float(v[2 * x + 1]);
+            float p0, p1;
+            tp[x & 3] = pr_max3(tp[x & 3], s0, s1);
+            pr_split(pr_fma2(pr_pair(s0, s1), ck2, mm2), p0, p1);
+            p0 = pr_ex2(p0);
+            p1 = pr_ex2(p1);
+            ll = pr_add2(ll, pr_pair(p0, p1));
+            pk[x] = pr_half2(p0, p1);
+          }
           const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
           const bool raise = top > m + 8.f;
-          if (__any_sync(kFull, raise)) {
-            const float up = raise ? top : m;
-            const float f = up == m ? 1.f : pr_ex2(m - up);
-            m = up;
-            mm = up == -INFINITY ? 0.f : up;
-            l0 *= f;
-            l1 *= f;
-            pr_wait_st();
+          if (!__any_sync(kFull, raise)) {
+            pr_split(ll, l0, l1);
+            pr_st16(s_t + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+            pr_st16(s_t + c * 16 + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+            c += 2;
+            continue;
+          }
+          const float up = raise ? top : m;
+          const float f = up == m ? 1.f : pr_ex2(m - up);
+          m = up;
+          mm = up == -INFINITY ? 0.f : up;
+          l0 *= f;
+          l1 *= f;
+          pr_wait_st();
 #pragma unroll 1
-            for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
-            if (it > wk.i0) {
-              if (NQ == 1) {  // the product before this one may still be running
-                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
-                tc_fence_after();
-              }
-              pr_scale<D>(o_t, f);
+          for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
+          if (it > wk.i0) {
+            if (NQ == 1) {  // the product before this one may still be running
+              pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+              tc_fence_after();
             }
+            pr_scale<D>(o_t, f);
           }
-          uint64_t ll = pr_pair(l0, l1);
-          const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float p0, p1;
-              pr_split(pr_fma2(pr_pair(__uint_as_float(v[k * 32 + 2 * x]), __uint_as_float(v[k * 32 + 2 * x + 1])), ck2, mm2), p0, p1);
-              p0 = pr_ex2(p0);
-              p1 = pr_ex2(p1);
-              ll = pr_add2(ll, pr_pair(p0, p1));
-              pk[x] = pr_half2(p0, p1);
-            }
-            pr_st16(s_t + (c + k) * 16, pk);
-          }
-          pr_split(ll, l0, l1);
         }
         // otherwise 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
 #pragma unroll 1
