@@ -7,6 +7,8 @@
 // expert applied to up to 8 tokens, so each weight row is read once for all of
 // them. Rows are split across CTAs; the CTA stages its task's inputs once and
 // keeps them while consecutive work items stay on the same task.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -663,9 +665,12 @@ cudaError_t launch_widen(const uint16_t* x, float* h, int n, cudaStream_t s) {
 }
 
 int num_sms() {
+  static std::atomic<int> known[64];  // per device; a property of the device, asked for once
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 132;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 132;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

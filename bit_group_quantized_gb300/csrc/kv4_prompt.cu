@@ -1151,7 +1151,8 @@ template <int D>
 static cudaError_t launch_prompt_t(const AttnArgs& a, cudaStream_t s) {
   using P = Prompt<D>;
   const PrWs w = carve_prompt(a.ws, a.v.batch, a.v.rows, a.q_heads / a.c.kv_heads, D, prompt_grid());
-  cudaError_t e = cudaFuncSetAttribute(k_attn_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  static std::atomic<uint64_t> allowed;
+  cudaError_t e = allow_smem(k_attn_prompt<D>, P::kSmem, allowed);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(k_prompt_plan, 1, kPlanThreads, 0, s, a, w, P::kRows);
   if (e != cudaSuccess) return e;

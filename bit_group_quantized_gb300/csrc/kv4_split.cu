@@ -901,7 +901,8 @@ size_t split_workspace_bytes(int max_q, int q_heads, int kv_heads, int d) {
 template <int D, int NT>
 static cudaError_t launch_split_t(const AttnArgs& a, cudaStream_t s) {
   using P = Split<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  static std::atomic<uint64_t> allowed;
+  cudaError_t e = allow_smem(k_attn_split<D, NT>, P::kSmem, allowed);
   if (e != cudaSuccess) return e;
   return launch_overlapped(k_attn_split<D, NT>, split_grid(D, NT), kSplitThreads, P::kSmem, s, a);
 }
