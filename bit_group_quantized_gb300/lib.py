@@ -412,48 +412,27 @@ def _heads(t, rows, heads, d: int, index, what: str):
     """t is bf16 [rows][heads][d] on CUDA device `index` (None: any), its heads one behind the other; rows and heads are
     free where None. Returns its rows, heads and the values between rows (of a single row, whose stride torch
     leaves open, its width)."""
-    _need(isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3
-          and (t.is_cuda if index is None else t.get_device() == index), what)
-    R, H, D = t.shape
-    sr, sh, sd = t.stride()
-    if D != d or sd != 1 or (sh != d and H != 1) or (rows is not None and R != rows) or (heads is not None and H != heads):
+    try:
+        R, H, D = t.shape
+        sr, sh, sd = t.stride()
+        dev = t.get_device()
+        ok = t.dtype is _BF16
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        raise BGQError(ERR_INVALID_ARG, what) from None
+    if (not ok or D != d or sd != 1 or (sh != d and H != 1) or (dev != index if index is not None else dev < 0)
+            or (rows is not None and R != rows) or (heads is not None and H != heads)):
         raise BGQError(ERR_INVALID_ARG, what)
     return R, H, sr if R > 1 else max(H * d, 8)
 
 
-def _raw_stream(index: int, stream) -> int:
-    """The stream to run on: the given one, else the device's current one."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+_BF16 = torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the device's current stream, as an address
+_device = torch._C._cuda_getDevice
 
 
-class _Here:
-    """Makes the call's device current, and the given stream, to which the buffers that the binding creates then belong."""
-
-    def __init__(self, index, stream):
-        self.guard = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        return self.guard.__enter__()
-
-    def __exit__(self, *e):
-        return self.guard.__exit__(*e)
-
-
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *e):
-        return None
-
-
-_NOTHING = _Nothing()
-
-
-def _here(index: int, stream):
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return _NOTHING
-    return _Here(index, stream)
+def _there(index, stream):
+    """Makes a call's device current, and the given stream, to which the buffers that the binding creates then belong."""
+    return torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
 
 class RopePlan:
@@ -477,18 +456,22 @@ def bgq_rope(plan: RopePlan, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor
     is allowed). inverse: the gradient's direction."""
     T, H, sx = _heads(x, None, None, plan.head_dim, None, "bgq_rope: x must be a CUDA bf16 tensor [tokens][heads][head_dim]")
     dev = x.get_device()
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_rope(plan, x, pos, y, inverse)
     _need(isinstance(pos, torch.Tensor) and pos.dtype is torch.int32 and pos.get_device() == dev,
           "bgq_rope: pos must be an int32 tensor [n_axes][tokens] on x's device")
-    ps, pt = tuple(pos.shape), pos.stride()
+    ps, pt = pos.shape, pos.stride()
     _need((ps == (plan.n_axes, T) or (plan.n_axes == 1 and ps == (T,))) and (T < 2 or pt[-1] == 1),
           "bgq_rope: pos must be [n_axes][tokens] with its tokens one behind the other")
-    with _here(dev, stream):
-        if y is None:
-            y = alloc((T, H, plan.head_dim), torch.bfloat16, x.device)
-        sy = _heads(y, T, H, plan.head_dim, dev, "bgq_rope: y must be a bf16 tensor like x")[2]
-        if T and H:
-            _check(load().bgq_rope(plan.ref, x.data_ptr(), sx, pos.data_ptr(), pt[0] if plan.n_axes > 1 else T, T, H,
-                                   y.data_ptr(), sy, inverse, _raw_stream(dev, stream)), "bgq_rope")
+    if y is None:
+        y = alloc((T, H, plan.head_dim), _BF16, x.device)
+    sy = _heads(y, T, H, plan.head_dim, dev, "bgq_rope: y must be a bf16 tensor like x")[2]
+    if T and H:
+        r = load().bgq_rope(plan.ref, x.data_ptr(), sx, pos.data_ptr(), pt[0] if plan.n_axes > 1 else T, T, H, y.data_ptr(),
+                            sy, inverse, _raw_stream(dev))
+        if r:
+            raise BGQError(r, "bgq_rope")
     return y
 
 
@@ -549,32 +532,37 @@ class KV4Seqs:
 
 def bgq_kv4_append(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """bgq_kv4_append: k, v bf16 [rows][kv_heads][head_dim] (rows may lie further apart) into the cache."""
-    dev, rows = cache.index, seqs.rows
+    dev, rows, H, d = cache.index, seqs.rows, cache.kv_heads, cache.head_dim
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_kv4_append(cache, seqs, k, v)
     what = "bgq_kv4_append: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache"
-    sk = _heads(k, rows, cache.kv_heads, cache.head_dim, dev, what)[2]
-    sv = _heads(v, rows, cache.kv_heads, cache.head_dim, dev, what)[2]
+    sk, sv = _heads(k, rows, H, d, dev, what)[2], _heads(v, rows, H, d, dev, what)[2]
     _need(seqs.index == dev, what)
     if rows:
-        with _here(dev, stream):
-            _check(load().bgq_kv4_append(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev, stream)),
-                   "bgq_kv4_append")
+        r = load().bgq_kv4_append(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev))
+        if r:
+            raise BGQError(r, "bgq_kv4_append")
 
 
 def bgq_kv4_read(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
                  stream=None):
     """bgq_kv4_read: (k, v) bf16 [rows][kv_heads][head_dim] of the rows' tokens."""
     dev, rows, H, d = cache.index, seqs.rows, cache.kv_heads, cache.head_dim
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_kv4_read(cache, seqs, k, v)
     what = "bgq_kv4_read: k and v must be bf16 [rows][kv_heads][head_dim] beside the cache"
     _need(seqs.index == dev, what)
-    with _here(dev, stream):
-        if k is None:
-            k = alloc((rows, H, d), torch.bfloat16, cache.device)
-        if v is None:
-            v = alloc((rows, H, d), torch.bfloat16, cache.device)
-        sk, sv = _heads(k, rows, H, d, dev, what)[2], _heads(v, rows, H, d, dev, what)[2]
-        if rows:
-            _check(load().bgq_kv4_read(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev, stream)),
-                   "bgq_kv4_read")
+    if k is None:
+        k = alloc((rows, H, d), _BF16, cache.device)
+    if v is None:
+        v = alloc((rows, H, d), _BF16, cache.device)
+    sk, sv = _heads(k, rows, H, d, dev, what)[2], _heads(v, rows, H, d, dev, what)[2]
+    if rows:
+        r = load().bgq_kv4_read(cache.ref, seqs.ref, k.data_ptr(), sk, v.data_ptr(), sv, _raw_stream(dev))
+        if r:
+            raise BGQError(r, "bgq_kv4_read")
     return k, v
 
 
@@ -589,26 +577,29 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
     """bgq_kv4_attention: q bf16 [rows][q_heads][head_dim] -> (out, lse or None). scale defaults to
     head_dim ** -0.5; lse fp32 [rows][q_heads] is written when given or wanted."""
     lib, dev, rows, d = load(), cache.index, seqs.rows, cache.head_dim
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_kv4_attention(cache, seqs, q, scale, causal, window, out, lse, want_lse, ws)
     _, H, sq = _heads(q, rows, None, d, dev, "bgq_kv4_attention: q must be bf16 [rows][q_heads][head_dim] beside the cache")
     _need(seqs.index == dev, "bgq_kv4_attention: the sequences must be beside the cache")
-    with _here(dev, stream):
-        if out is None:
-            out = alloc((rows, H, d), torch.bfloat16, cache.device)
-        so = _heads(out, rows, H, d, dev, "bgq_kv4_attention: out must be a bf16 tensor like q")[2]
-        if lse is None and want_lse:
-            lse = alloc((rows, H), torch.float32, cache.device)
-        if lse is not None:
-            _on(lse, torch.float32, dev, 2, "bgq_kv4_attention: lse must be fp32 [rows][q_heads]")
-            _need(tuple(lse.shape) == (rows, H) and lse.is_contiguous(),
-                  "bgq_kv4_attention: lse must be fp32 [rows][q_heads], contiguous")
-        if rows == 0:
-            return out, lse
-        if ws is None:
-            ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
-        _need(ws.get_device() == dev, "bgq_kv4_attention: ws must be beside the cache")
-        _check(lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), sq, H, d ** -0.5 if scale is None else scale, causal,
-                                     window, out.data_ptr(), so, None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), _raw_stream(dev, stream)), "bgq_kv4_attention")
+    if out is None:
+        out = alloc((rows, H, d), _BF16, cache.device)
+    so = _heads(out, rows, H, d, dev, "bgq_kv4_attention: out must be a bf16 tensor like q")[2]
+    if lse is None and want_lse:
+        lse = alloc((rows, H), torch.float32, cache.device)
+    if lse is not None:
+        _on(lse, torch.float32, dev, 2, "bgq_kv4_attention: lse must be fp32 [rows][q_heads]")
+        _need(lse.shape == (rows, H) and lse.is_contiguous(), "bgq_kv4_attention: lse must be fp32 [rows][q_heads], contiguous")
+    if rows == 0:
+        return out, lse
+    if ws is None:
+        ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
+    _need(ws.get_device() == dev, "bgq_kv4_attention: ws must be beside the cache")
+    r = lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), sq, H, d ** -0.5 if scale is None else scale, causal, window,
+                              out.data_ptr(), so, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+                              _raw_stream(dev))
+    if r:
+        raise BGQError(r, "bgq_kv4_attention")
     return out, lse
 
 
