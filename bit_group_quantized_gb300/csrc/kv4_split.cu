@@ -12,9 +12,8 @@
 // (cp.async), and takes tiles w, w + kWarps, ... of a segment (the part of a
 // unit inside the CTA's share) with a running maximum and sum per column.
 // Per tile, with mma.sync m16n8k16 (fp16 in, fp32 out):
-//   scores  S[token][col] = sum_g s_g (codes . x)_g + b_g sum(x)_g: the codes are the A
-//           operand as whole numbers (64 + code, placed by masks under the exponent of 64;
-//           the accumulator starts at -64 sum(x)), the query the B operand, scaled
+//   scores  S[token][col] = sum_g s_g ((64 + codes) . x)_g + (b_g - 64 s_g) sum(x)_g: the A operand
+//           is 64 + code, placed by masks under the exponent of 64, the query the B operand, scaled
 //           by a power of two per column, which is exact;
 //   output  O[dim][col] += (code - 8) (p s_g): the codes transposed by byte
 //           permutes as the A operand, the probabilities times the token's scale
@@ -77,13 +76,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same with an accumulator that starts from (c0, c1) in both rows.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1, float c0, float c1) {
+// The same with an accumulator that starts from zero.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Four 8x8 matrices of 16-bit units from shared memory, a row address a lane; TRANS: transposed.
 template <bool TRANS>
@@ -539,7 +538,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
 
     // ---- the query: fp16 fragments of column g, scaled by a power of two
     uint32_t qf[P::kQs ? 1 : NT * G * 8];
-    float xn[NT][2][G];             // of columns 2c, 2c + 1: -64 times the group's sum of x
+    float xs[NT][2][G];             // group sums of columns 2c, 2c + 1
     SplitAcc<D, NT> A;
     if (P::kQs) __syncthreads();    // the last segment's fragments are read
 #pragma unroll
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
       for (int k = 0; k < 2; ++k) {
         const int from = (2 * c + k) * 4;
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) xn[n][k][gr] = -64.f * __shfl_sync(kFull, sum[gr], from);
+        for (int gr = 0; gr < G; ++gr) xs[n][k][gr] = __shfl_sync(kFull, sum[gr], from);
         // at least the smallest normal number, so that -infinity times it stays -infinity
         A.cs[n][k] = fmaxf(fabsf(a.scale) * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from)), 0x1p-126f);
         const int cc = n * 8 + 2 * c + k, jj = (col0 + cc) / group;
@@ -686,7 +685,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
               }
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                if (k + i == 0) mma16816_from(acc[mt][n], f[mt][0], f[mt][1], f[mt][2], f[mt][3], b0, b1, xn[n][0][gr], xn[n][1][gr]);
+                if (k + i == 0) mma16816_zero(acc[mt][n], f[mt][0], f[mt][1], f[mt][2], f[mt][3], b0, b1);
                 else mma16816(acc[mt][n], f[mt][0], f[mt][1], f[mt][2], f[mt][3], b0, b1);
               }
             }
@@ -696,11 +695,11 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
         for (int mt = 0; mt < MT; ++mt) {
           const uint32_t* kp = reinterpret_cast<const uint32_t*>(st + 2 * P::kCode) + mt * 16 * G;
           const uint32_t p0 = kp[g * G + gr], p1 = kp[(g + 8) * G + gr];
-          // bias * sum(x): sum(x) is -1/64 of what the accumulator started from
-          const float b0 = bf16hi(p0) * -0x1p-6f, b1 = bf16hi(p1) * -0x1p-6f;
+          // the operand was 64 + code
+          const float b0 = fmaf(-64.f, bf16lo(p0), bf16hi(p0)), b1 = fmaf(-64.f, bf16lo(p1), bf16hi(p1));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const float x0 = xn[n][0][gr], x1 = xn[n][1][gr];
+            const float x0 = xs[n][0][gr], x1 = xs[n][1][gr];
             if (gr == 0) {
               s[mt][n][0] = fmaf(bf16lo(p0), acc[mt][n][0], b0 * x0);
               s[mt][n][1] = fmaf(bf16lo(p0), acc[mt][n][1], b0 * x1);
