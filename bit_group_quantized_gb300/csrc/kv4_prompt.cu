@@ -5,11 +5,16 @@
 // A unit is one key head of one sequence with kRows = 128 * NQ columns (a
 // column being one (query row, query head) pair that shares the key head), as
 // NQ tiles of 128 accumulator rows. Per 128 tokens:
-//   S = Q K^T   both fp16 in shared memory, S fp32 in tensor memory;
+//   S = Q K^T   both fp16 in shared memory, S fp32 in tensor memory. K's operand is (code - 8) * scale,
+//               which fp16 holds exactly; what is left of a key, bias + 8 * scale a group, is one more
+//               step of 16 columns: (bias, bias, scale, scale) a group against the query's group sum in
+//               two parts, and 8 times those. With code * scale + bias rounded to fp16 the logarithm of
+//               the sum was 1.2e-6 off (relative, 24 sequences of up to 9000 tokens, head dim 256), so
+//               it is 8e-8, for 3 % of the time;
 //   P = exp2(S c - m), fp16, written over S in tensor memory;
 //   O += P V    P from tensor memory, V fp16 in shared memory.
 // The warps are specialised: eight dequantise K and V (a thread takes a token: its codes
-// come by cp.async a tile ahead, value = code * scale + bias in fp16,
+// come by cp.async a tile ahead, V's value = code * scale + bias rounded to fp16 once,
 // stored in the 128-byte swizzled layout: K as the K-major, V as the MN-major
 // operand), four for each tile of rows do the softmax (a thread owns a row: its
 // maximum and sum need no shuffles), and bring the next unit's queries while the last
@@ -48,17 +53,23 @@ constexpr int kPlanThreads = 256;
 constexpr int kPlanSeqs = 4096;
 // What bringing a unit's queries and writing its rows costs, in tiles: CTAs with many short units take fewer tiles.
 constexpr int kUnitCost = 3;
+constexpr int kPanel = 128 * 128;  // bytes of an operand panel: 64 columns in 128-byte rows, 128-byte swizzle, 128 rows
+constexpr int kExtra = 128 * 32;   // bytes of an operand's 16 extra columns: 8 x 8 cores, unswizzled
 
 template <int D>
 struct Prompt {
   static constexpr int G = D / kGroup;
   static constexpr int NQ = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * NQ;
-  static constexpr int ST = D == 256 ? 1 : 2;  // K and V tiles held
-  static constexpr int kTile = kPrTok * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kRaw = kPrTok * D / 2;   // bytes of a tile's K or V codes
+  // K and V are held as rings of stages of some 64-column panels: two tiles of them, but at head dim 256, where a tile of
+  // Q alone is 64 KB, three quarters of a K tile and one V tile.
+  static constexpr int KP = D == 256 ? 1 : G, KST = D == 256 ? 3 : 2;
+  static constexpr int VP = D == 256 ? 2 : G, VST = 2;
+  static constexpr int kTile = kRows / NQ * D * 2;  // bytes of a Q tile
+  static constexpr int kRaw = kPrTok * D / 2;       // bytes of a tile's K or V codes
+  static constexpr int KE = G / KP > 1 ? 1 : KST;   // extra-column blocks of K held: each goes with its tile's first stage
   // more than half an SM's, so that no second CTA comes to wait for this one's tensor memory
-  static constexpr int kNeed = 1024 + (NQ + 2 * ST) * kTile + 2 * kRaw;
+  static constexpr int kNeed = 1024 + NQ * kTile + (KST * KP + VST * VP) * kPanel + 2 * kRaw + (NQ + KE) * kExtra;
   static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
   static constexpr int kSlot = 128 * D + 256;  // floats of a part: O by 4 columns and row, then m, then l
   // registers of a softmax, dequantisation and other warpgroup's threads: together at most the launch's
@@ -88,28 +99,28 @@ struct PrPlan {  // at the start of the workspace, behind the control block
   long long sum;  // cost of all units, for one key head
 };
 
-// A unit that CTA c began and did not end: CTAs c .. c1 have parts of it.
+// A unit that CTA c0 began and did not end: CTAs c0 .. c1 have parts of it.
 struct __align__(16) PrCut {
-  int c1;  // -1: none
+  int c0, c1;  // c1 -1: none
   int first, col0, cols;  // the sequence's first row, the unit's first column, the sequence's columns
-  int h, pad[3];
+  int h, pad[2];
 };
 
 struct PrWs {
   Ctrl* ctrl;
   PrPlan* plan;
-  PrCut* cuts;        // [grid]
+  PrCut* cuts;        // [ncut]: by unit and key head, or where CTAs are fewer than those, by c0
   PrUnit* units;      // [cap]
   long long* prefix;  // [cap] cost of the units before a unit
   float* part;        // [grid][2][NQ][kSlot]
-  int cap;
+  int cap, ncut;
   size_t bytes;
 };
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-static PrWs carve_prompt(void* ws, int batch, int rows, int group, int d, int grid) {
+static PrWs carve_prompt(void* ws, int batch, int rows, int q_heads, int kv_heads, int d, int grid) {
   char* p = static_cast<char*>(ws);
-  const int nq = d == 256 ? 1 : 2;
+  const int nq = d == 256 ? 1 : 2, group = q_heads / kv_heads;
   size_t at = 0;
   auto take = [&](size_t n) {
     char* r = p ? p + at : nullptr;
@@ -118,9 +129,10 @@ static PrWs carve_prompt(void* ws, int batch, int rows, int group, int d, int gr
   };
   PrWs w;
   w.cap = (int)((long long)rows * group / (128 * nq)) + batch + 1;
+  w.ncut = (int)std::min((long long)grid, (long long)w.cap * kv_heads);
   w.ctrl = reinterpret_cast<Ctrl*>(take(sizeof(Ctrl)));
   w.plan = reinterpret_cast<PrPlan*>(take(sizeof(PrPlan)));
-  w.cuts = reinterpret_cast<PrCut*>(take((size_t)grid * sizeof(PrCut)));
+  w.cuts = reinterpret_cast<PrCut*>(take((size_t)w.ncut * sizeof(PrCut)));
   w.units = reinterpret_cast<PrUnit*>(take((size_t)w.cap * sizeof(PrUnit)));
   w.prefix = reinterpret_cast<long long*>(take((size_t)w.cap * 8));
   w.part = reinterpret_cast<float*>(take((size_t)grid * 2 * nq * (128 * d + 256) * 4));
@@ -158,6 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_prompt_plan(const __grid_const
   __shared__ long long warp_sum[kPlanThreads / 32];
   pdl_wait();
   pdl_trigger();
+  for (int c = threadIdx.x; c < w.ncut; c += kPlanThreads) w.cuts[c].c1 = -1;
   const int per = (a.v.batch + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min((int)threadIdx.x * per, a.v.batch), b1 = min(b0 + per, a.v.batch);
   int own = 0;
@@ -293,10 +306,12 @@ __device__ __forceinline__ void pr_wait(uint64_t* m, uint32_t parity, volatile i
   if (!tc_mbar_try(m, parity)) pr_wait_loop(m, parity, fail);
 }
 
-// Operand tiles: panels of 64 columns (128-byte rows, 128-byte swizzle, 128 rows: 16 KB).
-constexpr int kPanel = 128 * 128;
+// Operand tiles: panels of 64 columns.
 __device__ __forceinline__ uint64_t pr_desc(uint32_t saddr, uint32_t lbo) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ uint64_t pr_extra_desc(uint32_t saddr) {  // cores: 128 bytes to the next 8 columns, 256 to the next 8 rows
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | 1ull << 46;
 }
 __device__ __forceinline__ constexpr uint32_t pr_idesc(int n, bool b_mn) {  // fp16 x fp16 -> fp32, M = 128
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -340,15 +355,15 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
   return d;
 }
 
-// Eight codes of a word as fp16 values code * s + b, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t s2, uint32_t b2) {
+// Eight codes of a word as fp16 values (64 + code + off) * s + b, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t off, uint32_t s2, uint32_t b2) {
   uint32_t o[4];
   const uint32_t r[4] = {w << 4, w, w >> 4, w >> 8};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 64 + code under the exponent of 64; exact, then one rounding
     uint32_t v;
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(r[i]), "r"(0x00F000F0u), "r"(0x54005400u));
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(0xD400D400u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(off));
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(v), "r"(s2), "r"(b2));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -366,8 +381,8 @@ constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at 
 
 template <int D>
 struct PrShared {
-  static constexpr int G = D / kGroup, NQ = Prompt<D>::NQ, ST = Prompt<D>::ST;
-  uint64_t k_full[ST], k_free[ST], v_full[ST], v_free[ST];
+  static constexpr int G = D / kGroup, NQ = Prompt<D>::NQ, KST = Prompt<D>::KST, VST = Prompt<D>::VST;
+  uint64_t k_full[KST], k_free[KST], v_full[VST], v_free[VST];
   uint64_t q_full[NQ], s_full[2], p_full[2], o_full[NQ], drain, pv_done;
   PrMeta meta[kMetaTiles][4];
   __align__(16) uint32_t odd[kMetaTiles][4];
@@ -498,27 +513,21 @@ __device__ __forceinline__ int pr_range(const uint32_t (&sb)[D / kGroup], uint32
   const int k = (int)(bits >> 23) - 127;
   return bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
 }
-// Writes the token's values into its row of the tile.
+// A token's values of group g into its row of a panel.
 template <int D>
-__device__ __forceinline__ void pr_store(const unsigned char* raw, const uint32_t (&sb)[D / kGroup], unsigned char* tile, int t,
-                                         int e) {
-  const float down = exp2i(-e);
+__device__ __forceinline__ void pr_store(const unsigned char* raw, int g, uint32_t off, uint32_t s2, uint32_t b2, unsigned char* panel, int t) {
+  unsigned char* row = panel + t * 128;
 #pragma unroll
-  for (int g = 0; g < D / kGroup; ++g) {
-    float s = bf16lo(sb[g]) * down, b = bf16hi(sb[g]) * down;
-    if (!(fabsf(s) < INFINITY && fabsf(b) < INFINITY)) s = b = 0.f;
-    const uint32_t s2 = pr_half2(s, s), b2 = pr_half2(b, b);
-    unsigned char* row = tile + g * kPanel + t * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 q = *reinterpret_cast<const uint4*>(raw + pr_raw<D>(t & 31, g * 2 + h));
-      *reinterpret_cast<uint4*>(row + (((h * 4) ^ (t & 7)) * 16)) = pr_values(q.x, s2, b2);
-      *reinterpret_cast<uint4*>(row + (((h * 4 + 1) ^ (t & 7)) * 16)) = pr_values(q.y, s2, b2);
-      *reinterpret_cast<uint4*>(row + (((h * 4 + 2) ^ (t & 7)) * 16)) = pr_values(q.z, s2, b2);
-      *reinterpret_cast<uint4*>(row + (((h * 4 + 3) ^ (t & 7)) * 16)) = pr_values(q.w, s2, b2);
-    }
+  for (int h = 0; h < 2; ++h) {
+    const uint4 q = *reinterpret_cast<const uint4*>(raw + pr_raw<D>(t & 31, g * 2 + h));
+    *reinterpret_cast<uint4*>(row + (((h * 4) ^ (t & 7)) * 16)) = pr_values(q.x, off, s2, b2);
+    *reinterpret_cast<uint4*>(row + (((h * 4 + 1) ^ (t & 7)) * 16)) = pr_values(q.y, off, s2, b2);
+    *reinterpret_cast<uint4*>(row + (((h * 4 + 2) ^ (t & 7)) * 16)) = pr_values(q.z, off, s2, b2);
+    *reinterpret_cast<uint4*>(row + (((h * 4 + 3) ^ (t & 7)) * 16)) = pr_values(q.w, off, s2, b2);
   }
 }
+// Byte of row t, columns 8 c of an operand's extra columns.
+__device__ __forceinline__ int pr_extra(int t, int c) { return (t >> 3) * 256 + c * 128 + (t & 7) * 16; }
 
 // The query row of a softmax thread in a unit.
 struct PrRowOf {
@@ -553,10 +562,10 @@ __device__ __forceinline__ void pr_query_fetch(const AttnArgs& a, const PrRowOf&
     pr_cp16(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16), a.q + (at < 0 ? 0 : at) + ch * 8, at >= 0);
   }
 }
-// Row r of the tile, in place: fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7; returns the
-// factor of its scores.
+// Row r of the tile, in place: fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7; and each group's sum,
+// in two parts, for the extra columns. Returns the factor of its scores.
 template <int D>
-__device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char* tile, int r) {
+__device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char* tile, unsigned char* extra, int r) {
   auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16)); };
   uint32_t t2[4] = {};
 #pragma unroll 8
@@ -571,12 +580,26 @@ __device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char
   for (int k = 0; k < 4; ++k) top = max(top, max(t2[k] & 0x7fff0000u, t2[k] << 17 >> 1));
   const int e = top && top < 0x7f800000u ? min(max((int)(top >> 23) - 130, -110), 110) : 0;
   const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint2 x = {};
+    if (g < D / kGroup) {
+      float sum[4] = {};
 #pragma unroll 4
-  for (int n = 0; n < D / 8; ++n) {
-    float f[8];
-    unpack_bf16x8(*chunk(n), f);
-    *chunk(n) = make_uint4(pr_half2(f[0] * up, f[4] * up), pr_half2(f[1] * up, f[5] * up), pr_half2(f[2] * up, f[6] * up),
-                           pr_half2(f[3] * up, f[7] * up));
+      for (int n = g * 8; n < g * 8 + 8; ++n) {
+        float f[8];
+        unpack_bf16x8(*chunk(n), f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= up;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] += f[k] + f[k + 4];
+        *chunk(n) = make_uint4(pr_half2(f[0], f[4]), pr_half2(f[1], f[5]), pr_half2(f[2], f[6]), pr_half2(f[3], f[7]));
+      }
+      const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);  // below 2^11
+      const float top = __half2float(__float2half_rn(all)), rest = all - top;
+      x = make_uint2(pr_half2(top, rest), pr_half2(8.f * top, 8.f * rest));
+    }
+    *reinterpret_cast<uint2*>(extra + pr_extra(r, g >> 1) + (g & 1) * 8) = x;
   }
   return fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
 }
@@ -584,20 +607,25 @@ __device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
   using P = Prompt<D>;
-  constexpr int G = P::G, NQ = P::NQ, ST = P::ST;
+  constexpr int G = P::G, NQ = P::NQ;
   extern __shared__ unsigned char smem_raw[];
   __shared__ PrShared<D> sh;
   unsigned char* const smem = smem_raw + ((1024 - (tc_smem(smem_raw) & 1023)) & 1023);
   unsigned char* const q_s = smem;
   unsigned char* const k_s = q_s + NQ * P::kTile;
-  unsigned char* const v_s = k_s + ST * P::kTile;
+  unsigned char* const v_s = k_s + P::KST * P::KP * kPanel;
+  unsigned char* const raw_s = v_s + P::VST * P::VP * kPanel;
+  unsigned char* const qe_s = raw_s + 2 * P::kRaw;   // extra columns
+  unsigned char* const ke_s = qe_s + NQ * kExtra;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* const fail = &sh.fail;
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < P::KST; ++i) {
       tc_mbar_init(&sh.k_full[i], 128);
-      tc_mbar_init(&sh.v_full[i], 128);
       tc_mbar_init(&sh.k_free[i]);
+    }
+    for (int i = 0; i < P::VST; ++i) {
+      tc_mbar_init(&sh.v_full[i], 128);
       tc_mbar_init(&sh.v_free[i]);
     }
     for (int i = 0; i < NQ; ++i) {
@@ -627,7 +655,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   const long long ctas = min((long long)gridDim.x, total / (kUnitCost + 1));
   const int cta = blockIdx.x;
   const int group = a.q_heads / a.c.kv_heads;
-  if (tid == 0) w.cuts[cta].c1 = -1;
   PrWalk<D> wk;
   wk.i0 = wk.i1 = 0;
   if (cta < ctas) wk.start(a, w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
@@ -827,7 +854,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         pr_query_fetch<D>(a, next_row, tc_smem(q_tile), r & ~31, lane);
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-        c2_next = pr_query_scale<D>(a, q_tile, r);
+        c2_next = pr_query_scale<D>(a, q_tile, qe_s + i * kExtra, r);
         tc_fence_proxy();
         tc_arrive(&sh.q_full[i]);
       }
@@ -878,7 +905,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       tc_fence_before();
       if (!whole && wk.i0 == 0 && r == 0 && i == 0) {
         const long long last = wk.x + wk.un.tiles - 1;  // the unit's last tile's place in the list
-        w.cuts[cta] = PrCut{(int)(((last + 1) * ctas - 1) / total), sp.first, wk.un.rt * P::kRows, min(sp.q_len, a.v.rows) * group, wk.h, {}};
+        w.cuts[w.ncut < (int)gridDim.x ? wk.h * w.cap + wk.u : cta] = PrCut{cta, (int)(((last + 1) * ctas - 1) / total), sp.first, wk.un.rt * P::kRows, min(sp.q_len, a.v.rows) * group, wk.h, {}};
       }
       }
       if (!nw.live()) break;
@@ -899,7 +926,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     unsigned char* const tiles = val ? v_s : k_s;
     const uint32_t* const codes = val ? a.c.v_q : a.c.k_q;
     const uint16_t* const pairs = val ? a.c.v_sb : a.c.k_sb;
-    const unsigned char* const raw = v_s + ST * P::kTile + (val ? P::kRaw : 0) + (warp & 3) * (P::kRaw / 4);
+    const unsigned char* const raw = raw_s + (val ? P::kRaw : 0) + (warp & 3) * (P::kRaw / 4);
+    // panels of a stage, stages; what turns 64 + code into V's code or K's code - 8
+    const int pan = val ? P::VP : P::KP, ring = val ? P::VST : P::KST;
+    const uint32_t off = val ? 0xD400D400u : 0xD480D480u;
+    if (!val && G < 4) {  // extra columns that no group has
+#pragma unroll
+      for (int i = 0; i < P::KE; ++i) *reinterpret_cast<uint4*>(ke_s + i * kExtra + pr_extra(part + lane, 1)) = make_uint4(0, 0, 0, 0);
+    }
     const uint32_t raw_u = tc_smem(raw);
     int st = 0;
     uint32_t par = 1;  // the first pass over the ring finds it free
@@ -937,6 +971,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int mt = x & (kMetaTiles - 1);
         uint32_t any, bad[G];
         const int e = pr_range<D>(sb, any, bad);
+        const float down = exp2i(-e);
+        uint32_t s2[G], b2[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float sc = bf16lo(sb[g]) * down, bi = bf16hi(sb[g]) * down;
+          if (!(fabsf(sc) < INFINITY && fabsf(bi) < INFINITY)) sc = bi = 0.f;
+          s2[g] = pr_half2(sc, sc);
+          b2[g] = pr_half2(bi, bi);
+        }
         pr_wait(&free_[st], par, fail);
         if (!val) {  // the notes on both go out with K, for the softmax reads them with the scores
           uint32_t vany, vbad[G];
@@ -952,17 +995,31 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
               for (int g = 0; g < G; ++g) sh.vbad[mt][c][g] = vany ? vbad[g] : 0;
             }
           }
+          unsigned char* const ext = ke_s + (P::KE > 1 ? st * kExtra : 0);
+#pragma unroll
+          for (int g = 0; g < G; g += 2)
+            *reinterpret_cast<uint4*>(ext + pr_extra(part + lane, g >> 1)) =
+                make_uint4(b2[g], s2[g], G > 1 ? b2[(g + 1) % G] : 0, G > 1 ? s2[(g + 1) % G] : 0);
+#pragma unroll
+          for (int g = 0; g < G; ++g) b2[g] = 0;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-        pr_store<D>(raw, sb, tiles + st * P::kTile, part + lane, e);
-        tc_fence_proxy();
-        tc_arrive(&full[st]);
-        __syncwarp();
-        if (++st == ST) {
-          st = 0;
-          par ^= 1;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int p = g & (pan - 1);  // the group's panel of its stage
+          if (g > 0 && p == 0) pr_wait(&free_[st], par, fail);
+          pr_store<D>(raw, g, off, s2[g], b2[g], tiles + (st * pan + p) * kPanel, part + lane);
+          if (p == pan - 1) {
+            tc_fence_proxy();
+            tc_arrive(&full[st]);
+            if (++st == ring) {
+              st = 0;
+              par ^= 1;
+            }
+          }
         }
+        __syncwarp();
       }
       // the next tile on its way, and the page of the one behind
       if (!more) break;
@@ -982,31 +1039,57 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     if (__shfl_sync(kFull, warp, 0) == 0) {
       const uint32_t lead = elect_lane();
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-      constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(D, true);
+      constexpr uint32_t id_s = pr_idesc(128, false), id_o = pr_idesc(P::VP * kGroup, true);
       // Short loops and few instructions per MMA: this thread's code competes with the other warps' for the
       // instruction caches. Only the low word of a descriptor changes (addresses stay below 2^18).
       const uint32_t hi_k = (uint32_t)(pr_desc(0, 16) >> 32), lo_k = (uint32_t)pr_desc(0, 16);
       const uint32_t hi_v = (uint32_t)(pr_desc(0, kPanel) >> 32), lo_v = (uint32_t)pr_desc(0, kPanel);
+      const uint32_t hi_e = (uint32_t)(pr_extra_desc(0) >> 32), lo_e = (uint32_t)pr_extra_desc(0);
       const uint32_t qa = lo_k + (tc_smem(q_s) >> 4), ka = lo_k + (tc_smem(k_s) >> 4), va = lo_v + (tc_smem(v_s) >> 4);
+      const uint32_t qe = lo_e + (tc_smem(qe_s) >> 4), ke = lo_e + (tc_smem(ke_s) >> 4);
       uint32_t q_par = 0, p_par = 0;          // bit per tile / slot
       int ks = 0, vs = 0;                      // ring places
       uint32_t k_par = 0, v_par = 0;
+      auto k_next = [&]() {
+        mma_commit(&sh.k_free[ks], lead);
+        if (++ks == P::KST) {
+          ks = 0;
+          k_par ^= 1;
+        }
+      };
+      auto v_next = [&]() {
+        mma_commit(&sh.v_free[vs], lead);
+        if (++vs == P::VST) {
+          vs = 0;
+          v_par ^= 1;
+        }
+      };
+      // Q K^T of row tile i; one row tile: stage by stage of K, as they come
       auto scores = [&](int i, int slot) {
         const uint32_t d = tm + slot * 128;
-        uint32_t qd = qa + i * (P::kTile >> 4), kd = ka + ks * (P::kTile >> 4);
+        uint32_t qd = qa + i * (P::kTile >> 4), kd = ka + ks * (P::KP * kPanel >> 4);
+        const uint32_t ked = ke + (P::KE > 1 ? ks * (kExtra >> 4) : 0);
 #pragma unroll 1
         for (int p = 0; p < G; ++p) {
+          if (NQ == 1) {
+            pr_wait(&sh.k_full[ks], k_par, fail);
+            tc_fence_after();
+            kd = ka + ks * (kPanel >> 4);
+          }
+          if (p == 0) mma_ss(d, (uint64_t)hi_e << 32 | (qe + i * (kExtra >> 4)), (uint64_t)hi_e << 32 | ked, id_s, 0, lead);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ss(d, (uint64_t)hi_k << 32 | (qd + k * 2), (uint64_t)hi_k << 32 | (kd + k * 2), id_s, p + k > 0, lead);
+            mma_ss(d, (uint64_t)hi_k << 32 | (qd + k * 2), (uint64_t)hi_k << 32 | (kd + k * 2), id_s, 1, lead);
           qd += kPanel >> 4;
           kd += kPanel >> 4;
+          if (NQ == 1) k_next();
         }
         mma_commit(&sh.s_full[slot], lead);
       };
-      auto product = [&](int i, int slot, bool first) {
-        const uint32_t d = tm + 256 + i * D;
-        uint32_t pa = tm + slot * 128, vd = va + vs * (P::kTile >> 4), acc = !first;
+      // P V of row tile i: the columns of one stage of V
+      auto product = [&](int i, int slot, int col, bool first) {
+        const uint32_t d = tm + 256 + i * D + col;
+        uint32_t pa = tm + slot * 128, vd = va + vs * (P::VP * kPanel >> 4), acc = !first;
 #pragma unroll 1
         for (int k = 0; k < kPrTok / 64; ++k) {
 #pragma unroll
@@ -1016,13 +1099,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
           pa += 32;
           vd += 512;
-        }
-      };
-      auto k_next = [&]() {
-        mma_commit(&sh.k_free[ks], lead);
-        if (++ks == ST) {
-          ks = 0;
-          k_par ^= 1;
         }
       };
       for (; __shfl_sync(kFull, (int)wk.live(), 0); wk.next(a, w, units)) {
@@ -1036,7 +1112,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 pr_wait(&sh.p_full[i], p_par >> i & 1, fail);
                 p_par ^= 1u << i;
                 tc_fence_after();
-                product(i, i, it == 0);
+                product(i, i, 0, it == 0);
                 if (it == n - 1) mma_commit(&sh.o_full[i], lead);
               } else {
                 pr_wait(&sh.q_full[i], q_par >> i & 1, fail);
@@ -1055,29 +1131,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
               q_par ^= 1;
             }
             const int slot = it & 1;
-            if (it + 1 < n) {
-              pr_wait(&sh.k_full[ks], k_par, fail);
-              tc_fence_after();
-              scores(0, (it + 1) & 1);
-              k_next();
-            }
+            if (it + 1 < n) scores(0, (it + 1) & 1);
             if (it >= 0) {
-              pr_wait(&sh.v_full[vs], v_par, fail);
               pr_wait(&sh.p_full[slot], p_par >> slot & 1, fail);
               p_par ^= 1u << slot;
-              tc_fence_after();
-              product(0, slot, it == 0);
+#pragma unroll 1
+              for (int col = 0; col < D; col += P::VP * kGroup) {
+                pr_wait(&sh.v_full[vs], v_par, fail);
+                tc_fence_after();
+                product(0, slot, col, it == 0);
+                v_next();
+              }
               mma_commit(&sh.pv_done, lead);
               if (it == n - 1) mma_commit(&sh.o_full[0], lead);
             }
           }
-          if (it >= 0) {
-            mma_commit(&sh.v_free[vs], lead);
-            if (++vs == ST) {
-              vs = 0;
-              v_par ^= 1;
-            }
-          }
+          if (NQ == 2 && it >= 0) v_next();
         }
       }
       // nothing is left in flight, whatever ended the loop
@@ -1096,61 +1165,104 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // The units that a CTA's share cut: every CTA's part, weighted, in CTA order. A block takes eight rows of one such unit, a
-// thread four columns (eight at head dim 256) of one row; neighbouring threads read neighbouring rows.
+// thread four columns (eight at head dim 256) of one row; neighbouring threads read neighbouring rows. Where units are
+// few, one may have a part of every CTA: then PG groups of threads take every PG-th part, and are joined in their order.
 // ---------------------------------------------------------------------------
 constexpr int kJoinRows = 8;
-template <int D>
-__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
+constexpr int kJoinThreads = 256;
+template <int D, int PG>
+__global__ void __launch_bounds__(kJoinThreads * PG) k_prompt_join(const __grid_constant__ AttnArgs a, const __grid_constant__ PrWs w) {
   using P = Prompt<D>;
-  constexpr int Q = D / 128 > 0 ? D / 128 : 1;
+  constexpr int Q = D / 128 > 0 ? D / 128 : 1, N = 4 * Q + 2, U = 4;
+  __shared__ float other[PG > 1 ? (PG - 1) * N * kJoinThreads : 1];
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x;
-  const PrCut cut = w.cuts[c0];
-  const int at_row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, col = cut.col0 + at_row, d4 = threadIdx.x / kJoinRows * Q;
-  if (cut.c1 < 0 || col >= cut.cols || d4 >= D / 4) return;
+  const int tid = threadIdx.x % kJoinThreads, pg = threadIdx.x / kJoinThreads;
+  const PrCut cut = w.cuts[blockIdx.x];
+  const int c0 = cut.c0;
+  const int at_row = blockIdx.y * kJoinRows + tid % kJoinRows, col = cut.col0 + at_row, d4 = tid / kJoinRows * Q;
+  if (cut.c1 < 0 || blockIdx.y * kJoinRows + cut.col0 >= cut.cols) return;
+  const bool live = col < cut.cols && d4 < D / 4;
   const int i = at_row >> 7, r = at_row & 127, group = a.q_heads / a.c.kv_heads;
   const int j = col / group, row = cut.first + j, head = cut.h * group + col - j * group;
   auto part = [&](int c) { return w.part + ((long long)(c * 2 + (c == c0)) * P::NQ + i) * P::kSlot; };
-  float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= cut.c1; ++c) top = fmaxf(top, __ldg(part(c) + 128 * D + r));
-  float4 v[Q];
+  float top = -INFINITY, sum = 0.f, v[4 * Q] = {};
+  if (live) {
+#pragma unroll 1
+    for (int c = c0 + pg; c <= cut.c1; c += PG * U) {  // U parts' loads at once
+      float mc[U], lc[U], up = top;
+      float4 p[U][Q];
 #pragma unroll
-  for (int x = 0; x < Q; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= cut.c1; ++c) {
-    const float* pp = part(c);
-    const float mc = __ldg(pp + 128 * D + r), f = mc == top ? 1.f : pr_ex2(mc - top);
-    sum = fmaf(f, __ldg(pp + 128 * D + 128 + r), sum);
+      for (int k = 0; k < U; ++k) {
+        const float* pp = part(min(c + k * PG, cut.c1));
+        mc[k] = __ldg(pp + 128 * D + r);
+        lc[k] = __ldg(pp + 128 * D + 128 + r);
 #pragma unroll
-    for (int x = 0; x < Q; ++x) {
-      const float4 p = __ldg(reinterpret_cast<const float4*>(pp) + (d4 + x) * 128 + r);
-      v[x].x = fmaf(f, p.x, v[x].x);
-      v[x].y = fmaf(f, p.y, v[x].y);
-      v[x].z = fmaf(f, p.z, v[x].z);
-      v[x].w = fmaf(f, p.w, v[x].w);
+        for (int x = 0; x < Q; ++x) p[k][x] = __ldg(reinterpret_cast<const float4*>(pp) + (d4 + x) * 128 + r);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (c + k * PG <= cut.c1) up = fmaxf(up, mc[k]);
+      const float f0 = top == up ? 1.f : pr_ex2(top - up);
+      top = up;
+      sum *= f0;
+#pragma unroll
+      for (int x = 0; x < 4 * Q; ++x) v[x] *= f0;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (c + k * PG > cut.c1) break;
+        const float f = mc[k] == top ? 1.f : pr_ex2(mc[k] - top);
+        sum = fmaf(f, lc[k], sum);
+#pragma unroll
+        for (int x = 0; x < Q; ++x) {
+          v[4 * x] = fmaf(f, p[k][x].x, v[4 * x]);
+          v[4 * x + 1] = fmaf(f, p[k][x].y, v[4 * x + 1]);
+          v[4 * x + 2] = fmaf(f, p[k][x].z, v[4 * x + 2]);
+          v[4 * x + 3] = fmaf(f, p[k][x].w, v[4 * x + 3]);
+        }
+      }
     }
   }
-  if (row < 0 || row >= a.v.rows) return;
+  if (PG > 1) {
+    if (pg > 0) {
+      float* o = other + (pg - 1) * N * kJoinThreads + tid;
+      o[0] = top;
+      o[kJoinThreads] = sum;
+#pragma unroll
+      for (int x = 0; x < 4 * Q; ++x) o[(2 + x) * kJoinThreads] = v[x];
+    }
+    __syncthreads();
+    if (pg > 0) return;
+#pragma unroll
+    for (int g = 0; g < PG - 1; ++g) {
+      const float* o = other + g * N * kJoinThreads + tid;
+      const float m2 = o[0], up = fmaxf(top, m2);
+      const float f = top == up ? 1.f : pr_ex2(top - up), f2 = m2 == up ? 1.f : pr_ex2(m2 - up);
+      top = up;
+      sum = sum * f + o[kJoinThreads] * f2;
+#pragma unroll
+      for (int x = 0; x < 4 * Q; ++x) v[x] = v[x] * f + o[(2 + x) * kJoinThreads] * f2;
+    }
+  }
+  if (!live || row < 0 || row >= a.v.rows) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int x = 0; x < Q; ++x)
     *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + head * D + (d4 + x) * 4) =
-        make_uint2(pr_bf2(v[x].x * inv, v[x].y * inv), pr_bf2(v[x].z * inv, v[x].w * inv));
+        make_uint2(pr_bf2(v[4 * x] * inv, v[4 * x + 1] * inv), pr_bf2(v[4 * x + 2] * inv, v[4 * x + 3] * inv));
   if (a.lse && d4 == 0) a.lse[(long long)row * a.q_heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
 }
 
 static int prompt_grid() { return num_sms(); }
 
 size_t prompt_workspace_bytes(int batch, int rows, int q_heads, int kv_heads, int d) {
-  return carve_prompt(nullptr, batch, rows, q_heads / kv_heads, d, prompt_grid()).bytes;
+  return carve_prompt(nullptr, batch, rows, q_heads, kv_heads, d, prompt_grid()).bytes;
 }
 
 template <int D>
 static cudaError_t launch_prompt_t(const AttnArgs& a, cudaStream_t s) {
   using P = Prompt<D>;
-  const PrWs w = carve_prompt(a.ws, a.v.batch, a.v.rows, a.q_heads / a.c.kv_heads, D, prompt_grid());
+  const PrWs w = carve_prompt(a.ws, a.v.batch, a.v.rows, a.q_heads, a.c.kv_heads, D, prompt_grid());
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem(k_attn_prompt<D>, P::kSmem, allowed);
   if (e != cudaSuccess) return e;
@@ -1160,15 +1272,16 @@ static cudaError_t launch_prompt_t(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int rows = (int)std::min((long long)P::kRows, (long long)a.v.rows * (a.q_heads / a.c.kv_heads));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(prompt_grid(), (rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(w.ncut, (rows + kJoinRows - 1) / kJoinRows);
+  const bool few = w.ncut * 8 <= prompt_grid();  // a unit has parts of eight CTAs or more
+  cfg.blockDim = dim3(few ? 4 * kJoinThreads : kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_prompt_join<D>, a, w);
+  return few ? cudaLaunchKernelEx(&cfg, k_prompt_join<D, 4>, a, w) : cudaLaunchKernelEx(&cfg, k_prompt_join<D, 1>, a, w);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t s) {
