@@ -103,7 +103,7 @@ struct AttnArgs {
 size_t attn_workspace_bytes(int batch, int rows, int max_q, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 
-size_t split_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim);
+size_t split_workspace_bytes(int batch, int max_q, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);
 size_t prompt_workspace_bytes(int batch, int rows, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn_prompt(const AttnArgs& a, cudaStream_t s);

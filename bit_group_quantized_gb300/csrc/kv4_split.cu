@@ -35,18 +35,20 @@ namespace bgq {
 
 constexpr int kSplitWarps = 8;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then the arrival counters
-constexpr int kSplitMaxGrid = (kSplitHead - 256) / 4;
+constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then two arrival counters a CTA
+constexpr int kSplitMaxGrid = (kSplitHead - 256) / 8;
 // What a unit costs beside its tiles (its queries, the joining of the warps), in tiles.
 constexpr int kSplitUnitCost = 20;
 
-template <int D, int NT>
+// CTAs: of an SM. Two of 128 registers a thread keep it busy while one joins its warps; one of 255 spares registers (at
+// 128, a head dim times column tiles of 256 or more spills them) and halves the parts to join.
+template <int D, int NT, int CTAS>
 struct Split {
   static constexpr int G = D / kGroup;
   static constexpr int C = 8 * NT;                 // columns of a unit
   static constexpr int TT = D == 256 ? 16 : 32;    // tokens of a tile
   static constexpr int MT = TT / 16;
-  static constexpr int ST = D == 64 ? 3 : D == 256 && NT == 2 ? 4 : 2;  // tiles of a warp's ring
+  static constexpr int ST = D == 64 ? 3 : CTAS == 1 ? 4 : 2;  // tiles of a warp's ring
   static constexpr int CPT = D / 32;               // 16-byte chunks of a token's codes
   static constexpr int kCode = TT * D / 2;         // bytes of a tile's K (or V) codes
   static constexpr int kSb = TT * D / 16;          // bytes of a tile's K (or V) pairs
@@ -56,9 +58,8 @@ struct Split {
   static constexpr bool kQs = D * NT > 64;         // query fragments in shared memory
   static constexpr int kQBytes = kQs ? NT * G * 4 * 32 * 8 : 0;
   static constexpr int kSmem = kSplitWarps * ST * kStage + kSplitWarps * C * RS * 4 + kQBytes;
-  static constexpr int kCtas = D == 256 && NT == 2 ? 1 : 2;  // per SM
   // the joining of CTAs keeps a weight for every part and column, and a column group for every thread
-  static_assert((kSplitWarps * C * RS) >= 304 / (3 - kCtas) * C + 4 + kSplitThreads * 4, "join area too small");
+  static_assert((kSplitWarps * C * RS) >= 304 / (3 - CTAS) * C + 4 + kSplitThreads * 4, "join area too small");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -210,9 +211,9 @@ struct SplitAcc {
 
 // What follows a tile's scores s; MASKED where some column does not see all of its tokens.
 template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT>::MT][NT][4], const unsigned char* st,
+__device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st,
                                              uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
-  using P = Split<D, NT>;
+  using P = Split<D, NT, 1>;  // nothing here goes by the CTAs
   constexpr int G = P::G, MT = P::MT;
   bool hid[MT][NT][4];
   uint32_t vp[MT][2][G], big = 0;  // V's pairs; the largest scale, as bits
@@ -364,9 +365,9 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
   }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_split(const __grid_constant__ AttnArgs a) {
-  using P = Split<D, NT>;
+template <int D, int NT, int CTAS>
+__global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid_constant__ AttnArgs a) {
+  using P = Split<D, NT, CTAS>;
   constexpr int G = P::G, C = P::C, TT = P::TT, MT = P::MT, ST = P::ST, RD = P::RD, RS = P::RS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_m[kSplitWarps][C], s_l[kSplitWarps][C];
@@ -811,45 +812,64 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
     if (!whole) {  // the last CTA to arrive joins the unit's parts
       const long long u0 = wk.x, u1 = u0 + wk.q.tiles - 1;  // the places of the unit's first and last tile
       const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const int last = atomicAdd(ws.count + c0, 1) == c1 - c0;
-        if (last) ws.count[c0] = 0;
-        s_last = last;
+      // Many and large parts are joined by eights first, each eight by its own last CTA: one SM alone reads half a MB too
+      // slowly (76 parts of 16 columns of 256: 49 us for the call with one join, 40 with two; 38 parts of 4 columns of
+      // 128: 44.5 with one, 46.9 with two).
+      const int np = c1 - c0 + 1;
+      int first = 0, step = 1, n = np, *count = ws.count + c0;
+      bool top_level = np * ncol * D <= 1 << 17;
+      if (!top_level) {
+        first = (cta - c0) / 8 * 8;
+        n = min(8, np - first);
+        count = ws.count + gridDim.x + c0 + first;
       }
-      __syncthreads();
-      if (s_last) {
+      for (;;) {
         __threadfence();
-        const int np = c1 - c0 + 1;
-        auto at = [&](int i) { return ws.part + ((long long)(c0 + i) * 2 + (i == 0)) * (C * (D + 2)); };
-        // the parts' weights: 2^(m - largest m) / sum, a warp a column
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          const int last = atomicAdd(count, 1) == n - 1;
+          if (last) *count = 0;
+          s_last = last;
+        }
+        __syncthreads();
+        if (!s_last) break;
+        __threadfence();
+        auto at = [&](int i) {
+          const int p = first + i * step;
+          return ws.part + ((long long)(c0 + p) * 2 + (p == 0)) * (C * (D + 2));
+        };
+        // the parts' weights: 2^(m - largest m), over the sum at last, a warp a column
         float* const wm = area;
-        for (int i = threadIdx.x; i < np * ncol; i += kSplitThreads) wm[i] = __ldcg(at(i / ncol) + C * D + i % ncol);
+        for (int i = threadIdx.x; i < n * ncol; i += kSplitThreads) wm[i] = __ldcg(at(i / ncol) + C * D + i % ncol);
         __syncthreads();
         for (int col = warp; col < ncol; col += kSplitWarps) {
           float top = -INFINITY, sum = 0.f;
-          for (int p = lane; p < np; p += 32) top = fmaxf(top, wm[p * ncol + col]);
+          for (int p = lane; p < n; p += 32) top = fmaxf(top, wm[p * ncol + col]);
           top = warp_max(top);
-#pragma unroll 4
-          for (int p = lane; p < np; p += 32) {
+          for (int p = lane; p < n; p += 32) {
             const float mp = wm[p * ncol + col];
             sum = fmaf(mp == top ? 1.f : ex2(mp - top), __ldcg(at(p) + C * D + C + col), sum);
           }
           sum = warp_sum(sum);
-          const float r = sum == 0.f ? 0.f : 1.f / sum;
-          for (int p = lane; p < np; p += 32) {
+          const float r = !top_level ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+          for (int p = lane; p < n; p += 32) {
             const float mp = wm[p * ncol + col];
             wm[p * ncol + col] = (mp == top ? 1.f : ex2(mp - top)) * r;
           }
           const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
-          if (a.lse && lane == 0 && row >= 0 && row < a.v.rows)
-            a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+          if (lane == 0) {
+            if (!top_level) {  // the eight's first part becomes all of it
+              at(0)[C * D + col] = top;
+              at(0)[C * D + C + col] = sum;
+            } else if (a.lse && row >= 0 && row < a.v.rows) {
+              a.lse[(long long)row * a.q_heads + h * group + hh] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(sum));
+            }
+          }
         }
         __syncthreads();
         // every thread four columns of a row; with threads to spare, the parts are dealt out over them
         const int items = ncol * (D / 4), deal = max(1, kSplitThreads / items);
-        float4* const sums = reinterpret_cast<float4*>(area + (np * ncol + 3) / 4 * 4);
+        float4* const sums = reinterpret_cast<float4*>(area + (n * ncol + 3) / 4 * 4);
         for (int i0 = 0; i0 < items; i0 += kSplitThreads) {
           const int i = i0 + (int)threadIdx.x % (items < kSplitThreads ? items : kSplitThreads);
           const int share = items < kSplitThreads ? threadIdx.x / items : 0;
@@ -857,7 +877,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < items && share < deal) {
 #pragma unroll 8
-            for (int p = share; p < np; p += deal) {
+            for (int p = share; p < n; p += deal) {
               const float w = wm[p * ncol + col];
               const float4 v = __ldcg(reinterpret_cast<const float4*>(at(p) + col * D + d4));
               acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
@@ -872,11 +892,19 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
               acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
             }
             const int j = (col0 + col) / group, hh = col0 + col - j * group, row = wk.q.sp.first + j;
-            if (row >= 0 && row < a.v.rows)
+            if (!top_level)
+              *reinterpret_cast<float4*>(at(0) + col * D + d4) = acc;
+            else if (row >= 0 && row < a.v.rows)
               *reinterpret_cast<uint2*>(a.out + (long long)row * a.out_stride + (h * group + hh) * D + d4) =
                   make_uint2((uint32_t)f2bf(acc.x) | (uint32_t)f2bf(acc.y) << 16, (uint32_t)f2bf(acc.z) | (uint32_t)f2bf(acc.w) << 16);
           }
         }
+        if (top_level) break;
+        first = 0;
+        step = 8;
+        n = (np + 7) / 8;
+        count = ws.count + c0;
+        top_level = true;
       }
     }
     __syncthreads();  // the join area and the sums are free again
@@ -887,32 +915,41 @@ __global__ void __launch_bounds__(kSplitThreads, Split<D, NT>::kCtas) k_attn_spl
 // Columns a unit takes: the smallest of 8 and 16 that holds a whole sequence's, else 16.
 static int split_nt(int max_q, int q_heads, int kv_heads) { return (long long)max_q * (q_heads / kv_heads) <= 8 ? 1 : 2; }
 
-static int split_grid(int d, int nt) {
-  const int n = num_sms() * (d == 256 && nt == 2 ? 1 : 2);
+// CTAs per SM: two, but one where units are few (then each has parts of many CTAs) or registers would be spilled. In us,
+// two and one: 131071 tokens, 8 key heads of 128, 4 columns: 44.7, 43.2; 8000 tokens: 18.8, 15.3; 65536 tokens, 2 key heads, 8
+// columns: 24.3, 20.0; 64 sequences of 512 to 16384 tokens, 8 key heads, 4 columns: 86.1, 92.3. Head dim 256, 131071 tokens:
+// 108, 70.
+static int split_ctas(int d, int nt, int batch, int kv_heads) {
+  return d * nt >= 256 || (long long)batch * kv_heads <= num_sms() ? 1 : 2;
+}
+static int split_grid(int ctas) {
+  const int n = num_sms() * ctas;
   return n < kSplitMaxGrid ? n : kSplitMaxGrid;
 }
 
-size_t split_workspace_bytes(int max_q, int q_heads, int kv_heads, int d) {
+size_t split_workspace_bytes(int batch, int max_q, int q_heads, int kv_heads, int d) {
   const int nt = split_nt(max_q, q_heads, kv_heads);
-  return kSplitHead + (((size_t)split_grid(d, nt) * 2 * 8 * nt * (d + 2) * 4 + 255) & ~(size_t)255);
+  const int grid = split_grid(split_ctas(d, nt, batch, kv_heads));
+  return kSplitHead + (((size_t)grid * 2 * 8 * nt * (d + 2) * 4 + 255) & ~(size_t)255);
 }
 
-template <int D, int NT>
+template <int D, int NT, int CTAS>
 static cudaError_t launch_split_t(const AttnArgs& a, cudaStream_t s) {
-  using P = Split<D, NT>;
+  using P = Split<D, NT, CTAS>;
   static std::atomic<uint64_t> allowed;
-  cudaError_t e = allow_smem(k_attn_split<D, NT>, P::kSmem, allowed);
+  cudaError_t e = allow_smem(k_attn_split<D, NT, CTAS>, P::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(k_attn_split<D, NT>, split_grid(D, NT), kSplitThreads, P::kSmem, s, a);
+  return launch_overlapped(k_attn_split<D, NT, CTAS>, split_grid(CTAS), kSplitThreads, P::kSmem, s, a);
 }
 
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s) {
-  const int nt = split_nt(a.max_q, a.q_heads, a.c.kv_heads);
-  switch (a.c.head_dim) {
-    case 64: return nt == 1 ? launch_split_t<64, 1>(a, s) : launch_split_t<64, 2>(a, s);
-    case 128: return nt == 1 ? launch_split_t<128, 1>(a, s) : launch_split_t<128, 2>(a, s);
-    default: return nt == 1 ? launch_split_t<256, 1>(a, s) : launch_split_t<256, 2>(a, s);
-  }
+  const int nt = split_nt(a.max_q, a.q_heads, a.c.kv_heads), d = a.c.head_dim;
+  const bool two = split_ctas(d, nt, a.v.batch, a.c.kv_heads) == 2;
+  if (d == 64 && nt == 1) return two ? launch_split_t<64, 1, 2>(a, s) : launch_split_t<64, 1, 1>(a, s);
+  if (d == 64) return two ? launch_split_t<64, 2, 2>(a, s) : launch_split_t<64, 2, 1>(a, s);
+  if (d == 128 && nt == 1) return two ? launch_split_t<128, 1, 2>(a, s) : launch_split_t<128, 1, 1>(a, s);
+  if (d == 128) return launch_split_t<128, 2, 1>(a, s);
+  return nt == 1 ? launch_split_t<256, 1, 1>(a, s) : launch_split_t<256, 2, 1>(a, s);
 }
 
 }  // namespace bgq
