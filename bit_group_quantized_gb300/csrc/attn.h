@@ -88,6 +88,10 @@ cudaError_t launch_kv4_append(const bgq_kv4_cache& c, const Kv4View& v, const ui
 cudaError_t launch_kv4_read(const bgq_kv4_cache& c, const Kv4View& v, uint16_t* k, long long k_stride, uint16_t* val,
                             long long v_stride, cudaStream_t s);
 
+// Bytes at the start of an attention workspace that only the control block and kv4_split.cu's arrival counters use, which
+// every call leaves at zero: calls of both kernels and of any shapes may share a workspace.
+constexpr int kAttnHead = 4096;
+
 struct AttnArgs {
   bgq_kv4_cache c;
   Kv4View v;

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kMaxHeads = 256;
 constexpr int kMaxSeqs = 4096;
+constexpr int64_t kMaxTokens = INT32_MAX - 65535;  // of a sequence: kernels step past the last by less than the rest
 
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline cudaStream_t st(void* s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -53,6 +54,7 @@ Kv4View view(const bgq_kv4_cache* c, const bgq_kv4_seqs* s) {
   v.page_size = c->page_size;
   v.heads = c->kv_heads;
   v.cap = (long long)v.max_pages * v.page_size;
+  if (v.cap > kMaxTokens) v.cap = kMaxTokens;
   return v;
 }
 

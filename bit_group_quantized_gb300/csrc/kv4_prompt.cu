@@ -130,7 +130,7 @@ static PrWs carve_prompt(void* ws, int batch, int rows, int q_heads, int kv_head
   PrWs w;
   w.cap = (int)((long long)rows * group / (128 * nq)) + batch + 1;
   w.ncut = (int)std::min((long long)grid, (long long)w.cap * kv_heads);
-  w.ctrl = reinterpret_cast<Ctrl*>(take(sizeof(Ctrl)));
+  w.ctrl = reinterpret_cast<Ctrl*>(take(kAttnHead));
   w.plan = reinterpret_cast<PrPlan*>(take(sizeof(PrPlan)));
   w.cuts = reinterpret_cast<PrCut*>(take((size_t)w.ncut * sizeof(PrCut)));
   w.units = reinterpret_cast<PrUnit*>(take((size_t)w.cap * sizeof(PrUnit)));

@@ -35,8 +35,7 @@ namespace bgq {
 
 constexpr int kSplitWarps = 8;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitHead = 4096;  // bytes before the parts: 256 of control block, then two arrival counters a CTA
-constexpr int kSplitMaxGrid = (kSplitHead - 256) / 8;
+constexpr int kSplitMaxGrid = (kAttnHead - 256) / 8;  // two arrival counters a CTA, behind the control block
 // What a unit costs beside its tiles (its queries, the joining of the warps), in tiles.
 constexpr int kSplitUnitCost = 20;
 
@@ -748,7 +747,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
         if (g == 0) s_l[warp][n * 8 + 2 * c + k] = A.l[n][k] * f[n][k];
       }
     const bool whole = wk.i0 == 0 && wk.i1 == wk.q.tiles;
-    const SplitWs ws{reinterpret_cast<int*>(static_cast<char*>(a.ws) + 256), reinterpret_cast<float*>(static_cast<char*>(a.ws) + kSplitHead)};
+    const SplitWs ws{reinterpret_cast<int*>(static_cast<char*>(a.ws) + 256), reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttnHead)};
     float* part = ws.part + ((long long)cta * 2 + (wk.i0 == 0)) * (C * (D + 2));
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += RD) {
@@ -930,7 +929,7 @@ static int split_grid(int ctas) {
 size_t split_workspace_bytes(int batch, int max_q, int q_heads, int kv_heads, int d) {
   const int nt = split_nt(max_q, q_heads, kv_heads);
   const int grid = split_grid(split_ctas(d, nt, batch, kv_heads));
-  return kSplitHead + (((size_t)grid * 2 * 8 * nt * (d + 2) * 4 + 255) & ~(size_t)255);
+  return kAttnHead + (((size_t)grid * 2 * 8 * nt * (d + 2) * 4 + 255) & ~(size_t)255);
 }
 
 template <int D, int NT, int CTAS>

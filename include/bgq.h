@@ -370,8 +370,9 @@ int32_t bgq_rope(const bgq_rope_plan* p, const uint16_t* x, int64_t x_stride, co
  *   k_sb, v_sb : bf16 (scale, bias) pairs [n_pages][kv_heads][page_size][head_dim/64][2].
  *   value = code*scale + bias, one pair for each 64 columns of a token's head
  *   (a page's head is a bgq_qmatrix of page_size rows).
- * head_dim 64, 128 or 256; page_size a multiple of 16; kv_heads <= 256; all
- * four arrays 16-byte aligned device memory. */
+ * head_dim 64, 128 or 256; page_size a multiple of 16; kv_heads <= 256;
+ * n_pages * kv_heads * (page_size / 16) below 2^31; all four arrays 16-byte
+ * aligned device memory. */
 typedef struct bgq_kv4_cache {
   uint32_t* k_q;
   uint16_t* k_sb;
@@ -398,7 +399,8 @@ typedef struct bgq_kv4_cache {
  * Rows of no sequence are left as they are. Tokens whose position is negative
  * or beyond the page list, or whose page number is outside 0..n_pages-1 (-1,
  * say, for a page given up) are absent: not written, read back as zeros, and
- * masked in attention. 1 <= batch <= 4096, rows may be 0. */
+ * masked in attention, and so are tokens from 2^31 - 65536 on. 1 <= batch <=
+ * 4096, rows may be 0. */
 typedef struct bgq_kv4_seqs {
   const int32_t* q_start;
   const int32_t* kv_len;
@@ -433,9 +435,13 @@ int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k,
  * of the sum of exponentials. A row that sees no token gets zeros and lse
  * -infinity. What a masked or absent token holds never reaches a row; a row
  * that sees a NaN gets NaN. q_heads a multiple of kv_heads, at most 64 times as many and
- * at most 1024.
+ * at most 1024; rows * (q_heads / kv_heads) below 2^31. out must not overlap
+ * q, nor lse anything.
  * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
- * max_q and heads). The same inputs give the same bits. */
+ * max_q and heads; a few MB for single tokens, up to 160 MB for prompts,
+ * whatever their length). Calls of any shapes may share one that is large
+ * enough for each, one after the other; calls of other entry points may not,
+ * unless it is zero-filled between. The same inputs give the same bits. */
 size_t bgq_kv4_attention_workspace_bytes(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, int32_t q_heads);
 int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const uint16_t* q, int64_t q_stride,
                           int32_t q_heads, float scale, int32_t causal, int32_t window, uint16_t* out,

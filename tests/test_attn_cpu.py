@@ -190,3 +190,24 @@ def test_binding_refuses_host_tensors(lib):
         lib.KV4Seqs(torch.zeros(1, dtype=i32))
     with pytest.raises(lib.BGQError):
         lib.bgq_rope(lib.RopePlan(64, 64, 1e4, [32]), torch.zeros(1, 1, 64, dtype=bf), torch.zeros(1, dtype=i32))
+
+
+def test_counts_beyond_32_bits(lib):
+    """What kernels would count past 2^31 is refused before anything is launched."""
+    for kw in [dict(n_pages=2 ** 30, page_size=32), dict(n_pages=2 ** 31 - 1, kv_heads=2), dict(n_pages=2 ** 20, page_size=2 ** 16)]:
+        for which in ("append", "read", "attention"):
+            assert _calls(lib, _cache(lib, **kw), _seqs(lib))[which]() == lib.ERR_UNSUPPORTED, kw
+    assert _calls(lib, _cache(lib, n_pages=2 ** 30 - 1), _seqs(lib, rows=0))["read"]() == lib.OK
+    c, s = _cache(lib), _seqs(lib, rows=2 ** 30, max_q=2 ** 30)
+    call = _calls(lib, c, s)["attention"]
+    assert call(wsb=1 << 62) == lib.ERR_UNSUPPORTED  # 2^30 rows of 4 query heads to a key head
+
+
+def test_attention_workspace_of_every_shape(lib):
+    """Its size does not follow the lengths, and rows only where a unit of the list is kept for 128 or 256 of them."""
+    size = lambda hq=8, **kw: lib.load().bgq_kv4_attention_workspace_bytes(  # noqa: E731
+        C.byref(_cache(lib, head_dim=kw.pop("d", 128))), C.byref(_seqs(lib, **kw)), hq)
+    for d in (64, 128, 256):
+        one, many, most = size(d=d, q_start=None, rows=3, max_q=1), size(d=d, rows=1 << 12, max_q=1 << 12), size(d=d, rows=1 << 20, max_q=1 << 20)
+        assert 4096 < one <= 16 << 20 and one < many <= 176 << 20
+        assert many < most <= many + (1 << 20) * 4 // 128 * 64 + 4096

@@ -541,3 +541,117 @@ def test_attention_block_of_a_decoder_layer(cuda_device):
         want = O.gemv(mats[1][0].numpy(), bits16(mats[1][1]), 4, f64(out[b].reshape(-1)))
         assert rel_l2(f64(y[b]), want) <= 2.0 ** -8
     assert torch.equal(res, h.to(cuda_device) + y.float())
+
+
+# ------------------------------------------------------------------ long lists, shared workspaces, hints
+LONG = [dict(kv=[40000], new=[1], hq=4, hkv=1, d=128), dict(kv=[30000], new=[1], hq=16, hkv=1, d=256), dict(kv=[17, 25000], new=[2, 3], hq=10, hkv=1, d=64),
+        dict(kv=[20000, 9], new=[3, 1], hq=8, hkv=1, d=128), dict(kv=[24000], new=[5], hq=8, hkv=1, d=256), dict(kv=[30000], new=[9], hq=8, hkv=1, d=64),
+        dict(kv=[26000, 70], new=[20, 33], hq=4, hkv=1, d=128)]
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 9001)])
+@pytest.mark.parametrize("kw", LONG)
+def test_units_cut_into_many_parts(cuda_device, kw, causal, window):
+    """One or two units that all CTAs share: their parts are joined in two levels (few rows) or by groups of threads."""
+    kw = dict(kw)
+    hq = kw.pop("hq")
+    c = Case(cuda_device, seed=11, page=64, **kw)
+    q = bf16(c.rng, c.rows, hq, c.d, dev=cuda_device, scale=1.5)
+    cache, seqs = c.cache(), c.seqs()
+    out, lse = lib.bgq_kv4_attention(cache, seqs, q, causal=causal, window=window, want_lse=True)
+    attn_close(c, q, out, lse, causal=causal, window=window)
+    again, _ = lib.bgq_kv4_attention(cache, seqs, q, causal=causal, window=window)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 1), (256, 1), (64, 40), (128, 40), (256, 40)])
+def test_lse_keeps_single_precision(cuda_device, d, new):
+    """Products of codes, scales and queries are exact, and a score is the sum of at most d/16 + 2d/64 + 4 <= 28 partial
+    sums in fp32, each off by 2^-23 of itself (truncation): independent errors of terms no larger than the sum add up to
+    sqrt(28) 2^-23 |score|, with scores of a few units against an lse of 5 or more below 2^-20 of it. A key rounded to fp16
+    would put 2^-12 / sqrt(80) of the score there."""
+    c = Case(cuda_device, [80, 75, 66, 71], [new] * 4, 2, d, 16, seed=12)
+    q = bf16(c.rng, c.rows, 8, d, dev=cuda_device, scale=1.5)
+    _, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+    want = c.oracle(q)[1]
+    assert rel_l2(f64(lse), want) <= 2.0 ** -20
+
+
+def test_one_workspace_for_all_shapes(cuda_device):
+    """Prompts, steps and drafted tokens of different sizes in turn through one workspace give the bits of fresh ones."""
+    calls = []
+    for i, (kv, new, hq, hkv, d) in enumerate([([300], [300], 8, 2, 128), ([5000], [1], 8, 1, 128), ([900, 70], [1, 1], 8, 2, 64), ([2000], [5], 16, 1, 256),
+                                               ([9000], [1], 16, 1, 256), ([130, 64], [100, 64], 4, 2, 64), ([8000, 3], [2, 3], 16, 1, 128)]):
+        c = Case(cuda_device, kv, new, hkv, d, 16, seed=20 + i)
+        calls.append((c.cache(), c.seqs(), bf16(c.rng, c.rows, hq, d, dev=cuda_device)))
+    want = [lib.bgq_kv4_attention(*c, want_lse=True) for c in calls]
+    ws = lib.workspace(max(lib.kv4_attention_workspace_bytes(c, s, q.shape[1]) for c, s, q in calls), cuda_device)
+    for _ in range(2):
+        for c, w in zip(calls, want):
+            out, lse = lib.bgq_kv4_attention(*c, want_lse=True, ws=ws)
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+    assert lib.read_device_status(ws) == lib.OK
+
+
+@pytest.mark.parametrize("hint", [1, 4, 1000])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_max_q_is_a_hint(cuda_device, d, hint):
+    """A sequence with more rows than max_q says is computed all the same, with fewer too."""
+    c = Case(cuda_device, [90, 200, 31], [33, 2, 31], 2, d, 48, seed=13)
+    q = bf16(c.rng, c.rows, 8, d, dev=cuda_device)
+    s = c.seqs()
+    out, lse = lib.bgq_kv4_attention(c.cache(), lib.KV4Seqs(s.kv_len, rows=c.rows, pages=s.pages, q_start=s.q_start, max_q=hint), q, want_lse=True)
+    attn_close(c, q, out, lse)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_no_sequence_has_a_row(cuda_device, max_q):
+    """Rows, but none of any sequence: nothing is written."""
+    c = Case(cuda_device, [50, 0, 20], [0, 0, 0], 2, 128, 16, behind=9)
+    q = bf16(c.rng, 9, 8, 128, dev=cuda_device)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((9, 8), 7.0, device=cuda_device)
+    s = c.seqs()
+    lib.bgq_kv4_attention(c.cache(), lib.KV4Seqs(s.kv_len, rows=9, pages=s.pages, q_start=s.q_start, max_q=max_q), q, out=out, lse=lse)
+    assert (out == 7.0).all() and (lse == 7.0).all()
+
+
+def test_largest_batch(cuda_device):
+    """4096 sequences of up to 40 tokens, single rows and (some without any) drafted ones."""
+    B = 4096
+    kv = [(7 * b) % 41 for b in range(B)]
+    for new in ([1] * B, [(b % 7) if kv[b] >= b % 7 else 0 for b in range(B)]):
+        c = Case(cuda_device, kv, new, 1, 64, 16, seed=14)
+        q = bf16(c.rng, c.rows, 8, 64, dev=cuda_device)
+        out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+        attn_close(c, q, out, lse)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls that run side by side, with workspaces of their own, give the bits of calls in turn."""
+    c = Case(cuda_device, [3000, 800], [1, 1], 2, 128, 16, seed=15)
+    p = Case(cuda_device, [700], [700], 2, 128, 16, seed=16)
+    jobs = [(x.cache(), x.seqs(), bf16(x.rng, x.rows, 8, 128, dev=cuda_device)) for x in (c, p)]
+    want = [lib.bgq_kv4_attention(*j)[0] for j in jobs]
+    ws = [lib.workspace(lib.kv4_attention_workspace_bytes(j[0], j[1], 8), cuda_device) for j in jobs]
+    outs = [[torch.empty_like(j[2]) for _ in range(8)] for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, w, o, s in zip(jobs, ws, outs, streams):
+            with torch.cuda.stream(s):
+                lib.bgq_kv4_attention(*j, out=o[i], ws=w)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for x in o:
+            assert torch.equal(x, w)
+
+
+def test_page_listed_twice_and_short_lists(cuda_device):
+    """Two sequences may read the same pages (a shared prefix); tokens beyond a page list are absent."""
+    c = Case(cuda_device, [64, 64, 70], [1, 1, 20], 2, 128, 16, seed=17)
+    c.pages[1] = c.pages[0]
+    c.kv[2] = 100  # its list has room for 80: rows stand at 80 .. 99
+    q = bf16(c.rng, c.rows, 8, 128, dev=cuda_device)
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+    attn_close(c, q, out, lse)
