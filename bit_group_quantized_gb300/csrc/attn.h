@@ -104,8 +104,8 @@ struct AttnArgs {
   float scale;
   void* ws;
 };
-size_t attn_workspace_bytes(int batch, int rows, int max_q, int q_heads, int kv_heads, int head_dim);
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+size_t attn_workspace_bytes(const bgq_kv4_cache& c, const bgq_kv4_seqs& s, int q_heads);
+cudaError_t launch_attn(const AttnArgs& a, const bgq_kv4_seqs& s, cudaStream_t stream);
 
 size_t split_workspace_bytes(int batch, int max_q, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);

@@ -151,7 +151,7 @@ static int check_heads(const bgq_kv4_cache* c, int32_t q_heads) {
 
 size_t bgq_kv4_attention_workspace_bytes(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, int32_t q_heads) {
   if (check_cache(c) || check_seqs(s) || check_heads(c, q_heads)) return 0;
-  return attn_workspace_bytes(s->batch, s->rows, s->max_q, q_heads, c->kv_heads, c->head_dim);
+  return attn_workspace_bytes(*c, *s, q_heads);
 }
 
 int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const uint16_t* q, int64_t q_stride,
@@ -163,7 +163,7 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   if ((r = check_rows(q, q_stride, width)) || (r = check_rows(out, out_stride, width))) return r;
   if (!al(lse, 4) || !isfinite(scale) || window < 0) return BGQ_ERR_INVALID_ARG;
   if (!ws || !al(ws, 256) ||
-      ws_bytes < attn_workspace_bytes(s->batch, s->rows, s->max_q, q_heads, c->kv_heads, c->head_dim))
+      ws_bytes < attn_workspace_bytes(*c, *s, q_heads))
     return BGQ_ERR_WORKSPACE;
   if ((int64_t)s->rows * (q_heads / c->kv_heads) > INT32_MAX) return BGQ_ERR_UNSUPPORTED;
   if (s->rows == 0) return BGQ_OK;
@@ -182,7 +182,7 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   a.page_shift = (c->page_size & (c->page_size - 1)) ? -1 : __builtin_ctz(c->page_size);
   a.scale = scale;
   a.ws = ws;
-  return cuda_status(launch_attn(a, st(stream)));
+  return cuda_status(launch_attn(a, *s, st(stream)));
 }
 
 }  // extern "C"

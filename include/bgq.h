@@ -438,7 +438,7 @@ int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k,
  * at most 1024; rows * (q_heads / kv_heads) below 2^31. out must not overlap
  * q, nor lse anything.
  * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
- * max_q and heads; a few MB for single tokens, up to 160 MB for prompts,
+ * max_q, max_pages and heads; a few MB for single tokens, up to 160 MB for prompts,
  * whatever their length). Calls of any shapes may share one that is large
  * enough for each, one after the other; calls of other entry points may not,
  * unless it is zero-filled between. The same inputs give the same bits. */

@@ -110,9 +110,10 @@ def test_rope_gradient(cuda_device):
 
 # ------------------------------------------------------------------ the cache
 class Case:
-    """Sequences with their tokens already in a cache of randomly placed pages."""
+    """Sequences with their tokens already in a cache of randomly placed pages; their page lists have room for `room` tokens
+    or more (those behind a sequence's own are -1)."""
 
-    def __init__(self, dev, kv, new, hkv, d, page, seed=0, spare=2, pages=True, gap=0, behind=0):
+    def __init__(self, dev, kv, new, hkv, d, page, seed=0, spare=2, pages=True, gap=0, behind=0, room=2048):
         rng = torch.Generator().manual_seed(seed)
         self.dev, self.kv, self.new, self.d, self.hkv = dev, kv, new, d, hkv
         B = len(kv)
@@ -120,7 +121,7 @@ class Case:
             need = [max(-(-n // page), 0) for n in kv]
             self.n_pages = sum(need) + spare
             order = torch.randperm(self.n_pages, generator=rng).tolist()
-            table = np.full((B, max(max(need), 1)), -1, dtype=np.int32)
+            table = np.full((B, max(max(need), 1, -(-room // page))), -1, dtype=np.int32)
             for b, n in enumerate(need):
                 for i in range(n):
                     table[b, i] = order.pop()
@@ -399,7 +400,7 @@ def test_lengths_grow_under_a_captured_graph(cuda_device):
     """rope, append and attention of a decode step captured once and replayed while the lengths on the device grow; two
     graphs with workspaces of their own replayed in turn give the bits of direct calls."""
     B, hq, hkv, d, page = 3, 8, 2, 128, 16
-    c = Case(cuda_device, [30, 5, 47], [1, 1, 1], hkv, d, page, spare=9)
+    c = Case(cuda_device, [30, 5, 47], [1, 1, 1], hkv, d, page, spare=9, room=0)
     table = np.full((B, 6), -1, dtype=np.int32)
     free = [p for p in range(c.n_pages) if p not in c.pages]
     table[:, :c.pages.shape[1]] = c.pages
@@ -577,6 +578,27 @@ def test_lse_keeps_single_precision(cuda_device, d, new):
     assert rel_l2(f64(lse), want) <= 2.0 ** -20
 
 
+SHORT = [dict(kv=[200], new=[200], hq=8, hkv=2, d=128, page=64), dict(kv=[311, 150, 129], new=[150, 1, 129], hq=4, hkv=1, d=128, page=16),
+         dict(kv=[160, 1000], new=[96, 3], hq=10, hkv=2, d=64, page=32), dict(kv=[140, 260, 0], new=[100, 33, 2], hq=6, hkv=1, d=256, page=64),
+         dict(kv=[270], new=[270], hq=3, hkv=1, d=128, page=16, pages=False), dict(kv=[1024, 5], new=[9, 5], hq=64, hkv=8, d=64, page=16),
+         dict(kv=[1040, 5], new=[9, 5], hq=64, hkv=8, d=64, page=16), dict(kv=[512], new=[20], hq=8, hkv=8, d=256, page=32)]
+
+
+@pytest.mark.parametrize("causal,window", MASKS)
+@pytest.mark.parametrize("kw", SHORT)
+def test_many_rows_of_short_page_lists(cuda_device, kw, causal, window):
+    """Page lists just long enough: where they hold little, many rows take another kernel than with long ones."""
+    kw = dict(kw)
+    hq = kw.pop("hq")
+    c = Case(cuda_device, seed=18, room=0, gap=1, behind=1, **kw)
+    q = bf16(c.rng, c.rows, hq, c.d, dev=cuda_device, scale=1.5)
+    out, lse = torch.full_like(q, 7.0), torch.full((c.rows, hq), 7.0, device=cuda_device)
+    lib.bgq_kv4_attention(c.cache(), c.seqs(), q, causal=causal, window=window, out=out, lse=lse)
+    live = attn_close(c, q, out, lse, causal=causal, window=window)
+    dead = torch.from_numpy(~live).to(cuda_device)
+    assert (out[dead] == 7.0).all() and (lse[dead] == 7.0).all()
+
+
 def test_one_workspace_for_all_shapes(cuda_device):
     """Prompts, steps and drafted tokens of different sizes in turn through one workspace give the bits of fresh ones."""
     calls = []
@@ -649,7 +671,7 @@ def test_two_streams_at_once(cuda_device):
 
 def test_page_listed_twice_and_short_lists(cuda_device):
     """Two sequences may read the same pages (a shared prefix); tokens beyond a page list are absent."""
-    c = Case(cuda_device, [64, 64, 70], [1, 1, 20], 2, 128, 16, seed=17)
+    c = Case(cuda_device, [64, 64, 70], [1, 1, 20], 2, 128, 16, seed=17, room=0)
     c.pages[1] = c.pages[0]
     c.kv[2] = 100  # its list has room for 80: rows stand at 80 .. 99
     q = bf16(c.rng, c.rows, 8, 128, dev=cuda_device)
