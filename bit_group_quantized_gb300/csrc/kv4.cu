@@ -8,8 +8,8 @@
 // of a step away from a half.
 //
 // Both kernels are bound by memory (2 bytes of bf16 and 0.56 bytes of cache a
-// value), and nearly as much by the instructions that place the codes: 18003 rows of 8 heads of 128 written
-// and read back in 32.1 us (5.9 TB/s of the 189 MB both move; issue slots 60 % full in the writing half), 74000 tokens
+// value), and nearly as much by the instructions that place the codes: 15349 rows of 8 heads of 128 written
+// and read back in 32.1 us (5.0 TB/s of the 161 MB both move; issue slots 60 % full in the writing half), 78514 tokens
 // of 2 heads of 256 read in 35.8 us (5.7 TB/s). Four lanes share a group, 16 values a lane in two 16-byte loads (the
 // reductions over a group then cost two shuffles, and the scale's division
 // is spread over 16 values); a lane's codes are two words of the group.
@@ -21,8 +21,8 @@ namespace bgq {
 
 constexpr int kKvThreads = 256;
 // A thread's unit is 16 values of a token's head, of K and of V; a block looks its rows' places up once and takes this many rounds of
-// units (18003 rows of 8 heads of 128 written and read back: 1 round 33.6 us, 2 32.1, 4 34.1, the blocks then being few; a read of
-// 74000 tokens of 2 heads of 256: 40.8, 36.2, 35.9).
+// units (15349 rows of 8 heads of 128 written and read back: 1 round 33.6 us, 2 32.1, 4 34.1, the blocks then being few; a read of
+// 78514 tokens of 2 heads of 256: 40.8, 36.2, 35.9).
 constexpr int kKvRounds = 2;
 constexpr int kKvMaxRows = 256;
 
