@@ -188,8 +188,13 @@ struct Walk {
     }
     if (h >= a.c.kv_heads) {
       h = 0;
-      do q = seq_tiles<TT, C>(a, ++b);
-      while (q.rtiles == 0 && b + 1 < a.v.batch);
+      q = seq_tiles<TT, C>(a, ++b);
+      while (q.rtiles == 0 && b + 1 < a.v.batch) {  // sequences without rows: 32 are looked at together
+        const int ahead = b + 1 + (threadIdx.x & 31);
+        const uint32_t some = __ballot_sync(kFull, ahead < a.v.batch && kv4_span(a.v, ahead).q_len > 0);
+        b = some ? b + __ffs(some) : min(b + 32, a.v.batch - 1);
+        if (some || b + 1 == a.v.batch) q = seq_tiles<TT, C>(a, b);
+      }
     }
     i1 = (int)min((long long)q.tiles, x1 - x);
   }

@@ -649,6 +649,16 @@ def test_largest_batch(cuda_device):
         attn_close(c, q, out, lse)
 
 
+@pytest.mark.parametrize("new", [1, 5, 40])
+def test_few_of_many_sequences_have_rows(cuda_device, new):
+    """Seven of 3000 sequences, runs of up to a thousand without rows between them."""
+    at = [3, 4, 40, 900, 1901, 1933, 2999]
+    c = Case(cuda_device, [1100 + 37 * (b % 5) if b in at else b % 3 for b in range(3000)], [new if b in at else 0 for b in range(3000)], 2, 64, 16, seed=19)
+    q = bf16(c.rng, c.rows, 16, 64, dev=cuda_device)
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+    attn_close(c, q, out, lse)
+
+
 def test_two_streams_at_once(cuda_device):
     """Calls that run side by side, with workspaces of their own, give the bits of calls in turn."""
     c = Case(cuda_device, [3000, 800], [1, 1], 2, 128, 16, seed=15)
