@@ -687,3 +687,63 @@ def test_page_listed_twice_and_short_lists(cuda_device):
     q = bf16(c.rng, c.rows, 8, 128, dev=cuda_device)
     out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
     attn_close(c, q, out, lse)
+
+
+# ------------------------------------------------------------------ rows far apart
+FAR = (1 << 31) + 4096  # values from a row to the next: past 32 bits in values, and in bytes
+
+
+def far_rows(x):
+    """The two rows of x, FAR values apart."""
+    big = torch.empty(FAR + x[0].numel(), dtype=BF, device=x.device)
+    far = big.as_strided(x.shape, (FAR, x.shape[2], 1))
+    far.copy_(x)
+    return far
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_rope_rows_far_apart(cuda_device, pairs):
+    x = bf16(torch.Generator().manual_seed(30), 2, 5, 64, dev=cuda_device)
+    plan, pos = lib.RopePlan(64, 48, 1e4, [24], pairs=pairs), ints([2 ** 31 - 1, -7], cuda_device)
+    want = lib.bgq_rope(plan, x, pos)
+    far = far_rows(x)
+    lib.bgq_rope(plan, far, pos, y=far)
+    assert torch.equal(far, want)
+
+
+@pytest.mark.parametrize("d,max_q,room", [(64, 1, 2048), (128, 1, 2048), (256, 1, 2048), (128, 64, 2048), (256, 64, 2048)])
+def test_attention_rows_far_apart(cuda_device, d, max_q, room):
+    c = Case(cuda_device, [90, 41], [1, 1], 2, d, 16, seed=31, room=room)
+    q, k = bf16(c.rng, 2, 8, d, dev=cuda_device), bf16(c.rng, 2, 2, d, dev=cuda_device)
+    s = c.seqs()
+    seqs = lib.KV4Seqs(s.kv_len, rows=2, pages=s.pages, q_start=s.q_start, max_q=max_q)
+    near, away = c.cache(), c.cache()
+    lib.bgq_kv4_append(near, seqs, k, k)
+    fk = far_rows(k)
+    lib.bgq_kv4_append(away, seqs, fk, fk)
+    for name in ("k_q", "k_sb", "v_q", "v_sb"):
+        assert torch.equal(getattr(near, name), getattr(away, name))
+    back = [far_rows(torch.zeros_like(k)) for _ in range(2)]
+    lib.bgq_kv4_read(away, seqs, *back)
+    for x, y in zip(back, lib.bgq_kv4_read(near, seqs)):
+        assert torch.equal(x, y)
+    want, _ = lib.bgq_kv4_attention(near, seqs, q)
+    out = far_rows(torch.zeros_like(q))
+    lib.bgq_kv4_attention(away, seqs, far_rows(q), out=out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_around_a_large_offset(cuda_device, d, new):
+    """Keys of 60 and a little: scores of thousands whose differences are small. They are off by 2^-22 of the partial sums
+    (scale * sum|q k|), probabilities by as much, and by the kernels' own 2^-10."""
+    c = Case(cuda_device, [150, 77], [new, new], 1, d, 16, seed=32)
+    code, scale, bias, _ = A.kv4_quantise(60 + 0.5 * np.random.default_rng(1).standard_normal((c.n_pages, 1, 16, d)))
+    c.np[0], c.np[1] = A.kv4_pack(code).astype(np.uint32), np.stack([O.f64_to_bf16_bits(scale), O.f64_to_bf16_bits(bias)], -1)
+    q = bf16(c.rng, c.rows, 8, d, dev=cuda_device)
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+    o, l, a, s = c.oracle(q)
+    e = 2.0 ** -22 * s * (d / 16 + 8)  # every one of the d/16 + 8 partial sums may be off by that
+    assert (np.abs(f64(lse) - l) <= e + 2.0 ** -18 * np.abs(l)).all()
+    assert (np.abs(f64(out) - o) <= 2.0 ** -8 * np.abs(o) + (2 * e + 2.0 ** -9)[..., None] * a).all()
