@@ -706,7 +706,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int mt = (wk.n0 + it - wk.i0) & (kMetaTiles - 1);
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
-        const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && !fresh && e_run == 0;
+        const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && e_run == 0;
+        if (plain) fresh = false;
         // Every row sees every token, and no factor but the row's: 64 tokens at a time. The probabilities are taken with the
         // maximum so far while the scores' own is found; where that is too far above (seldom), it is raised and they are taken again.
 #pragma unroll 1
