@@ -101,6 +101,8 @@ struct AttnArgs {
   long long q_stride, out_stride;
   int q_heads, causal, window, max_q;
   int page_shift;  // log2 of the page size, or -1
+  int group;       // q_heads / kv_heads
+  uint64_t group_inv;  // ceil(2^64 / group), 0 for one head
   float scale;
   void* ws;
 };

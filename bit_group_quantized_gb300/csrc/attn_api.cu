@@ -180,6 +180,8 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   a.window = window;
   a.max_q = s->max_q;
   a.page_shift = (c->page_size & (c->page_size - 1)) ? -1 : __builtin_ctz(c->page_size);
+  a.group = q_heads / c->kv_heads;
+  a.group_inv = a.group > 1 ? ~(uint64_t)0 / a.group + 1 : 0;
   a.scale = scale;
   a.ws = ws;
   return cuda_status(launch_attn(a, *s, st(stream)));

@@ -90,14 +90,18 @@ struct __align__(16) PrUnit {
   int b, rt, tiles, begin;
   Span sp;
 };
+// n / (q_heads / kv_heads), n below 2^31: by ceil(2^64 / .), whose excess n times stays below 2^64.
+__device__ __forceinline__ int pr_by_group(const AttnArgs& a, int n) {
+  return a.group_inv ? (int)__umul64hi((unsigned long long)n, a.group_inv) : n;
+}
 // A sequence's row tiles, and the tokens of one of them.
 __device__ __forceinline__ int pr_row_tiles(const AttnArgs& a, const Span& sp, int rows_unit) {
-  return (min(sp.q_len, a.v.rows) * (a.q_heads / a.c.kv_heads) + rows_unit - 1) / rows_unit;
+  return (min(sp.q_len, a.v.rows) * a.group + rows_unit - 1) / rows_unit;
 }
 __device__ __forceinline__ void pr_tokens(const AttnArgs& a, PrUnit& un, int rows_unit) {
-  const int group = a.q_heads / a.c.kv_heads, pos0 = un.sp.kv_len - un.sp.q_len;
-  const int j0 = un.rt * rows_unit / group;
-  const int j1 = min(un.sp.q_len - 1, (un.rt * rows_unit + rows_unit - 1) / group);
+  const int pos0 = un.sp.kv_len - un.sp.q_len;
+  const int j0 = pr_by_group(a, un.rt * rows_unit);
+  const int j1 = min(un.sp.q_len - 1, pr_by_group(a, un.rt * rows_unit + rows_unit - 1));
   un.begin = a.window > 0 ? min(max(0, pos0 + j0 - a.window + 1), un.sp.held) / 16 * 16 : 0;  // 16 tokens lie in one page
   const int end = a.causal ? min(un.sp.held, pos0 + j1 + 1) : un.sp.held;
   un.tiles = max(1, (end - un.begin + kPrTok - 1) / kPrTok);  // at least one: rows that see no token are written too
@@ -550,7 +554,7 @@ __device__ __forceinline__ PrRowOf pr_row(const AttnArgs& a, const PrWalk<D>& wk
   PrRowOf r;
   r.own = col < cols;
   const int cc = r.own ? col : cols - 1;  // rows behind the last see what it sees, and are dropped
-  const int j = cc / group;
+  const int j = pr_by_group(a, cc);
   r.head = wk.h * group + cc - j * group;
   r.row = sp.first + j;
   r.ok = r.own && r.row >= 0 && r.row < a.v.rows;
@@ -593,15 +597,18 @@ __device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char
     uint2 x = {};
     if (g < D / kGroup) {
       float sum[4] = {};
-#pragma unroll 4
-      for (int n = g * 8; n < g * 8 + 8; ++n) {
+      uint4 v[8];  // all loads ahead of the stores
+#pragma unroll
+      for (int n = 0; n < 8; ++n) v[n] = *chunk(g * 8 + n);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
         float f[8];
-        unpack_bf16x8(*chunk(n), f);
+        unpack_bf16x8(v[n], f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= up;
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum[k] += f[k] + f[k + 4];
-        *chunk(n) = make_uint4(pr_half2(f[0], f[4]), pr_half2(f[1], f[5]), pr_half2(f[2], f[6]), pr_half2(f[3], f[7]));
+        *chunk(g * 8 + n) = make_uint4(pr_half2(f[0], f[4]), pr_half2(f[1], f[5]), pr_half2(f[2], f[6]), pr_half2(f[3], f[7]));
       }
       const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);  // below 2^11
       const float top = __half2float(__float2half_rn(all)), rest = all - top;
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   // every CTA's share holds a tile, as its length is above kUnitCost
   const long long ctas = min((long long)gridDim.x, total / (kUnitCost + 1));
   const int cta = blockIdx.x;
-  const int group = a.q_heads / a.c.kv_heads;
+  const int group = a.group;
   PrWalk<D> wk;
   wk.i0 = wk.i1 = 0;
   if (cta < ctas) wk.start(a, w, total * cta / ctas, total * (cta + 1) / ctas, sum, units);
