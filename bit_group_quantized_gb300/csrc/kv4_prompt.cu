@@ -285,6 +285,18 @@ __device__ __forceinline__ void pr_scale_p(uint32_t t, float f) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
   }
 }
+// Lanes m apart: the lower one's b for the upper one's a.
+__device__ __forceinline__ void pr_swap(uint4& a, uint4& b, int m, int lane) {
+  const bool upper = lane & m;
+  auto one = [&](uint32_t& x, uint32_t& y) {
+    const uint32_t got = __shfl_xor_sync(kFull, upper ? x : y, m);
+    if (upper) x = got; else y = got;
+  };
+  one(a.x, b.x);
+  one(a.y, b.y);
+  one(a.z, b.z);
+  one(a.w, b.w);
+}
 // Two fp32 values in one register pair, one instruction for both.
 __device__ __forceinline__ uint64_t pr_pair(float a, float b) {
   uint64_t d;
@@ -883,7 +895,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       tc_fence_after();
       float l = poison & 1 ? NAN : l0 + l1;
       const float unit = exp2i(e_run);
-      uint16_t* out = a.out + (long long)(ok ? row : 0) * a.out_stride + head * D;
+      const long long out_at = ok ? (long long)row * a.out_stride + head * D : -1;
       if (!dead) {
         const float inv = l == 0.f ? 0.f : unit / l;
 #pragma unroll 1
@@ -896,12 +908,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
           if (whole) {
-            if (ok) {
+            // Columns come as 0 4 1 5 2 6 3 7. Four lanes exchange their 16-byte pieces, so that together they write 64 bytes of a
+            // row at a time, of eight rows a warp (4096 tokens causal: 147.8 us, 149.0 with each lane writing its own row).
+            uint4 w4[4];
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) {  // columns come as 0 4 1 5 2 6 3 7
-                auto b2 = [&](int p, int q) { return pr_bf2(__uint_as_float(v[x + p]), __uint_as_float(v[x + q])); };
-                *reinterpret_cast<uint4*>(out + d + x) = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
-              }
+            for (int x = 0; x < 4; ++x) {
+              auto b2 = [&](int p, int q) { return pr_bf2(__uint_as_float(v[x * 8 + p]), __uint_as_float(v[x * 8 + q])); };
+              w4[x] = make_uint4(b2(0, 2), b2(4, 6), b2(1, 3), b2(5, 7));
+            }
+            pr_swap(w4[0], w4[1], 1, lane);
+            pr_swap(w4[2], w4[3], 1, lane);
+            pr_swap(w4[0], w4[2], 2, lane);
+            pr_swap(w4[1], w4[3], 2, lane);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const long long at = __shfl_sync(kFull, out_at, lane & ~3 | x);
+              if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + d + (lane & 3) * 8) = w4[x];
             }
           } else {
 #pragma unroll
