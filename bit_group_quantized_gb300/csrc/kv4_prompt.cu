@@ -24,8 +24,8 @@
 // whose O fills tensor memory) S is double-buffered.
 // What bounds it: a tile's chain of scores, softmax and product, which two row tiles fill by turns, and beside it shared
 // memory, which the matrix instructions read at its full rate while they take Q and K from it (a tile of 2 x 128 rows
-// takes 3600 cycles, of which the matrix instructions take 2200). 4096 tokens causal, 32 heads of 128 over 8: 157 us,
-// 880 TFLOP/s; three chunks of 700 to 1100 rows behind up to 16000 tokens: 317 us, 1140 TFLOP/s (58 % of the matrix rate
+// takes 3600 cycles, of which the matrix instructions take 2200). 4096 tokens causal, 32 heads of 128 over 8: 147 us,
+// 935 TFLOP/s; three chunks of 700 to 1100 rows behind up to 16000 tokens: 303 us, 1190 TFLOP/s (61 % of the matrix rate
 // measured with a library product); 24 sequences of five rows, 16 heads of 256 over 2: 41 us, where dequantisation has
 // too few rows to serve (5000 cycles a tile).
 // The maximum is raised, and O rescaled, only where a row's scores pass it by
@@ -59,7 +59,7 @@ constexpr long long kPrTimeoutNs = 1000000000ll;
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSeqs = 4096;
 // What bringing a unit's queries and writing its rows costs, in tiles: CTAs with many short units take fewer tiles (4096
-// tokens causal: 186, 166, 150, 148 us with 1, 2, 3, 4; 24 sequences of five rows, which 4 serves worse: 39.5 with 3, 41 with 4).
+// tokens causal: 157, 147, 145 us with 2, 3, 4; 24 sequences of five rows, which 4 serves worse: 42.1, 40.8, 43.4).
 constexpr int kUnitCost = 3;
 constexpr int kPanel = 128 * 128;  // bytes of an operand panel: 64 columns in 128-byte rows, 128-byte swizzle, 128 rows
 constexpr int kExtra = 128 * 32;   // bytes of an operand's 16 extra columns: 8 x 8 cores, unswizzled
