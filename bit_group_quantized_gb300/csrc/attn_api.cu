@@ -165,7 +165,7 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
   if (!ws || !al(ws, 256) ||
       ws_bytes < attn_workspace_bytes(*c, *s, q_heads))
     return BGQ_ERR_WORKSPACE;
-  if ((int64_t)s->rows * (q_heads / c->kv_heads) > INT32_MAX) return BGQ_ERR_UNSUPPORTED;
+  if ((int64_t)s->rows * (q_heads / c->kv_heads) > kMaxTokens) return BGQ_ERR_UNSUPPORTED;  // kernels round it up to a tile
   if (s->rows == 0) return BGQ_OK;
   AttnArgs a;
   a.c = *c;

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
 template <typename... KArgs, typename... Args>
 static cudaError_t kv_launch(void (*kern)(KArgs...), const KvGeo& g, int rows, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + g.rb - 1) / g.rb, (g.units_row + g.chunk - 1) / g.chunk);
+  cfg.gridDim = dim3((unsigned)(((long long)rows + g.rb - 1) / g.rb), (g.units_row + g.chunk - 1) / g.chunk);
   cfg.blockDim = dim3(kKvThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

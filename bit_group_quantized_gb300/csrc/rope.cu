@@ -144,7 +144,7 @@ cudaError_t launch_rope(const bgq_rope_plan& p, const uint16_t* x, long long x_s
   g.m_upt = (uint32_t)((0x100000000ull + g.upt - 1) / g.upt);
   g.m_tok = (uint32_t)((0x100000000ull + g.units_tok - 1) / g.units_tok);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((tokens + g.tb - 1) / g.tb, (g.units_tok + g.chunk - 1) / g.chunk);
+  cfg.gridDim = dim3((unsigned)(((long long)tokens + g.tb - 1) / g.tb), (g.units_tok + g.chunk - 1) / g.chunk);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)g.tb * half * sizeof(float2);
   cfg.stream = s;

@@ -435,7 +435,7 @@ int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k,
  * of the sum of exponentials. A row that sees no token gets zeros and lse
  * -infinity. What a masked or absent token holds never reaches a row; a row
  * that sees a NaN gets NaN. q_heads a multiple of kv_heads, at most 64 times as many and
- * at most 1024; rows * (q_heads / kv_heads) below 2^31. out must not overlap
+ * at most 1024; rows * (q_heads / kv_heads) below 2^31 - 65536. out must not overlap
  * q, nor lse anything.
  * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
  * max_q, max_pages and heads; a few MB for single tokens, up to 160 MB for prompts,

@@ -201,6 +201,8 @@ def test_counts_beyond_32_bits(lib):
     c, s = _cache(lib), _seqs(lib, rows=2 ** 30, max_q=2 ** 30)
     call = _calls(lib, c, s)["attention"]
     assert call(wsb=1 << 62) == lib.ERR_UNSUPPORTED  # 2^30 rows of 4 query heads to a key head
+    s = _seqs(lib, rows=2 ** 29 - 2 ** 13, max_q=1)
+    assert _calls(lib, c, s)["attention"](wsb=1 << 62) == lib.ERR_UNSUPPORTED  # rounded up to tiles it would pass 2^31
 
 
 def test_attention_workspace_of_every_shape(lib):
