@@ -34,6 +34,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "split_join.h"
 
 namespace bgq {
 
@@ -820,22 +821,19 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
     }
     if (!whole) {  // the last CTA to arrive joins the unit's parts
       const long long u0 = wk.x, u1 = u0 + wk.q.tiles - 1;  // the places of the unit's first and last tile
-      const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)(((u1 + 1) * ctas - 1) / total);
-      // Many and large parts are joined by eights first, each eight by its own last CTA: one SM alone reads half a MB too
-      // slowly (76 parts of 16 columns of 256: 49 us for the call with one join, 40 with two; 38 parts of 4 columns of
-      // 128: 44.5 with one, 46.9 with two).
-      const int np = c1 - c0 + 1;
-      int first = 0, step = 1, n = np, *count = ws.count + c0;
-      bool top_level = np * ncol * D <= 1 << 17;
-      if (!top_level) {
-        first = (cta - c0) / 8 * 8;
-        n = min(8, np - first);
-        count = ws.count + gridDim.x + c0 + first;
+      const int c0 = split_cta(u0, ctas, total), c1 = split_cta(u1, ctas, total);
+      bool top_level = !split_two_levels(c1 - c0 + 1, ncol, D);
+      SplitJoin join = top_level ? split_all(c0, c1, false) : split_eight(c0, c1, cta, gridDim.x);
+      if (join.counter < 0) {  // an eight of one part is joined as it stands
+        join = split_all(c0, c1, true);
+        top_level = true;
       }
       for (;;) {
+        const int first = join.first, step = join.step, n = join.n;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
+          int* const count = ws.count + join.counter;
           const int last = atomicAdd(count, 1) == n - 1;
           if (last) *count = 0;
           s_last = last;
@@ -909,10 +907,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
           }
         }
         if (top_level) break;
-        first = 0;
-        step = 8;
-        n = (np + 7) / 8;
-        count = ws.count + c0;
+        join = split_all(c0, c1, true);
         top_level = true;
       }
     }
