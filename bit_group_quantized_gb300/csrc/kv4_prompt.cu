@@ -48,6 +48,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4_seen.h"
 #include "tc.cuh"
 
 namespace bgq {
@@ -102,8 +103,8 @@ __device__ __forceinline__ void pr_tokens(const AttnArgs& a, PrUnit& un, int row
   const int pos0 = un.sp.kv_len - un.sp.q_len;
   const int j0 = pr_by_group(a, un.rt * rows_unit);
   const int j1 = min(un.sp.q_len - 1, pr_by_group(a, un.rt * rows_unit + rows_unit - 1));
-  un.begin = a.window > 0 ? min(max(0, pos0 + j0 - a.window + 1), un.sp.held) / 16 * 16 : 0;  // 16 tokens lie in one page
-  const int end = a.causal ? min(un.sp.held, pos0 + j1 + 1) : un.sp.held;
+  un.begin = min(kv4_first_seen(pos0 + j0, a.window), un.sp.held) / 16 * 16;  // 16 tokens lie in one page
+  const int end = kv4_end_seen(pos0 + j1, un.sp.kv_len, un.sp.held, a.causal);
   un.tiles = max(1, (end - un.begin + kPrTok - 1) / kPrTok);  // at least one: rows that see no token are written too
 }
 struct PrPlan {  // at the start of the workspace, behind the control block
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       const int row = rw.row, pos = rw.pos, head = rw.head;
       const Span& sp = wk.un.sp;
       const bool own = !none && rw.own, ok = rw.ok;
-      const int hi = min(sp.held, a.causal ? pos + 1 : sp.kv_len), lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int hi = kv4_end_seen(pos, sp.kv_len, sp.held, a.causal), lo = kv4_first_seen(pos, a.window);
       const int hi_min = __reduce_min_sync(kFull, hi), hi_max = __reduce_max_sync(kFull, hi);
       const int lo_min = __reduce_min_sync(kFull, lo), lo_max = __reduce_max_sync(kFull, lo);
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going

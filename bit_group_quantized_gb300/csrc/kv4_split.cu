@@ -34,6 +34,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4_seen.h"
 #include "split_join.h"
 
 namespace bgq {
@@ -163,7 +164,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, int b) {
   SeqTiles s;
   s.sp = kv4_span(a.v, b);
   const int pos0 = s.sp.kv_len - s.sp.q_len;
-  s.begin = a.window > 0 ? max(0, pos0 - a.window + 1) / TT * TT : 0;
+  s.begin = min(kv4_first_seen(pos0, a.window), s.sp.held) / TT * TT;  // the look-up of pages runs up to 4064 tokens ahead of it
   s.tiles = max(1, (s.sp.held - s.begin + TT - 1) / TT);
   s.rtiles = (min(s.sp.q_len, a.v.rows) * (a.q_heads / a.c.kv_heads) + C - 1) / C;
   return s;
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
         const int pos = pos0 + jj;
         // columns behind the last see what the first one sees, and are dropped at the end
         const int p2 = cc < ncol ? pos : pos0 + col0 / group;
-        A.hi[n][k] = min(wk.q.sp.held, a.causal ? p2 + 1 : wk.q.sp.kv_len);
-        A.lo[n][k] = a.window > 0 ? p2 - a.window + 1 : 0;
+        A.hi[n][k] = kv4_end_seen(p2, wk.q.sp.kv_len, wk.q.sp.held, a.causal);
+        A.lo[n][k] = kv4_first_seen(p2, a.window);
       }
     }
     if (P::kQs) __syncthreads();

@@ -3,11 +3,7 @@
 // the arithmetic as the kernel runs it.
 #pragma once
 
-#ifdef __CUDACC__
-#define BGQ_HOST_DEVICE __host__ __device__ __forceinline__
-#else
-#define BGQ_HOST_DEVICE inline
-#endif
+#include "host_device.h"
 
 namespace bgq {
 
