@@ -31,10 +31,13 @@
 // The maximum is raised, and O rescaled, only where a row's scores pass it by
 // 2^8: P then reaches 2^8 at most, far inside fp16.
 //
-// Half precision's range: queries are scaled by a power of two per row, K and V
-// by one per 32 tokens where they leave [2^-6, 2^15) (else none); the softmax
-// undoes K's in the score's factor and V's in P. A key or value pair that is not
-// finite is stored as zeros, and the rows that see it are made NaN at the end.
+// Half precision's range: queries are scaled by a power of two per row, K by
+// one per 32 tokens where it leaves [2^-8, 2^15) (else none), which the softmax undoes in the score's factor. V is
+// scaled by one of three powers of two per 32 tokens, O's unit. Tokens that it does not fit (a group far smaller or larger than a
+// value's usual size) and blocks of another unit than O's are left out of the product, and their softmax thread adds p V in fp32,
+// slowly: no row's result depends on the size of values that it does not see, or of another group's. This costs ordinary values
+// 1 to 3 % (4096 tokens causal: 151.6 us, 147.6 with one exponent for all that a row had met, which lost small ones beside large).
+// A key or value pair that is not finite is stored as zeros, and the rows that see it are made NaN at the end.
 //
 // All (unit, key head, 128 tokens) triples form one list, which k_prompt_plan lays out from
 // the lengths on the device; every CTA takes an equal, contiguous share, and units cut by a
@@ -394,13 +397,21 @@ __device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t off, uint32_t s2
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The values of a block of 32 tokens are held in fp16 divided by 2^E, one of three E by a rule on the pairs alone: a token fits
+// where each of its groups' 16 |s| + |b| (which no value passes) is zero or in [2^(E - 8), 2^(E + 15)); there fp16 keeps
+// 2^-17 of a group's size, whatever the sizes beside it. The usual one is for 2^-14 to 2^9.
+constexpr int kVe = -6;
+constexpr int kVeStep = 20;   // the others: kVe - 20 and kVe + 20, for 2^-34 to 2^-11 and 2^6 to 2^29
+constexpr int kVeNone = 127;  // no token of the block has a value but zero that an E fits
 // What the softmax needs to know of 32 tokens. `odd` is zero for tokens all there, in half precision's range and
 // finite: then nothing else is looked at.
-struct PrMeta {
+struct __align__(16) PrMeta {
   float kf;        // 2^E of the keys: a score's factor
   int ve;          // E of the values
   uint32_t gap;    // tokens that are absent
   uint32_t bad;    // whether any pair is not finite (then the masks below)
+  uint32_t side;   // tokens whose values E does not fit: zeros in V's operand, the softmax adds them by itself
+  uint32_t pad[3];
 };
 constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at most two ahead of the softmax
 
@@ -509,34 +520,147 @@ __device__ __forceinline__ void pr_pairs(uint32_t (&sb)[D / kGroup], const uint1
     for (int i = 0; i < D / kGroup; ++i) sb[i] = ss[i];
   }
 }
-// The exponent that the values of the warp's 32 tokens are divided by (from 16 |s| + |b|, which none passes), and whether
-// any pair is not finite: then also which tokens' of which group.
+// Whether any of the warp's 32 tokens has a group whose 16 |s| + |b|, which none of its values passes, is outside [low, 2^23 low),
+// low given as bits. A zero, an infinity or a NaN is outside too.
 template <int D>
-__device__ __forceinline__ int pr_range(const uint32_t (&sb)[D / kGroup], uint32_t& any, uint32_t (&bad)[D / kGroup]) {
-  float big = 0.f;
+__device__ __forceinline__ bool pr_odd(const uint32_t (&sb)[D / kGroup], uint32_t low) {
   bool odd = false;
 #pragma unroll
-  for (int g = 0; g < D / kGroup; ++g) {
-    const float top = fmaf(16.f, fabsf(bf16lo(sb[g])), fabsf(bf16hi(sb[g])));
-    odd |= !(top < INFINITY);
-    big = fmaxf(big, top);
-  }
-  any = __ballot_sync(kFull, odd);
-  if (any) {
-    big = 0.f;
-    any = 0;
+  for (int g = 0; g < D / kGroup; ++g) odd |= __float_as_uint(fmaf(16.f, fabsf(bf16lo(sb[g])), fabsf(bf16hi(sb[g])))) - low >= 23u << 23;
+  return __any_sync(kFull, odd);
+}
+constexpr uint32_t kKeyLow = (uint32_t)(-8 + 127) << 23;        // keys: 2^-8 to 2^15 as they are
+constexpr uint32_t kValueLow = (uint32_t)(kVe - 8 + 127) << 23;
+// The same of a group, as bits; 0 where the pair is not finite.
+__device__ __forceinline__ uint32_t pr_top(uint32_t sb, bool& fin) {
+  const float s = fabsf(bf16lo(sb)), b = fabsf(bf16hi(sb));
+  fin = s < INFINITY && b < INFINITY;
+  return fin ? __float_as_uint(fminf(fmaf(16.f, s, b), 3e38f)) : 0u;
+}
+// What is divided out of odd keys: the exponent E that brings the block's largest into [2^13, 2^14). `any`, `bad`: tokens whose
+// pair (of which group) is not finite.
+template <int D>
+__device__ __forceinline__ int pr_key_range(const uint32_t (&sb)[D / kGroup], uint32_t& any, uint32_t (&bad)[D / kGroup]) {
+  uint32_t big = 0;
 #pragma unroll
-    for (int g = 0; g < D / kGroup; ++g) {
-      const float s = fabsf(bf16lo(sb[g])), b = fabsf(bf16hi(sb[g]));
-      const bool fin = s < INFINITY && b < INFINITY;
-      bad[g] = __ballot_sync(kFull, !fin);
-      any |= bad[g];
-      if (fin) big = fmaxf(big, fminf(fmaf(16.f, s, b), 3e38f));
+  for (int g = 0; g < D / kGroup; ++g) {
+    bool fin;
+    big = max(big, pr_top(sb[g], fin));
+    bad[g] = __ballot_sync(kFull, !fin);
+    any |= bad[g];
+  }
+  big = __reduce_max_sync(kFull, big);
+  return big && big - kKeyLow >= 23u << 23 ? min(max((int)(big >> 23) - 127 - 13, -120), 120) : 0;
+}
+// E of odd values: the one of three that fits most of the block's tokens. `side`: the tokens that it does not fit.
+template <int D>
+__device__ __forceinline__ int pr_value_range(const uint32_t (&sb)[D / kGroup], uint32_t& side, uint32_t& any, uint32_t (&bad)[D / kGroup]) {
+  uint32_t fit = 7;  // bit i: kVe + (0, -1, 1)[i] * kVeStep
+  bool some = false;
+#pragma unroll
+  for (int g = 0; g < D / kGroup; ++g) {
+    bool fin;
+    const uint32_t top = pr_top(sb[g], fin);
+    bad[g] = __ballot_sync(kFull, !fin);
+    any |= bad[g];
+    if (top) {
+      some = true;
+      if (top - kValueLow >= 23u << 23) fit &= ~1u;
+      if (top - (kValueLow - ((uint32_t)kVeStep << 23)) >= 23u << 23) fit &= ~2u;
+      if (top - (kValueLow + ((uint32_t)kVeStep << 23)) >= 23u << 23) fit &= ~4u;
     }
   }
-  const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(big));
-  const int k = (int)(bits >> 23) - 127;
-  return bits && (k >= 15 || k < -6) ? min(max(k - 13, -120), 120) : 0;
+  if (!some) fit = 0;
+  const uint32_t f0 = __ballot_sync(kFull, fit & 1), f1 = __ballot_sync(kFull, fit & 2), f2 = __ballot_sync(kFull, fit & 4);
+  const int n0 = __popc(f0), n1 = __popc(f1), n2 = __popc(f2);
+  const bool usual = n0 >= n1 && n0 >= n2, small = n1 >= n2;
+  const uint32_t f = usual ? f0 : small ? f1 : f2;
+  side = __ballot_sync(kFull, some) & ~f;
+  return !f ? kVeNone : usual ? kVe : small ? kVe - kVeStep : kVe + kVeStep;
+}
+// O's unit, by bits 29 and 30 of a softmax thread's notes.
+__device__ __forceinline__ int pr_unit(uint32_t rare) {
+  const uint32_t k = rare >> 29 & 3;
+  return k == 0 ? kVe : k == 1 ? kVe - kVeStep : kVe + kVeStep;
+}
+// Values that V's operand leaves out. They are summed in fp32 from their codes, in units of 1, in the place for a part that the CTA's
+// segment has (whole units have the one that only the share's last unit writes): `sums`, the row's columns four by four,
+// 512 floats apart, and, where a part has its maximum, the one that their probabilities refer to.
+template <int D>
+__device__ __forceinline__ float* pr_side_max(float* sums, int r) { return sums - r * 4 + 128 * D + r; }
+// Adds some of a block's tokens, which are all there. `score` is the row's scores of the block in tensor memory.
+template <int D>
+__device__ __forceinline__ void pr_side(const AttnArgs& a, int row0, int head, int t, uint32_t side, uint32_t see, uint32_t score, float ck, float m,
+                                        float* sums, int r, bool more) {
+  int b = row0;
+  if (a.v.q_start) {  // the last sequence that starts at or before the row
+    int lo = 0, hi = a.v.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.v.q_start[mid] <= row0) lo = mid; else hi = mid;
+    }
+    b = lo;
+  }
+  b = __shfl_sync(kFull, b, 0);
+  const int h = __shfl_sync(kFull, pr_by_group(a, head), 0);
+  const float mm = m == -INFINITY ? 0.f : m, was = more ? *pr_side_max<D>(sums, r) : m, f = was == m ? 1.f : pr_ex2(was - m);
+  *pr_side_max<D>(sums, r) = m;
+#pragma unroll 1
+  for (int d = 0; d < D; d += 8) {
+    float acc[8] = {};
+    float4* const at = reinterpret_cast<float4*>(sums + d / 4 * 512);
+    if (more) {
+      const float4 lo = at[0], hi = at[128];
+      acc[0] = lo.x * f; acc[1] = lo.y * f; acc[2] = lo.z * f; acc[3] = lo.w * f;
+      acc[4] = hi.x * f; acc[5] = hi.y * f; acc[6] = hi.z * f; acc[7] = hi.w * f;
+    }
+#pragma unroll 1
+    for (uint32_t left = side; left; left &= left - 1) {
+      const int x = __ffs(left) - 1, page = kv4_page(a.v, b, t + x);
+      uint32_t s;
+      __syncwarp();
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(s) : "r"(score + x));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s)::"memory");
+      const float p = see >> x & 1 ? pr_ex2(fmaf(__uint_as_float(s), ck, -mm)) : 0.f;
+      const long long row = ((long long)max(page, 0) * a.c.kv_heads + h) * a.c.page_size + (t + x) % a.c.page_size;
+      const uint32_t q = a.c.v_q[row * (D / 8) + d / 8], sb = reinterpret_cast<const uint32_t*>(a.c.v_sb)[row * (D / kGroup) + d / kGroup];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = fmaf(p, fmaf((float)(q >> k * 4 & 15u), bf16lo(sb), bf16hi(sb)), acc[k]);
+        acc[k] = p == 0.f ? acc[k] : v;  // a hidden token adds nothing, whatever it holds
+      }
+    }
+    at[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    at[128] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+}
+// Adds the sums to O, whose columns come as 0 4 1 5 2 6 3 7, and returns O's exponent: the one it had, or, for large sums, 60.
+template <int D>
+__device__ __forceinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float m, int e) {
+  const float was = *pr_side_max<D>(sums, r);
+  const float f = was == m ? 1.f : pr_ex2(was - m);
+  float top = 0.f;
+#pragma unroll 1
+  for (int d = 0; d < D; d += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(sums + d / 4 * 512);
+    top = fmaxf(fmaxf(fmaxf(top, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
+  }
+  const int unit = top * f > 0x1p40f ? 60 : e;
+  const float fo = exp2i(e - unit), fs = exp2i(-unit);
+#pragma unroll 1
+  for (int d = 0; d < D; d += 8) {
+    const float4 lo = *reinterpret_cast<const float4*>(sums + d / 4 * 512), hi = *reinterpret_cast<const float4*>(sums + (d / 4 + 1) * 512);
+    const float v[8] = {lo.x, hi.x, lo.y, hi.y, lo.z, hi.z, lo.w, hi.w};
+    uint32_t o[8];
+    __syncwarp();
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(o, 0) : "r"(o_t + d));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(o, 0)::"memory");
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(fmaf(v[x] * f, fs, __uint_as_float(o[x]) * fo));
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(o_t + d), BGQ_I8(o, 0) : "memory");
+  }
+  pr_wait_st();
+  return unit;
 }
 // A token's values of group g into its row of a panel.
 template <int D>
@@ -587,10 +711,11 @@ __device__ __forceinline__ void pr_query_fetch(const AttnArgs& a, const PrRowOf&
     pr_cp16(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16), a.q + (at < 0 ? 0 : at) + ch * 8, at >= 0);
   }
 }
+// (A function of its own, once a unit: inlined, the same kernel was 0.5 us slower for 4096 tokens.)
 // Row r of the tile, in place: fp16 scaled by a power of two, in the codes' order 0 4 1 5 2 6 3 7; and each group's sum,
 // in two parts, for the extra columns. Returns the factor of its scores.
 template <int D>
-__device__ __forceinline__ float pr_query_scale(const AttnArgs& a, unsigned char* tile, unsigned char* extra, int r) {
+__device__ __noinline__ float pr_query_scale(const AttnArgs& a, unsigned char* tile, unsigned char* extra, int r) {
   auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(tile + (ch >> 3) * kPanel + r * 128 + (((ch & 7) ^ (r & 7)) * 16)); };
   uint32_t t2[4] = {};
 #pragma unroll 8
@@ -712,9 +837,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
 
       float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;
-      int e_run = 0;        // O and P are in units of 2^e_run
-      bool fresh = true;    // no value has set e_run yet
-      uint32_t poison = 0;  // bit 0: a key that is not finite is seen; bit 1 + g: a value of group g
+      // Bit 0: a key that is not finite is seen; bit 1 + g: a value of group g. The same for all of a warp's rows: bits 29 and 30:
+      // O's unit (pr_unit); bit 31: some values are summed apart.
+      uint32_t rare = 0;
 #pragma unroll 1
       for (int it = wk.i0; it < (none ? wk.i0 : wk.i1); ++it) {
         const int slot = NQ == 2 ? i : (it - wk.i0) & 1;
@@ -726,8 +851,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int mt = (wk.n0 + it - wk.i0) & (kMetaTiles - 1);
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
-        const bool plain = !(odd4.x | odd4.y | odd4.z | odd4.w) && t0 >= lo_max && t0 + kPrTok <= hi_min && e_run == 0;
-        if (plain) fresh = false;
+        const uint32_t odd_tile = odd4.x | odd4.y | odd4.z | odd4.w | (rare & 3u << 29);
+        const bool plain = !odd_tile && t0 >= lo_max && t0 + kPrTok <= hi_min;
         // Every row sees every token, and no factor but the row's: 64 tokens at a time. The probabilities are taken with the
         // maximum so far while the scores' own is found; where that is too far above (seldom), it is raised and they are taken again.
 #pragma unroll 1
@@ -781,6 +906,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
         }
         // otherwise 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
+        int unit = kVe;  // of the tile: O's where a block has it, else that of the first block with any
+        if (odd_tile) {
+          bool keep = false;
+#pragma unroll
+          for (int c = 3; c >= 0; --c) {
+            const int ve = sh.meta[mt][c].ve;
+            keep |= ve == pr_unit(rare);
+            if (c == 3 || ve != kVeNone) unit = ve;
+          }
+          if (keep || unit == kVeNone) unit = pr_unit(rare);
+        }
 #pragma unroll 1
         for (int c = 0; c < (dead || plain ? 0 : 4); ++c) {
           const int t = t0 + c * 32;
@@ -792,22 +928,24 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           uint32_t v[32];
           pr_ld32(s_t + c * 32, v);
           const uint32_t odd = sh.odd[mt][c];
+          const bool look = odd || unit != kVe;
           const bool cut = t < lo_max || t + 32 > hi_min;
           float ck = c2;
-          int ve = 0;
-          uint32_t see = 0xffffffffu;
-          if (odd || cut) {
+          uint32_t see = 0xffffffffu, apart = 0;  // tokens whose values are summed apart
+          bool other = false;                     // all of them: the block's operand is of another unit than O
+          if (look || cut) {
             const PrMeta me = sh.meta[mt][c];
             ck *= me.kf;
-            ve = me.ve;
+            other = me.ve != unit && me.ve != kVeNone;
+            apart = (other ? 0xffffffffu : me.side) & ~me.gap;
             const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
             see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
             see &= ~me.gap;
             if (me.bad) {
-              if (see & sh.kbad[mt][c]) poison |= 1;
+              if (see & sh.kbad[mt][c]) rare |= 1;
 #pragma unroll
               for (int g = 0; g < G; ++g)
-                if (see & sh.vbad[mt][c][g]) poison |= 2u << g;
+                if (see & sh.vbad[mt][c][g]) rare |= 2u << g;
             }
           }
           ck = fmaxf(ck, 0x1p-126f);  // -infinity stays -infinity
@@ -825,29 +963,24 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
           const float top = pr_max3(fmaxf(ta, tb), __uint_as_float(v[30]), __uint_as_float(v[31])) * ck;
           const bool raise = top > m + 8.f;
-          if (__any_sync(kFull, raise || fresh || ve > e_run)) {
+          if (__any_sync(kFull, raise) || unit != pr_unit(rare)) {
             const float up = raise ? top : m;
-            float f = up == m ? 1.f : pr_ex2(m - up);
+            const float f = up == m ? 1.f : pr_ex2(m - up);
             m = up;
             mm = up == -INFINITY ? 0.f : up;
             l0 *= f;
             l1 *= f;
-            const int e_new = fresh ? ve : max(ve, e_run);
-            f *= exp2i(max(e_run - e_new, -126));
-            e_run = e_new;
-            if (!fresh) {
-              pr_wait_st();
+            pr_wait_st();
 #pragma unroll 1
-              for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
-              if (it > wk.i0) {
-                if (NQ == 1) {  // the product before this one may still be running
-                  pr_wait(&sh.pv_done, pv_par ^ 1, fail);
-                  tc_fence_after();
-                }
-                pr_scale<D>(o_t, f);
+            for (int k = 0; k < c; ++k) pr_scale_p(s_t + k * 16, f);  // this tile's P so far
+            if (it > wk.i0) {
+              if (NQ == 1) {  // the product before this one may still be running
+                pr_wait(&sh.pv_done, pv_par ^ 1, fail);
+                tc_fence_after();
               }
+              pr_scale<D>(o_t, f * exp2i(pr_unit(rare) - unit));  // units are at most 2^40 apart, which fp32 has to spare
             }
-            fresh = false;
+            rare = (rare & ~(3u << 29)) | (unit == kVe ? 0u : unit < kVe ? 1u << 29 : 2u << 29);
           }
           uint64_t ll = pr_pair(l0, l1);
           const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
@@ -863,11 +996,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             pk[x] = pr_half2(p0, p1);
           }
           pr_split(ll, l0, l1);
-          if (ve != e_run) {  // values of another unit than O, never larger
-            const float f = exp2i(max(ve - e_run, -24));
-            const uint32_t f2 = pr_half2(f, f);
+          if (apart) {  // seldom
+            pr_side<D>(a, row, head, t, apart, see, s_t + c * 32, ck, m, w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot + r * 4, r,
+                       rare >> 31);
+            rare |= 1u << 31;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(pk[x]) : "r"(pk[x]), "r"(f2));
+            for (int x = 0; x < 16; ++x) pk[x] = other ? 0u : pk[x];
           }
           pr_st16(s_t + c * 16, pk);
         }
@@ -894,8 +1028,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       pr_wait(&sh.o_full[i], o_par, fail);
       o_par ^= 1;
       tc_fence_after();
-      float l = poison & 1 ? NAN : l0 + l1;
-      const float unit = exp2i(e_run);
+      const int e = rare >> 31 ? pr_side_add<D>(part + r * 4, r, o_t, m, pr_unit(rare)) : pr_unit(rare);
+      float l = rare & 1 ? NAN : l0 + l1;
+      const float unit = exp2i(e);
       const long long out_at = ok ? (long long)row * a.out_stride + head * D : -1;
       if (!dead) {
         const float inv = l == 0.f ? 0.f : unit / l;
@@ -905,7 +1040,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           pr_ld32(o_t + d, v);
           pr_wait_ld(v);
           float f = whole ? inv : unit;
-          if (poison >> (1 + d / kGroup) & 1) f = NAN;
+          if (rare >> (1 + d / kGroup) & 1) f = NAN;
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
           if (whole) {
@@ -1008,26 +1143,39 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     for (int x = -1;; ++x) {  // tile x is stored, the next one fetched
       if (x >= 0) {
         const int mt = x & (kMetaTiles - 1);
-        uint32_t any, bad[G];
-        const int e = pr_range<D>(sb, any, bad);
-        const float down = exp2i(-e);
+        uint32_t any = 0, apart = 0, bad[G];
+        int e = val ? kVe : 0;
+        float down = val ? exp2i(-kVe) : 1.f;
         uint32_t s2[G], b2[G];
+        const bool odd_own = pr_odd<D>(sb, val ? kValueLow : kKeyLow);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          float sc = bf16lo(sb[g]) * down, bi = bf16hi(sb[g]) * down;
-          if (!(fabsf(sc) < INFINITY && fabsf(bi) < INFINITY)) sc = bi = 0.f;
+          const float sc = bf16lo(sb[g]) * down, bi = bf16hi(sb[g]) * down;
           s2[g] = pr_half2(sc, sc);
           b2[g] = pr_half2(bi, bi);
         }
+        if (odd_own) {
+          e = val ? pr_value_range<D>(sb, apart, any, bad) : pr_key_range<D>(sb, any, bad);
+          down = e == kVeNone || apart >> lane & 1 ? 0.f : exp2i(-e);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            float sc = bf16lo(sb[g]) * down, bi = bf16hi(sb[g]) * down;
+            if (!(fabsf(sc) < INFINITY && fabsf(bi) < INFINITY)) sc = bi = 0.f;
+            s2[g] = pr_half2(sc, sc);
+            b2[g] = pr_half2(bi, bi);
+          }
+        }
         pr_wait(&free_[st], par, fail);
         if (!val) {  // the notes on both go out with K, for the softmax reads them with the scores
-          uint32_t vany, vbad[G];
-          const int ve = pr_range<D>(vs, vany, vbad), c = part / 32;
+          uint32_t vside = 0, vany = 0, vbad[G];
+          int ve = kVe;
+          const int c = part / 32;
+          if (pr_odd<D>(vs, kValueLow)) ve = pr_value_range<D>(vs, vside, vany, vbad);
           const uint32_t gap = __ballot_sync(kFull, gone);
           if (lane == 0) {
-            const uint32_t odd = gap | any | vany | (uint32_t)e | (uint32_t)ve;
+            const uint32_t odd = gap | any | vany | (uint32_t)e | vside | (uint32_t)(ve != kVe && ve != kVeNone);
             sh.odd[mt][c] = odd;
-            sh.meta[mt][c] = PrMeta{exp2i(e), ve, gap, any | vany};
+            sh.meta[mt][c] = PrMeta{exp2i(e), ve, gap, any | vany, vside, {}};
             if (odd) {
               sh.kbad[mt][c] = any;
 #pragma unroll

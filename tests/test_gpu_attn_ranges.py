@@ -1,0 +1,103 @@
+"""Attention over keys and values of very different sizes beside each other: by blocks of tokens, by single tokens, by groups of
+64 columns, and in tokens that a row does not see. Every column's bound is that of tests/test_gpu_attn.py, which goes by
+what the row itself sees of that column: 2^-8 |out| + 2^-9 (1 + scale sum|q k|) sum p (|v| + 8 s)."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_group_quantized_gb300 import lib
+from oracle import attn_oracle as A
+from oracle import bgq_oracle as O
+from tests.test_gpu_attn import Case, attn_close, bf16
+
+pytestmark = pytest.mark.gpu
+
+VALUES, KEYS = 3, 1  # the pairs' places among a case's arrays
+
+
+def times(c, which, tokens, factor, group=slice(None), b=0):
+    """Multiplies the pairs (scale and bias) of these tokens of sequence b by a power of two."""
+    for t in tokens:
+        at = A.slot(t, b, c.pages, c.page, c.n_pages)
+        if at is not None:
+            c.np[which][at[0], :, at[1], group] = O.f64_to_bf16_bits(O.bf16_to_f64(c.np[which][at[0], :, at[1], group]) * factor)
+
+
+def run(c, hq, scale=1.5, **kw):
+    q = bf16(c.rng, c.rows, hq, c.d, dev=c.dev, scale=scale)
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True, **kw)
+    return q, out, lse
+
+
+ROWS = [64]  # the many-row kernel
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** -8, 2.0 ** -11, 2.0 ** -15, 2.0 ** -30, 2.0 ** 8, 2.0 ** 13])
+def test_blocks_of_values_around_a_size(cuda_device, size, d, new):
+    """Blocks of 32 tokens by turns a little above and a little below a size at which half precision's range may end."""
+    c = Case(cuda_device, [700], [new], 1, d, 16, seed=50)
+    for t in range(700):
+        times(c, VALUES, [t], size * (2.0 if t // 32 % 2 else 0.125))
+    q, out, lse = run(c, 4)
+    attn_close(c, q, out, lse)
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("before", ["absent", "zeros", "normal", "large"])
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** -16, 2.0 ** -40])
+def test_small_values_behind_others(cuda_device, size, before, new):
+    """Small values behind a given-up page, a block of zeros, one of ordinary values, one of large ones that a window hides."""
+    c = Case(cuda_device, [600], [new], 1, 128, 32, seed=51)
+    times(c, VALUES, range(32, 600), size)
+    if before == "absent":
+        c.pages[0, 0] = -1
+    times(c, VALUES, range(32), {"zeros": 0.0, "large": 2.0 ** 60}.get(before, 1.0))
+    for window in (0, 500):
+        q, out, lse = run(c, 4, window=window)
+        attn_close(c, q, out, lse, window=window)
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("factor", [2.0 ** -12, 2.0 ** -20, 2.0 ** -28, 2.0 ** -60, 2.0 ** 20, 2.0 ** 60])
+def test_groups_of_values_of_different_sizes(cuda_device, factor, d, new):
+    """A group of 64 columns far smaller or larger than the others, in every token, in every other one, in the first half."""
+    for tokens in (range(300), range(0, 300, 2), range(150)):
+        c = Case(cuda_device, [300], [new], 2, d, 16, seed=52)
+        times(c, VALUES, tokens, factor, group=1)
+        q, out, lse = run(c, 8)
+        attn_close(c, q, out, lse)
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("which", [VALUES])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("factor", [2.0 ** 24, 2.0 ** 60, 2.0 ** 110])
+def test_large_tokens_that_a_row_does_not_see(cuda_device, factor, d, which, new):
+    """Finite tokens of any size hidden by causality (the last) and by the window (the first ones) leave the other rows right."""
+    c = Case(cuda_device, [300], [new], 1, d, 16, seed=53)
+    times(c, which, [299], factor)
+    times(c, which, range(0, 300 - new - 100), factor)
+    q, out, lse = run(c, 4, window=101)
+    o, l, a, s = c.oracle(q, window=101)
+    see = slice(0, new - 1)  # all but the last row, which does see a large token
+    got = O.bf16_to_f64(out.cpu().view(torch.int16).numpy().astype(np.uint16))
+    assert (np.abs(got - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -9 * (1 + s)[..., None] * a)[see].all()
+    assert (np.abs(lse.cpu().double().numpy() - l) <= 2.0 ** -10 * (s + 1))[see].all()
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("exps", [(0, -9), (0, -25), (20, 0), (3, 40), (-30, -70)])
+def test_tokens_of_different_sizes(cuda_device, exps, new):
+    """Values by single tokens of two sizes, mixed; then keys."""
+    pick = np.random.default_rng(5).random(300) < 0.3
+    for which in (VALUES, KEYS):
+        c = Case(cuda_device, [300], [new], 1, 128, 16, seed=54)
+        for t in range(300):
+            times(c, which, [t], 2.0 ** exps[int(pick[t])])
+        # large keys: their scores stay within some tens
+        q, out, lse = run(c, 4, scale=1.5 if which == VALUES else 1.5 * 2.0 ** -max(exps))
+        attn_close(c, q, out, lse)
