@@ -32,11 +32,13 @@
 // 2^8: P then reaches 2^8 at most, far inside fp16.
 //
 // Half precision's range: queries are scaled by a power of two per row, K by
-// one per 32 tokens where it leaves [2^-8, 2^15) (else none), which the softmax undoes in the score's factor. V is
+// one per 32 tokens where it leaves [2^-8, 2^15) (else none), or one a token where one for all would lose some; the softmax
+// undoes it in the scores' factors. V is
 // scaled by one of three powers of two per 32 tokens, O's unit. Tokens that it does not fit (a group far smaller or larger than a
 // value's usual size) and blocks of another unit than O's are left out of the product, and their softmax thread adds p V in fp32,
 // slowly: no row's result depends on the size of values that it does not see, or of another group's. This costs ordinary values
-// 1 to 3 % (4096 tokens causal: 151.6 us, 147.6 with one exponent for all that a row had met, which lost small ones beside large).
+// 1 to 3 % (4096 tokens causal: 152.7 us, 148.1 with one exponent for all that a row had met, which lost small ones beside large; the
+// functions of the rare paths are not inlined: 154.2).
 // A key or value pair that is not finite is stored as zeros, and the rows that see it are made NaN at the end.
 //
 // All (unit, key head, 128 tokens) triples form one list, which k_prompt_plan lays out from
@@ -83,6 +85,7 @@ struct Prompt {
   // more than half an SM's, so that no second CTA comes to wait for this one's tensor memory
   static constexpr int kNeed = 1024 + NQ * kTile + (KST * KP + VST * VP) * kPanel + 2 * kRaw + (NQ + KE) * kExtra;
   static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+  static constexpr int kOwn = 232448 - kSmem;  // bytes left for PrShared
   static constexpr int kSlot = 128 * D + 256;  // floats of a part: O by 4 columns and row, then m, then l
   // registers of a softmax, dequantisation and other warpgroup's threads: together at most the launch's
   static constexpr int kRegSoft = D == 256 ? 176 : 136, kRegDeq = D == 256 ? 104 : 80, kRegRest = 40;
@@ -289,6 +292,21 @@ __device__ __forceinline__ void pr_scale_p(uint32_t t, float f) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
   }
 }
+// A score's factor: finite, so that zero times it stays zero, and not below normal numbers, so that -infinity times it stays that.
+__device__ __forceinline__ float pr_factor(float f) { return fminf(fmaxf(f, 0x1p-126f), 3e38f); }
+// 32 scores of the warp's rows times f and the powers of two of their tokens' keys.
+__device__ __noinline__ void pr_scale_s(uint32_t t, float f, const int8_t* ke) {
+#pragma unroll 1
+  for (int d = 0; d < 32; d += 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(r, 0) : "r"(t + d));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
+#pragma unroll
+    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * pr_factor(f * exp2i(ke[d + x])));
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
+  }
+  pr_wait_st();
+}
 // Lanes m apart: the lower one's b for the upper one's a.
 __device__ __forceinline__ void pr_swap(uint4& a, uint4& b, int m, int lane) {
   const bool upper = lane & m;
@@ -406,7 +424,7 @@ constexpr int kVeNone = 127;  // no token of the block has a value but zero that
 // What the softmax needs to know of 32 tokens. `odd` is zero for tokens all there, in half precision's range and
 // finite: then nothing else is looked at.
 struct __align__(16) PrMeta {
-  float kf;        // 2^E of the keys: a score's factor
+  float kf;        // 2^E of the keys: a score's factor; 0: each token has its own
   int ve;          // E of the values
   uint32_t gap;    // tokens that are absent
   uint32_t bad;    // whether any pair is not finite (then the masks below)
@@ -423,6 +441,7 @@ struct PrShared {
   PrMeta meta[kMetaTiles][4];
   __align__(16) uint32_t odd[kMetaTiles][4];
   uint32_t kbad[kMetaTiles][4], vbad[kMetaTiles][4][G];
+  int8_t ke[kMetaTiles][kPrTok];  // tokens' E, where a block has no common one
   uint32_t tmem;
   int fail;
 };
@@ -537,20 +556,24 @@ __device__ __forceinline__ uint32_t pr_top(uint32_t sb, bool& fin) {
   fin = s < INFINITY && b < INFINITY;
   return fin ? __float_as_uint(fminf(fmaf(16.f, s, b), 3e38f)) : 0u;
 }
-// What is divided out of odd keys: the exponent E that brings the block's largest into [2^13, 2^14). `any`, `bad`: tokens whose
-// pair (of which group) is not finite.
+// What is divided out of the lane's token of odd keys: the exponent E that brings the block's largest into [2^13, 2^14), or, for
+// tokens that it would put below 2^-6, the token's own one; `mix`: some have their own. `any`, `bad`: tokens whose pair (of which group) is not
+// finite.
 template <int D>
-__device__ __forceinline__ int pr_key_range(const uint32_t (&sb)[D / kGroup], uint32_t& any, uint32_t (&bad)[D / kGroup]) {
-  uint32_t big = 0;
+__device__ __forceinline__ int pr_key_range(const uint32_t (&sb)[D / kGroup], bool& mix, uint32_t& any, uint32_t (&bad)[D / kGroup]) {
+  uint32_t own = 0;
 #pragma unroll
   for (int g = 0; g < D / kGroup; ++g) {
     bool fin;
-    big = max(big, pr_top(sb[g], fin));
+    own = max(own, pr_top(sb[g], fin));
     bad[g] = __ballot_sync(kFull, !fin);
     any |= bad[g];
   }
-  big = __reduce_max_sync(kFull, big);
-  return big && big - kKeyLow >= 23u << 23 ? min(max((int)(big >> 23) - 127 - 13, -120), 120) : 0;
+  if (!__any_sync(kFull, own && own - kKeyLow >= 23u << 23)) return 0;
+  const int top = (int)(__reduce_max_sync(kFull, own) >> 23), it = (int)(own >> 23);
+  const bool apart = own && it < top - 19;
+  mix = __any_sync(kFull, apart);
+  return min(max((apart ? it : top) - 127 - 13, -120), 120);
 }
 // E of odd values: the one of three that fits most of the block's tokens. `side`: the tokens that it does not fit.
 template <int D>
@@ -590,7 +613,7 @@ template <int D>
 __device__ __forceinline__ float* pr_side_max(float* sums, int r) { return sums - r * 4 + 128 * D + r; }
 // Adds some of a block's tokens, which are all there. `score` is the row's scores of the block in tensor memory.
 template <int D>
-__device__ __forceinline__ void pr_side(const AttnArgs& a, int row0, int head, int t, uint32_t side, uint32_t see, uint32_t score, float ck, float m,
+__device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int t, uint32_t side, uint32_t see, uint32_t score, float ck, float m,
                                         float* sums, int r, bool more) {
   int b = row0;
   if (a.v.q_start) {  // the last sequence that starts at or before the row
@@ -636,7 +659,7 @@ __device__ __forceinline__ void pr_side(const AttnArgs& a, int row0, int head, i
 }
 // Adds the sums to O, whose columns come as 0 4 1 5 2 6 3 7, and returns O's exponent: the one it had, or, for large sums, 60.
 template <int D>
-__device__ __forceinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float m, int e) {
+__device__ __noinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float m, int e) {
   const float was = *pr_side_max<D>(sums, r);
   const float f = was == m ? 1.f : pr_ex2(was - m);
   float top = 0.f;
@@ -763,6 +786,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
   constexpr int G = P::G, NQ = P::NQ;
   extern __shared__ unsigned char smem_raw[];
   __shared__ PrShared<D> sh;
+  static_assert(sizeof(sh) <= P::kOwn, "more shared memory than a CTA can have");
   unsigned char* const smem = smem_raw + ((1024 - (tc_smem(smem_raw) & 1023)) & 1023);
   unsigned char* const q_s = smem;
   unsigned char* const k_s = q_s + NQ * P::kTile;
@@ -933,9 +957,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           float ck = c2;
           uint32_t see = 0xffffffffu, apart = 0;  // tokens whose values are summed apart
           bool other = false;                     // all of them: the block's operand is of another unit than O
+          bool mix = false;                       // each token's key has its own factor
           if (look || cut) {
             const PrMeta me = sh.meta[mt][c];
             ck *= me.kf;
+            mix = me.kf == 0.f;
             other = me.ve != unit && me.ve != kVeNone;
             apart = (other ? 0xffffffffu : me.side) & ~me.gap;
             const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
@@ -948,8 +974,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 if (see & sh.vbad[mt][c][g]) rare |= 2u << g;
             }
           }
-          ck = fmaxf(ck, 0x1p-126f);  // -infinity stays -infinity
+          ck = pr_factor(ck);
           pr_wait_ld(v);
+          if (mix) {  // seldom
+            pr_scale_s(s_t + c * 32, c2, sh.ke[mt] + c * 32);
+            pr_ld32(s_t + c * 32, v);
+            pr_wait_ld(v);
+            ck = 1.f;
+          }
           if (odd || cut) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = see >> x & 1 ? v[x] : 0xff800000u;
@@ -1144,6 +1176,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       if (x >= 0) {
         const int mt = x & (kMetaTiles - 1);
         uint32_t any = 0, apart = 0, bad[G];
+        bool mix = false;
         int e = val ? kVe : 0;
         float down = val ? exp2i(-kVe) : 1.f;
         uint32_t s2[G], b2[G];
@@ -1155,7 +1188,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           b2[g] = pr_half2(bi, bi);
         }
         if (odd_own) {
-          e = val ? pr_value_range<D>(sb, apart, any, bad) : pr_key_range<D>(sb, any, bad);
+          e = val ? pr_value_range<D>(sb, apart, any, bad) : pr_key_range<D>(sb, mix, any, bad);
           down = e == kVeNone || apart >> lane & 1 ? 0.f : exp2i(-e);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
@@ -1173,15 +1206,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           if (pr_odd<D>(vs, kValueLow)) ve = pr_value_range<D>(vs, vside, vany, vbad);
           const uint32_t gap = __ballot_sync(kFull, gone);
           if (lane == 0) {
-            const uint32_t odd = gap | any | vany | (uint32_t)e | vside | (uint32_t)(ve != kVe && ve != kVeNone);
+            const uint32_t odd = gap | any | vany | (uint32_t)e | (uint32_t)mix | vside | (uint32_t)(ve != kVe && ve != kVeNone);
             sh.odd[mt][c] = odd;
-            sh.meta[mt][c] = PrMeta{exp2i(e), ve, gap, any | vany, vside, {}};
+            sh.meta[mt][c] = PrMeta{mix ? 0.f : exp2i(e), ve, gap, any | vany, vside, {}};
             if (odd) {
               sh.kbad[mt][c] = any;
 #pragma unroll
               for (int g = 0; g < G; ++g) sh.vbad[mt][c][g] = vany ? vbad[g] : 0;
             }
           }
+          if (mix) sh.ke[mt][part + lane] = (int8_t)e;
           unsigned char* const ext = ke_s + (P::KE > 1 ? st * kExtra : 0);
 #pragma unroll
           for (int g = 0; g < G; g += 2)

@@ -73,7 +73,7 @@ def test_groups_of_values_of_different_sizes(cuda_device, factor, d, new):
 
 
 @pytest.mark.parametrize("new", ROWS)
-@pytest.mark.parametrize("which", [VALUES])
+@pytest.mark.parametrize("which", [KEYS, VALUES])
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("factor", [2.0 ** 24, 2.0 ** 60, 2.0 ** 110])
 def test_large_tokens_that_a_row_does_not_see(cuda_device, factor, d, which, new):
