@@ -20,7 +20,8 @@
 //           as the B operand; p (b_g + 8 s_g) is summed apart in fp32. Codes are
 //           centred so that long sums stay small beside what is added to them.
 // p s_g is rounded to fp16 (half a step 2^-12, a sixteenth of the bf16 output's, and of random sign); its exponent is kept in range by a power
-// of two 2^E per warp that follows the largest scale seen. The maximum is only
+// of two 2^E per warp that follows the largest scale of a tile; scales far from it, in tokens that a column may not even see, are
+// multiplied apart. The maximum is only
 // raised when a score passes it by 2^8, so that most tiles need no reduction over the warp.
 // What bounds it is the issue of instructions, not memory: 385 of them for 16 tokens of a head of 128, 55 for the
 // copies among them (taken out, no time was saved). 64 sequences of 512 to 16384 tokens, 8 key
@@ -217,17 +218,96 @@ struct SplitAcc {
   float cs[NT][2];                // scale * log2(e) / 2^shift
   int hi[NT][2], lo[NT][2];       // the tokens that the columns see: lo <= t < hi
   float unit, inv;                // 2^E, 2^-E
-  uint32_t limit;                 // bits of the largest scale that 2^-E takes in
+  uint32_t less;                  // minus the bits of 2^(E - 3), the smallest scale that 2^-E takes in
 };
+// p s 2^-E has a place in fp16 for the scales s from 2^(E - 3) to 2^(E + 6): below 2^8 2^6, and 2^-25 of it is lost. E follows the
+// largest scale of a tile, between -20 and 20, where fp32 has room for O in any such unit; scales that it does not take in (far
+// smaller than others of the tile, or very large) are multiplied apart.
+constexpr int kSplitTop = 5, kSplitMost = 20;
+constexpr uint32_t kSplitSpan = 9u << 23;
 
-// What follows a tile's scores s; MASKED where some column does not see all of its tokens.
-template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st,
-                                             uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
-  using P = Split<D, NT, 1>;  // nothing here goes by the CTAs
+// Codes less 8 of dims 4g + j (row g) and 32 + 4g + j (row g + 8), from transposed words.
+__device__ __forceinline__ void split_codes(uint32_t (&f)[4], const uint32_t (&w)[4], int j, const SplitK& k_) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = j & 2 ? w[i] >> 8 : w[i];
+    f[i] = j & 1 ? hfma2_u(and_or(x, 0x00F000F0u, k_.or1024), k_.by16, k_.less72)  // (1024 + 16q)/16 - 72
+                 : hadd2_u(and_or(x, 0x000F000Fu, k_.or1024), 0xE408E408u);              // 1024 + q - 1032
+  }
+}
+// What the scales that 2^-E does not take in add to O and the sums beside it: token by token in fp32, a lane its own dims of O, with few registers.
+// Seldom. Hidden tokens' scores are -infinity.
+template <int D, int NT>
+__device__ __forceinline__ void split_far(SplitAcc<D, NT>& A, const float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st, int t0, int held,
+                                          int g) {
+  using P = Split<D, NT, 1>;
   constexpr int G = P::G, MT = P::MT;
+  asm volatile("" : "+r"(g), "+r"(t0), "+l"(st));  // nothing is worked out ahead, in registers of the loop around it
+  const int c = threadIdx.x & 3;
+#pragma unroll 1
+  for (int mr = 0; mr < 2 * MT; ++mr) {  // eight tokens, of which the lane has one
+    float p[NT][2], v[G];
+    bool any = false;
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      const uint32_t pair = t0 + mr * 8 + g < held ? reinterpret_cast<const uint32_t*>(st + 2 * P::kCode + P::kSb)[(mr * 8 + g) * G + gr] : 0u;
+      const uint32_t mag = (pair & 0x7fffu) << 16;
+      const bool far = mag && mag < 0x7f800000u && mag + A.less >= kSplitSpan;
+      v[gr] = far ? bf16lo(pair) : 0.f;
+      any |= far;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x = s[0][n][k];
+#pragma unroll
+        for (int i = 1; i < 2 * MT; ++i) x = mr == i ? s[i / 2][n][i % 2 * 2 + k] : x;
+        p[n][k] = ex2(fmaf(x, A.cs[n][k], -A.mm[n][k]));
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] = fmaf(p[n][k], 8.f * v[gr], A.bias[n][k][gr]);
+      }
+#pragma unroll 1
+    for (uint32_t left = __ballot_sync(kFull, any) & 0x11111111u; left; left &= left - 1) {
+      const int from = __ffs(left) - 1, t = mr * 8 + (from >> 2);
+      float f[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) f[n][k] = __shfl_sync(kFull, p[n][k], from + c) * A.inv;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const float vt = __shfl_sync(kFull, v[gr], from);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // dims 4g + j, then 32 + those
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(st + P::kCode + (t >> 4) * (8 * D) + split_at<D>(t & 15, gr * 2 + h) + (g >> 1) * 4) >> (g & 1) * 16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float code = (float)(int)(w >> j * 4 & 15u) - 8.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) A.o[n][gr][j][h * 2 + k] = fmaf(f[n][k] * vt, code, A.o[n][gr][j][h * 2 + k]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// What follows a tile's scores s; MASKED where some column does not see all of its tokens, or some scale is far from the others:
+// without it nothing is done then, and false returned.
+template <int D, int NT, int CTAS, bool MASKED>
+__device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st,
+                                             uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
+  using P = Split<D, NT, 1>;  // a tile's layout does not go by the CTAs
+  constexpr int G = P::G, MT = P::MT;
+  // Where registers are short (128 a thread, or 16 columns of 256) the pairs are read again behind split_far and the hidden tokens found again,
+  // so that no register keeps them over it (64 sequences of 512 to 16384 tokens: 88.3 us, else 89.6); elsewhere the registers
+  // are there (131071 tokens: 42.6 us, else 43.4).
+  constexpr bool kAgain = CTAS == 2 || D * NT >= 512;
   bool hid[MT][NT][4];
-  uint32_t vp[MT][2][G], big = 0;  // V's pairs; the largest scale, as bits
+  uint32_t vp[MT][2][G], big = 0;  // V's pairs; how far their scales' bits pass the smallest
   bool raise = false;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -239,8 +319,9 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
         vp[mt][r][gr] = src[gr];
+        const uint32_t over = vp[mt][r][gr] * 65536u + A.less;
         if (MASKED && !some) vp[mt][r][gr] = 0u;
-        big = max(big, vp[mt][r][gr] << 16);
+        else big = max(big, over);
       }
       if (MASKED) {
 #pragma unroll
@@ -261,8 +342,31 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
       for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, mt ? fmaxf(s[mt][n][k], s[mt][n][2 + k]) : s[mt][n][2 + k]);
       raise |= top * A.cs[n][k] > A.m[n][k] + 8.f;
     }
-  // a scale with its sign set, an infinity or a NaN compares as large: looked at more closely there
-  if (__any_sync(kFull, raise || big > A.limit)) {
+  // a scale of zero or with its sign set, an infinity or a NaN passes the span: looked at more closely there
+  if (__any_sync(kFull, raise || big >= kSplitSpan)) {
+    uint32_t most = 0, least = ~0u;  // largest and (less one) smallest of the finite scales but zero
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const uint32_t mag = (vp[mt][r][gr] & 0x7fffu) << 16;
+          if (mag < 0x7f800000u) {
+            most = max(most, mag);
+            least = min(least, mag - 1);
+          }
+        }
+    most = __reduce_max_sync(kFull, most);
+    least = __reduce_min_sync(kFull, least) + 1;
+    int e = (int)(__float_as_uint(A.unit) >> 23) - 127;
+    uint32_t less = A.less;
+    if (most && most + less >= kSplitSpan) {
+      e = min(max((int)(most >> 23) - 127 - kSplitTop, -kSplitMost), kSplitMost);
+      less = 0u - __float_as_uint(exp2i(e + kSplitTop - 8));
+    }
+    const bool far = most && (most + less >= kSplitSpan || least < 0u - less);
+    if (!MASKED && far) return false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -288,23 +392,11 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
           }
         }
       }
-    big = 0;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          const uint32_t mag = (vp[mt][r][gr] & 0x7fffu) << 16;
-          if (mag < 0x7f800000u) big = max(big, mag);
-        }
-    big = __reduce_max_sync(kFull, big);
-    if (big > A.limit) {  // from here on p 2^-E s stays below 2^8 2^6
-      const int e = min(max((int)(big >> 23) - 132, -120), 120);
-      const float f = A.limit ? A.unit * exp2i(-e) : 0.f;
+    if (less != A.less) {
+      const float f = A.unit * exp2i(-e);
       A.unit = exp2i(e);
       A.inv = exp2i(-e);
-      A.limit = __float_as_uint(exp2i(e + 6));
+      A.less = less;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -313,6 +405,33 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) A.o[n][gr][j][i] *= f;
+    }
+    if (MASKED && far) {
+      split_far<D, NT>(A, s, st, t0, held, g);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const int t = mt * 16 + r * 8 + g;
+            if (kAgain) vp[mt][r][gr] = !(gaps >> mt & 1) && t0 + t < held ? reinterpret_cast<const volatile uint32_t*>(st + 2 * P::kCode + P::kSb)[t * G + gr] : 0u;
+            const uint32_t mag = (vp[mt][r][gr] & 0x7fffu) << 16;
+            if (mag < 0x7f800000u && mag + A.less >= kSplitSpan) vp[mt][r][gr] &= 0xffff0000u;
+          }
+      if (kAgain) {
+        asm volatile("" : "+r"(t0));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int t = t0 + mt * 16 + r * 8 + g;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) hid[mt][n][r * 2 + k] = (gaps >> mt & 1) || t >= held || t < A.lo[n][k] || t >= A.hi[n][k];
+          }
+      }
     }
   }
   // ---- probabilities, and the output
@@ -356,24 +475,18 @@ __device__ __forceinline__ void split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
       // four codes (dims 4g .. 4g + 3, then 32 + those) of tokens 2c and 2c + 1, then 8 + those, side by side
-      uint32_t r[4], r8[4];
+      uint32_t r[4];
       ldmat4<true>(r, (st_u + P::kCode + mt * (8 * D)) ^ (gr * 32));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r8[i] = r[i] >> 8;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // code - 8 of dims 4g + j (row g) and 32 + 4g + j (row g + 8)
+      for (int j = 0; j < 4; ++j) {
         uint32_t f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = j & 2 ? r8[i] : r[i];
-          f[i] = j & 1 ? hfma2_u(and_or(w, 0x00F000F0u, k_.or1024), k_.by16, k_.less72)  // (1024 + 16q)/16 - 72
-                       : hadd2_u(and_or(w, 0x000F000Fu, k_.or1024), 0xE408E408u);              // 1024 + q - 1032
-        }
+        split_codes(f, r, j, k_);
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma16816(A.o[n][gr][j], f[0], f[2], f[1], f[3], bf[n][gr][0], bf[n][gr][1]);
       }
     }
   }
+  return true;
 }
 
 template <int D, int NT, int CTAS>
@@ -651,7 +764,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
           for (int i = 0; i < 4; ++i) A.o[n][gr][j][i] = 0.f;
     }
     A.unit = A.inv = 1.f;
-    A.limit = 0;
+    A.less = 0u - 0x7f800000u;  // takes no scale in
 
     for (int it = wk.i0 + warp; it < wk.i1; it += kSplitWarps) {
       cp_wait<ST - 1>();
@@ -726,8 +839,8 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
           }
         }
       }
-      if (masked) split_finish<D, NT, true>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_);
-      else split_finish<D, NT, false>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_);
+      if (masked || !split_finish<D, NT, CTAS, false>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_))
+        split_finish<D, NT, CTAS, true>(A, s, st, st_u, t0, gaps, wk.q.sp.held, g, k_);
       __syncwarp();
       fetch(slot);
       slot = slot + 1 == ST ? 0 : slot + 1;
