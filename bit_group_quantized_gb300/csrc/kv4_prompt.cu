@@ -28,8 +28,9 @@
 // 935 TFLOP/s; three chunks of 700 to 1100 rows behind up to 16000 tokens: 303 us, 1190 TFLOP/s (61 % of the matrix rate
 // measured with a library product); 24 sequences of five rows, 16 heads of 256 over 2: 41 us, where dequantisation has
 // too few rows to serve (5000 cycles a tile).
-// The maximum is raised, and O rescaled, only where a row's scores pass it by
-// 2^8: P then reaches 2^8 at most, far inside fp16.
+// P refers to 2^-7 of a row's maximum, which is raised, and O rescaled, only where
+// scores pass it by 2^8: P then stays below 2^15, and a tail of tokens 2^-30 below the first one is still there. (Raised
+// at 2^6, for two places more: 4096 tokens causal 166 us.)
 //
 // Half precision's range: queries are scaled by a power of two per row, K by
 // one per 32 tokens where it leaves [2^-8, 2^15) (else none), or one a token where one for all would lose some; the softmax
@@ -431,6 +432,7 @@ struct __align__(16) PrMeta {
   uint32_t side;   // tokens whose values E does not fit: zeros in V's operand, the softmax adds them by itself
   uint32_t pad[3];
 };
+constexpr float kPrMost = 15.f, kPrLift = 7.f;  // log2 of the largest P; of P at a maximum that was raised
 constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at most two ahead of the softmax
 
 template <int D>
@@ -860,7 +862,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       const int lo_min = __reduce_min_sync(kFull, lo), lo_max = __reduce_max_sync(kFull, lo);
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
 
-      float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;
+      float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;  // m: what P refers to, 2^7 below the largest score when it was taken
       // Bit 0: a key that is not finite is seen; bit 1 + g: a value of group g. The same for all of a warp's rows: bits 29 and 30:
       // O's unit (pr_unit); bit 31: some values are summed apart.
       uint32_t rare = 0;
@@ -904,7 +906,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             pk[x] = pr_half2(p0, p1);
           }
           const float top = pr_max3(fmaxf(tp[0], tp[1]), tp[2], tp[3]) * ck;
-          const bool raise = top > m + 8.f;
+          const bool raise = top > m + kPrMost;
           if (!__any_sync(kFull, raise)) {
             pr_split(ll, l0, l1);
             pr_st16(s_t + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk));
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             c += 2;
             continue;
           }
-          const float up = raise ? top : m;
+          const float up = raise ? top - kPrLift : m;
           const float f = up == m ? 1.f : pr_ex2(m - up);
           m = up;
           mm = up == -INFINITY ? 0.f : up;
@@ -994,9 +996,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             tb = pr_max3(tb, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
           }
           const float top = pr_max3(fmaxf(ta, tb), __uint_as_float(v[30]), __uint_as_float(v[31])) * ck;
-          const bool raise = top > m + 8.f;
+          const bool raise = top > m + kPrMost;
           if (__any_sync(kFull, raise) || unit != pr_unit(rare)) {
-            const float up = raise ? top : m;
+            const float up = raise ? top - kPrLift : m;
             const float f = up == m ? 1.f : pr_ex2(m - up);
             m = up;
             mm = up == -INFINITY ? 0.f : up;

@@ -22,7 +22,7 @@
 // p s_g is rounded to fp16 (half a step 2^-12, a sixteenth of the bf16 output's, and of random sign); its exponent is kept in range by a power
 // of two 2^E per warp that follows the largest scale of a tile; scales far from it, in tokens that a column may not even see, are
 // multiplied apart. The maximum is only
-// raised when a score passes it by 2^8, so that most tiles need no reduction over the warp.
+// raised when a score passes it by 2^5, so that most tiles need no reduction over the warp.
 // What bounds it is the issue of instructions, not memory: 385 of them for 16 tokens of a head of 128, 55 for the
 // copies among them (taken out, no time was saved). 64 sequences of 512 to 16384 tokens, 8 key
 // heads of 128, 4 columns: 86 us, 3.9 TB/s (58 % of a copy's rate; issue slots 60 % full); one of 131071 tokens: 43 us, 3.5 TB/s
@@ -218,12 +218,14 @@ struct SplitAcc {
   float cs[NT][2];                // scale * log2(e) / 2^shift
   int hi[NT][2], lo[NT][2];       // the tokens that the columns see: lo <= t < hi
   float unit, inv;                // 2^E, 2^-E
-  uint32_t less;                  // minus the bits of 2^(E - 3), the smallest scale that 2^-E takes in
+  uint32_t less;                  // minus the bits of 2^E, the smallest scale that 2^-E takes in
 };
-// p s 2^-E has a place in fp16 for the scales s from 2^(E - 3) to 2^(E + 6): below 2^8 2^6, and 2^-25 of it is lost. E follows the
+// p s 2^-E has a place in fp16 for the scales s from 2^E to 2^(E + 9): p stays below 2^5, the product below 2^14, and only what is below
+// 2^-25 is lost: a tail of tokens 2^-25 below the first one is still there, whatever their scales. E follows the
 // largest scale of a tile, between -20 and 20, where fp32 has room for O in any such unit; scales that it does not take in (far
 // smaller than others of the tile, or very large) are multiplied apart.
-constexpr int kSplitTop = 5, kSplitMost = 20;
+constexpr int kSplitTop = 8, kSplitMost = 20;
+constexpr float kSplitRaise = 5.f;
 constexpr uint32_t kSplitSpan = 9u << 23;
 
 // Codes less 8 of dims 4g + j (row g) and 32 + 4g + j (row g + 8), from transposed words.
@@ -340,7 +342,7 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
       float top = s[0][n][k];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, mt ? fmaxf(s[mt][n][k], s[mt][n][2 + k]) : s[mt][n][2 + k]);
-      raise |= top * A.cs[n][k] > A.m[n][k] + 8.f;
+      raise |= top * A.cs[n][k] > A.m[n][k] + kSplitRaise;
     }
   // a scale of zero or with its sign set, an infinity or a NaN passes the span: looked at more closely there
   if (__any_sync(kFull, raise || big >= kSplitSpan)) {

@@ -101,3 +101,19 @@ def test_tokens_of_different_sizes(cuda_device, exps, new):
         # large keys: their scores stay within some tens
         q, out, lse = run(c, 4, scale=1.5 if which == VALUES else 1.5 * 2.0 ** -max(exps))
         attn_close(c, q, out, lse)
+
+
+@pytest.mark.parametrize("new", ROWS)
+@pytest.mark.parametrize("high", [6.0, 12.0, 16.0, 18.0])
+def test_a_flat_tail_behind_a_high_first_token(cuda_device, high, new):
+    """A first token that takes nearly all of the softmax and has a value of zeros: what a row gets is its tail's, thousands of
+    tokens whose probabilities are e^-high of the first one's."""
+    c = Case(cuda_device, [4000], [new], 1, 128, 16, seed=55)
+    for t in range(4000):
+        p, at = A.slot(t, 0, c.pages, 16, c.n_pages)
+        pair = O.bf16_to_f64(c.np[KEYS][p, :, at]) * 0.02
+        c.np[KEYS][p, :, at] = O.f64_to_bf16_bits(pair if t else pair * 0 + [0.0, high / (128 ** 0.5 * 0.8 * 1.5)])
+    times(c, VALUES, [0], 0.0)
+    q = bf16(c.rng, c.rows, 4, 128, dev=cuda_device, scale=1.5).abs()
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
+    attn_close(c, q, out, lse)
