@@ -38,6 +38,10 @@
  *     once before first use (the kernels leave their counters at zero).
  *   - bf16 values are passed as their uint16 bit patterns.
  *   - Calls sharing one workspace must not run concurrently.
+ *   - Weights (every bgq_qmatrix, expert and layer) are constants: a call may read
+ *     them before earlier work in its stream has ended. Whatever writes them must be
+ *     waited for on the host (a stream synchronisation) before the first call that
+ *     reads them. Inputs and outputs need no such wait.
  *   - Weights of moe_layer_forward, moe_stack_decode and moe_expert_swiglu
  *     (router, shared gate, expert pools, RMSNorm weights) may also live in
  *     pinned host memory mapped into the device address space (e.g. Grace
@@ -368,8 +372,10 @@ int32_t bgq_rope(const bgq_rope_plan* p, const uint16_t* x, int64_t x_stride, co
  *   k_q, v_q   : codes, uint32 [n_pages][kv_heads][page_size][head_dim/8], eight codes a word, the first in
  *                the lowest bits;
  *   k_sb, v_sb : bf16 (scale, bias) pairs [n_pages][kv_heads][page_size][head_dim/64][2].
- *   value = code*scale + bias, one pair for each 64 columns of a token's head
- *   (a page's head is a bgq_qmatrix of page_size rows).
+ *   value = code*scale + bias, one pair for each 64 columns of a token's head.
+ * The cache is written by earlier calls in the stream and belongs to the kv4
+ * calls: although a page's head is packed like a weight matrix, it must not be given to a call
+ * as its weights, which that call may read before the write has ended.
  * head_dim 64, 128 or 256; page_size a multiple of 16; kv_heads <= 256;
  * n_pages * kv_heads * (page_size / 16) below 2^31; all four arrays 16-byte
  * aligned device memory. */

@@ -1,0 +1,23 @@
+"""Rules that the attention operators state and keep, without a GPU."""
+
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "bit_group_quantized_gb300", "csrc")
+
+
+def text(*path):
+    return open(os.path.join(ROOT, *path), encoding="utf-8").read()
+
+
+def test_a_page_is_not_offered_as_weights():
+    """GEMVs read codes and scales ahead of their wait for earlier kernels; the cache is what an earlier kernel writes."""
+    gemv = text("bit_group_quantized_gb300", "csrc", "gemv.cu")
+    assert "pdl_wait();" in gemv
+    header = text("include", "bgq.h")
+    assert "is a bgq_qmatrix" not in header and "is a\n`bgq_qmatrix`" not in text("DESIGN.md")
+    about = header[header.index("A paged cache of keys and values in 4 bits"):header.index("typedef struct bgq_kv4_cache")]
+    assert re.search(r"must not be given to a call\s*\*?\s*as its weights", about)
+    rules = header[header.index("Conventions for every entry point"):header.index("#ifndef BGQ_H")]
+    assert "Weights (every bgq_qmatrix, expert and layer) are constants" in rules
