@@ -72,6 +72,12 @@ __device__ __forceinline__ void kv_rows(const Kv4View& v, int r0, int nr, long l
   if ((int)threadIdx.x < nr) at[threadIdx.x] = kv4_row_at(v, r0 + threadIdx.x);
   __syncthreads();
 }
+// 16 bytes that an earlier kernel may have written while this one was there already: not by the read-only path.
+__device__ __forceinline__ uint4 kv_load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 // Two fp32 values in a register pair: one instruction for both.
 __device__ __forceinline__ uint64_t kv_pair(float a, float b) {
   uint64_t d;
@@ -94,8 +100,8 @@ template <int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant__ bgq_kv4_cache c,
                                                            const __grid_constant__ Kv4View v,
                                                            const __grid_constant__ KvGeo g,
-                                                           const uint16_t* __restrict__ k, long long k_stride,
-                                                           const uint16_t* __restrict__ val, long long v_stride) {
+                                                           const uint16_t* k, long long k_stride,
+                                                           const uint16_t* val, long long v_stride) {
   __shared__ long long rows[kKvMaxRows];
   pdl_wait();
   pdl_trigger();
@@ -110,10 +116,10 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_append(const __grid_constant
     if (u < total) {
       const uint16_t* ks = k + (long long)(r0 + ku.row) * k_stride + col;
       const uint16_t* vs = val + (long long)(r0 + ku.row) * v_stride + col;
-      in[0][0] = ldg_stream16(ks);
-      in[0][1] = ldg_stream16(ks + 32);
-      in[1][0] = ldg_stream16(vs);
-      in[1][1] = ldg_stream16(vs + 32);
+      in[0][0] = kv_load16(ks);
+      in[0][1] = kv_load16(ks + 32);
+      in[1][0] = kv_load16(vs);
+      in[1][1] = kv_load16(vs + 32);
     } else {
       in[0][0] = in[0][1] = in[1][0] = in[1][1] = make_uint4(0, 0, 0, 0);
     }
@@ -204,9 +210,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv4_read(const __grid_constant__
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t* qs = (i ? c.v_q : c.k_q) + row * 8 + (ku.lane & 3);
-        q[i][0] = __ldg(qs);
-        q[i][1] = __ldg(qs + 4);
-        sb[i] = __ldg(reinterpret_cast<const uint32_t*>(i ? c.v_sb : c.k_sb) + row);
+        q[i][0] = __ldcg(qs);
+        q[i][1] = __ldcg(qs + 4);
+        sb[i] = __ldcg(reinterpret_cast<const uint32_t*>(i ? c.v_sb : c.k_sb) + row);
       }
     } else {
       q[0][0] = q[0][1] = q[1][0] = q[1][1] = sb[0] = sb[1] = 0;

@@ -1418,10 +1418,10 @@ __global__ void __launch_bounds__(kJoinThreads * PG) k_prompt_join(const __grid_
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const float* pp = part(min(c + k * PG, cut.c1));
-        mc[k] = __ldg(pp + 128 * D + r);
-        lc[k] = __ldg(pp + 128 * D + 128 + r);
+        mc[k] = __ldcg(pp + 128 * D + r);
+        lc[k] = __ldcg(pp + 128 * D + 128 + r);
 #pragma unroll
-        for (int x = 0; x < Q; ++x) p[k][x] = __ldg(reinterpret_cast<const float4*>(pp) + (d4 + x) * 128 + r);
+        for (int x = 0; x < Q; ++x) p[k][x] = __ldcg(reinterpret_cast<const float4*>(pp) + (d4 + x) * 128 + r);
       }
 #pragma unroll
       for (int k = 0; k < U; ++k)

@@ -36,7 +36,7 @@ struct RopeGeo {
 template <bool HALF>
 __global__ void __launch_bounds__(kRopeMaxThreads) k_rope(const __grid_constant__ bgq_rope_plan p,
                                                        const __grid_constant__ RopeGeo g, const uint16_t* x, long long x_stride,
-                                                       const int32_t* __restrict__ pos,
+                                                       const int32_t* pos,
                                                        long long pos_stride, int tokens, uint16_t* y,
                                                        long long y_stride, float sign) {
   // cos and sin of two pairs side by side, [tb][pairs of a unit / 2][units of a head]: threads on neighbouring units read

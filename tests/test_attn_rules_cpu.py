@@ -21,3 +21,11 @@ def test_a_page_is_not_offered_as_weights():
     assert re.search(r"must not be given to a call\s*\*?\s*as its weights", about)
     rules = header[header.index("Conventions for every entry point"):header.index("#ifndef BGQ_H")]
     assert "Weights (every bgq_qmatrix, expert and layer) are constants" in rules
+
+
+def test_no_read_only_loads_of_what_earlier_kernels_write():
+    """The kernels start while the one before still runs, so nothing that they read is constant for as long as they live."""
+    for name in ("kv4.cu", "kv4_split.cu", "kv4_prompt.cu", "rope.cu", "attn.h"):
+        code = re.sub(r"//.*", "", open(os.path.join(CSRC, name)).read())
+        assert "__ldg" not in code and "ldg_stream" not in code and "global.nc" not in code, name
+        assert not re.search(r"const\s+\w+\s*\*\s*__restrict__", code), name
