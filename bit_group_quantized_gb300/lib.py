@@ -431,7 +431,9 @@ _device = torch._C._cuda_getDevice
 
 
 def _there(index, stream):
-    """Makes a call's device current, and the given stream, to which the buffers that the binding creates then belong."""
+    """Makes a call's device current, and the given stream of that device, to which the buffers that the binding creates then
+    belong."""
+    _need(stream is None or stream.device.index == index, "the stream must be one of the tensors' device")
     return torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
 
