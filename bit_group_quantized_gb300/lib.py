@@ -402,6 +402,12 @@ def _need(ok: bool, what: str):
         raise BGQError(ERR_INVALID_ARG, what)
 
 
+def _int32(v, what: str) -> int:
+    """v, refused where it would lose bits on its way into an int32."""
+    _need(-1 << 31 <= v < 1 << 31, what)
+    return v
+
+
 def _on(t, dtype, index, dims: int, what: str):
     """t is a tensor of this type and rank on CUDA device `index` (None: any)."""
     _need(isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dims
@@ -444,6 +450,8 @@ class RopePlan:
     def __init__(self, head_dim: int, rot_dim: int, theta: float, sections, pairs: bool = False, cycle: bool = False,
                  restart: bool = False):
         self.c = bgq_rope_plan()
+        for v in (head_dim, rot_dim, *sections):
+            _int32(v, "RopePlan: head_dim, rot_dim and sections must fit in 32 bits")
         _check(load().bgq_rope_init(C.byref(self.c), head_dim, rot_dim, theta, len(sections),
                                     (_I * max(len(sections), 1))(*sections),
                                     int(pairs) | 2 * int(cycle) | 4 * int(restart)), "bgq_rope_init")
@@ -525,7 +533,8 @@ class KV4Seqs:
             _need(q_start.shape[0] == B + 1 and q_start.is_contiguous() and rows is not None,
                   "KV4Seqs: q_start must be [batch+1], contiguous, with rows given")
         self.kv_len, self.pages, self.q_start, self.index = kv_len, pages, q_start, dev
-        self.rows = B if rows is None else rows
+        self.rows = _int32(B if rows is None else rows, "KV4Seqs: rows must fit in 32 bits")
+        _int32(max_q, "KV4Seqs: max_q must fit in 32 bits")
         self.c = bgq_kv4_seqs(None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
                               None if pages is None else pages.data_ptr(), B,
                               0 if pages is None else pages.shape[1], self.rows, max_q)
@@ -569,6 +578,7 @@ def bgq_kv4_read(cache: KV4Cache, seqs: KV4Seqs, k: torch.Tensor | None = None, 
 
 
 def kv4_attention_workspace_bytes(cache: KV4Cache, seqs: KV4Seqs, q_heads: int) -> int:
+    _int32(q_heads, "kv4_attention_workspace_bytes: q_heads must fit in 32 bits")
     return load().bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, q_heads)
 
 
@@ -584,6 +594,7 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
             return bgq_kv4_attention(cache, seqs, q, scale, causal, window, out, lse, want_lse, ws)
     _, H, sq = _heads(q, rows, None, d, dev, "bgq_kv4_attention: q must be bf16 [rows][q_heads][head_dim] beside the cache")
     _need(seqs.index == dev, "bgq_kv4_attention: the sequences must be beside the cache")
+    _int32(window, "bgq_kv4_attention: window must fit in 32 bits")
     if out is None:
         out = alloc((rows, H, d), _BF16, cache.device)
     so = _heads(out, rows, H, d, dev, "bgq_kv4_attention: out must be a bf16 tensor like q")[2]

@@ -1,0 +1,25 @@
+"""What the binding of the attention operators refuses, and takes, on a GPU."""
+
+import pytest
+import torch
+
+from bit_group_quantized_gb300 import lib
+from tests.test_gpu_attn import Case, bf16
+
+pytestmark = pytest.mark.gpu
+
+
+def test_numbers_beyond_32_bits_are_refused(cuda_device):
+    """A window of 2^32 + 5 is not one of 5."""
+    c = Case(cuda_device, [50], [1], 2, 64, 16, seed=60)
+    q = bf16(c.rng, 1, 4, 64, dev=cuda_device)
+    cache, seqs = c.cache(), c.seqs()
+    for window in (2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(lib.BGQError) as e:
+            lib.bgq_kv4_attention(cache, seqs, q, window=window)
+        assert e.value.status == lib.ERR_INVALID_ARG
+    for kw in (dict(rows=2 ** 32 + 1), dict(rows=1, max_q=2 ** 32 + 1)):
+        with pytest.raises(lib.BGQError):
+            lib.KV4Seqs(seqs.kv_len, pages=seqs.pages, q_start=seqs.q_start, **kw)
+    with pytest.raises(lib.BGQError):
+        lib.kv4_attention_workspace_bytes(cache, seqs, 2 ** 32 + 4)
