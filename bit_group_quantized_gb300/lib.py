@@ -607,7 +607,7 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
         return out, lse
     if ws is None:
         ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
-    _need(ws.get_device() == dev, "bgq_kv4_attention: ws must be beside the cache")
+    _need(ws.get_device() == dev and ws.is_contiguous(), "bgq_kv4_attention: ws must be beside the cache, contiguous")
     r = lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), sq, H, d ** -0.5 if scale is None else scale, causal, window,
                               out.data_ptr(), so, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
                               _raw_stream(dev))

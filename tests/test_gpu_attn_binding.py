@@ -23,3 +23,15 @@ def test_numbers_beyond_32_bits_are_refused(cuda_device):
             lib.KV4Seqs(seqs.kv_len, pages=seqs.pages, q_start=seqs.q_start, **kw)
     with pytest.raises(lib.BGQError):
         lib.kv4_attention_workspace_bytes(cache, seqs, 2 ** 32 + 4)
+
+
+def test_a_workspace_that_only_seems_large_is_refused(cuda_device):
+    """An expanded tensor has the bytes of its shape to its name, not to its memory; a strided one has holes that belong to others."""
+    c = Case(cuda_device, [50], [1], 2, 64, 16, seed=61)
+    q = bf16(c.rng, 1, 4, 64, dev=cuda_device)
+    cache, seqs = c.cache(), c.seqs()
+    need = lib.kv4_attention_workspace_bytes(cache, seqs, 4)
+    for ws in (torch.zeros(256, dtype=torch.uint8, device=cuda_device)[:1].expand(need), torch.zeros(2 * need, dtype=torch.uint8, device=cuda_device)[::2]):
+        with pytest.raises(lib.BGQError) as e:
+            lib.bgq_kv4_attention(cache, seqs, q, ws=ws)
+        assert e.value.status == lib.ERR_INVALID_ARG
