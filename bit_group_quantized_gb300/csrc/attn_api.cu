@@ -117,7 +117,7 @@ int32_t bgq_rope(const bgq_rope_plan* p, const uint16_t* x, int64_t x_stride, co
   if (heads > 1024) return BGQ_ERR_UNSUPPORTED;
   const int64_t width = (int64_t)heads * p->head_dim;
   if ((r = check_rows(x, x_stride, width)) || (r = check_rows(y, y_stride, width))) return r;
-  if (!pos || !al(pos, 4) || pos_stride < 0 || (p->n_axes > 1 && pos_stride < tokens)) return BGQ_ERR_INVALID_ARG;
+  if (!pos || !al(pos, 4) || pos_stride < 0 || (p->n_axes > 1 && pos_stride && pos_stride < tokens)) return BGQ_ERR_INVALID_ARG;
   if (x == y && x_stride != y_stride) return BGQ_ERR_INVALID_ARG;
   if (tokens == 0) return BGQ_OK;
   return cuda_status(launch_rope(*p, x, x_stride, pos, pos_stride, tokens, heads, y, y_stride, inverse != 0, st(stream)));

@@ -462,8 +462,8 @@ class RopePlan:
 def bgq_rope(plan: RopePlan, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor | None = None,
              inverse: bool = False, stream=None) -> torch.Tensor:
     """bgq_rope: x bf16 [tokens][heads][head_dim] (tokens may lie further
-    apart), pos int32 [n_axes][tokens] ([tokens] for one axis) -> y (x itself
-    is allowed). inverse: the gradient's direction."""
+    apart), pos int32 [n_axes][tokens] ([tokens] for one axis; expanded over
+    the axes where they share it) -> y (x itself is allowed). inverse: the gradient's direction."""
     T, H, sx = _heads(x, None, None, plan.head_dim, None, "bgq_rope: x must be a CUDA bf16 tensor [tokens][heads][head_dim]")
     dev = x.get_device()
     if stream is not None or _device() != dev:

@@ -362,7 +362,8 @@ int32_t bgq_rope_init(bgq_rope_plan* p, int32_t head_dim, int32_t rot_dim, doubl
  * [head_dim], tokens x_stride / y_stride values apart (multiples of 8, at
  * least heads*head_dim: the query and key heads of a fused projection's output
  * can be turned where they stand). y may be x (with the same stride); any other overlap
- * is not allowed. pos: int32 [n_axes][pos_stride], axis by axis, any values.
+ * is not allowed. pos: int32 [n_axes][pos_stride], axis by axis, any values; pos_stride
+ * at least tokens, or 0 where all axes have the same positions (plain text).
  * inverse != 0 turns the other way: the gradient with respect to x of a
  * forward call, given the gradient of y. tokens may be 0; heads <= 1024. */
 int32_t bgq_rope(const bgq_rope_plan* p, const uint16_t* x, int64_t x_stride, const int32_t* pos, int64_t pos_stride,

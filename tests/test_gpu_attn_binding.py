@@ -35,3 +35,14 @@ def test_a_workspace_that_only_seems_large_is_refused(cuda_device):
         with pytest.raises(lib.BGQError) as e:
             lib.bgq_kv4_attention(cache, seqs, q, ws=ws)
         assert e.value.status == lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_rope_positions_shared_by_all_axes(cuda_device, tokens):
+    """Positions of plain text, expanded over the axes: the bits of a copy for each."""
+    rng = torch.Generator().manual_seed(62)
+    x = bf16(rng, tokens, 3, 64, dev=cuda_device)
+    plan = lib.RopePlan(64, 64, 10000.0, [12, 10, 10])
+    pos = torch.randint(0, 5000, (tokens,), generator=rng, dtype=torch.int32).to(cuda_device)
+    want = lib.bgq_rope(plan, x, pos.repeat(3, 1))
+    assert torch.equal(lib.bgq_rope(plan, x, pos.expand(3, tokens)), want)
