@@ -582,6 +582,17 @@ def kv4_attention_workspace_bytes(cache: KV4Cache, seqs: KV4Seqs, q_heads: int) 
     return load().bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, q_heads)
 
 
+def kv4_attention_workspace(cache: KV4Cache, seqs: KV4Seqs, q_heads: int) -> torch.Tensor:
+    """A workspace for such calls. Only the status and arrival counters at its start need to be zero: a large one (prompts' have
+    20 to 40 MB) is zero-filled there alone, a small one as a whole, which is the cheaper call."""
+    n = kv4_attention_workspace_bytes(cache, seqs, q_heads)
+    if n <= 8 << 20:
+        return workspace(n, cache.device)
+    ws = alloc((n,), torch.uint8, cache.device)
+    ws[:4096].zero_()
+    return ws
+
+
 def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: float | None = None,
                       causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
                       lse: torch.Tensor | None = None, want_lse: bool = False, ws: torch.Tensor | None = None,
@@ -606,7 +617,7 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
     if rows == 0:
         return out, lse
     if ws is None:
-        ws = workspace(lib.bgq_kv4_attention_workspace_bytes(cache.ref, seqs.ref, H), cache.device)
+        ws = kv4_attention_workspace(cache, seqs, H)
     _need(ws.get_device() == dev and ws.is_contiguous(), "bgq_kv4_attention: ws must be beside the cache, contiguous")
     r = lib.bgq_kv4_attention(cache.ref, seqs.ref, q.data_ptr(), sq, H, d ** -0.5 if scale is None else scale, causal, window,
                               out.data_ptr(), so, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,

@@ -446,7 +446,8 @@ int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k,
  * q, nor lse anything.
  * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
  * max_q, max_pages and heads; a few MB for single tokens, up to 160 MB for prompts,
- * whatever their length). Calls of any shapes may share one that is large
+ * whatever their length), of which the first 4096 must be zero before the first call. Calls of any shapes
+ * may share one that is large
  * enough for each, one after the other; calls of other entry points may not,
  * unless it is zero-filled between. The same inputs give the same bits. */
 size_t bgq_kv4_attention_workspace_bytes(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, int32_t q_heads);

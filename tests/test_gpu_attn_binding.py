@@ -46,3 +46,27 @@ def test_rope_positions_shared_by_all_axes(cuda_device, tokens):
     pos = torch.randint(0, 5000, (tokens,), generator=rng, dtype=torch.int32).to(cuda_device)
     want = lib.bgq_rope(plan, x, pos.repeat(3, 1))
     assert torch.equal(lib.bgq_rope(plan, x, pos.expand(3, tokens)), want)
+
+
+@pytest.mark.parametrize("kv,new,hq,hkv,d", [([700], [700], 8, 2, 128), ([3000, 90], [1, 1], 8, 2, 64), ([20000], [1], 16, 1, 256), ([900, 40], [33, 5], 8, 1, 256)])
+def test_only_the_head_of_a_workspace_is_zero_filled(cuda_device, guard_canaries, kv, new, hq, hkv, d):
+    """Calls do with any bytes behind the first 4096, and a call without a workspace fills no large one."""
+    c = Case(cuda_device, kv, new, hkv, d, 16, seed=63)
+    q = bf16(c.rng, c.rows, hq, d, dev=cuda_device)
+    cache, seqs = c.cache(), c.seqs()
+    asked = []
+
+    def allocator(shape, dtype, device, zero):
+        asked.append((torch.empty(0, dtype=dtype).element_size() * torch.Size(shape).numel(), zero))
+        return guard_canaries(shape, dtype, device, zero)
+
+    lib.set_allocator(allocator)
+    want, lse = lib.bgq_kv4_attention(cache, seqs, q, want_lse=True)
+    assert max(n for n, _ in asked) > 4096 and all(n <= 8 << 20 for n, zero in asked if zero)
+    ws = lib.kv4_attention_workspace(cache, seqs, hq)
+    for fill in (0xff, 0x7f, 0x01):
+        ws[4096:] = fill
+        for _ in range(2):
+            out, l = lib.bgq_kv4_attention(cache, seqs, q, want_lse=True, ws=ws)
+            assert torch.equal(out, want) and torch.equal(l, lse)
+    assert lib.read_device_status(ws) == lib.OK
