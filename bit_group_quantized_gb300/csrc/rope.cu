@@ -2,8 +2,8 @@
 //
 // Pair i of a head, (a, b), turns by the angle t = pos[axis(i)] * f_i:
 // (a cos t - b sin t, a sin t + b cos t). The plan holds f_i in turns (f_i / 2 pi) as a 64-bit
-// fixed-point fraction, so pos * f_i modulo 2^64 is the angle's fraction of a
-// turn to 2^-63, exact at any position: far positions lose nothing, and no
+// fixed-point fraction, off by at most 2^-54 as it comes from a double (theta >= 1). The product pos * f_i modulo 2^64 is exact, so
+// the angle is off by |pos| 2^-54 turns (2^-23 at the farthest positions, 2^-34 at a million), and no
 // range reduction is left to do. Its upper 32 bits go to sincospi.
 //
 // Bound by memory (2 bytes in, 2 bytes out per value). A block takes whole

@@ -338,8 +338,9 @@ int32_t bgq_gemv_chain(const bgq_qmatrix* W, int32_t n, const uint16_t* x, int32
  * BGQ_ROPE_CYCLE pair i belongs to axis a = i mod n_axes where i / n_axes <
  * sections[a], else to axis 0. With BGQ_ROPE_RESTART the frequencies start
  * again in every section: f = theta^(-j/sections[a]) for its pair j.
- * The angle is held as a 64-bit fixed-point fraction of a turn, exact at any
- * int32 position; the result is computed in fp32 and rounded once to bf16.
+ * The frequencies are worked out in double precision (off by at most 2^-54 of a turn a position
+ * for theta >= 1) and held as 64-bit fixed-point fractions of a turn, so that the angle at any int32 position
+ * is off by no more than |pos| * 2^-54 turns; the result is computed in fp32 and rounded once to bf16.
  *
  * bgq_rope_init fills a HOST struct from HOST arguments (sections: n_axes
  * counts with sum rot_dim/2; theta > 0 and finite); it makes no CUDA call.
