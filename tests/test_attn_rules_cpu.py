@@ -42,10 +42,11 @@ def test_rotary_frequencies_keep_the_stated_bound():
     getcontext().prec = 60
     pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
     for theta in (1.0, 1.5, 100.0, 10000.0, 5e5, 1e6, 1e12):
-        for rot in (16, 64, 96, 128, 256):
+        ln = Decimal(theta).ln()
+        for rot in (16, 96, 128, 256):
             plan = lib.RopePlan(256, rot, theta, [rot // 2]).c
             for i in range(rot // 2):
-                turn = (-(Decimal(2 * i) / Decimal(rot)) * Decimal(theta).ln()).exp() / (2 * pi)
+                turn = (-(Decimal(2 * i) / Decimal(rot)) * ln).exp() / (2 * pi)
                 off = abs(Decimal(int(plan.freq[i])) / Decimal(2) ** 64 - turn)
                 assert off <= Decimal(2) ** -54, (theta, rot, i, math.log2(off))
     header = text("include", "bgq.h")
