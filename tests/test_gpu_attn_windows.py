@@ -41,3 +41,24 @@ def test_length_far_beyond_the_page_list(cuda_device, new):
         assert not o.any() and torch.isneginf(l).all()
         o, l = lib.bgq_kv4_attention(cache, seqs, q, causal=False, want_lse=True)
         attn_close(c, q, o, l, causal=False)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+@pytest.mark.parametrize("first,end", [(0, 2 ** 29), (0, 2 ** 31 - 1), (1, 2 ** 30 + 1), (-(2 ** 31), 2 ** 31 - 1)])
+def test_sequences_of_more_rows_than_the_call_has(cuda_device, max_q, first, end):
+    """Row starts far beyond the rows: the rows there are belong to the sequence, at the negative positions that its length gives them,
+    where they see nothing; with a mask that hides none they see all."""
+    c = Case(cuda_device, [96], [3], 2, 128, 16, seed=43, behind=2)
+    q = bf16(c.rng, c.rows, 8, 128, dev=cuda_device)
+    s = c.seqs()
+    seqs = lib.KV4Seqs(s.kv_len, rows=c.rows, pages=s.pages, q_start=torch.tensor([first, end], dtype=torch.int32, device=cuda_device), max_q=max_q)
+    out, lse = torch.full_like(q, 7.0), torch.full((c.rows, 8), 7.0, device=cuda_device)
+    lib.bgq_kv4_attention(c.cache(), seqs, q, out=out, lse=lse)
+    own = slice(max(first, 0), c.rows) if first > -2 ** 31 else slice(0, 0)  # 2^32 - 1 rows are none that a position has
+    assert not out[own].any() and torch.isneginf(lse[own]).all()
+    assert (out[:own.start] == 7.0).all()
+    if first < 0:
+        return
+    lib.bgq_kv4_attention(c.cache(), seqs, q, causal=False, out=out, lse=lse)
+    c.q_start = [first, c.rows]
+    attn_close(c, q, out, lse, causal=False)
