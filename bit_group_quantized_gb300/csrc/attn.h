@@ -48,7 +48,7 @@ __device__ __forceinline__ Span kv4_span(const Kv4View& v, int b) {
   Span s;
   s.first = v.q_start ? v.q_start[b] : b;
   const int end = v.q_start ? v.q_start[b + 1] : b + 1;
-  s.q_len = (int)min(max((long long)end - s.first, 0ll), 0x7fffffffll);
+  s.q_len = end > s.first ? (int)min((uint32_t)end - (uint32_t)s.first, 0x7fffffffu) : 0;
   s.kv_len = max(v.kv_len[b], 0);
   s.held = s.kv_len > v.cap ? (int)v.cap : s.kv_len;
   return s;

@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
 
   for (; wk.live(); wk.next(a)) {
     const int h = wk.h, col0 = wk.rt * C;
-    const int ncol = min(C, min(wk.q.sp.q_len, a.v.rows) * group - col0);  // rows * group is below 2^31
+    // a sequence's columns may pass 2^32 where it claims more rows than there are
+    const int ncol = __umulhi(wk.q.sp.q_len, group) ? C : (int)min((unsigned)C, (unsigned)wk.q.sp.q_len * group - col0);
     const int pos0 = wk.q.sp.kv_len - wk.q.sp.q_len;
 
     // ---- the query: fp16 fragments of column g, scaled by a power of two
