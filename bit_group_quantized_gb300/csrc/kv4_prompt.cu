@@ -753,7 +753,7 @@ __device__ __noinline__ float pr_query_scale(const AttnArgs& a, unsigned char* t
   uint32_t top = 0;  // the largest magnitude's bits: without their signs they order like values (NaN is passed over)
 #pragma unroll
   for (int k = 0; k < 4; ++k) top = max(top, max(t2[k] & 0x7fff0000u, t2[k] << 17 >> 1));
-  const int e = top && top < 0x7f800000u ? min(max((int)(top >> 23) - 130, -110), 110) : 0;
+  const int e = top && top < 0x7f800000u ? min(max((int)(top >> 23) - 130, -110), 124) : 0;
   const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {
@@ -779,7 +779,7 @@ __device__ __noinline__ float pr_query_scale(const AttnArgs& a, unsigned char* t
     }
     *reinterpret_cast<uint2*>(extra + pr_extra(r, g >> 1) + (g & 1) * 8) = x;
   }
-  return fabsf(a.scale) * 1.4426950408889634f * exp2i(e);
+  return fminf(fabsf(a.scale) * 1.4426950408889634f * exp2i(e), 3e38f);
 }
 
 template <int D>

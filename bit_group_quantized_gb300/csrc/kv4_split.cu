@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
       // largest magnitude into [8, 16): fp16 keeps 2^-28 of it
-      const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 110) : 0;
+      const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 130, -110), 124) : 0;
       const float up = a.scale < 0.f ? -exp2i(-e) : exp2i(-e);
       float sum[G];
 #pragma unroll
@@ -728,8 +728,8 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
         const int from = (2 * c + k) * 4;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) xs[n][k][gr] = __shfl_sync(kFull, sum[gr], from);
-        // at least the smallest normal number, so that -infinity times it stays -infinity
-        A.cs[n][k] = fmaxf(fabsf(a.scale) * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from)), 0x1p-126f);
+        // at least the smallest normal number, so that -infinity times it stays -infinity, and finite, so that zero times it stays zero
+        A.cs[n][k] = fminf(fmaxf(fabsf(a.scale) * 1.4426950408889634f * exp2i(__shfl_sync(kFull, e, from)), 0x1p-126f), 3e38f);
         const int cc = n * 8 + 2 * c + k, jj = (col0 + cc) / group;
         const int pos = pos0 + jj;
         // columns behind the last see what the first one sees, and are dropped at the end
