@@ -34,12 +34,13 @@
 //
 // Half precision's range: queries are scaled by a power of two per row, K by
 // one per 32 tokens where it leaves [2^-8, 2^15) (else none), or one a token where one for all would lose some; the softmax
-// undoes it in the scores' factors. V is
-// scaled by one of three powers of two per 32 tokens, O's unit. Tokens that it does not fit (a group far smaller or larger than a
-// value's usual size) and blocks of another unit than O's are left out of the product, and their softmax thread adds p V in fp32,
-// slowly: no row's result depends on the size of values that it does not see, or of another group's. This costs ordinary values
-// 1 to 3 % (4096 tokens causal: 152.7 us, 148.1 with one exponent for all that a row had met, which lost small ones beside large; the
-// functions of the rare paths are not inlined: 154.2).
+// undoes it in the scores' factors. A group of 64 columns of V is
+// scaled by one of three powers of two per 32 tokens, the unit of those columns of O. Tokens that it does not fit (far smaller or
+// larger than the others' values) and blocks of other units than O's are left out of the product, and their softmax thread adds p V
+// in fp32, slowly: no row's result depends on the size of values that it does not see, or of another group's. This costs ordinary
+// values 1 to 3 % (4096 tokens causal: 152.5 us, 147.6 with one exponent for all that a row had met, which lost small values beside
+// large ones; the functions of the rare paths are not inlined: 154.2). In 4096 tokens, values of 2^-24 in one group of two: 261 us; in one token of
+// 32: 1.8 ms; values of 2^-40 throughout, which no unit fits: 15 ms.
 // A key or value pair that is not finite is stored as zeros, and the rows that see it are made NaN at the end.
 //
 // All (unit, key head, 128 tokens) triples form one list, which k_prompt_plan lays out from
@@ -416,21 +417,23 @@ __device__ __forceinline__ uint4 pr_values(uint32_t w, uint32_t off, uint32_t s2
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The values of a block of 32 tokens are held in fp16 divided by 2^E, one of three E by a rule on the pairs alone: a token fits
-// where each of its groups' 16 |s| + |b| (which no value passes) is zero or in [2^(E - 8), 2^(E + 15)); there fp16 keeps
-// 2^-17 of a group's size, whatever the sizes beside it. The usual one is for 2^-14 to 2^9.
-constexpr int kVe = -6;
-constexpr int kVeStep = 20;   // the others: kVe - 20 and kVe + 20, for 2^-34 to 2^-11 and 2^6 to 2^29
-constexpr int kVeNone = 127;  // no token of the block has a value but zero that an E fits
+// A group of 64 columns of 32 tokens' values is held in fp16 divided by 2^E, one of three E by a rule on the pairs alone: a token
+// fits where its 16 |s| + |b| (which no value of the group passes) is zero or in [2^(E - 8), 2^(E + 15)); there fp16 keeps
+// 2^-17 of it, whatever the sizes beside it. The usual one is for 2^-14 to 2^9. E by two bits, of which a word has one pair a group:
+constexpr int kVe = -6, kVeStep = 20;  // 0: kVe; 1: kVe - 20, for 2^-34 to 2^-11; 2: kVe + 20, for 2^6 to 2^29;
+constexpr uint32_t kVeNone = 3;        // no token has a value but zero that any E fits
+__device__ __forceinline__ int pr_unit(uint32_t word, int g) {
+  const uint32_t k = word >> 2 * g & 3;
+  return kVe + (k == 1 ? -kVeStep : k == 2 ? kVeStep : 0);
+}
 // What the softmax needs to know of 32 tokens. `odd` is zero for tokens all there, in half precision's range and
 // finite: then nothing else is looked at.
 struct __align__(16) PrMeta {
   float kf;        // 2^E of the keys: a score's factor; 0: each token has its own
-  int ve;          // E of the values
+  uint32_t ve;     // E of the values' groups
   uint32_t gap;    // tokens that are absent
   uint32_t bad;    // whether any pair is not finite (then the masks below)
-  uint32_t side;   // tokens whose values E does not fit: zeros in V's operand, the softmax adds them by itself
-  uint32_t pad[3];
+  uint32_t side[4];  // by group: tokens whose values E does not fit, zeros in V's operand; the softmax adds them by itself
 };
 constexpr float kPrMost = 15.f, kPrLift = 7.f;  // log2 of the largest P; of P at a maximum that was raised
 constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at most two ahead of the softmax
@@ -577,46 +580,60 @@ __device__ __forceinline__ int pr_key_range(const uint32_t (&sb)[D / kGroup], bo
   mix = __any_sync(kFull, apart);
   return min(max((apart ? it : top) - 127 - 13, -120), 120);
 }
-// E of odd values: the one of three that fits most of the block's tokens. `side`: the tokens that it does not fit.
+// E of odd values' groups, each the one of three that fits most of the block's tokens. `side`: by group, the tokens that it does not fit.
 template <int D>
-__device__ __forceinline__ int pr_value_range(const uint32_t (&sb)[D / kGroup], uint32_t& side, uint32_t& any, uint32_t (&bad)[D / kGroup]) {
-  uint32_t fit = 7;  // bit i: kVe + (0, -1, 1)[i] * kVeStep
-  bool some = false;
+__device__ __forceinline__ uint32_t pr_value_range(const uint32_t (&sb)[D / kGroup], uint32_t (&side)[D / kGroup], uint32_t& any,
+                                                   uint32_t (&bad)[D / kGroup]) {
+  uint32_t word = 0;
 #pragma unroll
   for (int g = 0; g < D / kGroup; ++g) {
     bool fin;
     const uint32_t top = pr_top(sb[g], fin);
     bad[g] = __ballot_sync(kFull, !fin);
     any |= bad[g];
-    if (top) {
-      some = true;
-      if (top - kValueLow >= 23u << 23) fit &= ~1u;
-      if (top - (kValueLow - ((uint32_t)kVeStep << 23)) >= 23u << 23) fit &= ~2u;
-      if (top - (kValueLow + ((uint32_t)kVeStep << 23)) >= 23u << 23) fit &= ~4u;
+    uint32_t f = 0, k = kVeNone;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t low = kValueLow + (uint32_t)((i == 1 ? -kVeStep : i == 2 ? kVeStep : 0) * (1 << 23));
+      const uint32_t fits = __ballot_sync(kFull, top && top - low < 23u << 23);
+      if (__popc(fits) > __popc(f)) {
+        f = fits;
+        k = i;
+      }
     }
+    side[g] = __ballot_sync(kFull, top != 0) & ~f;
+    word |= k << 2 * g;
   }
-  if (!some) fit = 0;
-  const uint32_t f0 = __ballot_sync(kFull, fit & 1), f1 = __ballot_sync(kFull, fit & 2), f2 = __ballot_sync(kFull, fit & 4);
-  const int n0 = __popc(f0), n1 = __popc(f1), n2 = __popc(f2);
-  const bool usual = n0 >= n1 && n0 >= n2, small = n1 >= n2;
-  const uint32_t f = usual ? f0 : small ? f1 : f2;
-  side = __ballot_sync(kFull, some) & ~f;
-  return !f ? kVeNone : usual ? kVe : small ? kVe - kVeStep : kVe + kVeStep;
+  return word;
 }
-// O's unit, by bits 29 and 30 of a softmax thread's notes.
-__device__ __forceinline__ int pr_unit(uint32_t rare) {
-  const uint32_t k = rare >> 29 & 3;
-  return k == 0 ? kVe : k == 1 ? kVe - kVeStep : kVe + kVeStep;
+// O of the warp's rows in other units: rare.
+template <int D>
+__device__ __noinline__ void pr_rescale(uint32_t t, uint32_t from, uint32_t to) {
+#pragma unroll 1
+  for (int d = 0; d < D; d += 8) {
+    const float f = exp2i(pr_unit(from, d / kGroup) - pr_unit(to, d / kGroup));  // at most 2^40 either way, which fp32 has to spare
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(r, 0) : "r"(t + d));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
+#pragma unroll
+    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
+  }
+  pr_wait_st();
 }
-// Values that V's operand leaves out. They are summed in fp32 from their codes, in units of 1, in the place for a part that the CTA's
-// segment has (whole units have the one that only the share's last unit writes): `sums`, the row's columns four by four,
-// 512 floats apart, and, where a part has its maximum, the one that their probabilities refer to.
+// Values that V's operand leaves out. They are summed in fp32 from their codes, in units of 2^15 (as P may be that large), in the place
+// for a part that the CTA's segment has (whole units have the one that only the share's last unit writes): `sums`, the row's columns
+// four by four, 512 floats apart, and, where a part has its maximum, what their probabilities refer to.
 template <int D>
 __device__ __forceinline__ float* pr_side_max(float* sums, int r) { return sums - r * 4 + 128 * D + r; }
-// Adds some of a block's tokens, which are all there. `score` is the row's scores of the block in tensor memory.
+struct PrMask4 {
+  uint32_t of[4];
+};
+// Adds some of a block's tokens, by group, which are all there. `score` is the row's scores of the block in tensor memory.
 template <int D>
-__device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int t, uint32_t side, uint32_t see, uint32_t score, float ck, float m,
-                                        float* sums, int r, bool more) {
+__device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int t, PrMask4 side, uint32_t see, uint32_t score, float ck, float m,
+                                     float* sums, int r, bool more) {
+  const int lane = threadIdx.x & 31;
   int b = row0;
   if (a.v.q_start) {  // the last sequence that starts at or before the row
     int lo = 0, hi = a.v.batch;
@@ -628,40 +645,46 @@ __device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int 
   }
   b = __shfl_sync(kFull, b, 0);
   const int h = __shfl_sync(kFull, pr_by_group(a, head), 0);
-  const float mm = m == -INFINITY ? 0.f : m, was = more ? *pr_side_max<D>(sums, r) : m, f = was == m ? 1.f : pr_ex2(was - m);
+  uint32_t some = 0;
+#pragma unroll
+  for (int g = 0; g < D / kGroup; ++g) some |= side.of[g];
+  const int page = some >> lane & 1 ? kv4_page(a.v, b, t + lane) : -1;
+  const long long mine = page < 0 ? 0 : ((long long)page * a.c.kv_heads + h) * a.c.page_size + (t + lane) % a.c.page_size;  // the lane's token
+  const float mm = (m == -INFINITY ? 0.f : m) + kPrMost, was = more ? *pr_side_max<D>(sums, r) : m, f = was == m ? 1.f : pr_ex2(was - m);
   *pr_side_max<D>(sums, r) = m;
 #pragma unroll 1
-  for (int d = 0; d < D; d += 8) {
-    float acc[8] = {};
+  for (int d = 0; d < D; d += 32) {
     float4* const at = reinterpret_cast<float4*>(sums + d / 4 * 512);
-    if (more) {
-      const float4 lo = at[0], hi = at[128];
-      acc[0] = lo.x * f; acc[1] = lo.y * f; acc[2] = lo.z * f; acc[3] = lo.w * f;
-      acc[4] = hi.x * f; acc[5] = hi.y * f; acc[6] = hi.z * f; acc[7] = hi.w * f;
+    float acc[32];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 v = more ? at[x * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[4 * x] = v.x * f; acc[4 * x + 1] = v.y * f; acc[4 * x + 2] = v.z * f; acc[4 * x + 3] = v.w * f;
     }
 #pragma unroll 1
-    for (uint32_t left = side; left; left &= left - 1) {
-      const int x = __ffs(left) - 1, page = kv4_page(a.v, b, t + x);
+    for (uint32_t left = side.of[d / kGroup]; left; left &= left - 1) {
+      const int x = __ffs(left) - 1;
+      const long long row = __shfl_sync(kFull, mine, x);
       uint32_t s;
-      __syncwarp();
       asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(s) : "r"(score + x));
+      const uint4 q = *reinterpret_cast<const uint4*>(a.c.v_q + row * (D / 8) + d / 8);
+      const uint32_t sb = reinterpret_cast<const uint32_t*>(a.c.v_sb)[row * (D / kGroup) + d / kGroup], w[4] = {q.x, q.y, q.z, q.w};
       asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s)::"memory");
       const float p = see >> x & 1 ? pr_ex2(fmaf(__uint_as_float(s), ck, -mm)) : 0.f;
-      const long long row = ((long long)max(page, 0) * a.c.kv_heads + h) * a.c.page_size + (t + x) % a.c.page_size;
-      const uint32_t q = a.c.v_q[row * (D / 8) + d / 8], sb = reinterpret_cast<const uint32_t*>(a.c.v_sb)[row * (D / kGroup) + d / kGroup];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float v = fmaf(p, fmaf((float)(q >> k * 4 & 15u), bf16lo(sb), bf16hi(sb)), acc[k]);
+      for (int k = 0; k < 32; ++k) {
+        const float v = fmaf(p, fmaf((float)(w[k / 8] >> k % 8 * 4 & 15u), bf16lo(sb), bf16hi(sb)), acc[k]);
         acc[k] = p == 0.f ? acc[k] : v;  // a hidden token adds nothing, whatever it holds
       }
+      __syncwarp();
     }
-    at[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    at[128] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) at[x * 128] = make_float4(acc[4 * x], acc[4 * x + 1], acc[4 * x + 2], acc[4 * x + 3]);
   }
 }
-// Adds the sums to O, whose columns come as 0 4 1 5 2 6 3 7, and returns O's exponent: the one it had, or, for large sums, 60.
+// Adds the sums to O, whose columns come as 0 4 1 5 2 6 3 7. Returns whether they are so large that O's unit is 2^60 from here on.
 template <int D>
-__device__ __noinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float m, int e) {
+__device__ __noinline__ bool pr_side_add(float* sums, int r, uint32_t o_t, float m, uint32_t units) {
   const float was = *pr_side_max<D>(sums, r);
   const float f = was == m ? 1.f : pr_ex2(was - m);
   float top = 0.f;
@@ -670,10 +693,11 @@ __device__ __noinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float 
     const float4 v = *reinterpret_cast<const float4*>(sums + d / 4 * 512);
     top = fmaxf(fmaxf(fmaxf(top, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
   }
-  const int unit = top * f > 0x1p40f ? 60 : e;
-  const float fo = exp2i(e - unit), fs = exp2i(-unit);
+  const bool large = top * f > 0x1p30f;
 #pragma unroll 1
   for (int d = 0; d < D; d += 8) {
+    const int e = pr_unit(units, d / kGroup), unit = large ? 60 : e;
+    const float fo = exp2i(e - unit), fs = exp2i((int)kPrMost - unit);
     const float4 lo = *reinterpret_cast<const float4*>(sums + d / 4 * 512), hi = *reinterpret_cast<const float4*>(sums + (d / 4 + 1) * 512);
     const float v[8] = {lo.x, hi.x, lo.y, hi.y, lo.z, hi.z, lo.w, hi.w};
     uint32_t o[8];
@@ -685,7 +709,7 @@ __device__ __noinline__ int pr_side_add(float* sums, int r, uint32_t o_t, float 
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(o_t + d), BGQ_I8(o, 0) : "memory");
   }
   pr_wait_st();
-  return unit;
+  return large;
 }
 // A token's values of group g into its row of a panel.
 template <int D>
@@ -863,8 +887,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       const bool dead = !__any_sync(kFull, own);  // a warp without rows only keeps the barriers going
 
       float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;  // m: what P refers to, 2^7 below the largest score when it was taken
-      // Bit 0: a key that is not finite is seen; bit 1 + g: a value of group g. The same for all of a warp's rows: bits 29 and 30:
-      // O's unit (pr_unit); bit 31: some values are summed apart.
+      // Bit 0: a key that is not finite is seen; bit 1 + g: a value of group g. The same for all of a warp's rows: bits 8 to 15: O's units
+      // (pr_unit); bit 31: some values are summed apart.
       uint32_t rare = 0;
 #pragma unroll 1
       for (int it = wk.i0; it < (none ? wk.i0 : wk.i1); ++it) {
@@ -877,7 +901,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int mt = (wk.n0 + it - wk.i0) & (kMetaTiles - 1);
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
-        const uint32_t odd_tile = odd4.x | odd4.y | odd4.z | odd4.w | (rare & 3u << 29);
+        const uint32_t odd_tile = odd4.x | odd4.y | odd4.z | odd4.w | (rare & 0xff00u);
         const bool plain = !odd_tile && t0 >= lo_max && t0 + kPrTok <= hi_min;
         // Every row sees every token, and no factor but the row's: 64 tokens at a time. The probabilities are taken with the
         // maximum so far while the scores' own is found; where that is too far above (seldom), it is raised and they are taken again.
@@ -932,16 +956,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
         }
         // otherwise 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
-        int unit = kVe;  // of the tile: O's where a block has it, else that of the first block with any
+        uint32_t unit = 0;  // the tile's units: by group O's where a block has it, else that of the first block with any
         if (odd_tile) {
-          bool keep = false;
+          const uint32_t now = rare >> 8 & 0xff, ve[4] = {sh.meta[mt][0].ve, sh.meta[mt][1].ve, sh.meta[mt][2].ve, sh.meta[mt][3].ve};
 #pragma unroll
-          for (int c = 3; c >= 0; --c) {
-            const int ve = sh.meta[mt][c].ve;
-            keep |= ve == pr_unit(rare);
-            if (c == 3 || ve != kVeNone) unit = ve;
+          for (int g = 0; g < G; ++g) {
+            const uint32_t o = now >> 2 * g & 3;
+            uint32_t u = kVeNone;
+            bool keep = false;
+#pragma unroll
+            for (int c = 3; c >= 0; --c) {
+              const uint32_t k = ve[c] >> 2 * g & 3;
+              keep |= k == o;
+              if (k != kVeNone) u = k;
+            }
+            unit |= (keep || u == kVeNone ? o : u) << 2 * g;
           }
-          if (keep || unit == kVeNone) unit = pr_unit(rare);
         }
 #pragma unroll 1
         for (int c = 0; c < (dead || plain ? 0 : 4); ++c) {
@@ -954,18 +984,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           uint32_t v[32];
           pr_ld32(s_t + c * 32, v);
           const uint32_t odd = sh.odd[mt][c];
-          const bool look = odd || unit != kVe;
+          const bool look = odd || unit;
           const bool cut = t < lo_max || t + 32 > hi_min;
           float ck = c2;
-          uint32_t see = 0xffffffffu, apart = 0;  // tokens whose values are summed apart
-          bool other = false;                     // all of them: the block's operand is of another unit than O
-          bool mix = false;                       // each token's key has its own factor
+          uint32_t see = 0xffffffffu;
+          bool other = false;  // the block's operand is of another unit than O: all of its values are summed apart
+          bool apart = false;  // some are
+          bool mix = false;    // each token's key has its own factor
           if (look || cut) {
             const PrMeta me = sh.meta[mt][c];
             ck *= me.kf;
             mix = me.kf == 0.f;
-            other = me.ve != unit && me.ve != kVeNone;
-            apart = (other ? 0xffffffffu : me.side) & ~me.gap;
+            other = (me.ve ^ unit | (me.ve ^ unit) >> 1) & ~(me.ve & me.ve >> 1) & 0x55;
+            apart = other || (me.side[0] | (G > 1 ? me.side[1] : 0) | (G > 2 ? me.side[2] | me.side[3] : 0));
             const int n0 = max(lo - t, 0), n1 = min(hi - t, 32);
             see = n1 > n0 ? (0xffffffffu >> (32 - n1)) & (0xffffffffu << n0) : 0u;
             see &= ~me.gap;
@@ -997,7 +1028,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
           const float top = pr_max3(fmaxf(ta, tb), __uint_as_float(v[30]), __uint_as_float(v[31])) * ck;
           const bool raise = top > m + kPrMost;
-          if (__any_sync(kFull, raise) || unit != pr_unit(rare)) {
+          if (__any_sync(kFull, raise) || unit != (rare >> 8 & 0xff)) {
             const float up = raise ? top - kPrLift : m;
             const float f = up == m ? 1.f : pr_ex2(m - up);
             m = up;
@@ -1012,9 +1043,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
                 pr_wait(&sh.pv_done, pv_par ^ 1, fail);
                 tc_fence_after();
               }
-              pr_scale<D>(o_t, f * exp2i(pr_unit(rare) - unit));  // units are at most 2^40 apart, which fp32 has to spare
+              pr_scale<D>(o_t, f);
+              if (unit != (rare >> 8 & 0xff)) {
+                pr_wait_st();
+                pr_rescale<D>(o_t, rare >> 8, unit);
+              }
             }
-            rare = (rare & ~(3u << 29)) | (unit == kVe ? 0u : unit < kVe ? 1u << 29 : 2u << 29);
+            rare = (rare & ~0xff00u) | unit << 8;
           }
           uint64_t ll = pr_pair(l0, l1);
           const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);
@@ -1031,7 +1066,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
           pr_split(ll, l0, l1);
           if (apart) {  // seldom
-            pr_side<D>(a, row, head, t, apart, see, s_t + c * 32, ck, m, w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot + r * 4, r,
+            const PrMeta& me = sh.meta[mt][c];
+            PrMask4 by;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) by.of[g] = g < G ? (other ? 0xffffffffu : me.side[g]) & ~me.gap : 0u;
+            pr_side<D>(a, row, head, t, by, see, s_t + c * 32, ck, m, w.part + ((long long)(cta * 2 + (wk.i0 == 0)) * NQ + i) * P::kSlot + r * 4, r,
                        rare >> 31);
             rare |= 1u << 31;
 #pragma unroll
@@ -1062,18 +1101,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
       pr_wait(&sh.o_full[i], o_par, fail);
       o_par ^= 1;
       tc_fence_after();
-      const int e = rare >> 31 ? pr_side_add<D>(part + r * 4, r, o_t, m, pr_unit(rare)) : pr_unit(rare);
+      const bool large = rare >> 31 && pr_side_add<D>(part + r * 4, r, o_t, m, rare >> 8);
       float l = rare & 1 ? NAN : l0 + l1;
-      const float unit = exp2i(e);
       const long long out_at = ok ? (long long)row * a.out_stride + head * D : -1;
       if (!dead) {
-        const float inv = l == 0.f ? 0.f : unit / l;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t v[32];
           pr_ld32(o_t + d, v);
           pr_wait_ld(v);
-          float f = whole ? inv : unit;
+          float f = inv * exp2i(large ? 60 : pr_unit(rare >> 8, d / kGroup));
           if (rare >> (1 + d / kGroup) & 1) f = NAN;
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
@@ -1177,10 +1215,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
     for (int x = -1;; ++x) {  // tile x is stored, the next one fetched
       if (x >= 0) {
         const int mt = x & (kMetaTiles - 1);
-        uint32_t any = 0, apart = 0, bad[G];
+        uint32_t any = 0, bad[G];
         bool mix = false;
-        int e = val ? kVe : 0;
-        float down = val ? exp2i(-kVe) : 1.f;
+        int e = 0;  // of the token's key
+        const float down = val ? exp2i(-kVe) : 1.f;
         uint32_t s2[G], b2[G];
         const bool odd_own = pr_odd<D>(sb, val ? kValueLow : kKeyLow);
 #pragma unroll
@@ -1190,11 +1228,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           b2[g] = pr_half2(bi, bi);
         }
         if (odd_own) {
-          e = val ? pr_value_range<D>(sb, apart, any, bad) : pr_key_range<D>(sb, mix, any, bad);
-          down = e == kVeNone || apart >> lane & 1 ? 0.f : exp2i(-e);
+          uint32_t apart[G] = {}, ve = 0;
+          if (val) ve = pr_value_range<D>(sb, apart, any, bad);
+          else e = pr_key_range<D>(sb, mix, any, bad);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            float sc = bf16lo(sb[g]) * down, bi = bf16hi(sb[g]) * down;
+            const float by = !val ? exp2i(-e) : apart[g] >> lane & 1 ? 0.f : exp2i(-pr_unit(ve, g));  // (without any, all is zero)
+            float sc = bf16lo(sb[g]) * by, bi = bf16hi(sb[g]) * by;
             if (!(fabsf(sc) < INFINITY && fabsf(bi) < INFINITY)) sc = bi = 0.f;
             s2[g] = pr_half2(sc, sc);
             b2[g] = pr_half2(bi, bi);
@@ -1202,15 +1242,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         }
         pr_wait(&free_[st], par, fail);
         if (!val) {  // the notes on both go out with K, for the softmax reads them with the scores
-          uint32_t vside = 0, vany = 0, vbad[G];
-          int ve = kVe;
+          uint32_t vside[G] = {}, vany = 0, vbad[G], ve = 0;
           const int c = part / 32;
           if (pr_odd<D>(vs, kValueLow)) ve = pr_value_range<D>(vs, vside, vany, vbad);
           const uint32_t gap = __ballot_sync(kFull, gone);
           if (lane == 0) {
-            const uint32_t odd = gap | any | vany | (uint32_t)e | (uint32_t)mix | vside | (uint32_t)(ve != kVe && ve != kVeNone);
+            uint32_t odd = gap | any | vany | (uint32_t)e | (uint32_t)mix | ((ve ^ ve >> 1) & 0x55);  // (an E but the usual one)
+#pragma unroll
+            for (int g = 0; g < G; ++g) odd |= vside[g];
             sh.odd[mt][c] = odd;
-            sh.meta[mt][c] = PrMeta{mix ? 0.f : exp2i(e), ve, gap, any | vany, vside, {}};
+            sh.meta[mt][c] = PrMeta{mix ? 0.f : exp2i(e), ve, gap, any | vany, {vside[0], G > 1 ? vside[1 % G] : 0, G > 2 ? vside[2 % G] : 0, G > 2 ? vside[3 % G] : 0}};
             if (odd) {
               sh.kbad[mt][c] = any;
 #pragma unroll
