@@ -616,6 +616,7 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
         _need(lse.shape == (rows, H) and lse.is_contiguous(), "bgq_kv4_attention: lse must be fp32 [rows][q_heads], contiguous")
     if rows == 0:
         return out, lse
+    _need(out.data_ptr() != q.data_ptr(), "bgq_kv4_attention: out must not be q")
     if ws is None:
         ws = kv4_attention_workspace(cache, seqs, H)
     _need(ws.get_device() == dev and ws.is_contiguous(), "bgq_kv4_attention: ws must be beside the cache, contiguous")

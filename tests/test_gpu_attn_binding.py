@@ -70,3 +70,13 @@ def test_only_the_head_of_a_workspace_is_zero_filled(cuda_device, guard_canaries
             out, l = lib.bgq_kv4_attention(cache, seqs, q, want_lse=True, ws=ws)
             assert torch.equal(out, want) and torch.equal(l, lse)
     assert lib.read_device_status(ws) == lib.OK
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_an_output_in_the_queries_place_is_refused(cuda_device, new):
+    """A row's heads are read by other blocks than the one that writes them."""
+    c = Case(cuda_device, [80], [new], 2, 64, 16, seed=64)
+    q = bf16(c.rng, new, 4, 64, dev=cuda_device)
+    with pytest.raises(lib.BGQError) as e:
+        lib.bgq_kv4_attention(c.cache(), c.seqs(), q, out=q)
+    assert e.value.status == lib.ERR_INVALID_ARG
