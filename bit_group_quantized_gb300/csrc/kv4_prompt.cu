@@ -296,7 +296,7 @@ __device__ __forceinline__ void pr_scale_p(uint32_t t, float f) {
 }
 // A score's factor: finite, so that zero times it stays zero, and not below normal numbers, so that -infinity times it stays that.
 __device__ __forceinline__ float pr_factor(float f) { return fminf(fmaxf(f, 0x1p-126f), 3e38f); }
-// 32 scores of the warp's rows times f and the powers of two of their tokens' keys.
+// 32 scores of the warp's rows times f, and the powers of two of their tokens' keys where those are given.
 __device__ __noinline__ void pr_scale_s(uint32_t t, float f, const int8_t* ke) {
 #pragma unroll 1
   for (int d = 0; d < 32; d += 8) {
@@ -304,7 +304,7 @@ __device__ __noinline__ void pr_scale_s(uint32_t t, float f, const int8_t* ke) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : BGQ_R8(r, 0) : "r"(t + d));
     asm volatile("tcgen05.wait::ld.sync.aligned;" : BGQ_U8(r, 0)::"memory");
 #pragma unroll
-    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * pr_factor(f * exp2i(ke[d + x])));
+    for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * (ke ? pr_factor(f * exp2i(ke[d + x])) : f));
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t + d), BGQ_I8(r, 0) : "memory");
   }
   pr_wait_st();
@@ -436,6 +436,9 @@ struct __align__(16) PrMeta {
   uint32_t side[4];  // by group: tokens whose values E does not fit, zeros in V's operand; the softmax adds them by itself
 };
 constexpr float kPrMost = 15.f, kPrLift = 7.f;  // log2 of the largest P; of P at a maximum that was raised
+// A fused S c - m is as far from its value at the maximum as the product's rounding: 2^-4 at 2^20, but more than any exponent at
+// 2^31. From here on a row's scores are multiplied and rounded first, as the maximum is.
+constexpr float kPrLarge = 0x1p20f;
 constexpr int kMetaTiles = 4;  // tiles whose notes are kept: the copies run at most two ahead of the softmax
 
 template <int D>
@@ -888,7 +891,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
 
       float m = -INFINITY, mm = 0.f, l0 = 0.f, l1 = 0.f;  // m: what P refers to, 2^7 below the largest score when it was taken
       // Bit 0: a key that is not finite is seen; bit 1 + g: a value of group g. The same for all of a warp's rows: bits 8 to 15: O's units
-      // (pr_unit); bit 31: some values are summed apart.
+      // (pr_unit); bit 30: scores are multiplied and rounded first (kPrLarge); bit 31: some values are summed apart.
       uint32_t rare = 0;
 #pragma unroll 1
       for (int it = wk.i0; it < (none ? wk.i0 : wk.i1); ++it) {
@@ -901,10 +904,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
         const int mt = (wk.n0 + it - wk.i0) & (kMetaTiles - 1);
         const int t0 = wk.un.begin + it * kPrTok;
         const uint4 odd4 = *reinterpret_cast<const uint4*>(sh.odd[mt]);
-        const uint32_t odd_tile = odd4.x | odd4.y | odd4.z | odd4.w | (rare & 0xff00u);
+        const uint32_t odd_tile = odd4.x | odd4.y | odd4.z | odd4.w | (rare & 0x4000ff00u);
         const bool plain = !odd_tile && t0 >= lo_max && t0 + kPrTok <= hi_min;
         // Every row sees every token, and no factor but the row's: 64 tokens at a time. The probabilities are taken with the
         // maximum so far while the scores' own is found; where that is too far above (seldom), it is raised and they are taken again.
+        int from = plain || dead ? 4 : 0;  // where the other way takes over
 #pragma unroll 1
         for (int c = 0; c < (plain && !dead ? 4 : 0);) {
           uint32_t v[64], pk[32];
@@ -954,6 +958,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             }
             pr_scale<D>(o_t, f);
           }
+          if (__any_sync(kFull, fabsf(mm) > kPrLarge)) {  // seldom: the tile's rest goes the other way
+            rare |= 1u << 30;
+            from = c;
+            break;
+          }
         }
         // otherwise 32 tokens at a time, in a short loop (the warps' loops share the instruction caches)
         uint32_t unit = 0;  // the tile's units: by group O's where a block has it, else that of the first block with any
@@ -974,7 +983,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
         }
 #pragma unroll 1
-        for (int c = 0; c < (dead || plain ? 0 : 4); ++c) {
+        for (int c = from; c < 4; ++c) {
           const int t = t0 + c * 32;
           if (t >= hi_max || t + 32 <= lo_min) {  // no row sees any
             const uint32_t none[16] = {};
@@ -1009,8 +1018,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
           }
           ck = pr_factor(ck);
           pr_wait_ld(v);
-          if (mix) {  // seldom
-            pr_scale_s(s_t + c * 32, c2, sh.ke[mt] + c * 32);
+          if (mix || rare >> 30 & 1) {  // seldom
+            pr_scale_s(s_t + c * 32, mix ? c2 : ck, mix ? sh.ke[mt] + c * 32 : nullptr);
             pr_ld32(s_t + c * 32, v);
             pr_wait_ld(v);
             ck = 1.f;
@@ -1027,7 +1036,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
             tb = pr_max3(tb, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
           }
           const float top = pr_max3(fmaxf(ta, tb), __uint_as_float(v[30]), __uint_as_float(v[31])) * ck;
-          const bool raise = top > m + kPrMost;
+          const bool raise = top - m > kPrMost;
           if (__any_sync(kFull, raise) || unit != (rare >> 8 & 0xff)) {
             const float up = raise ? top - kPrLift : m;
             const float f = up == m ? 1.f : pr_ex2(m - up);
@@ -1050,6 +1059,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_attn_prompt(const __grid_cons
               }
             }
             rare = (rare & ~0xff00u) | unit << 8;
+            if (!(rare >> 30 & 1) && __any_sync(kFull, fabsf(mm) > kPrLarge)) {
+              rare |= 1u << 30;
+              if (!mix) {  // these scores again
+                --c;
+                continue;
+              }
+            }
           }
           uint64_t ll = pr_pair(l0, l1);
           const uint64_t ck2 = pr_pair(ck, ck), mm2 = pr_pair(-mm, -mm);

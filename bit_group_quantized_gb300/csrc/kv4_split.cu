@@ -212,7 +212,9 @@ struct SplitWs {
 template <int D, int NT>
 struct SplitAcc {
   static constexpr int G = D / kGroup;
-  float m[NT][2], mm[NT][2];      // the maximum the probabilities refer to; the same, or 0 before the first score
+  // What the probabilities refer to, 0 before the first score; and what a score must pass to raise it: -infinity before the
+  // first, and kSplitSteep, which all pass, where it is so large that products with cs are rounded first (in the masked form).
+  float mm[NT][2], pass[NT][2];
   float l[NT][2], bias[NT][2][G];  // this lane's tokens' sums of p, and of p (b + 8 s)
   float o[NT][G][4][4];           // sum of (code - 8) p s, in units of 2^E
   float cs[NT][2];                // scale * log2(e) / 2^shift
@@ -227,6 +229,9 @@ struct SplitAcc {
 constexpr int kSplitTop = 8, kSplitMost = 20;
 constexpr float kSplitRaise = 5.f;
 constexpr uint32_t kSplitSpan = 9u << 23;
+// A fused difference s cs - mm is as far from zero at the maximum as the product's rounding: 2^-4 at 2^20, but more than any exponent
+// at 2^31. From kSplitLarge on scores are multiplied and rounded first, as the maximum is.
+constexpr float kSplitLarge = 0x1p20f, kSplitSteep = -3e38f;
 
 // Codes less 8 of dims 4g + j (row g) and 32 + 4g + j (row g + 8), from transposed words.
 __device__ __forceinline__ void split_codes(uint32_t (&f)[4], const uint32_t (&w)[4], int j, const SplitK& k_) {
@@ -238,7 +243,7 @@ __device__ __forceinline__ void split_codes(uint32_t (&f)[4], const uint32_t (&w
   }
 }
 // What the scales that 2^-E does not take in add to O and the sums beside it: token by token in fp32, a lane its own dims of O, with few registers.
-// Seldom. Hidden tokens' scores are -infinity.
+// Seldom. The scores are multiplied by cs, hidden tokens' are -infinity.
 template <int D, int NT>
 __device__ __forceinline__ void split_far(SplitAcc<D, NT>& A, const float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st, int t0, int held,
                                           int g) {
@@ -265,7 +270,7 @@ __device__ __forceinline__ void split_far(SplitAcc<D, NT>& A, const float (&s)[S
         float x = s[0][n][k];
 #pragma unroll
         for (int i = 1; i < 2 * MT; ++i) x = mr == i ? s[i / 2][n][i % 2 * 2 + k] : x;
-        p[n][k] = ex2(fmaf(x, A.cs[n][k], -A.mm[n][k]));
+        p[n][k] = ex2(x - A.mm[n][k]);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] = fmaf(p[n][k], 8.f * v[gr], A.bias[n][k][gr]);
       }
@@ -297,8 +302,8 @@ __device__ __forceinline__ void split_far(SplitAcc<D, NT>& A, const float (&s)[S
   }
 }
 
-// What follows a tile's scores s; MASKED where some column does not see all of its tokens, or some scale is far from the others:
-// without it nothing is done then, and false returned.
+// What follows a tile's scores s; MASKED where some column does not see all of its tokens, some scale is far from the others or
+// scores are very large: without it nothing is added then, and false returned.
 template <int D, int NT, int CTAS, bool MASKED>
 __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Split<D, NT, 1>::MT][NT][4], const unsigned char* st,
                                              uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
@@ -308,9 +313,17 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
   // so that no register keeps them over it (64 sequences of 512 to 16384 tokens: 88.3 us, else 89.6); elsewhere the registers
   // are there (131071 tokens: 42.6 us, else 43.4).
   constexpr bool kAgain = CTAS == 2 || D * NT >= 512;
-  bool hid[MT][NT][4];
   uint32_t vp[MT][2][G], big = 0;  // V's pairs; how far their scales' bits pass the smallest
   bool raise = false;
+  if (MASKED) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[mt][n][i] = __fmul_rn(s[mt][n][i], A.cs[n][i & 1]);
+  }
+  auto cs = [&](int n, int k) { return MASKED ? 1.f : A.cs[n][k]; };
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -330,8 +343,7 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            hid[mt][n][r * 2 + k] = !some || t < A.lo[n][k] || t >= A.hi[n][k];
-            if (hid[mt][n][r * 2 + k]) s[mt][n][r * 2 + k] = -INFINITY;
+            if (!some || t < A.lo[n][k] || t >= A.hi[n][k]) s[mt][n][r * 2 + k] = -INFINITY;
           }
       }
     }
@@ -342,7 +354,7 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
       float top = s[0][n][k];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, mt ? fmaxf(s[mt][n][k], s[mt][n][2 + k]) : s[mt][n][2 + k]);
-      raise |= top * A.cs[n][k] > A.m[n][k] + kSplitRaise;
+      raise |= top * cs(n, k) > A.pass[n][k];
     }
   // a scale of zero or with its sign set, an infinity or a NaN passes the span: looked at more closely there
   if (__any_sync(kFull, raise || big >= kSplitSpan)) {
@@ -368,7 +380,6 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
       less = 0u - __float_as_uint(exp2i(e + kSplitTop - 8));
     }
     const bool far = most && (most + less >= kSplitSpan || least < 0u - less);
-    if (!MASKED && far) return false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -379,10 +390,11 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-        top = fmaxf(A.m[n][k], top * A.cs[n][k]);
-        const float f = A.m[n][k] == top ? 1.f : ex2(A.m[n][k] - top);
-        A.m[n][k] = top;
+        const float m = A.pass[n][k] == -INFINITY ? -INFINITY : A.mm[n][k];
+        top = fmaxf(m, top * cs(n, k));
+        const float f = m == top ? 1.f : ex2(m - top);
         A.mm[n][k] = top == -INFINITY ? 0.f : top;
+        A.pass[n][k] = fabsf(A.mm[n][k]) > kSplitLarge ? kSplitSteep : top + kSplitRaise;
         A.l[n][k] *= f;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
@@ -394,6 +406,12 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
           }
         }
       }
+    if (!MASKED) {
+      bool steep = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) steep |= A.pass[n][0] == kSplitSteep || A.pass[n][1] == kSplitSteep;
+      if (far || __any_sync(kFull, steep)) return false;  // what was raised stays so
+    }
     if (less != A.less) {
       const float f = A.unit * exp2i(-e);
       A.unit = exp2i(e);
@@ -421,19 +439,6 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
             const uint32_t mag = (vp[mt][r][gr] & 0x7fffu) << 16;
             if (mag < 0x7f800000u && mag + A.less >= kSplitSpan) vp[mt][r][gr] &= 0xffff0000u;
           }
-      if (kAgain) {
-        asm volatile("" : "+r"(t0));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int t = t0 + mt * 16 + r * 8 + g;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) hid[mt][n][r * 2 + k] = (gaps >> mt & 1) || t >= held || t < A.lo[n][k] || t >= A.hi[n][k];
-          }
-      }
     }
   }
   // ---- probabilities, and the output
@@ -454,8 +459,7 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = ex2(fmaf(s[mt][n][r * 2 + k], A.cs[n][k], -A.mm[n][k]));
-          if (MASKED && hid[mt][n][r * 2 + k]) p[k] = 0.f;
+          p[k] = ex2(MASKED ? s[mt][n][r * 2 + k] - A.mm[n][k] : fmaf(s[mt][n][r * 2 + k], A.cs[n][k], -A.mm[n][k]));
           A.l[n][k] += p[k];
         }
 #pragma unroll
@@ -466,7 +470,7 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
           for (int k = 0; k < 2; ++k) {
             ps[k] = p[k] * sc[gr];
             const float bs = fmaf(p[k], vb[gr], A.bias[n][k][gr]);
-            const bool gone = MASKED && hid[mt][n][r * 2 + k];
+            const bool gone = MASKED && s[mt][n][r * 2 + k] == -INFINITY;
             if (gone) ps[k] = 0.f;
             A.bias[n][k][gr] = gone ? A.bias[n][k][gr] : bs;
           }
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        A.m[n][k] = -INFINITY;
+        A.pass[n][k] = -INFINITY;
         A.mm[n][k] = A.l[n][k] = 0.f;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] = 0.f;
@@ -860,7 +864,8 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) A.bias[n][k][gr] += __shfl_xor_sync(kFull, A.bias[n][k][gr], x);
         }
-        if (g == 0) s_m[warp][n * 8 + 2 * c + k] = A.m[n][k];
+        if (A.pass[n][k] == -INFINITY) A.mm[n][k] = -INFINITY;  // no score: the warp's part counts for nothing
+        if (g == 0) s_m[warp][n * 8 + 2 * c + k] = A.mm[n][k];
       }
     __syncthreads();
     float f[NT][2];
@@ -871,7 +876,7 @@ __global__ void __launch_bounds__(kSplitThreads, CTAS) k_attn_split(const __grid
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * c + k]);
-        f[n][k] = A.m[n][k] == top ? 1.f : ex2(A.m[n][k] - top);
+        f[n][k] = A.mm[n][k] == top ? 1.f : ex2(A.mm[n][k] - top);
         if (g == 0) s_l[warp][n * 8 + 2 * c + k] = A.l[n][k] * f[n][k];
       }
     const bool whole = wk.i0 == 0 && wk.i1 == wk.q.tiles;
