@@ -9,8 +9,8 @@
 //
 // Both kernels are bound by memory (2 bytes of bf16 and 0.56 bytes of cache a
 // value), and nearly as much by the instructions that place the codes: 15349 rows of 8 heads of 128 written
-// and read back in 32.1 us (5.0 TB/s of the 161 MB both move; issue slots 60 % full in the writing half), 78514 tokens
-// of 2 heads of 256 read in 35.8 us (5.7 TB/s). Four lanes share a group, 16 values a lane in two 16-byte loads (the
+// and read back in 33.3 us (4.8 TB/s of the 161 MB both move; issue slots 60 % full in the writing half), 78514 tokens
+// of 2 heads of 256 read in 36.5 us (5.6 TB/s). Four lanes share a group, 16 values a lane in two 16-byte loads (the
 // reductions over a group then cost two shuffles, and the scale's division
 // is spread over 16 values); a lane's codes are two words of the group.
 #include "attn.h"

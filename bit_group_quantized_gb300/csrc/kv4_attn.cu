@@ -12,6 +12,8 @@ namespace bgq {
 //   head dim 64  32, 62 / 66, 146 / 22, 30           48, 62 / 116, 148 / 22, 30          27, 29 / 51, 50
 //           128  45, 76 / 107, 187 / 25, 34          74, 78 / 197, 189 / 31, 33          36, 33 / 78, 59
 //           256  95, 111 / 220, 265 / 40, 42         157, 111 / 412, 268 / 53, 42        68, 41 / 169, 86
+// (caches still in L2; both kernels are 2 to 4 % slower since they hold values of any sizes. Read from memory, 16 columns of head dim
+// 128 take 58, 82 / 130, 194 / 47, 69, and 32 columns 96, 82 / 240, 196 / 76, 69.)
 // Where the page lists have room for few tokens (four tiles a warp) and an SM takes one unit of 16 columns at most, the split
 // kernel does with one short round what the other does in three launches: 16 sequences of 500 tokens, 40 columns, two key heads:
 // 9, 19 us with head dim 64, 12, 22 with 128, 17, 27 with 256; with 128 columns, two units an SM: 22, 20, 28, 24, 44, 29.

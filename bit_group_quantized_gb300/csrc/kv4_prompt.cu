@@ -6,7 +6,7 @@
 // column being one (query row, query head) pair that shares the key head), as
 // NQ tiles of 128 accumulator rows. Per 128 tokens:
 //   S = Q K^T   both fp16 in shared memory, S fp32 in tensor memory. K's operand is (code - 8) * scale,
-//               which fp16 holds exactly; what is left of a key, bias + 8 * scale a group, is one more
+//               which fp16 holds exactly (for scales from 2^-17 on, or 2^-17 of a shifted block's); what is left of a key, bias + 8 * scale a group, is one more
 //               step of 16 columns: (bias, bias, scale, scale) a group against the query's group sum in
 //               two parts, and 8 times those. With code * scale + bias rounded to fp16 the logarithm of
 //               the sum was 1.2e-6 off (relative, 24 sequences of up to 9000 tokens, head dim 256), so
@@ -24,9 +24,9 @@
 // whose O fills tensor memory) S is double-buffered.
 // What bounds it: a tile's chain of scores, softmax and product, which two row tiles fill by turns, and beside it shared
 // memory, which the matrix instructions read at its full rate while they take Q and K from it (a tile of 2 x 128 rows
-// takes 3600 cycles, of which the matrix instructions take 2200). 4096 tokens causal, 32 heads of 128 over 8: 147 us,
-// 935 TFLOP/s; three chunks of 700 to 1100 rows behind up to 16000 tokens: 303 us, 1190 TFLOP/s (61 % of the matrix rate
-// measured with a library product); 24 sequences of five rows, 16 heads of 256 over 2: 41 us, where dequantisation has
+// takes 3600 cycles, of which the matrix instructions take 2200). 4096 tokens causal, 32 heads of 128 over 8: 154 us,
+// 892 TFLOP/s; three chunks of 700 to 1100 rows behind up to 16000 tokens: 318 us, 1140 TFLOP/s (58 % of the matrix rate
+// measured with a library product); 24 sequences of five rows, 16 heads of 256 over 2: 44 us, where dequantisation has
 // too few rows to serve (5000 cycles a tile).
 // P refers to 2^-7 of a row's maximum, which is raised, and O rescaled, only where
 // scores pass it by 2^8: P then stays below 2^15, and a tail of tokens 2^-30 below the first one is still there. (Raised
@@ -37,9 +37,9 @@
 // undoes it in the scores' factors. A group of 64 columns of V is
 // scaled by one of three powers of two per 32 tokens, the unit of those columns of O. Tokens that it does not fit (far smaller or
 // larger than the others' values) and blocks of other units than O's are left out of the product, and their softmax thread adds p V
-// in fp32, slowly: no row's result depends on the size of values that it does not see, or of another group's. This costs ordinary
-// values 1 to 3 % (4096 tokens causal: 152.5 us, 147.6 with one exponent for all that a row had met, which lost small values beside
-// large ones; the functions of the rare paths are not inlined: 154.2). In 4096 tokens, values of 2^-24 in one group of two: 261 us; in one token of
+// in fp32, slowly: no row's result depends on the size of values that it does not see, or of another group's. This and the care for
+// very large scores cost ordinary values 2 to 4 % (4096 tokens causal: 154 us, 147.6 with one exponent for all that a row had met, which
+// lost small values beside large ones; with the functions of the rare paths inlined it was 1 % more). In 4096 tokens, values of 2^-24 in one group of two: 261 us; in one token of
 // 32: 1.8 ms; values of 2^-40 throughout, which no unit fits: 15 ms.
 // A key or value pair that is not finite is stored as zeros, and the rows that see it are made NaN at the end.
 //

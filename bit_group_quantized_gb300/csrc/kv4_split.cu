@@ -23,10 +23,10 @@
 // of two 2^E per warp that follows the largest scale of a tile; scales far from it, in tokens that a column may not even see, are
 // multiplied apart. The maximum is only
 // raised when a score passes it by 2^5, so that most tiles need no reduction over the warp.
-// What bounds it is the issue of instructions, not memory: 385 of them for 16 tokens of a head of 128, 55 for the
-// copies among them (taken out, no time was saved). 64 sequences of 512 to 16384 tokens, 8 key
-// heads of 128, 4 columns: 86 us, 3.9 TB/s (58 % of a copy's rate; issue slots 60 % full); one of 131071 tokens: 43 us, 3.5 TB/s
-// (eight warps an SM, latency); one of 513: 9.3 us, a call's latency.
+// What bounds it is the issue of instructions and the length of a tile's chain, not memory: 400 instructions for 16 tokens of a head of
+// 128, 55 for the copies among them (taken out, no time was saved). 64 sequences of 512 to 16384 tokens, 8 key
+// heads of 128, 4 columns: 88.3 us, 3.8 TB/s (57 % of a copy's rate; issue slots 61 % full); one of 131071 tokens: 42.6 us, 3.5 TB/s
+// (eight warps an SM, latency); one of 513: 8.8 us, a call's latency.
 // A segment ends with the CTA's warps joined in shared memory; a unit cut by a
 // CTA's share is joined by the last of its CTAs to arrive, in CTA order (the same
 // bits every time).

@@ -8,8 +8,8 @@
 //
 // Bound by memory (2 bytes in, 2 bytes out per value). A block takes whole
 // tokens: its first loads are in flight while it computes the angles of its
-// tokens once, for all heads, into shared memory. 8191 tokens of 40 heads of 128: 27.3 us, 6.1 TB/s,
-// 92 % of a copy's rate. Few tokens cost what a launch costs (64 tokens: 6.4 us a call through Python).
+// tokens once, for all heads, into shared memory. 8191 tokens of 40 heads of 128: 27.4 us, 6.1 TB/s,
+// 92 % of a copy's rate. Few tokens cost what a launch costs (64 tokens: about 7 us a call through Python).
 // Sums and products are fp32; the result is rounded to bf16 once.
 #include <algorithm>
 

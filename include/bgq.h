@@ -445,11 +445,15 @@ int32_t bgq_kv4_read(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, uint16_t* k,
  * that sees a NaN gets NaN. q_heads a multiple of kv_heads, at most 64 times as many and
  * at most 1024; rows * (q_heads / kv_heads) below 2^31 - 65536. out must not overlap
  * q, nor lse anything.
+ * Precision: scores are fp32 sums of exact products of codes and queries, a row's queries being held in fp16 beside a
+ * power of two (below 2^-21 of the row's largest they lose bits). Probabilities, or with few rows their products with a value's scale, and with
+ * many rows the values too, are rounded to fp16 once (half a step 2^-12 of each, of random sign over the tokens); softmax statistics and
+ * all sums are fp32. Tokens, groups and blocks of any finite sizes keep that precision beside each other; with few rows, scores of
+ * keys beyond 2^110 may overflow.
  * ws: bgq_kv4_attention_workspace_bytes bytes (for the same batch, rows,
- * max_q, max_pages and heads; a few MB for single tokens, up to 160 MB for prompts,
- * whatever their length), of which the first 4096 must be zero before the first call. Calls of any shapes
- * may share one that is large
- * enough for each, one after the other; calls of other entry points may not,
+ * max_q, max_pages and heads; a few MB for single tokens, 21 to 42 MB and 40 bytes for every 128 rows
+ * of a key head for prompts, whatever their past), of which the first 4096 must be zero before the first call. Calls of any shapes
+ * may share one that is large enough for each, one after the other; calls of other entry points may not,
  * unless it is zero-filled between. The same inputs give the same bits. */
 size_t bgq_kv4_attention_workspace_bytes(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, int32_t q_heads);
 int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const uint16_t* q, int64_t q_stride,
