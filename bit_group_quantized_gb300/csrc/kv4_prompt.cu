@@ -669,6 +669,7 @@ __device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int 
       const int x = __ffs(left) - 1;
       const long long row = __shfl_sync(kFull, mine, x);
       uint32_t s;
+      __syncwarp();
       asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(s) : "r"(score + x));
       const uint4 q = *reinterpret_cast<const uint4*>(a.c.v_q + row * (D / 8) + d / 8);
       const uint32_t sb = reinterpret_cast<const uint32_t*>(a.c.v_sb)[row * (D / kGroup) + d / kGroup], w[4] = {q.x, q.y, q.z, q.w};
@@ -679,7 +680,6 @@ __device__ __noinline__ void pr_side(const AttnArgs& a, int row0, int head, int 
         const float v = fmaf(p, fmaf((float)(w[k / 8] >> k % 8 * 4 & 15u), bf16lo(sb), bf16hi(sb)), acc[k]);
         acc[k] = p == 0.f ? acc[k] : v;  // a hidden token adds nothing, whatever it holds
       }
-      __syncwarp();
     }
 #pragma unroll
     for (int x = 0; x < 8; ++x) at[x * 128] = make_float4(acc[4 * x], acc[4 * x + 1], acc[4 * x + 2], acc[4 * x + 3]);

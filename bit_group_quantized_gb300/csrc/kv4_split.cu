@@ -309,9 +309,9 @@ __device__ __forceinline__ bool split_finish(SplitAcc<D, NT>& A, float (&s)[Spli
                                              uint32_t st_u, int t0, int gaps, int held, int g, const SplitK& k_) {
   using P = Split<D, NT, 1>;  // a tile's layout does not go by the CTAs
   constexpr int G = P::G, MT = P::MT;
-  // Where registers are short (128 a thread, or 16 columns of 256) the pairs are read again behind split_far and the hidden tokens found again,
-  // so that no register keeps them over it (64 sequences of 512 to 16384 tokens: 88.3 us, else 89.6); elsewhere the registers
-  // are there (131071 tokens: 42.6 us, else 43.4).
+  // Where registers are short (128 a thread, or 16 columns of 256) the pairs are read again behind split_far, so that no register keeps
+  // them over it (64 sequences of 512 to 16384 tokens: 88.3 us, else 89.6); elsewhere the registers are there (131071 tokens:
+  // 42.6 us, else 43.4).
   constexpr bool kAgain = CTAS == 2 || D * NT >= 512;
   uint32_t vp[MT][2][G], big = 0;  // V's pairs; how far their scales' bits pass the smallest
   bool raise = false;

@@ -117,3 +117,38 @@ def test_a_flat_tail_behind_a_high_first_token(cuda_device, high, new):
     q = bf16(c.rng, c.rows, 4, 128, dev=cuda_device, scale=1.5).abs()
     out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, want_lse=True)
     attn_close(c, q, out, lse)
+
+
+@pytest.mark.parametrize("d,hq,new", [(64, 4, 1), (64, 5, 3), (128, 8, 1), (128, 3, 2)])
+@pytest.mark.parametrize("what", ["tokens", "groups", "hidden", "scores"])
+def test_many_sequences_of_values_of_different_sizes(cuda_device, what, d, hq, new):
+    """More units than SMs, where two blocks share one and have half the registers: the same sizes beside each other.
+    Very large scores: the few-row kernel multiplies 64 + code, so that a group's partial sums reach s (64 |sum q| + 15 sum |q|). With
+    normal queries |sum q| of 64 stays below 28 (3.5 sigma of 8) and sum |q| near 51, so they reach 2560 s; sum |q k| is near
+    51 * 2.4 s (codes of a normal group are 2.4 from its middle on average): 21 times as much. Each of the d/16 + 8 <= 16 partial
+    sums and products is off by 2^-23 of itself (accumulation truncates): 16 * 21 * 2^-23 < 2^-14 of scale sum|q k| in all."""
+    B = 170
+    kv = [3 + 37 * b % 190 for b in range(B)]
+    c = Case(cuda_device, kv, [min(new, n) for n in kv], 1, d, 16, seed=56, room=0)
+    rng = np.random.default_rng(57)
+    P = O.bf16_to_f64(c.np[VALUES])
+    window = 0
+    if what == "tokens":
+        P = P * 2.0 ** np.round(rng.uniform(-40, 40, P.shape[:3] + (1, 1)))
+    elif what == "groups":
+        P = P * 2.0 ** np.round(rng.uniform(-40, 40, (1, 1, 1, P.shape[3], 1))) * (rng.random(P.shape[:3] + (1, 1)) > 0.2)
+    c.np[VALUES] = O.f64_to_bf16_bits(P)
+    if what == "hidden":
+        window = 30
+        for b, n in enumerate(kv):
+            times(c, VALUES, range(0, n - window - new, 2), 2.0 ** 70, b=b)
+            times(c, KEYS, range(1, n - window - new, 2), 2.0 ** 90, b=b)
+    q = bf16(c.rng, c.rows, hq, d, dev=cuda_device, scale=1.5)
+    scale = 1e7 * d ** -0.5 if what == "scores" else None
+    out, lse = lib.bgq_kv4_attention(c.cache(), c.seqs(), q, scale=scale, window=window, want_lse=True)
+    if what != "scores":
+        attn_close(c, q, out, lse, window=window)
+        return
+    o, l, a, s = c.oracle(q, scale=scale)
+    gl = lse.cpu().double().numpy()
+    assert np.isfinite(out.float().cpu().numpy()).all() and (np.abs(gl - l) <= 2.0 ** -14 * s + np.log(200)).all()
