@@ -1,0 +1,73 @@
+// f8.h — the e4m3 operators: arguments of their kernels, and device helpers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/bgq.h"
+
+namespace bgq {
+
+constexpr int kF8Block = 128;  // columns that share one scale (of weights, rows too)
+__host__ __device__ inline int f8_blocks(int cols) { return (cols + kF8Block - 1) / kF8Block; }
+
+struct Ctrl;
+
+// One product: y = x W^T, or silu(x W0^T) * (x W1^T) into h and / or y.
+struct F8Prod {
+  const uint8_t* w[2];   // codes of W, or of gate and up
+  const uint8_t* ws[2];  // their scales
+  int64_t w_stride[2], ws_stride[2];
+  const uint8_t* x;
+  const uint8_t* xs;
+  int64_t x_stride, xs_stride;
+  int M, N, K;  // rows of x, rows of W, columns of both
+  uint16_t* y;
+  float* yf;
+  int64_t y_stride;
+  uint8_t* h;  // codes of the result (gated), null where it is wanted in bf16 alone
+  uint8_t* hs;
+  int64_t h_stride, hs_stride;
+  Ctrl* ctrl;
+};
+
+cudaError_t launch_f8_quantise(const uint16_t* x, int64_t x_stride, const bgq_f8matrix& m, cudaStream_t s);
+cudaError_t launch_rmsnorm_f8(float* h, const void* delta, bool delta_f32, const uint16_t* rho, float eps,
+                              const bgq_f8matrix& m, uint16_t* a, cudaStream_t s);
+cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s);
+cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The scale byte of a block whose largest magnitude has these fp32 bits: the smallest power of two 2^(byte - 127) with
+// amax <= 448 * 2^(byte - 127). 448 = 1.75 * 2^8, so it goes by the exponent, one more where the fraction passes 1.75.
+__device__ __forceinline__ int f8_scale_byte(uint32_t amax_bits) {
+  return max(0, (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+__device__ __forceinline__ bool f8_finite(uint32_t amax_bits) { return amax_bits < 0x7f800000u; }
+// 2^(127 - byte), by which the block's values are multiplied; bytes here are at most 247.
+__device__ __forceinline__ float f8_inverse(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+
+// Four values as e4m3 codes, a in the lowest byte (to nearest, halves to even).
+__device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+constexpr uint32_t kF8Nan4 = 0x7f7f7f7fu;  // four codes of NaN
+constexpr int kF8One = 127;                // the scale byte of 1
+
+// silu(g) * u. The exponential's and the reciprocal's approximations are 2^-21 off or so, the result has 8 bits or 4.
+__device__ __forceinline__ float f8_swiglu(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  return g * r * u;
+}
+#endif
+
+}  // namespace bgq

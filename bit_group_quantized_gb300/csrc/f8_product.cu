@@ -1,0 +1,8 @@
+// f8_product.cu — which kernel multiplies two e4m3 matrices.
+#include "f8.h"
+
+namespace bgq {
+
+cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) { return launch_f8_few(p, gated, s); }
+
+}  // namespace bgq

@@ -59,6 +59,11 @@ class bgq_kv4_seqs(C.Structure):
                 ("max_pages", C.c_int32), ("rows", C.c_int32), ("max_q", C.c_int32)]
 
 
+class bgq_f8matrix(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scale", C.c_void_p), ("q_stride", C.c_int64), ("scale_stride", C.c_int64),
+                ("rows", C.c_int32), ("cols", C.c_int32), ("block_rows", C.c_int32)]
+
+
 _lib = None
 _P = C.c_void_p
 _I = C.c_int32
@@ -92,6 +97,12 @@ _SIGS = {
     "bgq_kv4_attention_workspace_bytes": (_S, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _I]),
     "bgq_kv4_attention": (_I, [C.POINTER(bgq_kv4_cache), C.POINTER(bgq_kv4_seqs), _P, C.c_int64, _I, C.c_float, _I,
                                _I, _P, C.c_int64, _P, _P, _S, _P]),
+    "bgq_f8_quantise": (_I, [_P, C.c_int64, C.POINTER(bgq_f8matrix), _P]),
+    "bgq_rmsnorm_f8": (_I, [_P, _P, _I, _P, _I, _I, C.c_float, C.POINTER(bgq_f8matrix), _P, _P]),
+    "bgq_f8_gemm_workspace_bytes": (_S, [C.POINTER(bgq_f8matrix), C.POINTER(bgq_f8matrix)]),
+    "bgq_f8_gemm": (_I, [C.POINTER(bgq_f8matrix), C.POINTER(bgq_f8matrix), _P, _P, C.c_int64, _P, _S, _P]),
+    "bgq_f8_swiglu": (_I, [C.POINTER(bgq_f8matrix), C.POINTER(bgq_f8matrix), C.POINTER(bgq_f8matrix),
+                           C.POINTER(bgq_f8matrix), _P, C.c_int64, _P, _S, _P]),
     "moe_stack_workspace_bytes": (_S, [C.POINTER(bgq_moe_layer), _I]),
     "moe_stack_decode": (_I, [C.POINTER(bgq_moe_layer), C.POINTER(_P), _I, C.c_float, _P, _P, _P, _P, _P, _S,
                               _P]),
@@ -626,6 +637,188 @@ def bgq_kv4_attention(cache: KV4Cache, seqs: KV4Seqs, q: torch.Tensor, scale: fl
     if r:
         raise BGQError(r, "bgq_kv4_attention")
     return out, lse
+
+
+# ------------------------------------------------------------------ e4m3
+F8_BLOCK = 128  # columns that share one scale (of weights, rows too)
+_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+class F8Matrix:
+    """An 8-bit floating-point matrix: q float8_e4m3fn [rows][cols] and scale float8_e8m0fnu [rows / block_rows][cols / 128]
+    (both rounded up), value = q * scale; block_rows 1 (inputs) or 128 (weights). Rows may lie further apart, those
+    of q a multiple of 16 bytes, those of scale a multiple of 4, the last one's rest included (see empty_scale)."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1):
+        what = "F8Matrix: q must be a CUDA float8_e4m3fn tensor [rows][cols], columns side by side"
+        _on(q, _F8, None, 2, what)
+        _need(block_rows in (1, F8_BLOCK), "F8Matrix: block_rows must be 1 or 128")
+        self.rows, self.cols = q.shape
+        self.block_rows, self.index, self.device = block_rows, q.get_device(), q.device
+        _need(self.cols > 0 and q.stride(1) == 1, what)
+        n, down, wide = -(-self.cols // F8_BLOCK), -(-self.rows // block_rows), -(-self.cols // (4 * F8_BLOCK)) * 4
+        _on(scale, _E8, self.index, 2, "F8Matrix: scale must be a float8_e8m0fnu tensor of rank 2 beside q")
+        _need(scale.shape == (down, n) and (n == 1 or scale.stride(1) == 1),
+              "F8Matrix: scale must be [rows / block_rows][cols / 128], both rounded up, columns side by side")
+        # strides of single rows are left open by torch
+        qs = q.stride(0) if self.rows > 1 else -(-self.cols // 16) * 16
+        ss = scale.stride(0) if down > 1 else wide
+        _need(down == 0 or scale.storage_offset() + (down - 1) * ss + wide <= scale.untyped_storage().nbytes(),
+              "F8Matrix: the last row of scale must have room for a multiple of four scales")
+        for v in (self.rows, self.cols):
+            _int32(v, "F8Matrix: rows and cols must fit in 32 bits")
+        self.q, self.scale = q, scale
+        # a matrix without rows has no addresses: any aligned ones do, nothing is read
+        self.c = bgq_f8matrix(q.data_ptr() or 256, scale.data_ptr() or 256, qs, ss, self.rows, self.cols, block_rows)
+        self.ref = C.byref(self.c)
+
+    @staticmethod
+    def empty_scale(rows: int, cols: int, device="cuda") -> torch.Tensor:
+        """Room for the scales of `rows` rows (or blocks of rows): rows a multiple of four bytes apart."""
+        n = -(-cols // F8_BLOCK)
+        return alloc((rows, -(-n // 4) * 4), torch.uint8, device).view(_E8)[:, :n]
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "F8Matrix":
+        """A matrix whose values are not set yet."""
+        _need(block_rows in (1, F8_BLOCK), "F8Matrix: block_rows must be 1 or 128")
+        _need(rows >= 0 and cols >= 16 and cols % 16 == 0, "F8Matrix: cols must be a multiple of 16")
+        return cls(alloc((rows, cols), torch.uint8, device).view(_F8), cls.empty_scale(-(-rows // block_rows), cols, device), block_rows)
+
+
+def _f8_like(m, rows: int, cols: int, block_rows: int | None, index: int, what: str):
+    """m is an F8Matrix of this shape on CUDA device `index`."""
+    _need(isinstance(m, F8Matrix) and m.index == index and (m.rows, m.cols) == (rows, cols)
+          and (block_rows is None or m.block_rows == block_rows), what)
+    return m
+
+
+def _rows_of(t, dtype, rows: int, cols: int, index: int, what: str) -> int:
+    """t is [rows][cols] of this type on CUDA device `index`, columns side by side; returns the values between rows."""
+    _on(t, dtype, index, 2, what)
+    _need(t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1), what)
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+
+
+def bgq_f8_quantise(x: torch.Tensor, out: F8Matrix | None = None, block_rows: int = 1, stream=None) -> F8Matrix:
+    """bgq_f8_quantise: x bf16 [rows][cols] (rows may lie further apart) as an F8Matrix."""
+    what = "bgq_f8_quantise: x must be a CUDA bf16 tensor [rows][cols], columns side by side"
+    _on(x, _BF16, None, 2, what)
+    dev, (rows, cols) = x.get_device(), x.shape
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_f8_quantise(x, out, block_rows)
+    sx = _rows_of(x, _BF16, rows, cols, dev, what)
+    if out is None:
+        out = F8Matrix.empty(rows, cols, block_rows, x.device)
+    _f8_like(out, rows, cols, None, dev, "bgq_f8_quantise: out must be an F8Matrix of x's shape beside it")
+    if rows:
+        r = load().bgq_f8_quantise(x.data_ptr(), sx, out.ref, _raw_stream(dev))
+        if r:
+            raise BGQError(r, "bgq_f8_quantise")
+    return out
+
+
+def bgq_rmsnorm_f8(h: torch.Tensor, rho: torch.Tensor | None, eps: float, delta: torch.Tensor | None = None,
+                   out: F8Matrix | None = None, a: torch.Tensor | None = None, want_a: bool = False, stream=None):
+    """bgq_rmsnorm_f8: h fp32 [batch][d] += delta (fp32 or bf16, nullable), in place -> (its RMSNorm times rho as an
+    F8Matrix, the same as bf16 `a` when given or wanted)."""
+    what = "bgq_rmsnorm_f8: h must be a CUDA fp32 tensor [batch][d], contiguous"
+    _on(h, torch.float32, None, 2, what)
+    dev, (B, d) = h.get_device(), h.shape
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_rmsnorm_f8(h, rho, eps, delta, out, a, want_a)
+    _need(h.is_contiguous(), what)
+    if delta is not None:
+        _on(delta, torch.float32 if delta.dtype is torch.float32 else _BF16, dev, 2, "bgq_rmsnorm_f8: delta must be fp32 or bf16 like h")
+        _need(delta.shape == h.shape and delta.is_contiguous(), "bgq_rmsnorm_f8: delta must be [batch][d], contiguous")
+    if rho is not None:
+        _on(rho, _BF16, dev, 1, "bgq_rmsnorm_f8: rho must be bf16 [d] beside h")
+        _need(rho.shape[0] == d and rho.is_contiguous(), "bgq_rmsnorm_f8: rho must be bf16 [d], contiguous")
+    if out is None:
+        out = F8Matrix.empty(B, d, 1, h.device)
+    _f8_like(out, B, d, 1, dev, "bgq_rmsnorm_f8: out must be an F8Matrix of h's shape beside it, with a scale for each row")
+    if a is None and want_a:
+        a = alloc((B, d), _BF16, h.device)
+    if a is not None:
+        _on(a, _BF16, dev, 2, "bgq_rmsnorm_f8: a must be bf16 like h")
+        _need(a.shape == h.shape and a.is_contiguous(), "bgq_rmsnorm_f8: a must be [batch][d], contiguous")
+    if B:
+        r = load().bgq_rmsnorm_f8(h.data_ptr(), _ptr(delta), delta is not None and delta.dtype is torch.float32, _ptr(rho), B, d,
+                                  eps, out.ref, _ptr(a), _raw_stream(dev))
+        if r:
+            raise BGQError(r, "bgq_rmsnorm_f8")
+    return out, a
+
+
+def f8_gemm_workspace_bytes(W: F8Matrix, x: F8Matrix) -> int:
+    return load().bgq_f8_gemm_workspace_bytes(W.ref, x.ref)
+
+
+def _f8_workspace(W: F8Matrix, x: F8Matrix, ws):
+    if ws is None:
+        return workspace(f8_gemm_workspace_bytes(W, x), x.device)
+    _need(isinstance(ws, torch.Tensor) and ws.get_device() == x.index and ws.is_contiguous(), "ws must be beside x, contiguous")
+    return ws
+
+
+def bgq_f8_gemm(W: F8Matrix, x: F8Matrix, out: torch.Tensor | None = None, out_f32: torch.Tensor | None = None,
+                want_out: bool = True, want_f32: bool = False, ws: torch.Tensor | None = None, stream=None):
+    """bgq_f8_gemm: y = x W^T, W with block_rows 128 -> (y bf16, y fp32), [x.rows][W.rows] each, rows a multiple of 8
+    values apart (both alike). Buffers that are given are filled; where none is, the bf16 one is made (unless
+    want_out is False) and the fp32 one where wanted."""
+    what = "bgq_f8_gemm: W and x must be F8Matrix on one device, of the same cols, W with block_rows 128"
+    _need(isinstance(W, F8Matrix) and isinstance(x, F8Matrix) and W.index == x.index, what)
+    dev, M, N = x.index, x.rows, W.rows
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_f8_gemm(W, x, out, out_f32, want_out, want_f32, ws)
+    wide = -(-N // 8) * 8
+    if out is None and want_out and out_f32 is None:
+        out = alloc((M, wide), _BF16, x.device)[:, :N]
+    if out_f32 is None and want_f32:
+        out_f32 = alloc((M, wide), torch.float32, x.device)[:, :N]
+    so = None if out is None else _rows_of(out, _BF16, M, N, dev, "bgq_f8_gemm: out must be bf16 [x.rows][W.rows], columns side by side")
+    sf = None if out_f32 is None else _rows_of(out_f32, torch.float32, M, N, dev,
+                                               "bgq_f8_gemm: out_f32 must be fp32 [x.rows][W.rows], columns side by side")
+    _need(so is None or sf is None or so == sf, "bgq_f8_gemm: out and out_f32 must have their rows equally far apart")
+    ws = _f8_workspace(W, x, ws)
+    r = load().bgq_f8_gemm(W.ref, x.ref, _out_ptr(out, M), _out_ptr(out_f32, M), sf if so is None else so or 0, ws.data_ptr(), ws.nbytes,
+                           _raw_stream(dev))
+    if r:
+        raise BGQError(r, "bgq_f8_gemm")
+    return out, out_f32
+
+
+def _out_ptr(t, rows: int):
+    """An output's address; one without rows has none, and any aligned one does."""
+    return None if t is None else t.data_ptr() if rows else 256
+
+
+def bgq_f8_swiglu(gate: F8Matrix, up: F8Matrix, x: F8Matrix, h: F8Matrix | None = None, out: torch.Tensor | None = None,
+                  want_h: bool = True, want_out: bool = False, ws: torch.Tensor | None = None, stream=None):
+    """bgq_f8_swiglu: silu(x gate^T) * (x up^T) -> (h as an F8Matrix, out bf16), [x.rows][gate.rows]. Buffers that
+    are given are filled; where none is, h is made (unless want_h is False) and out where wanted."""
+    what = "bgq_f8_swiglu: gate, up and x must be F8Matrix on one device"
+    _need(all(isinstance(m, F8Matrix) for m in (gate, up, x)) and gate.index == up.index == x.index, what)
+    dev, M, N = x.index, x.rows, gate.rows
+    if stream is not None or _device() != dev:
+        with _there(dev, stream):
+            return bgq_f8_swiglu(gate, up, x, h, out, want_h, want_out, ws)
+    if h is None and want_h and out is None:
+        h = F8Matrix.empty(M, N, 1, x.device)
+    if out is None and want_out:
+        out = alloc((M, N), _BF16, x.device)
+    if h is not None:
+        _f8_like(h, M, N, 1, dev, "bgq_f8_swiglu: h must be an F8Matrix [x.rows][gate.rows] beside x, with a scale for each row")
+    so = 0 if out is None else _rows_of(out, _BF16, M, N, dev, "bgq_f8_swiglu: out must be bf16 [x.rows][gate.rows], columns side by side")
+    ws = _f8_workspace(gate, x, ws)
+    r = load().bgq_f8_swiglu(gate.ref, up.ref, x.ref, None if h is None else h.ref, _out_ptr(out, M), so, ws.data_ptr(), ws.nbytes,
+                             _raw_stream(dev))
+    if r:
+        raise BGQError(r, "bgq_f8_swiglu")
+    return h, out
 
 
 class Stack:

@@ -460,6 +460,63 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
                           int32_t q_heads, float scale, int32_t causal, int32_t window, uint16_t* out,
                           int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------- the dense path in e4m3
+ * What stands around attention and beside the experts when many tokens pass at
+ * once (a prompt's projections and its dense feed-forward block), from single
+ * tokens on. The pages have no counterpart: their projections take one token.
+ *
+ * An 8-bit floating-point matrix (host struct, device arrays).
+ *   q     : e4m3 codes [rows][cols], rows q_stride bytes apart;
+ *   scale : e8m0 bytes e, one for each 128 columns of a row (block_rows 1: inputs) or of 128 rows
+ *           (block_rows 128: weights), [rows / block_rows rounded up][cols / 128 rounded up], rows scale_stride
+ *           bytes apart. value = code * 2^(e - 127).
+ * cols a multiple of 16, at most 65536; rows below 2^24; q 16-byte aligned, q_stride a multiple of 16 and at least
+ * cols; scale 4-byte aligned, scale_stride a multiple of 4 and at least cols / 128 rounded up to one: four
+ * scales are read at a time, so the last row too has that many bytes (what they hold does not matter).
+ * Codes of NaN (0x7f, 0xff) make NaN of every sum that they enter; the scale byte 255 is not allowed. Unlike
+ * other weights these may be written by the call just before on the same stream. */
+typedef struct bgq_f8matrix {
+  uint8_t* q;
+  uint8_t* scale;
+  int64_t q_stride;
+  int64_t scale_stride;
+  int32_t rows;
+  int32_t cols;
+  int32_t block_rows;
+} bgq_f8matrix;
+
+/* m = x quantised. x: bf16 [rows][cols], rows x_stride values apart (a multiple of 8). A block's scale is the
+ * smallest power of two, 2^-127 at least, that leaves none of its values beyond 448; codes are rounded to
+ * nearest, halves to even. A block that holds a NaN or an infinity reads back as NaN (scale 1). rows may be 0. */
+int32_t bgq_f8_quantise(const uint16_t* x, int64_t x_stride, const bgq_f8matrix* m, void* stream);
+
+/* h += delta; a = h / sqrt(mean(h^2) + eps) * rho; m = a quantised, as above, from its fp32 values.
+ * h: fp32 [batch][d], updated; delta (nullable): [batch][d], fp32 where delta_f32 != 0, else bf16;
+ * rho (nullable => 1): bf16 [d]; m: batch x d with block_rows 1; a (nullable): bf16 [batch][d], for what
+ * reads the same input in bf16 (a router). The sum of squares is fp32. d a multiple of 16, at most 65536;
+ * batch may be 0. h, delta, rho and a 16-byte aligned. */
+int32_t bgq_rmsnorm_f8(float* h, const void* delta, int32_t delta_f32, const uint16_t* rho, int32_t batch, int32_t d,
+                       float eps, const bgq_f8matrix* m, uint16_t* a, void* stream);
+
+/* y[b][n] = sum_k x[b][k] W[n][k]: x with block_rows 1, W (rows = outputs) with block_rows 128, the same cols.
+ * y (bf16) and y_f32 (fp32), nullable but not both: [x->rows][W->rows], rows y_stride values apart (a multiple
+ * of 8), 16-byte aligned. Products are exact and sums fp32 (each step of 32 columns is cut to fp32 where a tensor
+ * core adds it). The same inputs give the same bits; a row's do not depend on what the other rows hold.
+ * x->rows may be 0; W->rows at most 2^20. y must overlap no input.
+ * ws: bgq_f8_gemm_workspace_bytes bytes, for the status word; calls may share it, at once too. */
+size_t bgq_f8_gemm_workspace_bytes(const bgq_f8matrix* W, const bgq_f8matrix* x);
+int32_t bgq_f8_gemm(const bgq_f8matrix* W, const bgq_f8matrix* x, uint16_t* y, float* y_f32, int64_t y_stride,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* The first half of a gated feed-forward block, both projections and what joins them in one kernel:
+ *   out[b][n] = silu(g) * u,  g = sum_k x[b][k] gate[n][k],  u = sum_k x[b][k] up[n][k]   (fp32, rounded once).
+ * gate and up: the same rows and cols, block_rows 128, rows a multiple of 16. h (nullable): x->rows x gate->rows,
+ * block_rows 1, out quantised as by bgq_f8_quantise from its fp32 values: bgq_f8_gemm with the block's
+ * third matrix takes it as it is. y (nullable): bf16 [x->rows][gate->rows], rows y_stride apart. Not both NULL.
+ * Otherwise as bgq_f8_gemm (ws: its size for gate and x). */
+int32_t bgq_f8_swiglu(const bgq_f8matrix* gate, const bgq_f8matrix* up, const bgq_f8matrix* x, const bgq_f8matrix* h,
+                      uint16_t* y, int64_t y_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* One decode token through a stack of n_layers resident layers (batch 1):
  *   h = x (widened to fp32); for each layer l:
  *     a = bf16(rmsnorm(h, rho[l], eps)); h += layer_l(a)  (fp32, unrounded);
