@@ -1,0 +1,295 @@
+// f8_many.cu — products of e4m3 matrices for many rows, on tcgen05.
+//
+// Tiles of 256 rows of x by 256 rows of W (gated: 128 of gate beside the same 128 of up), each the work of two CTAs that
+// share their matrix instructions: a CTA brings 128 rows of both operands for every block of 128 columns, and has the sums of
+// its 128 rows of x and all 256 of W in tensor memory. A pair of CTAs on every two SMs walks through the tiles.
+// The warps are specialised: one copies, one (of the first CTA) issues, four keep the scales in tensor memory
+// (f8_tc.cuh), four write the results, a thread a row.
+//
+// Tensor memory has 512 columns: two tiles' sums of 256 and two sets of scales of 12 do not fit beside each other. The second
+// tile's sums start kManyShared columns before the first's end, and a tile's epilogue reads those columns first: the next tile's
+// instructions wait for them alone.
+#include "f8_tc.cuh"
+
+namespace bgq {
+
+constexpr int kManyThreads = 384;  // warp 0: copies, 1: instructions, 2: tensor memory, 4-7: scales, 8-11: results
+constexpr int kManyStages = 6, kManyStage = 2 * kF8Tile;
+constexpr int kManyRows = 256, kManyCols = 256;
+constexpr int kManyShared = 32;              // columns that both tiles' sums use
+constexpr int kManyScales = 512 - 32;        // two sets of scales, 16 columns apart: x's 4, then W's 8
+constexpr int kManyBars = 2 * kManyStages + 7;
+constexpr size_t kManySmem = 1024 + (size_t)kManyStages * kManyStage;
+
+struct ManyWork {
+  int tiles, down, group;  // tiles; tiles of x's rows; of which `group` are walked through beside each other
+  int across;
+  // Tile i: groups of `group` tiles of x's rows by all of W's, so that what runs at a time shares both operands.
+  __device__ __forceinline__ void at(int i, int& m, int& n) const {
+    const int wide = group * across, g = i / wide, in = i - g * wide, h = min(group, down - g * group);
+    n = in / h;
+    m = g * group + in - n * h;
+  }
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    k_f8_many(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0,
+              const __grid_constant__ CUtensorMap mw1, const F8Prod p, const ManyWork work) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ uint64_t bars[kManyBars];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail;
+  unsigned char* stages = smem_raw + (1024 - (tc_smem(smem_raw) & 1023)) % 1024;
+  uint64_t *full = bars, *empty = full + kManyStages, *sf_full = empty + kManyStages, *sf_free = sf_full + 2,
+           *acc_full = sf_free + 2, *acc_free = acc_full + 2;
+  volatile int* fail = &s_fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = f8_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int blocks = f8_blocks(p.K), groups = (blocks + 3) >> 2;
+  if (tid == 0) {
+    for (int i = 0; i < kManyStages; ++i) {
+      tc_mbar_init(&full[i]);
+      tc_mbar_init(&empty[i]);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc_mbar_init(&sf_full[i], 8);  // four warps of each CTA
+      tc_mbar_init(&sf_free[i]);
+      tc_mbar_init(&acc_full[i]);
+    }
+    tc_mbar_init(acc_free, 8);
+    s_fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    f8_map_ahead(&mx);
+    f8_map_ahead(rank ? &mw1 : &mw0);
+  }
+  pdl_wait();  // tensor memory, too, is taken only once earlier kernels have given theirs back
+  if (warp == 2) f8_tmem_alloc<2>(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  f8_cluster_sync();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* mw = GATED && rank ? &mw1 : &mw0;
+      int s = 0;
+      uint32_t par = 1;
+      bool ok = true;
+      for (int i = pair; ok && i < work.tiles; i += pairs) {
+        int tm, tn;
+        work.at(i, tm, tn);
+        const int m0 = tm * kManyRows + (int)rank * 128;
+        const int n0 = GATED ? tn * 128 : tn * kManyCols + (int)rank * 128;
+        for (int b = 0; b < blocks; ++b) {
+          if (!(ok = f8_wait(&empty[s], par, fail))) break;
+          unsigned char* st = stages + s * kManyStage;
+          const uint32_t bar = f8_at(&full[s], 0);
+          if (rank == 0) f8_expect(&full[s], 2 * kManyStage);
+          f8_load<2>(st, &mx, b * 128, m0, bar);
+          f8_load<2>(st + kF8Tile, mw, b * 128, n0, bar);
+          if (++s == kManyStages) {
+            s = 0;
+            par ^= 1;
+          }
+        }
+      }
+      // every stage's last use is over, and told, before the CTA may end
+      for (int i = 0; ok && i < kManyStages; ++i) {
+        ok = f8_wait(&empty[s], par, fail);
+        if (++s == kManyStages) {
+          s = 0;
+          par ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      int s = 0, set = 0, t = 0;
+      uint32_t par = 0, sf_par = 0;
+      bool ok = true;
+      for (int i = pair; ok && i < work.tiles; i += pairs, ++t) {
+        if (t && !(ok = f8_wait(acc_free, (t - 1) & 1, fail))) break;
+        const uint32_t d = tmem + (t & 1 ? kManyCols - kManyShared : 0);
+        for (int b = 0; b < blocks; ++b) {
+          const int sf = b & 3;
+          if (sf == 0 && !(ok = f8_wait(&sf_full[set], sf_par, fail))) break;
+          if (!(ok = f8_wait(&full[s], par, fail))) break;
+          tc_fence_after();
+          const uint32_t at = tc_smem(stages + s * kManyStage), scales = tmem + kManyScales + set * 16;
+          const uint64_t a = f8_desc(at), w = f8_desc(at + kF8Tile);
+          const uint32_t idesc = f8_idesc(kManyRows, kManyCols, sf);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f8_tc_mma<2>(d, a + 2 * k, w + 2 * k, idesc, scales, scales + 4, (b | k) ? 1u : 0u);
+          f8_commit<2>(&empty[s]);
+          if (++s == kManyStages) {
+            s = 0;
+            par ^= 1;
+          }
+          if (sf == 3 || b == blocks - 1) {
+            f8_commit<2>(&sf_free[set]);
+            if (set ^= 1; set == 0) sf_par ^= 1;
+          }
+        }
+        if (ok) f8_commit<2>(&acc_full[t & 1]);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // a lane has the scales of x's rows l, 32 + l, ...; W's are the same for a whole block of 128 rows
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kManyScales, ready[2] = {f8_at(&sf_full[0], 0), f8_at(&sf_full[1], 0)};
+    int set = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    for (int i = pair; ok && i < work.tiles; i += pairs) {
+      int tm, tn;
+      work.at(i, tm, tn);
+      const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn, wbs = f8_blocks(p.N);
+      const uint8_t* w0 = wb < wbs ? p.ws[0] + wb * p.ws_stride[0] : nullptr;
+      const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] : wb + 1 < wbs ? p.ws[0] + (wb + 1) * p.ws_stride[0] : nullptr;
+      uint32_t x[4], w[2];
+      auto load = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(p.xs + (int64_t)(m0 + 32 * j) * p.xs_stride + 4 * g) : 0u;
+        w[0] = w0 ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
+        w[1] = w1 ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
+      };
+      load(0);
+      for (int g = 0; g < groups; ++g) {
+        if (!(ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail)))) break;
+        tc_fence_after();
+        f8_tmem_st4(at + set * 16, x[0], x[1], x[2], x[3]);
+        f8_tmem_st4(at + set * 16 + 4, w[0], w[0], w[0], w[0]);
+        f8_tmem_st4(at + set * 16 + 8, w[1], w[1], w[1], w[1]);
+        f8_tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) f8_arrive_at(ready[set]);
+        if (g + 1 < groups) load(g + 1);
+        if (set ^= 1; set == 0) par ^= 1;
+      }
+    }
+    for (int i = 0; ok && i < 2; ++i) {
+      ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail));
+      if (set ^= 1; set == 0) par ^= 1;
+    }
+  } else if (warp >= 8) {
+    const uint32_t freed = f8_at(acc_free, 0), lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    int t = 0;
+    for (int i = pair; i < work.tiles; i += pairs, ++t) {
+      int tm, tn;
+      work.at(i, tm, tn);
+      const int row = tm * kManyRows + (int)rank * 128 + (warp & 3) * 32 + lane;
+      if (!__all_sync(kFull, f8_wait(&acc_full[t & 1], (t >> 1) & 1, fail))) break;
+      tc_fence_after();
+      // the columns that the next tile wants come first: the last ones of the first sums, the first of the second
+      const bool back = (t & 1) == 0;
+      const uint32_t acc = lanes + (back ? 0 : kManyCols - kManyShared);
+      if (!GATED) {
+#pragma unroll 1
+        for (int c = 0; c < kManyCols / 32; ++c) {
+          const int col = 32 * (back ? kManyCols / 32 - 1 - c : c);
+          float v[32];
+          f8_tmem_ld32(acc + col, v);
+          f8_tmem_ld_wait();
+          if (c == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) f8_arrive_at(freed);
+          }
+          if (row < p.M) f8_store32(p, row, tn * kManyCols + col, v);
+        }
+      } else {
+        float h[4][32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = 32 * (back ? 3 - c : c);
+          float u[32];
+          f8_tmem_ld32(acc + col, h[c]);
+          f8_tmem_ld32(acc + 128 + col, u);
+          f8_tmem_ld_wait();
+          if (c == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) f8_arrive_at(freed);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            h[c][j] = f8_swiglu(h[c][j], u[j]);
+            top = max(top, __float_as_uint(h[c][j]) & 0x7fffffffu);
+          }
+          if (p.y && row < p.M) f8_store32(p, row, tn * 128 + col, h[c]);
+        }
+        if (p.h && row < p.M) {
+          const bool fine = f8_finite(top);
+          const int byte = fine ? f8_scale_byte(top) : kF8One;
+          const float inv = f8_inverse(byte);
+          p.hs[row * p.hs_stride + tn] = (uint8_t)byte;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = tn * 128 + 32 * (back ? 3 - c : c);
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+              uint4 q = make_uint4(kF8Nan4, kF8Nan4, kF8Nan4, kF8Nan4);
+              const float* v = &h[c][j];
+              if (fine)
+                q = make_uint4(f8_codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), f8_codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
+                               f8_codes4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
+                               f8_codes4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
+              if (col + j < p.N) *reinterpret_cast<uint4*>(p.h + row * p.h_stride + col + j) = q;
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (*fail) {  // a wait has run out: tell the other CTA, let copies in flight land, and end
+    if (tid == 0) atomicExch(&p.ctrl->status, BGQ_ERR_TIMEOUT);
+    if (lane == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(f8_at(&s_fail, rank ^ 1)), "r"(1) : "memory");
+    for (const unsigned long long t0 = tc_time(); tc_time() - t0 < 5000000ull;) __nanosleep(10000);
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  f8_cluster_sync();
+  if (warp == 2) f8_tmem_free<2>(tmem, 512);
+}
+
+cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
+  CUtensorMap mx, mw[2];
+  if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride)) return cudaErrorInvalidValue;
+  for (int i = 0; i < 2; ++i)
+    if (!f8_map(&mw[i], p.w[i], p.N, p.K, p.w_stride[i])) return cudaErrorInvalidValue;
+  const int wide = gated ? 128 : kManyCols;
+  ManyWork work;
+  work.down = (p.M + kManyRows - 1) / kManyRows;
+  work.across = (p.N + wide - 1) / wide;
+  work.tiles = work.down * work.across;
+  work.group = work.down < 8 ? work.down : 8;
+  const int pairs = num_sms() / 2;
+  const void* kern = gated ? (const void*)k_f8_many<true> : (const void*)k_f8_many<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kManySmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (work.tiles < pairs ? work.tiles : pairs));
+  cfg.blockDim = dim3(kManyThreads);
+  cfg.dynamicSmemBytes = kManySmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return gated ? cudaLaunchKernelEx(&cfg, k_f8_many<true>, mx, mw[0], mw[1], p, work)
+               : cudaLaunchKernelEx(&cfg, k_f8_many<false>, mx, mw[0], mw[0], p, work);
+}
+
+}  // namespace bgq

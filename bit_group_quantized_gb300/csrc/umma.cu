@@ -36,8 +36,6 @@
 // every thread of every CTA on every path. The swizzled copies assume a
 // 1024-byte aligned dynamic shared-memory base; a launch that does not get
 // one writes BGQ_ERR_CUDA to the status word and computes nothing.
-#include <cuda.h>
-
 #include <mutex>
 #include <vector>
 #include <cuda_fp16.h>
@@ -46,6 +44,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tc_map.h"
 
 namespace bgq {
 
@@ -666,25 +665,6 @@ int tc_act_rows(int B, int K) { return ((plan_max_pairs(B, K) + 15 * plan_max_bi
 size_t tc_act_bytes(int d, int f, int B, int K) {
   const int kc = d > f ? d : f;
   return tc_up256((size_t)tc_act_rows(B, K) * (kc / kTcBK) * 128) + tc_up256((size_t)tc_act_rows(B, K) * 4);
-}
-
-// cuTensorMapEncodeTiled, found through the runtime (the library does not link
-// the driver library itself).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return (EncodeTiledFn) nullptr;
-    }
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
 }
 
 // A 3-D byte view [nexp][rows][row_bytes] of `base` (experts `estride` bytes
