@@ -16,9 +16,10 @@ namespace bgq {
 constexpr int kManyThreads = 384;  // warp 0: copies, 1: instructions, 2: tensor memory, 4-7: scales, 8-11: results
 constexpr int kManyStages = 6, kManyStage = 2 * kF8Tile;
 constexpr int kManyRows = 256, kManyCols = 256;
-constexpr int kManyShared = 32;              // columns that both tiles' sums use
-constexpr int kManyScales = 512 - 32;        // two sets of scales, 16 columns apart: x's 4, then W's 8
-constexpr int kManyBars = 2 * kManyStages + 7;
+constexpr int kManySets = 4;                 // sets of scales, 16 columns apart: x's 4, then W's 8
+constexpr int kManyScales = 512 - 16 * kManySets;
+constexpr int kManyShared = 16 * kManySets;  // columns that both tiles' sums use
+constexpr int kManyBars = 2 * kManyStages + 2 * kManySets + 3;
 constexpr size_t kManySmem = 1024 + (size_t)kManyStages * kManyStage;
 
 struct ManyWork {
@@ -41,8 +42,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   unsigned char* stages = smem_raw + (1024 - (tc_smem(smem_raw) & 1023)) % 1024;
-  uint64_t *full = bars, *empty = full + kManyStages, *sf_full = empty + kManyStages, *sf_free = sf_full + 2,
-           *acc_full = sf_free + 2, *acc_free = acc_full + 2;
+  uint64_t *full = bars, *empty = full + kManyStages, *sf_full = empty + kManyStages, *sf_free = sf_full + kManySets,
+           *acc_full = sf_free + kManySets, *acc_free = acc_full + 2;
   volatile int* fail = &s_fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = f8_rank();
@@ -53,11 +54,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       tc_mbar_init(&full[i]);
       tc_mbar_init(&empty[i]);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kManySets; ++i) {
       tc_mbar_init(&sf_full[i], 8);  // four warps of each CTA
       tc_mbar_init(&sf_free[i]);
-      tc_mbar_init(&acc_full[i]);
     }
+    for (int i = 0; i < 2; ++i) tc_mbar_init(&acc_full[i]);
     tc_mbar_init(acc_free, 8);
     s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -107,74 +108,103 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      const uint32_t lead = f8_elect();
       int s = 0, set = 0, t = 0;
       uint32_t par = 0, sf_par = 0;
       bool ok = true;
       for (int i = pair; ok && i < work.tiles; i += pairs, ++t) {
-        if (t && !(ok = f8_wait(acc_free, (t - 1) & 1, fail))) break;
+        if (t && !(ok = __all_sync(kFull, f8_wait(acc_free, (t - 1) & 1, fail)))) break;
         const uint32_t d = tmem + (t & 1 ? kManyCols - kManyShared : 0);
         for (int b = 0; b < blocks; ++b) {
           const int sf = b & 3;
-          if (sf == 0 && !(ok = f8_wait(&sf_full[set], sf_par, fail))) break;
-          if (!(ok = f8_wait(&full[s], par, fail))) break;
+          if (sf == 0 && !(ok = __all_sync(kFull, f8_wait(&sf_full[set], sf_par, fail)))) break;
+          if (!(ok = __all_sync(kFull, f8_wait(&full[s], par, fail)))) break;
           tc_fence_after();
           const uint32_t at = tc_smem(stages + s * kManyStage), scales = tmem + kManyScales + set * 16;
           const uint64_t a = f8_desc(at), w = f8_desc(at + kF8Tile);
           const uint32_t idesc = f8_idesc(kManyRows, kManyCols, sf);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f8_tc_mma<2>(d, a + 2 * k, w + 2 * k, idesc, scales, scales + 4, (b | k) ? 1u : 0u);
-          f8_commit<2>(&empty[s]);
+          for (int k = 0; k < 4; ++k) f8_tc_mma<2>(d, a + 2 * k, w + 2 * k, idesc, scales, scales + 4, (b | k) ? 1u : 0u, lead);
+          f8_commit<2>(&empty[s], lead);
           if (++s == kManyStages) {
             s = 0;
             par ^= 1;
           }
           if (sf == 3 || b == blocks - 1) {
-            f8_commit<2>(&sf_free[set]);
-            if (set ^= 1; set == 0) sf_par ^= 1;
+            f8_commit<2>(&sf_free[set], lead);
+            if (++set == kManySets) {
+              set = 0;
+              sf_par ^= 1;
+            }
           }
         }
-        if (ok) f8_commit<2>(&acc_full[t & 1]);
+        if (ok) f8_commit<2>(&acc_full[t & 1], lead);
       }
     }
   } else if (warp >= 4 && warp < 8) {
     // a lane has the scales of x's rows l, 32 + l, ...; W's are the same for a whole block of 128 rows
-    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kManyScales, ready[2] = {f8_at(&sf_full[0], 0), f8_at(&sf_full[1], 0)};
-    int set = 0;
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kManyScales, ready = f8_at(&sf_full[0], 0);
+    const int wbs = f8_blocks(p.N);
+    // A chunk: the words of four groups of blocks. They are loaded a chunk ahead, of this tile or the next (loaded a group
+    // or two ahead, they held the instructions up: 8191 x 12288 x 4096 took 298 us, 267 so).
+    struct Chunk {
+      uint32_t x[4][4], w[4][2];
+    } cur = {}, next = {};
+    int li = pair, lg = 0, set = 0;  // tile and first group of the next chunk
     uint32_t par = 1;
-    bool ok = true;
-    for (int i = pair; ok && i < work.tiles; i += pairs) {
+    auto load = [&](Chunk& v) {
+      if (li >= work.tiles) return;
       int tm, tn;
-      work.at(i, tm, tn);
-      const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn, wbs = f8_blocks(p.N);
-      const uint8_t* w0 = wb < wbs ? p.ws[0] + wb * p.ws_stride[0] : nullptr;
-      const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] : wb + 1 < wbs ? p.ws[0] + (wb + 1) * p.ws_stride[0] : nullptr;
-      uint32_t x[4], w[2];
-      auto load = [&](int g) {
+      work.at(li, tm, tn);
+      const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn;
+      const uint8_t* x = p.xs + (int64_t)m0 * p.xs_stride + 4 * lg;
+      const uint8_t* w0 = p.ws[0] + wb * p.ws_stride[0] + 4 * lg;
+      const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] + 4 * lg : wb + 1 < wbs ? w0 + p.ws_stride[0] : w0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const bool there = lg + g < groups;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          x[j] = m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(p.xs + (int64_t)(m0 + 32 * j) * p.xs_stride + 4 * g) : 0u;
-        w[0] = w0 ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
-        w[1] = w1 ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
-      };
-      load(0);
-      for (int g = 0; g < groups; ++g) {
-        if (!(ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail)))) break;
-        tc_fence_after();
-        f8_tmem_st4(at + set * 16, x[0], x[1], x[2], x[3]);
-        f8_tmem_st4(at + set * 16 + 4, w[0], w[0], w[0], w[0]);
-        f8_tmem_st4(at + set * 16 + 8, w[1], w[1], w[1], w[1]);
-        f8_tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) f8_arrive_at(ready[set]);
-        if (g + 1 < groups) load(g + 1);
-        if (set ^= 1; set == 0) par ^= 1;
+          v.x[g][j] = there && m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * g) : 0u;
+        v.w[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
+        v.w[g][1] = there ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
       }
-    }
-    for (int i = 0; ok && i < 2; ++i) {
+      if ((lg += 4) >= groups) {
+        lg = 0;
+        li += pairs;
+      }
+    };
+    load(cur);
+    bool ok = true;
+    for (int i = pair; ok && i < work.tiles; i += pairs)
+      for (int g0 = 0; ok && g0 < groups; g0 += 4) {
+        load(next);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (!ok || g0 + g >= groups) continue;
+          if (!(ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail)))) continue;
+          tc_fence_after();
+          f8_tmem_st4(at + set * 16, cur.x[g][0], cur.x[g][1], cur.x[g][2], cur.x[g][3]);
+          f8_tmem_st4(at + set * 16 + 4, cur.w[g][0], cur.w[g][0], cur.w[g][0], cur.w[g][0]);
+          f8_tmem_st4(at + set * 16 + 8, cur.w[g][1], cur.w[g][1], cur.w[g][1], cur.w[g][1]);
+          f8_tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) f8_arrive_at(ready + 8 * set);
+          if (++set == kManySets) {
+            set = 0;
+            par ^= 1;
+          }
+        }
+        cur = next;
+      }
+    for (int i = 0; ok && i < kManySets; ++i) {
       ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail));
-      if (set ^= 1; set == 0) par ^= 1;
+      if (++set == kManySets) {
+        set = 0;
+        par ^= 1;
+      }
     }
   } else if (warp >= 8) {
     const uint32_t freed = f8_at(acc_free, 0), lanes = tmem + ((uint32_t)(warp & 3) << 21);
@@ -188,41 +218,55 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // the columns that the next tile wants come first: the last ones of the first sums, the first of the second
       const bool back = (t & 1) == 0;
       const uint32_t acc = lanes + (back ? 0 : kManyCols - kManyShared);
+      auto drained = [&] {
+        f8_tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) f8_arrive_at(freed);
+      };
+      static_assert(kManyShared == 64, "two chunks of 32 columns");
       if (!GATED) {
+        auto column = [&](int c) { return 32 * (back ? kManyCols / 32 - 1 - c : c); };
+        float v[2][32];
 #pragma unroll 1
-        for (int c = 0; c < kManyCols / 32; ++c) {
-          const int col = 32 * (back ? kManyCols / 32 - 1 - c : c);
-          float v[32];
-          f8_tmem_ld32(acc + col, v);
-          f8_tmem_ld_wait();
-          if (c == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) f8_arrive_at(freed);
+        for (int c = 0; c < kManyCols / 32; c += 2) {
+          f8_tmem_ld32(acc + column(c), v[0]);
+          f8_tmem_ld32(acc + column(c + 1), v[1]);
+          if (c == 0)
+            drained();
+          else
+            f8_tmem_ld_wait();
+          if (row < p.M) {
+            f8_store32(p, row, tn * kManyCols + column(c), v[0]);
+            f8_store32(p, row, tn * kManyCols + column(c + 1), v[1]);
           }
-          if (row < p.M) f8_store32(p, row, tn * kManyCols + col, v);
         }
       } else {
+        auto column = [&](int c) { return 32 * (back ? 3 - c : c); };
         float h[4][32];
         uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = 32 * (back ? 3 - c : c);
-          float u[32];
-          f8_tmem_ld32(acc + col, h[c]);
-          f8_tmem_ld32(acc + 128 + col, u);
-          f8_tmem_ld_wait();
-          if (c == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) f8_arrive_at(freed);
-          }
+        auto join = [&](int c, float (&g)[32], const float (&u)[32]) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            h[c][j] = f8_swiglu(h[c][j], u[j]);
-            top = max(top, __float_as_uint(h[c][j]) & 0x7fffffffu);
+            g[j] = f8_swiglu(g[j], u[j]);
+            top = max(top, __float_as_uint(g[j]) & 0x7fffffffu);
           }
-          if (p.y && row < p.M) f8_store32(p, row, tn * 128 + col, h[c]);
+          if (p.y && row < p.M) f8_store32(p, row, tn * 128 + column(c), g);
+        };
+        float u[2][32];
+        f8_tmem_ld32(acc + column(0), h[0]);
+        f8_tmem_ld32(acc + 128 + column(0), u[0]);
+        f8_tmem_ld32(acc + column(1), h[1]);
+        f8_tmem_ld32(acc + 128 + column(1), u[1]);
+        drained();
+        join(0, h[0], u[0]);
+        join(1, h[1], u[1]);
+#pragma unroll
+        for (int c = 2; c < 4; ++c) {
+          f8_tmem_ld32(acc + column(c), h[c]);
+          f8_tmem_ld32(acc + 128 + column(c), u[0]);
+          f8_tmem_ld_wait();
+          join(c, h[c], u[0]);
         }
         if (p.h && row < p.M) {
           const bool fine = f8_finite(top);
@@ -231,7 +275,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           p.hs[row * p.hs_stride + tn] = (uint8_t)byte;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int col = tn * 128 + 32 * (back ? 3 - c : c);
+            const int col = tn * 128 + column(c);
 #pragma unroll
             for (int j = 0; j < 32; j += 16) {
               uint4 q = make_uint4(kF8Nan4, kF8Nan4, kF8Nan4, kF8Nan4);
@@ -248,14 +292,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   }
   __syncwarp();
-  if (*fail) {  // a wait has run out: tell the other CTA, let copies in flight land, and end
-    if (tid == 0) atomicExch(&p.ctrl->status, BGQ_ERR_TIMEOUT);
-    if (lane == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(f8_at(&s_fail, rank ^ 1)), "r"(1) : "memory");
-    for (const unsigned long long t0 = tc_time(); tc_time() - t0 < 5000000ull;) __nanosleep(10000);
-  }
+  if (*fail && lane == 0)  // a wait has run out: the other CTA's end too
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(f8_at(&s_fail, rank ^ 1)), "r"(1) : "memory");
   tc_fence_before();
-  __syncwarp();
   __syncthreads();
+  if (*fail) {  // copies in flight land before the CTA ends
+    if (tid == 0) atomicExch(&p.ctrl->status, BGQ_ERR_TIMEOUT);
+    for (const unsigned long long t0 = tc_time(); tc_time() - t0 < 5000000ull;) __nanosleep(10000);
+    __syncthreads();
+  }
   f8_cluster_sync();
   if (warp == 2) f8_tmem_free<2>(tmem, 512);
 }

@@ -19,23 +19,11 @@ namespace bgq {
 constexpr long long kF8TimeoutNs = 1000000000ll;
 constexpr int kF8Tile = 128 * 128;  // bytes of an operand tile
 
-// Bounded wait: on expiry, or once *fail is set elsewhere, it returns and *fail is set. Arrivals may come from the
-// other CTA of a cluster.
-__device__ __forceinline__ bool f8_try(uint64_t* m, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(tc_smem(m)), "r"(parity), "r"(kTcSuspendNs)
-      : "memory");
-  return ok != 0;
-}
+// Bounded wait: on expiry, or once *fail is set elsewhere, it returns false and *fail is set.
 static __device__ __noinline__ bool f8_wait_loop(uint64_t* m, uint32_t parity, volatile int* fail) {
   const unsigned long long t0 = tc_time();
   long long it = 0;
-  while (!f8_try(m, parity)) {
+  while (!tc_mbar_try_suspend(m, parity)) {
     if (*fail) return false;
     if ((long long)(tc_time() - t0) > kF8TimeoutNs || ++it > (1ll << 28)) {
       *fail = 1;
@@ -45,9 +33,8 @@ static __device__ __noinline__ bool f8_wait_loop(uint64_t* m, uint32_t parity, v
   return true;
 }
 __device__ __forceinline__ bool f8_wait(uint64_t* m, uint32_t parity, volatile int* fail) {
-  return f8_try(m, parity) || f8_wait_loop(m, parity, fail);
+  return tc_mbar_try(m, parity) || f8_wait_loop(m, parity, fail);
 }
-
 // The address of something of this CTA's shared memory in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t f8_at(const void* p, uint32_t rank) {
   uint32_t r;
@@ -59,8 +46,10 @@ __device__ __forceinline__ uint32_t f8_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// An arrival at a barrier of either CTA. What it tells of is tensor memory, which tcgen05's own fences order; released for the
+// whole cluster it would wait for every load in flight (2000 cycles for each set of scales).
 __device__ __forceinline__ void f8_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void f8_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -106,15 +95,27 @@ __device__ __forceinline__ void f8_tmem_free(uint32_t at, uint32_t cols) {
   else
     tmem_free(at, cols);
 }
+// Issued by the lane that has `lead`; the whole warp runs the code around them, so that addresses and descriptors stay
+// in uniform registers.
+__device__ __forceinline__ uint32_t f8_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
 template <int CG>
-__device__ __forceinline__ void f8_commit(uint64_t* m) {  // with two CTAs: the barrier of both
+__device__ __forceinline__ void f8_commit(uint64_t* m, uint32_t lead) {  // with two CTAs: the barrier of both
   if (CG == 2)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(tc_smem(m)),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(tc_smem(m)),
+        "h"((uint16_t)3), "r"(lead)
         : "memory");
   else
-    tc_commit(m);
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc_smem(m)),
+        "r"(lead)
+        : "memory");
 }
 
 // K-major operand in the 128-byte swizzled layout: 8 rows 1024 bytes apart.
@@ -126,18 +127,19 @@ __device__ __forceinline__ uint32_t f8_idesc(int m, int n, int sf) {
   return ((uint32_t)sf << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
 }
 template <int CG>
-__device__ __forceinline__ void f8_tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
+__device__ __forceinline__ void f8_tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc,
+                                          uint32_t lead) {
   if (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(lead)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(lead)
         : "memory");
 }
 
