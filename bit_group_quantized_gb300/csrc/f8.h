@@ -37,6 +37,7 @@ cudaError_t launch_rmsnorm_f8(float* h, const void* delta, bool delta_f32, const
                               const bgq_f8matrix& m, uint16_t* a, cudaStream_t s);
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s);
+cudaError_t launch_f8_mid(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s);
 
 #ifdef __CUDACC__

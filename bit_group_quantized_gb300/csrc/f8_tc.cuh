@@ -161,14 +161,23 @@ __device__ __forceinline__ void f8_tmem_ld32(uint32_t at, float (&v)[32]) {
       : "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void f8_tmem_ld16(uint32_t at, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ void f8_tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The tensor map of codes [rows][cols], in tiles of 128 rows and 128 columns; zeros beyond both ends.
-inline bool f8_map(CUtensorMap* m, const uint8_t* q, int rows, int cols, int64_t stride) {
+// The tensor map of codes [rows][cols], in tiles of `box_rows` rows and 128 columns; zeros beyond both ends.
+inline bool f8_map(CUtensorMap* m, const uint8_t* q, int rows, int cols, int64_t stride, int box_rows = 128) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
-  const cuuint32_t box[2] = {128, 128}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
