@@ -33,66 +33,84 @@ __device__ __forceinline__ uint4 f8_ld_weights(const uint8_t* p) {
   return v;
 }
 
+// Blocks a warp loads before it multiplies them: what its registers hold.
 template <int NT, bool GATED>
-__global__ void __launch_bounds__(kFewThreads) k_f8_few(const F8Prod p) {
-  constexpr int R = GATED ? 2 : 1, T = 8 * NT;
+constexpr int few_ahead() { return NT == 1 ? (GATED ? 2 : 4) : NT == 2 ? (GATED ? 1 : 2) : 1; }
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(kFewThreads, 2) k_f8_few(const F8Prod p) {
+  constexpr int R = GATED ? 2 : 1, T = 8 * NT, U = few_ahead<NT, GATED>();
   __shared__ __align__(16) float part[kFewWarps][R][T][kFewPitch];
   __shared__ uint32_t most[T];
-  pdl_wait();
-  pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * T;
   const int blocks = f8_blocks(p.K);
+  // W into L2 while the kernel before this one ends (L2 holds whatever is written there in the meantime)
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    for (int i = tid; i < 16 * blocks; i += kFewThreads) {
+      const int row = n0 + (i & 15), col = (i >> 4) * kF8Block;
+      if (row < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w[r] + row * p.w_stride[r] + col));
+    }
+  pdl_wait();
+  pdl_trigger();
   float sum[R][NT][4] = {};
-  for (int kb = warp; kb < blocks; kb += kFewWarps) {
-    uint4 w[R][2][2], x[NT][2];  // [.][half of the block][row g or g + 8]
-    int ew[R], ex[NT][2];
+  for (int first = warp; first < blocks; first += kFewWarps * U) {
+    uint4 w[U][R][2][2], x[U][NT][2];  // [.][.][half of the block][row g or g + 8]
+    int ew[U][R], ex[U][NT][2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      ew[r] = n0 < p.N ? p.ws[r][(int64_t)(n0 / kF8Block) * p.ws_stride[r] + kb] : 0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = kb * kF8Block + half * 64 + t * 16, row = n0 + g + 8 * i;
-          w[r][half][i] = make_uint4(0, 0, 0, 0);
-          if (row < p.N && col < p.K) w[r][half][i] = f8_ld_weights(p.w[r] + row * p.w_stride[r] + col);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int col = kb * kF8Block + half * 64 + t * 16, row = m0 + 8 * j + g;
-        x[j][half] = make_uint4(0, 0, 0, 0);
-        if (row < p.M && col < p.K) x[j][half] = *reinterpret_cast<const uint4*>(p.x + row * p.x_stride + col);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = m0 + 8 * j + 2 * t + i;
-        ex[j][i] = row < p.M ? p.xs[row * p.xs_stride + kb] : 0;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int k = 0; k < U; ++k) {
+      const int kb = first + k * kFewWarps, c0 = kb * kF8Block + t * 16;  // past the last block nothing is loaded
+      const bool there = kb < blocks;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int col = c0 + half * 64, row = n0 + g + 8 * i;
+            w[k][r][half][i] = make_uint4(0, 0, 0, 0);
+            if (row < p.N && col < p.K) w[k][r][half][i] = f8_ld_weights(p.w[r] + row * p.w_stride[r] + col);
+          }
+        ew[k][r] = there && n0 < p.N ? p.ws[r][(int64_t)(n0 / kF8Block) * p.ws_stride[r] + kb] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint4 &w0 = w[r][half][0], &w1 = w[r][half][1], &b = x[j][half];
-          f8_mma(d, w0.x, w1.x, w0.y, w1.y, b.x, b.y);
-          f8_mma(d, w0.z, w1.z, w0.w, w1.w, b.z, b.w);
+          const int col = c0 + half * 64, row = m0 + 8 * j + g;
+          x[k][j][half] = make_uint4(0, 0, 0, 0);
+          if (row < p.M && col < p.K) x[k][j][half] = *reinterpret_cast<const uint4*>(p.x + row * p.x_stride + col);
         }
-        // times 2^(ew + ex - 254) in two halves, neither of which leaves fp32's range unless the result does
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int e = ew[r] + ex[j][i] - 254, lo = e >> 1;
-          const float f0 = f8_pow2(lo), f1 = f8_pow2(e - lo);
-          sum[r][j][i] = fmaf(d[i] * f0, f1, sum[r][j][i]);
-          sum[r][j][i + 2] = fmaf(d[i + 2] * f0, f1, sum[r][j][i + 2]);
+          const int row = m0 + 8 * j + 2 * t + i;
+          ex[k][j][i] = there && row < p.M ? p.xs[row * p.xs_stride + kb] : 0;
         }
       }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint4 &w0 = w[k][r][half][0], &w1 = w[k][r][half][1], &b = x[k][j][half];
+            f8_mma(d, w0.x, w1.x, w0.y, w1.y, b.x, b.y);
+            f8_mma(d, w0.z, w1.z, w0.w, w1.w, b.z, b.w);
+          }
+          // times 2^(ew + ex - 254) in two halves, neither of which leaves fp32's range unless the result does
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int e = ew[k][r] + ex[k][j][i] - 254, lo = e >> 1;
+            const float f0 = f8_pow2(lo), f1 = f8_pow2(e - lo);
+            sum[r][j][i] = fmaf(d[i] * f0, f1, sum[r][j][i]);
+            sum[r][j][i + 2] = fmaf(d[i + 2] * f0, f1, sum[r][j][i + 2]);
+          }
+        }
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)

@@ -7,6 +7,7 @@
 // sums lie side by side, so gated products find a block's largest magnitude in one step, and stores are whole lines.
 // The warps are specialised: one copies, one issues, four keep the scales in tensor memory (f8_tc.cuh); all eight write the
 // results.
+#include <algorithm>
 #include <mutex>
 #include <vector>
 
@@ -15,17 +16,18 @@
 namespace bgq {
 
 constexpr int kMidThreads = 256, kMidSets = 4;  // warp 0: copies, 1: instructions, 2: tensor memory, 4-7: scales; all: results
+constexpr int kMidRing = 224 * 1024;  // bytes
 constexpr int kMidMaxStages = 8, kMidMaxSplit = 8;
 
 struct MidShape {
   int rows;    // of x a tile: a multiple of 16, at most 256 (gated 128)
   int split;   // CTAs that share a tile's columns
-  int stages;
+  int stages;  // each of DEEP blocks
   uint32_t tmem;  // columns of tensor memory
 };
 
 template <bool GATED>
-__host__ __device__ inline int mid_stage(int rows) { return (GATED ? 2 : 1) * kF8Tile + rows * 128; }
+__host__ __device__ inline int mid_block(int rows) { return (GATED ? 2 : 1) * kF8Tile + rows * 128; }
 
 __device__ __forceinline__ float4 mid_ld_peer(uint32_t at) {
   float4 v;
@@ -33,7 +35,8 @@ __device__ __forceinline__ float4 mid_ld_peer(uint32_t at) {
   return v;
 }
 
-template <bool GATED>
+// DEEP: blocks a stage (one barrier for two saves the issuing warp a third of a block's time, where it is what bounds).
+template <bool GATED, int DEEP>
 __global__ void __launch_bounds__(kMidThreads, 1)
     k_f8_mid(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0,
              const __grid_constant__ CUtensorMap mw1, const F8Prod p, const MidShape sh) {
@@ -46,7 +49,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = blockIdx.x / sh.split, share = blockIdx.x - tile * sh.split, n0 = tile * 128, m0 = blockIdx.y * sh.rows;
   const int all = f8_blocks(p.K), b0 = all * share / sh.split, b1 = all * (share + 1) / sh.split;
-  const int stage_bytes = mid_stage<GATED>(sh.rows);
+  const int block_bytes = mid_block<GATED>(sh.rows), stage_bytes = DEEP * block_bytes;
+  constexpr int kAligned = ~(DEEP - 1);  // a stage's blocks end at a multiple of its depth, so that they lie in one word of scales
   const uint32_t scales = GATED ? 2 * sh.rows : sh.rows;  // columns behind the sums: W's 4 (and 4 of up), then x's 8
   if (tid == 0) {
     for (int i = 0; i < sh.stages; ++i) {
@@ -76,13 +80,16 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     if (lane == 0) {
       int s = 0;
       uint32_t par = 1;
-      for (int b = b0; b < b1; ++b) {
+      for (int b = b0; b < b1;) {
         if (!f8_wait(&empty[s], par, fail)) break;
         unsigned char* st = stages + s * stage_bytes;
-        f8_expect(&full[s], stage_bytes);
-        f8_load<1>(st, &mw0, b * 128, n0, tc_smem(&full[s]));
-        if (GATED) f8_load<1>(st + kF8Tile, &mw1, b * 128, n0, tc_smem(&full[s]));
-        f8_load<1>(st + (GATED ? 2 : 1) * kF8Tile, &mx, b * 128, m0, tc_smem(&full[s]));
+        const int end = min(b1, (b + DEEP) & kAligned);
+        f8_expect(&full[s], (end - b) * block_bytes);
+        for (; b < end; ++b, st += block_bytes) {
+          f8_load<1>(st, &mw0, b * 128, n0, tc_smem(&full[s]));
+          if (GATED) f8_load<1>(st + kF8Tile, &mw1, b * 128, n0, tc_smem(&full[s]));
+          f8_load<1>(st + (GATED ? 2 : 1) * kF8Tile, &mx, b * 128, m0, tc_smem(&full[s]));
+        }
         if (++s == sh.stages) {
           s = 0;
           par ^= 1;
@@ -94,25 +101,32 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     int s = 0, set = 0;
     uint32_t par = 0, sf_par = 0;
     bool ok = true;
-    for (int b = b0; b < b1; ++b) {
-      const int sf = b & 3;
-      if ((sf == 0 || b == b0) && !(ok = __all_sync(kFull, f8_wait(&sf_full[set], sf_par, fail)))) break;
+    for (int b = b0; b < b1;) {
+      if (((b & 3) == 0 || b == b0) && !(ok = __all_sync(kFull, f8_wait(&sf_full[set], sf_par, fail)))) break;
       if (!(ok = __all_sync(kFull, f8_wait(&full[s], par, fail)))) break;
       tc_fence_after();
       const uint32_t at = tc_smem(stages + s * stage_bytes), sc = tmem + scales + set * 16;
-      const uint64_t w = f8_desc(at), u = f8_desc(at + kF8Tile), x = f8_desc(at + (GATED ? 2 : 1) * kF8Tile);
-      const uint32_t idesc = f8_idesc(128, sh.rows, sf);
+      const int end = min(b1, (b + DEEP) & kAligned), first = b;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f8_tc_mma<1>(tmem, w + 2 * k, x + 2 * k, idesc, sc, sc + 8, b > b0 || k ? 1u : 0u, lead);
-        if (GATED) f8_tc_mma<1>(tmem + sh.rows, u + 2 * k, x + 2 * k, idesc, sc + 4, sc + 8, b > b0 || k ? 1u : 0u, lead);
+      for (int i = 0; i < DEEP; ++i) {
+        if (first + i >= end) break;
+        const uint64_t w = f8_desc(at + i * block_bytes), u = f8_desc(at + i * block_bytes + kF8Tile),
+                       x = f8_desc(at + i * block_bytes + (GATED ? 2 : 1) * kF8Tile);
+        const uint32_t idesc = f8_idesc(128, sh.rows, (first + i) & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t acc = first + i > b0 || k ? 1u : 0u;
+          f8_tc_mma<1>(tmem, w + 2 * k, x + 2 * k, idesc, sc, sc + 8, acc, lead);
+          if (GATED) f8_tc_mma<1>(tmem + sh.rows, u + 2 * k, x + 2 * k, idesc, sc + 4, sc + 8, acc, lead);
+        }
       }
+      b = end;
       f8_commit<1>(&empty[s], lead);
       if (++s == sh.stages) {
         s = 0;
         par ^= 1;
       }
-      if (sf == 3) {
+      if ((b & 3) == 0) {
         f8_commit<1>(&sf_free[set], lead);
         if (++set == kMidSets) {
           set = 0;
@@ -242,12 +256,15 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       if (lane == 0) p.hs[row * p.hs_stride + tile] = (uint8_t)byte;
     }
   }
+  __syncwarp();
+  // the peers' sums have been read, and this CTA's by them (nothing is written for another CTA, so nothing is released)
+  if (sh.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (*fail) {  // a wait has run out: copies in flight land before the CTA ends
     if (tid == 0) atomicExch(&p.ctrl->status, BGQ_ERR_TIMEOUT);
     for (const unsigned long long t0 = tc_time(); tc_time() - t0 < 5000000ull;) __nanosleep(10000);
   }
   __syncwarp();
-  if (sh.split > 1) f8_cluster_sync();  // peers have read this CTA's sums
+  if (sh.split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Clusters of n CTAs of a kernel that the device can hold at once (asked once for each device, kernel, shared memory and n).
@@ -284,20 +301,15 @@ static int mid_clusters(const void* kern, size_t smem, int n) {
   return count;
 }
 
-template <bool GATED>
-static cudaError_t mid(const F8Prod& p, cudaStream_t s) {
-  constexpr int kMost = GATED ? 128 : 256;
-  MidShape sh;
-  const int down = (p.M + kMost - 1) / kMost;
-  sh.rows = ((p.M + down - 1) / down + 15) / 16 * 16;
-  const int tiles = (p.N + 127) / 128, blocks = f8_blocks(p.K);
-  const int stage = mid_stage<GATED>(sh.rows);
-  sh.stages = 224 * 1024 / stage;
-  if (sh.stages > kMidMaxStages) sh.stages = kMidMaxStages;
+template <bool GATED, int DEEP>
+static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s) {
+  const int tiles = (p.N + 127) / 128, blocks = f8_blocks(p.K), stage = DEEP * mid_block<GATED>(sh.rows);
+  sh.stages = std::min(kMidRing / stage, kMidMaxStages);
   const uint32_t cols = (GATED ? 2 : 1) * sh.rows + 16 * kMidSets;
   for (sh.tmem = 32; sh.tmem < cols;) sh.tmem <<= 1;
-  const size_t smem = 1024 + (size_t)sh.stages * stage;
-  const void* kern = GATED ? (const void*)k_f8_mid<true> : (const void*)k_f8_mid<false>;
+  const int sums = (GATED ? 2 : 1) * sh.rows * 512;  // take the ring's place
+  const size_t smem = 1024 + std::max(sh.stages * stage, sums);
+  const void* kern = (const void*)k_f8_mid<GATED, DEEP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // the most CTAs a tile for which all are there at once, each with two blocks of columns at least
@@ -320,7 +332,16 @@ static cudaError_t mid(const F8Prod& p, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_f8_mid<GATED>, mx, mw[0], mw[1], p, sh);
+  return cudaLaunchKernelEx(&cfg, k_f8_mid<GATED, DEEP>, mx, mw[0], mw[1], p, sh);
+}
+
+template <bool GATED>
+static cudaError_t mid(const F8Prod& p, cudaStream_t s) {
+  constexpr int kMost = GATED ? 128 : 256;
+  MidShape sh = {};
+  const int down = (p.M + kMost - 1) / kMost;
+  sh.rows = ((p.M + down - 1) / down + 15) / 16 * 16;
+  return 6 * mid_block<GATED>(sh.rows) <= kMidRing ? mid_of<GATED, 2>(p, down, sh, s) : mid_of<GATED, 1>(p, down, sh, s);
 }
 
 cudaError_t launch_f8_mid(const F8Prod& p, bool gated, cudaStream_t s) { return gated ? mid<true>(p, s) : mid<false>(p, s); }
