@@ -20,7 +20,7 @@ constexpr int kManySets = 4;                 // sets of scales, 16 columns apart
 constexpr int kManyScales = 512 - 16 * kManySets;
 constexpr int kManyShared = 16 * kManySets;  // columns that both tiles' sums use
 constexpr int kManyBars = 2 * kManyStages + 2 * kManySets + 3;
-constexpr size_t kManySmem = 1024 + (size_t)kManyStages * kManyStage;
+constexpr size_t kManySmem = 1024 + (size_t)kManyStages * kManyStage + 4 * 2 * kF8Room;
 
 struct ManyWork {
   int tiles, down, group;  // tiles; tiles of x's rows; of which `group` are walked through beside each other
@@ -33,10 +33,14 @@ struct ManyWork {
   }
 };
 
+struct ManyOut {
+  CUtensorMap y, yf, h;  // those that are wanted
+};
+
 template <bool GATED>
 __global__ void __launch_bounds__(kManyThreads, 1)
     k_f8_many(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0,
-              const __grid_constant__ CUtensorMap mw1, const F8Prod p, const ManyWork work) {
+              const __grid_constant__ CUtensorMap mw1, const __grid_constant__ ManyOut out, const F8Prod p, const ManyWork work) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ uint64_t bars[kManyBars];
   __shared__ uint32_t s_tmem;
@@ -208,11 +212,51 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   } else if (warp >= 8) {
     const uint32_t freed = f8_at(acc_free, 0), lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    unsigned char* rooms = stages + kManyStages * kManyStage + (warp & 3) * 2 * kF8Room;
+    int room = 0;
+    auto store = [&](const uint4(&line)[8], const CUtensorMap* map, int col, int row) {
+      f8_store_rows(rooms + room * kF8Room, line, map, col, row);
+      room ^= 1;
+    };
+    // 64 columns of the warp's rows, of which a thread has a row. (A TMA store writes 16 bytes or nothing: where the columns end
+    // within that, the last pieces are written value by value.)
+    auto store64 = [&](const float(&lo)[32], const float(&hi)[32], int col, int row) {
+      uint4 line[8];
+      if (row >= p.M) return;
+      const int left = row + lane < p.M ? p.N - col : 0;
+      if (p.y && col < p.N) {
+        if (col + 64 <= p.N || p.N % 8 == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) line[i] = f8_bf16x8(i < 4 ? &lo[8 * i] : &hi[8 * i - 32]);
+          store(line, &out.y, col, row);
+        } else {
+          uint16_t* y = p.y + (int64_t)(row + lane) * p.y_stride + col;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < left) y[i] = f2bf(i < 32 ? lo[i & 31] : hi[i & 31]);
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int c = col + 32 * half;
+        if (!p.yf || c >= p.N) continue;
+        if (c + 32 <= p.N || p.N % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) line[i] = f8_fp32x4(half ? &hi[4 * i] : &lo[4 * i]);
+          store(line, &out.yf, c, row);
+        } else {
+          float* y = p.yf + (int64_t)(row + lane) * p.y_stride + c;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < left - 32 * half) y[i] = half ? hi[i] : lo[i];
+        }
+      }
+    };
     int t = 0;
     for (int i = pair; i < work.tiles; i += pairs, ++t) {
       int tm, tn;
       work.at(i, tm, tn);
-      const int row = tm * kManyRows + (int)rank * 128 + (warp & 3) * 32 + lane;
+      const int row = tm * kManyRows + (int)rank * 128 + (warp & 3) * 32;  // the warp's first
       if (!__all_sync(kFull, f8_wait(&acc_full[t & 1], (t >> 1) & 1, fail))) break;
       tc_fence_after();
       // the columns that the next tile wants come first: the last ones of the first sums, the first of the second
@@ -226,70 +270,70 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       };
       static_assert(kManyShared == 64, "two chunks of 32 columns");
       if (!GATED) {
-        auto column = [&](int c) { return 32 * (back ? kManyCols / 32 - 1 - c : c); };
         float v[2][32];
 #pragma unroll 1
-        for (int c = 0; c < kManyCols / 32; c += 2) {
-          f8_tmem_ld32(acc + column(c), v[0]);
-          f8_tmem_ld32(acc + column(c + 1), v[1]);
+        for (int c = 0; c < kManyCols / 64; ++c) {
+          const int col = 64 * (back ? kManyCols / 64 - 1 - c : c);
+          f8_tmem_ld32(acc + col, v[0]);
+          f8_tmem_ld32(acc + col + 32, v[1]);
           if (c == 0)
             drained();
           else
             f8_tmem_ld_wait();
-          if (row < p.M) {
-            f8_store32(p, row, tn * kManyCols + column(c), v[0]);
-            f8_store32(p, row, tn * kManyCols + column(c + 1), v[1]);
-          }
+          store64(v[0], v[1], tn * kManyCols + col, row);
         }
       } else {
-        auto column = [&](int c) { return 32 * (back ? 3 - c : c); };
-        float h[4][32];
+        // columns 64 c .. of the result, c = 1, 0 or 0, 1
+        float h[2][2][32];
         uint32_t top = 0;
-        auto join = [&](int c, float (&g)[32], const float (&u)[32]) {
+        auto column = [&](int c) { return 64 * (back ? 1 - c : c); };
+        auto join = [&](float (&g)[32], const float (&u)[32]) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             g[j] = f8_swiglu(g[j], u[j]);
             top = max(top, __float_as_uint(g[j]) & 0x7fffffffu);
           }
-          if (p.y && row < p.M) f8_store32(p, row, tn * 128 + column(c), g);
         };
         float u[2][32];
-        f8_tmem_ld32(acc + column(0), h[0]);
+        f8_tmem_ld32(acc + column(0), h[0][0]);
         f8_tmem_ld32(acc + 128 + column(0), u[0]);
-        f8_tmem_ld32(acc + column(1), h[1]);
-        f8_tmem_ld32(acc + 128 + column(1), u[1]);
+        f8_tmem_ld32(acc + column(0) + 32, h[0][1]);
+        f8_tmem_ld32(acc + 128 + column(0) + 32, u[1]);
         drained();
-        join(0, h[0], u[0]);
-        join(1, h[1], u[1]);
+        join(h[0][0], u[0]);
+        join(h[0][1], u[1]);
 #pragma unroll
-        for (int c = 2; c < 4; ++c) {
-          f8_tmem_ld32(acc + column(c), h[c]);
-          f8_tmem_ld32(acc + 128 + column(c), u[0]);
+        for (int c = 0; c < 2; ++c) {
+          f8_tmem_ld32(acc + column(1) + 32 * c, h[1][c]);
+          f8_tmem_ld32(acc + 128 + column(1) + 32 * c, u[0]);
           f8_tmem_ld_wait();
-          join(c, h[c], u[0]);
+          join(h[1][c], u[0]);
         }
-        if (p.h && row < p.M) {
+        if (p.y)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) store64(h[c][0], h[c][1], tn * 128 + column(c), row);
+        if (p.h) {
           const bool fine = f8_finite(top);
           const int byte = fine ? f8_scale_byte(top) : kF8One;
           const float inv = f8_inverse(byte);
-          p.hs[row * p.hs_stride + tn] = (uint8_t)byte;
+          if (row + lane < p.M) p.hs[(int64_t)(row + lane) * p.hs_stride + tn] = (uint8_t)byte;
+          uint4 line[8], codes[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int col = tn * 128 + column(c);
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint4 q = make_uint4(kF8Nan4, kF8Nan4, kF8Nan4, kF8Nan4);
-              const float* v = &h[c][j];
-              if (fine)
-                q = make_uint4(f8_codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), f8_codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
-                               f8_codes4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
-                               f8_codes4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
-              if (col + j < p.N) *reinterpret_cast<uint4*>(p.h + row * p.h_stride + col + j) = q;
-            }
+          for (int j = 0; j < 8; ++j) {
+            const float* v = &h[j >> 2][(j >> 1) & 1][16 * (j & 1)];
+            codes[j] = make_uint4(kF8Nan4, kF8Nan4, kF8Nan4, kF8Nan4);
+            if (fine)
+              codes[j] = make_uint4(f8_codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), f8_codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
+                                    f8_codes4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
+                                    f8_codes4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv));
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) line[j] = back ? codes[(j + 4) & 7] : codes[j];
+          if (row < p.M) store(line, &out.h, tn * 128, row);
         }
       }
     }
+    f8_stores_done();
   }
   __syncwarp();
   if (*fail && lane == 0)  // a wait has run out: the other CTA's end too
@@ -310,6 +354,10 @@ cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
   if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride)) return cudaErrorInvalidValue;
   for (int i = 0; i < 2; ++i)
     if (!f8_map(&mw[i], p.w[i], p.N, p.K, p.w_stride[i])) return cudaErrorInvalidValue;
+  ManyOut out = {};
+  if (p.y && !f8_out_map(&out.y, p.y, 2, p.M, p.N, p.y_stride)) return cudaErrorInvalidValue;
+  if (p.yf && !f8_out_map(&out.yf, p.yf, 4, p.M, p.N, p.y_stride)) return cudaErrorInvalidValue;
+  if (p.h && !f8_out_map(&out.h, p.h, 1, p.M, p.N, p.h_stride)) return cudaErrorInvalidValue;
   const int wide = gated ? 128 : kManyCols;
   ManyWork work;
   work.down = (p.M + kManyRows - 1) / kManyRows;
@@ -333,8 +381,8 @@ cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return gated ? cudaLaunchKernelEx(&cfg, k_f8_many<true>, mx, mw[0], mw[1], p, work)
-               : cudaLaunchKernelEx(&cfg, k_f8_many<false>, mx, mw[0], mw[0], p, work);
+  return gated ? cudaLaunchKernelEx(&cfg, k_f8_many<true>, mx, mw[0], mw[1], out, p, work)
+               : cudaLaunchKernelEx(&cfg, k_f8_many<false>, mx, mw[0], mw[0], out, p, work);
 }
 
 }  // namespace bgq

@@ -184,37 +184,44 @@ inline bool f8_map(CUtensorMap* m, const uint8_t* q, int rows, int cols, int64_t
 }
 
 // ------------------------------------------------------------------ results
-// 32 columns from col of a row of y and yf, those that there are.
-__device__ __forceinline__ void f8_store32(const F8Prod& p, int64_t row, int col, const float (&v)[32]) {
-  const int n = p.N - col;
-  if (n <= 0) return;
-  if (p.y) {
-    uint16_t* y = p.y + row * p.y_stride + col;
-    if (n >= 32) {
+// A warp writes 32 rows of 128 bytes at a time, a row a thread, by way of shared memory and a TMA store, which also cuts them where
+// the matrix ends: a thread's own 16-byte stores touch 32 lines at a time, and a tile's took 2 us.
+// The room is 4096 bytes, 1024-byte aligned, in the 128-byte swizzled layout; a warp has two.
+constexpr int kF8Room = 32 * 128;
+__device__ __forceinline__ void f8_store_rows(unsigned char* room, const uint4 (&line)[8], const CUtensorMap* map, int col, int row) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before the last has read this room
+  __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)f2bf(v[i + 2 * j]) | ((uint32_t)f2bf(v[i + 2 * j + 1]) << 16);
-        *reinterpret_cast<uint4*>(y + i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) y[i] = f2bf(v[i]);
-    }
+  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(room + lane * 128 + ((i ^ lane) & 7) * 16) = line[i];
+  tc_fence_proxy();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(tc_smem(room))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
-  if (p.yf) {
-    float* y = p.yf + row * p.y_stride + col;
-    if (n >= 32) {
+}
+__device__ __forceinline__ void f8_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ uint4 f8_bf16x8(const float* v) {
+  uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(y + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) y[i] = v[i];
-    }
-  }
+  for (int j = 0; j < 4; ++j) w[j] = (uint32_t)f2bf(v[2 * j]) | ((uint32_t)f2bf(v[2 * j + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 f8_fp32x4(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+// The tensor map of a result of `size` bytes a value, in pieces of 32 rows of 128 bytes.
+inline bool f8_out_map(CUtensorMap* m, void* y, int size, int rows, int cols, int64_t stride) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(stride * size)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, es[2] = {1, 1};
+  const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  return enc(m, type, 2, y, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace bgq
