@@ -262,11 +262,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // the columns that the next tile wants come first: the last ones of the first sums, the first of the second
       const bool back = (t & 1) == 0;
       const uint32_t acc = lanes + (back ? 0 : kManyCols - kManyShared);
-      auto drained = [&] {
+      auto drained = [&](float(&v)[2][32]) {
         f8_tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) f8_arrive_at(freed);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) asm volatile("" : "+f"(v[j >> 5][j & 31]));  // what is done with them comes behind the arrival
       };
       static_assert(kManyShared == 64, "two chunks of 32 columns");
       if (!GATED) {
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           f8_tmem_ld32(acc + col, v[0]);
           f8_tmem_ld32(acc + col + 32, v[1]);
           if (c == 0)
-            drained();
+            drained(v);
           else
             f8_tmem_ld_wait();
           store64(v[0], v[1], tn * kManyCols + col, row);
@@ -294,12 +296,22 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             top = max(top, __float_as_uint(g[j]) & 0x7fffffffu);
           }
         };
+        // the shared columns are the second half of up's sums, or the first of gate's
         float u[2][32];
-        f8_tmem_ld32(acc + column(0), h[0][0]);
-        f8_tmem_ld32(acc + 128 + column(0), u[0]);
-        f8_tmem_ld32(acc + column(0) + 32, h[0][1]);
-        f8_tmem_ld32(acc + 128 + column(0) + 32, u[1]);
-        drained();
+        if (back) {
+          f8_tmem_ld32(acc + 128 + 64, u[0]);
+          f8_tmem_ld32(acc + 128 + 96, u[1]);
+          drained(u);
+          f8_tmem_ld32(acc + 64, h[0][0]);
+          f8_tmem_ld32(acc + 96, h[0][1]);
+        } else {
+          f8_tmem_ld32(acc, h[0][0]);
+          f8_tmem_ld32(acc + 32, h[0][1]);
+          drained(h[0]);
+          f8_tmem_ld32(acc + 128, u[0]);
+          f8_tmem_ld32(acc + 128 + 32, u[1]);
+        }
+        f8_tmem_ld_wait();
         join(h[0][0], u[0]);
         join(h[0][1], u[1]);
 #pragma unroll
