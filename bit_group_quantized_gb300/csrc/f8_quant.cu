@@ -4,6 +4,8 @@
 //
 // Both are bound by memory: 3 bytes a value (2 read, 1 written), and 11 (h read and
 // written, a bf16 addend read, a code written; 2 more for the bf16 copy).
+#include <type_traits>
+
 #include "common.cuh"
 #include "f8.h"
 #include "kernels.h"
@@ -123,115 +125,168 @@ cudaError_t launch_f8_quantise(const uint16_t* x, int64_t x_stride, const bgq_f8
 }
 
 // ----------------------------------------------------------------------- norm
-// A CTA takes a row, a warp whole blocks of 128 columns of it (a lane 4 columns: loads and stores of a warp lie
-// side by side, and a block's largest magnitude is one warp-wide maximum). With V blocks a warp the row stays in registers
-// between the sum of squares and its use; with V = 0 (rows of more than 32 * 4 blocks) each thread reads back what it wrote.
-template <int V, bool F32>
-__global__ void __launch_bounds__(1024)
-    k_rmsnorm_f8(float* h, const void* delta, const uint16_t* rho, int d, float eps, uint8_t* q, int64_t q_stride,
-                 uint8_t* scale, int64_t s_stride, uint16_t* a) {
+// A warp has whole blocks of 128 columns of a row (a lane 4 columns: loads and stores of a warp lie side by side, and a block's
+// largest magnitude is one warp-wide maximum), V of them, which stay in registers between the sum of squares and its use. A
+// row is a warp's alone (ALONE: up to 8 blocks) or a CTA's. (CTAs that walk through the rows and load the next one meanwhile
+// need twice the registers: 8191 x 4096 took 75 us, 60 so.)
+template <bool F32>
+struct NormRaw {
+  float4 h;
+  typename std::conditional<F32, float4, uint2>::type delta;
+};
+
+struct NormArgs {
+  float* h;
+  const void* delta;
+  const uint16_t* rho;
+  uint8_t* q;
+  uint8_t* scale;
+  uint16_t* a;
+  int64_t q_stride, s_stride;
+  int rows, d;
+  float eps;
+};
+
+__device__ __forceinline__ float norm_squares(float4 v, float s) {
+  return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s))));
+}
+template <bool F32>
+__device__ __forceinline__ float4 norm_sum(const NormArgs& n, const NormRaw<F32>& r) {
+  float4 v = r.h;
+  if (n.delta) {
+    if constexpr (F32)
+      v = make_float4(v.x + r.delta.x, v.y + r.delta.y, v.z + r.delta.z, v.w + r.delta.w);
+    else
+      v = make_float4(v.x + bf16lo(r.delta.x), v.y + bf16hi(r.delta.x), v.z + bf16lo(r.delta.y), v.w + bf16hi(r.delta.y));
+  }
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ void norm_load(const NormArgs& n, int64_t row, int col, NormRaw<F32>& r) {
+  r.h = *reinterpret_cast<const float4*>(n.h + row * n.d + col);
+  if (n.delta) {
+    if constexpr (F32)
+      r.delta = *reinterpret_cast<const float4*>(static_cast<const float*>(n.delta) + row * n.d + col);
+    else
+      r.delta = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(n.delta) + row * n.d + col);
+  }
+}
+// One block of a row by one warp: w times r and rho, as codes and, where wanted, in bf16.
+__device__ __forceinline__ void norm_finish(const NormArgs& n, int64_t row, int b, float4 w, float r, uint2 rho) {
+  const int lane = threadIdx.x & 31, col = b * kF8Block + lane * 4;
+  w = make_float4(w.x * r, w.y * r, w.z * r, w.w * r);
+  if (n.rho) w = make_float4(w.x * bf16lo(rho.x), w.y * bf16hi(rho.x), w.z * bf16lo(rho.y), w.w * bf16hi(rho.y));
+  const uint32_t most = 0x7fffffffu;
+  const uint32_t m = max(max(__float_as_uint(w.x) & most, __float_as_uint(w.y) & most),
+                         max(__float_as_uint(w.z) & most, __float_as_uint(w.w) & most));
+  const uint32_t top = __reduce_max_sync(kFull, col < n.d ? m : 0u);
+  if (col >= n.d) return;
+  const bool fine = f8_finite(top);
+  const int byte = fine ? f8_scale_byte(top) : kF8One;
+  const float inv = f8_inverse(byte);
+  *reinterpret_cast<uint32_t*>(n.q + row * n.q_stride + col) = fine ? f8_codes4(w.x * inv, w.y * inv, w.z * inv, w.w * inv) : kF8Nan4;
+  if (lane == 0) n.scale[row * n.s_stride + b] = (uint8_t)byte;
+  if (n.a)
+    *reinterpret_cast<uint2*>(n.a + row * n.d + col) = make_uint2((uint32_t)f2bf(w.x) | ((uint32_t)f2bf(w.y) << 16),
+                                                                  (uint32_t)f2bf(w.z) | ((uint32_t)f2bf(w.w) << 16));
+}
+
+template <int V, bool F32, bool ALONE>
+__global__ void __launch_bounds__(ALONE ? 256 : 512, V == 8 && !ALONE ? 2 : 1) k_rmsnorm_f8(const NormArgs n) {
   __shared__ float part[32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, blocks = (d + kF8Block - 1) / kF8Block;
-  const size_t row = blockIdx.x;
-  float* hr = h + row * d;
-  auto load = [&](int col) {
-    float4 v = *reinterpret_cast<const float4*>(hr + col);
-    if (delta) {
-      float4 w;
-      if (F32) {
-        w = *reinterpret_cast<const float4*>(static_cast<const float*>(delta) + row * d + col);
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(delta) + row * d + col);
-        w = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-      }
-      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-    }
-    return v;
-  };
-  auto squares = [](float4 v, float s) { return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s)))); };
-  float4 v[V ? V : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, blocks = (n.d + kF8Block - 1) / kF8Block;
+  // the row's blocks that this warp has: first, first + step, ...
+  const int first = ALONE ? 0 : warp, step = ALONE ? 1 : warps;
+  const int64_t row = ALONE ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
+  if (ALONE && row >= n.rows) return;
+  float4 v[V];
   float ss = 0.f;
-  if (V) {
+  {
+    NormRaw<F32> raw[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int col = (warp + i * warps) * kF8Block + lane * 4;
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (col < d) v[i] = load(col);
+      const int col = (first + i * step) * kF8Block + lane * 4;
+      raw[i] = {};
+      if (col < n.d) norm_load<F32>(n, row, col, raw[i]);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int col = (warp + i * warps) * kF8Block + lane * 4;
-      ss = squares(v[i], ss);
-      if (delta && col < d) *reinterpret_cast<float4*>(hr + col) = v[i];
+      const int col = (first + i * step) * kF8Block + lane * 4;
+      v[i] = norm_sum<F32>(n, raw[i]);  // zeros past the row's end
+      ss = norm_squares(v[i], ss);
+      if (n.delta && col < n.d) *reinterpret_cast<float4*>(n.h + row * n.d + col) = v[i];
     }
-  } else {
-    for (int b = warp; b < blocks; b += warps) {
-      const int col = b * kF8Block + lane * 4;
-      if (col >= d) break;
-      const float4 w = load(col);
-      ss = squares(w, ss);
-      if (delta) *reinterpret_cast<float4*>(hr + col) = w;
-    }
+  }
+  ss = warp_sum(ss);
+  if (!ALONE) {
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int i = 0; i < warps; ++i) ss += part[i];
+  }
+  const float r = 1.f / sqrtf(ss / (float)n.d + n.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int b = first + i * step, col = b * kF8Block + lane * 4;
+    if (b < blocks) norm_finish(n, row, b, v[i], r, n.rho && col < n.d ? *reinterpret_cast<const uint2*>(n.rho + col) : make_uint2(0, 0));
+  }
+}
+
+// Rows of more than 128 blocks: each thread reads back what it wrote.
+template <bool F32>
+__global__ void __launch_bounds__(1024) k_rmsnorm_f8_long(const NormArgs n) {
+  __shared__ float part[32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, blocks = (n.d + kF8Block - 1) / kF8Block;
+  const int64_t row = blockIdx.x;
+  float ss = 0.f;
+#pragma unroll 4
+  for (int b = warp; b < blocks; b += warps) {
+    const int col = b * kF8Block + lane * 4;
+    if (col >= n.d) break;
+    NormRaw<F32> raw;
+    norm_load<F32>(n, row, col, raw);
+    const float4 v = norm_sum<F32>(n, raw);
+    ss = norm_squares(v, ss);
+    if (n.delta) *reinterpret_cast<float4*>(n.h + row * n.d + col) = v;
   }
   ss = warp_sum(ss);
   if (lane == 0) part[warp] = ss;
   __syncthreads();
-  float sum = 0.f;
-  for (int i = 0; i < warps; ++i) sum += part[i];
-  const float r = 1.f / sqrtf(sum / (float)d + eps);
-  auto finish = [&](int b, float4 w) {
+  ss = 0.f;
+  for (int i = 0; i < warps; ++i) ss += part[i];
+  const float r = 1.f / sqrtf(ss / (float)n.d + n.eps);
+  for (int b = warp; b < blocks; b += warps) {
     const int col = b * kF8Block + lane * 4;
-    w = make_float4(w.x * r, w.y * r, w.z * r, w.w * r);
-    if (rho && col < d) {
-      const uint2 u = *reinterpret_cast<const uint2*>(rho + col);
-      w = make_float4(w.x * bf16lo(u.x), w.y * bf16hi(u.x), w.z * bf16lo(u.y), w.w * bf16hi(u.y));
-    }
-    const uint32_t most = 0x7fffffffu;
-    const uint32_t m = max(max(__float_as_uint(w.x) & most, __float_as_uint(w.y) & most),
-                           max(__float_as_uint(w.z) & most, __float_as_uint(w.w) & most));
-    const uint32_t top = __reduce_max_sync(kFull, col < d ? m : 0u);
-    if (col >= d) return;
-    const bool fine = f8_finite(top);
-    const int byte = fine ? f8_scale_byte(top) : kF8One;
-    const float inv = f8_inverse(byte);
-    *reinterpret_cast<uint32_t*>(q + row * q_stride + col) =
-        fine ? f8_codes4(w.x * inv, w.y * inv, w.z * inv, w.w * inv) : kF8Nan4;
-    if (lane == 0) scale[row * s_stride + b] = (uint8_t)byte;
-    if (a)
-      *reinterpret_cast<uint2*>(a + row * d + col) = make_uint2((uint32_t)f2bf(w.x) | ((uint32_t)f2bf(w.y) << 16),
-                                                                (uint32_t)f2bf(w.z) | ((uint32_t)f2bf(w.w) << 16));
-  };
-  if (V) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (warp + i * warps < blocks) finish(warp + i * warps, v[i]);
-  } else {
-    for (int b = warp; b < blocks; b += warps) {
-      const int col = b * kF8Block + lane * 4;
-      finish(b, col < d ? *reinterpret_cast<const float4*>(hr + col) : make_float4(0.f, 0.f, 0.f, 0.f));
-    }
+    const bool there = col < n.d;
+    norm_finish(n, row, b, there ? *reinterpret_cast<const float4*>(n.h + row * n.d + col) : make_float4(0.f, 0.f, 0.f, 0.f), r,
+                there && n.rho ? *reinterpret_cast<const uint2*>(n.rho + col) : make_uint2(0, 0));
   }
 }
 
 template <bool F32>
-static cudaError_t norm_by_size(float* h, const void* delta, const uint16_t* rho, float eps, const bgq_f8matrix& m,
-                                uint16_t* a, cudaStream_t s) {
-  const int blocks = f8_blocks(m.cols);
-  auto go = [&](auto kern, int warps) {
-    return launch_overlapped(kern, m.rows, warps * 32, 0, s, h, delta, rho, m.cols, eps, m.q, m.q_stride, m.scale,
-                             m.scale_stride, a);
-  };
-  if (blocks <= 8) return go(k_rmsnorm_f8<1, F32>, blocks);
-  if (blocks <= 16) return go(k_rmsnorm_f8<2, F32>, (blocks + 1) / 2);
-  if (blocks <= 128) return go(k_rmsnorm_f8<4, F32>, (blocks + 3) / 4);
-  return go(k_rmsnorm_f8<0, F32>, 32);
+static cudaError_t norm_by_size(const NormArgs& n, cudaStream_t s) {
+  const int blocks = f8_blocks(n.d);
+  auto alone = [&](auto kern) { return launch_overlapped(kern, (n.rows + 7) / 8, 256, 0, s, n); };
+  auto rows = [&](auto kern, int warps) { return launch_overlapped(kern, n.rows, warps * 32, 0, s, n); };
+  if (blocks <= 1) return alone(k_rmsnorm_f8<1, F32, true>);
+  if (blocks <= 2) return alone(k_rmsnorm_f8<2, F32, true>);
+  if (blocks <= 4) return alone(k_rmsnorm_f8<4, F32, true>);
+  if (blocks <= 8) return alone(k_rmsnorm_f8<8, F32, true>);
+  // few rows: more warps each (512 x 4096: 5.4 us so, 6.5 with four blocks a warp; 8191 x 4096: 58 and 56)
+  if (blocks <= 32 && n.rows <= 4 * num_sms()) return rows(k_rmsnorm_f8<2, F32, false>, (blocks + 1) / 2);
+  if (blocks <= 64) return rows(k_rmsnorm_f8<4, F32, false>, (blocks + 3) / 4);
+  if (blocks <= 128) return rows(k_rmsnorm_f8<8, F32, false>, (blocks + 7) / 8);
+  return launch_overlapped(k_rmsnorm_f8_long<F32>, n.rows, 1024, 0, s, n);
 }
 
 cudaError_t launch_rmsnorm_f8(float* h, const void* delta, bool delta_f32, const uint16_t* rho, float eps,
                               const bgq_f8matrix& m, uint16_t* a, cudaStream_t s) {
-  return delta_f32 ? norm_by_size<true>(h, delta, rho, eps, m, a, s) : norm_by_size<false>(h, delta, rho, eps, m, a, s);
+  const NormArgs n = {h, delta, rho, m.q, m.scale, a, m.q_stride, m.scale_stride, m.rows, m.cols, eps};
+  return delta_f32 ? norm_by_size<true>(n, s) : norm_by_size<false>(n, s);
 }
 
 }  // namespace bgq
