@@ -688,27 +688,41 @@ class F8Matrix:
 
 def _f8_like(m, rows: int, cols: int, block_rows: int | None, index: int, what: str):
     """m is an F8Matrix of this shape on CUDA device `index`."""
-    _need(isinstance(m, F8Matrix) and m.index == index and (m.rows, m.cols) == (rows, cols)
+    _need(isinstance(m, F8Matrix) and m.index == index and m.rows == rows and m.cols == cols
           and (block_rows is None or m.block_rows == block_rows), what)
-    return m
 
 
-def _rows_of(t, dtype, rows: int, cols: int, index: int, what: str) -> int:
-    """t is [rows][cols] of this type on CUDA device `index`, columns side by side; returns the values between rows."""
-    _on(t, dtype, index, 2, what)
-    _need(t.shape == (rows, cols) and (cols == 1 or t.stride(1) == 1), what)
-    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+def _plain(t, dtype, shape, index: int, what: str):
+    """t is a contiguous tensor of this type and shape on CUDA device `index`; returns its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            return t.data_ptr()
+    except (AttributeError, TypeError, RuntimeError):
+        pass
+    raise BGQError(ERR_INVALID_ARG, what)
+
+
+def _rows_of(t, dtype, index, what: str):
+    """t is [rows][cols] of this type on CUDA device `index` (None: any), columns side by side; returns its rows and cols and
+    the values between rows (of a single row, whose stride torch leaves open, its width rounded up)."""
+    try:
+        rows, cols = t.shape
+        s, one = t.stride()
+        dev = t.get_device()
+        if t.dtype is dtype and (one == 1 or cols == 1) and (dev == index if index is not None else dev >= 0):
+            return rows, cols, s if rows > 1 else -(-cols // 8) * 8
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        pass
+    raise BGQError(ERR_INVALID_ARG, what)
 
 
 def bgq_f8_quantise(x: torch.Tensor, out: F8Matrix | None = None, block_rows: int = 1, stream=None) -> F8Matrix:
     """bgq_f8_quantise: x bf16 [rows][cols] (rows may lie further apart) as an F8Matrix."""
-    what = "bgq_f8_quantise: x must be a CUDA bf16 tensor [rows][cols], columns side by side"
-    _on(x, _BF16, None, 2, what)
-    dev, (rows, cols) = x.get_device(), x.shape
+    rows, cols, sx = _rows_of(x, _BF16, None, "bgq_f8_quantise: x must be a CUDA bf16 tensor [rows][cols], columns side by side")
+    dev = x.get_device()
     if stream is not None or _device() != dev:
         with _there(dev, stream):
             return bgq_f8_quantise(x, out, block_rows)
-    sx = _rows_of(x, _BF16, rows, cols, dev, what)
     if out is None:
         out = F8Matrix.empty(rows, cols, block_rows, x.device)
     _f8_like(out, rows, cols, None, dev, "bgq_f8_quantise: out must be an F8Matrix of x's shape beside it")
@@ -724,29 +738,24 @@ def bgq_rmsnorm_f8(h: torch.Tensor, rho: torch.Tensor | None, eps: float, delta:
     """bgq_rmsnorm_f8: h fp32 [batch][d] += delta (fp32 or bf16, nullable), in place -> (its RMSNorm times rho as an
     F8Matrix, the same as bf16 `a` when given or wanted)."""
     what = "bgq_rmsnorm_f8: h must be a CUDA fp32 tensor [batch][d], contiguous"
-    _on(h, torch.float32, None, 2, what)
-    dev, (B, d) = h.get_device(), h.shape
+    B, d, _ = _rows_of(h, torch.float32, None, what)
+    dev, shape = h.get_device(), h.shape
     if stream is not None or _device() != dev:
         with _there(dev, stream):
             return bgq_rmsnorm_f8(h, rho, eps, delta, out, a, want_a)
     _need(h.is_contiguous(), what)
-    if delta is not None:
-        _on(delta, torch.float32 if delta.dtype is torch.float32 else _BF16, dev, 2, "bgq_rmsnorm_f8: delta must be fp32 or bf16 like h")
-        _need(delta.shape == h.shape and delta.is_contiguous(), "bgq_rmsnorm_f8: delta must be [batch][d], contiguous")
-    if rho is not None:
-        _on(rho, _BF16, dev, 1, "bgq_rmsnorm_f8: rho must be bf16 [d] beside h")
-        _need(rho.shape[0] == d and rho.is_contiguous(), "bgq_rmsnorm_f8: rho must be bf16 [d], contiguous")
+    f32 = getattr(delta, "dtype", None) is torch.float32
+    pd = None if delta is None else _plain(delta, torch.float32 if f32 else _BF16, shape, dev,
+                                           "bgq_rmsnorm_f8: delta must be fp32 or bf16 [batch][d] beside h, contiguous")
+    pr = None if rho is None else _plain(rho, _BF16, (d,), dev, "bgq_rmsnorm_f8: rho must be bf16 [d] beside h, contiguous")
     if out is None:
         out = F8Matrix.empty(B, d, 1, h.device)
     _f8_like(out, B, d, 1, dev, "bgq_rmsnorm_f8: out must be an F8Matrix of h's shape beside it, with a scale for each row")
     if a is None and want_a:
         a = alloc((B, d), _BF16, h.device)
-    if a is not None:
-        _on(a, _BF16, dev, 2, "bgq_rmsnorm_f8: a must be bf16 like h")
-        _need(a.shape == h.shape and a.is_contiguous(), "bgq_rmsnorm_f8: a must be [batch][d], contiguous")
+    pa = None if a is None else _plain(a, _BF16, shape, dev, "bgq_rmsnorm_f8: a must be bf16 [batch][d] beside h, contiguous")
     if B:
-        r = load().bgq_rmsnorm_f8(h.data_ptr(), _ptr(delta), delta is not None and delta.dtype is torch.float32, _ptr(rho), B, d,
-                                  eps, out.ref, _ptr(a), _raw_stream(dev))
+        r = load().bgq_rmsnorm_f8(h.data_ptr(), pd, f32, pr, B, d, eps, out.ref, pa, _raw_stream(dev))
         if r:
             raise BGQError(r, "bgq_rmsnorm_f8")
     return out, a
@@ -763,45 +772,46 @@ def _f8_workspace(W: F8Matrix, x: F8Matrix, ws):
     return ws
 
 
+def _f8_out(t, dtype, rows: int, cols: int, index: int, what: str):
+    """An output's address (one without rows has none, and any aligned one does) and the values between its rows."""
+    if t is None:
+        return None, 0
+    r, c, s = _rows_of(t, dtype, index, what)
+    _need(r == rows and c == cols, what)
+    return t.data_ptr() if rows else 256, s
+
+
 def bgq_f8_gemm(W: F8Matrix, x: F8Matrix, out: torch.Tensor | None = None, out_f32: torch.Tensor | None = None,
                 want_out: bool = True, want_f32: bool = False, ws: torch.Tensor | None = None, stream=None):
     """bgq_f8_gemm: y = x W^T, W with block_rows 128 -> (y bf16, y fp32), [x.rows][W.rows] each, rows a multiple of 8
     values apart (both alike). Buffers that are given are filled; where none is, the bf16 one is made (unless
     want_out is False) and the fp32 one where wanted."""
-    what = "bgq_f8_gemm: W and x must be F8Matrix on one device, of the same cols, W with block_rows 128"
-    _need(isinstance(W, F8Matrix) and isinstance(x, F8Matrix) and W.index == x.index, what)
+    _need(isinstance(W, F8Matrix) and isinstance(x, F8Matrix) and W.index == x.index,
+          "bgq_f8_gemm: W and x must be F8Matrix on one device")
     dev, M, N = x.index, x.rows, W.rows
     if stream is not None or _device() != dev:
         with _there(dev, stream):
             return bgq_f8_gemm(W, x, out, out_f32, want_out, want_f32, ws)
-    wide = -(-N // 8) * 8
     if out is None and want_out and out_f32 is None:
-        out = alloc((M, wide), _BF16, x.device)[:, :N]
+        out = alloc((M, -(-N // 8) * 8), _BF16, x.device)[:, :N]
     if out_f32 is None and want_f32:
-        out_f32 = alloc((M, wide), torch.float32, x.device)[:, :N]
-    so = None if out is None else _rows_of(out, _BF16, M, N, dev, "bgq_f8_gemm: out must be bf16 [x.rows][W.rows], columns side by side")
-    sf = None if out_f32 is None else _rows_of(out_f32, torch.float32, M, N, dev,
-                                               "bgq_f8_gemm: out_f32 must be fp32 [x.rows][W.rows], columns side by side")
-    _need(so is None or sf is None or so == sf, "bgq_f8_gemm: out and out_f32 must have their rows equally far apart")
+        out_f32 = alloc((M, -(-N // 8) * 8), torch.float32, x.device)[:, :N]
+    py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_gemm: out must be bf16 [x.rows][W.rows] beside x, columns side by side")
+    pf, sf = _f8_out(out_f32, torch.float32, M, N, dev, "bgq_f8_gemm: out_f32 must be fp32 [x.rows][W.rows] beside x, columns side by side")
+    _need(py is None or pf is None or so == sf, "bgq_f8_gemm: out and out_f32 must have their rows equally far apart")
     ws = _f8_workspace(W, x, ws)
-    r = load().bgq_f8_gemm(W.ref, x.ref, _out_ptr(out, M), _out_ptr(out_f32, M), sf if so is None else so or 0, ws.data_ptr(), ws.nbytes,
-                           _raw_stream(dev))
+    r = load().bgq_f8_gemm(W.ref, x.ref, py, pf, so or sf, ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     if r:
         raise BGQError(r, "bgq_f8_gemm")
     return out, out_f32
-
-
-def _out_ptr(t, rows: int):
-    """An output's address; one without rows has none, and any aligned one does."""
-    return None if t is None else t.data_ptr() if rows else 256
 
 
 def bgq_f8_swiglu(gate: F8Matrix, up: F8Matrix, x: F8Matrix, h: F8Matrix | None = None, out: torch.Tensor | None = None,
                   want_h: bool = True, want_out: bool = False, ws: torch.Tensor | None = None, stream=None):
     """bgq_f8_swiglu: silu(x gate^T) * (x up^T) -> (h as an F8Matrix, out bf16), [x.rows][gate.rows]. Buffers that
     are given are filled; where none is, h is made (unless want_h is False) and out where wanted."""
-    what = "bgq_f8_swiglu: gate, up and x must be F8Matrix on one device"
-    _need(all(isinstance(m, F8Matrix) for m in (gate, up, x)) and gate.index == up.index == x.index, what)
+    _need(isinstance(gate, F8Matrix) and isinstance(up, F8Matrix) and isinstance(x, F8Matrix) and gate.index == up.index == x.index,
+          "bgq_f8_swiglu: gate, up and x must be F8Matrix on one device")
     dev, M, N = x.index, x.rows, gate.rows
     if stream is not None or _device() != dev:
         with _there(dev, stream):
@@ -812,10 +822,9 @@ def bgq_f8_swiglu(gate: F8Matrix, up: F8Matrix, x: F8Matrix, h: F8Matrix | None 
         out = alloc((M, N), _BF16, x.device)
     if h is not None:
         _f8_like(h, M, N, 1, dev, "bgq_f8_swiglu: h must be an F8Matrix [x.rows][gate.rows] beside x, with a scale for each row")
-    so = 0 if out is None else _rows_of(out, _BF16, M, N, dev, "bgq_f8_swiglu: out must be bf16 [x.rows][gate.rows], columns side by side")
+    py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_swiglu: out must be bf16 [x.rows][gate.rows] beside x, columns side by side")
     ws = _f8_workspace(gate, x, ws)
-    r = load().bgq_f8_swiglu(gate.ref, up.ref, x.ref, None if h is None else h.ref, _out_ptr(out, M), so, ws.data_ptr(), ws.nbytes,
-                             _raw_stream(dev))
+    r = load().bgq_f8_swiglu(gate.ref, up.ref, x.ref, None if h is None else h.ref, py, so, ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     if r:
         raise BGQError(r, "bgq_f8_swiglu")
     return h, out
