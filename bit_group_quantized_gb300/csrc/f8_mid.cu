@@ -69,6 +69,24 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     if (GATED) f8_map_ahead(&mw1);
   }
   pdl_wait();
+  // Scales: a lane has those of x's rows l, 32 + l, ...; W's are the same for its whole tile. Words of four groups of blocks at a
+  // time, the first while tensor memory is taken.
+  const int c0 = b0 >> 2, c1 = (b1 + 3) >> 2;
+  uint32_t xs[4][8], wsc[4][2];
+  auto load = [&](int c) {
+    const uint8_t* x = p.xs + (int64_t)(m0 + lane) * p.xs_stride + 4 * c;
+    const uint8_t *w0 = p.ws[0] + tile * p.ws_stride[0] + 4 * c, *w1 = p.ws[1] + tile * p.ws_stride[1] + 4 * c;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const bool there = c + g < c1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        xs[g][j] = there && 32 * j < sh.rows && m0 + lane + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * g) : 0u;
+      wsc[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
+      wsc[g][1] = there && GATED ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
+    }
+  };
+  if (warp >= 4) load(c0);
   if (warp == 2) tmem_alloc(&s_tmem, sh.tmem);
   tc_fence_before();
   __syncthreads();
@@ -136,35 +154,21 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     }
     if (ok) f8_commit<1>(&done, lead);
   } else if (warp >= 4) {
-    // a lane has the scales of x's rows l, 32 + l, ...; W's are the same for its whole tile. Words of four groups of blocks at a time.
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + scales;
-    const int g1 = (b1 + 3) >> 2;
-    const uint8_t* x = p.xs + (int64_t)(m0 + lane) * p.xs_stride;
-    const uint8_t *w0 = p.ws[0] + tile * p.ws_stride[0], *w1 = p.ws[1] + tile * p.ws_stride[1];
     int set = 0;
     uint32_t par = 1;
     bool ok = true;
-    for (int c = b0 >> 2; ok && c < g1; c += 4) {
-      uint32_t v[4][8], w[4][2];
+    for (int c = c0; ok && c < c1; c += 4) {
+      if (c > c0) load(c);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const bool there = c + g < g1;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[g][j] = there && 32 * j < sh.rows && m0 + lane + 32 * j < p.M
-                        ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * (c + g)) : 0u;
-        w[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * (c + g)) : 0u;
-        w[g][1] = there && GATED ? *reinterpret_cast<const uint32_t*>(w1 + 4 * (c + g)) : 0u;
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (!ok || c + g >= g1) continue;
+        if (!ok || c + g >= c1) continue;
         if (!(ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail)))) continue;
         tc_fence_after();
-        f8_tmem_st4(at + set * 16, w[g][0], w[g][0], w[g][0], w[g][0]);
-        if (GATED) f8_tmem_st4(at + set * 16 + 4, w[g][1], w[g][1], w[g][1], w[g][1]);
-        f8_tmem_st4(at + set * 16 + 8, v[g][0], v[g][1], v[g][2], v[g][3]);
-        if (sh.rows > 128) f8_tmem_st4(at + set * 16 + 12, v[g][4], v[g][5], v[g][6], v[g][7]);
+        f8_tmem_st4(at + set * 16, wsc[g][0], wsc[g][0], wsc[g][0], wsc[g][0]);
+        if (GATED) f8_tmem_st4(at + set * 16 + 4, wsc[g][1], wsc[g][1], wsc[g][1], wsc[g][1]);
+        f8_tmem_st4(at + set * 16 + 8, xs[g][0], xs[g][1], xs[g][2], xs[g][3]);
+        if (sh.rows > 128) f8_tmem_st4(at + set * 16 + 12, xs[g][4], xs[g][5], xs[g][6], xs[g][7]);
         f8_tmem_st_wait();
         tc_fence_before();
         __syncwarp();
