@@ -70,6 +70,37 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     f8_map_ahead(rank ? &mw1 : &mw0);
   }
   pdl_wait();  // tensor memory, too, is taken only once earlier kernels have given theirs back
+  // Scales: a lane has those of x's rows l, 32 + l, ...; W's are the same for a whole block of 128 rows.
+  // A chunk: the words of four groups of blocks. They are loaded a chunk ahead, of this tile or the next (loaded a group
+  // or two ahead, they held the instructions up: 8191 x 12288 x 4096 took 298 us, 267 so).
+  const int wbs = f8_blocks(p.N);
+  struct Chunk {
+    uint32_t x[4][4], w[4][2];
+  } cur = {}, next = {};
+  int li = pair, lg = 0;  // tile and first group of the next chunk
+  auto load = [&](Chunk& v) {
+    if (li >= work.tiles) return;
+    int tm, tn;
+    work.at(li, tm, tn);
+    const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn;
+    const uint8_t* x = p.xs + (int64_t)m0 * p.xs_stride + 4 * lg;
+    const uint8_t* w0 = p.ws[0] + wb * p.ws_stride[0] + 4 * lg;
+    const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] + 4 * lg : wb + 1 < wbs ? w0 + p.ws_stride[0] : w0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const bool there = lg + g < groups;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v.x[g][j] = there && m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * g) : 0u;
+      v.w[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
+      v.w[g][1] = there ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
+    }
+    if ((lg += 4) >= groups) {
+      lg = 0;
+      li += pairs;
+    }
+  };
+  if (warp >= 4 && warp < 8) load(cur);
   if (warp == 2) f8_tmem_alloc<2>(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -147,39 +178,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     }
   } else if (warp >= 4 && warp < 8) {
-    // a lane has the scales of x's rows l, 32 + l, ...; W's are the same for a whole block of 128 rows
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21) + kManyScales, ready = f8_at(&sf_full[0], 0);
-    const int wbs = f8_blocks(p.N);
-    // A chunk: the words of four groups of blocks. They are loaded a chunk ahead, of this tile or the next (loaded a group
-    // or two ahead, they held the instructions up: 8191 x 12288 x 4096 took 298 us, 267 so).
-    struct Chunk {
-      uint32_t x[4][4], w[4][2];
-    } cur = {}, next = {};
-    int li = pair, lg = 0, set = 0;  // tile and first group of the next chunk
+    int set = 0;
     uint32_t par = 1;
-    auto load = [&](Chunk& v) {
-      if (li >= work.tiles) return;
-      int tm, tn;
-      work.at(li, tm, tn);
-      const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn;
-      const uint8_t* x = p.xs + (int64_t)m0 * p.xs_stride + 4 * lg;
-      const uint8_t* w0 = p.ws[0] + wb * p.ws_stride[0] + 4 * lg;
-      const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] + 4 * lg : wb + 1 < wbs ? w0 + p.ws_stride[0] : w0;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const bool there = lg + g < groups;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v.x[g][j] = there && m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * g) : 0u;
-        v.w[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
-        v.w[g][1] = there ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
-      }
-      if ((lg += 4) >= groups) {
-        lg = 0;
-        li += pairs;
-      }
-    };
-    load(cur);
     bool ok = true;
     for (int i = pair; ok && i < work.tiles; i += pairs)
       for (int g0 = 0; ok && g0 < groups; g0 += 4) {

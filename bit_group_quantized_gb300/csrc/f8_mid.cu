@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     tc_mbar_init(&done);
     s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc_fence_proxy();
     f8_map_ahead(&mx);
     f8_map_ahead(&mw0);
     if (GATED) f8_map_ahead(&mw1);
@@ -87,6 +88,26 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     }
   };
   if (warp >= 4) load(c0);
+  // Copies, by the thread that set the barriers up: the ring is filled once before the others know of it.
+  int next = b0, stage = 0;
+  uint32_t par = 1;
+  auto copy = [&] {
+    unsigned char* st = stages + stage * stage_bytes;
+    uint64_t* bar = &full[stage];
+    const int end = min(b1, (next + DEEP) & kAligned);
+    f8_expect(bar, (end - next) * block_bytes);
+    for (; next < end; ++next, st += block_bytes) {
+      f8_load<1>(st, &mw0, next * 128, n0, tc_smem(bar));
+      if (GATED) f8_load<1>(st + kF8Tile, &mw1, next * 128, n0, tc_smem(bar));
+      f8_load<1>(st + (GATED ? 2 : 1) * kF8Tile, &mx, next * 128, m0, tc_smem(bar));
+    }
+    if (++stage == sh.stages) {
+      stage = 0;
+      par ^= 1;
+    }
+  };
+  if (tid == 0)
+    for (int i = 0; i < sh.stages && next < b1; ++i) copy();
   if (warp == 2) tmem_alloc(&s_tmem, sh.tmem);
   tc_fence_before();
   __syncthreads();
@@ -95,25 +116,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t par = 1;
-      for (int b = b0; b < b1;) {
-        if (!f8_wait(&empty[s], par, fail)) break;
-        unsigned char* st = stages + s * stage_bytes;
-        const int end = min(b1, (b + DEEP) & kAligned);
-        f8_expect(&full[s], (end - b) * block_bytes);
-        for (; b < end; ++b, st += block_bytes) {
-          f8_load<1>(st, &mw0, b * 128, n0, tc_smem(&full[s]));
-          if (GATED) f8_load<1>(st + kF8Tile, &mw1, b * 128, n0, tc_smem(&full[s]));
-          f8_load<1>(st + (GATED ? 2 : 1) * kF8Tile, &mx, b * 128, m0, tc_smem(&full[s]));
-        }
-        if (++s == sh.stages) {
-          s = 0;
-          par ^= 1;
-        }
-      }
-    }
+    while (lane == 0 && next < b1 && f8_wait(&empty[stage], par, fail)) copy();
   } else if (warp == 1) {
     const uint32_t lead = f8_elect();
     int s = 0, set = 0;
