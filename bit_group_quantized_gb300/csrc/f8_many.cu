@@ -378,8 +378,9 @@ cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
   work.tiles = work.down * work.across;
   work.group = work.down < 8 ? work.down : 8;
   const int pairs = num_sms() / 2;
+  static std::atomic<uint64_t> known[2];
   const void* kern = gated ? (const void*)k_f8_many<true> : (const void*)k_f8_many<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kManySmem);
+  const cudaError_t e = f8_room(kern, (int)kManySmem, known[gated]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (work.tiles < pairs ? work.tiles : pairs));

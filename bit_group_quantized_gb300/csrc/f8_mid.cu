@@ -317,7 +317,9 @@ static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s
   const int sums = (GATED ? 2 : 1) * sh.rows * 512;  // take the ring's place
   const size_t smem = 1024 + std::max(sh.stages * stage, sums);
   const void* kern = (const void*)k_f8_mid<GATED, DEEP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static_assert(kMidRing >= 2 * 128 * 512, "the ring holds the most sums");
+  static std::atomic<uint64_t> known;
+  const cudaError_t e = f8_room(kern, 1024 + kMidRing, known);
   if (e != cudaSuccess) return e;
   // the most CTAs a tile for which all are there at once, each with two blocks of columns at least
   for (sh.split = kMidMaxSplit; sh.split > 1; sh.split >>= 1)

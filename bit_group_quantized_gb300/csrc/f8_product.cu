@@ -46,29 +46,30 @@ static double few_us(const F8Prod& p, bool gated, double weights) {
 }
 
 // A batch: blocks of 128 columns one after the other in a CTA, or W's bytes, and the shares' sums.
-static double mid_us(const F8Prod& p, bool gated, double weights) {
+static double mid_us(const F8Prod& p, bool gated, double weights, int sms) {
   const int blocks = f8_blocks(p.K), down = ceil_div(p.M, gated ? 128 : 256), tiles = ceil_div(p.N, 128) * down;
   const int rows = ceil_div(ceil_div(p.M, down), 16) * 16;
   int split = 8;
-  while (split > 1 && (2 * split > blocks || tiles * split > num_sms() * 7 / 8)) split >>= 1;
+  while (split > 1 && (2 * split > blocks || tiles * split > sms * 7 / 8)) split >>= 1;
   const double block = gated ? 0.46 + 0.0021 * rows : 0.22 + 0.00105 * rows;
-  const double waves = ceil_div(tiles * split, num_sms());
+  const double waves = ceil_div(tiles * split, sms);
   return 2.9 + std::max(waves * ceil_div(blocks, split) * block, weights / 6.5) + rows * (split == 1 ? 0.006 : gated ? 0.029 : 0.0137);
 }
 
 // Many rows: a pair of CTAs' tiles one after the other, or W's bytes.
-static double many_us(const F8Prod& p, bool gated, double weights) {
+static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
   const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : 256);
-  return 6.7 + std::max(0.28 * f8_blocks(p.K) * ceil_div(tiles, std::max(1, num_sms() / 2)), weights / 4.4);
+  return 6.7 + std::max(0.28 * f8_blocks(p.K) * ceil_div(tiles, std::max(1, sms / 2)), weights / 4.4);
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
   if (p.K < kF8Block) return launch_f8_few(p, gated, s);  // the tensor maps' boxes are a block of columns wide
   if (p.M > 2048) return launch_f8_many(p, gated, s);
   const double weights = (double)p.N * p.K * (gated ? 2e-6 : 1e-6);
-  const double mid = mid_us(p, gated, weights);
+  const int sms = num_sms();
+  const double mid = mid_us(p, gated, weights, sms);
   if (p.M <= 32 && few_us(p, gated, weights) <= mid) return launch_f8_few(p, gated, s);
-  return mid < many_us(p, gated, weights) ? launch_f8_mid(p, gated, s) : launch_f8_many(p, gated, s);
+  return mid < many_us(p, gated, weights, sms) ? launch_f8_mid(p, gated, s) : launch_f8_many(p, gated, s);
 }
 
 }  // namespace bgq

@@ -8,6 +8,8 @@
 // steps name the same one, and a word serves four blocks: 512 columns.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "f8.h"
 #include "kernels.h"
@@ -171,6 +173,16 @@ __device__ __forceinline__ void f8_tmem_ld16(uint32_t at, float (&v)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void f8_tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Lets a kernel have `most` bytes of dynamic shared memory: asked for once a device (`known`: a bit for each).
+inline cudaError_t f8_room(const void* kern, int most, std::atomic<uint64_t>& known) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && known.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && dev < 64) known.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // The tensor map of codes [rows][cols], in tiles of `box_rows` rows and 128 columns; zeros beyond both ends.
 inline bool f8_map(CUtensorMap* m, const uint8_t* q, int rows, int cols, int64_t stride, int box_rows = 128) {

@@ -737,14 +737,19 @@ def bgq_rmsnorm_f8(h: torch.Tensor, rho: torch.Tensor | None, eps: float, delta:
                    out: F8Matrix | None = None, a: torch.Tensor | None = None, want_a: bool = False, stream=None):
     """bgq_rmsnorm_f8: h fp32 [batch][d] += delta (fp32 or bf16, nullable), in place -> (its RMSNorm times rho as an
     F8Matrix, the same as bf16 `a` when given or wanted)."""
-    what = "bgq_rmsnorm_f8: h must be a CUDA fp32 tensor [batch][d], contiguous"
-    B, d, _ = _rows_of(h, torch.float32, None, what)
-    dev, shape = h.get_device(), h.shape
+    try:
+        shape = h.shape
+        B, d = shape
+        dev = h.get_device()
+        ok = h.dtype is torch.float32 and dev >= 0 and h.is_contiguous()
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        ok = False
+    if not ok:
+        raise BGQError(ERR_INVALID_ARG, "bgq_rmsnorm_f8: h must be a CUDA fp32 tensor [batch][d], contiguous")
     if stream is not None or _device() != dev:
         with _there(dev, stream):
             return bgq_rmsnorm_f8(h, rho, eps, delta, out, a, want_a)
-    _need(h.is_contiguous(), what)
-    f32 = getattr(delta, "dtype", None) is torch.float32
+    f32 = delta is not None and getattr(delta, "dtype", None) is torch.float32
     pd = None if delta is None else _plain(delta, torch.float32 if f32 else _BF16, shape, dev,
                                            "bgq_rmsnorm_f8: delta must be fp32 or bf16 [batch][d] beside h, contiguous")
     pr = None if rho is None else _plain(rho, _BF16, (d,), dev, "bgq_rmsnorm_f8: rho must be bf16 [d] beside h, contiguous")
@@ -765,20 +770,30 @@ def f8_gemm_workspace_bytes(W: F8Matrix, x: F8Matrix) -> int:
     return load().bgq_f8_gemm_workspace_bytes(W.ref, x.ref)
 
 
-def _f8_workspace(W: F8Matrix, x: F8Matrix, ws):
-    if ws is None:
-        return workspace(f8_gemm_workspace_bytes(W, x), x.device)
-    _need(isinstance(ws, torch.Tensor) and ws.get_device() == x.index and ws.is_contiguous(), "ws must be beside x, contiguous")
-    return ws
+def _f8_workspace(W: F8Matrix, x: F8Matrix):
+    return workspace(f8_gemm_workspace_bytes(W, x), x.device)
+
+
+def _f8_ws(ws, index: int):
+    """A workspace's address and bytes."""
+    try:
+        if ws.get_device() == index and ws.is_contiguous():
+            return ws.data_ptr(), ws.nbytes
+    except (AttributeError, RuntimeError):
+        pass
+    raise BGQError(ERR_INVALID_ARG, "ws must be a tensor beside x, contiguous")
 
 
 def _f8_out(t, dtype, rows: int, cols: int, index: int, what: str):
     """An output's address (one without rows has none, and any aligned one does) and the values between its rows."""
-    if t is None:
-        return None, 0
-    r, c, s = _rows_of(t, dtype, index, what)
-    _need(r == rows and c == cols, what)
-    return t.data_ptr() if rows else 256, s
+    try:
+        r, c = t.shape
+        s, one = t.stride()
+        if t.dtype is dtype and r == rows and c == cols and (one == 1 or c == 1) and t.get_device() == index:
+            return t.data_ptr() if r else 256, s if r > 1 else -(-c // 8) * 8
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        pass
+    raise BGQError(ERR_INVALID_ARG, what)
 
 
 def bgq_f8_gemm(W: F8Matrix, x: F8Matrix, out: torch.Tensor | None = None, out_f32: torch.Tensor | None = None,
@@ -786,8 +801,8 @@ def bgq_f8_gemm(W: F8Matrix, x: F8Matrix, out: torch.Tensor | None = None, out_f
     """bgq_f8_gemm: y = x W^T, W with block_rows 128 -> (y bf16, y fp32), [x.rows][W.rows] each, rows a multiple of 8
     values apart (both alike). Buffers that are given are filled; where none is, the bf16 one is made (unless
     want_out is False) and the fp32 one where wanted."""
-    _need(isinstance(W, F8Matrix) and isinstance(x, F8Matrix) and W.index == x.index,
-          "bgq_f8_gemm: W and x must be F8Matrix on one device")
+    if not (isinstance(W, F8Matrix) and isinstance(x, F8Matrix) and W.index == x.index):
+        raise BGQError(ERR_INVALID_ARG, "bgq_f8_gemm: W and x must be F8Matrix on one device")
     dev, M, N = x.index, x.rows, W.rows
     if stream is not None or _device() != dev:
         with _there(dev, stream):
@@ -796,11 +811,15 @@ def bgq_f8_gemm(W: F8Matrix, x: F8Matrix, out: torch.Tensor | None = None, out_f
         out = alloc((M, -(-N // 8) * 8), _BF16, x.device)[:, :N]
     if out_f32 is None and want_f32:
         out_f32 = alloc((M, -(-N // 8) * 8), torch.float32, x.device)[:, :N]
-    py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_gemm: out must be bf16 [x.rows][W.rows] beside x, columns side by side")
-    pf, sf = _f8_out(out_f32, torch.float32, M, N, dev, "bgq_f8_gemm: out_f32 must be fp32 [x.rows][W.rows] beside x, columns side by side")
-    _need(py is None or pf is None or so == sf, "bgq_f8_gemm: out and out_f32 must have their rows equally far apart")
-    ws = _f8_workspace(W, x, ws)
-    r = load().bgq_f8_gemm(W.ref, x.ref, py, pf, so or sf, ws.data_ptr(), ws.nbytes, _raw_stream(dev))
+    py = pf = None
+    so = sf = 0
+    if out is not None:
+        py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_gemm: out must be bf16 [x.rows][W.rows] beside x, columns side by side")
+    if out_f32 is not None:
+        pf, sf = _f8_out(out_f32, torch.float32, M, N, dev, "bgq_f8_gemm: out_f32 must be fp32 [x.rows][W.rows] beside x, columns side by side")
+        _need(py is None or so == sf, "bgq_f8_gemm: out and out_f32 must have their rows equally far apart")
+    pw, nw = _f8_ws(_f8_workspace(W, x) if ws is None else ws, dev)
+    r = load().bgq_f8_gemm(W.ref, x.ref, py, pf, so or sf, pw, nw, _raw_stream(dev))
     if r:
         raise BGQError(r, "bgq_f8_gemm")
     return out, out_f32
@@ -810,8 +829,8 @@ def bgq_f8_swiglu(gate: F8Matrix, up: F8Matrix, x: F8Matrix, h: F8Matrix | None 
                   want_h: bool = True, want_out: bool = False, ws: torch.Tensor | None = None, stream=None):
     """bgq_f8_swiglu: silu(x gate^T) * (x up^T) -> (h as an F8Matrix, out bf16), [x.rows][gate.rows]. Buffers that
     are given are filled; where none is, h is made (unless want_h is False) and out where wanted."""
-    _need(isinstance(gate, F8Matrix) and isinstance(up, F8Matrix) and isinstance(x, F8Matrix) and gate.index == up.index == x.index,
-          "bgq_f8_swiglu: gate, up and x must be F8Matrix on one device")
+    if not (isinstance(gate, F8Matrix) and isinstance(up, F8Matrix) and isinstance(x, F8Matrix) and gate.index == up.index == x.index):
+        raise BGQError(ERR_INVALID_ARG, "bgq_f8_swiglu: gate, up and x must be F8Matrix on one device")
     dev, M, N = x.index, x.rows, gate.rows
     if stream is not None or _device() != dev:
         with _there(dev, stream):
@@ -820,11 +839,13 @@ def bgq_f8_swiglu(gate: F8Matrix, up: F8Matrix, x: F8Matrix, h: F8Matrix | None 
         h = F8Matrix.empty(M, N, 1, x.device)
     if out is None and want_out:
         out = alloc((M, N), _BF16, x.device)
-    if h is not None:
-        _f8_like(h, M, N, 1, dev, "bgq_f8_swiglu: h must be an F8Matrix [x.rows][gate.rows] beside x, with a scale for each row")
-    py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_swiglu: out must be bf16 [x.rows][gate.rows] beside x, columns side by side")
-    ws = _f8_workspace(gate, x, ws)
-    r = load().bgq_f8_swiglu(gate.ref, up.ref, x.ref, None if h is None else h.ref, py, so, ws.data_ptr(), ws.nbytes, _raw_stream(dev))
+    if h is not None and not (isinstance(h, F8Matrix) and h.index == dev and h.rows == M and h.cols == N and h.block_rows == 1):
+        raise BGQError(ERR_INVALID_ARG, "bgq_f8_swiglu: h must be an F8Matrix [x.rows][gate.rows] beside x, with a scale for each row")
+    py, so = None, 0
+    if out is not None:
+        py, so = _f8_out(out, _BF16, M, N, dev, "bgq_f8_swiglu: out must be bf16 [x.rows][gate.rows] beside x, columns side by side")
+    pw, nw = _f8_ws(_f8_workspace(gate, x) if ws is None else ws, dev)
+    r = load().bgq_f8_swiglu(gate.ref, up.ref, x.ref, None if h is None else h.ref, py, so, pw, nw, _raw_stream(dev))
     if r:
         raise BGQError(r, "bgq_f8_swiglu")
     return h, out
