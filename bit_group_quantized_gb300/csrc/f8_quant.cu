@@ -3,7 +3,9 @@
 // quantisation in one pass over the row).
 //
 // Both are bound by memory: 3 bytes a value (2 read, 1 written), and 11 (h read and
-// written, a bf16 addend read, a code written; 2 more for the bf16 copy).
+// written, a bf16 addend read, a code written; 2 more for the bf16 copy). Measured (a graph of calls over more than L2
+// holds): quantiser 12288 x 4096 in blocks 22.7 us, 6.6 TB/s; 4097 x 8192 in rows 17.0 us, 5.9 TB/s; norm 8191 x 4096 56.0 us, 6.6
+// TB/s; 2049 x 5008 with fp32 addend and bf16 copy 28.1 us, 5.5 TB/s, where 2.2 waves of CTAs take the time of three.
 #include <type_traits>
 
 #include "common.cuh"
