@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     f8_map_ahead(&mx);
     f8_map_ahead(rank ? &mw1 : &mw0);
   }
+  // The other CTA's barriers are there before anything is copied for them. (That its tensor memory is there, too, its scales tell.)
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();  // tensor memory, too, is taken only once earlier kernels have given theirs back
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   // Scales: a lane has those of x's rows l, 32 + l, ...; W's are the same for a whole block of 128 rows.
   // A chunk: the words of four groups of blocks. They are loaded a chunk ahead, of this tile or the next (loaded a group
   // or two ahead, they held the instructions up: 8191 x 12288 x 4096 took 298 us, 267 so).
@@ -109,11 +113,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   };
   if (warp >= 4 && warp < 8) load(cur);
   if (warp == 2) f8_tmem_alloc<2>(&s_tmem, 512);
-  tc_fence_before();
-  __syncthreads();
-  f8_cluster_sync();
-  tc_fence_after();
-  pdl_trigger();
+  if (warp > 0) {  // warp 0 needs none of it
+    tc_fence_before();
+    asm volatile("bar.sync 1, 352;" ::: "memory");
+    tc_fence_after();
+    pdl_trigger();
+  }
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
