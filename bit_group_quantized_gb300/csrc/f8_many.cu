@@ -121,6 +121,58 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
   const uint32_t tmem = s_tmem;
 
+  // Results. A warp that writes them has two rooms; the scales' warps, which share a pair's last tile, have theirs in the ring.
+  unsigned char* rooms = stages + (warp >= 8 ? kManyStages * kManyStage : 0) + (warp & 3) * 2 * kF8Room;
+  const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+  int room = 0;
+  auto store = [&](const uint4(&line)[8], const CUtensorMap* map, int col, int row) {
+    f8_store_rows(rooms + room * kF8Room, line, map, col, row);
+    room ^= 1;
+  };
+  // 64 columns of the warp's rows, of which a thread has a row. (A TMA store writes 16 bytes or nothing: where the columns end
+  // within that, the last pieces are written value by value.)
+  auto store64 = [&](const float(&lo)[32], const float(&hi)[32], int col, int row) {
+    uint4 line[8];
+    if (row >= p.M) return;
+    const int left = row + lane < p.M ? p.N - col : 0;
+    if (p.y && col < p.N) {
+      if (col + 64 <= p.N || p.N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) line[i] = f8_bf16x8(i < 4 ? &lo[8 * i] : &hi[8 * i - 32]);
+        store(line, &out.y, col, row);
+      } else {
+        uint16_t* y = p.y + (int64_t)(row + lane) * p.y_stride + col;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i < left) y[i] = f2bf(i < 32 ? lo[i & 31] : hi[i & 31]);
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = col + 32 * half;
+      if (!p.yf || c >= p.N) continue;
+      if (c + 32 <= p.N || p.N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) line[i] = f8_fp32x4(half ? &hi[4 * i] : &lo[4 * i]);
+        store(line, &out.yf, c, row);
+      } else {
+        float* y = p.yf + (int64_t)(row + lane) * p.y_stride + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left - 32 * half) y[i] = half ? hi[i] : lo[i];
+      }
+    }
+  };
+  // 64 columns, the c-th, of a tile's sums at `acc`.
+  auto sums64 = [&](int c, uint32_t acc, int tn, int row, auto read) {
+    float v[2][32];
+    f8_tmem_ld32(acc + 64 * c, v[0]);
+    f8_tmem_ld32(acc + 64 * c + 32, v[1]);
+    read(v);
+    store64(v[0], v[1], tn * kManyCols + 64 * c, row);
+  };
+  auto plain_read = [](float(&)[2][32]) { f8_tmem_ld_wait(); };
+
   if (warp == 0) {
     if (lane == 0) {
       const CUtensorMap* mw = GATED && rank ? &mw1 : &mw0;
@@ -223,48 +275,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         par ^= 1;
       }
     }
+    if (!GATED && ok) {
+      const int t = (work.tiles - 1 - pair) / pairs;
+      int tm, tn;
+      work.at(pair + t * pairs, tm, tn);
+      ok = __all_sync(kFull, f8_wait(&acc_full[t & 1], (t >> 1) & 1, fail));
+      tc_fence_after();
+      const bool back = (t & 1) == 0;
+#pragma unroll 1
+      for (int c = kManyCols / 128; ok && c < kManyCols / 64; ++c)
+        sums64(back ? kManyCols / 64 - 1 - c : c, lanes + (back ? 0 : kManyCols - kManyShared), tn,
+               tm * kManyRows + (int)rank * 128 + (warp & 3) * 32, plain_read);
+      f8_stores_done();
+    }
   } else if (warp >= 8) {
-    const uint32_t freed = f8_at(acc_free, 0), lanes = tmem + ((uint32_t)(warp & 3) << 21);
-    unsigned char* rooms = stages + kManyStages * kManyStage + (warp & 3) * 2 * kF8Room;
-    int room = 0;
-    auto store = [&](const uint4(&line)[8], const CUtensorMap* map, int col, int row) {
-      f8_store_rows(rooms + room * kF8Room, line, map, col, row);
-      room ^= 1;
-    };
-    // 64 columns of the warp's rows, of which a thread has a row. (A TMA store writes 16 bytes or nothing: where the columns end
-    // within that, the last pieces are written value by value.)
-    auto store64 = [&](const float(&lo)[32], const float(&hi)[32], int col, int row) {
-      uint4 line[8];
-      if (row >= p.M) return;
-      const int left = row + lane < p.M ? p.N - col : 0;
-      if (p.y && col < p.N) {
-        if (col + 64 <= p.N || p.N % 8 == 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) line[i] = f8_bf16x8(i < 4 ? &lo[8 * i] : &hi[8 * i - 32]);
-          store(line, &out.y, col, row);
-        } else {
-          uint16_t* y = p.y + (int64_t)(row + lane) * p.y_stride + col;
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i < left) y[i] = f2bf(i < 32 ? lo[i & 31] : hi[i & 31]);
-        }
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int c = col + 32 * half;
-        if (!p.yf || c >= p.N) continue;
-        if (c + 32 <= p.N || p.N % 4 == 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) line[i] = f8_fp32x4(half ? &hi[4 * i] : &lo[4 * i]);
-          store(line, &out.yf, c, row);
-        } else {
-          float* y = p.yf + (int64_t)(row + lane) * p.y_stride + c;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < left - 32 * half) y[i] = half ? hi[i] : lo[i];
-        }
-      }
-    };
+    const uint32_t freed = f8_at(acc_free, 0);
     int t = 0;
     for (int i = pair; i < work.tiles; i += pairs, ++t) {
       int tm, tn;
@@ -285,18 +310,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       };
       static_assert(kManyShared == 64, "two chunks of 32 columns");
       if (!GATED) {
-        float v[2][32];
+        // (of a pair's last tile the scales' warps, which are done, have the second half)
+        const int most = i + pairs < work.tiles ? kManyCols / 64 : kManyCols / 128;
+        sums64(back ? kManyCols / 64 - 1 : 0, acc, tn, row, drained);
 #pragma unroll 1
-        for (int c = 0; c < kManyCols / 64; ++c) {
-          const int col = 64 * (back ? kManyCols / 64 - 1 - c : c);
-          f8_tmem_ld32(acc + col, v[0]);
-          f8_tmem_ld32(acc + col + 32, v[1]);
-          if (c == 0)
-            drained(v);
-          else
-            f8_tmem_ld_wait();
-          store64(v[0], v[1], tn * kManyCols + col, row);
-        }
+        for (int c = 1; c < most; ++c) sums64(back ? kManyCols / 64 - 1 - c : c, acc, tn, row, plain_read);
       } else {
         // columns 64 c .. of the result, c = 1, 0 or 0, 1
         float h[2][2][32];
