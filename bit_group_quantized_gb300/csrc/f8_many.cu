@@ -10,10 +10,10 @@
 // tile's sums start kManyShared columns before the first's end, and a tile's epilogue reads those columns first: the next tile's
 // instructions wait for them alone.
 //
-// What bounds it: the matrix instructions, 128 cycles for 256 x 256 x 32, and the power that they draw. 8191 x 12288 x 4096: 235 us,
+// What bounds it: the matrix instructions, 128 cycles for 256 x 256 x 32, and the power that they draw. 8191 x 12288 x 4096: 226 to 235 us,
 // 3.5 PFLOP/s, 373k cycles of which the instructions take 344k, at 1.6 GHz where the SMs could run at 2.07; the rest is the wait between
 // tiles (1800 cycles for the last instructions and the shared columns). Gated 4095 x 2 * 12288 x 4096: 255 to 264 us. Seconds on end (1.4 kW): 273 us each.
-// A launch of one tile a pair spends 7 us besides its instructions (4096 x 4096, 512 rows: 16.6 us).
+// A launch of one tile a pair spends 5 to 8 us besides its instructions (512 x 4096 x 4096: 14.9 us, 777 x 4096 x 8192: 25 us).
 // What it took: instructions issued by a whole warp with one elected lane, so that descriptors stay in uniform registers (358 -> 313 us);
 // scales in four sets, loaded far ahead (267); arrivals that release nothing (243); results by TMA stores (235).
 #include "f8_tc.cuh"

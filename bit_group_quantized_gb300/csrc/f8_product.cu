@@ -3,31 +3,31 @@
 // Three read the same operands and give the same kinds of results:
 //   f8_few.cu   few rows, mma.sync, W straight into registers: next to nothing besides W's bytes, which come at 4.4 TB/s;
 //   f8_mid.cu   W as the tensor cores' operand of 128 rows, columns split over CTAs: 3 us besides W's bytes at 6.5 TB/s;
-//   f8_many.cu  tiles of 256 x 256: 7 us besides, and the most arithmetic a second.
+//   f8_many.cu  tiles of 256 x 256: 5 us besides, and the most arithmetic a second.
 // The rule below goes by sizes alone: the one that the estimates call soonest. Measured (CUDA graphs of 24 calls over 130 to 300 MB of
 // weights; us, N x K, gated: 2 N x K):
 //                     rows:     1     8    16    32    64   128   256   512  1024  2048
 //   4096 x 4096       few     4.3   4.7   5.9   8.6  15.9
 //                     mid     6.1   6.2   6.3   6.5   7.1   8.1  11.0  15.0  18.2
-//                     many                          16.1              16.6  17.7  26.6
+//                     many                          14.0  14.6  14.7  15.0  16.7  25.7
 //   12288 x 4096      few    11.8  12.2  15.0  23.3
 //                     mid    10.4  10.5  10.7  10.9  11.8  13.9  19.2
-//                     many                                18.1  18.2  27.2  37.1  65.6
+//                     many                          15.8  16.5  16.6  25.6  35.6  64.7
 //   4096 x 1024       few     3.2   3.3   3.3   3.5   5.8
 //                     mid     3.7   3.6   3.8   3.9   4.5   5.6   7.9  10.2
-//                     many                    8.7   8.7   9.1   9.1   9.2   9.5  13.3
+//                     many                    6.8   6.8   7.2   7.2   7.5   8.4  12.1
 //   1024 x 1024       few     2.1   2.2   2.2   2.5   2.6
 //                     mid     3.1   3.2   3.3   3.5   3.9
 //   256 x 16384       few     7.7   8.5  11.3  19.4
 //                     mid     7.0   7.4   7.4   7.5
 //   1024 x 4096       few     5.0   5.4   8.9  12.8
 //   gated             mid     4.8   4.9   5.2   5.8   7.7  10.3  11.1  11.9  16.1
-//                     many                                      15.5  15.7  16.1  17.7
+//                     many                          14.4  14.8  14.8  15.2  15.8  17.4
 //   512 x 1024        few     2.9   3.0   3.8   5.8
 //   gated             mid     3.4   3.6   3.8   4.4
 //   12288 x 4096      few    24.9  25.2  36.6  57.5
 //   gated             mid    18.2  18.3  18.7  19.6  21.8  25.7  47.0
-//                     many                                29.3  30.0  38.7  67.6   121
+//                     many                          28.4  28.7  29.3  38.5  67.3   121
 #include <algorithm>
 
 #include "f8.h"
@@ -53,13 +53,13 @@ static double mid_us(const F8Prod& p, bool gated, double weights, int sms) {
   while (split > 1 && (2 * split > blocks || tiles * split > sms * 7 / 8)) split >>= 1;
   const double block = gated ? 0.46 + 0.0021 * rows : 0.22 + 0.00105 * rows;
   const double waves = ceil_div(tiles * split, sms);
-  return 2.9 + std::max(waves * ceil_div(blocks, split) * block, weights / 6.5) + rows * (split == 1 ? 0.006 : gated ? 0.029 : 0.0137);
+  return 3.1 + std::max(waves * ceil_div(blocks, split) * block, weights / 6.5) + rows * (split == 1 ? 0.006 : gated ? 0.029 : 0.0137);
 }
 
 // Many rows: a pair of CTAs' tiles one after the other, or W's bytes.
 static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
   const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : 256);
-  return 6.7 + std::max(0.28 * f8_blocks(p.K) * ceil_div(tiles, std::max(1, sms / 2)), weights / 4.4);
+  return 5.4 + std::max(0.28 * f8_blocks(p.K) * ceil_div(tiles, std::max(1, sms / 2)), weights / 4.4);
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
