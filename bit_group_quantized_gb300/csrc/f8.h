@@ -67,7 +67,8 @@ constexpr int kF8One = 127;                // the scale byte of 1
 // silu(g) * u. The exponential's and the reciprocal's approximations are 2^-21 off or so, the result has 8 bits or 4.
 __device__ __forceinline__ float f8_swiglu(float g, float u) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  // (not its flushing form: near g = -88 the reciprocal is subnormal, and u may be large)
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
   return g * r * u;
 }
 #endif

@@ -2,6 +2,8 @@
 // checks, then the launches of f8_quant.cu and f8_product.cu.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "f8.h"
 #include "kernels.h"
 
@@ -88,6 +90,7 @@ int32_t bgq_rmsnorm_f8(float* h, const void* delta, int32_t delta_f32, const uin
   if (r) return r;
   if (!h || !al(h, 16) || !al(delta, 16) || !al(rho, 16) || !al(a, 16)) return BGQ_ERR_INVALID_ARG;
   if (batch != m->rows || d != m->cols || !(eps >= 0.f)) return BGQ_ERR_INVALID_ARG;
+  if (batch && (h == delta || h == (const void*)a || h == (const void*)m->q)) return BGQ_ERR_INVALID_ARG;
   if (batch == 0) return BGQ_OK;
   return cuda_status(launch_rmsnorm_f8(h, delta, delta_f32 != 0, rho, eps, *m, a, st(stream)));
 }
@@ -101,6 +104,8 @@ int32_t bgq_f8_gemm(const bgq_f8matrix* W, const bgq_f8matrix* x, uint16_t* y, f
   int r = check_product(W, x);
   if (r || (r = check_out(y, y_stride, W->rows)) || (r = check_out(y_f32, y_stride, W->rows))) return r;
   if (!y && !y_f32) return BGQ_ERR_INVALID_ARG;
+  for (const void* in : {(const void*)x->q, (const void*)x->scale, (const void*)W->q, (const void*)W->scale})
+    if (x->rows && (y == in || y_f32 == in)) return BGQ_ERR_INVALID_ARG;
   if (!ws || !al(ws, 256) || ws_bytes < kWsBytes) return BGQ_ERR_WORKSPACE;
   if (x->rows == 0) return BGQ_OK;
   return cuda_status(launch_f8_product(product(W, nullptr, x, y, y_f32, y_stride, ws), false, st(stream)));
@@ -113,6 +118,9 @@ int32_t bgq_f8_swiglu(const bgq_f8matrix* gate, const bgq_f8matrix* up, const bg
   if (gate->rows != up->rows || gate->rows % 16 || (!h && !y)) return BGQ_ERR_INVALID_ARG;
   if (h && (r = check_f8(h, 1))) return r;
   if (h && (h->rows != x->rows || h->cols != gate->rows)) return BGQ_ERR_INVALID_ARG;
+  for (const bgq_f8matrix* in : {gate, up, x})
+    if (x->rows && ((h && (h->q == in->q || h->scale == in->scale)) || y == (const void*)in->q || y == (const void*)in->scale))
+      return BGQ_ERR_INVALID_ARG;
   if (!ws || !al(ws, 256) || ws_bytes < kWsBytes) return BGQ_ERR_WORKSPACE;
   if (x->rows == 0) return BGQ_OK;
   F8Prod p = product(gate, up, x, y, nullptr, y_stride, ws);

@@ -13,8 +13,6 @@
 // 4096: 7.2 to 7.7). Half the shared memory, so that the next launch's CTAs start beside this one's, gave nothing (12.0 us for 11.5), nor did asking
 // W into L2 ahead of the wait for the kernel before.
 #include <algorithm>
-#include <mutex>
-#include <vector>
 
 #include "f8_tc.cuh"
 
@@ -22,7 +20,7 @@ namespace bgq {
 
 constexpr int kMidThreads = 256, kMidSets = 4;  // warp 0: copies, 1: instructions, 2: tensor memory, 4-7: scales; all: results
 constexpr int kMidRing = 224 * 1024;  // bytes
-constexpr int kMidMaxStages = 8, kMidMaxSplit = 8;
+constexpr int kMidMaxStages = 8, kMidMaxSplit = 8;  // 2^3
 
 struct MidShape {
   int rows;    // of x a tile: a multiple of 16, at most 256 (gated 128)
@@ -279,37 +277,26 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   if (sh.split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Clusters of n CTAs of a kernel that the device can hold at once (asked once for each device, kernel, shared memory and n).
-static int mid_clusters(const void* kern, size_t smem, int n) {
-  struct Entry {
-    int dev;
-    const void* kern;
-    size_t smem;
-    int n, count;
-  };
-  static std::mutex mu;
-  static std::vector<Entry> seen;
-  int dev = 0;
+// Clusters of 2^n CTAs that the device can hold at once, one CTA an SM (`known`: by device and n, asked for once).
+static int mid_clusters(const void* kern, size_t smem, int n, std::atomic<int> (&known)[64][4]) {
+  int dev = 0, count = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const Entry& e : seen)
-    if (e.dev == dev && e.kern == kern && e.smem == smem && e.n == n) return e.count;
+  if (dev < 64 && (count = known[dev][n].load(std::memory_order_relaxed)) > 0) return count;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n);
+  cfg.gridDim = dim3(1 << n);
   cfg.blockDim = dim3(kMidThreads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)n;
+  at[0].val.clusterDim.x = 1u << n;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  int count = 0;
   if (cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    count = 0;
+    return 0;
   }
-  seen.push_back(Entry{dev, kern, smem, n, count});
+  if (dev < 64) known[dev][n].store(count, std::memory_order_relaxed);
   return count;
 }
 
@@ -327,8 +314,10 @@ static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s
   const cudaError_t e = f8_room(kern, 1024 + kMidRing, known);
   if (e != cudaSuccess) return e;
   // the most CTAs a tile for which all are there at once, each with two blocks of columns at least
-  for (sh.split = kMidMaxSplit; sh.split > 1; sh.split >>= 1)
-    if (2 * sh.split <= blocks && tiles * down <= mid_clusters(kern, smem, sh.split)) break;
+  static std::atomic<int> clusters[64][4];
+  int n = 3;
+  while (n > 0 && (2 << n > blocks || tiles * down > mid_clusters(kern, 1024 + kMidRing, n, clusters))) --n;
+  sh.split = 1 << n;
   CUtensorMap mx, mw[2];
   if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride, sh.rows)) return cudaErrorInvalidValue;
   for (int i = 0; i < 2; ++i)

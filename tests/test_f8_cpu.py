@@ -10,6 +10,7 @@ import torch
 from oracle import f8_oracle as F
 
 FAKE = 0x10000000  # 256-byte aligned, never dereferenced: validation fails first
+OUT, OTHER = FAKE + (1 << 20), FAKE + (2 << 20)  # results and a second result, which may not be an input
 
 
 @pytest.fixture(scope="module")
@@ -75,7 +76,7 @@ def calls(lib, matrix, **kw):
     """Each entry point on these matrices, the other arguments as they should be unless kw says otherwise."""
     L = lib.load()
     w = dict(block_rows=128)
-    x, h, b, c = mat(lib), mat(lib, cols=128), mat(lib, rows=128, **w), mat(lib, rows=128, **w)
+    x, h, b, c = mat(lib), mat(lib, q=OUT, scale=OUT, cols=128), mat(lib, rows=128, **w), mat(lib, rows=128, **w)
 
     def ref(m):
         return None if m is False else C.byref(m)
@@ -85,15 +86,15 @@ def calls(lib, matrix, **kw):
         return L.bgq_f8_quantise(k["x"], k["xs"], ref(m), None)
 
     def norm(m=matrix):
-        k = {**dict(h=FAKE, delta=FAKE, f32=0, rho=FAKE, batch=130, d=256, eps=1e-6, a=FAKE), **kw}
+        k = {**dict(h=OUT, delta=FAKE, f32=0, rho=FAKE, batch=130, d=256, eps=1e-6, a=OTHER), **kw}
         return L.bgq_rmsnorm_f8(k["h"], k["delta"], k["f32"], k["rho"], k["batch"], k["d"], k["eps"], ref(m), k["a"], None)
 
     def gemm(W=b, X=x):
-        k = {**dict(y=FAKE, yf=FAKE, ys=128, ws=FAKE, wsb=256), **kw}
+        k = {**dict(y=OUT, yf=OTHER, ys=128, ws=FAKE, wsb=256), **kw}
         return L.bgq_f8_gemm(ref(W), ref(X), k["y"], k["yf"], k["ys"], k["ws"], k["wsb"], None)
 
     def swiglu(G=b, U=c, X=x, H=h):
-        k = {**dict(y=FAKE, ys=128, ws=FAKE, wsb=256), **kw}
+        k = {**dict(y=OTHER, ys=128, ws=FAKE, wsb=256), **kw}
         return L.bgq_f8_swiglu(ref(G), ref(U), ref(X), ref(H), k["y"], k["ys"], k["ws"], k["wsb"], None)
 
     return quantise, norm, gemm, swiglu
@@ -145,10 +146,21 @@ def test_other_arguments_that_are_refused(lib):
     assert L.bgq_f8_gemm_workspace_bytes(C.byref(x), C.byref(x)) == 0
 
 
+def test_results_over_inputs_are_refused(lib):
+    m = mat(lib)
+    for kw in [dict(h=FAKE), dict(a=OUT), dict(h=FAKE, delta=None)]:
+        assert calls(lib, m, **kw)[1]() == lib.ERR_INVALID_ARG, kw
+    assert calls(lib, m, y=FAKE)[2]() == calls(lib, m, yf=FAKE)[2]() == calls(lib, m, y=FAKE)[3]() == lib.ERR_INVALID_ARG
+    square = mat(lib, cols=128, q=FAKE + (3 << 20))
+    for h in (mat(lib, cols=128), mat(lib, cols=128, q=OUT), mat(lib, cols=128, scale=OUT)):
+        assert calls(lib, m)[3](H=h) == lib.ERR_INVALID_ARG
+    assert square.cols == 128
+
+
 def test_nothing_to_do(lib):
-    none = mat(lib, rows=0)
+    none, gone = mat(lib, rows=0), mat(lib, rows=0, q=OUT, scale=OUT, cols=128)
     assert calls(lib, none)[0]() == calls(lib, none, batch=0)[1]() == calls(lib, none)[2](X=none) == lib.OK
-    assert calls(lib, none)[3](X=none, H=mat(lib, rows=0, cols=128)) == lib.OK
+    assert calls(lib, none)[3](X=none, H=gone) == lib.OK
 
 
 def test_binding_refuses_host_tensors(lib):

@@ -290,3 +290,25 @@ def test_swiglu_blocks_that_are_not_finite(cuda_device, m):
     assert np.isnan(v[:, 128:256]).all() and np.isnan(v[1]).all()
     assert (v[2, :128] == 0).all() and (v[2, 256:] == 0).all()
     assert np.isfinite(v[0, :128]).all() and np.isfinite(v[0, 256:]).all()
+
+
+@pytest.mark.parametrize("m", [2, 40, 500])
+def test_swiglu_of_far_negative_gates(cuda_device, m):
+    """silu(-88) is below fp32's normal numbers, its product with a large up is not."""
+    k, n = 256, 144
+    q = np.zeros((m, k), dtype=np.uint8)
+    q[:, 0] = 0x38  # 1
+    w = np.zeros((n, k), dtype=np.uint8)
+    w[:, 0] = np.where(np.arange(n) % 2, 0xeb, 0xea)  # -88 and -80
+    u = np.zeros((n, k), dtype=np.uint8)
+    u[:, 0] = 0x38
+    X = matrix(cuda_device, q, np.full((m, 2), 127, dtype=np.uint8), 1)
+    G = matrix(cuda_device, w, np.full((2, 2), 127, dtype=np.uint8), 128)
+    U = matrix(cuda_device, u, np.full((2, 2), 227, dtype=np.uint8), 128)
+    g = F.values(w, np.full((2, 2), 127, dtype=np.uint8), 128)[:, 0]
+    ref = np.tile(F.swiglu(g, 2.0 ** 100), (m, 1))
+    # a subnormal reciprocal of 2^-127 or so is off by 2^-150 at most, the exponential by 2 + 1.2 * 88 units of 2^-23
+    off = np.abs(ref) * (120 * 2.0 ** -23 + 2.0 ** -22)
+    h, y = lib.bgq_f8_swiglu(G, U, X, want_out=True)
+    assert (np.abs(f64(y) - ref) <= off + (np.abs(ref) + off) * 2.0 ** -8).all()
+    check_codes(h, ref, off)
