@@ -382,11 +382,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (*fail && lane == 0)  // a wait has run out: the other CTA's end too
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(f8_at(&s_fail, rank ^ 1)), "r"(1) : "memory");
   tc_fence_before();
-  __syncthreads();
-  if (*fail) {  // copies in flight land before the CTA ends
+  if (__syncthreads_or(*fail)) {  // copies in flight land before the CTA ends
     if (tid == 0) atomicExch(&p.ctrl->status, BGQ_ERR_TIMEOUT);
     for (const unsigned long long t0 = tc_time(); tc_time() - t0 < 5000000ull;) __nanosleep(10000);
-    __syncthreads();
+    __syncwarp();
   }
   f8_cluster_sync();
   if (warp == 2) f8_tmem_free<2>(tmem, 512);

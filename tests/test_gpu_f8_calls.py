@@ -1,5 +1,9 @@
 """The e4m3 operators as a program calls them: one after the other, captured, on several streams, far apart in memory, refused."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -129,6 +133,41 @@ def test_captured_and_replayed(cuda_device, m, n, k):
             assert torch.equal(y, want[seed])
     assert not torch.equal(want[0], want[1])
     assert lib.read_device_status(ws) == lib.OK
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from bit_group_quantized_gb300 import lib
+m, n, k, dev = {m}, 640, 1152, torch.device("cuda")
+h, x, act = torch.randn(m, k, device=dev), lib.F8Matrix.empty(m, k), lib.F8Matrix.empty(m, n)
+w, W, V = torch.randn(n, k, device=dev).bfloat16(), lib.F8Matrix.empty(n, k, 128), lib.F8Matrix.empty(k, n, 128)
+y, ws = torch.zeros(m, k, device=dev), lib.workspace(256, dev)
+def call():
+    lib.bgq_f8_quantise(w, out=W)
+    lib.bgq_f8_quantise(w.view(k, n), out=V)
+    lib.bgq_rmsnorm_f8(h, None, 1e-6, out=x)
+    lib.bgq_f8_swiglu(W, W, x, h=act, ws=ws)
+    lib.bgq_f8_gemm(V, act, out_f32=y, ws=ws)
+torch.cuda.synchronize()
+s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = y.clone()
+y.zero_()
+call()
+torch.cuda.synchronize()
+assert torch.equal(got, y) and bool(torch.isfinite(y).all()) and float(y.abs().max()) > 0
+"""
+
+
+@pytest.mark.parametrize("m", [3, 70, 2100])
+def test_the_first_call_of_a_process_captured(cuda_device, m):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, m=m)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_graphs_and_streams_share_a_workspace(cuda_device):
