@@ -39,6 +39,7 @@ cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_mid(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s);
+int f8_many_wide(const F8Prod& p, int pairs);
 
 #ifdef __CUDACC__
 // The scale byte of a block whose largest magnitude has these fp32 bits: the smallest power of two 2^(byte - 127) with

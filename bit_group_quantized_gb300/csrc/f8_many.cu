@@ -32,6 +32,7 @@ constexpr size_t kManySmem = 1024 + (size_t)kManyStages * kManyStage + 4 * 2 * k
 struct ManyWork {
   int tiles, down, group;  // tiles; tiles of x's rows; of which `group` are walked through beside each other
   int across;
+  int wide;  // rows of W a tile: 256, or less (in thirty-twos, as the instructions of two CTAs take them) where that leaves fewer SMs idle at the end; gated 128 of each
   // Tile i: groups of `group` tiles of x's rows by all of W's, so that what runs at a time shares both operands.
   __device__ __forceinline__ void at(int i, int& m, int& n) const {
     const int wide = group * across, g = i / wide, in = i - g * wide, h = min(group, down - g * group);
@@ -44,7 +45,8 @@ struct ManyOut {
   CUtensorMap y, yf, h;  // those that are wanted
 };
 
-template <bool GATED>
+// WHOLE: tiles of 256 rows of W (gated ones always; known to the compiler, they take 1 to 2 % less time).
+template <bool GATED, bool WHOLE>
 __global__ void __launch_bounds__(kManyThreads, 1)
     k_f8_many(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0,
               const __grid_constant__ CUtensorMap mw1, const __grid_constant__ ManyOut out, const F8Prod p, const ManyWork work) {
@@ -60,6 +62,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const uint32_t rank = f8_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int blocks = f8_blocks(p.K), groups = (blocks + 3) >> 2;
+  const int cols = WHOLE ? kManyCols : work.wide;  // of a tile's sums
   if (tid == 0) {
     for (int i = 0; i < kManyStages; ++i) {
       tc_mbar_init(&full[i]);
@@ -85,18 +88,26 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   // A chunk: the words of four groups of blocks. They are loaded a chunk ahead, of this tile or the next (loaded a group
   // or two ahead, they held the instructions up: 8191 x 12288 x 4096 took 298 us, 267 so).
   const int wbs = f8_blocks(p.N);
+  // A tile's rows of W lie in up to three blocks of 128 (gated: a block of gate, then one of up): `pick` has two bits for each 32 of
+  // them, which of the three words this lane's row takes.
   struct Chunk {
-    uint32_t x[4][4], w[4][2];
+    uint32_t x[4][4], w[4][3], pick;
   } cur = {}, next = {};
   int li = pair, lg = 0;  // tile and first group of the next chunk
   auto load = [&](Chunk& v) {
     if (li >= work.tiles) return;
     int tm, tn;
     work.at(li, tm, tn);
-    const int m0 = tm * kManyRows + (int)rank * 128 + lane, wb = GATED ? tn : 2 * tn;
+    const int m0 = tm * kManyRows + (int)rank * 128 + lane, n0 = GATED ? tn * 128 : tn * cols, wb = n0 / kF8Block;
     const uint8_t* x = p.xs + (int64_t)m0 * p.xs_stride + 4 * lg;
     const uint8_t* w0 = p.ws[0] + wb * p.ws_stride[0] + 4 * lg;
-    const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] + 4 * lg : wb + 1 < wbs ? w0 + p.ws_stride[0] : w0;
+    const uint8_t* w1 = GATED ? p.ws[1] + wb * p.ws_stride[1] + 4 * lg : w0 + (wb + 1 < wbs ? p.ws_stride[0] : 0);
+    const uint8_t* w2 = WHOLE ? w1 : w0 + (wb + 2 < wbs ? 2 * p.ws_stride[0] : 0);
+    if (!WHOLE) {
+      v.pick = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v.pick |= (uint32_t)(((n0 & 127) + 32 * j + lane) >> 7) << 2 * j;
+    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const bool there = lg + g < groups;
@@ -105,6 +116,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         v.x[g][j] = there && m0 + 32 * j < p.M ? *reinterpret_cast<const uint32_t*>(x + 32 * j * p.xs_stride + 4 * g) : 0u;
       v.w[g][0] = there ? *reinterpret_cast<const uint32_t*>(w0 + 4 * g) : 0u;
       v.w[g][1] = there ? *reinterpret_cast<const uint32_t*>(w1 + 4 * g) : 0u;
+      v.w[g][2] = there && !WHOLE ? *reinterpret_cast<const uint32_t*>(w2 + 4 * g) : 0u;
     }
     if ((lg += 4) >= groups) {
       lg = 0;
@@ -163,13 +175,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     }
   };
-  // 64 columns, the c-th, of a tile's sums at `acc`.
-  auto sums64 = [&](int c, uint32_t acc, int tn, int row, auto read) {
+  // 64 columns, the c-th, of a tile's sums at `acc`, from the end or from the beginning (what is left of less than 64 is written again
+  // with columns beside it).
+  const int chunks = (cols + 63) / 64;
+  auto sums64 = [&](int c, bool back, uint32_t acc, int tn, int row, auto read) {
+    const int first = back ? max(0, cols - 64 * (c + 1)) : min(64 * c, cols - 64);
     float v[2][32];
-    f8_tmem_ld32(acc + 64 * c, v[0]);
-    f8_tmem_ld32(acc + 64 * c + 32, v[1]);
+    f8_tmem_ld32(acc + first, v[0]);
+    f8_tmem_ld32(acc + first + 32, v[1]);
     read(v);
-    store64(v[0], v[1], tn * kManyCols + 64 * c, row);
+    store64(v[0], v[1], tn * cols + first, row);
   };
   auto plain_read = [](float(&)[2][32]) { f8_tmem_ld_wait(); };
 
@@ -183,12 +198,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         int tm, tn;
         work.at(i, tm, tn);
         const int m0 = tm * kManyRows + (int)rank * 128;
-        const int n0 = GATED ? tn * 128 : tn * kManyCols + (int)rank * 128;
+        const int n0 = GATED ? tn * 128 : tn * cols + (int)rank * (cols / 2);
         for (int b = 0; b < blocks; ++b) {
           if (!(ok = f8_wait(&empty[s], par, fail))) break;
           unsigned char* st = stages + s * kManyStage;
           const uint32_t bar = f8_at(&full[s], 0);
-          if (rank == 0) f8_expect(&full[s], 2 * kManyStage);
+          if (rank == 0) f8_expect(&full[s], 2 * kF8Tile + 128 * cols);
           f8_load<2>(st, &mx, b * 128, m0, bar);
           f8_load<2>(st + kF8Tile, mw, b * 128, n0, bar);
           if (++s == kManyStages) {
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tc_fence_after();
           const uint32_t at = tc_smem(stages + s * kManyStage), scales = tmem + kManyScales + set * 16;
           const uint64_t a = f8_desc(at), w = f8_desc(at + kF8Tile);
-          const uint32_t idesc = f8_idesc(kManyRows, kManyCols, sf);
+          const uint32_t idesc = f8_idesc(kManyRows, cols, sf);
 #pragma unroll
           for (int k = 0; k < 4; ++k) f8_tc_mma<2>(d, a + 2 * k, w + 2 * k, idesc, scales, scales + 4, (b | k) ? 1u : 0u, lead);
           f8_commit<2>(&empty[s], lead);
@@ -255,8 +270,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (!(ok = __all_sync(kFull, f8_wait(&sf_free[set], par, fail)))) continue;
           tc_fence_after();
           f8_tmem_st4(at + set * 16, cur.x[g][0], cur.x[g][1], cur.x[g][2], cur.x[g][3]);
-          f8_tmem_st4(at + set * 16 + 4, cur.w[g][0], cur.w[g][0], cur.w[g][0], cur.w[g][0]);
-          f8_tmem_st4(at + set * 16 + 8, cur.w[g][1], cur.w[g][1], cur.w[g][1], cur.w[g][1]);
+          auto word = [&](int j) {
+            if (WHOLE) return cur.w[g][j >> 2];
+            const uint32_t k = cur.pick >> 2 * j & 3;
+            return k == 0 ? cur.w[g][0] : k == 1 ? cur.w[g][1] : cur.w[g][2];
+          };
+          f8_tmem_st4(at + set * 16 + 4, word(0), word(1), word(2), word(3));
+          f8_tmem_st4(at + set * 16 + 8, word(4), word(5), word(6), word(7));
           f8_tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -283,9 +303,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       tc_fence_after();
       const bool back = (t & 1) == 0;
 #pragma unroll 1
-      for (int c = kManyCols / 128; ok && c < kManyCols / 64; ++c)
-        sums64(back ? kManyCols / 64 - 1 - c : c, lanes + (back ? 0 : kManyCols - kManyShared), tn,
-               tm * kManyRows + (int)rank * 128 + (warp & 3) * 32, plain_read);
+      for (int c = (chunks + 1) / 2; ok && c < chunks; ++c)
+        sums64(c, back, lanes + (back ? 0 : kManyCols - kManyShared), tn, tm * kManyRows + (int)rank * 128 + (warp & 3) * 32, plain_read);
       f8_stores_done();
     }
   } else if (warp >= 8) {
@@ -311,10 +330,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       static_assert(kManyShared == 64, "two chunks of 32 columns");
       if (!GATED) {
         // (of a pair's last tile the scales' warps, which are done, have the second half)
-        const int most = i + pairs < work.tiles ? kManyCols / 64 : kManyCols / 128;
-        sums64(back ? kManyCols / 64 - 1 : 0, acc, tn, row, drained);
+        const int most = i + pairs < work.tiles ? chunks : (chunks + 1) / 2;
+        sums64(0, back, acc, tn, row, drained);
 #pragma unroll 1
-        for (int c = 1; c < most; ++c) sums64(back ? kManyCols / 64 - 1 - c : c, acc, tn, row, plain_read);
+        for (int c = 1; c < most; ++c) sums64(c, back, acc, tn, row, plain_read);
       } else {
         // columns 64 c .. of the result, c = 1, 0 or 0, 1
         float h[2][2][32];
@@ -391,25 +410,45 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (warp == 2) f8_tmem_free<2>(tmem, 512);
 }
 
+// Rows of W a tile (not gated) for so many pairs of CTAs: fewer where that keeps more of them busy. A block of a tile takes what its
+// operands' bytes take to an SM, 62 a cycle (264 + 1.03 cycles a row; the instructions take 2 a row), and a tile 2000 cycles besides.
+// Measured: 512 x 12288 x 4096 24.2 us with 192, 25.4 with 256; 512 x 4096 x 4096 13.5 with 128, 14.9 with 256; where 224 would give 6 %,
+// it gives 2 or takes 3 (777 x 4096 x 8192: 24.9 and 25.3; 2048 x 4096 x 1024: 12.3 and 11.9), so no change for less than a twelfth.
+int f8_many_wide(const F8Prod& p, int pairs) {
+  const int64_t down = (p.M + kManyRows - 1) / kManyRows, blocks = f8_blocks(p.K);
+  int best = kManyCols;
+  int64_t least = INT64_MAX;
+  for (int wide = kManyCols; wide >= 128; wide -= 32) {
+    const int64_t tiles = down * ((p.N + wide - 1) / wide), waves = (tiles + pairs - 1) / pairs;
+    const int64_t cost = waves * ((264 + 103 * wide / 100) * blocks + 2000);
+    if (cost < least - least / 12) {
+      best = wide;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
+  const int pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1, wide = gated ? 128 : f8_many_wide(p, pairs);
   CUtensorMap mx, mw[2];
   if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride)) return cudaErrorInvalidValue;
-  for (int i = 0; i < 2; ++i)
-    if (!f8_map(&mw[i], p.w[i], p.N, p.K, p.w_stride[i])) return cudaErrorInvalidValue;
+  for (int i = 0; i < (gated ? 2 : 1); ++i)
+    if (!f8_map(&mw[i], p.w[i], p.N, p.K, p.w_stride[i], gated ? 128 : wide / 2)) return cudaErrorInvalidValue;
   ManyOut out = {};
   if (p.y && !f8_out_map(&out.y, p.y, 2, p.M, p.N, p.y_stride)) return cudaErrorInvalidValue;
   if (p.yf && !f8_out_map(&out.yf, p.yf, 4, p.M, p.N, p.y_stride)) return cudaErrorInvalidValue;
   if (p.h && !f8_out_map(&out.h, p.h, 1, p.M, p.N, p.h_stride)) return cudaErrorInvalidValue;
-  const int wide = gated ? 128 : kManyCols;
   ManyWork work;
   work.down = (p.M + kManyRows - 1) / kManyRows;
   work.across = (p.N + wide - 1) / wide;
+  work.wide = wide;
   work.tiles = work.down * work.across;
   work.group = work.down < 8 ? work.down : 8;
-  const int pairs = num_sms() / 2;
-  static std::atomic<uint64_t> known[2];
-  const void* kern = gated ? (const void*)k_f8_many<true> : (const void*)k_f8_many<false>;
-  const cudaError_t e = f8_room(kern, (int)kManySmem, known[gated]);
+  static std::atomic<uint64_t> known[3];
+  const int which = gated ? 0 : wide == kManyCols ? 1 : 2;
+  const auto kern = gated ? k_f8_many<true, true> : which == 1 ? k_f8_many<false, true> : k_f8_many<false, false>;
+  const cudaError_t e = f8_room((const void*)kern, (int)kManySmem, known[which]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (work.tiles < pairs ? work.tiles : pairs));
@@ -424,8 +463,7 @@ cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return gated ? cudaLaunchKernelEx(&cfg, k_f8_many<true>, mx, mw[0], mw[1], out, p, work)
-               : cudaLaunchKernelEx(&cfg, k_f8_many<false>, mx, mw[0], mw[0], out, p, work);
+  return cudaLaunchKernelEx(&cfg, kern, mx, mw[0], mw[gated ? 1 : 0], out, p, work);
 }
 
 }  // namespace bgq

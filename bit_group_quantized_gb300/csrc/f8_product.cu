@@ -58,8 +58,9 @@ static double mid_us(const F8Prod& p, bool gated, double weights, int sms) {
 
 // Many rows: a pair of CTAs' tiles one after the other, or W's bytes.
 static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
-  const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : 256);
-  return 5.4 + std::max(0.28 * f8_blocks(p.K) * ceil_div(tiles, std::max(1, sms / 2)), weights / 4.4);
+  const int pairs = std::max(1, sms / 2), wide = gated ? 256 : f8_many_wide(p, pairs);
+  const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : wide);
+  return 5.4 + std::max((0.14 + 0.00055 * wide) * f8_blocks(p.K) * ceil_div(tiles, pairs), weights / 4.4);
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
