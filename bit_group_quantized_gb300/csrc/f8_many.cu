@@ -1,19 +1,20 @@
 // f8_many.cu — products of e4m3 matrices for many rows, on tcgen05.
 //
-// Tiles of 256 rows of x by 256 rows of W (gated: 128 of gate beside the same 128 of up), each the work of two CTAs that
-// share their matrix instructions: a CTA brings 128 rows of both operands for every block of 128 columns, and has the sums of
-// its 128 rows of x and all 256 of W in tensor memory. A pair of CTAs on every two SMs walks through the tiles.
+// Tiles of 256 rows of x by 256 rows of W (gated: 128 of gate beside the same 128 of up; fewer rows of W where that keeps more SMs busy),
+// each the work of two CTAs that share their matrix instructions: a CTA brings 128 rows of x and half of W's for every block of 128
+// columns, and has the sums of its 128 rows of x and all of W's in tensor memory. A pair of CTAs on every two SMs walks through the tiles.
 // The warps are specialised: one copies, one (of the first CTA) issues, four keep the scales in tensor memory
-// (f8_tc.cuh), four write the results, a thread a row.
+// (f8_tc.cuh), four write the results, a thread a row; of a pair's last tile the scales' warps write half.
 //
-// Tensor memory has 512 columns: two tiles' sums of 256 and two sets of scales of 12 do not fit beside each other. The second
+// Tensor memory has 512 columns: two tiles' sums of 256 and four sets of scales of 12 do not fit beside each other. The second
 // tile's sums start kManyShared columns before the first's end, and a tile's epilogue reads those columns first: the next tile's
 // instructions wait for them alone.
 //
-// What bounds it: the matrix instructions, 128 cycles for 256 x 256 x 32, and the power that they draw. 8191 x 12288 x 4096: 226 to 235 us,
-// 3.5 PFLOP/s, 373k cycles of which the instructions take 344k, at 1.6 GHz where the SMs could run at 2.07; the rest is the wait between
-// tiles (1800 cycles for the last instructions and the shared columns). Gated 4095 x 2 * 12288 x 4096: 255 to 264 us. Seconds on end (1.4 kW): 273 us each.
-// A launch of one tile a pair spends 5 to 8 us besides its instructions (512 x 4096 x 4096: 14.9 us, 777 x 4096 x 8192: 25 us).
+// What bounds it: the matrix instructions, 128 cycles for 256 x 256 x 32, beside them the operands' bytes (64 KB a pair in 512 cycles, where an
+// SM takes 62 bytes a cycle), and the power that all of it draws. 8191 x 12288 x 4096: 226 to 238 us, 3.5 PFLOP/s, 373k cycles of which the
+// instructions take 344k, at 1.6 GHz where the SMs could run at 2.07; the rest is the wait between tiles (1800 cycles for the last
+// instructions and the shared columns). Gated 4095 x 2 * 12288 x 4096: 238 to 264 us. For seconds on end (1.4 kW): 267 and 273 us.
+// A launch of one tile a pair spends 5 to 8 us besides its instructions (777 x 4096 x 8192: 25 us).
 // What it took: instructions issued by a whole warp with one elected lane, so that descriptors stay in uniform registers (358 -> 313 us);
 // scales in four sets, loaded far ahead (267); arrivals that release nothing (243); results by TMA stores (235).
 #include "f8_tc.cuh"

@@ -8,25 +8,25 @@
 // weights; us, N x K, gated: 2 N x K):
 //                     rows:     1     8    16    32    64   128   256   512  1024  2048
 //   4096 x 4096       few     4.3   4.7   5.9   8.6  15.9
-//                     mid     6.1   6.2   6.3   6.5   7.1   8.1  11.0  15.0  18.2
-//                     many                          14.0  14.6  14.7  15.0  16.7  25.7
+//                     mid     6.0   6.1   6.2   6.4   7.0   8.1  11.1  14.8  18.0
+//                     many                          12.3  12.9  12.9  13.6  16.4  25.3
 //   12288 x 4096      few    11.8  12.2  15.0  23.3
-//                     mid    10.4  10.5  10.7  10.9  11.8  13.9  19.2
-//                     many                          15.8  16.5  16.6  25.6  35.6  64.7
+//                     mid    11.0  11.0  11.1  11.2  11.7  13.7  19.3
+//                     many                          14.8  15.1  15.4  23.8  35.1  64.2
 //   4096 x 1024       few     3.2   3.3   3.3   3.5   5.8
-//                     mid     3.7   3.6   3.8   3.9   4.5   5.6   7.9  10.2
-//                     many                    6.8   6.8   7.2   7.2   7.5   8.4  12.1
+//                     mid     3.5   3.6   3.6   3.9   4.4   5.6   7.8   9.5
+//                     many                    5.9   6.0   6.2   6.2   6.7   8.2  11.9
 //   1024 x 1024       few     2.1   2.2   2.2   2.5   2.6
-//                     mid     3.1   3.2   3.3   3.5   3.9
+//                     mid     3.0   3.1   3.1   3.3   3.8
 //   256 x 16384       few     7.7   8.5  11.3  19.4
-//                     mid     7.0   7.4   7.4   7.5
+//                     mid     6.0   6.2   6.3   6.7
 //   1024 x 4096       few     5.0   5.4   8.9  12.8
-//   gated             mid     4.8   4.9   5.2   5.8   7.7  10.3  11.1  11.9  16.1
+//   gated             mid     4.5   4.6   4.8   5.5   7.0   9.8  10.4  11.6  15.6
 //                     many                          14.4  14.8  14.8  15.2  15.8  17.4
 //   512 x 1024        few     2.9   3.0   3.8   5.8
-//   gated             mid     3.4   3.6   3.8   4.4
+//   gated             mid     3.4   3.6   3.8   4.3
 //   12288 x 4096      few    24.9  25.2  36.6  57.5
-//   gated             mid    18.2  18.3  18.7  19.6  21.8  25.7  47.0
+//   gated             mid    18.6  18.8  19.2  20.0  22.2  26.1  46.9
 //                     many                          28.4  28.7  29.3  38.5  67.3   121
 #include <algorithm>
 
@@ -60,7 +60,7 @@ static double mid_us(const F8Prod& p, bool gated, double weights, int sms) {
 static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
   const int pairs = std::max(1, sms / 2), wide = gated ? 256 : f8_many_wide(p, pairs);
   const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : wide);
-  return 5.4 + std::max((0.14 + 0.00055 * wide) * f8_blocks(p.K) * ceil_div(tiles, pairs), weights / 4.4);
+  return 5.4 + std::max((0.14 + 0.00055 * wide) * f8_blocks(p.K) * ceil_div(tiles, pairs), weights / (gated ? 4.4 : 4.8));
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
