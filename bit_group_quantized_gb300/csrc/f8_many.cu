@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 // Rows of W a tile (not gated) for so many pairs of CTAs: fewer where that keeps more of them busy. A block of a tile takes what its
 // operands' bytes take to an SM, 62 a cycle (264 + 1.03 cycles a row; the instructions take 2 a row), and a tile 2000 cycles besides.
 // Measured: 512 x 12288 x 4096 24.2 us with 192, 25.4 with 256; 512 x 4096 x 4096 13.5 with 128, 14.9 with 256; where 224 would give 6 %,
-// it gives 2 or takes 3 (777 x 4096 x 8192: 24.9 and 25.3; 2048 x 4096 x 1024: 12.3 and 11.9), so no change for less than a twelfth.
+// it gives 2 or takes 3 (777 x 4096 x 8192: 24.9 and 25.3; 2048 x 4096 x 1024: 12.3 and 11.9; x is then read more often), so no change for less
+// than a twelfth.
 int f8_many_wide(const F8Prod& p, int pairs) {
   const int64_t down = (p.M + kManyRows - 1) / kManyRows, blocks = f8_blocks(p.K);
   int best = kManyCols;
