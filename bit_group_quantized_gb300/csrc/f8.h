@@ -37,7 +37,12 @@ cudaError_t launch_rmsnorm_f8(float* h, const void* delta, bool delta_f32, const
                               const bgq_f8matrix& m, uint16_t* a, cudaStream_t s);
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s);
-cudaError_t launch_f8_mid(const F8Prod& p, bool gated, cudaStream_t s);
+struct F8MidPlan {
+  int down, rows, split;  // tiles of x's rows, of so many each; CTAs that share a tile's columns
+  double us;
+};
+F8MidPlan f8_mid_plan(const F8Prod& p, bool gated, int sms);
+cudaError_t launch_f8_mid(const F8Prod& p, bool gated, const F8MidPlan& plan, cudaStream_t s);
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s);
 int f8_many_wide(const F8Prod& p, int pairs);
 

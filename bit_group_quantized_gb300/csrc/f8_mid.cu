@@ -305,8 +305,8 @@ static int mid_clusters(const void* kern, size_t smem, int n, std::atomic<int> (
 }
 
 template <bool GATED, int DEEP>
-static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s) {
-  const int tiles = (p.N + 127) / 128, blocks = f8_blocks(p.K), stage = DEEP * mid_block<GATED>(sh.rows);
+static cudaError_t mid_of(const F8Prod& p, const F8MidPlan& plan, MidShape sh, cudaStream_t s) {
+  const int tiles = (p.N + 127) / 128, stage = DEEP * mid_block<GATED>(sh.rows);
   sh.stages = std::min(kMidRing / stage, kMidMaxStages);
   const uint32_t cols = (GATED ? 2 : 1) * sh.rows + 16 * kMidSets;
   for (sh.tmem = 32; sh.tmem < cols;) sh.tmem <<= 1;
@@ -317,17 +317,17 @@ static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s
   static std::atomic<uint64_t> known;
   const cudaError_t e = f8_room(kern, 1024 + kMidRing, known);
   if (e != cudaSuccess) return e;
-  // the most CTAs a tile for which all are there at once, each with two blocks of columns at least
+  // as many CTAs a tile as planned, if all are there at once
   static std::atomic<int> clusters[64][4];
-  int n = 3;
-  while (n > 0 && (2 << n > blocks || tiles * down > mid_clusters(kern, 1024 + kMidRing, n, clusters))) --n;
+  int n = __builtin_ctz(plan.split);
+  while (n > 0 && tiles * plan.down > mid_clusters(kern, 1024 + kMidRing, n, clusters)) --n;
   sh.split = 1 << n;
   CUtensorMap mx, mw[2];
   if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride, sh.rows)) return cudaErrorInvalidValue;
   for (int i = 0; i < 2; ++i)
     if (!f8_map(&mw[i], p.w[i], p.N, p.K, p.w_stride[i])) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * sh.split, down);
+  cfg.gridDim = dim3(tiles * sh.split, plan.down);
   cfg.blockDim = dim3(kMidThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -342,15 +342,38 @@ static cudaError_t mid_of(const F8Prod& p, int down, MidShape sh, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, k_f8_mid<GATED, DEEP>, mx, mw[0], mw[1], p, sh);
 }
 
-template <bool GATED>
-static cudaError_t mid(const F8Prod& p, cudaStream_t s) {
-  constexpr int kMost = GATED ? 128 : 256;
-  MidShape sh = {};
-  const int down = (p.M + kMost - 1) / kMost;
-  sh.rows = ((p.M + down - 1) / down + 15) / 16 * 16;
-  return 6 * mid_block<GATED>(sh.rows) <= kMidRing ? mid_of<GATED, 2>(p, down, sh, s) : mid_of<GATED, 1>(p, down, sh, s);
+// How x's rows are cut into tiles and columns into shares, and the microseconds that it takes by the estimate that fits what was measured
+// (f8_product.cu): a CTA's blocks of 128 columns one after the other, or W's bytes, and the shares' sums; more than 14 clusters of eight
+// are not all there at once. Few tiles of W leave SMs idle with all rows in one tile of x; cut in several, W is read again, from L2, and
+// the sums are shorter (256 x 4096 x 1024: 4.9 us in four tiles, 7.7 in one; gated 128 x 2 * 1024 x 4096: 7.2 in four, 9.8).
+F8MidPlan f8_mid_plan(const F8Prod& p, bool gated, int sms) {
+  const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
+  const int blocks = f8_blocks(p.K), across = ceil_div(p.N, 128), least = ceil_div(p.M, gated ? 128 : 256);
+  const double weights = (double)p.N * p.K * (gated ? 2e-6 : 1e-6);
+  F8MidPlan best = {};
+  for (int down = least; down <= 8 * least && (down == least || 16 * (down - 1) < p.M); ++down) {
+    F8MidPlan q = {};
+    q.down = down;
+    q.rows = ceil_div(ceil_div(p.M, down), 16) * 16;
+    for (q.split = 8; q.split > 1 && (2 * q.split > blocks || across * down * q.split > sms * 7 / 8);) q.split >>= 1;
+    const double block = gated ? 0.46 + 0.0021 * q.rows : 0.22 + 0.00105 * q.rows;
+    const double waves = ceil_div(across * down * q.split, sms);
+    q.us = 3.1 + std::max(waves * ceil_div(blocks, q.split) * block, weights / 6.5) + q.rows * (q.split == 1 ? 0.006 : gated ? 0.029 : 0.0137) +
+           (q.split == 8 && across * down > 14 ? 1 : 0);
+    if (down == least || q.us < best.us) best = q;
+  }
+  return best;
 }
 
-cudaError_t launch_f8_mid(const F8Prod& p, bool gated, cudaStream_t s) { return gated ? mid<true>(p, s) : mid<false>(p, s); }
+template <bool GATED>
+static cudaError_t mid(const F8Prod& p, const F8MidPlan& plan, cudaStream_t s) {
+  MidShape sh = {};
+  sh.rows = plan.rows;
+  return 6 * mid_block<GATED>(sh.rows) <= kMidRing ? mid_of<GATED, 2>(p, plan, sh, s) : mid_of<GATED, 1>(p, plan, sh, s);
+}
+
+cudaError_t launch_f8_mid(const F8Prod& p, bool gated, const F8MidPlan& plan, cudaStream_t s) {
+  return gated ? mid<true>(p, plan, s) : mid<false>(p, plan, s);
+}
 
 }  // namespace bgq
