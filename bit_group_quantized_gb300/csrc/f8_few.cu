@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_f8_few(const F8Prod p) {
   __shared__ __align__(16) float part[kFewWarps][R][T][kFewPitch];
   __shared__ uint32_t most[T];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * T;
+  const int n0 = blockIdx.x * 16;
   const int blocks = f8_blocks(p.K);
   // W into L2 while the kernel before this one ends (L2 holds whatever is written there in the meantime)
 #pragma unroll
@@ -81,13 +81,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_f8_few(const F8Prod p) {
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int col = c0 + half * 64, row = m0 + 8 * j + g;
+          const int col = c0 + half * 64, row = 8 * j + g;
           x[k][j][half] = make_uint4(0, 0, 0, 0);
           if (row < p.M && col < p.K) x[k][j][half] = *reinterpret_cast<const uint4*>(p.x + row * p.x_stride + col);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int row = m0 + 8 * j + 2 * t + i;
+          const int row = 8 * j + 2 * t + i;
           ex[k][j][i] = there && row < p.M ? p.xs[row * p.xs_stride + kb] : 0;
         }
       }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_f8_few(const F8Prod p) {
       for (int w = 1; w < kFewWarps; ++w) s[r] += part[w][r][b][n];
     }
     out[e] = GATED ? f8_swiglu(s[0], s[R - 1]) : s[0];
-    const int row = m0 + b;
+    const int row = b;
     if (row >= p.M || n0 + n >= p.N) continue;
     if (p.y) p.y[row * p.y_stride + n0 + n] = f2bf(out[e]);
     if (p.yf) p.yf[row * p.y_stride + n0 + n] = out[e];
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_f8_few(const F8Prod p) {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int b = (tid >> 4) + 16 * e, row = m0 + b;
+    const int b = (tid >> 4) + 16 * e, row = b;
     const bool fine = f8_finite(top[e]);
     const int byte = fine ? f8_scale_byte(top[e]) : kF8One;
     const uint32_t code = fine ? f8_codes4(out[e] * f8_inverse(byte), 0.f, 0.f, 0.f) & 0xffu : kF8Nan4 & 0xffu;
@@ -187,7 +187,7 @@ static cudaError_t few(const F8Prod& p, cudaStream_t s) {
   const int tiles = (p.N + 15) / 16;
   const bool cluster = GATED && p.h;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster ? (tiles + kFewCluster - 1) / kFewCluster * kFewCluster : tiles, (p.M + 8 * NT - 1) / (8 * NT));
+  cfg.gridDim = dim3(cluster ? (tiles + kFewCluster - 1) / kFewCluster * kFewCluster : tiles);
   cfg.blockDim = dim3(kFewThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -201,30 +201,12 @@ static cudaError_t few(const F8Prod& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_f8_few<NT, GATED>, p);
 }
 
+// At most 32 rows of x.
 cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s) {
-  // a launch's grid has at most 65535 groups of rows of x
-  constexpr int kMost = 65535 * 32;
-  F8Prod part = p;
-  for (int m0 = 0; m0 < p.M; m0 += kMost) {
-    part.M = p.M - m0 < kMost ? p.M - m0 : kMost;
-    part.x = p.x + m0 * p.x_stride;
-    part.xs = p.xs + m0 * p.xs_stride;
-    if (p.y) part.y = p.y + m0 * p.y_stride;
-    if (p.yf) part.yf = p.yf + m0 * p.y_stride;
-    if (p.h) {
-      part.h = p.h + m0 * p.h_stride;
-      part.hs = p.hs + m0 * p.hs_stride;
-    }
-    cudaError_t e;
-    if (part.M <= 8)
-      e = gated ? few<1, true>(part, s) : few<1, false>(part, s);
-    else if (part.M <= 16)
-      e = gated ? few<2, true>(part, s) : few<2, false>(part, s);
-    else
-      e = gated ? few<4, true>(part, s) : few<4, false>(part, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  if (p.M <= 8) return gated ? few<1, true>(p, s) : few<1, false>(p, s);
+  if (p.M <= 16) return gated ? few<2, true>(p, s) : few<2, false>(p, s);
+  if (p.M <= 32) return gated ? few<4, true>(p, s) : few<4, false>(p, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace bgq

@@ -53,7 +53,6 @@ static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
-  if (p.K < kF8Block) return launch_f8_few(p, gated, s);  // the tensor maps' boxes are a block of columns wide
   if (p.M > 2048) return launch_f8_many(p, gated, s);
   const double weights = (double)p.N * p.K * (gated ? 2e-6 : 1e-6);
   const int sms = num_sms();

@@ -168,7 +168,8 @@ def check_gemm(dev, m, n, k, seed=0, pads=None, **scales):
 
 SIZES = [(1, 16, 16), (1, 1, 128), (1, 128, 144), (2, 17, 256), (8, 130, 512), (9, 300, 640), (16, 144, 1040), (17, 256, 384), (31, 257, 1024),
          (33, 128, 4096), (64, 1000, 2064), (65, 96, 128), (127, 272, 272), (128, 128, 128), (129, 129, 144), (200, 512, 1536), (255, 384, 4112),
-         (257, 520, 1168), (300, 1000, 640), (513, 260, 144), (700, 1296, 2048), (1025, 777, 16), (2600, 2064, 528), (4100, 5003, 128), (2100, 16, 256), (2050, 1, 128), (40, 3, 128)]
+         (257, 520, 1168), (300, 1000, 640), (513, 260, 144), (700, 1296, 2048), (1025, 777, 16), (2600, 2064, 528), (4100, 5003, 128), (2100, 16, 256), (2050, 1, 128), (40, 3, 128), (40, 100, 16), (300, 260, 112),
+         (2100, 700, 64)]
 # tiles of 192 (one and three of a pair of CTAs), 160 and 128 rows of W
 NARROW = [(2100, 1187, 2064), (4600, 2300, 2064), (2100, 2301, 640), (2100, 1000, 2064)]
 

@@ -291,8 +291,8 @@ def test_rows_beyond_32_bits(cuda_device, m):
     assert torch.equal(H.q.contiguous().view(U8), h.q.view(U8)) and np.array_equal(byts(H.scale), byts(h.scale))
 
 
-def test_more_rows_than_a_launch_has(cuda_device):
-    """Narrow matrices take the kernel for few rows, 32 rows a time: a launch has 65535 of those."""
+def test_two_million_narrow_rows(cuda_device):
+    """Rows counted beyond 16 bits of everything, 16 columns each."""
     dev, m, k, n = cuda_device, 65535 * 32 + 37, 16, 16
     W, w = random_matrix(dev, np.random.default_rng(1), n, k, 128)
     q = torch.randint(0, 127, (m, k), dtype=U8, device=dev, generator=torch.Generator(device=dev).manual_seed(2))
