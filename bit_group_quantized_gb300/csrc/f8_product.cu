@@ -49,11 +49,11 @@ static double few_us(const F8Prod& p, bool gated, double weights) {
 static double many_us(const F8Prod& p, bool gated, double weights, int sms) {
   const int pairs = std::max(1, sms / 2), wide = gated ? 256 : f8_many_wide(p, pairs);
   const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, gated ? 128 : wide);
-  return 5.4 + std::max((0.14 + 0.00055 * wide) * f8_blocks(p.K) * ceil_div(tiles, pairs), weights / (gated ? 4.4 : 4.8));
+  const double tile = std::max((0.14 + 0.00055 * wide) * f8_blocks(p.K), gated ? 3.2 : 2.4);  // its instructions, or its results
+  return 5.4 + std::max(tile * ceil_div(tiles, pairs), weights / (gated ? 4.4 : 4.8));
 }
 
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s) {
-  if (p.M > 2048) return launch_f8_many(p, gated, s);
   const double weights = (double)p.N * p.K * (gated ? 2e-6 : 1e-6);
   const int sms = num_sms();
   const F8MidPlan mid = f8_mid_plan(p, gated, sms);
