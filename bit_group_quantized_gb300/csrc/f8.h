@@ -6,10 +6,10 @@
 #include <stdint.h>
 
 #include "../../include/bgq.h"
+#include "f8_rule.h"
 
 namespace bgq {
 
-constexpr int kF8Block = 128;  // columns that share one scale (of weights, rows too)
 __host__ __device__ inline int f8_blocks(int cols) { return (cols + kF8Block - 1) / kF8Block; }
 
 struct Ctrl;
@@ -37,14 +37,8 @@ cudaError_t launch_rmsnorm_f8(float* h, const void* delta, bool delta_f32, const
                               const bgq_f8matrix& m, uint16_t* a, cudaStream_t s);
 cudaError_t launch_f8_product(const F8Prod& p, bool gated, cudaStream_t s);
 cudaError_t launch_f8_few(const F8Prod& p, bool gated, cudaStream_t s);
-struct F8MidPlan {
-  int down, rows, split;  // tiles of x's rows, of so many each; CTAs that share a tile's columns
-  double us;
-};
-F8MidPlan f8_mid_plan(const F8Prod& p, bool gated, int sms);
 cudaError_t launch_f8_mid(const F8Prod& p, bool gated, const F8MidPlan& plan, cudaStream_t s);
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s);
-int f8_many_wide(const F8Prod& p, int pairs);
 
 #ifdef __CUDACC__
 // The scale byte of a block whose largest magnitude has these fp32 bits: the smallest power of two 2^(byte - 127) with

@@ -23,7 +23,6 @@ namespace bgq {
 
 constexpr int kManyThreads = 384;  // warp 0: copies, 1: instructions, 2: tensor memory, 4-7: scales, 8-11: results
 constexpr int kManyStages = 6, kManyStage = 2 * kF8Tile;
-constexpr int kManyRows = 256, kManyCols = 256;
 constexpr int kManySets = 4;                 // sets of scales, 16 columns apart: x's 4, then W's 8
 constexpr int kManyScales = 512 - 16 * kManySets;
 constexpr int kManyShared = 16 * kManySets;  // columns that both tiles' sums use
@@ -411,28 +410,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (warp == 2) f8_tmem_free<2>(tmem, 512);
 }
 
-// Rows of W a tile (not gated) for so many pairs of CTAs: fewer where that keeps more of them busy. A block of a tile takes what its
-// operands' bytes take to an SM, 62 a cycle (264 + 1.03 cycles a row; the instructions take 2 a row), and a tile 2000 cycles besides.
-// Measured: 512 x 12288 x 4096 24.2 us with 192, 25.4 with 256; 512 x 4096 x 4096 13.5 with 128, 14.9 with 256; where 224 would give 6 %,
-// it gives 2 or takes 3 (777 x 4096 x 8192: 24.9 and 25.3; 2048 x 4096 x 1024: 12.3 and 11.9; x is then read more often), so no change for less
-// than a twelfth.
-int f8_many_wide(const F8Prod& p, int pairs) {
-  const int64_t down = (p.M + kManyRows - 1) / kManyRows, blocks = f8_blocks(p.K);
-  int best = kManyCols;
-  int64_t least = INT64_MAX;
-  for (int wide = kManyCols; wide >= 128; wide -= 32) {
-    const int64_t tiles = down * ((p.N + wide - 1) / wide), waves = (tiles + pairs - 1) / pairs;
-    const int64_t cost = waves * ((264 + 103 * wide / 100) * blocks + 2000);
-    if (cost < least - least / 12) {
-      best = wide;
-      least = cost;
-    }
-  }
-  return best;
-}
-
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {
-  const int pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1, wide = gated ? 128 : f8_many_wide(p, pairs);
+  const int pairs = num_sms() / 2 > 0 ? num_sms() / 2 : 1, wide = gated ? 128 : f8_many_wide({p.M, p.N, p.K, gated}, pairs);
   CUtensorMap mx, mw[2];
   if (!f8_map(&mx, p.x, p.M, p.K, p.x_stride)) return cudaErrorInvalidValue;
   for (int i = 0; i < (gated ? 2 : 1); ++i)

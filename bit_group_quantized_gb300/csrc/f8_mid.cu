@@ -13,7 +13,6 @@
 // 4096: 7.2 to 7.7). Half the shared memory, so that the next launch's CTAs start beside this one's, gave nothing (12.0 us for 11.5), nor did asking
 // W into L2 ahead of the wait for the kernel before.
 #include <algorithm>
-#include <initializer_list>
 
 #include "f8_tc.cuh"
 
@@ -341,31 +340,6 @@ static cudaError_t mid_of(const F8Prod& p, const F8MidPlan& plan, MidShape sh, c
   cfg.attrs = at;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k_f8_mid<GATED, DEEP>, mx, mw[0], mw[1], p, sh);
-}
-
-// How x's rows are cut into tiles and columns into shares, and the microseconds that it takes by the estimate that fits what was measured
-// (f8_product.cu): a CTA's blocks of 128 columns one after the other, or W's bytes, the shares' sums, 4 us for every wave of CTAs behind
-// the first; more than 14 clusters of eight are not all there at once. Few tiles of W leave SMs idle with all rows in one tile of x; cut in several, W is read again, from L2, and
-// the sums are shorter (256 x 4096 x 1024: 4.9 us in four tiles, 7.7 in one; gated 128 x 2 * 1024 x 4096: 7.2 in four, 9.8).
-F8MidPlan f8_mid_plan(const F8Prod& p, bool gated, int sms) {
-  const auto ceil_div = [](int a, int b) { return (a + b - 1) / b; };
-  const int blocks = f8_blocks(p.K), across = ceil_div(p.N, 128), least = ceil_div(p.M, gated ? 128 : 256);
-  const double weights = (double)p.N * p.K * (gated ? 2e-6 : 1e-6);
-  F8MidPlan best = {};
-  for (int times : {1, 2, 3, 4, 6, 8}) {
-    const int down = times * least;
-    if (times > 1 && (16 * (down - 1) >= p.M || p.M > 2048)) break;
-    F8MidPlan q = {};
-    q.down = down;
-    q.rows = ceil_div(ceil_div(p.M, down), 16) * 16;
-    for (q.split = 8; q.split > 1 && (2 * q.split > blocks || across * down * q.split > sms * 7 / 8);) q.split >>= 1;
-    const double block = gated ? 0.46 + 0.0021 * q.rows : 0.22 + 0.00105 * q.rows;
-    const double waves = ceil_div(across * down * q.split, sms);
-    q.us = 3.1 + 4 * (waves - 1) + std::max(waves * ceil_div(blocks, q.split) * block, weights / 6.5) + q.rows * (q.split == 1 ? 0.006 : gated ? 0.029 : 0.0137) +
-           (q.split == 8 && across * down > 14 ? 1 : 0);
-    if (times == 1 || q.us < best.us) best = q;
-  }
-  return best;
 }
 
 template <bool GATED>
