@@ -64,12 +64,32 @@ __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d
 constexpr uint32_t kF8Nan4 = 0x7f7f7f7fu;  // four codes of NaN
 constexpr int kF8One = 127;                // the scale byte of 1
 
-// silu(g) * u. The exponential's and the reciprocal's approximations are 2^-21 off or so, the result has 8 bits or 4.
-__device__ __forceinline__ float f8_swiglu(float g, float u) {
+// silu(g) * u for g >= kF8Far, or NaN. __expf is off by 2 + 1.2 |g| units of 2^-23 (at -64 some 2^-17), the reciprocal by one;
+// the result has 8 bits or 4. At -64 the exponential is 2^92.
+constexpr float kF8Far = -64.f;
+__device__ __forceinline__ float f8_swiglu_near(float g, float u) {
   float r;
-  // (not its flushing form: near g = -88 the reciprocal is subnormal, and u may be large)
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
   return g * r * u;
+}
+// For g < kF8Far, where 1 + exp(-g) is exp(-g) to fp32's last place: g exp(g) u, which u may bring back from far below fp32's range
+// (exp(-g) passes its other end at -88.7). A quarter of the exponent at a time: no factor is subnormal down to g = -349, where the
+// result is below fp32's range whatever u is, and each is less than one, so that nothing on the way is smaller than the result.
+__device__ __forceinline__ float f8_swiglu_far(float g, float u) {
+  const float t = expf(0.25f * g);
+  return u * t * t * t * (g * t);
+}
+__device__ __forceinline__ float f8_swiglu(float g, float u) {
+  float r = f8_swiglu_near(g, u);
+  if (g < kF8Far) r = f8_swiglu_far(g, u);
+  return r;
+}
+// Four of them with one branch, far gates being rare (a branch each: gated 64 x 2 * 1024 x 4096 took 6.9 us for 6.7).
+__device__ __forceinline__ float4 f8_swiglu4(float4 g, float4 u) {
+  float4 r = make_float4(f8_swiglu_near(g.x, u.x), f8_swiglu_near(g.y, u.y), f8_swiglu_near(g.z, u.z), f8_swiglu_near(g.w, u.w));
+  if (fminf(fminf(g.x, g.y), fminf(g.z, g.w)) < kF8Far)
+    r = make_float4(f8_swiglu(g.x, u.x), f8_swiglu(g.y, u.y), f8_swiglu(g.z, u.z), f8_swiglu(g.w, u.w));
+  return r;
 }
 #endif
 

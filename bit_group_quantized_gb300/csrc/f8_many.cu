@@ -337,14 +337,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       } else {
         // columns 64 c .. of the result, c = 1, 0 or 0, 1
         float h[2][2][32];
-        uint32_t top = 0;
+        float most = 0.f;
         auto column = [&](int c) { return 64 * (back ? 1 - c : c); };
         auto join = [&](float (&g)[32], const float (&u)[32]) {
+          float least = g[0];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            g[j] = f8_swiglu(g[j], u[j]);
-            top = max(top, __float_as_uint(g[j]) & 0x7fffffffu);
+          for (int j = 1; j < 31; j += 2) least = f8_min3(least, g[j], g[j + 1]);
+          if (__any_sync(kFull, fminf(least, g[31]) < kF8Far)) {  // one branch for all 32 columns of the warp: far gates are rare
+#pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] = g[j] < kF8Far ? f8_swiglu_far(g[j], u[j]) : f8_swiglu_near(g[j], u[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] = f8_swiglu_near(g[j], u[j]);
           }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) most = f8_most3(most, g[j], g[j + 1]);
         };
         // the shared columns are the second half of up's sums, or the first of gate's
         float u[2][32];
@@ -375,6 +382,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) store64(h[c][0], h[c][1], tn * 128 + column(c), row);
         if (p.h) {
+          const uint32_t top = __float_as_uint(most);
           const bool fine = f8_finite(top);
           const int byte = fine ? f8_scale_byte(top) : kF8One;
           const float inv = f8_inverse(byte);

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       g = *reinterpret_cast<const float4*>(sums + r * 128 + lane * 4);
       if (GATED) u = *reinterpret_cast<const float4*>(sums + (sh.rows + r) * 128 + lane * 4);
     }
-    if (GATED) g = make_float4(f8_swiglu(g.x, u.x), f8_swiglu(g.y, u.y), f8_swiglu(g.z, u.z), f8_swiglu(g.w, u.w));
+    if (GATED) g = f8_swiglu4(g, u);
     const int64_t row = m0 + r;
     const int n = n0 + lane * 4, left = p.N - n;
     if (p.y && left > 0) {

@@ -216,6 +216,17 @@ __device__ __forceinline__ void f8_store_rows(unsigned char* room, const uint4 (
   }
 }
 __device__ __forceinline__ void f8_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// The least of three (a NaN only if all are), and the largest magnitude of three (a NaN if one is).
+__device__ __forceinline__ float f8_min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float f8_most3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint4 f8_bf16x8(const float* v) {
   uint32_t w[4];
 #pragma unroll
