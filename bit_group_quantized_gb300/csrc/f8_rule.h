@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <limits>
 
 namespace bgq {
 
@@ -46,6 +47,7 @@ struct F8Size {
 };
 
 inline int f8_ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline int64_t f8_ceil_div(int64_t a, int b) { return (a + b - 1) / b; }
 inline double f8_weights(const F8Size& s) { return (double)s.N * s.K * (s.gated ? 2e-6 : 1e-6); }  // millions of bytes
 
 // ----------------------------------------------------------------- few rows
@@ -62,13 +64,15 @@ struct F8MidPlan {
   int down, rows, split;  // tiles of x's rows, of so many each; CTAs that share a tile's columns
   double us;
 };
+constexpr int kMidMaxDown = 65535;  // a tile of x's rows is a grid's y
 
 // How x's rows are cut into tiles and columns into shares, and the microseconds that it takes by the estimate that fits what was
 // measured: a CTA's blocks of 128 columns one after the other, or W's bytes, the shares' sums, 4 us for every wave of CTAs behind
 // the first; more than 14 clusters of eight are not all there at once. Few tiles of W leave SMs idle with all rows in one tile of x; cut in several, W is read again, from L2, and
 // the sums are shorter (256 x 4096 x 1024: 4.9 us in four tiles, 7.7 in one; gated 128 x 2 * 1024 x 4096: 7.2 in four, 9.8).
 inline F8MidPlan f8_mid_plan(const F8Size& s, int sms) {
-  const int blocks = f8_ceil_div(s.K, kF8Block), across = f8_ceil_div(s.N, 128), least = f8_ceil_div(s.M, s.gated ? 128 : 256);
+  const int blocks = f8_ceil_div(s.K, kF8Block), least = f8_ceil_div(s.M, s.gated ? 128 : 256);
+  const int64_t across = f8_ceil_div(s.N, 128);
   F8MidPlan best = {};
   for (int times : {1, 2, 3, 4, 6, 8}) {
     const int down = times * least;
@@ -78,9 +82,10 @@ inline F8MidPlan f8_mid_plan(const F8Size& s, int sms) {
     q.rows = f8_ceil_div(f8_ceil_div(s.M, down), 16) * 16;
     for (q.split = 8; q.split > 1 && (2 * q.split > blocks || across * down * q.split > sms * 7 / 8);) q.split >>= 1;
     const double block = s.gated ? 0.46 + 0.0021 * q.rows : 0.22 + 0.00105 * q.rows;
-    const double waves = f8_ceil_div(across * down * q.split, sms);
+    const double waves = (double)f8_ceil_div(across * down * q.split, sms);
     q.us = 3.1 + 4 * (waves - 1) + std::max(waves * f8_ceil_div(blocks, q.split) * block, f8_weights(s) / 6.5) +
            q.rows * (q.split == 1 ? 0.006 : s.gated ? 0.029 : 0.0137) + (q.split == 8 && across * down > 14 ? 1 : 0);
+    if (down > kMidMaxDown) q.us = std::numeric_limits<double>::infinity();  // cannot be launched
     if (times == 1 || q.us < best.us) best = q;
   }
   return best;
@@ -112,10 +117,10 @@ inline int f8_many_wide(const F8Size& s, int pairs) {
 // Microseconds: a pair of CTAs' tiles one after the other, or W's bytes.
 inline double f8_many_us(const F8Size& s, int sms) {
   const int pairs = std::max(1, sms / 2), wide = s.gated ? 256 : f8_many_wide(s, pairs);
-  const int tiles = f8_ceil_div(s.M, kManyRows) * f8_ceil_div(s.N, s.gated ? 128 : wide);
+  const int64_t tiles = (int64_t)f8_ceil_div(s.M, kManyRows) * f8_ceil_div(s.N, s.gated ? 128 : wide);
   // its instructions, or its results
   const double tile = std::max((0.14 + 0.00055 * wide) * f8_ceil_div(s.K, kF8Block), s.gated ? 3.2 : 2.4);
-  return 5.4 + std::max(tile * f8_ceil_div(tiles, pairs), f8_weights(s) / (s.gated ? 4.4 : 4.8));
+  return 5.4 + std::max(tile * (double)f8_ceil_div(tiles, pairs), f8_weights(s) / (s.gated ? 4.4 : 4.8));
 }
 
 // ------------------------------------------------------------------- choice

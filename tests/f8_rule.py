@@ -34,7 +34,7 @@ def _lib():
     src, out = os.path.join(at, "rule.cpp"), os.path.join(at, "rule.so")
     with open(src, "w") as f:
         f.write(SOURCE)
-    subprocess.run([cxx, "-O2", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, src, "-o", out], check=True)
+    subprocess.run([cxx, "-O2", "-std=c++17", "-Wall", "-Werror", "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error", "-shared", "-fPIC", "-I", CSRC, src, "-o", out], check=True)
     lib = C.CDLL(out)
     shutil.rmtree(at)
     return lib

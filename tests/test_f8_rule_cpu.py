@@ -32,3 +32,19 @@ def test_few_rows_are_few():
         assert 16 <= c.rows <= (128 if gated else 256) and c.rows % 16 == 0 and c.split in (1, 2, 4, 8)
         assert c.rows * c.down >= m and 2 * c.split <= max(2, -(-k // 128))
         assert SMS == 152
+
+
+def test_every_size_has_a_kernel_that_can_launch():
+    """A grid's y ends at 65535 and a launch has fewer than 2^31 CTAs; the sizes are all that the entry points take, up to the most
+    rows, those among them whose results no memory holds."""
+    most = (1 << 24) - 1
+    ends = [(m, n, k, g) for m in (16776960, 16776961, most, 65535 * 128, 65535 * 128 + 1) for n in (1, 16, 128, 129, 1 << 20)
+            for k in (16, 128, 1024, 65536) for g in (False, True)]
+    for m, n, k, gated in ends + list(sizes(3000, 2)):
+        for sms in (SMS, 148, 132, 80):
+            c = Choice(m, n, k, gated, sms)
+            assert min(c.few_us, c.mid_us, c.many_us) > 0
+            if c.kernel == "mid":
+                assert 1 <= c.down <= 65535 and -(-n // 128) * c.split * c.down < 1 << 31, (m, n, k, gated)
+    # 65536 tiles of 256 rows
+    assert kernel(16776961, 128, 128) == "many" and kernel(16776960, 128, 128) == "mid"
