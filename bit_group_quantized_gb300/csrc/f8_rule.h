@@ -75,17 +75,16 @@ inline F8MidPlan f8_mid_plan(const F8Size& s, int sms) {
   const int64_t across = f8_ceil_div(s.N, 128);
   F8MidPlan best = {};
   for (int times : {1, 2, 3, 4, 6, 8}) {
-    const int down = times * least;
-    if (times > 1 && (16 * (down - 1) >= s.M || s.M > 2048)) break;
+    if (times > 1 && (16 * (times * least - 1) >= s.M || s.M > 2048)) break;
     F8MidPlan q = {};
-    q.down = down;
-    q.rows = f8_ceil_div(f8_ceil_div(s.M, down), 16) * 16;
-    for (q.split = 8; q.split > 1 && (2 * q.split > blocks || across * down * q.split > sms * 7 / 8);) q.split >>= 1;
+    q.rows = f8_ceil_div(f8_ceil_div(s.M, times * least), 16) * 16;
+    q.down = f8_ceil_div(s.M, q.rows);  // fewer than asked for where the rows of a tile were rounded up
+    for (q.split = 8; q.split > 1 && (2 * q.split > blocks || across * q.down * q.split > sms * 7 / 8);) q.split >>= 1;
     const double block = s.gated ? 0.46 + 0.0021 * q.rows : 0.22 + 0.00105 * q.rows;
-    const double waves = (double)f8_ceil_div(across * down * q.split, sms);
+    const double waves = (double)f8_ceil_div(across * q.down * q.split, sms);
     q.us = 3.1 + 4 * (waves - 1) + std::max(waves * f8_ceil_div(blocks, q.split) * block, f8_weights(s) / 6.5) +
-           q.rows * (q.split == 1 ? 0.006 : s.gated ? 0.029 : 0.0137) + (q.split == 8 && across * down > 14 ? 1 : 0);
-    if (down > kMidMaxDown) q.us = std::numeric_limits<double>::infinity();  // cannot be launched
+           q.rows * (q.split == 1 ? 0.006 : s.gated ? 0.029 : 0.0137) + (q.split == 8 && across * q.down > 14 ? 1 : 0);
+    if (q.down > kMidMaxDown) q.us = std::numeric_limits<double>::infinity();  // cannot be launched
     if (times == 1 || q.us < best.us) best = q;
   }
   return best;

@@ -48,3 +48,15 @@ def test_every_size_has_a_kernel_that_can_launch():
                 assert 1 <= c.down <= 65535 and -(-n // 128) * c.split * c.down < 1 << 31, (m, n, k, gated)
     # 65536 tiles of 256 rows
     assert kernel(16776961, 128, 128) == "many" and kernel(16776960, 128, 128) == "mid"
+
+
+def test_no_tile_without_rows():
+    """Tiles of x's rows as many as hold some; the tiles' rows are rounded up to 16 after x is cut."""
+    for m, n, k, gated in [(1078, 128, 4096, False), (1063, 128, 4096, True), (864, 512, 1024, False)]:
+        c = Choice(m, n, k, gated)
+        assert c.kernel == "mid" and (c.down - 1) * c.rows < m <= c.down * c.rows
+    for gated in (False, True):
+        for n, k in ((128, 128), (128, 4096), (512, 1024), (1040, 2064), (4096, 4096)):
+            for m in range(1, 2100):
+                c = Choice(m, n, k, gated)
+                assert (c.down - 1) * c.rows < m <= c.down * c.rows, (m, n, k, gated)
