@@ -2,10 +2,9 @@
 // checks, then the launches of f8_quant.cu and f8_product.cu.
 #include <math.h>
 
-#include <initializer_list>
-
 #include "f8.h"
 #include "kernels.h"
+#include "overlap.h"
 
 using namespace bgq;
 
@@ -45,6 +44,13 @@ int check_out(const void* y, int64_t stride, int64_t width) {
   return BGQ_OK;
 }
 
+// What a call reads and writes of a matrix, and of `size` bytes a value elsewhere.
+Rows codes(const bgq_f8matrix& m) { return {m.q, m.rows, m.cols, m.q_stride}; }
+Rows scales(const bgq_f8matrix& m) {
+  return {m.scale, ((int64_t)m.rows + m.block_rows - 1) / m.block_rows, f8_blocks(m.cols), m.scale_stride};
+}
+Rows values(const void* p, int64_t rows, int64_t width, int64_t stride, int size) { return {p, rows, width * size, stride * size}; }
+
 constexpr size_t kWsBytes = sizeof(Ctrl);
 
 F8Prod product(const bgq_f8matrix* W, const bgq_f8matrix* up, const bgq_f8matrix* x, uint16_t* y, float* yf,
@@ -81,6 +87,7 @@ int32_t bgq_f8_quantise(const uint16_t* x, int64_t x_stride, const bgq_f8matrix*
   if (!x || !al(x, 16) || x_stride < m->cols || x_stride % 8) return BGQ_ERR_INVALID_ARG;
   if (x_stride >= (int64_t)1 << 36) return BGQ_ERR_UNSUPPORTED;
   if (m->rows == 0) return BGQ_OK;
+  if (overlap({codes(*m), scales(*m)}, {values(x, m->rows, m->cols, x_stride, 2)})) return BGQ_ERR_INVALID_ARG;
   return cuda_status(launch_f8_quantise(x, x_stride, *m, st(stream)));
 }
 
@@ -90,8 +97,10 @@ int32_t bgq_rmsnorm_f8(float* h, const void* delta, int32_t delta_f32, const uin
   if (r) return r;
   if (!h || !al(h, 16) || !al(delta, 16) || !al(rho, 16) || !al(a, 16)) return BGQ_ERR_INVALID_ARG;
   if (batch != m->rows || d != m->cols || !(eps >= 0.f)) return BGQ_ERR_INVALID_ARG;
-  if (batch && (h == delta || h == (const void*)a || h == (const void*)m->q)) return BGQ_ERR_INVALID_ARG;
   if (batch == 0) return BGQ_OK;
+  if (overlap({values(h, batch, d, d, 4), codes(*m), scales(*m), values(a, batch, d, d, 2)},
+              {values(delta, batch, d, d, delta_f32 ? 4 : 2), values(rho, 1, d, d, 2)}))
+    return BGQ_ERR_INVALID_ARG;
   return cuda_status(launch_rmsnorm_f8(h, delta, delta_f32 != 0, rho, eps, *m, a, st(stream)));
 }
 
@@ -104,10 +113,11 @@ int32_t bgq_f8_gemm(const bgq_f8matrix* W, const bgq_f8matrix* x, uint16_t* y, f
   int r = check_product(W, x);
   if (r || (r = check_out(y, y_stride, W->rows)) || (r = check_out(y_f32, y_stride, W->rows))) return r;
   if (!y && !y_f32) return BGQ_ERR_INVALID_ARG;
-  for (const void* in : {(const void*)x->q, (const void*)x->scale, (const void*)W->q, (const void*)W->scale})
-    if (x->rows && (y == in || y_f32 == in)) return BGQ_ERR_INVALID_ARG;
   if (!ws || !al(ws, 256) || ws_bytes < kWsBytes) return BGQ_ERR_WORKSPACE;
   if (x->rows == 0) return BGQ_OK;
+  if (overlap({values(y, x->rows, W->rows, y_stride, 2), values(y_f32, x->rows, W->rows, y_stride, 4)},
+              {codes(*x), scales(*x), codes(*W), scales(*W)}))
+    return BGQ_ERR_INVALID_ARG;
   return cuda_status(launch_f8_product(product(W, nullptr, x, y, y_f32, y_stride, ws), false, st(stream)));
 }
 
@@ -118,11 +128,12 @@ int32_t bgq_f8_swiglu(const bgq_f8matrix* gate, const bgq_f8matrix* up, const bg
   if (gate->rows != up->rows || gate->rows % 16 || (!h && !y)) return BGQ_ERR_INVALID_ARG;
   if (h && (r = check_f8(h, 1))) return r;
   if (h && (h->rows != x->rows || h->cols != gate->rows)) return BGQ_ERR_INVALID_ARG;
-  for (const bgq_f8matrix* in : {gate, up, x})
-    if (x->rows && ((h && (h->q == in->q || h->scale == in->scale)) || y == (const void*)in->q || y == (const void*)in->scale))
-      return BGQ_ERR_INVALID_ARG;
   if (!ws || !al(ws, 256) || ws_bytes < kWsBytes) return BGQ_ERR_WORKSPACE;
   if (x->rows == 0) return BGQ_OK;
+  const Rows none = {};
+  if (overlap({values(y, x->rows, gate->rows, y_stride, 2), h ? codes(*h) : none, h ? scales(*h) : none},
+              {codes(*x), scales(*x), codes(*gate), scales(*gate), codes(*up), scales(*up)}))
+    return BGQ_ERR_INVALID_ARG;
   F8Prod p = product(gate, up, x, y, nullptr, y_stride, ws);
   if (h) {
     p.h = h->q;

@@ -474,7 +474,10 @@ int32_t bgq_kv4_attention(const bgq_kv4_cache* c, const bgq_kv4_seqs* s, const u
  * cols; scale 4-byte aligned, scale_stride a multiple of 4 and at least cols / 128 rounded up to one: four
  * scales are read at a time, so the last row too has that many bytes (what they hold does not matter).
  * Codes of NaN (0x7f, 0xff) make NaN of every sum that they enter; the scale byte 255 is not allowed. Unlike
- * other weights these may be written by the call just before on the same stream. */
+ * other weights these may be written by the call just before on the same stream.
+ * What one of the four calls below writes must share no byte with anything else that it reads or writes, its codes
+ * and scales included (BGQ_ERR_INVALID_ARG). Rows of one array may lie between the rows of another
+ * where both are the same number of bytes apart; arrays that alternate at other distances are refused too. */
 typedef struct bgq_f8matrix {
   uint8_t* q;
   uint8_t* scale;
@@ -494,7 +497,7 @@ int32_t bgq_f8_quantise(const uint16_t* x, int64_t x_stride, const bgq_f8matrix*
  * h: fp32 [batch][d], updated; delta (nullable): [batch][d], fp32 where delta_f32 != 0, else bf16;
  * rho (nullable => 1): bf16 [d]; m: batch x d with block_rows 1; a (nullable): bf16 [batch][d], for what
  * reads the same input in bf16 (a router). The sum of squares is fp32. d a multiple of 16, at most 65536;
- * batch may be 0. h, delta, rho and a 16-byte aligned; what is written (h, m, a) must overlap nothing else. */
+ * batch may be 0. h, delta, rho and a 16-byte aligned. */
 int32_t bgq_rmsnorm_f8(float* h, const void* delta, int32_t delta_f32, const uint16_t* rho, int32_t batch, int32_t d,
                        float eps, const bgq_f8matrix* m, uint16_t* a, void* stream);
 
@@ -502,7 +505,7 @@ int32_t bgq_rmsnorm_f8(float* h, const void* delta, int32_t delta_f32, const uin
  * y (bf16) and y_f32 (fp32), nullable but not both: [x->rows][W->rows], rows y_stride values apart (a multiple
  * of 8), 16-byte aligned. Products are exact and sums fp32 (each step of 32 columns is cut to fp32 where a tensor
  * core adds it). The same inputs give the same bits; a row's do not depend on what the other rows hold.
- * x->rows may be 0; W->rows at most 2^20. Results must overlap no input, nor each other.
+ * x->rows may be 0; W->rows at most 2^20.
  * ws: bgq_f8_gemm_workspace_bytes bytes, for the status word; calls may share it, at once too. */
 size_t bgq_f8_gemm_workspace_bytes(const bgq_f8matrix* W, const bgq_f8matrix* x);
 int32_t bgq_f8_gemm(const bgq_f8matrix* W, const bgq_f8matrix* x, uint16_t* y, float* y_f32, int64_t y_stride,
