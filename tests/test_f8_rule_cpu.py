@@ -1,10 +1,12 @@
 """The rule that chooses between the e4m3 products' kernels (csrc/f8_rule.h), compiled for the host."""
 
+import os
 import random
+import re
 
 import pytest
 
-from tests.f8_rule import SMS, Choice, kernel
+from tests.f8_rule import ROOT, SMS, Choice, kernel
 
 
 def sizes(n, seed, most_rows=1 << 24):
@@ -60,3 +62,12 @@ def test_no_tile_without_rows():
             for m in range(1, 2100):
                 c = Choice(m, n, k, gated)
                 assert (c.down - 1) * c.rows < m <= c.down * c.rows, (m, n, k, gated)
+
+
+def test_smoke_takes_each_kernel():
+    """The feed-forward block of the smoke test, 640 wide and 1040 inside, by all three kernels."""
+    text = open(os.path.join(ROOT, "__graft_entry__.py"), encoding="utf-8").read()
+    rows = [int(m) for m in re.search(r"for m in \(([\d, ]+)\):\n        h = torch.randn\(m, 640", text).group(1).split(",")]
+    assert "((1040, 640), (1040, 640), (640, 1040))" in text
+    assert [kernel(m, 1040, 640, True) for m in rows] == ["few", "mid", "many"]
+    assert [kernel(m, 640, 1040) for m in rows] == ["few", "mid", "many"]
