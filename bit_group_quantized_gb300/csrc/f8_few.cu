@@ -27,7 +27,8 @@ __device__ __forceinline__ void f8_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 2^e for -127 <= e <= 127 (2^-127 as 0: what it would scale is below fp32's range by then, see f8_scaled).
+// 2^e for -127 <= e <= 127. 2^-127 as 0: it is half of a scale of 2^-253 or 2^-254 then, and a block's sum, below 2^25, is far below
+// fp32's range behind it.
 __device__ __forceinline__ float f8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 __device__ __forceinline__ uint4 f8_ld_weights(const uint8_t* p) {

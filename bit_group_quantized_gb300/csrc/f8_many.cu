@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   };
   if (warp >= 4 && warp < 8) load(cur);
-  if (warp == 2) f8_tmem_alloc<2>(&s_tmem, 512);
+  if (warp == 2) f8_tmem_alloc(&s_tmem, 512);
   if (warp > 0) {  // warp 0 needs none of it
     tc_fence_before();
     asm volatile("bar.sync 1, 352;" ::: "memory");
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     __syncwarp();
   }
   f8_cluster_sync();
-  if (warp == 2) f8_tmem_free<2>(tmem, 512);
+  if (warp == 2) f8_tmem_free(tmem, 512);
 }
 
 cudaError_t launch_f8_many(const F8Prod& p, bool gated, cudaStream_t s) {

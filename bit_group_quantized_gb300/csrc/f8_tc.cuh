@@ -81,21 +81,13 @@ __device__ __forceinline__ void f8_map_ahead(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-template <int CG>
+// Tensor memory of both CTAs of a pair, by one whole warp of each (of a single CTA: tc.cuh).
 __device__ __forceinline__ void f8_tmem_alloc(uint32_t* slot, uint32_t cols) {
-  if (CG == 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(slot)), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    tmem_alloc(slot, cols);
-  }
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(slot)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-template <int CG>
 __device__ __forceinline__ void f8_tmem_free(uint32_t at, uint32_t cols) {
-  if (CG == 2)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
-  else
-    tmem_free(at, cols);
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
 }
 // Issued by the lane that has `lead`; the whole warp runs the code around them, so that addresses and descriptors stay
 // in uniform registers.
