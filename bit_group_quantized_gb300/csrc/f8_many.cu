@@ -11,9 +11,9 @@
 // instructions wait for them alone.
 //
 // What bounds it: the matrix instructions, 128 cycles for 256 x 256 x 32, beside them the operands' bytes (64 KB a pair in 512 cycles, where an
-// SM takes 62 bytes a cycle), and the power that all of it draws. 8191 x 12288 x 4096: 226 to 238 us, 3.5 PFLOP/s, 373k cycles of which the
+// SM takes 62 bytes a cycle), and the power that all of it draws. 8191 x 12288 x 4096: 226 to 244 us, 3.5 PFLOP/s, 373k cycles of which the
 // instructions take 344k, at 1.6 GHz where the SMs could run at 2.07; the rest is the wait between tiles (1800 cycles for the last
-// instructions and the shared columns). Gated 4095 x 2 * 12288 x 4096: 238 to 264 us. For seconds on end (1.4 kW): 267 and 273 us.
+// instructions and the shared columns). Gated 4095 x 2 * 12288 x 4096: 238 to 264 us. For seconds on end (1.4 kW): 267 and 271 to 283 us.
 // A launch of one tile a pair spends 5 to 8 us besides its instructions (777 x 4096 x 8192: 25 us).
 // What it took: instructions issued by a whole warp with one elected lane, so that descriptors stay in uniform registers (358 -> 313 us);
 // scales in four sets, loaded far ahead (267); arrivals that release nothing (243); results by TMA stores (235).
@@ -339,19 +339,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         float h[2][2][32];
         float most = 0.f;
         auto column = [&](int c) { return 64 * (back ? 1 - c : c); };
-        auto join = [&](float (&g)[32], const float (&u)[32]) {
-          float least = g[0];
+        auto join = [&](auto& g, auto& u) {  // 32 columns, or 16
+          constexpr int n = sizeof(g) / sizeof(float);
+          float least = fminf(g[0], g[1]);
 #pragma unroll
-          for (int j = 1; j < 31; j += 2) least = f8_min3(least, g[j], g[j + 1]);
-          if (__any_sync(kFull, fminf(least, g[31]) < kF8Far)) {  // one branch for all 32 columns of the warp: far gates are rare
+          for (int j = 2; j < n; j += 2) least = f8_min3(least, g[j], g[j + 1]);
+          if (__any_sync(kFull, least < kF8Far)) {  // one branch for all of the warp: far gates are rare
 #pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = g[j] < kF8Far ? f8_swiglu_far(g[j], u[j]) : f8_swiglu_near(g[j], u[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = f8_swiglu_near(g[j], u[j]);
+            for (int j = 0; j < n; ++j) f8_nearer(g[j], u[j]);
           }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) most = f8_most3(most, g[j], g[j + 1]);
+          for (int j = 0; j < n; ++j) g[j] = f8_swiglu_near(g[j], u[j]);
+#pragma unroll
+          for (int j = 0; j < n; j += 2) most = f8_most3(most, g[j], g[j + 1]);
         };
         // the shared columns are the second half of up's sums, or the first of gate's
         float u[2][32];
@@ -372,11 +372,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         join(h[0][0], u[0]);
         join(h[0][1], u[1]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          f8_tmem_ld32(acc + column(1) + 32 * c, h[1][c]);
-          f8_tmem_ld32(acc + 128 + column(1) + 32 * c, u[0]);
+        for (int c = 0; c < 4; ++c) {  // (32 at a time the registers do not suffice: 2048 x 2 * 4096 x 1024 22.5 us, 20.5 so)
+          auto& g = *reinterpret_cast<float(*)[16]>(&h[1][c >> 1][16 * (c & 1)]);
+          auto& v = *reinterpret_cast<float(*)[16]>(&u[0][0]);
+          f8_tmem_ld16(acc + column(1) + 16 * c, g);
+          f8_tmem_ld16(acc + 128 + column(1) + 16 * c, v);
           f8_tmem_ld_wait();
-          join(h[1][c], u[0]);
+          join(g, v);
         }
         if (p.y)
 #pragma unroll

@@ -35,8 +35,11 @@ def test_far_gates(cuda_device, name, m, up):
     gate, other = F.values(g, np.full((3, 1), 127, dtype=np.uint8), 128)[:, 0], F.values(u, np.full((3, 1), 127.0 + up), 128)[:, 0]
     ref = F.swiglu(gate, other)
     # g and u are exact. Down to -64 the exponential is off by 2 + 1.2 |g| units of 2^-23, the reciprocal and the products by one
-    # each; below, four exponentials by two units each and four products by half of one.
-    off = np.abs(ref) * (8 + 1.2 * np.minimum(np.abs(gate), 64)) * 2.0 ** -23 + 2.0 ** -149
+    # each. Below, that of -64 is multiplied by the square of 2^a, a = (g + 64) / 2 * log2(e): a is rounded once and its constant once, each by
+    # 2^-24 |a| at most: log(2) times both is 0.5 |g + 64| units of 2^-23 in each of two factors. Each power is off by two units besides,
+    # and four products by half of one.
+    far = np.maximum(-64 - gate, 0)
+    off = np.abs(ref) * (8 + 1.2 * np.minimum(np.abs(gate), 64) + np.where(far > 0, 6 + far, 0)) * 2.0 ** -23 + 2.0 ** -149
     h, y = lib.bgq_f8_swiglu(G, U, X, want_out=True)
     got = f64(y)
     assert (got == got[0]).all()
