@@ -5,9 +5,9 @@
 // in one load, of rows g and g + 8, which serve two matrix instructions (the columns of a step may be any, as long as
 // both operands take the same). A block's sum (four steps, each cut to fp32) is scaled and added in fp32; the warps' sums meet in shared
 // memory and are added in warp order. What bounds it: loads in flight, two CTAs an SM with 128 registers a thread, which
-// bring W at 4.4 TB/s (1 row, 12288 x 4096: 11.8 us; 4096 x 4096: 4.3). Four CTAs with half the loads each: 13.8 us; 32-byte loads: 12.7;
+// bring W at 4.4 TB/s (1 row, 12288 x 4096: 11.4 us; 4096 x 4096: 5.1). Four CTAs with half the loads each: 13.8 us; 32-byte loads: 12.7;
 // pieces of rows by bulk copies to shared memory: 12.8. W's lines are asked into L2 while the kernel before still runs (without: 5.6 us
-// where it is 4.3).
+// where it was 4.3 then).
 //
 // Gated with an e4m3 result: a block of 128 columns of the result is the work of 8 CTAs, one cluster, which exchange
 // their rows' largest magnitudes.
@@ -37,7 +37,7 @@ __device__ __forceinline__ uint4 f8_ld_weights(const uint8_t* p) {
   return v;
 }
 
-// Blocks a warp loads before it multiplies them: what its registers hold.
+// Blocks a warp loads before it multiplies them: what its registers hold (17 to 32 rows, gated, spill 268 bytes all the same; few sizes take that).
 template <int NT, bool GATED>
 constexpr int few_ahead() { return NT == 1 ? (GATED ? 2 : 4) : NT == 2 ? (GATED ? 1 : 2) : 1; }
 

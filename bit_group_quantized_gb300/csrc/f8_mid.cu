@@ -10,7 +10,7 @@
 // results. Copies and scales start before tensor memory is there.
 // What bounds it: W's bytes (1 row, 12288 x 4096: 10.5 to 11 us, of which 7.5 at 6.7 TB/s) behind 3 us of start, first loads and end; with
 // more rows the shares' sums, which cross between SMs at 20 bytes a ns each (64 rows, 4096 x 4096: 7.0 us; gated 64 rows, 2 x 1024 x
-// 4096: 7.2 to 7.7). Half the shared memory, so that the next launch's CTAs start beside this one's, gave nothing (12.0 us for 11.5), nor did asking
+// 4096: 6.7 to 7.0). Half the shared memory, so that the next launch's CTAs start beside this one's, gave nothing (12.0 us for 11.5), nor did asking
 // W into L2 ahead of the wait for the kernel before.
 #include <algorithm>
 

@@ -5,30 +5,39 @@
 //   f8_few.cu   few rows, mma.sync, W straight into registers: next to nothing besides W's bytes, which come at 4.4 TB/s;
 //   f8_mid.cu   W as the tensor cores' operand of 128 rows, columns split over CTAs: 3 us besides W's bytes at 6.5 TB/s;
 //   f8_many.cu  tiles of 256 x 256: 5 us besides, and the most arithmetic a second.
-// The one that the estimates call soonest. Measured (CUDA graphs of 24 calls over 130 to 300 MB of
-// weights; us, N x K, gated: 2 N x K):
-//                     rows:     1     8    16    32    64   128   256   512  1024  2048
-//   4096 x 4096       few     4.3   4.7   5.9   8.6  15.9
-//                     mid     6.0   6.1   6.2   6.3   7.0   8.0  11.0  14.6  18.0
-//                     many                          12.3  12.9  12.9  13.6  16.4  25.3
-//   12288 x 4096      few    11.8  12.2  15.0  23.3
-//                     mid    11.1  11.1  11.2  11.3  11.8  13.7  19.0
-//                     many                          14.8  15.1  15.4  23.8  35.1  64.2
-//   4096 x 1024       few     3.2   3.3   3.3   3.5   5.8
-//                     mid     3.5   3.5   3.6   3.8   4.4   5.0   4.9   6.2   9.0
-//                     many                    5.9   6.0   6.2   6.2   6.7   8.2  11.9
-//   1024 x 1024       few     2.1   2.2   2.2   2.5   2.6
-//                     mid     3.0   3.0   3.1   3.1   3.5   3.8   4.3
-//   256 x 16384       few     7.7   8.5  11.3  19.4
-//                     mid     6.0   6.2   6.3   6.7
-//   1024 x 4096       few     5.0   5.4   8.9  12.8
-//   gated             mid     4.5   4.7   4.8   5.5   6.5   7.1   9.0  11.5  15.6
-//                     many                          14.4  14.8  14.8  15.2  15.8  17.4
-//   512 x 1024        few     2.9   3.0   3.8   5.8
-//   gated             mid     3.5   3.6   3.7   3.8
-//   12288 x 4096      few    24.9  25.2  36.6  57.5
-//   gated             mid    18.7  18.8  19.2  20.0  22.3  26.2  45.1
-//                     many                          28.4  28.7  29.3  38.5  67.3   121
+// The one that the estimates call soonest. Measured (CUDA graphs of 24 calls or more, each over weights of its own, 260 MB together,
+// us; N x K, gated: 2 N x K):
+//                     rows:     1     8    16    32    64   128   256   512  1024  2048  8192
+//   4096 x 4096       few      5.1   5.0   6.1   8.7
+//                     mid      6.0   6.0   6.1   6.4   7.0   8.0  11.0  14.8  17.8
+//                     many                      12.3  12.3  12.8  12.9  13.5  16.4  25.2  81.6
+//   12288 x 4096      few     11.4  11.8  14.6  23.0
+//                     mid     10.8  10.8  10.9  11.0  11.5  13.5  19.1  35.2  55.6
+//                     many                      14.6  16.3  16.6  15.5  23.9  35.8  66.2   254
+//   4096 x 1024       few      3.5   3.6   3.2   3.5
+//                     mid      3.8   3.9   4.0   4.2   4.5   5.3   5.0   6.3   9.2
+//                     many                       7.8   8.2   8.5   6.7   7.1   9.1  13.2  30.7
+//   1024 x 1024       few      2.5   2.6   2.1   2.5
+//                     mid      3.0   3.1   3.2   3.2   3.6   3.8   4.3   5.0   4.9
+//                     many                       5.9   5.9   6.1   6.1   6.1   6.1   6.5  11.8
+//   256 x 16384       few      8.5   9.2  11.7  20.2
+//                     mid      6.3   6.6   6.6   6.7   6.7   7.0   7.4   8.9  12.7
+//                     many                      34.9  35.5  37.0  37.2  37.1  37.0  37.0  40.0
+//   1024 x 4096       few      2.9   3.2   3.9   6.2
+//                     mid      4.1   4.2   4.3   4.6   5.3   5.2   5.8   7.0  10.0
+//                     many                      11.8  11.8  12.3  12.4  12.4  12.6  13.2  25.0
+//   1024 x 4096       few      5.2   5.5   9.3  12.6
+//   gated             mid      5.2   5.4   5.6   6.2   6.9   7.3   9.2  11.7  15.7
+//                     many                      14.8  14.9  15.2  15.3  15.5  16.0  17.8  46.7
+//   512 x 1024        few      3.0   3.0   4.1   5.4
+//   gated             mid      3.5   3.7   3.9   3.8   3.8   4.3   5.0   5.4   7.1
+//                     many                       8.1   8.2   8.3   8.4   8.4   8.4   8.7  13.5
+//   12288 x 4096      few     25.0  25.5  37.2  57.0
+//   gated             mid     18.1  18.3  18.6  19.4  21.8  25.8  46.9  71.9   142
+//                     many                      28.4  28.4  28.8  29.4  38.9  69.6   129   546
+// Of these sizes the estimates take the fastest kernel or one within 0.3 us of it. Where no two kernels come
+// near each other they may be short, for many rows most: 8192 x 4096 x 1024 22 us (a tile's end lasts longer than its few
+// instructions), 8192 x 12288 x 4096 194 (the clock follows the power).
 #pragma once
 
 #include <stdint.h>
@@ -61,15 +70,17 @@ inline double f8_few_us(const F8Size& s) {
 
 // ------------------------------------------------------------------ a batch
 struct F8MidPlan {
-  int down, rows, split;  // tiles of x's rows, of so many each; CTAs that share a tile's columns
+  int down, rows, split;  // tiles of x's rows, of so many each; CTAs that share a tile's columns, at most
   double us;
 };
 constexpr int kMidMaxDown = 65535;  // a tile of x's rows is a grid's y
 
 // How x's rows are cut into tiles and columns into shares, and the microseconds that it takes by the estimate that fits what was
 // measured: a CTA's blocks of 128 columns one after the other, or W's bytes, the shares' sums, 4 us for every wave of CTAs behind
-// the first; more than 14 clusters of eight are not all there at once. Few tiles of W leave SMs idle with all rows in one tile of x; cut in several, W is read again, from L2, and
-// the sums are shorter (256 x 4096 x 1024: 4.9 us in four tiles, 7.7 in one; gated 128 x 2 * 1024 x 4096: 7.2 in four, 9.8).
+// the first. A launch takes half the shares as long as not all of its clusters are there at once (f8_mid.cu; 36 of four, 14 or 15 of eight were);
+// the estimate's extra microsecond beyond 14 clusters of eight stands for that, and was fitted with it (gated 64 x 2 * 1024 x 4096, planned
+// as 16 of eight, runs as 16 of four). Few tiles of W leave SMs idle with all rows in one tile of x; cut in several, W is read again, from L2,
+// and the sums are shorter (256 x 4096 x 1024: 5.0 us in four tiles, 7.7 in one; gated 128 x 2 * 1024 x 4096: 7.3 in four, 9.8).
 inline F8MidPlan f8_mid_plan(const F8Size& s, int sms) {
   const int blocks = f8_ceil_div(s.K, kF8Block), least = f8_ceil_div(s.M, s.gated ? 128 : 256);
   const int64_t across = f8_ceil_div(s.N, 128);
